@@ -29,31 +29,31 @@ _DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 def listed():
     return [
         # the byte model's input: 16 sequences of 512 bytes, width 512
-        {"name": "embed fwd, bytes", "op": "embed_fwd", "n": 8192, "V": 256, "D": 512, "table": "f32"},
+        {"name": "embed fwd bytes", "op": "embed_fwd", "n": 8192, "V": 256, "D": 512, "table": "f32"},
         # a large vocabulary's input at the large projection's width, prime table height
-        {"name": "embed fwd, vocabulary", "op": "embed_fwd", "n": 32768, "V": 100003, "D": 4096, "table": "bf16"},
+        {"name": "embed fwd vocabulary", "op": "embed_fwd", "n": 32768, "V": 100003, "D": 4096, "table": "bf16"},
         # the byte model's table gradient: few rows, each the sum of many tokens
-        {"name": "embed bwd, bytes", "op": "embed_bwd", "n": 8192, "V": 256, "D": 512},
+        {"name": "embed bwd bytes", "op": "embed_bwd", "n": 8192, "V": 256, "D": 512},
         # a large vocabulary's table gradient: many rows, most of them untouched
-        {"name": "embed bwd, vocabulary", "op": "embed_bwd", "n": 32768, "V": 100003, "D": 2048},
+        {"name": "embed bwd vocabulary", "op": "embed_bwd", "n": 32768, "V": 100003, "D": 2048},
         # prompts of uneven length before generation, fp32 activations, odd sizes
-        {"name": "scan fwd, prompts", "op": "scan_fwd", "B": 3, "T": 1000, "D": 521, "dtype": "f32",
+        {"name": "scan fwd prompts", "op": "scan_fwd", "B": 3, "T": 1000, "D": 521, "dtype": "f32",
          "lengths": True, "starts": False},
         # one long document
-        {"name": "scan fwd, long", "op": "scan_fwd", "B": 1, "T": 65536, "D": 512, "dtype": "bf16",
+        {"name": "scan fwd long", "op": "scan_fwd", "B": 1, "T": 65536, "D": 512, "dtype": "bf16",
          "lengths": False, "starts": False},
         # the byte model's training block
-        {"name": "scan train, block", "op": "scan_train", "B": 16, "T": 512, "D": 512, "dtype": "bf16",
+        {"name": "scan train block", "op": "scan_train", "B": 16, "T": 512, "D": 512, "dtype": "bf16",
          "lengths": False, "starts": False},
         # training at the wide layer's width and tokens, several documents packed in a row
-        {"name": "scan train, packed wide", "op": "scan_train", "B": 8, "T": 2048, "D": 2048, "dtype": "bf16",
+        {"name": "scan train packed wide", "op": "scan_train", "B": 8, "T": 2048, "D": 2048, "dtype": "bf16",
          "lengths": False, "starts": True},
         # generation: one sequence, and a batch of them
-        {"name": "scan step, one", "op": "scan_step", "B": 1, "D": 512, "dtype": "bf16"},
-        {"name": "scan step, batch", "op": "scan_step", "B": 256, "D": 2048, "dtype": "bf16"},
+        {"name": "scan step one", "op": "scan_step", "B": 1, "D": 512, "dtype": "bf16"},
+        {"name": "scan step batch", "op": "scan_step", "B": 256, "D": 2048, "dtype": "bf16"},
         # the byte model's FFN matrix, and the large projection
-        {"name": "orthogonalize, ffn", "op": "orthogonalize", "K": 512, "N": 2048},
-        {"name": "orthogonalize, large", "op": "orthogonalize", "K": 4096, "N": 12288},
+        {"name": "orthogonalize ffn", "op": "orthogonalize", "K": 512, "N": 2048},
+        {"name": "orthogonalize large", "op": "orthogonalize", "K": 4096, "N": 12288},
     ]
 
 
