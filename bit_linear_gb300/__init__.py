@@ -9,7 +9,14 @@ current stream.  The functions carry the C names:
     tern_linear_bwd(X, dY, tiles, scale, dX, gq, sgrad, workspace)
     adamw_step(w, g, m, v, t, lr, b1, b2, eps, wd, gmul=1.0, decoupled=True)
 
-Materialize, MaterializeGrouped, GroupedForward, GroupedBackward and MultiAdamW are the same calls with
+    tern_embed_fwd(tokens, table, out, scale=1.0)
+    tern_embed_bwd(tokens, dout, dtable, workspace, scale=1.0)
+    tern_scan_fwd(f, v, r, y, f_bias=None, h0=None, hT=None, ...)
+    tern_scan_bwd(f, v, r, dy, saved, workspace, df, dv, dr, ...)
+    tern_scan_step(f, v, r, h, y, h_out=None, f_bias=None)
+
+Materialize, MaterializeGrouped, GroupedForward, GroupedBackward, MultiAdamW, EmbedForward,
+EmbedBackward, ScanForward, ScanBackward and ScanStep are the same calls with
 their arguments checked and marshalled once, for loops that repeat them on the
 same buffers.
 
@@ -41,13 +48,16 @@ TERN_TILE_PACKED, TERN_TILE_T, TERN_TILE_WHI, TERN_TILE_WLO, TERN_TILE_WHI16, TE
 TERN_ADAM_MAX_TENSORS = 64
 TERN_BWD_ACCUMULATE = 1
 TERN_BWD_DX_SPLIT8 = 2
+TERN_BF16, TERN_F32, TERN_I32, TERN_I64 = 0, 1, 2, 3
 
 # the C ABI's exported symbols (tests check the library exports every one)
 ABI_SYMBOLS = ("tern_tiles_bytes", "tern_materialize", "tern_materialize_grouped", "tern_linear_fwd", "tern_linear_bwd_workspace_min",
                "tern_linear_bwd_workspace", "tern_linear_bwd_workspace_ex",
                "tern_linear_bwd", "tern_linear_bwd_ex", "tern_linear_bwd_noalloc", "tern_linear_fwd_grouped",
                "tern_linear_bwd_grouped_workspace", "tern_linear_bwd_grouped", "adamw_step", "tern_grad_sumsq_workspace",
-               "tern_grad_sumsq", "adamw_step_multi", "tern_sr4_workspace", "tern_sr4_step", "tern_sr4_panel", "tern_strerror",
+               "tern_grad_sumsq", "adamw_step_multi", "tern_sr4_workspace", "tern_sr4_step", "tern_sr4_panel",
+               "tern_embed_fwd", "tern_embed_bwd_workspace", "tern_embed_bwd", "tern_scan_saved", "tern_scan_fwd",
+               "tern_scan_bwd_workspace", "tern_scan_bwd", "tern_scan_step", "tern_strerror",
                "tern_device_status", "tern_device_diagnostics", "tern_selftest_wait_timeout")
 
 
@@ -74,6 +84,16 @@ class _Layer(ctypes.Structure):
                 ("gq", ctypes.c_void_p), ("sgrad", ctypes.c_void_p), ("M", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("Y_bf16", ctypes.c_void_p),
                 ("dX_bf16", ctypes.c_void_p)]
+
+
+class _Act(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64)]
+
+
+class _Scan(ctypes.Structure):
+    _fields_ = [("f", _Act), ("v", _Act), ("r", _Act), ("f_bias", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 def _load():
@@ -104,6 +124,15 @@ def _load():
         "tern_sr4_workspace": ([i64], sz),
         "tern_sr4_step": ([vp, vp, i64, cf, cf, ctypes.c_uint64, i64, ctypes.c_uint64, ci, ci, vp, vp, sz, vp], ci),
         "tern_sr4_panel": ([vp, vp, vp, i64, i64, ci, ci, vp, vp, vp], ci),
+        "tern_embed_fwd": ([vp, ci, vp, ci, i64, i64, i64, cf, vp, i64, vp], ci),
+        "tern_embed_bwd_workspace": ([i64, i64, i64], sz),
+        "tern_embed_bwd": ([vp, ci, vp, i64, i64, i64, i64, cf, ci, vp, vp, sz, vp], ci),
+        "tern_scan_saved": ([i64, i64, i64], sz),
+        "tern_scan_fwd": ([ctypes.POINTER(_Scan), vp, ctypes.POINTER(_Act), vp, vp, sz, vp], ci),
+        "tern_scan_bwd_workspace": ([i64, i64, i64], sz),
+        "tern_scan_bwd": ([ctypes.POINTER(_Scan), vp, ctypes.POINTER(_Act), vp] + [ctypes.POINTER(_Act)] * 3 +
+                          [vp, vp, vp, sz, vp], ci),
+        "tern_scan_step": ([ctypes.POINTER(_Scan), vp, vp, ctypes.POINTER(_Act), vp], ci),
         "tern_strerror": ([ci], ctypes.c_char_p),
         "tern_device_status": ([vp, ci], ci),
         "tern_device_diagnostics": ([ctypes.POINTER(i64), ci], ci),
@@ -476,6 +505,189 @@ def tern_sr4_panel(q, scale, counts, scale_stats, packed_prev=None, theta=2, q_c
                               _ptr(counts, torch.int64, (6,), "counts"),
                               _ptr(scale_stats, torch.float64, (3,), "scale_stats"), _stream(stream)),
            "tern_sr4_panel")
+
+
+_TYPES = {torch.bfloat16: TERN_BF16, torch.float32: TERN_F32, torch.int32: TERN_I32, torch.int64: TERN_I64}
+
+
+def _kind(t, allowed, name):
+    """The TERN_* element type of a tensor, one of `allowed`."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in allowed:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, "
+                        f"got {getattr(t, 'dtype', type(t).__name__)}")
+    return _TYPES[t.dtype]
+
+
+def _scratch(t, name):
+    """(pointer, bytes) of a contiguous CUDA tensor used as raw memory."""
+    if t is None:
+        return None, 0
+    return _ptr(t, t.dtype, None, name), t.numel() * t.element_size()
+
+
+def _rows(t, dtype, shape, name):
+    """(pointer, row stride in elements) of a CUDA matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if t.shape[0] > 1 and t.numel() else t.shape[1]
+    return ctypes.c_void_p(t.data_ptr()), int(ld)
+
+
+class EmbedForward:
+    """tern_embed_fwd with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, tokens, table, out, scale=1.0):
+        n = tokens.numel()
+        V, D = table.shape
+        optr, ld = _rows(out, torch.bfloat16, (n, D), "out")
+        tk, tb = _kind(tokens, (torch.int32, torch.int64), "tokens"), _kind(table, (torch.bfloat16, torch.float32), "table")
+        self._args = (_ptr(tokens, tokens.dtype, None, "tokens"), tk, _ptr(table, table.dtype, None, "table"), tb,
+                      n, V, D, float(scale), optr, ld)
+        self._refs = (tokens, table, out)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_embed_fwd(*self._args, _stream(stream)), "tern_embed_fwd")
+
+
+def tern_embed_fwd(tokens, table, out, scale=1.0, stream=None):
+    """out [n, D] bf16 = scale * table[tokens]; ids outside the table give rows of zeros."""
+    EmbedForward(tokens, table, out, scale)(stream)
+
+
+def tern_embed_bwd_workspace(n, V, D) -> int:
+    return int(lib.tern_embed_bwd_workspace(int(n), int(V), int(D)))
+
+
+class EmbedBackward:
+    """tern_embed_bwd with its arguments (and workspace) marshalled once; see GroupedForward."""
+
+    def __init__(self, tokens, dout, dtable, workspace, scale=1.0, accumulate=False):
+        n = tokens.numel()
+        V, D = dtable.shape
+        dptr, ld = _rows(dout, torch.bfloat16, (n, D), "dout")
+        self._args = (_ptr(tokens, tokens.dtype, None, "tokens"), _kind(tokens, (torch.int32, torch.int64), "tokens"),
+                      dptr, ld, n, V, D, float(scale), 1 if accumulate else 0,
+                      _ptr(dtable, torch.float32, None, "dtable"), *_scratch(workspace, "workspace"))
+        self._refs = (tokens, dout, dtable, workspace)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_embed_bwd(*self._args, _stream(stream)), "tern_embed_bwd")
+
+
+def tern_embed_bwd(tokens, dout, dtable, workspace, scale=1.0, accumulate=False, stream=None):
+    """dtable [V, D] fp32 = scale * (sum of dout's rows per token); += with accumulate."""
+    EmbedBackward(tokens, dout, dtable, workspace, scale, accumulate)(stream)
+
+
+def _act(t, dtype, shape, name):
+    """tern_act of a [B, T, D] CUDA tensor with contiguous channels, any row and sequence strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    strides = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]   # of a size of one: any
+    return _Act(ctypes.c_void_p(t.data_ptr()), strides[0], strides[1] if len(strides) > 1 else 0)
+
+
+def _scan(f, v, r, f_bias, lengths, starts):
+    dt = _kind(f, (torch.bfloat16, torch.float32), "f")
+    B, D = f.shape[0], f.shape[-1]
+    T = f.shape[1] if f.dim() == 3 else 1
+    return _Scan(_act(f, f.dtype, f.shape, "f"), _act(v, f.dtype, f.shape, "v"), _act(r, f.dtype, f.shape, "r"),
+                 _ptr(f_bias, torch.float32, (D,), "f_bias"), _ptr(lengths, torch.int32, (B,), "lengths"),
+                 _ptr(starts, torch.uint8, (B, T), "starts"), B, T, D, dt)
+
+
+def tern_scan_saved(B, T, D) -> int:
+    return int(lib.tern_scan_saved(int(B), int(T), int(D)))
+
+
+def tern_scan_bwd_workspace(B, T, D) -> int:
+    return int(lib.tern_scan_bwd_workspace(int(B), int(T), int(D)))
+
+
+class ScanForward:
+    """tern_scan_fwd with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, f, v, r, y, f_bias=None, h0=None, hT=None, lengths=None, starts=None, saved=None):
+        if f.dim() != 3:
+            raise ValueError("f must be [B, T, D]")
+        B, _, D = f.shape
+        self._s = _scan(f, v, r, f_bias, lengths, starts)
+        self._y = _act(y, f.dtype, f.shape, "y")
+        self._args = (ctypes.byref(self._s), _ptr(h0, torch.float32, (B, D), "h0"), ctypes.byref(self._y),
+                      _ptr(hT, torch.float32, (B, D), "hT"), *_scratch(saved, "saved"))
+        self._refs = (f, v, r, y, f_bias, h0, hT, lengths, starts, saved)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_scan_fwd(*self._args, _stream(stream)), "tern_scan_fwd")
+
+
+def tern_scan_fwd(f, v, r, y, f_bias=None, h0=None, hT=None, lengths=None, starts=None, saved=None, stream=None):
+    """Gated linear recurrence over [B, T, D]: a = sigmoid(f + f_bias), h = a h + (1 - a) v,
+    y = sigmoid(r) h (see tern.h).  `saved` (tern_scan_saved bytes) keeps what the gradient needs."""
+    ScanForward(f, v, r, y, f_bias, h0, hT, lengths, starts, saved)(stream)
+
+
+class ScanBackward:
+    """tern_scan_bwd with its arguments (and workspace) marshalled once; see GroupedForward."""
+
+    def __init__(self, f, v, r, dy, saved, workspace, df, dv, dr, f_bias=None, dhT=None, dbias=None, dh0=None,
+                 lengths=None, starts=None):
+        if f.dim() != 3:
+            raise ValueError("f must be [B, T, D]")
+        B, T, D = f.shape
+        self._s = _scan(f, v, r, f_bias, lengths, starts)
+        self._acts = [_act(x, f.dtype, f.shape, name) for x, name in ((dy, "dy"), (df, "df"), (dv, "dv"), (dr, "dr"))]
+        sptr, sbytes = _scratch(saved, "saved")
+        if sbytes < tern_scan_saved(B, T, D):
+            raise ValueError(f"saved holds {sbytes} bytes, the states of this shape take {tern_scan_saved(B, T, D)}")
+        a = [ctypes.byref(x) for x in self._acts]
+        self._args = (ctypes.byref(self._s), sptr, a[0], _ptr(dhT, torch.float32, (B, D), "dhT"), *a[1:],
+                      _ptr(dbias, torch.float32, (D,), "dbias"), _ptr(dh0, torch.float32, (B, D), "dh0"),
+                      *_scratch(workspace, "workspace"))
+        self._refs = (f, v, r, dy, saved, workspace, df, dv, dr, f_bias, dhT, dbias, dh0, lengths, starts)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_scan_bwd(*self._args, _stream(stream)), "tern_scan_bwd")
+
+
+def tern_scan_bwd(f, v, r, dy, saved, workspace, df, dv, dr, f_bias=None, dhT=None, dbias=None, dh0=None,
+                  lengths=None, starts=None, stream=None):
+    """df, dv, dr (and dbias, dh0 where given) from dy and dhT; `saved` from tern_scan_fwd."""
+    ScanBackward(f, v, r, dy, saved, workspace, df, dv, dr, f_bias, dhT, dbias, dh0, lengths, starts)(stream)
+
+
+class ScanStep:
+    """tern_scan_step with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, f, v, r, h, y, h_out=None, f_bias=None):
+        if f.dim() != 2:
+            raise ValueError("f must be [B, D]")
+        self._s = _scan(f, v, r, f_bias, None, None)
+        self._y = _act(y, f.dtype, f.shape, "y")
+        h_out = h if h_out is None else h_out
+        self._args = (ctypes.byref(self._s), _ptr(h, torch.float32, f.shape, "h"),
+                      _ptr(h_out, torch.float32, f.shape, "h_out"), ctypes.byref(self._y))
+        self._refs = (f, v, r, h, y, h_out, f_bias)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_scan_step(*self._args, _stream(stream)), "tern_scan_step")
+
+
+def tern_scan_step(f, v, r, h, y, h_out=None, f_bias=None, stream=None):
+    """One token of every sequence, all [B, D]: the state h (fp32) moves on, in place unless h_out is given."""
+    ScanStep(f, v, r, h, y, h_out, f_bias)(stream)
 
 
 def tern_device_status(stream=None, clear=True) -> int:

@@ -1,0 +1,575 @@
+// Embedding of tokens and the gradient of its table.
+//
+//   out[i]    = scale * table[tok[i]]                       (ids outside the table: a row of zeros)
+//   dtable[k] = scale * sum over i with tok[i] = k of dout[i]   (ids outside the table: dropped)
+//
+// Forward: HBM-bound gather; a thread moves eight channels of a row (16-byte loads and stores).
+//
+// Gradient: the positions are sorted by token (stable radix sort, hand-written here) and each
+// token's rows are then summed in the order of their positions, so no atomic adds in floating
+// point and the same bits on every run.
+//   sort     digits of up to 11 bits, one pass for tables below 2048 rows and two below 4 million:
+//            digit counts per 2048-position tile, a scan of each digit's counts over the tiles,
+//            then each tile places its positions (rank within the tile from warp match masks)
+//   sum      a block takes 256 sorted positions and 256 channels; each warp sums runs of equal
+//            tokens over its 32 positions in registers; the block joins the runs that cross
+//            its warps.  A run inside the block is written once, straight to dtable.  The block's
+//            first run, if it began before the block, and its last, if it goes on, go to a
+//            partial buffer.
+//   join     for each run that leaves its block: the block where it begins adds the partials of
+//            the blocks that it covers, in order.
+// Rows of dtable without a token are written as zeros by extra blocks of the sum launch, from a
+// byte per row that the sort's last pass sets (with accumulate they are left alone).
+// Bounded by HBM for large tables and batches (dout read once, dtable written once), by the
+// launches of the sort for a few thousand tokens.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace tern {
+namespace {
+
+constexpr int kMaxBits = 11;         // digit bits of a sort pass
+constexpr int kSortTile = 2048;      // positions per block of the sort (256 threads x 8)
+constexpr int kRunTile = 256;        // sorted positions per block of the sum (8 warps x 32)
+constexpr int kChTile = 256;         // channels per block of the sum
+
+// ------------------------------------------------------------------------------ forward
+struct EmbedArgs {
+    const void* tokens;
+    const void* table;
+    __nv_bfloat16* out;
+    int64_t n, ld_out;
+    int V, D;
+    float scale;
+};
+
+template <class TOK>
+__device__ __forceinline__ int token_row(const void* tokens, int64_t i, int V) {
+    const TOK t = __ldg(static_cast<const TOK*>(tokens) + i);
+    return t >= 0 && t < static_cast<TOK>(V) ? static_cast<int>(t) : -1;
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+
+// WIDE: eight channels per thread by 16-byte accesses; otherwise one.  A block covers `rows`
+// consecutive tokens, a power of two chosen so that its 256 threads span whole rows.
+template <class TOK, class TAB, bool WIDE>
+__global__ void __launch_bounds__(256) tern_embed_fwd_kernel(const __grid_constant__ EmbedArgs a, int tx) {
+    constexpr int VEC = WIDE ? 8 : 1;
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int x = threadIdx.x & (tx - 1), ty = threadIdx.x / tx;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (256 / tx) + ty;
+    if (i >= a.n) return;
+    const int row = token_row<TOK>(a.tokens, i, a.V);
+    const TAB* src = static_cast<const TAB*>(a.table) + static_cast<int64_t>(max(row, 0)) * a.D;
+    __nv_bfloat16* dst = a.out + i * a.ld_out;
+#pragma unroll 4
+    for (int d = x * VEC; d < a.D; d += tx * VEC) {
+        if constexpr (WIDE) {
+            float v[8] = {};
+            if (row >= 0) {
+                if constexpr (sizeof(TAB) == 4) {
+                    const float4 p = __ldg(reinterpret_cast<const float4*>(src + d));
+                    const float4 q = __ldg(reinterpret_cast<const float4*>(src + d) + 1);
+                    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+                } else {
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(src + d)), v);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+            }
+            *reinterpret_cast<uint4*>(dst + d) = pack8(v);
+        } else {
+            float v = 0.0f;
+            if (row >= 0) {
+                if constexpr (sizeof(TAB) == 4) v = __ldg(src + d) * a.scale;
+                else v = __bfloat162float(src[d]) * a.scale;
+            }
+            dst[d] = __float2bfloat16_rn(v);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------ the sort
+struct SortArgs {
+    const void* tokens;        // first pass: the ids; later: null
+    const int32_t* keys_in;
+    const int32_t* pos_in;
+    int32_t* keys_out;
+    int32_t* pos_out;
+    int32_t* counts;           // [digits][tiles], then (scanned) each tile's offset within the digit
+    int32_t* totals;           // [digits]
+    uint8_t* present;          // [V], or null
+    int n, V, tiles, shift, bits, tokens64;
+    int last;
+};
+
+// The key of position i: its token, or V for an id outside the table (sorted to the end).
+__device__ __forceinline__ int sort_key(const SortArgs& a, int i) {
+    if (a.tokens == nullptr) return a.keys_in[i];
+    const int row = a.tokens64 ? token_row<long long>(a.tokens, i, a.V) : token_row<int>(a.tokens, i, a.V);
+    return row >= 0 ? row : a.V;
+}
+
+__global__ void __launch_bounds__(256) tern_embed_count_kernel(const __grid_constant__ SortArgs a) {
+    __shared__ int32_t hist[1 << kMaxBits];
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int digits = 1 << a.bits;
+    for (int k = threadIdx.x; k < digits; k += 256) hist[k] = 0;
+    if (a.present != nullptr && a.tokens != nullptr) {   // first pass: no row has a token yet
+        uint32_t* words = reinterpret_cast<uint32_t*>(a.present);   // the plan rounds its size up to 256 bytes
+        for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k * 4 < a.V; k += static_cast<int64_t>(gridDim.x) * 256)
+            words[k] = 0u;
+    }
+    if (blockIdx.x >= a.tiles) return;   // blocks beyond the tiles only clear
+    __syncthreads();
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortTile;
+#pragma unroll
+    for (int r = 0; r < kSortTile / 256; ++r) {
+        const int64_t i = base + r * 256 + threadIdx.x;
+        if (i < a.n) atomicAdd(&hist[(sort_key(a, static_cast<int>(i)) >> a.shift) & (digits - 1)], 1);
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < digits; k += 256) a.counts[static_cast<int64_t>(k) * a.tiles + blockIdx.x] = hist[k];
+}
+
+// Exclusive scan of each digit's counts over the tiles, one warp per digit; the sum to totals.
+__global__ void __launch_bounds__(256) tern_embed_offsets_kernel(int32_t* counts, int32_t* totals, int digits, int tiles) {
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int k = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (k >= digits) return;
+    int32_t* c = counts + static_cast<int64_t>(k) * tiles;
+    int run = 0;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+        const int t = t0 + lane;
+        const int x = t < tiles ? c[t] : 0;
+        int s = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        if (t < tiles) c[t] = run + s - x;
+        run += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) totals[k] = run;
+}
+
+// Stable placement: within a tile the order is (warp, round, lane), as the positions lie.
+__global__ void __launch_bounds__(256) tern_embed_place_kernel(const __grid_constant__ SortArgs a) {
+    __shared__ int32_t base[1 << kMaxBits];            // where this tile's positions of a digit go
+    __shared__ uint16_t cnt[8][1 << kMaxBits];         // per warp: count of a digit, then its offset in the tile
+    __shared__ int32_t wsum[8];
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int digits = 1 << a.bits, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int k = threadIdx.x; k < digits * 4; k += 256) reinterpret_cast<uint32_t*>(&cnt[k / (digits / 2)][0])[k % (digits / 2)] = 0;
+    // exclusive scan of the digits' totals: each thread takes `per` consecutive digits
+    const int per = (digits + 255) / 256;
+    int own = 0;
+    for (int j = 0; j < per; ++j) {
+        const int k = threadIdx.x * per + j;
+        own += k < digits ? a.totals[k] : 0;
+    }
+    int s = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    if (lane == 31) wsum[w] = s;
+    __syncthreads();
+    int before = s - own;
+    for (int k = 0; k < w; ++k) before += wsum[k];
+    for (int j = 0; j < per; ++j) {
+        const int k = threadIdx.x * per + j;
+        if (k < digits) {
+            base[k] = before + a.counts[static_cast<int64_t>(k) * a.tiles + blockIdx.x];
+            before += a.totals[k];
+        }
+    }
+    // ranks within the warp's 256 positions
+    constexpr int R = kSortTile / 256;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + w * (kSortTile / 8);
+    int key[R], rank[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) key[r] = i0 + r * 32 + lane < a.n ? sort_key(a, static_cast<int>(i0 + r * 32 + lane)) : -1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int dg = key[r] >= 0 ? (key[r] >> a.shift) & (digits - 1) : digits;
+        const uint32_t same = __match_any_sync(0xffffffffu, dg);
+        const uint32_t lower = same & ((1u << lane) - 1u);
+        rank[r] = 0;
+        if (dg < digits) rank[r] = cnt[w][dg] + __popc(lower);
+        __syncwarp();
+        if (dg < digits && lower == 0) cnt[w][dg] = static_cast<uint16_t>(cnt[w][dg] + __popc(same));
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < digits; k += 256) {
+        int run = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = cnt[j][k];
+            cnt[j][k] = static_cast<uint16_t>(run);
+            run += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (key[r] < 0) continue;
+        const int i = static_cast<int>(i0) + r * 32 + lane;
+        const int dg = (key[r] >> a.shift) & (digits - 1);
+        const int at = base[dg] + cnt[w][dg] + rank[r];
+        a.keys_out[at] = key[r];
+        a.pos_out[at] = a.pos_in != nullptr ? a.pos_in[i] : i;
+        if (a.last && a.present != nullptr && key[r] < a.V) a.present[key[r]] = 1;
+    }
+}
+
+// ------------------------------------------------------------------------------ the sums
+struct RunArgs {
+    const int32_t* keys;       // sorted
+    const int32_t* pos;
+    const __nv_bfloat16* dout;
+    float* dtable;
+    float* partial;            // [run tiles][2][D]: 0 the run that began before the tile, 1 the one that goes on
+    const uint8_t* present;    // null with accumulate
+    int64_t ld_dout;
+    int n, V, D, run_tiles, ch_tiles;
+    int accumulate;
+    float scale;
+};
+
+// The eight channels of a lane in a 256-channel tile: consecutive (WIDE), or 32 apart.
+template <bool WIDE>
+__device__ __forceinline__ int channel(int c0, int lane, int k) {
+    return WIDE ? c0 + lane * 8 + k : c0 + k * 32 + lane;
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void write_row(const RunArgs& a, int key, int c0, int lane, const float (&x)[8]) {
+    float* row = a.dtable + static_cast<int64_t>(key) * a.D;
+    if constexpr (WIDE) {
+        const int c = c0 + lane * 8;
+        if (c >= a.D) return;
+        float4* p = reinterpret_cast<float4*>(row + c);
+        float4 u = make_float4(x[0] * a.scale, x[1] * a.scale, x[2] * a.scale, x[3] * a.scale);
+        float4 v = make_float4(x[4] * a.scale, x[5] * a.scale, x[6] * a.scale, x[7] * a.scale);
+        if (a.accumulate) {
+            const float4 s = p[0], t = p[1];
+            u = make_float4(s.x + u.x, s.y + u.y, s.z + u.z, s.w + u.w);
+            v = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
+        }
+        p[0] = u, p[1] = v;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int c = channel<false>(c0, lane, k);
+            if (c < a.D) row[c] = (a.accumulate ? row[c] : 0.0f) + x[k] * a.scale;
+        }
+    }
+}
+
+template <bool WIDE>
+__global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_constant__ RunArgs a) {
+    __shared__ float first_s[8][kChTile], last_s[8][kChTile];
+    __shared__ int first_key[8], last_key[8];   // of a warp's positions; -1 without any
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t unit = blockIdx.x;
+    if (unit >= static_cast<int64_t>(a.run_tiles) * a.ch_tiles) {
+        // rows without a token: zeros, one warp per row
+        const int64_t fill = unit - static_cast<int64_t>(a.run_tiles) * a.ch_tiles;
+        const int64_t stride = (static_cast<int64_t>(gridDim.x) - static_cast<int64_t>(a.run_tiles) * a.ch_tiles) * 8;
+        for (int64_t v = fill * 8 + w; v < a.V; v += stride) {
+            if (a.present[v]) continue;
+            float* row = a.dtable + v * a.D;
+            if constexpr (WIDE) {
+                for (int c = lane * 4; c < a.D; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+                for (int c = lane; c < a.D; c += 32) row[c] = 0.0f;
+            }
+        }
+        return;
+    }
+    const int tile = static_cast<int>(unit / a.ch_tiles), c0 = static_cast<int>(unit % a.ch_tiles) * kChTile;
+    const int p0 = tile * kRunTile + w * 32;
+    const int mine = p0 + lane < a.n ? a.keys[p0 + lane] : a.V;
+    const int where = mine < a.V ? a.pos[p0 + lane] : 0;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, mine < a.V));   // sorted: the live ones come first
+    float acc[8] = {};
+    int cur = __shfl_sync(0xffffffffu, mine, 0);
+    bool first = true;      // still in the warp's first run
+    if (lane == 0) first_key[w] = cnt > 0 ? cur : -1;
+    constexpr int U = 8;    // rows in flight
+    for (int i0 = 0; i0 < cnt; i0 += U) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int src = __shfl_sync(0xffffffffu, where, i0 + u);
+            raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (i0 + u < cnt) {
+                const __nv_bfloat16* row = a.dout + static_cast<int64_t>(src) * a.ld_dout;
+                if constexpr (WIDE) {
+                    if (c0 + lane * 8 < a.D) raw[u] = __ldg(reinterpret_cast<const uint4*>(row + c0 + lane * 8));
+                } else {
+                    uint32_t h[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int c = channel<false>(c0, lane, k);
+                        h[k] = c < a.D ? __ldg(reinterpret_cast<const unsigned short*>(row) + c) : 0u;
+                    }
+                    raw[u] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u >= cnt) break;
+            const int key = __shfl_sync(0xffffffffu, mine, i0 + u);
+            if (key != cur) {
+                if (first) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) first_s[w][channel<WIDE>(0, lane, k)] = acc[k];
+                    first = false;
+                } else {
+                    write_row<WIDE>(a, cur, c0, lane, acc);
+                }
+                cur = key;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+            }
+            float x[8];
+            unpack8(raw[u], x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] += x[k];
+        }
+    }
+    // the warp's open run: its only one (first) or its last
+#pragma unroll
+    for (int k = 0; k < 8; ++k) (first ? first_s : last_s)[w][channel<WIDE>(0, lane, k)] = acc[k];
+    if (lane == 0) last_key[w] = cnt == 0 ? -1 : (first ? -2 : cur);   // -2: a single run
+    __syncthreads();
+    // join the runs across the warps, a thread per channel
+    const int c = c0 + threadIdx.x;
+    if (c >= a.D || first_key[0] < 0) return;
+    const int begin = tile * kRunTile, end = min(begin + kRunTile, a.n);
+    const bool from_before = begin > 0 && a.keys[begin - 1] == first_key[0];
+    float* part = a.partial + static_cast<int64_t>(tile) * 2 * a.D + c;
+    int key = first_key[0];
+    float sum = first_s[0][threadIdx.x];
+    bool opening = true;    // the run began at the tile's first position
+    auto flush = [&]() {
+        if (opening && from_before) part[0] = sum;
+        else {
+            float* p = a.dtable + static_cast<int64_t>(key) * a.D + c;
+            *p = (a.accumulate ? *p : 0.0f) + sum * a.scale;
+        }
+        opening = false;
+    };
+    for (int k = 0; k < 8; ++k) {
+        if (first_key[k] < 0) break;
+        if (k > 0) {
+            if (first_key[k] == key) sum += first_s[k][threadIdx.x];
+            else {
+                flush();
+                key = first_key[k], sum = first_s[k][threadIdx.x];
+            }
+        }
+        if (last_key[k] >= 0) {
+            flush();
+            key = last_key[k], sum = last_s[k][threadIdx.x];
+        }
+    }
+    const bool goes_on = end < a.n && a.keys[end] == key;
+    if (goes_on && !(opening && from_before)) part[a.D] = sum;
+    else flush();
+}
+
+// Runs that leave the tile they begin in: partial 1 of that tile, then partial 0 of the tiles
+// that they cover; eight warps take every eighth tile, then add up in order.
+__global__ void __launch_bounds__(256) tern_embed_join_kernel(const __grid_constant__ RunArgs a) {
+    __shared__ float red[8][32];
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int tile = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int end = min((tile + 1) * kRunTile, a.n);
+    const int key = a.keys[end - 1];
+    if (key >= a.V || end >= a.n || a.keys[end] != key) return;              // ends with the tile
+    const int begin = tile * kRunTile;
+    if (begin > 0 && a.keys[begin] == key && a.keys[begin - 1] == key) return;   // began before it
+    // the last tile of the run: the largest t whose first key is `key`
+    int lo = tile + 1, hi = a.run_tiles - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.keys[mid * kRunTile] == key) lo = mid;
+        else hi = mid - 1;
+    }
+    for (int c0 = blockIdx.y * 32; c0 < a.D; c0 += gridDim.y * 32) {
+        const int c = c0 + lane;
+        float sum = 0.0f;
+        if (c < a.D) {
+#pragma unroll 4
+            for (int t = tile + 1 + w; t <= lo; t += 8) sum += a.partial[static_cast<int64_t>(t) * 2 * a.D + c];
+        }
+        red[w][lane] = sum;
+        __syncthreads();
+        if (w == 0 && c < a.D) {
+            sum = a.partial[(static_cast<int64_t>(tile) * 2 + 1) * a.D + c];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += red[k][lane];
+            float* p = a.dtable + static_cast<int64_t>(key) * a.D + c;
+            *p = (a.accumulate ? *p : 0.0f) + sum * a.scale;
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------------------ host side
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+struct Plan {   // the sort's passes and the workspace's parts, in bytes
+    int passes = 0, bits = 0, sort_tiles = 0, run_tiles = 0;
+    int64_t keys[2], pos[2], counts, totals, present, partial, bytes = 0;
+};
+
+Plan make_plan(int64_t n, int64_t V, int64_t D) {
+    Plan p;
+    int need = 1;
+    while ((static_cast<int64_t>(1) << need) <= V) ++need;   // keys 0..V
+    p.passes = (need + kMaxBits - 1) / kMaxBits;
+    p.bits = (need + p.passes - 1) / p.passes;
+    p.sort_tiles = static_cast<int>((n + kSortTile - 1) / kSortTile);
+    p.run_tiles = static_cast<int>((n + kRunTile - 1) / kRunTile);
+    auto take = [&](int64_t bytes) {
+        const int64_t at = p.bytes;
+        p.bytes += round256(bytes);
+        return at;
+    };
+    for (int i = 0; i < 2; ++i) p.keys[i] = take(4 * n), p.pos[i] = take(4 * n);
+    p.counts = take(4 * (static_cast<int64_t>(1) << p.bits) * p.sort_tiles);
+    p.totals = take(4 * (static_cast<int64_t>(1) << p.bits));
+    p.present = take(V);
+    p.partial = take(8 * static_cast<int64_t>(p.run_tiles) * D);
+    return p;
+}
+
+bool bad_sizes(int64_t n, int64_t V, int64_t D) {
+    return n < 0 || V < 1 || D < 0 || n > INT32_MAX - kSortTile || V >= INT32_MAX || D > INT32_MAX - 1024;
+}
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <class TOK, class TAB>
+int launch_embed(const EmbedArgs& a, cudaStream_t s) {
+    const bool wide = a.D % 8 == 0 && a.ld_out % 8 == 0 && aligned16(a.table) && aligned16(a.out);
+    const int items = wide ? a.D / 8 : a.D;
+    int tx = 8;                                   // threads per row
+    while (tx < 256 && tx < items) tx *= 2;
+    const int64_t blocks = (a.n + 256 / tx - 1) / (256 / tx);
+    if (blocks > INT32_MAX) return TERN_ERR_ARG;
+    return launch_pdl(wide ? tern_embed_fwd_kernel<TOK, TAB, true> : tern_embed_fwd_kernel<TOK, TAB, false>,
+                      dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, tx);
+}
+
+}  // namespace
+}  // namespace tern
+
+using namespace tern;
+
+extern "C" int tern_embed_fwd(const void* tokens, int tokens_dtype, const void* table, int table_dtype, int64_t n,
+                              int64_t V, int64_t D, float scale, void* out, int64_t ld_out, void* stream) {
+    if (bad_sizes(n, V, D) || ld_out < D) return TERN_ERR_ARG;
+    if ((tokens_dtype != TERN_I32 && tokens_dtype != TERN_I64) || (table_dtype != TERN_BF16 && table_dtype != TERN_F32))
+        return TERN_ERR_ARG;
+    if (n == 0 || D == 0) return TERN_OK;
+    if (!tokens || !table || !out) return TERN_ERR_ARG;
+    if (!aligned(tokens, tokens_dtype == TERN_I64 ? 8 : 4) || !aligned(table, table_dtype == TERN_F32 ? 4 : 2) || !aligned(out, 2))
+        return TERN_ERR_ALIGN;
+    if (int st = check_device(nullptr)) return st;
+    EmbedArgs a{tokens, table, static_cast<__nv_bfloat16*>(out), n, ld_out, static_cast<int>(V), static_cast<int>(D), scale};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tokens_dtype == TERN_I64)
+        return table_dtype == TERN_F32 ? launch_embed<long long, float>(a, s) : launch_embed<long long, __nv_bfloat16>(a, s);
+    return table_dtype == TERN_F32 ? launch_embed<int, float>(a, s) : launch_embed<int, __nv_bfloat16>(a, s);
+}
+
+extern "C" size_t tern_embed_bwd_workspace(int64_t n, int64_t V, int64_t D) {
+    return bad_sizes(n, V, D) ? 0 : static_cast<size_t>(make_plan(n, V, D).bytes);
+}
+
+extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* dout, int64_t ld_dout, int64_t n, int64_t V,
+                              int64_t D, float scale, int accumulate, float* dtable, void* workspace, size_t ws_bytes,
+                              void* stream) {
+    if (bad_sizes(n, V, D) || ld_dout < D || (tokens_dtype != TERN_I32 && tokens_dtype != TERN_I64)) return TERN_ERR_ARG;
+    if (D == 0 || (n == 0 && accumulate)) return TERN_OK;
+    if (!dtable || (n > 0 && (!tokens || !dout))) return TERN_ERR_ARG;
+    if (!aligned(tokens, tokens_dtype == TERN_I64 ? 8 : 4) || !aligned(dout, 2) || !aligned(dtable, 4)) return TERN_ERR_ALIGN;
+    const Plan p = make_plan(n, V, D);
+    if (!workspace || ws_bytes < static_cast<size_t>(p.bytes)) return TERN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TERN_ERR_ALIGN;
+    int num_sms = 0;
+    if (int st = check_device(&num_sms)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    auto i32 = [&](int64_t at) { return reinterpret_cast<int32_t*>(ws + at); };
+
+    SortArgs q{};
+    q.n = static_cast<int>(n), q.V = static_cast<int>(V), q.tiles = p.sort_tiles, q.bits = p.bits;
+    q.tokens64 = tokens_dtype == TERN_I64;
+    q.counts = i32(p.counts), q.totals = i32(p.totals);
+    q.present = accumulate ? nullptr : ws + p.present;
+    if (n == 0) {   // nothing to sort: every row is without a token
+        TERN_CUDA_TRY(cudaMemsetAsync(dtable, 0, static_cast<size_t>(V) * D * sizeof(float), s));
+        return TERN_OK;
+    }
+    const int digits = 1 << p.bits;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        q.tokens = pass == 0 ? tokens : nullptr;
+        q.keys_in = pass == 0 ? nullptr : i32(p.keys[(pass - 1) & 1]);
+        q.pos_in = pass == 0 ? nullptr : i32(p.pos[(pass - 1) & 1]);
+        q.keys_out = i32(p.keys[pass & 1]), q.pos_out = i32(p.pos[pass & 1]);
+        q.shift = pass * p.bits, q.last = pass == p.passes - 1;
+        // the first pass also clears `present`, four bytes a thread, by up to one block per SM
+        const int clear = pass == 0 && q.present != nullptr ? static_cast<int>(V / 4096 < num_sms ? V / 4096 : num_sms) : 0;
+        const int blocks = clear > p.sort_tiles ? clear : p.sort_tiles;
+        if (int st = launch_pdl(tern_embed_count_kernel, dim3(blocks), dim3(256), 0, s, q)) return st;
+        if (int st = launch_pdl(tern_embed_offsets_kernel, dim3((digits + 7) / 8), dim3(256), 0, s, q.counts, q.totals, digits, p.sort_tiles)) return st;
+        if (int st = launch_pdl(tern_embed_place_kernel, dim3(p.sort_tiles), dim3(256), 0, s, q)) return st;
+    }
+    RunArgs a{};
+    a.keys = q.keys_out, a.pos = q.pos_out, a.dout = static_cast<const __nv_bfloat16*>(dout), a.dtable = dtable;
+    a.partial = reinterpret_cast<float*>(ws + p.partial), a.present = q.present, a.ld_dout = ld_dout;
+    a.n = q.n, a.V = q.V, a.D = static_cast<int>(D), a.run_tiles = p.run_tiles;
+    a.ch_tiles = static_cast<int>((D + kChTile - 1) / kChTile);
+    a.accumulate = accumulate ? 1 : 0, a.scale = scale;
+    const bool wide = D % 8 == 0 && ld_dout % 8 == 0 && aligned16(dout) && aligned16(dtable);
+    const int64_t units = static_cast<int64_t>(a.run_tiles) * a.ch_tiles;
+    const int64_t fill = accumulate ? 0 : (V + 7) / 8 < 8 * num_sms ? (V + 7) / 8 : 8 * num_sms;
+    if (units + fill > INT32_MAX) return TERN_ERR_ARG;
+    if (int st = launch_pdl(wide ? tern_embed_sum_kernel<true> : tern_embed_sum_kernel<false>,
+                            dim3(static_cast<unsigned>(units + fill)), dim3(256), 0, s, a)) return st;
+    if (p.run_tiles < 2) return TERN_OK;
+    const unsigned gy = static_cast<unsigned>((D + 31) / 32 < 32 ? (D + 31) / 32 : 32);
+    return launch_pdl(tern_embed_join_kernel, dim3(static_cast<unsigned>(p.run_tiles), gy), dim3(256), 0, s, a);
+}

@@ -371,6 +371,95 @@ int tern_sr4_step(int8_t* q, const float* gq, int64_t numel, float inv_bs, float
 int tern_sr4_panel(const int8_t* q, const uint32_t* packed_prev, const float* scale, int64_t K, int64_t N,
                    int theta, int q_clamp, unsigned long long* counts, double* scale_stats, void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------
+ * Around the ternary projections: the embedding of tokens, the gated linear recurrence
+ * that the projections of a recurrent block feed, and the orthogonalised update of a
+ * weight's gradient.  The same rules hold (ownership, ordering, errors); unlike the
+ * ternary weights, these take any size, zero included, and any alignment of whole
+ * elements unless a line below says otherwise.
+ * ------------------------------------------------------------------------------------
+ */
+#define TERN_BF16 0               /* element types of activations and tables */
+#define TERN_F32 1
+#define TERN_I32 2                /* element types of token ids */
+#define TERN_I64 3
+
+/*
+ * Embedding of n tokens from a table [V][D] (TERN_BF16 or TERN_F32, dense):
+ *   out[i][:] = bf16_rne(scale * table[tokens[i]][:])
+ * tokens: TERN_I32 or TERN_I64 ids; an id outside 0..V-1 is padding and gives a row of zeros.
+ * out: bf16, rows ld_out >= D elements apart.  n, D >= 0; n, V and D below 2^31 - 2048.
+ */
+int tern_embed_fwd(const void* tokens, int tokens_dtype, const void* table, int table_dtype, int64_t n,
+                   int64_t V, int64_t D, float scale, void* out, int64_t ld_out, void* stream);
+/*
+ * Gradient of the table, from dout (bf16, rows ld_dout >= D elements apart):
+ *   dtable[k][:] = scale * sum over i with tokens[i] = k of dout[i][:]      (fp32, dense [V][D])
+ * Every row is written (zeros without a token); with accumulate != 0 the sums are added to
+ * dtable and the other rows left alone.  The positions are sorted by token and summed in
+ * position order within each token: no floating-point atomics, the same bits every time.
+ *   workspace: >= tern_embed_bwd_workspace() bytes, 16-byte aligned.
+ */
+size_t tern_embed_bwd_workspace(int64_t n, int64_t V, int64_t D);
+int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* dout, int64_t ld_dout, int64_t n, int64_t V,
+                   int64_t D, float scale, int accumulate, float* dtable, void* workspace, size_t ws_bytes,
+                   void* stream);
+
+/* Activations [B][T][D] with D contiguous: element (b,t,d) at p[b*stride_b + t*stride_t + d],
+ * strides in elements, >= 0.  Outputs must not overlap themselves or an input. */
+typedef struct tern_act {
+    void* p;
+    int64_t stride_b, stride_t;
+} tern_act;
+
+/*
+ * Gated linear recurrence, per sequence b and channel d:
+ *   a_t = sigmoid(f_t + f_bias)
+ *   h_t = a_t h_{t-1} + (1 - a_t) v_t          h_{-1} = h0
+ *   y_t = sigmoid(r_t) h_t
+ * f, v, r, y: `dtype` (TERN_BF16 or TERN_F32); gates and states are fp32, y is rounded once.
+ *   f_bias   [D] fp32, or NULL (0)
+ *   lengths  [B], or NULL (T): rows t >= lengths[b] are padding; they are not read, the state
+ *            passes them unchanged, and y there is 0.  Values are clamped to 0..T.
+ *   starts   [B][T] bytes, or NULL: where nonzero (and not padding) a document starts: h_{t-1}
+ *            is taken as 0, whatever it was.
+ * B, T, D >= 0, B, T and D below 2^31 - 256.
+ */
+typedef struct tern_scan {
+    tern_act f, v, r;
+    const float* f_bias;
+    const int32_t* lengths;
+    const uint8_t* starts;
+    int64_t B, T, D;
+    int dtype;
+} tern_scan;
+
+/* Bytes of the states that tern_scan_fwd saves for tern_scan_bwd (one per 64 rows, fp32). */
+size_t tern_scan_saved(int64_t B, int64_t T, int64_t D);
+/*
+ * Forward.  h0 [B][D] fp32 or NULL (0); hT [B][D] fp32, the state after the last live row, or
+ * NULL; saved: tern_scan_saved() bytes, or NULL when no backward follows.  hT may equal h0.
+ */
+int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act* y, float* hT, float* saved,
+                  size_t saved_bytes, void* stream);
+/*
+ * Gradient, from the same inputs and the forward's saved states.  dy and the outputs df, dv, dr
+ * have s->dtype (0 is written in padding; dy is not read there); dhT [B][D] fp32 is the gradient
+ * of hT, or NULL (0); dh0 [B][D] fp32 and dbias [D] fp32 (the sum of df over sequences and rows,
+ * before df is rounded) are written unless NULL.  dbias wants tern_scan_bwd_workspace() bytes
+ * and B >= 1.  Sums run in a fixed order.
+ */
+size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D);
+int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_act* dy, const float* dhT,
+                  const tern_act* df, const tern_act* dv, const tern_act* dr, float* dbias, float* dh0,
+                  void* workspace, size_t ws_bytes, void* stream);
+/*
+ * One token of every sequence (s->T must be 1; no lengths, no starts): h_out = the state after
+ * it, y its output.  h_out may equal h_in (the state moves in place).
+ */
+int tern_scan_step(const tern_scan* s, const float* h_in, float* h_out, const tern_act* y, void* stream);
+
 /* Text of a status code (static storage). */
 const char* tern_strerror(int status);
 
