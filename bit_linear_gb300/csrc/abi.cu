@@ -55,5 +55,6 @@ extern "C" const char* tern_strerror(int status) {
 
 extern "C" int tern_device_status(void* stream, int clear) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TERN_ERR_CUDA;
-    return tern::gemm_status_read(clear);
+    const int gemm = tern::gemm_status_read(clear), scan = tern::scan_status_read(clear);
+    return gemm != TERN_OK ? gemm : scan;
 }

@@ -6,10 +6,12 @@
 // lengths[b] are padding (never read: a = 1, no input, y = 0, gradients 0).
 //
 // The map of one row, h -> a h + b, composes: rows i..j act as h -> A h + H with A = prod a and
-// H the state reached from 0.  A block takes 32*VEC channels and ROWS consecutive rows, RPT rows
-// per warp (lane = VEC channels, so a warp's loads are whole lines), all held in registers:
-//   1. each thread folds its RPT rows into (A, H) and leaves the pair in shared memory;
-//   2. after a barrier it folds the pairs of the warps before it onto the block's incoming state;
+// H the state reached from 0.  A block takes a tile of channels and ROWS consecutive rows, all
+// held in registers: a lane has VEC neighbouring channels of RPT rows (a segment), LPR lanes side
+// by side make a row's whole 128-byte line, and a warp holds 32/LPR segments.
+//   1. each lane folds its RPT rows into (A, H); a warp's segments are joined by shuffles and
+//      its pair left in shared memory;
+//   2. after a barrier each lane folds what lies before it onto the block's incoming state;
 //   3. it runs its rows again from that state and writes y.
 // A block walks T in steps of ROWS.  Where sequences times channel tiles are too few blocks to
 // fill the GPU, a cluster of S blocks takes S consecutive steps at a time and exchanges the
@@ -19,12 +21,14 @@
 // The gradient runs the same way from the end of the sequence, with e_t = a_t dh_t as its state:
 //   dh_t = g_t + e_{t+1}, e_t = a_t dh_t, g_t = sigmoid(r_t) dy_t, e_T = dhT
 //   dv = (1 - a) dh, df = dh (h_{t-1} - v) a (1 - a), dr = dy h s (1 - s), dh0 = e_0
-// and recomputes h inside its 64 rows from the states the forward saved every 64 rows (1/16 B
+// and recomputes h inside its 64 rows from the states the forward saved every 64 rows (1/8 B
 // per element beside the 22 B of a forward and a backward in bf16).
 //
-// Bounded by HBM (each input read once, each output written once) with the special-function
-// unit next: four operations per element (two sigmoids) against the 5.4 per element that its
-// rate allows at 8 B per element.  Gates and states are fp32; outputs are rounded once.
+// Bounded by HBM (each input read once, each output written once), with the instruction rate
+// close behind: 8 B per element at 45 B/ns per SM leave about 40 instructions per element.
+// Gates and states are fp32; outputs are rounded once.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -32,76 +36,180 @@
 namespace tern {
 namespace {
 
-constexpr int kSaveRows = 64;    // rows between saved states; the backward's block step
-constexpr int kMaxCluster = 8;   // portable cluster size
+constexpr int kSaveRows = 64;     // rows between saved states
+constexpr int kMaxCluster = 16;   // blocks of a cluster (8 portable, 16 by a function attribute)
+
+__device__ int g_scan_status;     // 1 once a wait for a peer's totals gave up
+
+// --------------------------------------------------------------- pairs of fp32
+// Two neighbouring channels in one 64-bit register pair: sm_103a multiplies and adds both in one
+// instruction, which the instruction count of these kernels needs.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xffffffffu, a.v, from)}; }
 
 // --------------------------------------------------------------- element access
-template <class T, int VEC>
+// NP pairs of neighbouring elements of a row.  WIDE: one 8-byte access; otherwise element by
+// element (odd widths, strides or addresses), where a row's last lane may hold fewer: nch
+// elements are there, loads repeat the last and stores leave the others out.
+template <class T, bool WIDE_>
 struct Io;
-template <>
-struct Io<__nv_bfloat16, 2> {
-    using Raw = uint32_t;
-    static __device__ __forceinline__ Raw load(const void* p, int64_t i) {
-        return __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p) + i));
+template <bool WIDE>
+struct Io<__nv_bfloat16, WIDE> {
+    static constexpr int NP = 2;
+    using Raw = uint2;
+    static __device__ __forceinline__ Raw load(const char* p, int nch) {
+        if constexpr (WIDE) return __ldg(reinterpret_cast<const uint2*>(p));
+        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+        const uint32_t x0 = __ldg(q), x1 = __ldg(q + min(1, nch - 1)), x2 = __ldg(q + min(2, nch - 1)), x3 = __ldg(q + min(3, nch - 1));
+        return make_uint2(x0 | x1 << 16, x2 | x3 << 16);
     }
-    static __device__ __forceinline__ void get(Raw r, float (&x)[2]) {
-        x[0] = __uint_as_float(r << 16);
-        x[1] = __uint_as_float(r & 0xFFFF0000u);
+    static __device__ __forceinline__ void get(const Raw& r, F2 (&x)[2]) {
+        x[0] = pair(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
+        x[1] = pair(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[2]) {
-        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + i) = __floats2bfloat162_rn(x[0], x[1]);
+    static __device__ __forceinline__ uint32_t round2(F2 a) {
+        float x, y;
+        split(a, x, y);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&t);
+    }
+    static __device__ __forceinline__ void store(char* p, const F2 (&x)[2], int nch) {
+        const uint32_t a = round2(x[0]), b = round2(x[1]);
+        if constexpr (WIDE) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+        } else {
+            unsigned short* q = reinterpret_cast<unsigned short*>(p);
+            q[0] = static_cast<unsigned short>(a);
+            if (nch > 1) q[1] = static_cast<unsigned short>(a >> 16);
+            if (nch > 2) q[2] = static_cast<unsigned short>(b);
+            if (nch > 3) q[3] = static_cast<unsigned short>(b >> 16);
+        }
     }
 };
-template <>
-struct Io<__nv_bfloat16, 1> {
-    using Raw = unsigned short;
-    static __device__ __forceinline__ Raw load(const void* p, int64_t i) {
-        return __ldg(static_cast<const unsigned short*>(p) + i);
-    }
-    static __device__ __forceinline__ void get(Raw r, float (&x)[1]) { x[0] = __uint_as_float(static_cast<uint32_t>(r) << 16); }
-    static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[1]) {
-        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x[0]);
-    }
-};
-template <>
-struct Io<float, 2> {
+template <bool WIDE>
+struct Io<float, WIDE> {
+    static constexpr int NP = 1;
     using Raw = float2;
-    static __device__ __forceinline__ Raw load(const void* p, int64_t i) {
-        return __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p) + i));
+    static __device__ __forceinline__ Raw load(const char* p, int nch) {
+        if constexpr (WIDE) return __ldg(reinterpret_cast<const float2*>(p));
+        const float* q = reinterpret_cast<const float*>(p);
+        return make_float2(__ldg(q), __ldg(q + min(1, nch - 1)));
     }
-    static __device__ __forceinline__ void get(Raw r, float (&x)[2]) { x[0] = r.x, x[1] = r.y; }
-    static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[2]) {
-        *reinterpret_cast<float2*>(static_cast<float*>(p) + i) = make_float2(x[0], x[1]);
+    static __device__ __forceinline__ void get(const Raw& r, F2 (&x)[1]) { x[0] = pair(r.x, r.y); }
+    static __device__ __forceinline__ void store(char* p, const F2 (&x)[1], int nch) {
+        float a, b;
+        split(x[0], a, b);
+        if constexpr (WIDE) {
+            *reinterpret_cast<float2*>(p) = make_float2(a, b);
+        } else {
+            reinterpret_cast<float*>(p)[0] = a;
+            if (nch > 1) reinterpret_cast<float*>(p)[1] = b;
+        }
     }
 };
-template <>
-struct Io<float, 1> {
-    using Raw = float;
-    static __device__ __forceinline__ Raw load(const void* p, int64_t i) { return __ldg(static_cast<const float*>(p) + i); }
-    static __device__ __forceinline__ void get(Raw r, float (&x)[1]) { x[0] = r; }
-    static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[1]) { static_cast<float*>(p)[i] = x[0]; }
-};
+// fp32 values of a lane's channels in arrays [..][D] (bias, states); nch as above.
+template <int NP>
+__device__ __forceinline__ void load_f32(const float* p, int nch, F2 (&x)[NP], float none) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+        x[j] = p == nullptr ? both(none) : pair(p[min(2 * j, nch - 1)], p[min(2 * j + 1, nch - 1)]);
+}
+template <int NP>
+__device__ __forceinline__ void store_f32(float* p, int nch, const F2 (&x)[NP]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        float a, b;
+        split(x[j], a, b);
+        if (2 * j < nch) p[2 * j] = a;
+        if (2 * j + 1 < nch) p[2 * j + 1] = b;
+    }
+}
 
-// s = sigmoid(x) and n = sigmoid(-x), each to a few units in the last place (n is not formed
-// as 1 - s, which loses it where s is near 1).  e = exp(-x) is capped at 2^125 so that s and
-// e*s stay normal numbers: for x below -86 (-inf included) s is 2^-125 and n is 1.  A NaN
-// stays one.
-__device__ __forceinline__ void gate(float x, float& s, float& n) {
-    float e = __expf(-x);
-    asm("min.NaN.f32 %0, %1, 0f7E000000;" : "=f"(e) : "f"(e));
-    s = __fdividef(1.0f, 1.0f + e);
-    n = e * s;
+// s = sigmoid(x + bias) and n = 1 - s = sigmoid(-x - bias), both good to a few units in the last
+// place: n is not formed as 1 - s, which loses it where s is near 1.  `lb` is -bias * log2(e).
+// e = exp(-(x + bias)) is capped at 2^125 so that s and e*s stay normal numbers: for arguments
+// below -86 (-inf included) s is 2^-125 and n is 1.  A NaN stays one.  The approximate
+// exponential and reciprocal are taken without their subnormal paths, which the cap rules out
+// and which flush an s or n below 2^-126 to 0.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ F2 exp2_capped(F2 t) {
+    float x, y;
+    split(t, x, y);
+    asm("min.NaN.f32 %0, %1, 0f42FA0000;" : "=f"(x) : "f"(x));
+    asm("min.NaN.f32 %0, %1, 0f42FA0000;" : "=f"(y) : "f"(y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(y));
+    return pair(x, y);
+}
+__device__ __forceinline__ F2 rcp_neg(F2 u) {   // -1 / u
+    float x, y;
+    split(u, x, y);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(-x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-y));
+    return pair(x, y);
+}
+__device__ __forceinline__ void gate(F2 x, F2& s, F2& n) {
+    const F2 e = exp2_capped(mul2(x, both(-kLog2e)));
+    s = rcp_neg(fma2(e, both(-1.0f), both(-1.0f)));
+    n = mul2(e, s);
+}
+// The same for the gate whose products run over thousands of rows, with one step of Newton's
+// method on the reciprocal: near 1 its last place is twice what rounding leaves.
+__device__ __forceinline__ void decay(F2 x, F2 lb, F2& s, F2& n) {
+    const F2 e = exp2_capped(fma2(x, both(-kLog2e), lb));
+    const F2 u = fma2(e, both(-1.0f), both(-1.0f));   // -(1 + e)
+    s = rcp_neg(u);
+    s = fma2(s, fma2(u, s, both(1.0f)), s);
+    n = mul2(e, s);
 }
 
 // A row map whose A carries the sign bit ignores the state before it (a document start lies in
 // its rows): -0 keeps its sign through products with the a >= 0 of later rows, and no value of
-// an earlier document, NaN included, passes.
-__device__ __forceinline__ bool cuts(float A) { return (__float_as_uint(A) >> 31) != 0; }
-__device__ __forceinline__ float apply(float A, float H, float h) { return cuts(A) ? H : fmaf(A, h, H); }
+// an earlier document, NaN included, passes.  docs: whether there are any.
+__device__ __forceinline__ F2 where_cut(F2 A, F2 yes, F2 no) {
+    float a, b, x, y, z, w;
+    split(A, a, b);
+    split(yes, x, y);
+    split(no, z, w);
+    return pair((__float_as_uint(a) >> 31) != 0 ? x : z, (__float_as_uint(b) >> 31) != 0 ? y : w);
+}
+__device__ __forceinline__ F2 apply(F2 A, F2 H, F2 h, bool docs) {
+    const F2 x = fma2(A, h, H);
+    return docs ? where_cut(A, H, x) : x;
+}
+// (A, H) := the map (A2, H2) after (A, H)
+__device__ __forceinline__ void compose(F2 A2, F2 H2, F2& A, F2& H, bool docs) {
+    H = apply(A2, H2, H, docs);
+    A = docs ? where_cut(A2, A2, mul2(A, A2)) : mul2(A, A2);
+}
 
 struct Strided {
-    const void* p;
-    int64_t sb, st;   // elements between sequences and between rows
+    char* p;
+    int64_t sb, st;   // bytes between sequences and between rows
 };
 struct ScanArgs {
     Strided f, v, r, y;   // y: the forward's output, or the backward's dy
@@ -119,386 +227,558 @@ struct GradArgs {
     float* partial;       // [B*S][D] sums of df, or null
 };
 
+// How a block cuts its rows and channels: LPR lanes make a row of CH channels, a lane's segment
+// has RPT rows, a warp SEGS segments.
+template <class T_, bool WIDE_, int LPR_, int RPT_>
+struct Shape {
+    using T = T_;
+    using X = Io<T_, WIDE_>;
+    static constexpr int NP = X::NP, LPR = LPR_, RPT = RPT_;
+    static constexpr int WARPS = 8, SEGS = 32 / LPR, CH = LPR * NP * 2, WROWS = SEGS * RPT, ROWS = WARPS * WROWS;
+};
+
+// Totals of the S blocks of a cluster, pushed by each block into every block's shared memory
+// (st.async) and counted there on an mbarrier: two of each in turn.  A block sends those of
+// iteration i+1 only after all its warps have read those of i, and i+2 needs everyone's i+1, so a
+// buffer is read before it is written again.
+template <class C>
+struct Exchange {
+    alignas(16) float A[2][kMaxCluster][C::CH], H[2][kMaxCluster][C::CH];
+    uint64_t bar[2];
+};
+template <int NP>
+__device__ __forceinline__ void push_pairs(const float* mine, const F2 (&x)[NP], const uint64_t* bar, uint32_t rank) {
+    const uint32_t at = ptx::mapa_shared(ptx::smem_u32(mine), rank), b = ptx::mapa_shared(ptx::smem_u32(bar), rank);
+    if constexpr (NP == 2) {
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(at),
+                     "l"(x[0].v), "l"(x[1].v), "r"(b) : "memory");
+    } else {
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(at), "l"(x[0].v), "r"(b)
+                     : "memory");
+    }
+}
+// Waits for a phase of the exchange, at most about two seconds: a peer block is resident and a
+// healthy wait takes microseconds.  On expiry the status word is set; the thread waits no more
+// and runs its steps to the end, so that the block's barriers still match (its results are void).
+__device__ __forceinline__ bool wait_peers(uint64_t* bar, uint32_t parity) {
+    const uint32_t b = ptx::smem_u32(bar);
+    uint64_t last = 0, waited = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(b), "r"(parity) : "memory");
+        if (ok) return true;
+        if ((it & 63u) == 63u) {
+            const uint64_t now = ptx::globaltimer();
+            // forward steps of the timer, each counted up to 1 ms, as in the GEMMs' waits
+            const int64_t step = last == 0 ? 0 : static_cast<int64_t>(now - last);
+            last = now;
+            if (step > 0) waited += static_cast<uint64_t>(step < 1000000 ? step : 1000000);
+            if (waited > 2000000000ull || it >= (1u << 30)) {
+                atomicExch(&g_scan_status, 1);
+                return false;
+            }
+        }
+    }
+}
+
 __device__ __forceinline__ int rows_live(const ScanArgs& a, int b) {
     return a.lengths != nullptr ? min(max(a.lengths[b], 0), a.T) : a.T;
 }
-// bit i: row0 + i (of the nl live rows of this warp) starts a document
-__device__ __forceinline__ uint32_t start_bits(const ScanArgs& a, int64_t b, int row0, int nl, int lane) {
+// bit i: row0 + i (of the nl live rows of this lane's segment) starts a document
+template <class C>
+__device__ __forceinline__ uint32_t start_bits(const ScanArgs& a, int64_t b, int row0, int nl) {
     if (a.starts == nullptr) return 0;
-    const int st = lane < nl ? a.starts[b * a.T + row0 + lane] : 0;
-    return __ballot_sync(0xffffffffu, st != 0);
+    const uint8_t* p = a.starts + b * a.T + row0;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i) m |= i < nl && p[i] != 0 ? 1u << i : 0u;
+    return m;
 }
-
-// N consecutive floats of this block's shared memory at `p`, read from block `rank` of the cluster.
-template <int N>
-__device__ __forceinline__ void load_peer(const float* p, uint32_t rank, float (&x)[N]) {
-    const uint32_t at = ptx::mapa_shared(ptx::smem_u32(p), rank);
-    if constexpr (N == 4) {
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at) : "memory");
+// The segment's rows of one tensor; rows that are not live stay zero.
+template <class C>
+__device__ __forceinline__ void load_rows(typename C::X::Raw (&raw)[C::RPT], const char* p, int64_t st, int nl, int nch) {
+    if (__all_sync(0xffffffffu, nl == C::RPT)) {
+#pragma unroll
+        for (int i = 0; i < C::RPT; ++i) raw[i] = C::X::load(p + i * st, nch);
     } else {
-        static_assert(N == 2, "two or four");
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(at) : "memory");
+#pragma unroll
+        for (int i = 0; i < C::RPT; ++i) {
+            raw[i] = typename C::X::Raw{};
+            if (i < nl) raw[i] = C::X::load(p + i * st, nch);
+        }
     }
 }
+// Within a warp: (PA, PH) = the map of the segments before this one (after it, for REV), from
+// each segment's (A, H).
+template <class C, bool REV>
+__device__ __forceinline__ void warp_prefix(const F2 (&A)[C::NP], const F2 (&H)[C::NP], F2 (&PA)[C::NP], F2 (&PH)[C::NP],
+                                            int seg, int c, bool docs) {
+#pragma unroll
+    for (int j = 0; j < C::NP; ++j) PA[j] = both(1.0f), PH[j] = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < C::SEGS - 1; ++k) {
+        const int from = REV ? C::SEGS - 1 - k : k;
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) {
+            const F2 Ak = shfl2(A[j], from * C::LPR + c), Hk = shfl2(H[j], from * C::LPR + c);
+            if (REV ? seg < from : seg > from) compose(Ak, Hk, PA[j], PH[j], docs);
+        }
+    }
+}
+// Pairs in shared memory: a lane's channels of one row of an [..][CH] array.
+template <int NP>
+__device__ __forceinline__ void get_s(const float* p, F2 (&x)[NP]) {
+    if constexpr (NP == 2) {
+        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p);
+        x[0].v = t.x, x[1].v = t.y;
+    } else {
+        x[0].v = *reinterpret_cast<const unsigned long long*>(p);
+    }
+}
+template <int NP>
+__device__ __forceinline__ void put_s(float* p, const F2 (&x)[NP]) {
+    if constexpr (NP == 2) *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x[0].v, x[1].v);
+    else *reinterpret_cast<unsigned long long*>(p) = x[0].v;
+}
+// h := the maps at A, H (rows `stride` floats apart) k0, k0 + dk, ... up to but without k1, after h
+template <int NP>
+__device__ __forceinline__ void fold(const float* A, const float* H, int stride, int k0, int k1, int dk, F2 (&h)[NP], bool docs) {
+    for (int k = k0; k != k1; k += dk) {
+        F2 Ak[NP], Hk[NP];
+        get_s(A + k * stride, Ak);
+        get_s(H + k * stride, Hk);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) h[j] = apply(Ak[j], Hk[j], h[j], docs);
+    }
+}
+// The same as one map: (PA, PH) := the maps at A, H after (PA, PH)
+template <int NP>
+__device__ __forceinline__ void fold_map(const float* A, const float* H, int stride, int k0, int k1, int dk, F2 (&PA)[NP],
+                                         F2 (&PH)[NP], bool docs) {
+    for (int k = k0; k != k1; k += dk) {
+        F2 Ak[NP], Hk[NP];
+        get_s(A + k * stride, Ak);
+        get_s(H + k * stride, Hk);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) compose(Ak[j], Hk[j], PA[j], PH[j], docs);
+    }
+}
+
+// What every block of the two kernels starts from.
+template <class C>
+struct Place {
+    int w, lane, seg, c, ch, rank, d, nch;
+    int64_t b;
+    bool on;      // this lane has channels; the others repeat the row's last and store nothing
+    __device__ __forceinline__ explicit Place(const ScanArgs& a) {
+        w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        seg = lane / C::LPR, c = lane % C::LPR, ch = c * C::NP * 2;
+        const int cl = blockIdx.x / a.S;
+        rank = blockIdx.x - cl * a.S;
+        b = cl / a.tiles;
+        const int d0 = (cl - static_cast<int>(b) * a.tiles) * C::CH + ch;
+        on = d0 < a.D;
+        d = on ? d0 : max(a.D - C::NP * 2, 0);
+        nch = min(a.D - d, C::NP * 2);
+    }
+    __device__ __forceinline__ char* at(const Strided& x) const {
+        return x.p + b * x.sb + static_cast<int64_t>(d) * static_cast<int64_t>(sizeof(typename C::T));
+    }
+};
 
 }  // namespace
 
 // ------------------------------------------------------------------------------ forward
 // CL: the S blocks of a cluster take S consecutive steps at a time; otherwise S is 1.
-template <class T, int VEC, int RPT, int WARPS, bool CL>
-__global__ void __launch_bounds__(WARPS * 32, 2) tern_scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
-    using X = Io<T, VEC>;
-    constexpr int ROWS = RPT * WARPS;
-    static_assert(kSaveRows % RPT == 0 && RPT <= 32, "saved states fall on warp boundaries");
-    __shared__ alignas(16) float agg[2][WARPS][32][2 * VEC];
-    __shared__ alignas(16) float tot[2][32][2 * VEC];      // CL: this block's (A, H)
-    __shared__ float carry_s[2][32][VEC];                  // not CL: the state after a step
+template <class C, bool CL>
+__global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
+    using X = typename C::X;
+    constexpr int NP = C::NP, RPT = C::RPT, WARPS = C::WARPS, ROWS = C::ROWS;
+    static_assert(kSaveRows % RPT == 0, "saved states fall on segment boundaries");
+    __shared__ alignas(16) float aggA[2][WARPS][C::CH], aggH[2][WARPS][C::CH];
+    __shared__ alignas(16) float carry_s[2][C::CH];                // not CL: the state after a step
+    __shared__ typename std::conditional<CL, Exchange<C>, int>::type ex;
+    const Place<C> q(a);
+    if constexpr (CL) {
+        if (threadIdx.x == 0) {
+            ptx::mbar_init(ptx::smem_u32(&ex.bar[0]), 1);
+            ptx::mbar_init(ptx::smem_u32(&ex.bar[1]), 1);
+            ptx::fence_mbar_init();
+        }
+        ptx::cluster_sync();
+    }
     ptx::pdl_trigger();
     ptx::pdl_wait();
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cl = blockIdx.x / a.S, rank = blockIdx.x - cl * a.S;
-    const int64_t b = cl / a.tiles;
-    const int d = (cl - static_cast<int>(b) * a.tiles) * (32 * VEC) + lane * VEC;
-    const bool on = d < a.D;
-    const int len = rows_live(a, static_cast<int>(b));
+    const bool docs = a.starts != nullptr;
+    const int len = rows_live(a, static_cast<int>(q.b));
     const int64_t nsaved = (static_cast<int64_t>(a.T) + kSaveRows - 1) / kSaveRows;
-    const int64_t fo = b * a.f.sb + d, vo = b * a.v.sb + d, ro = b * a.r.sb + d, yo = b * a.y.sb + d;
+    const char *fp = q.at(a.f), *vp = q.at(a.v), *rp = q.at(a.r);
+    char* yp = q.at(a.y);
 
-    float bias[VEC], carry[VEC];
+    F2 lb[NP], carry[NP];
+    load_f32(a.f_bias == nullptr ? nullptr : a.f_bias + q.d, q.nch, lb, 0.0f);
+    load_f32(a.h_in == nullptr ? nullptr : a.h_in + q.b * a.D + q.d, q.nch, carry, 0.0f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        bias[j] = on && a.f_bias != nullptr ? a.f_bias[d + j] : 0.0f;
-        carry[j] = on && a.h_in != nullptr ? a.h_in[b * a.D + d + j] : 0.0f;
-    }
+    for (int j = 0; j < NP; ++j) lb[j] = mul2(lb[j], both(-kLog2e));
     const int steps = (a.T + ROWS - 1) / ROWS;
     const int iters = (steps + a.S - 1) / a.S;
+    [[maybe_unused]] bool ok = true;
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
-        const int64_t first = static_cast<int64_t>(it * a.S + rank) * ROWS + w * RPT;
+        const int64_t first = static_cast<int64_t>(it * a.S + q.rank) * ROWS + q.w * C::WROWS + q.seg * RPT;
         const int row0 = first < a.T ? static_cast<int>(first) : a.T;
-        const int nl = min(max(len - row0, 0), RPT);   // live rows of this warp
-        const uint32_t cut = start_bits(a, b, row0, nl, lane);
-        typename X::Raw rf[RPT], rv[RPT], rr[RPT];
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            rf[i] = typename X::Raw{}, rv[i] = typename X::Raw{}, rr[i] = typename X::Raw{};
-            if (on && i < nl) {
-                const int64_t t = row0 + i;
-                rf[i] = X::load(a.f.p, fo + t * a.f.st);
-                rv[i] = X::load(a.v.p, vo + t * a.v.st);
-                rr[i] = X::load(a.r.p, ro + t * a.r.st);
-            }
+        const int nl = min(max(len - row0, 0), RPT);   // live rows of this segment
+        if constexpr (CL) {
+            if (threadIdx.x == 0)
+                ptx::mbar_arrive_expect_tx(ptx::smem_u32(&ex.bar[p]), static_cast<uint32_t>(a.S * C::CH * 2 * sizeof(float)));
         }
-        // (A, H) of this thread's rows
-        float ga[RPT][VEC], gb[RPT][VEC], A[VEC], H[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) A[j] = 1.0f, H[j] = 0.0f;
+        typename X::Raw rf[RPT], rv[RPT], rr[RPT];
+        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch);
+        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch);
+        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch);
+        const uint32_t cut = start_bits<C>(a, q.b, row0, nl);
+        // (A, H) of this lane's rows
+        F2 ga[RPT][NP], gb[RPT][NP], A[NP], H[NP];
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            float f[VEC], v[VEC];
+            F2 f[NP], v[NP], n;
             X::get(rf[i], f);
             X::get(rv[i], v);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float s, n;
-                gate(f[j] + bias[j], s, n);
-                ga[i][j] = i < nl ? s : 1.0f;
-                gb[i][j] = i < nl ? n * v[j] : 0.0f;
+            for (int j = 0; j < NP; ++j) {
+                decay(f[j], lb[j], ga[i][j], n);
+                gb[i][j] = mul2(n, v[j]);
             }
         }
-        if (cut == 0) {
+        if (nl < RPT) {
 #pragma unroll
             for (int i = 0; i < RPT; ++i)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) A[j] *= ga[i][j], H[j] = fmaf(ga[i][j], H[j], gb[i][j]);
-        } else {
+                for (int j = 0; j < NP; ++j)
+                    if (i >= nl) ga[i][j] = both(1.0f), gb[i][j] = both(0.0f);
+        }
+        if (cut != 0) {
 #pragma unroll
             for (int i = 0; i < RPT; ++i)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const bool c = (cut >> i) & 1u;
-                    A[j] = c ? -0.0f : A[j] * ga[i][j];
-                    H[j] = c ? gb[i][j] : fmaf(ga[i][j], H[j], gb[i][j]);
-                }
+                for (int j = 0; j < NP; ++j)
+                    if ((cut >> i) & 1u) ga[i][j] = both(-0.0f);
         }
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) agg[p][w][lane][j] = A[j], agg[p][w][lane][VEC + j] = H[j];
+        for (int j = 0; j < NP; ++j) A[j] = ga[0][j], H[j] = gb[0][j];
+        if (cut == 0) {
+#pragma unroll
+            for (int i = 1; i < RPT; ++i)
+#pragma unroll
+                for (int j = 0; j < NP; ++j) A[j] = mul2(A[j], ga[i][j]), H[j] = fma2(ga[i][j], H[j], gb[i][j]);
+        } else {
+#pragma unroll
+            for (int i = 1; i < RPT; ++i)
+#pragma unroll
+                for (int j = 0; j < NP; ++j) compose(ga[i][j], gb[i][j], A[j], H[j], true);
+        }
+        F2 PA[NP], PH[NP];
+        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, docs);
+        if (q.seg == C::SEGS - 1) {
+            F2 TA[NP], TH[NP];
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                TA[j] = PA[j], TH[j] = PH[j];
+                compose(A[j], H[j], TA[j], TH[j], docs);
+            }
+            put_s(&aggA[p][q.w][q.ch], TA);
+            put_s(&aggH[p][q.w][q.ch], TH);
+        }
         __syncthreads();
         // the state before this block's rows
-        float h[VEC];
+        F2 h[NP];
         if constexpr (CL) {
-            if (w == WARPS - 1) {
+            if (q.w == WARPS - 1) {   // the block's total, to every block: a segment's lanes each serve S / SEGS of them
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) A[j] = 1.0f, H[j] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < WARPS; ++k)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float Ak = agg[p][k][lane][j], Hk = agg[p][k][lane][VEC + j];
-                        H[j] = apply(Ak, Hk, H[j]);
-                        A[j] = cuts(Ak) ? Ak : A[j] * Ak;
-                    }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) tot[p][lane][j] = A[j], tot[p][lane][VEC + j] = H[j];
-            }
-            ptx::cluster_sync();
-            for (int k = 0; k < a.S; ++k) {
-                float x[2 * VEC];
-                load_peer(&tot[p][lane][0], k, x);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    if (k == rank) h[j] = carry[j];
-                    carry[j] = apply(x[j], x[VEC + j], carry[j]);
+                for (int j = 0; j < NP; ++j) A[j] = both(1.0f), H[j] = both(0.0f);
+                fold_map(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, 0, WARPS, 1, A, H, docs);
+                for (int k = q.seg; k < a.S; k += C::SEGS) {
+                    push_pairs(&ex.A[p][q.rank][q.ch], A, &ex.bar[p], k);
+                    push_pairs(&ex.H[p][q.rank][q.ch], H, &ex.bar[p], k);
                 }
             }
+            ok = ok && wait_peers(&ex.bar[p], (it >> 1) & 1);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) h[j] = carry[j];
+            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, h, docs);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) carry[j] = h[j];
+            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, q.rank, a.S, 1, carry, docs);
         } else {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) h[j] = it == 0 ? carry[j] : carry_s[p ^ 1][lane][j];
+            for (int j = 0; j < NP; ++j) h[j] = carry[j];
+            if (it > 0) get_s(&carry_s[p ^ 1][q.ch], h);
         }
-        for (int k = 0; k < w; ++k)
+        fold(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, 0, q.w, 1, h, docs);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) h[j] = apply(agg[p][k][lane][j], agg[p][k][lane][VEC + j], h[j]);
-        if (a.saved != nullptr && on && row0 < a.T && row0 % kSaveRows == 0) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) a.saved[(b * nsaved + row0 / kSaveRows) * a.D + d + j] = h[j];
-        }
-        // the rows again, from the state before them
+        for (int j = 0; j < NP; ++j) h[j] = apply(PA[j], PH[j], h[j], docs);
+        if (a.saved != nullptr && q.on && row0 < a.T && row0 % kSaveRows == 0)
+            store_f32(a.saved + (q.b * nsaved + row0 / kSaveRows) * a.D + q.d, q.nch, h);
+        // the rows again, from the state before them; gb becomes the states
         if (cut == 0) {
 #pragma unroll
             for (int i = 0; i < RPT; ++i)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) h[j] = fmaf(ga[i][j], h[j], gb[i][j]), gb[i][j] = h[j];
+                for (int j = 0; j < NP; ++j) h[j] = fma2(ga[i][j], h[j], gb[i][j]), gb[i][j] = h[j];
         } else {
 #pragma unroll
             for (int i = 0; i < RPT; ++i)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    h[j] = (cut >> i) & 1u ? gb[i][j] : fmaf(ga[i][j], h[j], gb[i][j]);
-                    gb[i][j] = h[j];
-                }
+                for (int j = 0; j < NP; ++j) h[j] = apply(ga[i][j], gb[i][j], h[j], true), gb[i][j] = h[j];
         }
         if constexpr (!CL) {
-            if (w == WARPS - 1) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) carry_s[p][lane][j] = h[j];
-            }
+            if (q.w == WARPS - 1 && q.seg == C::SEGS - 1) put_s(&carry_s[p][q.ch], h);
         }
+        char* yr = yp + row0 * a.y.st;
+        const int nr = q.on ? min(a.T - row0, RPT) : 0;   // rows to write
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            float r[VEC], y[VEC];
+            F2 r[NP], y[NP], s, n;
             X::get(rr[i], r);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float s, n;
+            for (int j = 0; j < NP; ++j) {
                 gate(r[j], s, n);
-                y[j] = i < nl ? s * gb[i][j] : 0.0f;
+                y[j] = mul2(s, gb[i][j]);
             }
-            if (on && row0 + i < a.T) X::store(const_cast<void*>(a.y.p), yo + static_cast<int64_t>(row0 + i) * a.y.st, y);
+            if (nl < RPT) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+                    if (i >= nl) y[j] = both(0.0f);
+            }
+            if (i < nr) X::store(yr + i * a.y.st, y, q.nch);
         }
     }
     if constexpr (CL) {
-        ptx::cluster_sync();   // the peers have read this block's totals
+        ptx::cluster_sync();   // no block leaves while another may still write to it
     } else {
         __syncthreads();
-        if (iters > 0) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) carry[j] = carry_s[(iters - 1) & 1][lane][j];
-        }
+        if (iters > 0) get_s(&carry_s[(iters - 1) & 1][q.ch], carry);
     }
-    if (a.h_out != nullptr && on && rank == 0 && w == 0) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) a.h_out[b * a.D + d + j] = carry[j];
-    }
+    if (a.h_out != nullptr && q.on && q.rank == 0 && q.w == 0 && q.seg == 0)
+        store_f32(a.h_out + q.b * a.D + q.d, q.nch, carry);
 }
 
 // ------------------------------------------------------------------------------ backward
-template <class T, int VEC, bool CL>
-__global__ void __launch_bounds__(256, 2) tern_scan_bwd_kernel(const __grid_constant__ GradArgs g) {
-    using X = Io<T, VEC>;
-    constexpr int RPT = 8, WARPS = 8, ROWS = RPT * WARPS;
-    static_assert(ROWS == kSaveRows, "a step starts from a saved state");
+template <class C, bool CL>
+__global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_bwd_kernel(const __grid_constant__ GradArgs g) {
+    using X = typename C::X;
+    constexpr int NP = C::NP, RPT = C::RPT, WARPS = C::WARPS, ROWS = C::ROWS;
+    constexpr int GROUP = kSaveRows / C::WROWS;   // warps from one saved state to the next
+    static_assert(ROWS % kSaveRows == 0 && kSaveRows % C::WROWS == 0, "steps start from saved states");
     const ScanArgs& a = g.s;
-    __shared__ alignas(16) float agg[2][WARPS][32][2 * VEC];   // A and G (the gradient's fold)
-    __shared__ alignas(16) float aggh[2][WARPS][32][VEC];      // H (the state's fold)
-    __shared__ alignas(16) float tot[2][32][2 * VEC];
-    __shared__ float carry_s[2][32][VEC];
+    __shared__ alignas(16) float aggA[2][WARPS][C::CH], aggH[2][WARPS][C::CH], aggG[2][WARPS][C::CH];
+    __shared__ alignas(16) float carry_s[2][C::CH];
+    __shared__ typename std::conditional<CL, Exchange<C>, int>::type ex;
+    const Place<C> q(a);
+    if constexpr (CL) {
+        if (threadIdx.x == 0) {
+            ptx::mbar_init(ptx::smem_u32(&ex.bar[0]), 1);
+            ptx::mbar_init(ptx::smem_u32(&ex.bar[1]), 1);
+            ptx::fence_mbar_init();
+        }
+        ptx::cluster_sync();
+    }
     ptx::pdl_trigger();
     ptx::pdl_wait();
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cl = blockIdx.x / a.S, rank = blockIdx.x - cl * a.S;
-    const int64_t b = cl / a.tiles;
-    const int d = (cl - static_cast<int>(b) * a.tiles) * (32 * VEC) + lane * VEC;
-    const bool on = d < a.D;
-    const int len = rows_live(a, static_cast<int>(b));
+    const bool docs = a.starts != nullptr;
+    const int len = rows_live(a, static_cast<int>(q.b));
+    const int64_t nsaved = (static_cast<int64_t>(a.T) + kSaveRows - 1) / kSaveRows;
     const int steps = (a.T + ROWS - 1) / ROWS;
     const int iters = (steps + a.S - 1) / a.S;
-    const int64_t fo = b * a.f.sb + d, vo = b * a.v.sb + d, ro = b * a.r.sb + d, yo = b * a.y.sb + d;
-    const int64_t dfo = b * g.df.sb + d, dvo = b * g.dv.sb + d, dro = b * g.dr.sb + d;
+    const char *fp = q.at(a.f), *vp = q.at(a.v), *rp = q.at(a.r), *yp = q.at(a.y);
+    char *dfp = q.at(g.df), *dvp = q.at(g.dv), *drp = q.at(g.dr);
 
-    float bias[VEC], carry[VEC], dbias[VEC];
+    [[maybe_unused]] bool ok = true;
+    F2 lb[NP], carry[NP], dbias[NP];
+    load_f32(a.f_bias == nullptr ? nullptr : a.f_bias + q.d, q.nch, lb, 0.0f);
+    load_f32(a.h_in == nullptr ? nullptr : a.h_in + q.b * a.D + q.d, q.nch, carry, 0.0f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        bias[j] = on && a.f_bias != nullptr ? a.f_bias[d + j] : 0.0f;
-        carry[j] = on && a.h_in != nullptr ? a.h_in[b * a.D + d + j] : 0.0f;
-        dbias[j] = 0.0f;
-    }
+    for (int j = 0; j < NP; ++j) lb[j] = mul2(lb[j], both(-kLog2e)), dbias[j] = both(0.0f);
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
-        const int step = steps - 1 - (it * a.S + rank);   // below 0: nothing left for this block
-        const int row0 = step >= 0 ? min(step * ROWS + w * RPT, a.T) : a.T;
+        const int step = steps - 1 - (it * a.S + q.rank);   // below 0: nothing left for this block
+        const int64_t first = static_cast<int64_t>(step) * ROWS + q.w * C::WROWS + q.seg * RPT;
+        const int row0 = step >= 0 && first < a.T ? static_cast<int>(first) : a.T;
         const int nl = min(max(len - row0, 0), RPT);
-        const uint32_t cut = start_bits(a, b, row0, nl, lane);
-        typename X::Raw rf[RPT], rv[RPT], rr[RPT], rd[RPT];
-        float h[VEC];
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            rf[i] = rv[i] = rr[i] = rd[i] = typename X::Raw{};
-            if (on && i < nl) {
-                const int64_t t = row0 + i;
-                rf[i] = X::load(a.f.p, fo + t * a.f.st);
-                rv[i] = X::load(a.v.p, vo + t * a.v.st);
-                rr[i] = X::load(a.r.p, ro + t * a.r.st);
-                rd[i] = X::load(a.y.p, yo + t * a.y.st);
-            }
+        if constexpr (CL) {
+            if (threadIdx.x == 0)
+                ptx::mbar_arrive_expect_tx(ptx::smem_u32(&ex.bar[p]), static_cast<uint32_t>(a.S * C::CH * 2 * sizeof(float)));
         }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            h[j] = on && step >= 0 ? a.saved[(b * steps + step) * a.D + d + j] : 0.0f;
-        // per row: s = a, n = 1 - a, o = g = sigmoid(r) dy, q = sigmoid(-r)
-        float s[RPT][VEC], n[RPT][VEC], o[RPT][VEC], q[RPT][VEC];
-        float A[VEC], H[VEC], G[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) A[j] = 1.0f, H[j] = 0.0f, G[j] = 0.0f;
+        typename X::Raw rf[RPT], rv[RPT], rr[RPT], rd[RPT];
+        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch);
+        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch);
+        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch);
+        load_rows<C>(rd, yp + row0 * a.y.st, a.y.st, nl, q.nch);
+        const uint32_t cut = start_bits<C>(a, q.b, row0, nl);
+        F2 h[NP];
+        load_f32(row0 < a.T ? a.saved + (q.b * nsaved + row0 / kSaveRows) * a.D + q.d : nullptr, q.nch, h, 0.0f);
+        // per row: s = a, n = 1 - a, o = g = sigmoid(r) dy, x = sigmoid(-r)
+        F2 s[RPT][NP], n[RPT][NP], o[RPT][NP], x[RPT][NP], A[NP], H[NP], G[NP];
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            float f[VEC], v[VEC], r[VEC], dy[VEC];
+            F2 f[NP], r[NP], dy[NP], so;
             X::get(rf[i], f);
-            X::get(rv[i], v);
             X::get(rr[i], r);
             X::get(rd[i], dy);
-            const bool c = (cut >> i) & 1u;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float so;
-                gate(f[j] + bias[j], s[i][j], n[i][j]);
-                gate(r[j], so, q[i][j]);
-                o[i][j] = so * dy[j];
-                if (i >= nl) s[i][j] = 1.0f, n[i][j] = 0.0f, o[i][j] = 0.0f;
-                A[j] = c ? -0.0f : A[j] * s[i][j];
-                H[j] = c ? n[i][j] * v[j] : fmaf(s[i][j], H[j], n[i][j] * v[j]);
+            for (int j = 0; j < NP; ++j) {
+                decay(f[j], lb[j], s[i][j], n[i][j]);
+                gate(r[j], so, x[i][j]);
+                o[i][j] = mul2(so, dy[j]);
             }
         }
+        if (nl < RPT) {
+#pragma unroll
+            for (int i = 0; i < RPT; ++i)
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+                    if (i >= nl) s[i][j] = both(1.0f), n[i][j] = both(0.0f), o[i][j] = both(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            F2 v[NP];
+            X::get(rv[i], v);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                const F2 m = (cut >> i) & 1u ? both(-0.0f) : s[i][j], b = mul2(n[i][j], v[j]);
+                if (i == 0) A[j] = m, H[j] = b;
+                else if (cut == 0) A[j] = mul2(A[j], m), H[j] = fma2(m, H[j], b);
+                else compose(m, b, A[j], H[j], true);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NP; ++j) G[j] = both(0.0f);
 #pragma unroll
         for (int i = RPT - 1; i >= 0; --i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) G[j] = (cut >> i) & 1u ? 0.0f : s[i][j] * (o[i][j] + G[j]);
+            for (int j = 0; j < NP; ++j) {
+                G[j] = mul2(s[i][j], add2(o[i][j], G[j]));
+                if ((cut >> i) & 1u) G[j] = both(0.0f);
+            }
+        F2 PA[NP], PH[NP], QA[NP], QG[NP];
+        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, docs);
+        warp_prefix<C, true>(A, G, QA, QG, q.seg, q.c, docs);
+        if (q.seg == C::SEGS - 1) {
+            F2 TA[NP], TH[NP];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            agg[p][w][lane][j] = A[j], agg[p][w][lane][VEC + j] = G[j];
-            aggh[p][w][lane][j] = H[j];
+            for (int j = 0; j < NP; ++j) {
+                TA[j] = PA[j], TH[j] = PH[j];
+                compose(A[j], H[j], TA[j], TH[j], docs);
+            }
+            put_s(&aggA[p][q.w][q.ch], TA);
+            put_s(&aggH[p][q.w][q.ch], TH);
+        }
+        if (q.seg == 0) {
+            F2 TG[NP];
+#pragma unroll
+            for (int j = 0; j < NP; ++j) TG[j] = apply(A[j], G[j], QG[j], docs);
+            put_s(&aggG[p][q.w][q.ch], TG);
         }
         __syncthreads();
-        float e[VEC];   // e after this thread's rows
+        F2 e[NP];   // e after this segment's rows
         if constexpr (CL) {
-            if (w == 0) {
+            if (q.w == 0) {
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) A[j] = 1.0f, G[j] = 0.0f;
-#pragma unroll
-                for (int k = WARPS - 1; k >= 0; --k)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float Ak = agg[p][k][lane][j], Gk = agg[p][k][lane][VEC + j];
-                        G[j] = apply(Ak, Gk, G[j]);
-                        A[j] = cuts(Ak) ? Ak : A[j] * Ak;
-                    }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) tot[p][lane][j] = A[j], tot[p][lane][VEC + j] = G[j];
-            }
-            ptx::cluster_sync();
-            for (int k = 0; k < a.S; ++k) {
-                float x[2 * VEC];
-                load_peer(&tot[p][lane][0], k, x);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    if (k == rank) e[j] = carry[j];
-                    carry[j] = apply(x[j], x[VEC + j], carry[j]);
+                for (int j = 0; j < NP; ++j) A[j] = both(1.0f), G[j] = both(0.0f);
+                fold_map(&aggA[p][0][q.ch], &aggG[p][0][q.ch], C::CH, WARPS - 1, -1, -1, A, G, docs);
+                for (int k = q.seg; k < a.S; k += C::SEGS) {
+                    push_pairs(&ex.A[p][q.rank][q.ch], A, &ex.bar[p], k);
+                    push_pairs(&ex.H[p][q.rank][q.ch], G, &ex.bar[p], k);
                 }
             }
+            ok = ok && wait_peers(&ex.bar[p], (it >> 1) & 1);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) e[j] = carry[j];
+            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, e, docs);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) carry[j] = e[j];
+            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, q.rank, a.S, 1, carry, docs);
         } else {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) e[j] = it == 0 ? carry[j] : carry_s[p ^ 1][lane][j];
+            for (int j = 0; j < NP; ++j) e[j] = carry[j];
+            if (it > 0) get_s(&carry_s[p ^ 1][q.ch], e);
         }
-        for (int k = WARPS - 1; k > w; --k)
+        fold(&aggA[p][0][q.ch], &aggG[p][0][q.ch], C::CH, WARPS - 1, q.w, -1, e, docs);
+        fold(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, q.w / GROUP * GROUP, q.w, 1, h, docs);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) e[j] = apply(agg[p][k][lane][j], agg[p][k][lane][VEC + j], e[j]);
-        for (int k = 0; k < w; ++k)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) h[j] = apply(agg[p][k][lane][j], aggh[p][k][lane][j], h[j]);
-        // the states before and after each row: hp = h_{t-1}; q becomes dr = g h (1 - sigmoid(r))
-        float hp[RPT][VEC];
+        for (int j = 0; j < NP; ++j) {
+            e[j] = apply(QA[j], QG[j], e[j], docs);
+            h[j] = apply(PA[j], PH[j], h[j], docs);
+        }
+        // o stays g; x becomes dr = g h (1 - sigmoid(r)); hv = h_{t-1} - v
+        F2 hv[RPT][NP];
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            float v[VEC];
+            F2 v[NP];
             X::get(rv[i], v);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                hp[i][j] = (cut >> i) & 1u ? 0.0f : h[j];
-                h[j] = fmaf(s[i][j], hp[i][j], n[i][j] * v[j]);
-                q[i][j] = i < nl ? o[i][j] * h[j] * q[i][j] : 0.0f;
+            for (int j = 0; j < NP; ++j) {
+                if ((cut >> i) & 1u) h[j] = both(0.0f);
+                hv[i][j] = fma2(v[j], both(-1.0f), h[j]);
+                h[j] = fma2(s[i][j], h[j], mul2(n[i][j], v[j]));
+                x[i][j] = mul2(mul2(o[i][j], h[j]), x[i][j]);
             }
         }
+        const int nr = q.on ? min(a.T - row0, RPT) : 0;   // rows to write
+        char *dfr = dfp + row0 * g.df.st, *dvr = dvp + row0 * g.dv.st, *drr = drp + row0 * g.dr.st;
 #pragma unroll
         for (int i = RPT - 1; i >= 0; --i) {
-            float v[VEC], df[VEC], dv[VEC];
-            X::get(rv[i], v);
+            F2 df[NP], dv[NP];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float dh = o[i][j] + e[j];
-                const float e2 = s[i][j] * dh;
-                dv[j] = i < nl ? n[i][j] * dh : 0.0f;
-                df[j] = i < nl ? e2 * n[i][j] * (hp[i][j] - v[j]) : 0.0f;
-                dbias[j] += df[j];
-                e[j] = (cut >> i) & 1u ? 0.0f : e2;
+            for (int j = 0; j < NP; ++j) {
+                const F2 dh = add2(o[i][j], e[j]);
+                const F2 e2 = mul2(s[i][j], dh);
+                dv[j] = mul2(n[i][j], dh);
+                df[j] = mul2(mul2(e2, n[i][j]), hv[i][j]);
+                if (i >= nl) dv[j] = df[j] = x[i][j] = both(0.0f);
+                dbias[j] = add2(dbias[j], df[j]);
+                e[j] = (cut >> i) & 1u ? both(0.0f) : e2;
             }
-            if (on && row0 + i < a.T) {
-                const int64_t t = row0 + i;
-                X::store(const_cast<void*>(g.df.p), dfo + t * g.df.st, df);
-                X::store(const_cast<void*>(g.dv.p), dvo + t * g.dv.st, dv);
-                X::store(const_cast<void*>(g.dr.p), dro + t * g.dr.st, q[i]);
+            if (i < nr) {
+                X::store(dfr + i * g.df.st, df, q.nch);
+                X::store(dvr + i * g.dv.st, dv, q.nch);
+                X::store(drr + i * g.dr.st, x[i], q.nch);
             }
         }
         if constexpr (!CL) {
-            if (w == 0) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) carry_s[p][lane][j] = e[j];
-            }
+            if (q.w == 0 && q.seg == 0) put_s(&carry_s[p][q.ch], e);
         }
     }
-    if constexpr (CL) ptx::cluster_sync();   // the peers have read this block's totals
+    if constexpr (CL) ptx::cluster_sync();   // no block leaves while another may still write to it
     __syncthreads();
     if constexpr (!CL) {
-        if (iters > 0) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) carry[j] = carry_s[(iters - 1) & 1][lane][j];
-        }
+        if (iters > 0) get_s(&carry_s[(iters - 1) & 1][q.ch], carry);
     }
-    if (a.h_out != nullptr && on && rank == 0 && w == 0) {
+    if (a.h_out != nullptr && q.on && q.rank == 0 && q.w == 0 && q.seg == 0)
+        store_f32(a.h_out + q.b * a.D + q.d, q.nch, carry);
+    if (g.partial != nullptr) {   // this block's sum of df: a warp's segments, then the warps, in order
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a.h_out[b * a.D + d + j] = carry[j];
-    }
-    if (g.partial != nullptr) {   // this block's sum of df, warps in order
+        for (int j = 0; j < NP; ++j)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) aggh[0][w][lane][j] = dbias[j];
-        __syncthreads();
-        if (w == 0 && on) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int k = 0; k < WARPS; ++k) sum += aggh[0][k][lane][j];
-                g.partial[(b * a.S + rank) * a.D + d + j] = sum;
+            for (int k = 1; k < C::SEGS; ++k) {
+                const F2 other = shfl2(dbias[j], (k * C::LPR + q.c) & 31);
+                if (q.seg == 0) dbias[j] = add2(dbias[j], other);
             }
+        if (q.seg == 0) put_s(&aggH[0][q.w][q.ch], dbias);
+        __syncthreads();
+        if (q.w == 0 && q.seg == 0 && q.on) {
+            F2 sum[NP];
+            get_s(&aggH[0][0][q.ch], sum);
+            for (int k = 1; k < WARPS; ++k) {
+                F2 part[NP];
+                get_s(&aggH[0][k][q.ch], part);
+#pragma unroll
+                for (int j = 0; j < NP; ++j) sum[j] = add2(sum[j], part[j]);
+            }
+            store_f32(g.partial + (q.b * a.S + q.rank) * a.D + q.d, q.nch, sum);
         }
     }
 }
@@ -527,39 +807,43 @@ __global__ void __launch_bounds__(256) tern_scan_dbias_kernel(const float* __res
 
 // ------------------------------------------------------------------------------ one token
 struct StepArgs {
-    const void *f, *v, *r;
+    const char *f, *v, *r;
+    char* y;
     const float* f_bias;
     const float* h_in;
     float* h_out;
-    void* y;
-    int64_t rows, f_sb, v_sb, r_sb, y_sb;
+    int64_t rows, f_sb, v_sb, r_sb, y_sb;   // strides in bytes
     int D;
 };
 
-template <class T, int VEC>
+template <class T, bool WIDE>
 __global__ void __launch_bounds__(128) tern_scan_step_kernel(const __grid_constant__ StepArgs a) {
-    using X = Io<T, VEC>;
+    using X = Io<T, WIDE>;
+    constexpr int NP = X::NP;
     ptx::pdl_trigger();
     ptx::pdl_wait();
-    const int per_row = a.D / VEC;
+    const int per_row = (a.D + 2 * NP - 1) / (2 * NP);
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
     const int64_t b = i / per_row;
     if (b >= a.rows) return;
-    const int d = static_cast<int>(i - b * per_row) * VEC;
-    float f[VEC], v[VEC], r[VEC], y[VEC];
-    X::get(X::load(a.f, b * a.f_sb + d), f);
-    X::get(X::load(a.v, b * a.v_sb + d), v);
-    X::get(X::load(a.r, b * a.r_sb + d), r);
+    const int d = static_cast<int>(i - b * per_row) * 2 * NP, nch = min(a.D - d, 2 * NP);
+    const int64_t at = static_cast<int64_t>(d) * static_cast<int64_t>(sizeof(T)), hd = b * a.D + d;
+    F2 f[NP], v[NP], r[NP], h[NP], lb[NP], y[NP];
+    X::get(X::load(a.f + b * a.f_sb + at, nch), f);
+    X::get(X::load(a.v + b * a.v_sb + at, nch), v);
+    X::get(X::load(a.r + b * a.r_sb + at, nch), r);
+    load_f32(a.h_in + hd, nch, h, 0.0f);
+    load_f32(a.f_bias == nullptr ? nullptr : a.f_bias + d, nch, lb, 0.0f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        float s, n, o, q;
-        gate(f[j] + (a.f_bias != nullptr ? a.f_bias[d + j] : 0.0f), s, n);
+    for (int j = 0; j < NP; ++j) {
+        F2 s, n, o, q;
+        decay(f[j], mul2(lb[j], both(-kLog2e)), s, n);
         gate(r[j], o, q);
-        const float h = fmaf(s, a.h_in[b * a.D + d + j], n * v[j]);
-        a.h_out[b * a.D + d + j] = h;
-        y[j] = o * h;
+        h[j] = fma2(s, h[j], mul2(n, v[j]));
+        y[j] = mul2(o, h[j]);
     }
-    X::store(a.y, b * a.y_sb + d, y);
+    store_f32(a.h_out + hd, nch, h);
+    X::store(a.y + b * a.y_sb + at, y, nch);
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -580,32 +864,37 @@ int launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, unsi
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cluster > 8) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     TERN_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
     return TERN_OK;
 }
 
 size_t elem(int dtype) { return dtype == TERN_F32 ? 4 : 2; }
 
-// TERN_OK when x can be read or written as `rows` of D elements, else the error; vec2 is cleared
-// when its address or strides keep it from pairs of elements.
-int check_act(const tern_act& x, int dtype, bool& vec2) {
-    const size_t es = elem(dtype);
+// TERN_OK when x can be read or written as rows of elements, else the error; `wide` is cleared
+// when its address or strides keep it from 8-byte accesses.
+int check_act(const tern_act& x, int dtype, bool& wide) {
+    const int64_t es = static_cast<int64_t>(elem(dtype));
     if (x.p == nullptr || x.stride_b < 0 || x.stride_t < 0) return TERN_ERR_ARG;
+    if (x.stride_b > INT64_MAX / 4 / es || x.stride_t > INT64_MAX / 4 / es) return TERN_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(x.p) % es != 0) return TERN_ERR_ALIGN;
-    if (reinterpret_cast<uintptr_t>(x.p) % (2 * es) != 0 || x.stride_b % 2 != 0 || x.stride_t % 2 != 0) vec2 = false;
+    if (reinterpret_cast<uintptr_t>(x.p) % 8 != 0 || x.stride_b * es % 8 != 0 || x.stride_t * es % 8 != 0) wide = false;
     return TERN_OK;
 }
-Strided strided(const tern_act& x) { return Strided{x.p, x.stride_b, x.stride_t}; }
+Strided strided(const tern_act& x, int dtype) {
+    const int64_t es = static_cast<int64_t>(elem(dtype));
+    return Strided{static_cast<char*>(x.p), x.stride_b * es, x.stride_t * es};
+}
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-int check_scan(const tern_scan* s, bool& vec2) {
+int check_scan(const tern_scan* s, bool& wide) {
     if (s == nullptr || (s->dtype != TERN_BF16 && s->dtype != TERN_F32)) return TERN_ERR_ARG;
     if (s->B < 0 || s->T < 0 || s->D < 0 || s->T > INT32_MAX - 256 || s->D > INT32_MAX - 256 || s->B > INT32_MAX - 256) return TERN_ERR_ARG;
-    vec2 = s->D % 2 == 0;
+    wide = s->D * static_cast<int64_t>(elem(s->dtype)) % 8 == 0;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (s->T > 0) {
         for (const tern_act* x : {&s->f, &s->v, &s->r})
-            if (int st = check_act(*x, s->dtype, vec2)) return st;
+            if (int st = check_act(*x, s->dtype, wide)) return st;
     }
     if (!aligned4(s->f_bias) || !aligned4(s->lengths)) return TERN_ERR_ALIGN;
     return TERN_OK;
@@ -621,30 +910,29 @@ int cluster_size(int64_t blocks, int64_t steps, int num_sms) {
 
 int64_t steps_of(int64_t T, int64_t rows) { return (T + rows - 1) / rows; }
 
-template <class T, int VEC>
+template <class C>
 int launch_fwd(const ScanArgs& a0, int64_t B, int num_sms, cudaStream_t s) {
-    constexpr int RPT = 16, WARPS = 8;
     ScanArgs a = a0;
-    a.tiles = (a.D + 32 * VEC - 1) / (32 * VEC);
+    a.tiles = (a.D + C::CH - 1) / C::CH;
     const int64_t blocks = B * a.tiles;
-    a.S = cluster_size(blocks, steps_of(a.T, RPT * WARPS), num_sms);
+    a.S = cluster_size(blocks, steps_of(a.T, C::ROWS), num_sms);
     if (blocks * a.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * a.S);
-    if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<T, VEC, RPT, WARPS, true>, grid, WARPS * 32, a.S, s, a);
-    return launch_cluster(tern_scan_fwd_kernel<T, VEC, RPT, WARPS, false>, grid, WARPS * 32, 1, s, a);
+    if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, a.S, s, a);
+    return launch_cluster(tern_scan_fwd_kernel<C, false>, grid, C::WARPS * 32, 1, s, a);
 }
 
-template <class T, int VEC>
+template <class C>
 int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStream_t s) {
     GradArgs g = g0;
-    g.s.tiles = (g.s.D + 32 * VEC - 1) / (32 * VEC);
+    g.s.tiles = (g.s.D + C::CH - 1) / C::CH;
     const int64_t blocks = B * g.s.tiles;
-    g.s.S = cluster_size(blocks, steps_of(g.s.T, kSaveRows), num_sms);
+    g.s.S = cluster_size(blocks, steps_of(g.s.T, C::ROWS), num_sms);
     if (blocks * g.s.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * g.s.S);
     if (g.s.S > 1) {
-        if (int st = launch_cluster(tern_scan_bwd_kernel<T, VEC, true>, grid, 256, g.s.S, s, g)) return st;
-    } else if (int st = launch_cluster(tern_scan_bwd_kernel<T, VEC, false>, grid, 256, 1, s, g)) {
+        if (int st = launch_cluster(tern_scan_bwd_kernel<C, true>, grid, C::WARPS * 32, g.s.S, s, g)) return st;
+    } else if (int st = launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, 1, s, g)) {
         return st;
     }
     if (dbias == nullptr) return TERN_OK;
@@ -654,13 +942,22 @@ int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStr
 
 ScanArgs scan_args(const tern_scan* s) {
     ScanArgs a{};
-    a.f = strided(s->f), a.v = strided(s->v), a.r = strided(s->r);
+    a.f = strided(s->f, s->dtype), a.v = strided(s->v, s->dtype), a.r = strided(s->r, s->dtype);
     a.f_bias = s->f_bias, a.lengths = s->lengths, a.starts = s->starts;
     a.T = static_cast<int>(s->T), a.D = static_cast<int>(s->D);
     return a;
 }
 
 }  // namespace
+
+int scan_status_read(int clear) {
+    int v = 0;
+    TERN_CUDA_TRY(cudaMemcpyFromSymbol(&v, g_scan_status, sizeof(v)));
+    const int zero = 0;
+    if (v != 0 && clear) TERN_CUDA_TRY(cudaMemcpyToSymbol(g_scan_status, &zero, sizeof(zero)));
+    return v != 0 ? TERN_ERR_TIMEOUT : TERN_OK;
+}
+
 }  // namespace tern
 
 using namespace tern;
@@ -672,24 +969,26 @@ extern "C" size_t tern_scan_saved(int64_t B, int64_t T, int64_t D) {
 
 extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act* y, float* hT, float* saved,
                              size_t saved_bytes, void* stream) {
-    bool vec2;
-    if (int st = check_scan(s, vec2)) return st;
+    bool wide;
+    if (int st = check_scan(s, wide)) return st;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (s->T > 0) {
         if (y == nullptr) return TERN_ERR_ARG;
-        if (int st = check_act(*y, s->dtype, vec2)) return st;
+        if (int st = check_act(*y, s->dtype, wide)) return st;
     }
     if (!aligned4(h0) || !aligned4(hT) || !aligned4(saved)) return TERN_ERR_ALIGN;
     if (saved != nullptr && saved_bytes < tern_scan_saved(s->B, s->T, s->D)) return TERN_ERR_WORKSPACE;
     int num_sms = 0;
     if (int st = check_device(&num_sms)) return st;
     ScanArgs a = scan_args(s);
-    if (s->T > 0) a.y = strided(*y);
+    if (s->T > 0) a.y = strided(*y, s->dtype);
     a.saved = saved, a.h_in = h0, a.h_out = hT;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (s->dtype == TERN_BF16)
-        return vec2 ? launch_fwd<__nv_bfloat16, 2>(a, s->B, num_sms, cs) : launch_fwd<__nv_bfloat16, 1>(a, s->B, num_sms, cs);
-    return vec2 ? launch_fwd<float, 2>(a, s->B, num_sms, cs) : launch_fwd<float, 1>(a, s->B, num_sms, cs);
+        return wide ? launch_fwd<Shape<__nv_bfloat16, true, 16, 8>>(a, s->B, num_sms, cs)
+                    : launch_fwd<Shape<__nv_bfloat16, false, 16, 8>>(a, s->B, num_sms, cs);
+    return wide ? launch_fwd<Shape<float, true, 16, 8>>(a, s->B, num_sms, cs)
+                : launch_fwd<Shape<float, false, 16, 8>>(a, s->B, num_sms, cs);
 }
 
 extern "C" size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D) {
@@ -700,14 +999,14 @@ extern "C" size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D) {
 extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_act* dy, const float* dhT,
                              const tern_act* df, const tern_act* dv, const tern_act* dr, float* dbias, float* dh0,
                              void* workspace, size_t ws_bytes, void* stream) {
-    bool vec2;
-    if (int st = check_scan(s, vec2)) return st;
+    bool wide;
+    if (int st = check_scan(s, wide)) return st;
     if (s->B == 0 || s->D == 0) return s->D == 0 || dbias == nullptr ? TERN_OK : TERN_ERR_ARG;
     if (s->T > 0) {
         if (saved == nullptr) return TERN_ERR_ARG;
         for (const tern_act* x : {dy, df, dv, dr}) {
             if (x == nullptr) return TERN_ERR_ARG;
-            if (int st = check_act(*x, s->dtype, vec2)) return st;
+            if (int st = check_act(*x, s->dtype, wide)) return st;
         }
     }
     if (!aligned4(saved) || !aligned4(dhT) || !aligned4(dbias) || !aligned4(dh0) || !aligned4(workspace)) return TERN_ERR_ALIGN;
@@ -718,38 +1017,46 @@ extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_
     GradArgs g{};
     g.s = scan_args(s);
     g.s.saved = const_cast<float*>(saved), g.s.h_in = dhT, g.s.h_out = dh0;
-    if (s->T > 0) g.s.y = strided(*dy), g.df = strided(*df), g.dv = strided(*dv), g.dr = strided(*dr);
+    if (s->T > 0) {
+        g.s.y = strided(*dy, s->dtype);
+        g.df = strided(*df, s->dtype), g.dv = strided(*dv, s->dtype), g.dr = strided(*dr, s->dtype);
+    }
     g.partial = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (s->dtype == TERN_BF16)
-        return vec2 ? launch_bwd<__nv_bfloat16, 2>(g, s->B, num_sms, dbias, cs) : launch_bwd<__nv_bfloat16, 1>(g, s->B, num_sms, dbias, cs);
-    return vec2 ? launch_bwd<float, 2>(g, s->B, num_sms, dbias, cs) : launch_bwd<float, 1>(g, s->B, num_sms, dbias, cs);
+        return wide ? launch_bwd<Shape<__nv_bfloat16, true, 16, 4>>(g, s->B, num_sms, dbias, cs)
+                    : launch_bwd<Shape<__nv_bfloat16, false, 16, 4>>(g, s->B, num_sms, dbias, cs);
+    return wide ? launch_bwd<Shape<float, true, 16, 4>>(g, s->B, num_sms, dbias, cs)
+                : launch_bwd<Shape<float, false, 16, 4>>(g, s->B, num_sms, dbias, cs);
 }
 
 namespace {
-template <class T>
-int launch_step(const StepArgs& a, bool vec2, cudaStream_t s) {
-    const int64_t blocks = (a.rows * (vec2 ? a.D / 2 : a.D) + 127) / 128;
+template <class T, bool WIDE>
+int launch_step(const StepArgs& a, cudaStream_t s) {
+    constexpr int VEC = 2 * Io<T, WIDE>::NP;
+    const int64_t blocks = (a.rows * ((a.D + VEC - 1) / VEC) + 127) / 128;
     if (blocks > INT32_MAX) return TERN_ERR_ARG;
-    return launch_pdl(vec2 ? tern_scan_step_kernel<T, 2> : tern_scan_step_kernel<T, 1>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(128), 0, s, a);
+    return launch_pdl(tern_scan_step_kernel<T, WIDE>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, s, a);
 }
 }  // namespace
 
 extern "C" int tern_scan_step(const tern_scan* s, const float* h_in, float* h_out, const tern_act* y, void* stream) {
-    bool vec2;
-    if (int st = check_scan(s, vec2)) return st;
+    bool wide;
+    if (int st = check_scan(s, wide)) return st;
     if (s->T != 1 || s->lengths != nullptr || s->starts != nullptr) return TERN_ERR_ARG;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (h_in == nullptr || h_out == nullptr || y == nullptr) return TERN_ERR_ARG;
-    if (int st = check_act(*y, s->dtype, vec2)) return st;
+    if (int st = check_act(*y, s->dtype, wide)) return st;
     if (!aligned4(h_in) || !aligned4(h_out)) return TERN_ERR_ALIGN;
     if (int st = check_device(nullptr)) return st;
     StepArgs a{};
-    a.f = s->f.p, a.v = s->v.p, a.r = s->r.p, a.y = y->p;
-    a.f_sb = s->f.stride_b, a.v_sb = s->v.stride_b, a.r_sb = s->r.stride_b, a.y_sb = y->stride_b;
+    const int64_t es = static_cast<int64_t>(elem(s->dtype));
+    a.f = static_cast<char*>(s->f.p), a.v = static_cast<char*>(s->v.p), a.r = static_cast<char*>(s->r.p);
+    a.y = static_cast<char*>(y->p);
+    a.f_sb = s->f.stride_b * es, a.v_sb = s->v.stride_b * es, a.r_sb = s->r.stride_b * es, a.y_sb = y->stride_b * es;
     a.f_bias = s->f_bias, a.h_in = h_in, a.h_out = h_out;
     a.rows = s->B, a.D = static_cast<int>(s->D);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return s->dtype == TERN_BF16 ? launch_step<__nv_bfloat16>(a, vec2, cs) : launch_step<float>(a, vec2, cs);
+    if (s->dtype == TERN_BF16) return wide ? launch_step<__nv_bfloat16, true>(a, cs) : launch_step<__nv_bfloat16, false>(a, cs);
+    return wide ? launch_step<float, true>(a, cs) : launch_step<float, false>(a, cs);
 }
