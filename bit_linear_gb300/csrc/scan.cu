@@ -246,6 +246,23 @@ struct Exchange {
     alignas(16) float A[2][kMaxCluster][C::CH], H[2][kMaxCluster][C::CH];
     uint64_t bar[2];
 };
+// A block may leave once its last wait has succeeded: all that its peers send has arrived, and
+// what it sent is what they wait for.  After a wait that gave up nothing is known, and the thread
+// stays until the peers' threads have left or come here too.
+template <class E>
+__device__ __forceinline__ void open_exchange(E& ex) {
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(ptx::smem_u32(&ex.bar[0]), 1);
+        ptx::mbar_init(ptx::smem_u32(&ex.bar[1]), 1);
+        ptx::fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_leave() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 template <int NP>
 __device__ __forceinline__ void push_pairs(const float* mine, const F2 (&x)[NP], const uint64_t* bar, uint32_t rank) {
     const uint32_t at = ptx::mapa_shared(ptx::smem_u32(mine), rank), b = ptx::mapa_shared(ptx::smem_u32(bar), rank);
@@ -287,20 +304,18 @@ __device__ __forceinline__ bool wait_peers(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ int rows_live(const ScanArgs& a, int b) {
     return a.lengths != nullptr ? min(max(a.lengths[b], 0), a.T) : a.T;
 }
-// bit i: row0 + i (of the nl live rows of this lane's segment) starts a document
+// bit i: row i of this lane's segment (live) starts a document; a lane of the warp reads each row's
 template <class C>
-__device__ __forceinline__ uint32_t start_bits(const ScanArgs& a, int64_t b, int row0, int nl) {
+__device__ __forceinline__ uint32_t start_bits(const ScanArgs& a, int64_t b, int warp_row0, int len, int seg, int lane) {
+    static_assert(C::WROWS <= 32, "a byte per lane");
     if (a.starts == nullptr) return 0;
-    const uint8_t* p = a.starts + b * a.T + row0;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < C::RPT; ++i) m |= i < nl && p[i] != 0 ? 1u << i : 0u;
-    return m;
+    const bool st = lane < C::WROWS && warp_row0 + lane < len && a.starts[b * a.T + warp_row0 + lane] != 0;
+    return (__ballot_sync(0xffffffffu, st) >> (seg * C::RPT)) & ((1u << C::RPT) - 1u);
 }
-// The segment's rows of one tensor; rows that are not live stay zero.
+// The segment's rows of one tensor.  full: all are live; otherwise the others stay zero.
 template <class C>
-__device__ __forceinline__ void load_rows(typename C::X::Raw (&raw)[C::RPT], const char* p, int64_t st, int nl, int nch) {
-    if (__all_sync(0xffffffffu, nl == C::RPT)) {
+__device__ __forceinline__ void load_rows(typename C::X::Raw (&raw)[C::RPT], const char* p, int64_t st, int nl, int nch, bool full) {
+    if (full) {
 #pragma unroll
         for (int i = 0; i < C::RPT; ++i) raw[i] = C::X::load(p + i * st, nch);
     } else {
@@ -367,6 +382,134 @@ __device__ __forceinline__ void fold_map(const float* A, const float* H, int str
     }
 }
 
+// The parts of a step that run over a segment's rows.  PLAIN: all rows of the warp are live and
+// none starts a document, which leaves out the selects.
+template <class C, bool PLAIN>
+__device__ __forceinline__ void fwd_rows(const typename C::X::Raw (&rf)[C::RPT], const typename C::X::Raw (&rv)[C::RPT],
+                                         const F2 (&lb)[C::NP], int nl, uint32_t cut, F2 (&ga)[C::RPT][C::NP],
+                                         F2 (&gb)[C::RPT][C::NP], F2 (&A)[C::NP], F2 (&H)[C::NP]) {
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i) {
+        F2 f[C::NP], v[C::NP], n;
+        C::X::get(rf[i], f);
+        C::X::get(rv[i], v);
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) {
+            decay(f[j], lb[j], ga[i][j], n);
+            gb[i][j] = mul2(n, v[j]);
+            if constexpr (!PLAIN) {
+                if (i >= nl) ga[i][j] = both(1.0f), gb[i][j] = both(0.0f);
+                if ((cut >> i) & 1u) ga[i][j] = both(-0.0f);
+            }
+            if (i == 0) A[j] = ga[i][j], H[j] = gb[i][j];
+            else compose(ga[i][j], gb[i][j], A[j], H[j], !PLAIN);
+        }
+    }
+}
+// gb becomes the states; h the state after the rows.
+template <class C, bool PLAIN>
+__device__ __forceinline__ void fwd_again(const F2 (&ga)[C::RPT][C::NP], F2 (&gb)[C::RPT][C::NP], F2 (&h)[C::NP]) {
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) gb[i][j] = h[j] = apply(ga[i][j], gb[i][j], h[j], !PLAIN);
+}
+template <class C, bool PLAIN>
+__device__ __forceinline__ void fwd_store(const typename C::X::Raw (&rr)[C::RPT], const F2 (&hs)[C::RPT][C::NP], char* y, int64_t st,
+                                          int nl, int nr, int nch) {
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i) {
+        F2 r[C::NP], o[C::NP], s, n;
+        C::X::get(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) {
+            gate(r[j], s, n);
+            o[j] = mul2(s, hs[i][j]);
+            if (!PLAIN && i >= nl) o[j] = both(0.0f);
+        }
+        if (PLAIN ? nr > 0 : i < nr) C::X::store(y + i * st, o, nch);
+    }
+}
+// Per row: s = a, n = 1 - a, o = sigmoid(r) dy, x = sigmoid(-r); and the segment's folds.
+template <class C, bool PLAIN>
+__device__ __forceinline__ void bwd_rows(const typename C::X::Raw (&rf)[C::RPT], const typename C::X::Raw (&rv)[C::RPT],
+                                         const typename C::X::Raw (&rr)[C::RPT], const typename C::X::Raw (&rd)[C::RPT],
+                                         const F2 (&lb)[C::NP], int nl, uint32_t cut, F2 (&s)[C::RPT][C::NP],
+                                         F2 (&n)[C::RPT][C::NP], F2 (&o)[C::RPT][C::NP], F2 (&x)[C::RPT][C::NP],
+                                         F2 (&A)[C::NP], F2 (&H)[C::NP], F2 (&G)[C::NP]) {
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i) {
+        F2 f[C::NP], v[C::NP], r[C::NP], dy[C::NP], so;
+        C::X::get(rf[i], f);
+        C::X::get(rv[i], v);
+        C::X::get(rr[i], r);
+        C::X::get(rd[i], dy);
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) {
+            decay(f[j], lb[j], s[i][j], n[i][j]);
+            gate(r[j], so, x[i][j]);
+            o[i][j] = mul2(so, dy[j]);
+            if (!PLAIN && i >= nl) s[i][j] = both(1.0f), n[i][j] = both(0.0f), o[i][j] = both(0.0f);
+            const F2 m = !PLAIN && ((cut >> i) & 1u) ? both(-0.0f) : s[i][j], b = mul2(n[i][j], v[j]);
+            if (i == 0) A[j] = m, H[j] = b;
+            else compose(m, b, A[j], H[j], !PLAIN);
+        }
+    }
+#pragma unroll
+    for (int i = C::RPT - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) {
+            G[j] = mul2(s[i][j], i == C::RPT - 1 ? o[i][j] : add2(o[i][j], G[j]));
+            if (!PLAIN && ((cut >> i) & 1u)) G[j] = both(0.0f);
+        }
+}
+// From h before the rows and e after them: the gradients, written; e before the rows.
+template <class C, bool PLAIN>
+__device__ __forceinline__ void bwd_store(const typename C::X::Raw (&rv)[C::RPT], const F2 (&s)[C::RPT][C::NP],
+                                          const F2 (&n)[C::RPT][C::NP], const F2 (&o)[C::RPT][C::NP], F2 (&x)[C::RPT][C::NP],
+                                          int nl, uint32_t cut, int nr, int nch, F2 (&h)[C::NP], F2 (&e)[C::NP],
+                                          F2 (&dbias)[C::NP], char* df_p, int64_t df_st, char* dv_p, int64_t dv_st, char* dr_p,
+                                          int64_t dr_st) {
+    F2 hv[C::RPT][C::NP];   // n (h_{t-1} - v); x becomes dr = g h (1 - sigmoid(r))
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i) {
+        F2 v[C::NP];
+        C::X::get(rv[i], v);
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) {
+            if (!PLAIN && ((cut >> i) & 1u)) h[j] = both(0.0f);
+            hv[i][j] = mul2(n[i][j], fma2(v[j], both(-1.0f), h[j]));
+            h[j] = fma2(s[i][j], h[j], mul2(n[i][j], v[j]));
+            x[i][j] = mul2(mul2(o[i][j], h[j]), x[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = C::RPT - 1; i >= 0; --i) {
+        F2 df[C::NP], dv[C::NP];
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) {
+            const F2 dh = add2(o[i][j], e[j]);
+            e[j] = mul2(s[i][j], dh);
+            dv[j] = mul2(n[i][j], dh);
+            df[j] = mul2(e[j], hv[i][j]);
+            if (!PLAIN && i >= nl) dv[j] = df[j] = x[i][j] = both(0.0f);
+            dbias[j] = add2(dbias[j], df[j]);
+            if (!PLAIN && ((cut >> i) & 1u)) e[j] = both(0.0f);
+        }
+        if (PLAIN ? nr > 0 : i < nr) {
+            C::X::store(df_p + i * df_st, df, nch);
+            C::X::store(dv_p + i * dv_st, dv, nch);
+            C::X::store(dr_p + i * dr_st, x[i], nch);
+        }
+    }
+}
+// The block barrier after which `agg` holds; whether a document starts in any of its rows.
+__device__ __forceinline__ bool sync_cuts(bool docs, uint32_t cut) {
+    if (docs) return __syncthreads_or(cut != 0) != 0;
+    __syncthreads();
+    return false;
+}
+
 // What every block of the two kernels starts from.
 template <class C>
 struct Place {
@@ -402,14 +545,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_fwd_kernel(const _
     __shared__ alignas(16) float carry_s[2][C::CH];                // not CL: the state after a step
     __shared__ typename std::conditional<CL, Exchange<C>, int>::type ex;
     const Place<C> q(a);
-    if constexpr (CL) {
-        if (threadIdx.x == 0) {
-            ptx::mbar_init(ptx::smem_u32(&ex.bar[0]), 1);
-            ptx::mbar_init(ptx::smem_u32(&ex.bar[1]), 1);
-            ptx::fence_mbar_init();
-        }
-        ptx::cluster_sync();
-    }
+    if constexpr (CL) open_exchange(ex);
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const bool docs = a.starts != nullptr;
@@ -435,71 +571,38 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_fwd_kernel(const _
             if (threadIdx.x == 0)
                 ptx::mbar_arrive_expect_tx(ptx::smem_u32(&ex.bar[p]), static_cast<uint32_t>(a.S * C::CH * 2 * sizeof(float)));
         }
+        const bool full = __all_sync(0xffffffffu, nl == RPT);
         typename X::Raw rf[RPT], rv[RPT], rr[RPT];
-        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch);
-        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch);
-        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch);
-        const uint32_t cut = start_bits<C>(a, q.b, row0, nl);
+        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch, full);
+        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch, full);
+        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch, full);
+        const uint32_t cut = start_bits<C>(a, q.b, static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))), len, q.seg, q.lane);
+        const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
         // (A, H) of this lane's rows
         F2 ga[RPT][NP], gb[RPT][NP], A[NP], H[NP];
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            F2 f[NP], v[NP], n;
-            X::get(rf[i], f);
-            X::get(rv[i], v);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                decay(f[j], lb[j], ga[i][j], n);
-                gb[i][j] = mul2(n, v[j]);
-            }
-        }
-        if (nl < RPT) {
-#pragma unroll
-            for (int i = 0; i < RPT; ++i)
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-                    if (i >= nl) ga[i][j] = both(1.0f), gb[i][j] = both(0.0f);
-        }
-        if (cut != 0) {
-#pragma unroll
-            for (int i = 0; i < RPT; ++i)
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-                    if ((cut >> i) & 1u) ga[i][j] = both(-0.0f);
-        }
-#pragma unroll
-        for (int j = 0; j < NP; ++j) A[j] = ga[0][j], H[j] = gb[0][j];
-        if (cut == 0) {
-#pragma unroll
-            for (int i = 1; i < RPT; ++i)
-#pragma unroll
-                for (int j = 0; j < NP; ++j) A[j] = mul2(A[j], ga[i][j]), H[j] = fma2(ga[i][j], H[j], gb[i][j]);
-        } else {
-#pragma unroll
-            for (int i = 1; i < RPT; ++i)
-#pragma unroll
-                for (int j = 0; j < NP; ++j) compose(ga[i][j], gb[i][j], A[j], H[j], true);
-        }
+        if (plain) fwd_rows<C, true>(rf, rv, lb, nl, cut, ga, gb, A, H);
+        else fwd_rows<C, false>(rf, rv, lb, nl, cut, ga, gb, A, H);
         F2 PA[NP], PH[NP];
-        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, docs);
+        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, !plain);
         if (q.seg == C::SEGS - 1) {
             F2 TA[NP], TH[NP];
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
                 TA[j] = PA[j], TH[j] = PH[j];
-                compose(A[j], H[j], TA[j], TH[j], docs);
+                compose(A[j], H[j], TA[j], TH[j], !plain);
             }
             put_s(&aggA[p][q.w][q.ch], TA);
             put_s(&aggH[p][q.w][q.ch], TH);
         }
-        __syncthreads();
+        const bool cuts_here = sync_cuts(docs, cut);
         // the state before this block's rows
         F2 h[NP];
         if constexpr (CL) {
+            if (it == 0) cluster_wait();   // every peer has set up its barriers
             if (q.w == WARPS - 1) {   // the block's total, to every block: a segment's lanes each serve S / SEGS of them
 #pragma unroll
                 for (int j = 0; j < NP; ++j) A[j] = both(1.0f), H[j] = both(0.0f);
-                fold_map(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, 0, WARPS, 1, A, H, docs);
+                fold_map(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, 0, WARPS, 1, A, H, cuts_here);
                 for (int k = q.seg; k < a.S; k += C::SEGS) {
                     push_pairs(&ex.A[p][q.rank][q.ch], A, &ex.bar[p], k);
                     push_pairs(&ex.H[p][q.rank][q.ch], H, &ex.bar[p], k);
@@ -517,47 +620,23 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_fwd_kernel(const _
             for (int j = 0; j < NP; ++j) h[j] = carry[j];
             if (it > 0) get_s(&carry_s[p ^ 1][q.ch], h);
         }
-        fold(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, 0, q.w, 1, h, docs);
+        fold(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, 0, q.w, 1, h, cuts_here);
 #pragma unroll
-        for (int j = 0; j < NP; ++j) h[j] = apply(PA[j], PH[j], h[j], docs);
+        for (int j = 0; j < NP; ++j) h[j] = apply(PA[j], PH[j], h[j], !plain);
         if (a.saved != nullptr && q.on && row0 < a.T && row0 % kSaveRows == 0)
             store_f32(a.saved + (q.b * nsaved + row0 / kSaveRows) * a.D + q.d, q.nch, h);
-        // the rows again, from the state before them; gb becomes the states
-        if (cut == 0) {
-#pragma unroll
-            for (int i = 0; i < RPT; ++i)
-#pragma unroll
-                for (int j = 0; j < NP; ++j) h[j] = fma2(ga[i][j], h[j], gb[i][j]), gb[i][j] = h[j];
-        } else {
-#pragma unroll
-            for (int i = 0; i < RPT; ++i)
-#pragma unroll
-                for (int j = 0; j < NP; ++j) h[j] = apply(ga[i][j], gb[i][j], h[j], true), gb[i][j] = h[j];
-        }
+        // the rows again, from the state before them
+        if (plain) fwd_again<C, true>(ga, gb, h);
+        else fwd_again<C, false>(ga, gb, h);
         if constexpr (!CL) {
             if (q.w == WARPS - 1 && q.seg == C::SEGS - 1) put_s(&carry_s[p][q.ch], h);
         }
-        char* yr = yp + row0 * a.y.st;
         const int nr = q.on ? min(a.T - row0, RPT) : 0;   // rows to write
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            F2 r[NP], y[NP], s, n;
-            X::get(rr[i], r);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                gate(r[j], s, n);
-                y[j] = mul2(s, gb[i][j]);
-            }
-            if (nl < RPT) {
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-                    if (i >= nl) y[j] = both(0.0f);
-            }
-            if (i < nr) X::store(yr + i * a.y.st, y, q.nch);
-        }
+        if (plain) fwd_store<C, true>(rr, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
+        else fwd_store<C, false>(rr, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
     }
     if constexpr (CL) {
-        ptx::cluster_sync();   // no block leaves while another may still write to it
+        if (!ok) cluster_leave();
     } else {
         __syncthreads();
         if (iters > 0) get_s(&carry_s[(iters - 1) & 1][q.ch], carry);
@@ -578,14 +657,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_bwd_kernel(const _
     __shared__ alignas(16) float carry_s[2][C::CH];
     __shared__ typename std::conditional<CL, Exchange<C>, int>::type ex;
     const Place<C> q(a);
-    if constexpr (CL) {
-        if (threadIdx.x == 0) {
-            ptx::mbar_init(ptx::smem_u32(&ex.bar[0]), 1);
-            ptx::mbar_init(ptx::smem_u32(&ex.bar[1]), 1);
-            ptx::fence_mbar_init();
-        }
-        ptx::cluster_sync();
-    }
+    if constexpr (CL) open_exchange(ex);
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const bool docs = a.starts != nullptr;
@@ -612,66 +684,29 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_bwd_kernel(const _
             if (threadIdx.x == 0)
                 ptx::mbar_arrive_expect_tx(ptx::smem_u32(&ex.bar[p]), static_cast<uint32_t>(a.S * C::CH * 2 * sizeof(float)));
         }
+        const bool full = __all_sync(0xffffffffu, nl == RPT);
         typename X::Raw rf[RPT], rv[RPT], rr[RPT], rd[RPT];
-        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch);
-        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch);
-        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch);
-        load_rows<C>(rd, yp + row0 * a.y.st, a.y.st, nl, q.nch);
-        const uint32_t cut = start_bits<C>(a, q.b, row0, nl);
+        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch, full);
+        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch, full);
+        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch, full);
+        load_rows<C>(rd, yp + row0 * a.y.st, a.y.st, nl, q.nch, full);
+        const uint32_t cut = start_bits<C>(a, q.b, step >= 0 ? static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))) : a.T,
+                                           len, q.seg, q.lane);
+        const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
         F2 h[NP];
         load_f32(row0 < a.T ? a.saved + (q.b * nsaved + row0 / kSaveRows) * a.D + q.d : nullptr, q.nch, h, 0.0f);
-        // per row: s = a, n = 1 - a, o = g = sigmoid(r) dy, x = sigmoid(-r)
         F2 s[RPT][NP], n[RPT][NP], o[RPT][NP], x[RPT][NP], A[NP], H[NP], G[NP];
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            F2 f[NP], r[NP], dy[NP], so;
-            X::get(rf[i], f);
-            X::get(rr[i], r);
-            X::get(rd[i], dy);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                decay(f[j], lb[j], s[i][j], n[i][j]);
-                gate(r[j], so, x[i][j]);
-                o[i][j] = mul2(so, dy[j]);
-            }
-        }
-        if (nl < RPT) {
-#pragma unroll
-            for (int i = 0; i < RPT; ++i)
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-                    if (i >= nl) s[i][j] = both(1.0f), n[i][j] = both(0.0f), o[i][j] = both(0.0f);
-        }
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            F2 v[NP];
-            X::get(rv[i], v);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const F2 m = (cut >> i) & 1u ? both(-0.0f) : s[i][j], b = mul2(n[i][j], v[j]);
-                if (i == 0) A[j] = m, H[j] = b;
-                else if (cut == 0) A[j] = mul2(A[j], m), H[j] = fma2(m, H[j], b);
-                else compose(m, b, A[j], H[j], true);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NP; ++j) G[j] = both(0.0f);
-#pragma unroll
-        for (int i = RPT - 1; i >= 0; --i)
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                G[j] = mul2(s[i][j], add2(o[i][j], G[j]));
-                if ((cut >> i) & 1u) G[j] = both(0.0f);
-            }
+        if (plain) bwd_rows<C, true>(rf, rv, rr, rd, lb, nl, cut, s, n, o, x, A, H, G);
+        else bwd_rows<C, false>(rf, rv, rr, rd, lb, nl, cut, s, n, o, x, A, H, G);
         F2 PA[NP], PH[NP], QA[NP], QG[NP];
-        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, docs);
-        warp_prefix<C, true>(A, G, QA, QG, q.seg, q.c, docs);
+        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, !plain);
+        warp_prefix<C, true>(A, G, QA, QG, q.seg, q.c, !plain);
         if (q.seg == C::SEGS - 1) {
             F2 TA[NP], TH[NP];
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
                 TA[j] = PA[j], TH[j] = PH[j];
-                compose(A[j], H[j], TA[j], TH[j], docs);
+                compose(A[j], H[j], TA[j], TH[j], !plain);
             }
             put_s(&aggA[p][q.w][q.ch], TA);
             put_s(&aggH[p][q.w][q.ch], TH);
@@ -679,16 +714,17 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_bwd_kernel(const _
         if (q.seg == 0) {
             F2 TG[NP];
 #pragma unroll
-            for (int j = 0; j < NP; ++j) TG[j] = apply(A[j], G[j], QG[j], docs);
+            for (int j = 0; j < NP; ++j) TG[j] = apply(A[j], G[j], QG[j], !plain);
             put_s(&aggG[p][q.w][q.ch], TG);
         }
-        __syncthreads();
+        const bool cuts_here = sync_cuts(docs, cut);
         F2 e[NP];   // e after this segment's rows
         if constexpr (CL) {
+            if (it == 0) cluster_wait();   // every peer has set up its barriers
             if (q.w == 0) {
 #pragma unroll
                 for (int j = 0; j < NP; ++j) A[j] = both(1.0f), G[j] = both(0.0f);
-                fold_map(&aggA[p][0][q.ch], &aggG[p][0][q.ch], C::CH, WARPS - 1, -1, -1, A, G, docs);
+                fold_map(&aggA[p][0][q.ch], &aggG[p][0][q.ch], C::CH, WARPS - 1, -1, -1, A, G, cuts_here);
                 for (int k = q.seg; k < a.S; k += C::SEGS) {
                     push_pairs(&ex.A[p][q.rank][q.ch], A, &ex.bar[p], k);
                     push_pairs(&ex.H[p][q.rank][q.ch], G, &ex.bar[p], k);
@@ -706,53 +742,24 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_bwd_kernel(const _
             for (int j = 0; j < NP; ++j) e[j] = carry[j];
             if (it > 0) get_s(&carry_s[p ^ 1][q.ch], e);
         }
-        fold(&aggA[p][0][q.ch], &aggG[p][0][q.ch], C::CH, WARPS - 1, q.w, -1, e, docs);
-        fold(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, q.w / GROUP * GROUP, q.w, 1, h, docs);
+        fold(&aggA[p][0][q.ch], &aggG[p][0][q.ch], C::CH, WARPS - 1, q.w, -1, e, cuts_here);
+        fold(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, q.w / GROUP * GROUP, q.w, 1, h, cuts_here);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-            e[j] = apply(QA[j], QG[j], e[j], docs);
-            h[j] = apply(PA[j], PH[j], h[j], docs);
-        }
-        // o stays g; x becomes dr = g h (1 - sigmoid(r)); hv = h_{t-1} - v
-        F2 hv[RPT][NP];
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            F2 v[NP];
-            X::get(rv[i], v);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                if ((cut >> i) & 1u) h[j] = both(0.0f);
-                hv[i][j] = fma2(v[j], both(-1.0f), h[j]);
-                h[j] = fma2(s[i][j], h[j], mul2(n[i][j], v[j]));
-                x[i][j] = mul2(mul2(o[i][j], h[j]), x[i][j]);
-            }
+            e[j] = apply(QA[j], QG[j], e[j], !plain);
+            h[j] = apply(PA[j], PH[j], h[j], !plain);
         }
         const int nr = q.on ? min(a.T - row0, RPT) : 0;   // rows to write
         char *dfr = dfp + row0 * g.df.st, *dvr = dvp + row0 * g.dv.st, *drr = drp + row0 * g.dr.st;
-#pragma unroll
-        for (int i = RPT - 1; i >= 0; --i) {
-            F2 df[NP], dv[NP];
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const F2 dh = add2(o[i][j], e[j]);
-                const F2 e2 = mul2(s[i][j], dh);
-                dv[j] = mul2(n[i][j], dh);
-                df[j] = mul2(mul2(e2, n[i][j]), hv[i][j]);
-                if (i >= nl) dv[j] = df[j] = x[i][j] = both(0.0f);
-                dbias[j] = add2(dbias[j], df[j]);
-                e[j] = (cut >> i) & 1u ? both(0.0f) : e2;
-            }
-            if (i < nr) {
-                X::store(dfr + i * g.df.st, df, q.nch);
-                X::store(dvr + i * g.dv.st, dv, q.nch);
-                X::store(drr + i * g.dr.st, x[i], q.nch);
-            }
-        }
+        if (plain) bwd_store<C, true>(rv, s, n, o, x, nl, cut, nr, q.nch, h, e, dbias, dfr, g.df.st, dvr, g.dv.st, drr, g.dr.st);
+        else bwd_store<C, false>(rv, s, n, o, x, nl, cut, nr, q.nch, h, e, dbias, dfr, g.df.st, dvr, g.dv.st, drr, g.dr.st);
         if constexpr (!CL) {
             if (q.w == 0 && q.seg == 0) put_s(&carry_s[p][q.ch], e);
         }
     }
-    if constexpr (CL) ptx::cluster_sync();   // no block leaves while another may still write to it
+    if constexpr (CL) {
+        if (!ok) cluster_leave();
+    }
     __syncthreads();
     if constexpr (!CL) {
         if (iters > 0) get_s(&carry_s[(iters - 1) & 1][q.ch], carry);
