@@ -172,6 +172,13 @@ __device__ __forceinline__ F2 rcp_neg(F2 u) {   // -1 / u
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-y));
     return pair(x, y);
 }
+__device__ __forceinline__ F2 gate(F2 x) {   // s alone: an infinite e gives 0
+    float a, b;
+    split(mul2(x, both(-kLog2e)), a, b);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(a));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(b));
+    return rcp_neg(fma2(pair(a, b), both(-1.0f), both(-1.0f)));
+}
 __device__ __forceinline__ void gate(F2 x, F2& s, F2& n) {
     const F2 e = exp2_capped(mul2(x, both(-kLog2e)));
     s = rcp_neg(fma2(e, both(-1.0f), both(-1.0f)));
@@ -229,12 +236,12 @@ struct GradArgs {
 
 // How a block cuts its rows and channels: LPR lanes make a row of CH channels, a lane's segment
 // has RPT rows, a warp SEGS segments.
-template <class T_, bool WIDE_, int LPR_, int RPT_>
+template <class T_, bool WIDE_, int LPR_, int RPT_, int WARPS_ = 8, int MINB_ = 2>
 struct Shape {
     using T = T_;
     using X = Io<T_, WIDE_>;
     static constexpr int NP = X::NP, LPR = LPR_, RPT = RPT_;
-    static constexpr int WARPS = 8, SEGS = 32 / LPR, CH = LPR * NP * 2, WROWS = SEGS * RPT, ROWS = WARPS * WROWS;
+    static constexpr int WARPS = WARPS_, MINB = MINB_, SEGS = 32 / LPR, CH = LPR * NP * 2, WROWS = SEGS * RPT, ROWS = WARPS * WROWS;
 };
 
 // Totals of the S blocks of a cluster, pushed by each block into every block's shared memory
@@ -325,6 +332,13 @@ __device__ __forceinline__ void load_rows(typename C::X::Raw (&raw)[C::RPT], con
             if (i < nl) raw[i] = C::X::load(p + i * st, nch);
         }
     }
+}
+// Asks for a warp's rows of the next step in L2, a lane per row; p is this lane's channel 0 of the
+// tile, row the warp's first.
+template <class C>
+__device__ __forceinline__ void prefetch_rows(const char* p, int64_t st, int64_t row, int len, int lane) {
+    if (lane < C::WROWS && row >= 0 && row + lane < len)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (row + lane) * st));
 }
 // Within a warp: (PA, PH) = the map of the segments before this one (after it, for REV), from
 // each segment's (A, H).
@@ -419,12 +433,11 @@ __device__ __forceinline__ void fwd_store(const typename C::X::Raw (&rr)[C::RPT]
                                           int nl, int nr, int nch) {
 #pragma unroll
     for (int i = 0; i < C::RPT; ++i) {
-        F2 r[C::NP], o[C::NP], s, n;
+        F2 r[C::NP], o[C::NP];
         C::X::get(rr[i], r);
 #pragma unroll
         for (int j = 0; j < C::NP; ++j) {
-            gate(r[j], s, n);
-            o[j] = mul2(s, hs[i][j]);
+            o[j] = mul2(gate(r[j]), hs[i][j]);
             if (!PLAIN && i >= nl) o[j] = both(0.0f);
         }
         if (PLAIN ? nr > 0 : i < nr) C::X::store(y + i * st, o, nch);
@@ -537,7 +550,7 @@ struct Place {
 // ------------------------------------------------------------------------------ forward
 // CL: the S blocks of a cluster take S consecutive steps at a time; otherwise S is 1.
 template <class C, bool CL>
-__global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
+__global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
     using X = typename C::X;
     constexpr int NP = C::NP, RPT = C::RPT, WARPS = C::WARPS, ROWS = C::ROWS;
     static_assert(kSaveRows % RPT == 0, "saved states fall on segment boundaries");
@@ -577,6 +590,10 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_fwd_kernel(const _
         load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch, full);
         load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch, full);
         const uint32_t cut = start_bits<C>(a, q.b, static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))), len, q.seg, q.lane);
+        const int64_t ahead = first - q.seg * RPT + static_cast<int64_t>(a.S) * ROWS;
+        prefetch_rows<C>(fp, a.f.st, ahead, len, q.lane);
+        prefetch_rows<C>(vp, a.v.st, ahead, len, q.lane);
+        prefetch_rows<C>(rp, a.r.st, ahead, len, q.lane);
         const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
         // (A, H) of this lane's rows
         F2 ga[RPT][NP], gb[RPT][NP], A[NP], H[NP];
@@ -647,7 +664,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_fwd_kernel(const _
 
 // ------------------------------------------------------------------------------ backward
 template <class C, bool CL>
-__global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_bwd_kernel(const __grid_constant__ GradArgs g) {
+__global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(const __grid_constant__ GradArgs g) {
     using X = typename C::X;
     constexpr int NP = C::NP, RPT = C::RPT, WARPS = C::WARPS, ROWS = C::ROWS;
     constexpr int GROUP = kSaveRows / C::WROWS;   // warps from one saved state to the next
@@ -692,6 +709,11 @@ __global__ void __launch_bounds__(C::WARPS * 32, 2) tern_scan_bwd_kernel(const _
         load_rows<C>(rd, yp + row0 * a.y.st, a.y.st, nl, q.nch, full);
         const uint32_t cut = start_bits<C>(a, q.b, step >= 0 ? static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))) : a.T,
                                            len, q.seg, q.lane);
+        const int64_t ahead = first - q.seg * RPT - static_cast<int64_t>(a.S) * ROWS;
+        prefetch_rows<C>(fp, a.f.st, ahead, len, q.lane);
+        prefetch_rows<C>(vp, a.v.st, ahead, len, q.lane);
+        prefetch_rows<C>(rp, a.r.st, ahead, len, q.lane);
+        prefetch_rows<C>(yp, a.y.st, ahead, len, q.lane);
         const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
         F2 h[NP];
         load_f32(row0 < a.T ? a.saved + (q.b * nsaved + row0 / kSaveRows) * a.D + q.d : nullptr, q.nch, h, 0.0f);
@@ -843,11 +865,10 @@ __global__ void __launch_bounds__(128) tern_scan_step_kernel(const __grid_consta
     load_f32(a.f_bias == nullptr ? nullptr : a.f_bias + d, nch, lb, 0.0f);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-        F2 s, n, o, q;
+        F2 s, n;
         decay(f[j], mul2(lb[j], both(-kLog2e)), s, n);
-        gate(r[j], o, q);
         h[j] = fma2(s, h[j], mul2(n, v[j]));
-        y[j] = mul2(o, h[j]);
+        y[j] = mul2(gate(r[j]), h[j]);
     }
     store_f32(a.h_out + hd, nch, h);
     X::store(a.y + b * a.y_sb + at, y, nch);
@@ -907,11 +928,11 @@ int check_scan(const tern_scan* s, bool& wide) {
     return TERN_OK;
 }
 
-// Blocks per cluster: the smallest power of two that gives every SM two blocks, at most
-// kMaxCluster and no more than there are steps.
-int cluster_size(int64_t blocks, int64_t steps, int num_sms) {
+// Blocks per cluster: the largest power of two, at most kMaxCluster and less than twice the steps,
+// with which the blocks are all resident at once.
+int cluster_size(int64_t blocks, int64_t steps, int64_t slots) {
     int S = 1;
-    while (S < kMaxCluster && S < steps && blocks * S < 2 * num_sms) S *= 2;
+    while (S < kMaxCluster && S < steps && 2 * S * blocks <= slots) S *= 2;
     return S;
 }
 
@@ -922,7 +943,7 @@ int launch_fwd(const ScanArgs& a0, int64_t B, int num_sms, cudaStream_t s) {
     ScanArgs a = a0;
     a.tiles = (a.D + C::CH - 1) / C::CH;
     const int64_t blocks = B * a.tiles;
-    a.S = cluster_size(blocks, steps_of(a.T, C::ROWS), num_sms);
+    a.S = cluster_size(blocks, steps_of(a.T, C::ROWS), static_cast<int64_t>(C::MINB) * num_sms);
     if (blocks * a.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * a.S);
     if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, a.S, s, a);
@@ -934,7 +955,7 @@ int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStr
     GradArgs g = g0;
     g.s.tiles = (g.s.D + C::CH - 1) / C::CH;
     const int64_t blocks = B * g.s.tiles;
-    g.s.S = cluster_size(blocks, steps_of(g.s.T, C::ROWS), num_sms);
+    g.s.S = cluster_size(blocks, steps_of(g.s.T, C::ROWS), static_cast<int64_t>(C::MINB) * num_sms);
     if (blocks * g.s.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * g.s.S);
     if (g.s.S > 1) {
@@ -992,10 +1013,10 @@ extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act
     a.saved = saved, a.h_in = h0, a.h_out = hT;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (s->dtype == TERN_BF16)
-        return wide ? launch_fwd<Shape<__nv_bfloat16, true, 16, 8>>(a, s->B, num_sms, cs)
-                    : launch_fwd<Shape<__nv_bfloat16, false, 16, 8>>(a, s->B, num_sms, cs);
-    return wide ? launch_fwd<Shape<float, true, 16, 8>>(a, s->B, num_sms, cs)
-                : launch_fwd<Shape<float, false, 16, 8>>(a, s->B, num_sms, cs);
+        return wide ? launch_fwd<Shape<__nv_bfloat16, true, 8, 8, 4, 4>>(a, s->B, num_sms, cs)
+                    : launch_fwd<Shape<__nv_bfloat16, false, 8, 8, 4, 4>>(a, s->B, num_sms, cs);
+    return wide ? launch_fwd<Shape<float, true, 8, 8, 4, 4>>(a, s->B, num_sms, cs)
+                : launch_fwd<Shape<float, false, 8, 8, 4, 4>>(a, s->B, num_sms, cs);
 }
 
 extern "C" size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D) {
@@ -1031,10 +1052,10 @@ extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_
     g.partial = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (s->dtype == TERN_BF16)
-        return wide ? launch_bwd<Shape<__nv_bfloat16, true, 16, 4>>(g, s->B, num_sms, dbias, cs)
-                    : launch_bwd<Shape<__nv_bfloat16, false, 16, 4>>(g, s->B, num_sms, dbias, cs);
-    return wide ? launch_bwd<Shape<float, true, 16, 4>>(g, s->B, num_sms, dbias, cs)
-                : launch_bwd<Shape<float, false, 16, 4>>(g, s->B, num_sms, dbias, cs);
+        return wide ? launch_bwd<Shape<__nv_bfloat16, true, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs)
+                    : launch_bwd<Shape<__nv_bfloat16, false, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs);
+    return wide ? launch_bwd<Shape<float, true, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs)
+                : launch_bwd<Shape<float, false, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs);
 }
 
 namespace {
