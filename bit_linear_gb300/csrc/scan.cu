@@ -77,8 +77,9 @@ __device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xff
 // elements are there, loads repeat the last and stores leave the others out.
 template <class T, bool WIDE_>
 struct Io;
-template <bool WIDE>
-struct Io<__nv_bfloat16, WIDE> {
+template <bool WIDE_>
+struct Io<__nv_bfloat16, WIDE_> {
+    static constexpr bool WIDE = WIDE_;
     static constexpr int NP = 2;
     using Raw = uint2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
@@ -110,8 +111,9 @@ struct Io<__nv_bfloat16, WIDE> {
         }
     }
 };
-template <bool WIDE>
-struct Io<float, WIDE> {
+template <bool WIDE_>
+struct Io<float, WIDE_> {
+    static constexpr bool WIDE = WIDE_;
     static constexpr int NP = 1;
     using Raw = float2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
@@ -333,13 +335,6 @@ __device__ __forceinline__ void load_rows(typename C::X::Raw (&raw)[C::RPT], con
         }
     }
 }
-// Asks for a warp's rows of the next step in L2, a lane per row; p is this lane's channel 0 of the
-// tile, row the warp's first.
-template <class C>
-__device__ __forceinline__ void prefetch_rows(const char* p, int64_t st, int64_t row, int len, int lane) {
-    if (lane < C::WROWS && row >= 0 && row + lane < len)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (row + lane) * st));
-}
 // Within a warp: (PA, PH) = the map of the segments before this one (after it, for REV), from
 // each segment's (A, H).
 template <class C, bool REV>
@@ -538,7 +533,7 @@ struct Place {
         const int d0 = (cl - static_cast<int>(b) * a.tiles) * C::CH + ch;
         on = d0 < a.D;
         d = on ? d0 : max(a.D - C::NP * 2, 0);
-        nch = min(a.D - d, C::NP * 2);
+        nch = C::X::WIDE ? C::NP * 2 : min(a.D - d, C::NP * 2);
     }
     __device__ __forceinline__ char* at(const Strided& x) const {
         return x.p + b * x.sb + static_cast<int64_t>(d) * static_cast<int64_t>(sizeof(typename C::T));
@@ -590,10 +585,6 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
         load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch, full);
         load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch, full);
         const uint32_t cut = start_bits<C>(a, q.b, static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))), len, q.seg, q.lane);
-        const int64_t ahead = first - q.seg * RPT + static_cast<int64_t>(a.S) * ROWS;
-        prefetch_rows<C>(fp, a.f.st, ahead, len, q.lane);
-        prefetch_rows<C>(vp, a.v.st, ahead, len, q.lane);
-        prefetch_rows<C>(rp, a.r.st, ahead, len, q.lane);
         const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
         // (A, H) of this lane's rows
         F2 ga[RPT][NP], gb[RPT][NP], A[NP], H[NP];
@@ -709,11 +700,6 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
         load_rows<C>(rd, yp + row0 * a.y.st, a.y.st, nl, q.nch, full);
         const uint32_t cut = start_bits<C>(a, q.b, step >= 0 ? static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))) : a.T,
                                            len, q.seg, q.lane);
-        const int64_t ahead = first - q.seg * RPT - static_cast<int64_t>(a.S) * ROWS;
-        prefetch_rows<C>(fp, a.f.st, ahead, len, q.lane);
-        prefetch_rows<C>(vp, a.v.st, ahead, len, q.lane);
-        prefetch_rows<C>(rp, a.r.st, ahead, len, q.lane);
-        prefetch_rows<C>(yp, a.y.st, ahead, len, q.lane);
         const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
         F2 h[NP];
         load_f32(row0 < a.T ? a.saved + (q.b * nsaved + row0 / kSaveRows) * a.D + q.d : nullptr, q.nch, h, 0.0f);
