@@ -14,9 +14,10 @@ current stream.  The functions carry the C names:
     tern_scan_fwd(f, v, r, y, f_bias=None, h0=None, hT=None, ...)
     tern_scan_bwd(f, v, r, dy, saved, workspace, df, dv, dr, ...)
     tern_scan_step(f, v, r, h, y, h_out=None, f_bias=None)
+    tern_orthogonalize(G, out, workspace, steps=5, eps=1e-7, gain=1.0)
 
 Materialize, MaterializeGrouped, GroupedForward, GroupedBackward, MultiAdamW, EmbedForward,
-EmbedBackward, ScanForward, ScanBackward and ScanStep are the same calls with
+EmbedBackward, ScanForward, ScanBackward, ScanStep and Orthogonalize are the same calls with
 their arguments checked and marshalled once, for loops that repeat them on the
 same buffers.
 
@@ -57,7 +58,8 @@ ABI_SYMBOLS = ("tern_tiles_bytes", "tern_materialize", "tern_materialize_grouped
                "tern_linear_bwd_grouped_workspace", "tern_linear_bwd_grouped", "adamw_step", "tern_grad_sumsq_workspace",
                "tern_grad_sumsq", "adamw_step_multi", "tern_sr4_workspace", "tern_sr4_step", "tern_sr4_panel",
                "tern_embed_fwd", "tern_embed_bwd_workspace", "tern_embed_bwd", "tern_scan_saved", "tern_scan_fwd",
-               "tern_scan_bwd_workspace", "tern_scan_bwd", "tern_scan_step", "tern_strerror",
+               "tern_scan_bwd_workspace", "tern_scan_bwd", "tern_scan_step",
+               "tern_orthogonalize_workspace", "tern_orthogonalize", "tern_strerror",
                "tern_device_status", "tern_device_diagnostics", "tern_selftest_wait_timeout")
 
 
@@ -133,6 +135,8 @@ def _load():
         "tern_scan_bwd": ([ctypes.POINTER(_Scan), vp, ctypes.POINTER(_Act), vp] + [ctypes.POINTER(_Act)] * 3 +
                           [vp, vp, vp, sz, vp], ci),
         "tern_scan_step": ([ctypes.POINTER(_Scan), vp, vp, ctypes.POINTER(_Act), vp], ci),
+        "tern_orthogonalize_workspace": ([i64, i64], sz),
+        "tern_orthogonalize": ([vp, i64, i64, ci, cf, cf, vp, vp, sz, vp], ci),
         "tern_strerror": ([ci], ctypes.c_char_p),
         "tern_device_status": ([vp, ci], ci),
         "tern_device_diagnostics": ([ctypes.POINTER(i64), ci], ci),
@@ -688,6 +692,28 @@ class ScanStep:
 def tern_scan_step(f, v, r, h, y, h_out=None, f_bias=None, stream=None):
     """One token of every sequence, all [B, D]: the state h (fp32) moves on, in place unless h_out is given."""
     ScanStep(f, v, r, h, y, h_out, f_bias)(stream)
+
+
+def tern_orthogonalize_workspace(K, N) -> int:
+    return int(lib.tern_orthogonalize_workspace(int(K), int(N)))
+
+
+class Orthogonalize:
+    """tern_orthogonalize with its arguments (and workspace) marshalled once; see GroupedForward."""
+
+    def __init__(self, G, out, workspace, steps=5, eps=1e-7, gain=1.0):
+        K, N = G.shape
+        self._args = (_ptr(G, torch.float32, (K, N), "G"), K, N, int(steps), float(eps), float(gain),
+                      _ptr(out, torch.bfloat16, (K, N), "out"), *_scratch(workspace, "workspace"))
+        self._refs = (G, out, workspace)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_orthogonalize(*self._args, _stream(stream)), "tern_orthogonalize")
+
+
+def tern_orthogonalize(G, out, workspace, steps=5, eps=1e-7, gain=1.0, stream=None):
+    """out (bf16) = gain * G with its singular values moved to about 1 by Newton-Schulz products."""
+    Orthogonalize(G, out, workspace, steps, eps, gain)(stream)
 
 
 def tern_device_status(stream=None, clear=True) -> int:

@@ -55,6 +55,10 @@ extern "C" const char* tern_strerror(int status) {
 
 extern "C" int tern_device_status(void* stream, int clear) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TERN_ERR_CUDA;
-    const int gemm = tern::gemm_status_read(clear), scan = tern::scan_status_read(clear);
-    return gemm != TERN_OK ? gemm : scan;
+    int status = TERN_OK;
+    for (int (*read)(int) : {tern::gemm_status_read, tern::scan_status_read, tern::ortho_status_read}) {
+        const int st = read(clear);
+        if (status == TERN_OK) status = st;
+    }
+    return status;
 }

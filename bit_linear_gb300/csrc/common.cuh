@@ -21,9 +21,10 @@ namespace tern {
 int check_device(int* num_sms);   // TERN_OK or TERN_ERR_DEVICE / TERN_ERR_CUDA
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Host side of the device status words (defined in gemm.cu and scan.cu).
+// Host side of the device status words (defined in gemm.cu, scan.cu and ortho.cu).
 int gemm_status_read(int clear);
 int scan_status_read(int clear);
+int ortho_status_read(int clear);
 
 // The fp16 + e4m3 split of the dX operands (split8.cu): the weight planes h_c*T and
 // l_c*T from q and scale, and the per-call split of dY into the workspace (binary16 and

@@ -55,7 +55,7 @@
 
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "mma.cuh"
 
 namespace tern {
 
@@ -69,10 +69,8 @@ __device__ int g_gemm_site[4];
 namespace {
 
 constexpr int kBM = 128;           // rows of A (and of D) per CTA
-constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s per wait; a healthy wait takes microseconds
 
 enum { EPI_FWD = 0, EPI_DX = 1, EPI_DW = 2 };
-enum { SW128 = 2, SW64 = 4 };   // tcgen05 descriptor layout codes
 
 struct GemmArgs {
     int Mg, Ng, Kg;
@@ -188,55 +186,6 @@ using DxP2 = Cfg<2, 256, 64, false, false, 2, EPI_DX, 4, true>;
 using Dx8_1 = Cfg<1, 256, 64, false, false, 1, EPI_DX, 3, false, true>;
 using Dx8_2 = Cfg<2, 256, 64, false, false, 1, EPI_DX, 4, false, true>;
 
-// tcgen05 instruction descriptor: fp32 D, M x N, operand majors and the A/B format code
-// (kind::f16: 0 = f16, 1 = bf16; kind::f8f6f4: 0 = e4m3).
-__host__ __device__ constexpr uint32_t make_idesc(int M, int N, bool a_mn, bool b_mn, uint32_t fmt = 1u) {
-    return (1u << 4)                       // D format: f32
-           | (fmt << 7)                    // A format
-           | (fmt << 10)                   // B format
-           | (static_cast<uint32_t>(a_mn) << 15)
-           | (static_cast<uint32_t>(b_mn) << 16)
-           | (static_cast<uint32_t>(N >> 3) << 17)
-           | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// tcgen05 shared-memory matrix descriptor.
-__device__ __forceinline__ uint64_t make_sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) |
-           (static_cast<uint64_t>(layout) << 61);
-}
-
-// Descriptor of the kk-th 16-deep k-slice of an operand tile at `base`.
-//  K-major, BK = 64: rows of 128 B (SW128), 8-row atoms 1024 B apart; the slice
-//                    starts 32 B further along the row.
-//  K-major, BK = 32: rows of 64 B (SW64), 8-row atoms 512 B apart.
-//  MN-major (BK 64): 64-element MN chunks of BK k-rows (128 B each, SW128);
-//                    chunks LBO = 64*BK*2 B apart, 8-k-row groups SBO = 1024 B
-//                    apart; the slice starts two groups (2048 B) further.
-template <bool MN, int BK>
-__device__ __forceinline__ uint64_t op_desc(uint32_t base, int kk) {
-    if constexpr (MN) {
-        return make_sdesc(base + kk * 2048u, 64u * BK * 2u, 1024u, SW128);
-    } else if constexpr (BK == 64) {
-        return make_sdesc(base + kk * 32u, 16u, 1024u, SW128);
-    } else {
-        return make_sdesc(base + kk * 32u, 16u, 512u, SW64);
-    }
-}
-
-// Grouped raster: runs of GM m-tiles share an n-tile, so neighbouring CTAs reuse
-// the same B panel and A panels stay resident in L2.
-template <int GM>
-__host__ __device__ __forceinline__ void tile_coords(int tile, int tiles_m, int tiles_n, int& mt, int& nt) {
-    const int group = tile / (GM * tiles_n);
-    const int first_m = group * GM;
-    const int gm = min(GM, tiles_m - first_m);
-    const int local = tile - group * GM * tiles_n;
-    mt = first_m + local % gm;
-    nt = local / gm;
-}
-
 // Bounded wait on an mbarrier phase.  Returns false on timeout (after recording
 // it) or, when `watch_abort`, once another role has raised the abort flag.
 // Site codes: (epilogue kind + 1) * 100 + CTA group * 10 + role, role 1 producer
@@ -245,31 +194,14 @@ __host__ __device__ __forceinline__ void tile_coords(int tile, int tiles_m, int 
 // the self-test.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                              bool watch_abort, int site, uint64_t limit_ns = kWaitLimitNs) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    // The time waited is the sum of the timer's forward steps between polls, each
-    // counted up to 1 ms: a timer that steps backwards, or jumps forward once, cannot
-    // end a healthy wait.  A poll count backs the bound should the timer stall.
-    uint64_t last = ptx::globaltimer(), waited = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (watch_abort && *abort_flag) return false;
-            const uint64_t now = ptx::globaltimer();
-            const int64_t step = static_cast<int64_t>(now - last);
-            last = now;
-            if (step > 0) waited += static_cast<uint64_t>(step < 1000000 ? step : 1000000);
-            if (waited > limit_ns || it >= (1u << 30)) {
-                *abort_flag = 1;
-                atomicExch(&g_gemm_status, 1);
-                if (atomicCAS(&g_gemm_site[0], 0, site) == 0) {
-                    g_gemm_site[1] = static_cast<int>(blockIdx.x);
-                    g_gemm_site[2] = static_cast<int>(bar);
-                    g_gemm_site[3] = static_cast<int>(parity);
-                }
-                return false;
-            }
+    return wait_limited(bar, parity, abort_flag, watch_abort, limit_ns, [&] {
+        atomicExch(&g_gemm_status, 1);
+        if (atomicCAS(&g_gemm_site[0], 0, site) == 0) {
+            g_gemm_site[1] = static_cast<int>(blockIdx.x);
+            g_gemm_site[2] = static_cast<int>(bar);
+            g_gemm_site[3] = static_cast<int>(parity);
         }
-    }
+    });
 }
 
 // Sum over the 32 lanes of v[0..31] (lane l's row of a 32 x 32 block); on
@@ -1167,6 +1099,15 @@ int encode_2d(CUtensorMap* m, const MapKey& k) {
     slot.valid = true;
     return TERN_OK;
 }
+
+}  // namespace
+
+int tensor_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, int64_t inner, int64_t outer, int box_inner,
+                  int box_outer, CUtensorMapSwizzle sw) {
+    return encode_2d(m, MapKey{ptr, inner, outer, box_inner, box_outer, static_cast<int>(sw), static_cast<int>(type)});
+}
+
+namespace {
 
 // Tensor map of a row-major bf16 matrix [outer][inner] read in boxes of box_outer x box_inner.
 int map_bf16(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int box_inner, int box_outer,

@@ -1,0 +1,601 @@
+// Orthogonalised update of a weight's gradient by Newton-Schulz products.
+//
+//   X = G / (|G|_F + eps), then `steps` times  A = X X^T,  M = a I + b A + c A A,  X = M X
+//
+// with (a, b, c) = (3.4445, -4.7750, 2.0315): an odd quintic applied to every singular value,
+// which takes those of X (at most 1) to about 1 (0.7 to 1.2) and leaves the singular vectors
+// alone.  For K > N the products are taken on the other side (A = X^T X, X = X M), so A is always
+// of the smaller side, and G is never transposed.
+//
+// Precision.  A singular value of 1e-3 of the largest grows by up to 3.4445 a step, 480 times in
+// five, and with it whatever noise the roundings before left in its directions: one binary16 or
+// bf16 plane per operand (2^-12, 2^-9) would leave directions of a real gradient's weak singular
+// values to chance.  Every matrix is therefore kept as two binary16 planes hi + lo, 22 bits, and a
+// product is three tensor-core passes into one fp32 accumulator, hi*hi + hi*lo + lo*hi; the
+// dropped lo*lo is 2^-22 of the product.  Scales of powers of two keep both planes normal numbers:
+// |X| <= 1.21 is stored times 2^14, |A| <= 1.46 and |M| <= 3.45 times 2^13 (bounds of the quintic
+// on [0, 1] and its image), so a lo plane's smallest spacing is 2^-38 of 1.
+//
+// Cost: A and M are symmetric, so half of their tiles are computed (and mirrored), and a step is
+// m^2 n + m^3 + 2 m^2 n multiply-adds of one plane, three times that in tensor-core work; bounded
+// by the tensor cores for m >= 2048, by the launches of 3 * steps products for m of some hundreds.
+//
+// The GEMM: a persistent kernel, operands by TMA with the 128-byte swizzle (K-major or MN-major,
+// as the products need), accumulators in TMEM, two of them so that the epilogue of a tile overlaps
+// the next one's main loop.  warp 0 copies, warp 1 issues the MMAs, warps 2-9 drain (two per TMEM
+// lane quarter).  The four operand tiles of a 64-deep k-block feed twelve MMAs: one and a half
+// times the work per byte of shared memory of a plain product.  256 x 256 tiles by CTA pairs where
+// they fill the GPU, else 128 x 128 or 128 x 64 by single CTAs.
+#include <algorithm>
+#include <mutex>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mma.cuh"
+
+namespace tern {
+
+__device__ int g_ortho_status;   // 1 once a bounded wait gave up
+
+namespace {
+
+constexpr int kRows = 128;       // rows of A (and of D) per CTA
+constexpr int kBK = 64;
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScaleX = 16384.0f, kScaleA = 8192.0f, kScaleM = 8192.0f;
+
+enum { OUT_SYM, OUT_POLY, OUT_X, OUT_FINAL };
+
+struct OrthoArgs {
+    CUtensorMap ah, al, bh, bl;
+    int rows, cols, ld;           // D: rows x cols, planes with rows of ld elements (ld % 8 == 0)
+    int tiles_m, tiles_n, units, num_kb;
+    int kind;
+    __half *oh, *ol;              // D's planes
+    const __half *ch, *cl;        // OUT_POLY: A's planes
+    float alpha, pa, pb;          // OUT_POLY: pa I + pb A + alpha acc; else alpha acc
+    __nv_bfloat16* out;           // OUT_FINAL: [rows][cols]
+};
+
+template <int CG_, int BN_, bool A_MN_, bool B_MN_>
+struct OCfg {
+    static constexpr int CG = CG_, BN = BN_;
+    static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
+    static constexpr int THREADS = 64 + 256;
+    static constexpr int TILE_M = kRows * CG, B_ROWS = BN / CG;
+    static constexpr int A_BYTES = kRows * kBK * 2, B_BYTES = B_ROWS * kBK * 2;   // of one plane
+    static constexpr int STAGE_BYTES = 2 * (A_BYTES + B_BYTES);
+    static constexpr int STAGES = 196608 / STAGE_BYTES;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+    static constexpr int RASTER = 16 / CG;
+    static_assert(B_ROWS % 64 == 0 && TMEM_COLS <= 512 && SMEM_BYTES <= 232448, "tile");
+};
+
+// The symmetric products' tiles: those with an element on or above the diagonal, row by row.
+template <class C>
+__host__ __device__ __forceinline__ int sym_first(int mt) { return mt * C::TILE_M / C::BN; }
+
+template <class C>
+__device__ __forceinline__ void unit_tile(const OrthoArgs& a, int unit, int& mt, int& nt) {
+    if (a.kind == OUT_SYM || a.kind == OUT_POLY) {
+        mt = 0;
+        int n = a.tiles_n;
+        while (unit >= n) {
+            unit -= n;
+            ++mt;
+            n = a.tiles_n - sym_first<C>(mt);
+        }
+        nt = sym_first<C>(mt) + unit;
+    } else {
+        tile_coords<C::RASTER>(unit, a.tiles_m, a.tiles_n, mt, nt);
+    }
+}
+
+__device__ __forceinline__ void split16(float v, __half& hi, __half& lo) {
+    hi = __float2half_rn(v);
+    lo = __float2half_rn(v - __half2float(hi));
+}
+
+// One 32-column chunk of a row: r holds columns c0..c0+31 of row `row` of the accumulator.
+__device__ __forceinline__ void ortho_chunk(const OrthoArgs& a, const uint32_t (&r)[32], int row, int c0) {
+    if (row >= a.rows) return;
+    const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
+    const int64_t base = static_cast<int64_t>(row) * a.ld;
+    if (a.kind == OUT_FINAL) {
+        __nv_bfloat16* o = a.out + static_cast<int64_t>(row) * a.cols;
+        const bool wide = a.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int c = c0 + 8 * g;
+            if (wide && c < a.cols) {
+                uint32_t u[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 t = __floats2bfloat162_rn(a.alpha * __uint_as_float(r[8 * g + 2 * k]),
+                                                                   a.alpha * __uint_as_float(r[8 * g + 2 * k + 1]));
+                    u[k] = *reinterpret_cast<const uint32_t*>(&t);
+                }
+                *reinterpret_cast<uint4*>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + k < a.cols) o[c + k] = __float2bfloat16_rn(a.alpha * __uint_as_float(r[8 * g + k]));
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int c = c0 + 8 * g;
+        if (c >= a.ld || (sym && c + 7 < row)) continue;
+        __align__(16) __half hi[8], lo[8];
+        if (a.kind == OUT_POLY) {
+            __align__(16) __half ah[8], al[8];
+            *reinterpret_cast<uint4*>(ah) = *reinterpret_cast<const uint4*>(a.ch + base + c);
+            *reinterpret_cast<uint4*>(al) = *reinterpret_cast<const uint4*>(a.cl + base + c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float x = __half2float(ah[k]) + __half2float(al[k]);
+                const float v = fmaf(a.alpha, __uint_as_float(r[8 * g + k]), a.pb * x) + (c + k == row ? a.pa : 0.0f);
+                split16(v, hi[k], lo[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) split16(a.alpha * __uint_as_float(r[8 * g + k]), hi[k], lo[k]);
+        }
+        if (!sym || c >= row) {
+            *reinterpret_cast<uint4*>(a.oh + base + c) = *reinterpret_cast<const uint4*>(hi);
+            *reinterpret_cast<uint4*>(a.ol + base + c) = *reinterpret_cast<const uint4*>(lo);
+        } else {   // the diagonal lies in the group: one writer per element
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k >= row) a.oh[base + c + k] = hi[k], a.ol[base + c + k] = lo[k];
+        }
+        if (sym) {   // mirrored: a warp's 32 rows are 64 neighbouring bytes
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k > row && c + k < a.rows) {
+                    const int64_t at = static_cast<int64_t>(c + k) * a.ld + row;
+                    a.oh[at] = hi[k], a.ol[at] = lo[k];
+                }
+        }
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_constant__ OrthoArgs a) {
+    constexpr int CG = C::CG;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + C::STAGES * C::STAGE_BYTES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t FULL0 = ptx::smem_u32(bars), EMPTY0 = FULL0 + 8u * C::STAGES;
+    const uint32_t TFULL0 = FULL0 + 16u * C::STAGES, TEMPTY0 = TFULL0 + 16u, DRAIN = TFULL0 + 32u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;   // 0 = leader of the pair
+    const int unit0 = static_cast<int>(blockIdx.x) / CG, stride = static_cast<int>(gridDim.x) / CG;
+    auto wait = [&](uint32_t bar, uint32_t parity, bool watch = true) {
+        return wait_limited(bar, parity, abort_flag, watch, kWaitLimitNs, [&] { atomicExch(&g_ortho_status, 1); });
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            ptx::mbar_init(FULL0 + 8u * s, 1);
+            ptx::mbar_init(EMPTY0 + 8u * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(TFULL0 + 8u * b, 1);
+            ptx::mbar_init(TEMPTY0 + 8u * b, 8 * CG);   // every epilogue warp of the group
+        }
+        ptx::mbar_init(DRAIN, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) {
+            ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+
+    uint32_t issued = 0, issued_parity = 0;   // producer: stages with a copy issued, and its phase
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = unit0; ok && u < a.units; u += stride) {
+            int mt, nt;
+            unit_tile<C>(a, u, mt, nt);
+            const int arow = mt * C::TILE_M + static_cast<int>(rank) * kRows;
+            const int brow = nt * C::BN + static_cast<int>(rank) * C::B_ROWS;
+            for (int kb = 0; kb < a.num_kb; ++kb) {
+                if (!wait(EMPTY0 + 8u * stage, phase ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = FULL0 + 8u * stage;
+                const uint32_t full_at = CG == 2 ? ptx::mapa_shared(full, 0) : full;   // the pair counts on the leader's
+                const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + 2 * C::A_BYTES;
+                if (rank == 0) ptx::mbar_arrive_expect_tx(full, CG * C::STAGE_BYTES);
+                auto load = [&](uint32_t dst, const CUtensorMap* m, bool mn, int rows, int r0) {
+                    const int k0 = kb * kBK;
+                    if (mn) {
+                        for (int j = 0; j < rows / 64; ++j) {
+                            if constexpr (CG == 2) ptx::tma_load_2d_pair(dst + j * 64 * kBK * 2, m, r0 + j * 64, k0, full_at);
+                            else ptx::tma_load_2d(dst + j * 64 * kBK * 2, m, r0 + j * 64, k0, full_at);
+                        }
+                    } else {
+                        if constexpr (CG == 2) ptx::tma_load_2d_pair(dst, m, k0, r0, full_at);
+                        else ptx::tma_load_2d(dst, m, k0, r0, full_at);
+                    }
+                };
+                load(sA, &a.ah, C::A_MN, kRows, arow);
+                load(sB, &a.bh, C::B_MN, C::B_ROWS, brow);
+                load(sB + C::B_BYTES, &a.bl, C::B_MN, C::B_ROWS, brow);
+                load(sA + C::A_BYTES, &a.al, C::A_MN, kRows, arow);
+                issued |= 1u << stage;
+                issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == C::STAGES) stage = 0, phase ^= 1u;
+            }
+        }
+        // Until the MMA has released every stage filled above: the release is an asynchronous
+        // arrival that may otherwise land in the barriers of the next CTA on this SM.
+        if (ok) {
+            for (int s = 0; s < C::STAGES; ++s)
+                if (issued & (1u << s)) wait(EMPTY0 + 8u * s, (issued_parity >> s) & 1u);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ------------------------------------------------------------ MMA issuer (leader only)
+        constexpr uint32_t IDESC = make_idesc(C::TILE_M, C::BN, C::A_MN, C::B_MN, 0u);   // binary16 operands
+        auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t acc) {
+            if constexpr (CG == 2) ptx::mma_bf16_pair(d, da, db, IDESC, acc);
+            else ptx::mma_bf16(d, da, db, IDESC, acc);
+        };
+        auto commit = [&](uint32_t bar) {
+            if constexpr (CG == 2) ptx::mma_commit_pair_mc(bar, 0x3);
+            else ptx::mma_commit(bar);
+        };
+        int stage = 0, local = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = unit0; ok && u < a.units; u += stride, ++local) {
+            const int acc = local & 1;
+            if (!wait(TEMPTY0 + 8u * acc, ((local >> 1) & 1) ^ 1u)) break;
+            ptx::tc_fence_after();
+            const uint32_t d = tmem_base + acc * C::BN;
+            for (int kb = 0; kb < a.num_kb; ++kb) {
+                if (!wait(FULL0 + 8u * stage, phase)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + 2 * C::A_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                    const uint64_t ah = op_desc<C::A_MN, kBK>(sA, kk), al = op_desc<C::A_MN, kBK>(sA + C::A_BYTES, kk);
+                    const uint64_t bh = op_desc<C::B_MN, kBK>(sB, kk), bl = op_desc<C::B_MN, kBK>(sB + C::B_BYTES, kk);
+                    mma(d, ah, bl, kb != 0 || kk != 0 ? 1u : 0u);
+                    mma(d, al, bh, 1u);
+                    mma(d, ah, bh, 1u);
+                }
+                commit(EMPTY0 + 8u * stage);
+                if (++stage == C::STAGES) stage = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+            commit(TFULL0 + 8u * acc);
+        }
+        // every MMA issued completes before TMEM and shared memory go away
+        if constexpr (CG == 2) ptx::mma_commit_pair(DRAIN); else ptx::mma_commit(DRAIN);
+        wait(DRAIN, 0, false);
+        // and the epilogues' release of each accumulator's last use has landed
+        if (ok && !*abort_flag) {
+            for (int acc = 0; acc < 2; ++acc) {
+                if (local <= acc) continue;
+                const int last = (local - 1) - (((local - 1) - acc) & 1);
+                wait(TEMPTY0 + 8u * acc, static_cast<uint32_t>(last >> 1) & 1u);
+            }
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue
+        const int quad = warp & 3;   // TMEM lanes 32*quad .. +31
+        const uint32_t tempty = CG == 2 ? ptx::mapa_shared(TEMPTY0, 0) : TEMPTY0;
+        constexpr int JPW = C::BN / 64;   // 32-column chunks per warp: each quarter's two warps take half
+        const int j0 = ((warp - 2) / 4) * JPW;
+        int local = 0;
+        for (int u = unit0; u < a.units; u += stride, ++local) {
+            const int acc = local & 1;
+            const bool full = wait(TFULL0 + 8u * acc, (local >> 1) & 1);
+            if (!__all_sync(0xffffffffu, full)) break;   // one decision per warp: the loads are collective
+            ptx::tc_fence_after();
+            int mt, nt;
+            unit_tile<C>(a, u, mt, nt);
+            const int row0 = mt * C::TILE_M + static_cast<int>(rank) * kRows;
+            const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::BN;
+            const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
+            if (row0 < a.rows) {
+#pragma unroll 1
+                for (int j = j0; j < j0 + JPW; ++j) {
+                    const int c0 = nt * C::BN + j * 32;
+                    if (c0 >= a.ld) break;
+                    if (sym && c0 + 31 < row0 + quad * 32) continue;   // wholly below the diagonal
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(trow + j * 32, r);
+                    ptx::tmem_wait_ld();
+                    ortho_chunk(a, r, row0 + quad * 32 + lane, c0);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) ptx::mbar_arrive_cluster(tempty + 8u * acc);
+                else ptx::mbar_arrive(TEMPTY0 + 8u * acc);
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if constexpr (CG == 2) ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        // after an abort, copies still in flight must land before the shared memory is released
+        if constexpr (CG == 1) {
+            for (int s = 0; s < C::STAGES; ++s)
+                if (issued & (1u << s)) wait(FULL0 + 8u * s, (issued_parity >> s) & 1u, false);
+        } else {
+            // a pair's copies complete on the leader's barriers; give them time to land
+            const uint64_t t0 = ptx::globaltimer();
+            for (uint32_t i = 0; i < (1u << 24) && ptx::globaltimer() - t0 < 100000ull; ++i) {
+            }
+        }
+    }
+}
+
+}  // namespace
+
+// X's planes from G: rows of ld columns, zeros past the last.
+__global__ void __launch_bounds__(256) tern_ortho_load_kernel(const float* __restrict__ G, int64_t rows, int cols, int ld,
+                                                              const double* __restrict__ sumsq, float eps,
+                                                              __half* __restrict__ hi, __half* __restrict__ lo) {
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const float inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(*sumsq) + static_cast<double>(eps)));
+    const int per_row = ld / 8;
+    const bool wide = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(G) & 15u) == 0;
+    const int64_t total = rows * per_row;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = i / per_row;
+        const int c = static_cast<int>(i - row * per_row) * 8;
+        const float* g = G + row * cols + c;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (wide) {
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + 4 * q < cols) t = __ldg(reinterpret_cast<const float4*>(g + 4 * q));
+                v[4 * q] = t.x, v[4 * q + 1] = t.y, v[4 * q + 2] = t.z, v[4 * q + 3] = t.w;
+            } else {
+#pragma unroll
+                for (int k = 4 * q; k < 4 * q + 4; ++k) v[k] = c + k < cols ? __ldg(g + k) : 0.0f;
+            }
+        }
+        __align__(16) __half h[8], l[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) split16(v[k] * inv, h[k], l[k]);
+        *reinterpret_cast<uint4*>(hi + row * ld + c) = *reinterpret_cast<const uint4*>(h);
+        *reinterpret_cast<uint4*>(lo + row * ld + c) = *reinterpret_cast<const uint4*>(l);
+    }
+}
+
+// ------------------------------------------------------------------------------ host side
+namespace {
+
+// Configures a GEMM kernel once per device; the co-resident CTAs (or pairs).
+template <class C>
+int ortho_units(int num_sms, int* units) {
+    static std::once_flag once[64];
+    static int status[64], clusters[64];
+    int dev = 0;
+    TERN_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return TERN_ERR_DEVICE;
+    std::call_once(once[dev], [&] {
+        status[dev] = TERN_ERR_CUDA;
+        if (cudaFuncSetAttribute(tern_ortho_gemm<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+            return;
+        clusters[dev] = num_sms;
+        if (C::CG == 2) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(2 * (num_sms / 2));
+            cfg.blockDim = dim3(C::THREADS);
+            cfg.dynamicSmemBytes = C::SMEM_BYTES;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, tern_ortho_gemm<C>, &cfg) != cudaSuccess) return;
+            clusters[dev] = std::max(n, 1);
+        }
+        status[dev] = TERN_OK;
+    });
+    *units = clusters[dev];
+    return status[dev];
+}
+
+// An operand: two planes of [outer][inner] binary16, read K-major (inner is the contraction) or MN-major.
+struct Operand {
+    const __half *hi, *lo;
+    int64_t inner, outer;
+};
+
+int map_planes(CUtensorMap* hi, CUtensorMap* lo, const Operand& x, bool mn, int rows) {
+    for (int p = 0; p < 2; ++p) {
+        const int st = tensor_map_2d(p == 0 ? hi : lo, p == 0 ? x.hi : x.lo, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x.inner, x.outer,
+                                     64, mn ? kBK : rows, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != TERN_OK) return st;
+    }
+    return TERN_OK;
+}
+
+template <class C>
+int ortho_gemm(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, int num_sms, cudaStream_t s) {
+    int max_units = 0;
+    if (int st = ortho_units<C>(num_sms, &max_units)) return st;
+    if (int st = map_planes(&a.ah, &a.al, A, C::A_MN, kRows)) return st;
+    if (int st = map_planes(&a.bh, &a.bl, B, C::B_MN, C::B_ROWS)) return st;
+    a.tiles_m = (a.rows + C::TILE_M - 1) / C::TILE_M;
+    a.tiles_n = (a.ld + C::BN - 1) / C::BN;
+    a.num_kb = static_cast<int>((depth + kBK - 1) / kBK);
+    a.units = a.tiles_m * a.tiles_n;
+    if (a.kind == OUT_SYM || a.kind == OUT_POLY) {
+        a.units = 0;
+        for (int mt = 0; mt < a.tiles_m; ++mt) a.units += a.tiles_n - sym_first<C>(mt);
+    }
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(C::CG * std::min(a.units, max_units));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = C::CG == 2 ? 1 : 0;
+    // no programmatic stream serialization, as the library's other GEMMs: the grid starts once every
+    // earlier kernel on the stream has completed, so its TMEM allocation never waits on another grid
+    TERN_CUDA_TRY(cudaLaunchKernelEx(&cfg, tern_ortho_gemm<C>, static_cast<const OrthoArgs&>(a)));
+    return TERN_OK;
+}
+
+// The largest tile of which there are enough for three quarters of the GPU, else the smallest.
+template <bool A_MN, bool B_MN>
+int ortho_product(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, int num_sms, cudaStream_t s) {
+    const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
+    auto tiles = [&](int64_t tm, int64_t tn) {
+        const int64_t n = ((a.rows + tm - 1) / tm) * ((a.ld + tn - 1) / tn);
+        return sym ? n / 2 : n;
+    };
+    if (tiles(256, 256) * 8 >= 3 * num_sms) return ortho_gemm<OCfg<2, 256, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
+    if (tiles(128, 128) * 4 >= 3 * num_sms) return ortho_gemm<OCfg<1, 128, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
+    return ortho_gemm<OCfg<1, 64, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
+}
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+struct OrthoPlan {
+    int64_t m, ldx, ldm;                     // smaller side; elements between rows of X and of A, M
+    int64_t sumsq, sums, x, a, mm, bytes;    // parts of the workspace, in bytes (x: two X of two planes)
+    int64_t x_plane, m_plane;                // bytes of one plane
+};
+
+OrthoPlan ortho_plan(int64_t K, int64_t N) {
+    OrthoPlan p{};
+    p.m = std::min(K, N);
+    p.ldx = round_up(N, 8);
+    p.ldm = round_up(p.m, 8);
+    p.x_plane = round_up(K * p.ldx * 2, 256);
+    p.m_plane = round_up(p.m * p.ldm * 2, 256);
+    const int64_t n = K * N;
+    p.sumsq = 0;
+    p.sums = 256;
+    p.x = p.sums + round_up(static_cast<int64_t>(tern_grad_sumsq_workspace(&n, 1)), 256);
+    p.a = p.x + 4 * p.x_plane;
+    p.mm = p.a + 2 * p.m_plane;
+    p.bytes = p.mm + 2 * p.m_plane;
+    return p;
+}
+
+bool ortho_sizes_ok(int64_t K, int64_t N) { return K >= 0 && N >= 0 && K < (1 << 30) && N < (1 << 30) && (N == 0 || K <= (1ll << 40) / N); }
+
+}  // namespace
+
+int ortho_status_read(int clear) {
+    int v = 0;
+    TERN_CUDA_TRY(cudaMemcpyFromSymbol(&v, g_ortho_status, sizeof(v)));
+    const int zero = 0;
+    if (v != 0 && clear) TERN_CUDA_TRY(cudaMemcpyToSymbol(g_ortho_status, &zero, sizeof(zero)));
+    return v != 0 ? TERN_ERR_TIMEOUT : TERN_OK;
+}
+
+}  // namespace tern
+
+using namespace tern;
+
+extern "C" size_t tern_orthogonalize_workspace(int64_t K, int64_t N) {
+    return ortho_sizes_ok(K, N) && K > 0 && N > 0 ? static_cast<size_t>(ortho_plan(K, N).bytes) : 0;
+}
+
+extern "C" int tern_orthogonalize(const float* G, int64_t K, int64_t N, int steps, float eps, float gain, uint16_t* out,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+    if (!ortho_sizes_ok(K, N) || steps < 1 || steps > 64 || !(eps >= 1e-30f)) return TERN_ERR_ARG;
+    if (K == 0 || N == 0) return TERN_OK;
+    if (!G || !out) return TERN_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(G) % 4 || reinterpret_cast<uintptr_t>(out) % 2) return TERN_ERR_ALIGN;
+    const OrthoPlan p = ortho_plan(K, N);
+    if (!workspace || ws_bytes < static_cast<size_t>(p.bytes)) return TERN_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 128) return TERN_ERR_ALIGN;
+    int num_sms = 0;
+    if (int st = check_device(&num_sms)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    double* sumsq = reinterpret_cast<double*>(ws + p.sumsq);
+    auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
+    __half *x[2][2], *A[2], *M[2];
+    for (int q = 0; q < 2; ++q) {
+        for (int b = 0; b < 2; ++b) x[b][q] = half(p.x + (2 * b + q) * p.x_plane);
+        A[q] = half(p.a + q * p.m_plane), M[q] = half(p.mm + q * p.m_plane);
+    }
+    const int64_t n = K * N;
+    if (int st = tern_grad_sumsq(&G, &n, 1, sumsq, ws + p.sums, static_cast<size_t>(p.x - p.sums), stream)) return st;
+    const int64_t chunks = K * (p.ldx / 8);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, 8 * num_sms));
+    if (int st = launch_pdl(tern_ortho_load_kernel, dim3(blocks), dim3(256), 0, s, G, K, static_cast<int>(N),
+                            static_cast<int>(p.ldx), static_cast<const double*>(sumsq), eps, x[0][0], x[0][1]))
+        return st;
+    const bool tall = K > N;
+    const Operand opA{A[0], A[1], p.ldm, p.m}, opM{M[0], M[1], p.ldm, p.m};
+    for (int t = 0; t < steps; ++t) {
+        const Operand opX{x[t & 1][0], x[t & 1][1], p.ldx, K};
+        OrthoArgs a{};
+        a.rows = static_cast<int>(p.m), a.cols = a.rows, a.ld = static_cast<int>(p.ldm);
+        a.kind = OUT_SYM, a.oh = A[0], a.ol = A[1];
+        a.alpha = kScaleA / (kScaleX * kScaleX);
+        if (int st = tall ? ortho_product<true, true>(a, opX, opX, K, num_sms, s)
+                          : ortho_product<false, false>(a, opX, opX, p.ldx, num_sms, s))
+            return st;
+        a.kind = OUT_POLY, a.oh = M[0], a.ol = M[1], a.ch = A[0], a.cl = A[1];
+        a.alpha = kScaleM * kC / (kScaleA * kScaleA), a.pa = kScaleM * kA, a.pb = kScaleM * kB / kScaleA;
+        if (int st = ortho_product<false, false>(a, opA, opA, p.ldm, num_sms, s)) return st;
+        a.rows = static_cast<int>(K), a.cols = static_cast<int>(N), a.ld = static_cast<int>(p.ldx);
+        a.kind = t + 1 == steps ? OUT_FINAL : OUT_X;
+        a.oh = x[(t + 1) & 1][0], a.ol = x[(t + 1) & 1][1], a.out = reinterpret_cast<__nv_bfloat16*>(out);
+        a.alpha = a.kind == OUT_FINAL ? gain / (kScaleM * kScaleX) : 1.0f / kScaleM;
+        if (int st = tall ? ortho_product<false, false>(a, opX, opM, p.ldm, num_sms, s)
+                          : ortho_product<false, true>(a, opM, opX, p.m, num_sms, s))
+            return st;
+    }
+    return TERN_OK;
+}

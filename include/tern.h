@@ -460,6 +460,20 @@ int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_act* dy, co
  */
 int tern_scan_step(const tern_scan* s, const float* h_in, float* h_out, const tern_act* y, void* stream);
 
+/*
+ * Orthogonalised update: G [K][N] fp32 (a weight's gradient, e.g. gq) to out [K][N] bf16,
+ *   X = G / (|G|_F + eps);  `steps` times  A = X X^T, X = a X + (b A + c A A) X;  out = gain * X
+ * with (a, b, c) = (3.4445, -4.7750, 2.0315): G with its singular values moved to about 1 by
+ * Newton-Schulz products (on the smaller side).  Products run on the tensor cores with operands
+ * of 22 bits (two binary16 planes) and fp32 sums; out is rounded once.
+ *   K, N < 2^30; steps 1..64 (5 is usual); eps >= 1e-30 (1e-7 is usual); G zero gives zeros, a
+ *   non-finite element gives NaN.
+ *   workspace: >= tern_orthogonalize_workspace() bytes, 128-byte aligned.
+ */
+size_t tern_orthogonalize_workspace(int64_t K, int64_t N);
+int tern_orthogonalize(const float* G, int64_t K, int64_t N, int steps, float eps, float gain, uint16_t* out,
+                       void* workspace, size_t ws_bytes, void* stream);
+
 /* Text of a status code (static storage). */
 const char* tern_strerror(int status);
 
