@@ -70,6 +70,7 @@ struct OCfg {
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
     static constexpr int RASTER = 16 / CG;
+    static_assert(2 * SMEM_BYTES > 233472, "one CTA per SM");
     static_assert(B_ROWS % 64 == 0 && TMEM_COLS <= 512 && SMEM_BYTES <= 232448, "tile");
 };
 
@@ -209,6 +210,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
     if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    if (threadIdx.x == 0)
+        for (const CUtensorMap* m : {&a.ah, &a.al, &a.bh, &a.bl}) ptx::tma_prefetch_desc(m);
     ptx::pdl_trigger();
     ptx::pdl_wait();
 
@@ -371,13 +374,71 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
 
 }  // namespace
 
-// X's planes from G: rows of ld columns, zeros past the last.
-__global__ void __launch_bounds__(256) tern_ortho_load_kernel(const float* __restrict__ G, int64_t rows, int cols, int ld,
-                                                              const double* __restrict__ sumsq, float eps,
-                                                              __half* __restrict__ hi, __half* __restrict__ lo) {
+// Sum of squares of G, a partial sum per block in fp64 (fixed chunks and order).  Sixteen squares
+// at a time are added in fp32, whose rounding is then that of sixteen terms, unless their range
+// does not allow it: fp64 throughout would take as long as the arithmetic, not the reads
+// (227 us against 40 us for the 4096 x 12288 gradient).
+constexpr int kSumBlocks = 304;
+__global__ void __launch_bounds__(256) tern_ortho_sumsq_kernel(const float* __restrict__ G, int64_t n, double* __restrict__ partial) {
+    __shared__ double red[256];
     ptx::pdl_trigger();
     ptx::pdl_wait();
-    const float inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(*sumsq) + static_cast<double>(eps)));
+    const bool wide = (reinterpret_cast<uintptr_t>(G) & 15u) == 0;
+    double sum = 0.0;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256 * 16;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n; i += stride) {
+        // four groups of four, a block's threads side by side in each
+        float v[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int64_t at = i + static_cast<int64_t>(q) * gridDim.x * 1024;
+            if (wide && at + 4 <= n) {
+                const float4 t = __ldg(reinterpret_cast<const float4*>(G + at));
+                v[4 * q] = t.x, v[4 * q + 1] = t.y, v[4 * q + 2] = t.z, v[4 * q + 3] = t.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[4 * q + k] = at + k < n ? __ldg(G + at + k) : 0.0f;
+            }
+        }
+        float top = 0.0f, s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            top = fmaxf(top, fabsf(v[k]));
+            s = fmaf(v[k], v[k], s);
+        }
+        // squares between 2^-100 (what underflows is 2^-26 of the largest) and 2^120; a NaN is in s
+        if (top > 8.9e-16f && top < 1e18f) sum += static_cast<double>(s);
+        else if (top != 0.0f || s != s) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum += static_cast<double>(v[k]) * static_cast<double>(v[k]);
+        }
+    }
+    red[threadIdx.x] = sum;
+    __syncthreads();
+    for (int k = 128; k > 0; k >>= 1) {
+        if (threadIdx.x < k) red[threadIdx.x] += red[threadIdx.x + k];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) partial[blockIdx.x] = red[0];
+}
+
+// X's planes from G: rows of ld columns, zeros past the last.  Every block adds up the partial
+// sums for itself, in the same order.
+__global__ void __launch_bounds__(256) tern_ortho_load_kernel(const float* __restrict__ G, int64_t rows, int cols, int ld,
+                                                              const double* __restrict__ partial, int parts, float eps,
+                                                              __half* __restrict__ hi, __half* __restrict__ lo) {
+    __shared__ double red[256];
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < parts; k += 256) sum += partial[k];
+    red[threadIdx.x] = sum;
+    __syncthreads();
+    for (int k = 128; k > 0; k >>= 1) {
+        if (threadIdx.x < k) red[threadIdx.x] += red[threadIdx.x + k];
+        __syncthreads();
+    }
+    const float inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(red[0]) + static_cast<double>(eps)));
     const int per_row = ld / 8;
     const bool wide = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(G) & 15u) == 0;
     const int64_t total = rows * per_row;
@@ -474,18 +535,27 @@ int ortho_gemm(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, 
     }
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    if (C::CG == 2) {
+        // no programmatic stream serialization, as the library's other pair GEMMs: the grid starts once
+        // every earlier kernel on the stream has completed
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+    } else {
+        // A chain of products of some hundred rows is bound by launches: let each set itself up while
+        // the one before it runs.  Two of these CTAs never share an SM (each takes most of its shared
+        // memory), and a grid lets the next one launch only once all its own CTAs hold their TMEM, so
+        // no allocation waits on a grid that waits in turn.
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.gridDim = dim3(C::CG * std::min(a.units, max_units));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = C::CG == 2 ? 1 : 0;
-    // no programmatic stream serialization, as the library's other GEMMs: the grid starts once every
-    // earlier kernel on the stream has completed, so its TMEM allocation never waits on another grid
+    cfg.numAttrs = 1;
     TERN_CUDA_TRY(cudaLaunchKernelEx(&cfg, tern_ortho_gemm<C>, static_cast<const OrthoArgs&>(a)));
     return TERN_OK;
 }
@@ -507,7 +577,7 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 struct OrthoPlan {
     int64_t m, ldx, ldm;                     // smaller side; elements between rows of X and of A, M
-    int64_t sumsq, sums, x, a, mm, bytes;    // parts of the workspace, in bytes (x: two X of two planes)
+    int64_t sums, x, a, mm, bytes;             // parts of the workspace, in bytes (x: two X of two planes)
     int64_t x_plane, m_plane;                // bytes of one plane
 };
 
@@ -518,10 +588,8 @@ OrthoPlan ortho_plan(int64_t K, int64_t N) {
     p.ldm = round_up(p.m, 8);
     p.x_plane = round_up(K * p.ldx * 2, 256);
     p.m_plane = round_up(p.m * p.ldm * 2, 256);
-    const int64_t n = K * N;
-    p.sumsq = 0;
-    p.sums = 256;
-    p.x = p.sums + round_up(static_cast<int64_t>(tern_grad_sumsq_workspace(&n, 1)), 256);
+    p.sums = 0;
+    p.x = round_up(kSumBlocks * static_cast<int64_t>(sizeof(double)), 256);
     p.a = p.x + 4 * p.x_plane;
     p.mm = p.a + 2 * p.m_plane;
     p.bytes = p.mm + 2 * p.m_plane;
@@ -561,19 +629,19 @@ extern "C" int tern_orthogonalize(const float* G, int64_t K, int64_t N, int step
     if (int st = check_device(&num_sms)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    double* sumsq = reinterpret_cast<double*>(ws + p.sumsq);
+    double* sums = reinterpret_cast<double*>(ws + p.sums);
     auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
     __half *x[2][2], *A[2], *M[2];
     for (int q = 0; q < 2; ++q) {
         for (int b = 0; b < 2; ++b) x[b][q] = half(p.x + (2 * b + q) * p.x_plane);
         A[q] = half(p.a + q * p.m_plane), M[q] = half(p.mm + q * p.m_plane);
     }
-    const int64_t n = K * N;
-    if (int st = tern_grad_sumsq(&G, &n, 1, sumsq, ws + p.sums, static_cast<size_t>(p.x - p.sums), stream)) return st;
+    const int parts = static_cast<int>(std::min<int64_t>((K * N + 4095) / 4096, kSumBlocks));
+    if (int st = launch_pdl(tern_ortho_sumsq_kernel, dim3(parts), dim3(256), 0, s, G, K * N, sums)) return st;
     const int64_t chunks = K * (p.ldx / 8);
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, 8 * num_sms));
     if (int st = launch_pdl(tern_ortho_load_kernel, dim3(blocks), dim3(256), 0, s, G, K, static_cast<int>(N),
-                            static_cast<int>(p.ldx), static_cast<const double*>(sumsq), eps, x[0][0], x[0][1]))
+                            static_cast<int>(p.ldx), static_cast<const double*>(sums), parts, eps, x[0][0], x[0][1]))
         return st;
     const bool tall = K > N;
     const Operand opA{A[0], A[1], p.ldm, p.m}, opM{M[0], M[1], p.ldm, p.m};
