@@ -161,12 +161,20 @@ def _check(status: int, where: str):
         raise TernError(status, where)
 
 
+# The handle of the current stream without building a Stream object, which costs about 3 us a call
+# against 0.2 us: as much as a small launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None or _device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _ptr(t, dtype, shape=None, name="tensor"):
