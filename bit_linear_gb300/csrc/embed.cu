@@ -9,8 +9,10 @@
 // token's rows are then summed in the order of their positions, so no atomic adds in floating
 // point and the same bits on every run.
 //   sort     digits of up to 11 bits, one pass for tables below 2048 rows and two below 4 million:
-//            digit counts per 2048-position tile, a scan of each digit's counts over the tiles,
-//            then each tile places its positions (rank within the tile from warp match masks)
+//            digit counts per tile of positions, a scan of each digit's counts over the tiles,
+//            then each tile places its positions (rank within the tile from warp match masks).  Up
+//            to 131072 positions one cluster does it all in one launch (8192 positions, 256 rows:
+//            the gradient takes 26.6 us with three launches a pass)
 //   sum      a block takes 256 sorted positions and 256 channels; each warp sums runs of equal
 //            tokens over its 32 positions in registers; the block joins the runs that cross
 //            its warps.  A run inside the block is written once, straight to dtable.  The block's
@@ -245,6 +247,119 @@ __global__ void __launch_bounds__(256) tern_embed_place_kernel(const __grid_cons
     }
 }
 
+// The whole sort by one cluster, for up to 16 * WARPS * 256 positions: every block ranks a tile of
+// WARPS * 256, the digits' counts are exchanged through distributed shared memory, and the passes
+// follow one another in the launch (place and count take three launches a pass otherwise, most of
+// the time of a sort of some thousand tokens).
+struct ClusterSortArgs {
+    SortArgs s;                // tokens, V, n, bits, present
+    int32_t *keys[2], *pos[2]; // pass i reads i-1 and writes i & 1
+    int passes;
+};
+
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __grid_constant__ ClusterSortArgs g) {
+    constexpr int THREADS = WARPS * 32, R = 8, TILE = THREADS * R;
+    extern __shared__ __align__(16) char smem[];
+    const int digits = 1 << g.s.bits;
+    int32_t* hist = reinterpret_cast<int32_t*>(smem);                    // this tile's counts, read by the peers
+    int32_t* base = hist + digits;                                      // where its positions of a digit go
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(base + digits);         // [WARPS][digits]
+    __shared__ int32_t wsum[WARPS];
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, P = gridDim.x, rank = blockIdx.x;
+    const int64_t i0 = static_cast<int64_t>(rank) * TILE + w * (32 * R);
+    if (g.s.present != nullptr) {
+        uint32_t* words = reinterpret_cast<uint32_t*>(g.s.present);      // the plan rounds its size up to 256 bytes
+        for (int64_t k = static_cast<int64_t>(rank) * THREADS + threadIdx.x; k * 4 < g.s.V; k += static_cast<int64_t>(P) * THREADS)
+            words[k] = 0u;
+    }
+    for (int pass = 0; pass < g.passes; ++pass) {
+        const int shift = pass * g.s.bits;
+        int key[R], at[R], rk[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t i = i0 + r * 32 + lane;
+            key[r] = -1, at[r] = static_cast<int>(i);
+            if (i < g.s.n) {
+                if (pass == 0) {
+                    key[r] = sort_key(g.s, static_cast<int>(i));
+                } else {
+                    key[r] = __ldcg(g.keys[(pass - 1) & 1] + i);
+                    at[r] = __ldcg(g.pos[(pass - 1) & 1] + i);
+                }
+            }
+        }
+        for (int k = threadIdx.x; k < WARPS * digits / 2; k += THREADS) reinterpret_cast<uint32_t*>(cnt)[k] = 0u;
+        __syncthreads();
+        uint16_t* mine = cnt + w * digits;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int dg = key[r] >= 0 ? (key[r] >> shift) & (digits - 1) : digits;
+            const uint32_t same = __match_any_sync(0xffffffffu, dg);
+            const uint32_t lower = same & ((1u << lane) - 1u);
+            rk[r] = dg < digits ? mine[dg] + __popc(lower) : 0;
+            __syncwarp();
+            if (dg < digits && lower == 0) mine[dg] = static_cast<uint16_t>(mine[dg] + __popc(same));
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int k = threadIdx.x; k < digits; k += THREADS) {
+            int run = 0;
+            for (int j = 0; j < WARPS; ++j) {
+                const int x = cnt[j * digits + k];
+                cnt[j * digits + k] = static_cast<uint16_t>(run);
+                run += x;
+            }
+            hist[k] = run;
+        }
+        ptx::cluster_sync();
+        // of each digit: the counts of the tiles before this one, and of all; then a scan over the digits
+        const int per = (digits + THREADS - 1) / THREADS;
+        int own = 0;
+        for (int j = 0; j < per; ++j) {
+            const int k = threadIdx.x * per + j;
+            if (k >= digits) break;
+            const uint32_t here = ptx::smem_u32(hist + k);
+            int before = 0, all = 0;
+            for (int q = 0; q < P; ++q) {
+                int x;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(ptx::mapa_shared(here, q)) : "memory");
+                if (q < rank) before += x;
+                all += x;
+            }
+            base[k] = own + before;      // without the digits of lower threads, added below
+            own += all;
+        }
+        int sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) wsum[w] = sum;
+        __syncthreads();
+        int lower_threads = sum - own;
+        for (int k = 0; k < w; ++k) lower_threads += wsum[k];
+        for (int j = 0; j < per; ++j) {
+            const int k = threadIdx.x * per + j;
+            if (k < digits) base[k] += lower_threads;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (key[r] < 0) continue;
+            const int dg = (key[r] >> shift) & (digits - 1);
+            const int to = base[dg] + mine[dg] + rk[r];
+            g.keys[pass & 1][to] = key[r];
+            g.pos[pass & 1][to] = at[r];
+            if (pass + 1 == g.passes && g.s.present != nullptr && key[r] < g.s.V) g.s.present[key[r]] = 1;
+        }
+        ptx::cluster_sync();   // the placed keys are visible to the cluster, and the peers have read hist
+    }
+}
+
 // ------------------------------------------------------------------------------ the sums
 struct RunArgs {
     const int32_t* keys;       // sorted
@@ -475,6 +590,16 @@ Plan make_plan(int64_t n, int64_t V, int64_t D) {
     return p;
 }
 
+constexpr int64_t kClusterSort = 16 * 32 * 256;   // positions that one cluster sorts
+
+template <int WARPS>
+int launch_sort(const ClusterSortArgs& c, int digits, cudaStream_t s) {
+    const int64_t tile = WARPS * 256;
+    unsigned P = 1;
+    while (P * tile < c.s.n) P *= 2;
+    return launch_cluster(tern_embed_sort_kernel<WARPS>, P, WARPS * 32, digits * (8 + 2 * WARPS), P, s, c);
+}
+
 bool bad_sizes(int64_t n, int64_t V, int64_t D) {
     return n < 0 || V < 1 || D < 0 || n > INT32_MAX - kSortTile || V >= INT32_MAX || D > INT32_MAX - 1024;
 }
@@ -544,18 +669,28 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
         return TERN_OK;
     }
     const int digits = 1 << p.bits;
-    for (int pass = 0; pass < p.passes; ++pass) {
-        q.tokens = pass == 0 ? tokens : nullptr;
-        q.keys_in = pass == 0 ? nullptr : i32(p.keys[(pass - 1) & 1]);
-        q.pos_in = pass == 0 ? nullptr : i32(p.pos[(pass - 1) & 1]);
-        q.keys_out = i32(p.keys[pass & 1]), q.pos_out = i32(p.pos[pass & 1]);
-        q.shift = pass * p.bits, q.last = pass == p.passes - 1;
-        // the first pass also clears `present`, four bytes a thread, by up to one block per SM
-        const int clear = pass == 0 && q.present != nullptr ? static_cast<int>(V / 4096 < num_sms ? V / 4096 : num_sms) : 0;
-        const int blocks = clear > p.sort_tiles ? clear : p.sort_tiles;
-        if (int st = launch_pdl(tern_embed_count_kernel, dim3(blocks), dim3(256), 0, s, q)) return st;
-        if (int st = launch_pdl(tern_embed_offsets_kernel, dim3((digits + 7) / 8), dim3(256), 0, s, q.counts, q.totals, digits, p.sort_tiles)) return st;
-        if (int st = launch_pdl(tern_embed_place_kernel, dim3(p.sort_tiles), dim3(256), 0, s, q)) return st;
+    if (n <= kClusterSort) {
+        ClusterSortArgs c{};
+        c.s = q, c.passes = p.passes;
+        c.s.tokens = tokens;
+        for (int i = 0; i < 2; ++i) c.keys[i] = i32(p.keys[i]), c.pos[i] = i32(p.pos[i]);
+        const int st = n <= 32768 ? launch_sort<8>(c, digits, s) : n <= 65536 ? launch_sort<16>(c, digits, s) : launch_sort<32>(c, digits, s);
+        if (st != TERN_OK) return st;
+        q.keys_out = c.keys[(p.passes - 1) & 1], q.pos_out = c.pos[(p.passes - 1) & 1];
+    } else {
+        for (int pass = 0; pass < p.passes; ++pass) {
+            q.tokens = pass == 0 ? tokens : nullptr;
+            q.keys_in = pass == 0 ? nullptr : i32(p.keys[(pass - 1) & 1]);
+            q.pos_in = pass == 0 ? nullptr : i32(p.pos[(pass - 1) & 1]);
+            q.keys_out = i32(p.keys[pass & 1]), q.pos_out = i32(p.pos[pass & 1]);
+            q.shift = pass * p.bits, q.last = pass == p.passes - 1;
+            // the first pass also clears `present`, four bytes a thread, by up to one block per SM
+            const int clear = pass == 0 && q.present != nullptr ? static_cast<int>(V / 4096 < num_sms ? V / 4096 : num_sms) : 0;
+            const int blocks = clear > p.sort_tiles ? clear : p.sort_tiles;
+            if (int st = launch_pdl(tern_embed_count_kernel, dim3(blocks), dim3(256), 0, s, q)) return st;
+            if (int st = launch_pdl(tern_embed_offsets_kernel, dim3((digits + 7) / 8), dim3(256), 0, s, q.counts, q.totals, digits, p.sort_tiles)) return st;
+            if (int st = launch_pdl(tern_embed_place_kernel, dim3(p.sort_tiles), dim3(256), 0, s, q)) return st;
+        }
     }
     RunArgs a{};
     a.keys = q.keys_out, a.pos = q.pos_out, a.dout = static_cast<const __nv_bfloat16*>(dout), a.dtable = dtable;
@@ -570,6 +705,6 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
     if (int st = launch_pdl(wide ? tern_embed_sum_kernel<true> : tern_embed_sum_kernel<false>,
                             dim3(static_cast<unsigned>(units + fill)), dim3(256), 0, s, a)) return st;
     if (p.run_tiles < 2) return TERN_OK;
-    const unsigned gy = static_cast<unsigned>((D + 31) / 32 < 32 ? (D + 31) / 32 : 32);
+    const unsigned gy = static_cast<unsigned>((D + 31) / 32 < 16 ? (D + 31) / 32 : 16);
     return launch_pdl(tern_embed_join_kernel, dim3(static_cast<unsigned>(p.run_tiles), gy), dim3(256), 0, s, a);
 }

@@ -863,26 +863,6 @@ __global__ void __launch_bounds__(128) tern_scan_step_kernel(const __grid_consta
 // ------------------------------------------------------------------------------ host side
 namespace {
 
-template <class... KArgs, class... Args>
-int launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, unsigned cluster, cudaStream_t s, Args&&... args) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cluster > 8) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-    TERN_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
-    return TERN_OK;
-}
-
 size_t elem(int dtype) { return dtype == TERN_F32 ? 4 : 2; }
 
 // TERN_OK when x can be read or written as rows of elements, else the error; `wide` is cleared
@@ -932,8 +912,8 @@ int launch_fwd(const ScanArgs& a0, int64_t B, int num_sms, cudaStream_t s) {
     a.S = cluster_size(blocks, steps_of(a.T, C::ROWS), static_cast<int64_t>(C::MINB) * num_sms);
     if (blocks * a.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * a.S);
-    if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, a.S, s, a);
-    return launch_cluster(tern_scan_fwd_kernel<C, false>, grid, C::WARPS * 32, 1, s, a);
+    if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, 0, a.S, s, a);
+    return launch_cluster(tern_scan_fwd_kernel<C, false>, grid, C::WARPS * 32, 0, 1, s, a);
 }
 
 template <class C>
@@ -945,8 +925,8 @@ int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStr
     if (blocks * g.s.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * g.s.S);
     if (g.s.S > 1) {
-        if (int st = launch_cluster(tern_scan_bwd_kernel<C, true>, grid, C::WARPS * 32, g.s.S, s, g)) return st;
-    } else if (int st = launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, 1, s, g)) {
+        if (int st = launch_cluster(tern_scan_bwd_kernel<C, true>, grid, C::WARPS * 32, 0, g.s.S, s, g)) return st;
+    } else if (int st = launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, 0, 1, s, g)) {
         return st;
     }
     if (dbias == nullptr) return TERN_OK;

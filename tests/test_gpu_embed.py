@@ -78,6 +78,21 @@ def test_embed_bwd(cuda_lib, n, V, D, accumulate):
         assert torch.equal(g, g2)
 
 
+@pytest.mark.parametrize("n,V", [(32768, 300), (32769, 5000), (65537, 3), (100000, 2047), (131072, 2048), (140000, 9000), (131073, 2)])
+def test_embed_bwd_many_positions(cuda_lib, n, V):
+    """Each of the ways to sort: one cluster with tiles of three sizes, and three launches a pass."""
+    bl = cuda_lib
+    D = 3
+    t = _tok(n, V, n)
+    dout = torch.randint(-8, 9, (n, D), device="cuda").bfloat16()      # integers: the sums are exact
+    g = torch.full((V, D), float("nan"), device="cuda")
+    ws = torch.full((bl.tern_embed_bwd_workspace(n, V, D),), 0xAB, dtype=torch.uint8, device="cuda")
+    bl.tern_embed_bwd(t, dout, g, ws)
+    ok = (t >= 0) & (t < V)
+    ref = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, t[ok], dout[ok].double())
+    assert torch.equal(g.double(), ref)
+
+
 @pytest.mark.parametrize("n", [255, 256, 257, 512, 4096, 5001])
 def test_embed_bwd_long_runs(cuda_lib, n):
     """One token for all positions, and three whose runs end at, before and past the tiles' edges."""
