@@ -13,15 +13,17 @@
 //            then each tile places its positions (rank within the tile from warp match masks).  Up
 //            to 131072 positions one cluster does it all in one launch (8192 positions, 256 rows:
 //            the gradient takes 26.6 us with three launches a pass)
-//   sum      a block takes 256 sorted positions and 256 channels; each warp sums runs of equal
-//            tokens over its 32 positions in registers; the block joins the runs that cross
+//   sum      a block takes 256 sorted positions (64 where those are too few blocks) and 256
+//            channels; each warp sums runs of equal tokens over its positions in registers; the block joins the runs that cross
 //            its warps.  A run inside the block is written once, straight to dtable.  The block's
 //            first run, if it began before the block, and its last, if it goes on, go to a
 //            partial buffer.
 //   join     for each run that leaves its block: the block where it begins adds the partials of
 //            the blocks that it covers, in order.
 // Rows of dtable without a token are written as zeros by extra blocks of the sum launch, from a
-// byte per row that the sort's last pass sets (with accumulate they are left alone).
+// byte per row that the sort's last pass sets (with accumulate they are left alone).  Writing them
+// beside the sort instead, on the SMs it leaves idle, was slower: 279 against 177 us at 32768
+// positions, 100003 x 2048.
 // Bounded by HBM for large tables and batches (dout read once, dtable written once), by the
 // launches of the sort for a few thousand tokens.
 #include <cuda_bf16.h>
@@ -33,7 +35,6 @@ namespace {
 
 constexpr int kMaxBits = 11;         // digit bits of a sort pass
 constexpr int kSortTile = 2048;      // positions per block of the sort (256 threads x 8)
-constexpr int kRunTile = 256;        // sorted positions per block of the sum (8 warps x 32)
 constexpr int kChTile = 256;         // channels per block of the sum
 
 // ------------------------------------------------------------------------------ forward
@@ -247,19 +248,34 @@ __global__ void __launch_bounds__(256) tern_embed_place_kernel(const __grid_cons
     }
 }
 
-// The whole sort by one cluster, for up to 16 * WARPS * 256 positions: every block ranks a tile of
-// WARPS * 256, the digits' counts are exchanged through distributed shared memory, and the passes
-// follow one another in the launch (place and count take three launches a pass otherwise, most of
-// the time of a sort of some thousand tokens).
+// Zeros for the rows [first, last) of dtable that have no token, one warp per row; `has` tells.
+template <bool WIDE, class F>
+__device__ __forceinline__ void fill_rows(float* dtable, int D, int64_t first, int64_t last, int warp, int warps, F has) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t v = first + warp; v < last; v += warps) {
+        if (has(v)) continue;
+        float* row = dtable + v * D;
+        if constexpr (WIDE) {
+            for (int c = lane * 4; c < D; c += 128) __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
+        } else {
+            for (int c = lane; c < D; c += 32) __stcs(row + c, 0.0f);
+        }
+    }
+}
+
+// The whole sort by one cluster, for up to 16 * WARPS * 32 * R positions: every block ranks a tile of
+// WARPS * 32 * R, the digits' counts are exchanged through distributed shared memory, and the passes
+// follow one another in the launch (count, offsets and place take three launches a pass otherwise,
+// most of the time of a sort of some thousand tokens).
 struct ClusterSortArgs {
     SortArgs s;                // tokens, V, n, bits, present
     int32_t *keys[2], *pos[2]; // pass i reads i-1 and writes i & 1
     int passes;
 };
 
-template <int WARPS>
+template <int WARPS, int R>
 __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __grid_constant__ ClusterSortArgs g) {
-    constexpr int THREADS = WARPS * 32, R = 8, TILE = THREADS * R;
+    constexpr int THREADS = WARPS * 32, TILE = THREADS * R;
     extern __shared__ __align__(16) char smem[];
     const int digits = 1 << g.s.bits;
     int32_t* hist = reinterpret_cast<int32_t*>(smem);                    // this tile's counts, read by the peers
@@ -269,12 +285,12 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, P = gridDim.x, rank = blockIdx.x;
-    const int64_t i0 = static_cast<int64_t>(rank) * TILE + w * (32 * R);
     if (g.s.present != nullptr) {
         uint32_t* words = reinterpret_cast<uint32_t*>(g.s.present);      // the plan rounds its size up to 256 bytes
         for (int64_t k = static_cast<int64_t>(rank) * THREADS + threadIdx.x; k * 4 < g.s.V; k += static_cast<int64_t>(P) * THREADS)
             words[k] = 0u;
     }
+    const int64_t i0 = static_cast<int64_t>(rank) * TILE + w * (32 * R);
     for (int pass = 0; pass < g.passes; ++pass) {
         const int shift = pass * g.s.bits;
         int key[R], at[R], rk[R];
@@ -369,7 +385,7 @@ struct RunArgs {
     float* partial;            // [run tiles][2][D]: 0 the run that began before the tile, 1 the one that goes on
     const uint8_t* present;    // null with accumulate
     int64_t ld_dout;
-    int n, V, D, run_tiles, ch_tiles;
+    int n, V, D, run, run_tiles, ch_tiles;   // run: sorted positions per block of the sum
     int accumulate;
     float scale;
 };
@@ -404,7 +420,8 @@ __device__ __forceinline__ void write_row(const RunArgs& a, int key, int c0, int
     }
 }
 
-template <bool WIDE>
+// PW: positions per warp.
+template <bool WIDE, int PW>
 __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_constant__ RunArgs a) {
     __shared__ float first_s[8][kChTile], last_s[8][kChTile];
     __shared__ int first_key[8], last_key[8];   // of a warp's positions; -1 without any
@@ -413,23 +430,15 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t unit = blockIdx.x;
     if (unit >= static_cast<int64_t>(a.run_tiles) * a.ch_tiles) {
-        // rows without a token: zeros, one warp per row
-        const int64_t fill = unit - static_cast<int64_t>(a.run_tiles) * a.ch_tiles;
-        const int64_t stride = (static_cast<int64_t>(gridDim.x) - static_cast<int64_t>(a.run_tiles) * a.ch_tiles) * 8;
-        for (int64_t v = fill * 8 + w; v < a.V; v += stride) {
-            if (a.present[v]) continue;
-            float* row = a.dtable + v * a.D;
-            if constexpr (WIDE) {
-                for (int c = lane * 4; c < a.D; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-            } else {
-                for (int c = lane; c < a.D; c += 32) row[c] = 0.0f;
-            }
-        }
+        // rows without a token
+        const int64_t sums = static_cast<int64_t>(a.run_tiles) * a.ch_tiles;
+        fill_rows<WIDE>(a.dtable, a.D, 0, a.V, static_cast<int>(unit - sums) * 8 + w, static_cast<int>(gridDim.x - sums) * 8,
+                        [&](int64_t v) { return a.present[v] != 0; });
         return;
     }
     const int tile = static_cast<int>(unit / a.ch_tiles), c0 = static_cast<int>(unit % a.ch_tiles) * kChTile;
-    const int p0 = tile * kRunTile + w * 32;
-    const int mine = p0 + lane < a.n ? a.keys[p0 + lane] : a.V;
+    const int p0 = tile * (8 * PW) + w * PW;
+    const int mine = lane < PW && p0 + lane < a.n ? a.keys[p0 + lane] : a.V;
     const int where = mine < a.V ? a.pos[p0 + lane] : 0;
     const int cnt = __popc(__ballot_sync(0xffffffffu, mine < a.V));   // sorted: the live ones come first
     float acc[8] = {};
@@ -488,7 +497,7 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
     // join the runs across the warps, a thread per channel
     const int c = c0 + threadIdx.x;
     if (c >= a.D || first_key[0] < 0) return;
-    const int begin = tile * kRunTile, end = min(begin + kRunTile, a.n);
+    const int begin = tile * (8 * PW), end = min(begin + 8 * PW, a.n);
     const bool from_before = begin > 0 && a.keys[begin - 1] == first_key[0];
     float* part = a.partial + static_cast<int64_t>(tile) * 2 * a.D + c;
     int key = first_key[0];
@@ -521,43 +530,44 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
     else flush();
 }
 
-// Runs that leave the tile they begin in: partial 1 of that tile, then partial 0 of the tiles
-// that they cover; eight warps take every eighth tile, then add up in order.
+// Runs that leave the tile they begin in: partial 1 of that tile, then partial 0 of the tiles that
+// they cover.  A block takes 64 channels; its eight warps take every eighth tile, then add up in order.
 __global__ void __launch_bounds__(256) tern_embed_join_kernel(const __grid_constant__ RunArgs a) {
-    __shared__ float red[8][32];
+    __shared__ float red[8][64];
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const int tile = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int end = min((tile + 1) * kRunTile, a.n);
-    const int key = a.keys[end - 1];
-    if (key >= a.V || end >= a.n || a.keys[end] != key) return;              // ends with the tile
-    const int begin = tile * kRunTile;
-    if (begin > 0 && a.keys[begin] == key && a.keys[begin - 1] == key) return;   // began before it
-    // the last tile of the run: the largest t whose first key is `key`
-    int lo = tile + 1, hi = a.run_tiles - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.keys[mid * kRunTile] == key) lo = mid;
-        else hi = mid - 1;
+    const int begin = tile * a.run, end = min(begin + a.run, a.n);
+    const int key = a.keys[end - 1], next = end < a.n ? a.keys[end] : -1;
+    const int first = a.keys[begin], prev = begin > 0 ? a.keys[begin - 1] : -1;
+    if (key >= a.V || next != key) return;           // ends with the tile
+    if (first == key && prev == key) return;         // began before it
+    // the tiles after this one whose first key is still `key`
+    int more = 0;
+    for (;;) {
+        const int64_t at = static_cast<int64_t>(tile + 1 + more + lane) * a.run;
+        const uint32_t same = __ballot_sync(0xffffffffu, at < a.n && a.keys[at < a.n ? at : 0] == key);
+        more += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+        if (same != 0xffffffffu) break;
     }
-    for (int c0 = blockIdx.y * 32; c0 < a.D; c0 += gridDim.y * 32) {
-        const int c = c0 + lane;
-        float sum = 0.0f;
-        if (c < a.D) {
+    const float* part = a.partial + static_cast<int64_t>(tile + 1) * 2 * a.D;   // partial 0 of the next tile
+    const int c0 = blockIdx.y * 64 + lane, c1 = c0 + 32;
+    float x = 0.0f, y = 0.0f;
 #pragma unroll 4
-            for (int t = tile + 1 + w; t <= lo; t += 8) sum += a.partial[static_cast<int64_t>(t) * 2 * a.D + c];
-        }
-        red[w][lane] = sum;
-        __syncthreads();
-        if (w == 0 && c < a.D) {
-            sum = a.partial[(static_cast<int64_t>(tile) * 2 + 1) * a.D + c];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += red[k][lane];
-            float* p = a.dtable + static_cast<int64_t>(key) * a.D + c;
-            *p = (a.accumulate ? *p : 0.0f) + sum * a.scale;
-        }
-        __syncthreads();
+    for (int t = w; t < more; t += 8) {
+        const float* p = part + static_cast<int64_t>(t) * 2 * a.D;
+        if (c0 < a.D) x += p[c0];
+        if (c1 < a.D) y += p[c1];
     }
+    red[w][lane] = x, red[w][lane + 32] = y;
+    __syncthreads();
+    const int c = blockIdx.y * 64 + threadIdx.x;
+    if (threadIdx.x >= 64 || c >= a.D) return;
+    float sum = part[c - a.D];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += red[k][threadIdx.x];
+    float* p = a.dtable + static_cast<int64_t>(key) * a.D + c;
+    *p = (a.accumulate ? *p : 0.0f) + sum * a.scale;
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -565,7 +575,7 @@ __global__ void __launch_bounds__(256) tern_embed_join_kernel(const __grid_const
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {   // the sort's passes and the workspace's parts, in bytes
-    int passes = 0, bits = 0, sort_tiles = 0, run_tiles = 0;
+    int passes = 0, bits = 0, sort_tiles = 0, run = 0, run_tiles = 0;
     int64_t keys[2], pos[2], counts, totals, present, partial, bytes = 0;
 };
 
@@ -576,7 +586,10 @@ Plan make_plan(int64_t n, int64_t V, int64_t D) {
     p.passes = (need + kMaxBits - 1) / kMaxBits;
     p.bits = (need + p.passes - 1) / p.passes;
     p.sort_tiles = static_cast<int>((n + kSortTile - 1) / kSortTile);
-    p.run_tiles = static_cast<int>((n + kRunTile - 1) / kRunTile);
+    // 64 positions a block while 256 would leave SMs without one (8192 x 512: 20.2 to 16.5 us together
+    // with the smaller sort tiles)
+    p.run = (n + 255) / 256 * ((D + kChTile - 1) / kChTile) < 152 ? 64 : 256;
+    p.run_tiles = static_cast<int>((n + p.run - 1) / p.run);
     auto take = [&](int64_t bytes) {
         const int64_t at = p.bytes;
         p.bytes += round256(bytes);
@@ -592,16 +605,16 @@ Plan make_plan(int64_t n, int64_t V, int64_t D) {
 
 constexpr int64_t kClusterSort = 16 * 32 * 256;   // positions that one cluster sorts
 
-template <int WARPS>
+template <int WARPS, int R>
 int launch_sort(const ClusterSortArgs& c, int digits, cudaStream_t s) {
-    const int64_t tile = WARPS * 256;
+    const int64_t tile = WARPS * 32 * R;
     unsigned P = 1;
     while (P * tile < c.s.n) P *= 2;
-    return launch_cluster(tern_embed_sort_kernel<WARPS>, P, WARPS * 32, digits * (8 + 2 * WARPS), P, s, c);
+    return launch_cluster(tern_embed_sort_kernel<WARPS, R>, P, WARPS * 32, digits * (8 + 2 * WARPS), P, s, c);
 }
 
 bool bad_sizes(int64_t n, int64_t V, int64_t D) {
-    return n < 0 || V < 1 || D < 0 || n > INT32_MAX - kSortTile || V >= INT32_MAX || D > INT32_MAX - 1024;
+    return n < 0 || V < 1 || D < 0 || n > INT32_MAX - kSortTile || V >= INT32_MAX || D > 65535 * 64;
 }
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -669,12 +682,16 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
         return TERN_OK;
     }
     const int digits = 1 << p.bits;
+    const bool wide = D % 8 == 0 && ld_dout % 8 == 0 && aligned16(dout) && aligned16(dtable);
     if (n <= kClusterSort) {
         ClusterSortArgs c{};
         c.s = q, c.passes = p.passes;
         c.s.tokens = tokens;
         for (int i = 0; i < 2; ++i) c.keys[i] = i32(p.keys[i]), c.pos[i] = i32(p.pos[i]);
-        const int st = n <= 32768 ? launch_sort<8>(c, digits, s) : n <= 65536 ? launch_sort<16>(c, digits, s) : launch_sort<32>(c, digits, s);
+        const int st = n <= 8192    ? launch_sort<8, 2>(c, digits, s)
+                       : n <= 32768 ? launch_sort<32, 2>(c, digits, s)
+                       : n <= 65536 ? launch_sort<32, 4>(c, digits, s)
+                                    : launch_sort<32, 8>(c, digits, s);
         if (st != TERN_OK) return st;
         q.keys_out = c.keys[(p.passes - 1) & 1], q.pos_out = c.pos[(p.passes - 1) & 1];
     } else {
@@ -695,16 +712,16 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
     RunArgs a{};
     a.keys = q.keys_out, a.pos = q.pos_out, a.dout = static_cast<const __nv_bfloat16*>(dout), a.dtable = dtable;
     a.partial = reinterpret_cast<float*>(ws + p.partial), a.present = q.present, a.ld_dout = ld_dout;
-    a.n = q.n, a.V = q.V, a.D = static_cast<int>(D), a.run_tiles = p.run_tiles;
+    a.n = q.n, a.V = q.V, a.D = static_cast<int>(D), a.run = p.run, a.run_tiles = p.run_tiles;
     a.ch_tiles = static_cast<int>((D + kChTile - 1) / kChTile);
     a.accumulate = accumulate ? 1 : 0, a.scale = scale;
-    const bool wide = D % 8 == 0 && ld_dout % 8 == 0 && aligned16(dout) && aligned16(dtable);
     const int64_t units = static_cast<int64_t>(a.run_tiles) * a.ch_tiles;
     const int64_t fill = accumulate ? 0 : (V + 7) / 8 < 8 * num_sms ? (V + 7) / 8 : 8 * num_sms;
     if (units + fill > INT32_MAX) return TERN_ERR_ARG;
-    if (int st = launch_pdl(wide ? tern_embed_sum_kernel<true> : tern_embed_sum_kernel<false>,
-                            dim3(static_cast<unsigned>(units + fill)), dim3(256), 0, s, a)) return st;
+    void (*const sum)(RunArgs) = p.run == 64 ? (wide ? tern_embed_sum_kernel<true, 8> : tern_embed_sum_kernel<false, 8>)
+                                             : (wide ? tern_embed_sum_kernel<true, 32> : tern_embed_sum_kernel<false, 32>);
+    if (int st = launch_pdl(sum, dim3(static_cast<unsigned>(units + fill)), dim3(256), 0, s, a)) return st;
     if (p.run_tiles < 2) return TERN_OK;
-    const unsigned gy = static_cast<unsigned>((D + 31) / 32 < 16 ? (D + 31) / 32 : 16);
+    const unsigned gy = static_cast<unsigned>((D + 63) / 64);
     return launch_pdl(tern_embed_join_kernel, dim3(static_cast<unsigned>(p.run_tiles), gy), dim3(256), 0, s, a);
 }

@@ -389,7 +389,8 @@ int tern_sr4_panel(const int8_t* q, const uint32_t* packed_prev, const float* sc
  * Embedding of n tokens from a table [V][D] (TERN_BF16 or TERN_F32, dense):
  *   out[i][:] = bf16_rne(scale * table[tokens[i]][:])
  * tokens: TERN_I32 or TERN_I64 ids; an id outside 0..V-1 is padding and gives a row of zeros.
- * out: bf16, rows ld_out >= D elements apart.  n, D >= 0; n, V and D below 2^31 - 2048.
+ * out: bf16, rows ld_out >= D elements apart.  n, D >= 0, V >= 1; n and V below 2^31 - 2048,
+ * D at most 2^22 - 64.
  */
 int tern_embed_fwd(const void* tokens, int tokens_dtype, const void* table, int table_dtype, int64_t n,
                    int64_t V, int64_t D, float scale, void* out, int64_t ld_out, void* stream);
