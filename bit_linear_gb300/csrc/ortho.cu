@@ -50,7 +50,7 @@ enum { OUT_SYM, OUT_POLY, OUT_X, OUT_FINAL };
 struct OrthoArgs {
     CUtensorMap ah, al, bh, bl;
     int rows, cols, ld;           // D: rows x cols, planes with rows of ld elements (ld % 8 == 0)
-    int tiles_m, tiles_n, units, num_kb;
+    int tiles_m, tiles_n, units, num_kb, split;
     int kind;
     __half *oh, *ol;              // D's planes
     const __half *ch, *cl;        // OUT_POLY: A's planes
@@ -58,10 +58,13 @@ struct OrthoArgs {
     __nv_bfloat16* out;           // OUT_FINAL: [rows][cols]
 };
 
-template <int CG_, int BN_, bool A_MN_, bool B_MN_>
+// CG CTAs share one MMA (a pair has the tile's 256 rows between them).  SPLIT: one tile per cluster,
+// whose CTAs each take a part of the contraction.
+template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool SPLIT_ = false>
 struct OCfg {
     static constexpr int CG = CG_, BN = BN_;
-    static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
+    static constexpr bool A_MN = A_MN_, B_MN = B_MN_, SPLIT = SPLIT_;
+    static constexpr int PART_LD = BN + 4;   // SPLIT: floats between the rows of a partial tile in shared memory
     static constexpr int THREADS = 64 + 256;
     static constexpr int TILE_M = kRows * CG, B_ROWS = BN / CG;
     static constexpr int A_BYTES = kRows * kBK * 2, B_BYTES = B_ROWS * kBK * 2;   // of one plane
@@ -99,69 +102,57 @@ __device__ __forceinline__ void split16(float v, __half& hi, __half& lo) {
     lo = __float2half_rn(v - __half2float(hi));
 }
 
-// One 32-column chunk of a row: r holds columns c0..c0+31 of row `row` of the accumulator.
-__device__ __forceinline__ void ortho_chunk(const OrthoArgs& a, const uint32_t (&r)[32], int row, int c0) {
-    if (row >= a.rows) return;
+// Eight columns c..c+7 (c % 8 == 0) of row `row`, from the accumulator's values.
+__device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&acc)[8], int row, int c) {
     const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
-    const int64_t base = static_cast<int64_t>(row) * a.ld;
+    if (row >= a.rows || c >= a.ld || (sym && c + 7 < row)) return;
     if (a.kind == OUT_FINAL) {
-        __nv_bfloat16* o = a.out + static_cast<int64_t>(row) * a.cols;
-        const bool wide = a.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+        __nv_bfloat16* o = a.out + static_cast<int64_t>(row) * a.cols + c;
+        if (a.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
+            uint32_t u[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int c = c0 + 8 * g;
-            if (wide && c < a.cols) {
-                uint32_t u[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 t = __floats2bfloat162_rn(a.alpha * __uint_as_float(r[8 * g + 2 * k]),
-                                                                   a.alpha * __uint_as_float(r[8 * g + 2 * k + 1]));
-                    u[k] = *reinterpret_cast<const uint32_t*>(&t);
-                }
-                *reinterpret_cast<uint4*>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (c + k < a.cols) o[c + k] = __float2bfloat16_rn(a.alpha * __uint_as_float(r[8 * g + k]));
+            for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(a.alpha * acc[2 * k], a.alpha * acc[2 * k + 1]);
+                u[k] = *reinterpret_cast<const uint32_t*>(&t);
             }
+            *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < a.cols) o[k] = __float2bfloat16_rn(a.alpha * acc[k]);
         }
         return;
     }
+    const int64_t base = static_cast<int64_t>(row) * a.ld + c;
+    __align__(16) __half hi[8], lo[8];
+    if (a.kind == OUT_POLY) {
+        __align__(16) __half ah[8], al[8];
+        *reinterpret_cast<uint4*>(ah) = *reinterpret_cast<const uint4*>(a.ch + base);
+        *reinterpret_cast<uint4*>(al) = *reinterpret_cast<const uint4*>(a.cl + base);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int c = c0 + 8 * g;
-        if (c >= a.ld || (sym && c + 7 < row)) continue;
-        __align__(16) __half hi[8], lo[8];
-        if (a.kind == OUT_POLY) {
-            __align__(16) __half ah[8], al[8];
-            *reinterpret_cast<uint4*>(ah) = *reinterpret_cast<const uint4*>(a.ch + base + c);
-            *reinterpret_cast<uint4*>(al) = *reinterpret_cast<const uint4*>(a.cl + base + c);
+        for (int k = 0; k < 8; ++k) {
+            const float x = __half2float(ah[k]) + __half2float(al[k]);
+            split16(fmaf(a.alpha, acc[k], a.pb * x) + (c + k == row ? a.pa : 0.0f), hi[k], lo[k]);
+        }
+    } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float x = __half2float(ah[k]) + __half2float(al[k]);
-                const float v = fmaf(a.alpha, __uint_as_float(r[8 * g + k]), a.pb * x) + (c + k == row ? a.pa : 0.0f);
-                split16(v, hi[k], lo[k]);
+        for (int k = 0; k < 8; ++k) split16(a.alpha * acc[k], hi[k], lo[k]);
+    }
+    if (!sym || c >= row) {
+        *reinterpret_cast<uint4*>(a.oh + base) = *reinterpret_cast<const uint4*>(hi);
+        *reinterpret_cast<uint4*>(a.ol + base) = *reinterpret_cast<const uint4*>(lo);
+    } else {   // the diagonal lies in the group: one writer per element
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k >= row) a.oh[base + k] = hi[k], a.ol[base + k] = lo[k];
+    }
+    if (sym) {   // mirrored: a warp's 32 rows are 64 neighbouring bytes
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k > row && c + k < a.rows) {
+                const int64_t at = static_cast<int64_t>(c + k) * a.ld + row;
+                a.oh[at] = hi[k], a.ol[at] = lo[k];
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) split16(a.alpha * __uint_as_float(r[8 * g + k]), hi[k], lo[k]);
-        }
-        if (!sym || c >= row) {
-            *reinterpret_cast<uint4*>(a.oh + base + c) = *reinterpret_cast<const uint4*>(hi);
-            *reinterpret_cast<uint4*>(a.ol + base + c) = *reinterpret_cast<const uint4*>(lo);
-        } else {   // the diagonal lies in the group: one writer per element
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (c + k >= row) a.oh[base + c + k] = hi[k], a.ol[base + c + k] = lo[k];
-        }
-        if (sym) {   // mirrored: a warp's 32 rows are 64 neighbouring bytes
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (c + k > row && c + k < a.rows) {
-                    const int64_t at = static_cast<int64_t>(c + k) * a.ld + row;
-                    a.oh[at] = hi[k], a.ol[at] = lo[k];
-                }
-        }
     }
 }
 
@@ -178,7 +169,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
     const uint32_t TFULL0 = FULL0 + 16u * C::STAGES, TEMPTY0 = TFULL0 + 16u, DRAIN = TFULL0 + 32u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;   // 0 = leader of the pair
-    const int unit0 = static_cast<int>(blockIdx.x) / CG, stride = static_cast<int>(gridDim.x) / CG;
+    const int part = C::SPLIT ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const int group = C::SPLIT ? a.split : CG;                     // CTAs per unit
+    const int unit0 = static_cast<int>(blockIdx.x) / group, stride = static_cast<int>(gridDim.x) / group;
+    const int kb0 = C::SPLIT ? a.num_kb * part / a.split : 0, kb1 = C::SPLIT ? a.num_kb * (part + 1) / a.split : a.num_kb;
     auto wait = [&](uint32_t bar, uint32_t parity, bool watch = true) {
         return wait_limited(bar, parity, abort_flag, watch, kWaitLimitNs, [&] { atomicExch(&g_ortho_status, 1); });
     };
@@ -226,7 +220,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
             unit_tile<C>(a, u, mt, nt);
             const int arow = mt * C::TILE_M + static_cast<int>(rank) * kRows;
             const int brow = nt * C::BN + static_cast<int>(rank) * C::B_ROWS;
-            for (int kb = 0; kb < a.num_kb; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait(EMPTY0 + 8u * stage, phase ^ 1u)) {
                     ok = false;
                     break;
@@ -281,7 +275,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
             if (!wait(TEMPTY0 + 8u * acc, ((local >> 1) & 1) ^ 1u)) break;
             ptx::tc_fence_after();
             const uint32_t d = tmem_base + acc * C::BN;
-            for (int kb = 0; kb < a.num_kb; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait(FULL0 + 8u * stage, phase)) {
                     ok = false;
                     break;
@@ -292,7 +286,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
                 for (int kk = 0; kk < kBK / 16; ++kk) {
                     const uint64_t ah = op_desc<C::A_MN, kBK>(sA, kk), al = op_desc<C::A_MN, kBK>(sA + C::A_BYTES, kk);
                     const uint64_t bh = op_desc<C::B_MN, kBK>(sB, kk), bl = op_desc<C::B_MN, kBK>(sB + C::B_BYTES, kk);
-                    mma(d, ah, bl, kb != 0 || kk != 0 ? 1u : 0u);
+                    mma(d, ah, bl, kb != kb0 || kk != 0 ? 1u : 0u);
                     mma(d, al, bh, 1u);
                     mma(d, ah, bh, 1u);
                 }
@@ -330,7 +324,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
             const int row0 = mt * C::TILE_M + static_cast<int>(rank) * kRows;
             const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::BN;
             const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
-            if (row0 < a.rows) {
+            if constexpr (C::SPLIT) {
+                // the partial tile to shared memory, over the operand stages (all read by now)
+                float* p = reinterpret_cast<float*>(smem_raw + (base - raw)) + (quad * 32 + lane) * C::PART_LD;
+#pragma unroll 1
+                for (int j = j0; j < j0 + JPW; ++j) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(trow + j * 32, r);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<uint4*>(p + j * 32 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                }
+            } else if (row0 < a.rows) {
 #pragma unroll 1
                 for (int j = j0; j < j0 + JPW; ++j) {
                     const int c0 = nt * C::BN + j * 32;
@@ -339,7 +345,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
                     uint32_t r[32];
                     ptx::tmem_ld_32x32b_x32(trow + j * 32, r);
                     ptx::tmem_wait_ld();
-                    ortho_chunk(a, r, row0 + quad * 32 + lane, c0);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[8 * g + k]);
+                        ortho_group(a, v, row0 + quad * 32 + lane, c0 + 8 * g);
+                    }
                 }
             }
             ptx::tc_fence_before();
@@ -351,8 +363,41 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
         }
     }
 
+    if constexpr (C::SPLIT) {
+        // each CTA adds up its share of the tile's columns over the partial tiles, in order
+        __syncwarp();
+        ptx::cluster_sync();
+        if (warp >= 2 && unit0 < a.units) {
+            int mt, nt;
+            unit_tile<C>(a, unit0, mt, nt);
+            const int r = (warp & 3) * 32 + lane, share = C::BN / a.split;
+            for (int g = (warp - 2) / 4; g < share / 8; g += 2) {
+                const int col = part * share + 8 * g;
+                const uint32_t at = base + static_cast<uint32_t>(r * C::PART_LD + col) * 4u;
+                float v[8] = {};
+                for (int k = 0; k < a.split; ++k) {
+                    const uint32_t peer = ptx::mapa_shared(at, k);
+                    float x[8];
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(peer) : "memory");
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]) : "r"(peer + 16u) : "memory");
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += x[i];
+                }
+                ortho_group(a, v, mt * C::TILE_M + r, nt * C::BN + col);
+            }
+        }
+    }
     ptx::tc_fence_before();
-    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    if constexpr (C::SPLIT) {
+        __syncwarp();
+        ptx::cluster_sync();   // the peers have read this CTA's partial tile
+    } else if constexpr (CG == 2) {
+        ptx::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         ptx::tc_fence_after();
         if constexpr (CG == 2) ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
@@ -520,7 +565,7 @@ int map_planes(CUtensorMap* hi, CUtensorMap* lo, const Operand& x, bool mn, int 
 }
 
 template <class C>
-int ortho_gemm(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, int num_sms, cudaStream_t s) {
+int ortho_gemm(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, int num_sms, cudaStream_t s, int split = 1) {
     int max_units = 0;
     if (int st = ortho_units<C>(num_sms, &max_units)) return st;
     if (int st = map_planes(&a.ah, &a.al, A, C::A_MN, kRows)) return st;
@@ -534,28 +579,30 @@ int ortho_gemm(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, 
         for (int mt = 0; mt < a.tiles_m; ++mt) a.units += a.tiles_n - sym_first<C>(mt);
     }
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    if (C::CG == 2) {
-        // no programmatic stream serialization, as the library's other pair GEMMs: the grid starts once
-        // every earlier kernel on the stream has completed
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-    } else {
+    cudaLaunchAttribute attr[2];
+    cfg.numAttrs = 0;
+    a.split = C::SPLIT ? split : 1;
+    const int group = C::SPLIT ? split : C::CG;
+    if (group > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = group;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    if (C::CG == 1) {
         // A chain of products of some hundred rows is bound by launches: let each set itself up while
         // the one before it runs.  Two of these CTAs never share an SM (each takes most of its shared
         // memory), and a grid lets the next one launch only once all its own CTAs hold their TMEM, so
-        // no allocation waits on a grid that waits in turn.
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        // no allocation waits on a grid that waits in turn.  The pairs start, as the library's other
+        // pair GEMMs, once every earlier kernel on the stream has completed.
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
-    cfg.gridDim = dim3(C::CG * std::min(a.units, max_units));
+    cfg.gridDim = dim3(C::SPLIT ? a.units * split : C::CG * std::min(a.units, max_units));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
     TERN_CUDA_TRY(cudaLaunchKernelEx(&cfg, tern_ortho_gemm<C>, static_cast<const OrthoArgs&>(a)));
     return TERN_OK;
 }
@@ -570,6 +617,11 @@ int ortho_product(OrthoArgs& a, const Operand& A, const Operand& B, int64_t dept
     };
     if (tiles(256, 256) * 8 >= 3 * num_sms) return ortho_gemm<OCfg<2, 256, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
     if (tiles(128, 128) * 4 >= 3 * num_sms) return ortho_gemm<OCfg<1, 128, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
+    // Few tiles: clusters of S CTAs share each one's contraction, at least two k-blocks a CTA.  Clusters
+    // of 8, 4 and 2 CTAs of this size fit 16, 36 and 76 times.
+    const int64_t n = tiles(128, 64) + (sym ? (a.rows + 127) / 128 : 0), kb = (depth + kBK - 1) / kBK;
+    const int S = n <= 16 && kb >= 16 ? 8 : n <= 36 && kb >= 8 ? 4 : n <= 76 && kb >= 4 ? 2 : 1;
+    if (S > 1) return ortho_gemm<OCfg<1, 64, A_MN, B_MN, true>>(a, A, B, depth, num_sms, s, S);
     return ortho_gemm<OCfg<1, 64, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
 }
 
