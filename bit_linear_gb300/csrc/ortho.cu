@@ -16,6 +16,12 @@
 // |X| <= 1.21 is stored times 2^14, |A| <= 1.46 and |M| <= 3.45 times 2^13 (bounds of the quintic
 // on [0, 1] and its image), so a lo plane's smallest spacing is 2^-38 of 1.
 //
+// Two steps at once, for m >= 1024 and n >= 1.5 m: with M0 = p(A), the next step's A is M0 A M0 =
+// (M0 M0) A, as all of these commute, and X = (M1 M0) X, so the pair needs one product of X in place
+// of two: 3 m^2 n / 2 + 5 m^3 / 2 multiply-adds against 3 m^2 n + m^3.  More than two would pass the
+// square of the amplification on to A's rounding.  The weak directions stay sound: where the
+// eigenvalue of A is lost in A's rounding M is still a, and they are X's own.
+//
 // Cost: A and M are symmetric, so half of their tiles are computed (and mirrored), and a step is
 // m^2 n + m^3 + 2 m^2 n multiply-adds of one plane, three times that in tensor-core work; bounded
 // by the tensor cores for m >= 2048, by the launches of 3 * steps products for m of some hundreds.
@@ -44,6 +50,7 @@ constexpr int kRows = 128;       // rows of A (and of D) per CTA
 constexpr int kBK = 64;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 16384.0f, kScaleA = 8192.0f, kScaleM = 8192.0f;
+constexpr float kScaleQ = 4096.0f;   // of products of two M, at most 11.9
 
 enum { OUT_SYM, OUT_POLY, OUT_X, OUT_FINAL };
 
@@ -64,7 +71,6 @@ template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool SPLIT_ = false>
 struct OCfg {
     static constexpr int CG = CG_, BN = BN_;
     static constexpr bool A_MN = A_MN_, B_MN = B_MN_, SPLIT = SPLIT_;
-    static constexpr int PART_LD = BN + 4;   // SPLIT: floats between the rows of a partial tile in shared memory
     static constexpr int THREADS = 64 + 256;
     static constexpr int TILE_M = kRows * CG, B_ROWS = BN / CG;
     static constexpr int A_BYTES = kRows * kBK * 2, B_BYTES = B_ROWS * kBK * 2;   // of one plane
@@ -159,6 +165,7 @@ __device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&ac
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_constant__ OrthoArgs a) {
     constexpr int CG = C::CG;
+    [[maybe_unused]] constexpr int PART_LD = C::BN + 4;   // SPLIT: floats between the rows of a partial tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
             const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
             if constexpr (C::SPLIT) {
                 // the partial tile to shared memory, over the operand stages (all read by now)
-                float* p = reinterpret_cast<float*>(smem_raw + (base - raw)) + (quad * 32 + lane) * C::PART_LD;
+                float* p = reinterpret_cast<float*>(smem_raw + (base - raw)) + (quad * 32 + lane) * PART_LD;
 #pragma unroll 1
                 for (int j = j0; j < j0 + JPW; ++j) {
                     uint32_t r[32];
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
             const int r = (warp & 3) * 32 + lane, share = C::BN / a.split;
             for (int g = (warp - 2) / 4; g < share / 8; g += 2) {
                 const int col = part * share + 8 * g;
-                const uint32_t at = base + static_cast<uint32_t>(r * C::PART_LD + col) * 4u;
+                const uint32_t at = base + static_cast<uint32_t>(r * PART_LD + col) * 4u;
                 float v[8] = {};
                 for (int k = 0; k < a.split; ++k) {
                     const uint32_t peer = ptx::mapa_shared(at, k);
@@ -629,8 +636,9 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 struct OrthoPlan {
     int64_t m, ldx, ldm;                     // smaller side; elements between rows of X and of A, M
-    int64_t sums, x, a, mm, bytes;             // parts of the workspace, in bytes (x: two X of two planes)
+    int64_t sums, x, mat[4], bytes;            // parts of the workspace, in bytes (x: two X of two planes; A, M and two more for pairs of steps)
     int64_t x_plane, m_plane;                // bytes of one plane
+    bool pairs;                              // steps two at a time
 };
 
 OrthoPlan ortho_plan(int64_t K, int64_t N) {
@@ -642,9 +650,9 @@ OrthoPlan ortho_plan(int64_t K, int64_t N) {
     p.m_plane = round_up(p.m * p.ldm * 2, 256);
     p.sums = 0;
     p.x = round_up(kSumBlocks * static_cast<int64_t>(sizeof(double)), 256);
-    p.a = p.x + 4 * p.x_plane;
-    p.mm = p.a + 2 * p.m_plane;
-    p.bytes = p.mm + 2 * p.m_plane;
+    p.pairs = p.m >= 1024 && 2 * std::max(K, N) >= 3 * p.m;
+    p.bytes = p.x + 4 * p.x_plane;
+    for (int i = 0; i < (p.pairs ? 4 : 2); ++i) p.mat[i] = p.bytes, p.bytes += 2 * p.m_plane;
     return p;
 }
 
@@ -683,11 +691,9 @@ extern "C" int tern_orthogonalize(const float* G, int64_t K, int64_t N, int step
     char* ws = static_cast<char*>(workspace);
     double* sums = reinterpret_cast<double*>(ws + p.sums);
     auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
-    __half *x[2][2], *A[2], *M[2];
-    for (int q = 0; q < 2; ++q) {
-        for (int b = 0; b < 2; ++b) x[b][q] = half(p.x + (2 * b + q) * p.x_plane);
-        A[q] = half(p.a + q * p.m_plane), M[q] = half(p.mm + q * p.m_plane);
-    }
+    __half* x[2][2];
+    for (int q = 0; q < 2; ++q)
+        for (int i = 0; i < 2; ++i) x[i][q] = half(p.x + (2 * i + q) * p.x_plane);
     const int parts = static_cast<int>(std::min<int64_t>((K * N + 4095) / 4096, kSumBlocks));
     if (int st = launch_pdl(tern_ortho_sumsq_kernel, dim3(parts), dim3(256), 0, s, G, K * N, sums)) return st;
     const int64_t chunks = K * (p.ldx / 8);
@@ -696,25 +702,53 @@ extern "C" int tern_orthogonalize(const float* G, int64_t K, int64_t N, int step
                             static_cast<int>(p.ldx), static_cast<const double*>(sums), parts, eps, x[0][0], x[0][1]))
         return st;
     const bool tall = K > N;
-    const Operand opA{A[0], A[1], p.ldm, p.m}, opM{M[0], M[1], p.ldm, p.m};
-    for (int t = 0; t < steps; ++t) {
-        const Operand opX{x[t & 1][0], x[t & 1][1], p.ldx, K};
+    Operand mat[4];   // symmetric, by commuting factors: A, M, and for pairs of steps M0 M0 then M1, and the second A
+    for (int i = 0; i < (p.pairs ? 4 : 2); ++i) mat[i] = Operand{half(p.mat[i]), half(p.mat[i] + p.m_plane), p.ldm, p.m};
+    auto to = [](OrthoArgs& a, const Operand& d) { a.oh = const_cast<__half*>(d.hi), a.ol = const_cast<__half*>(d.lo); };
+    // D = alpha L R, of which half the tiles are computed
+    auto product = [&](const Operand& L, const Operand& R, const Operand& D, float alpha) {
         OrthoArgs a{};
         a.rows = static_cast<int>(p.m), a.cols = a.rows, a.ld = static_cast<int>(p.ldm);
-        a.kind = OUT_SYM, a.oh = A[0], a.ol = A[1];
-        a.alpha = kScaleA / (kScaleX * kScaleX);
-        if (int st = tall ? ortho_product<true, true>(a, opX, opX, K, num_sms, s)
-                          : ortho_product<false, false>(a, opX, opX, p.ldx, num_sms, s))
-            return st;
-        a.kind = OUT_POLY, a.oh = M[0], a.ol = M[1], a.ch = A[0], a.cl = A[1];
+        a.kind = OUT_SYM, a.alpha = alpha;
+        to(a, D);
+        return ortho_product<false, false>(a, L, R, p.ldm, num_sms, s);
+    };
+    // D = a I + b A + c A A
+    auto poly = [&](const Operand& A, const Operand& D) {
+        OrthoArgs a{};
+        a.rows = static_cast<int>(p.m), a.cols = a.rows, a.ld = static_cast<int>(p.ldm);
+        a.kind = OUT_POLY, a.ch = A.hi, a.cl = A.lo;
         a.alpha = kScaleM * kC / (kScaleA * kScaleA), a.pa = kScaleM * kA, a.pb = kScaleM * kB / kScaleA;
-        if (int st = ortho_product<false, false>(a, opA, opA, p.ldm, num_sms, s)) return st;
+        to(a, D);
+        return ortho_product<false, false>(a, A, A, p.ldm, num_sms, s);
+    };
+    int cur = 0;
+    for (int t = 0; t < steps; cur ^= 1) {
+        const Operand X{x[cur][0], x[cur][1], p.ldx, K};
+        OrthoArgs a{};
+        a.rows = static_cast<int>(p.m), a.cols = a.rows, a.ld = static_cast<int>(p.ldm);
+        a.kind = OUT_SYM, a.alpha = kScaleA / (kScaleX * kScaleX);
+        to(a, mat[0]);
+        if (int st = tall ? ortho_product<true, true>(a, X, X, K, num_sms, s) : ortho_product<false, false>(a, X, X, p.ldx, num_sms, s))
+            return st;
+        if (int st = poly(mat[0], mat[1])) return st;
+        Operand Q = mat[1];
+        float q_scale = kScaleM;
+        t += 1;
+        if (p.pairs && t < steps) {
+            if (int st = product(mat[1], mat[1], mat[2], kScaleQ / (kScaleM * kScaleM))) return st;   // M0 M0
+            if (int st = product(mat[2], mat[0], mat[3], 1.0f / kScaleQ)) return st;                  // the second A
+            if (int st = poly(mat[3], mat[2])) return st;                                             // M1
+            if (int st = product(mat[2], mat[1], mat[0], kScaleQ / (kScaleM * kScaleM))) return st;   // M1 M0
+            Q = mat[0], q_scale = kScaleQ;
+            t += 1;
+        }
+        a = OrthoArgs{};
         a.rows = static_cast<int>(K), a.cols = static_cast<int>(N), a.ld = static_cast<int>(p.ldx);
-        a.kind = t + 1 == steps ? OUT_FINAL : OUT_X;
-        a.oh = x[(t + 1) & 1][0], a.ol = x[(t + 1) & 1][1], a.out = reinterpret_cast<__nv_bfloat16*>(out);
-        a.alpha = a.kind == OUT_FINAL ? gain / (kScaleM * kScaleX) : 1.0f / kScaleM;
-        if (int st = tall ? ortho_product<false, false>(a, opX, opM, p.ldm, num_sms, s)
-                          : ortho_product<false, true>(a, opM, opX, p.m, num_sms, s))
+        a.kind = t == steps ? OUT_FINAL : OUT_X;
+        a.oh = x[cur ^ 1][0], a.ol = x[cur ^ 1][1], a.out = reinterpret_cast<__nv_bfloat16*>(out);
+        a.alpha = a.kind == OUT_FINAL ? gain / (q_scale * kScaleX) : 1.0f / q_scale;
+        if (int st = tall ? ortho_product<false, false>(a, X, Q, p.ldm, num_sms, s) : ortho_product<false, true>(a, Q, X, p.m, num_sms, s))
             return st;
     }
     return TERN_OK;
