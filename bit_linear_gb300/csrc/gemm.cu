@@ -1107,6 +1107,43 @@ int tensor_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, int
     return encode_2d(m, MapKey{ptr, inner, outer, box_inner, box_outer, static_cast<int>(sw), static_cast<int>(type)});
 }
 
+int tensor_map_3d(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, int64_t n0, int64_t n1, int64_t n2, int64_t s1,
+                  int64_t s2, int box0, int box1) {
+    struct Slot {
+        const void* ptr;
+        int64_t key[8];
+        CUtensorMap map;
+        bool valid;
+    };
+    static Slot cache[256];
+    const int64_t key[8] = {static_cast<int64_t>(type), n0, n1, n2, s1, s2, box0, box1};
+    size_t h = reinterpret_cast<uintptr_t>(ptr) >> 4;
+    for (int64_t k : key) h = (h ^ static_cast<size_t>(k)) * 0x9E3779B97F4A7C15ull;
+    Slot& slot = cache[(h >> 32) % 256];
+    {
+        std::lock_guard<std::mutex> lock(g_map_mu);
+        if (slot.valid && slot.ptr == ptr && std::memcmp(slot.key, key, sizeof(key)) == 0) {
+            *m = slot.map;
+            return TERN_OK;
+        }
+    }
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return TERN_ERR_CUDA;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n0), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(s2)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return TERN_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_map_mu);
+    slot.ptr = ptr;
+    std::memcpy(slot.key, key, sizeof(key));
+    slot.map = *m;
+    slot.valid = true;
+    return TERN_OK;
+}
+
 namespace {
 
 // Tensor map of a row-major bf16 matrix [outer][inner] read in boxes of box_outer x box_inner.

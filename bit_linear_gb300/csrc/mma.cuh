@@ -11,6 +11,11 @@ namespace tern {
 int tensor_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, int64_t inner, int64_t outer, int box_inner,
                   int box_outer, CUtensorMapSwizzle sw);
 
+// Tensor map of [n2][n1][n0] elements with strides of s1 and s2 bytes, read in boxes of box1 x box0
+// (gemm.cu; cached).
+int tensor_map_3d(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, int64_t n0, int64_t n1, int64_t n2, int64_t s1,
+                  int64_t s2, int box0, int box1);
+
 namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s per wait; a healthy wait takes microseconds

@@ -31,7 +31,7 @@
 
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "mma.cuh"
 
 namespace tern {
 namespace {
@@ -72,9 +72,10 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 __device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xffffffffu, a.v, from)}; }
 
 // --------------------------------------------------------------- element access
-// NP pairs of neighbouring elements of a row.  WIDE: one 8-byte access; otherwise element by
-// element (odd widths, strides or addresses), where a row's last lane may hold fewer: nch
-// elements are there, loads repeat the last and stores leave the others out.
+// NP pairs of neighbouring elements of a row, eight bytes.  WIDE: inputs come by TMA and outputs are
+// stored eight bytes at a time; otherwise element by element (odd widths, strides or addresses),
+// where a row's last lane may hold fewer: nch elements are there, loads repeat the last and stores
+// leave the others out.
 template <class T, bool WIDE_>
 struct Io;
 template <bool WIDE_>
@@ -83,7 +84,6 @@ struct Io<__nv_bfloat16, WIDE_> {
     static constexpr int NP = 2;
     using Raw = uint2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
-        if constexpr (WIDE) return __ldg(reinterpret_cast<const uint2*>(p));
         const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
         const uint32_t x0 = __ldg(q), x1 = __ldg(q + min(1, nch - 1)), x2 = __ldg(q + min(2, nch - 1)), x3 = __ldg(q + min(3, nch - 1));
         return make_uint2(x0 | x1 << 16, x2 | x3 << 16);
@@ -117,7 +117,6 @@ struct Io<float, WIDE_> {
     static constexpr int NP = 1;
     using Raw = float2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
-        if constexpr (WIDE) return __ldg(reinterpret_cast<const float2*>(p));
         const float* q = reinterpret_cast<const float*>(p);
         return make_float2(__ldg(q), __ldg(q + min(1, nch - 1)));
     }
@@ -229,6 +228,7 @@ struct ScanArgs {
     const float* h_in;    // h0 (forward) or dhT (backward); may be null
     float* h_out;         // hT or dh0; may be null
     int T, D, tiles, S;
+    CUtensorMap maps[4];  // WIDE: f, v, r and dy
 };
 struct GradArgs {
     ScanArgs s;
@@ -238,12 +238,12 @@ struct GradArgs {
 
 // How a block cuts its rows and channels: LPR lanes make a row of CH channels, a lane's segment
 // has RPT rows, a warp SEGS segments.
-template <class T_, bool WIDE_, int LPR_, int RPT_, int WARPS_ = 8, int MINB_ = 2>
+template <class T_, bool WIDE_, int LPR_, int RPT_, int WARPS_, int MINB_, int STAGES_>
 struct Shape {
     using T = T_;
     using X = Io<T_, WIDE_>;
     static constexpr int NP = X::NP, LPR = LPR_, RPT = RPT_;
-    static constexpr int WARPS = WARPS_, MINB = MINB_, SEGS = 32 / LPR, CH = LPR * NP * 2, WROWS = SEGS * RPT, ROWS = WARPS * WROWS;
+    static constexpr int WARPS = WARPS_, MINB = MINB_, STAGES = STAGES_, SEGS = 32 / LPR, CH = LPR * NP * 2, WROWS = SEGS * RPT, ROWS = WARPS * WROWS;
 };
 
 // Totals of the S blocks of a cluster, pushed by each block into every block's shared memory
@@ -283,10 +283,10 @@ __device__ __forceinline__ void push_pairs(const float* mine, const F2 (&x)[NP],
                      : "memory");
     }
 }
-// Waits for a phase of the exchange, at most about two seconds: a peer block is resident and a
-// healthy wait takes microseconds.  On expiry the status word is set; the thread waits no more
+// Waits for a phase of the exchange or of a copy, at most about two seconds: a peer block is
+// resident, a copy on its way, and a healthy wait takes microseconds.  On expiry the status word is set; the thread waits no more
 // and runs its steps to the end, so that the block's barriers still match (its results are void).
-__device__ __forceinline__ bool wait_peers(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
     const uint32_t b = ptx::smem_u32(bar);
     uint64_t last = 0, waited = 0;
     for (uint32_t it = 0;; ++it) {
@@ -314,26 +314,62 @@ __device__ __forceinline__ int rows_live(const ScanArgs& a, int b) {
     return a.lengths != nullptr ? min(max(a.lengths[b], 0), a.T) : a.T;
 }
 // bit i: row i of this lane's segment (live) starts a document; a lane of the warp reads each row's
+// byte, or two of them.
 template <class C>
 __device__ __forceinline__ uint32_t start_bits(const ScanArgs& a, int64_t b, int warp_row0, int len, int seg, int lane) {
-    static_assert(C::WROWS <= 32, "a byte per lane");
+    static_assert(C::WROWS == 16 || C::WROWS == 32 || C::WROWS == 64, "whole bytes of rows per lane");
     if (a.starts == nullptr) return 0;
-    const bool st = lane < C::WROWS && warp_row0 + lane < len && a.starts[b * a.T + warp_row0 + lane] != 0;
-    return (__ballot_sync(0xffffffffu, st) >> (seg * C::RPT)) & ((1u << C::RPT) - 1u);
+    const uint8_t* p = a.starts + b * a.T + warp_row0;
+    auto vote = [&](int r) { return __ballot_sync(0xffffffffu, r < C::WROWS && warp_row0 + r < len && p[r] != 0); };
+    const uint32_t lo = vote(lane), hi = C::WROWS > 32 ? vote(lane + 32) : 0u;
+    const int at = seg * C::RPT;
+    return ((at < 32 ? lo : hi) >> (at & 31)) & ((1u << C::RPT) - 1u);
 }
-// The segment's rows of one tensor.  full: all are live; otherwise the others stay zero.
-template <class C>
-__device__ __forceinline__ void load_rows(typename C::X::Raw (&raw)[C::RPT], const char* p, int64_t st, int nl, int nch, bool full) {
-    if (full) {
+// A step's inputs: NT tensors of ROWS rows by CH channels.  WIDE: copied by TMA into a ring of
+// STAGES tiles in shared memory, ahead of their use, where a lane reads its eight bytes of a row at
+// constant offsets; otherwise loaded into registers by the lanes that use them.
+template <class C, int NT>
+struct Inputs {
+    static constexpr bool WIDE = C::X::WIDE;
+    static constexpr int ROW_BYTES = C::CH * static_cast<int>(sizeof(typename C::T)), TILE_BYTES = C::ROWS * ROW_BYTES;
+    static constexpr int SMEM = WIDE ? C::STAGES * NT * TILE_BYTES + 128 : 0;
+    using Raw = typename C::X::Raw;
+    Raw raw[WIDE ? 1 : NT][WIDE ? 1 : C::RPT];
+    const char* at;   // WIDE: this lane's bytes of its segment's first row, in the current stage's first tensor
+
+    __device__ __forceinline__ Raw get(int t, int i) const {
+        if constexpr (WIDE) return *reinterpret_cast<const Raw*>(at + t * TILE_BYTES + i * ROW_BYTES);
+        else return raw[t][i];
+    }
+    // The rows of tensor t; those that are not live stay zero.
+    __device__ __forceinline__ void load(int t, const char* p, int64_t st, int nl, int nch, bool full) {
+        if constexpr (!WIDE) {
+            if (full) {
 #pragma unroll
-        for (int i = 0; i < C::RPT; ++i) raw[i] = C::X::load(p + i * st, nch);
-    } else {
+                for (int i = 0; i < C::RPT; ++i) raw[t][i] = C::X::load(p + i * st, nch);
+            } else {
 #pragma unroll
-        for (int i = 0; i < C::RPT; ++i) {
-            raw[i] = typename C::X::Raw{};
-            if (i < nl) raw[i] = C::X::load(p + i * st, nch);
+                for (int i = 0; i < C::RPT; ++i) {
+                    raw[t][i] = Raw{};
+                    if (i < nl) raw[t][i] = C::X::load(p + i * st, nch);
+                }
+            }
         }
     }
+};
+// One step's tiles: rows from step * ROWS on of sequence b, channels from ch0 on (one thread).
+// What lies past the last row or channel arrives as zeros.
+template <class C, int NT>
+__device__ __forceinline__ void copy_step(const CUtensorMap* maps, uint32_t stage, uint32_t bar, int ch0, int64_t step, int b) {
+    using I = Inputs<C, NT>;
+    ptx::mbar_arrive_expect_tx(bar, NT * I::TILE_BYTES);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(stage + t * I::TILE_BYTES),
+            "l"(reinterpret_cast<uint64_t>(maps + t)), "r"(ch0), "r"(static_cast<int>(step * C::ROWS)), "r"(b), "r"(bar)
+            : "memory");
 }
 // Within a warp: (PA, PH) = the map of the segments before this one (after it, for REV), from
 // each segment's (A, H).
@@ -394,14 +430,13 @@ __device__ __forceinline__ void fold_map(const float* A, const float* H, int str
 // The parts of a step that run over a segment's rows.  PLAIN: all rows of the warp are live and
 // none starts a document, which leaves out the selects.
 template <class C, bool PLAIN>
-__device__ __forceinline__ void fwd_rows(const typename C::X::Raw (&rf)[C::RPT], const typename C::X::Raw (&rv)[C::RPT],
-                                         const F2 (&lb)[C::NP], int nl, uint32_t cut, F2 (&ga)[C::RPT][C::NP],
+__device__ __forceinline__ void fwd_rows(const Inputs<C, 3>& in, const F2 (&lb)[C::NP], int nl, uint32_t cut, F2 (&ga)[C::RPT][C::NP],
                                          F2 (&gb)[C::RPT][C::NP], F2 (&A)[C::NP], F2 (&H)[C::NP]) {
 #pragma unroll
     for (int i = 0; i < C::RPT; ++i) {
         F2 f[C::NP], v[C::NP], n;
-        C::X::get(rf[i], f);
-        C::X::get(rv[i], v);
+        C::X::get(in.get(0, i), f);
+        C::X::get(in.get(1, i), v);
 #pragma unroll
         for (int j = 0; j < C::NP; ++j) {
             decay(f[j], lb[j], ga[i][j], n);
@@ -424,12 +459,12 @@ __device__ __forceinline__ void fwd_again(const F2 (&ga)[C::RPT][C::NP], F2 (&gb
         for (int j = 0; j < C::NP; ++j) gb[i][j] = h[j] = apply(ga[i][j], gb[i][j], h[j], !PLAIN);
 }
 template <class C, bool PLAIN>
-__device__ __forceinline__ void fwd_store(const typename C::X::Raw (&rr)[C::RPT], const F2 (&hs)[C::RPT][C::NP], char* y, int64_t st,
+__device__ __forceinline__ void fwd_store(const Inputs<C, 3>& in, const F2 (&hs)[C::RPT][C::NP], char* y, int64_t st,
                                           int nl, int nr, int nch) {
 #pragma unroll
     for (int i = 0; i < C::RPT; ++i) {
         F2 r[C::NP], o[C::NP];
-        C::X::get(rr[i], r);
+        C::X::get(in.get(2, i), r);
 #pragma unroll
         for (int j = 0; j < C::NP; ++j) {
             o[j] = mul2(gate(r[j]), hs[i][j]);
@@ -440,18 +475,16 @@ __device__ __forceinline__ void fwd_store(const typename C::X::Raw (&rr)[C::RPT]
 }
 // Per row: s = a, n = 1 - a, o = sigmoid(r) dy, x = sigmoid(-r); and the segment's folds.
 template <class C, bool PLAIN>
-__device__ __forceinline__ void bwd_rows(const typename C::X::Raw (&rf)[C::RPT], const typename C::X::Raw (&rv)[C::RPT],
-                                         const typename C::X::Raw (&rr)[C::RPT], const typename C::X::Raw (&rd)[C::RPT],
-                                         const F2 (&lb)[C::NP], int nl, uint32_t cut, F2 (&s)[C::RPT][C::NP],
+__device__ __forceinline__ void bwd_rows(const Inputs<C, 4>& in, const F2 (&lb)[C::NP], int nl, uint32_t cut, F2 (&s)[C::RPT][C::NP],
                                          F2 (&n)[C::RPT][C::NP], F2 (&o)[C::RPT][C::NP], F2 (&x)[C::RPT][C::NP],
                                          F2 (&A)[C::NP], F2 (&H)[C::NP], F2 (&G)[C::NP]) {
 #pragma unroll
     for (int i = 0; i < C::RPT; ++i) {
         F2 f[C::NP], v[C::NP], r[C::NP], dy[C::NP], so;
-        C::X::get(rf[i], f);
-        C::X::get(rv[i], v);
-        C::X::get(rr[i], r);
-        C::X::get(rd[i], dy);
+        C::X::get(in.get(0, i), f);
+        C::X::get(in.get(1, i), v);
+        C::X::get(in.get(2, i), r);
+        C::X::get(in.get(3, i), dy);
 #pragma unroll
         for (int j = 0; j < C::NP; ++j) {
             decay(f[j], lb[j], s[i][j], n[i][j]);
@@ -473,7 +506,7 @@ __device__ __forceinline__ void bwd_rows(const typename C::X::Raw (&rf)[C::RPT],
 }
 // From h before the rows and e after them: the gradients, written; e before the rows.
 template <class C, bool PLAIN>
-__device__ __forceinline__ void bwd_store(const typename C::X::Raw (&rv)[C::RPT], const F2 (&s)[C::RPT][C::NP],
+__device__ __forceinline__ void bwd_store(const Inputs<C, 4>& in, const F2 (&s)[C::RPT][C::NP],
                                           const F2 (&n)[C::RPT][C::NP], const F2 (&o)[C::RPT][C::NP], F2 (&x)[C::RPT][C::NP],
                                           int nl, uint32_t cut, int nr, int nch, F2 (&h)[C::NP], F2 (&e)[C::NP],
                                           F2 (&dbias)[C::NP], char* df_p, int64_t df_st, char* dv_p, int64_t dv_st, char* dr_p,
@@ -482,7 +515,7 @@ __device__ __forceinline__ void bwd_store(const typename C::X::Raw (&rv)[C::RPT]
 #pragma unroll
     for (int i = 0; i < C::RPT; ++i) {
         F2 v[C::NP];
-        C::X::get(rv[i], v);
+        C::X::get(in.get(1, i), v);
 #pragma unroll
         for (int j = 0; j < C::NP; ++j) {
             if (!PLAIN && ((cut >> i) & 1u)) h[j] = both(0.0f);
@@ -521,7 +554,7 @@ __device__ __forceinline__ bool sync_cuts(bool docs, uint32_t cut) {
 // What every block of the two kernels starts from.
 template <class C>
 struct Place {
-    int w, lane, seg, c, ch, rank, d, nch;
+    int w, lane, seg, c, ch, rank, d0, d, nch;
     int64_t b;
     bool on;      // this lane has channels; the others repeat the row's last and store nothing
     __device__ __forceinline__ explicit Place(const ScanArgs& a) {
@@ -530,7 +563,7 @@ struct Place {
         const int cl = blockIdx.x / a.S;
         rank = blockIdx.x - cl * a.S;
         b = cl / a.tiles;
-        const int d0 = (cl - static_cast<int>(b) * a.tiles) * C::CH + ch;
+        d0 = (cl - static_cast<int>(b) * a.tiles) * C::CH + ch;
         on = d0 < a.D;
         d = on ? d0 : max(a.D - C::NP * 2, 0);
         nch = C::X::WIDE ? C::NP * 2 : min(a.D - d, C::NP * 2);
@@ -549,10 +582,18 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
     using X = typename C::X;
     constexpr int NP = C::NP, RPT = C::RPT, WARPS = C::WARPS, ROWS = C::ROWS;
     static_assert(kSaveRows % RPT == 0, "saved states fall on segment boundaries");
+    extern __shared__ __align__(128) char smem[];
+    __shared__ uint64_t full[C::STAGES];
     __shared__ alignas(16) float aggA[2][WARPS][C::CH], aggH[2][WARPS][C::CH];
     __shared__ alignas(16) float carry_s[2][C::CH];                // not CL: the state after a step
     __shared__ typename std::conditional<CL, Exchange<C>, int>::type ex;
     const Place<C> q(a);
+    if constexpr (C::X::WIDE) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < C::STAGES; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
+            ptx::fence_mbar_init();
+        }
+    }
     if constexpr (CL) open_exchange(ex);
     ptx::pdl_trigger();
     ptx::pdl_wait();
@@ -562,34 +603,53 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
     const char *fp = q.at(a.f), *vp = q.at(a.v), *rp = q.at(a.r);
     char* yp = q.at(a.y);
 
+    const int steps = (a.T + ROWS - 1) / ROWS;
+    const int iters = (steps + a.S - 1) / a.S;
+    using In = Inputs<C, 3>;
+    const uint32_t ring = (ptx::smem_u32(smem) + 127u) & ~127u;
+    [[maybe_unused]] const char* lane_at = smem + (ring - ptx::smem_u32(smem)) + (q.w * C::WROWS + q.seg * RPT) * In::ROW_BYTES + q.c * 8;
+    auto step_of = [&](int it) { return static_cast<int64_t>(it) * a.S + q.rank; };
+    auto has_rows = [&](int it) { return it < iters && step_of(it) * ROWS < len; };   // live rows to copy
+    auto copy = [&](int it) {
+        if (has_rows(it))
+            copy_step<C, 3>(a.maps, ring + it % C::STAGES * (3 * In::TILE_BYTES), ptx::smem_u32(&full[it % C::STAGES]),
+                            q.d0 - q.ch, step_of(it), static_cast<int>(q.b));
+    };
+    if constexpr (C::X::WIDE) {
+        if (threadIdx.x == 0)
+            for (int i = 0; i < C::STAGES; ++i) copy(i);
+        __syncthreads();   // the barriers are set up before anyone waits
+    }
     F2 lb[NP], carry[NP];
     load_f32(a.f_bias == nullptr ? nullptr : a.f_bias + q.d, q.nch, lb, 0.0f);
     load_f32(a.h_in == nullptr ? nullptr : a.h_in + q.b * a.D + q.d, q.nch, carry, 0.0f);
 #pragma unroll
     for (int j = 0; j < NP; ++j) lb[j] = mul2(lb[j], both(-kLog2e));
-    const int steps = (a.T + ROWS - 1) / ROWS;
-    const int iters = (steps + a.S - 1) / a.S;
     [[maybe_unused]] bool ok = true;
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
-        const int64_t first = static_cast<int64_t>(it * a.S + q.rank) * ROWS + q.w * C::WROWS + q.seg * RPT;
+        const int64_t first = step_of(it) * ROWS + q.w * C::WROWS + q.seg * RPT;
         const int row0 = first < a.T ? static_cast<int>(first) : a.T;
         const int nl = min(max(len - row0, 0), RPT);   // live rows of this segment
         if constexpr (CL) {
             if (threadIdx.x == 0)
                 ptx::mbar_arrive_expect_tx(ptx::smem_u32(&ex.bar[p]), static_cast<uint32_t>(a.S * C::CH * 2 * sizeof(float)));
         }
-        const bool full = __all_sync(0xffffffffu, nl == RPT);
-        typename X::Raw rf[RPT], rv[RPT], rr[RPT];
-        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch, full);
-        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch, full);
-        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch, full);
+        const bool all_live = __all_sync(0xffffffffu, nl == RPT);
+        In in;
+        if constexpr (C::X::WIDE) {
+            in.at = lane_at + it % C::STAGES * (3 * In::TILE_BYTES);
+            if (has_rows(it)) ok = ok && wait_phase(&full[it % C::STAGES], (it / C::STAGES) & 1);
+        }
+        in.load(0, fp + row0 * a.f.st, a.f.st, nl, q.nch, all_live);
+        in.load(1, vp + row0 * a.v.st, a.v.st, nl, q.nch, all_live);
+        in.load(2, rp + row0 * a.r.st, a.r.st, nl, q.nch, all_live);
         const uint32_t cut = start_bits<C>(a, q.b, static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))), len, q.seg, q.lane);
-        const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
+        const bool plain = all_live && (!docs || __all_sync(0xffffffffu, cut == 0));
         // (A, H) of this lane's rows
         F2 ga[RPT][NP], gb[RPT][NP], A[NP], H[NP];
-        if (plain) fwd_rows<C, true>(rf, rv, lb, nl, cut, ga, gb, A, H);
-        else fwd_rows<C, false>(rf, rv, lb, nl, cut, ga, gb, A, H);
+        if (plain) fwd_rows<C, true>(in, lb, nl, cut, ga, gb, A, H);
+        else fwd_rows<C, false>(in, lb, nl, cut, ga, gb, A, H);
         F2 PA[NP], PH[NP];
         warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, !plain);
         if (q.seg == C::SEGS - 1) {
@@ -603,6 +663,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
             put_s(&aggH[p][q.w][q.ch], TH);
         }
         const bool cuts_here = sync_cuts(docs, cut);
+        if constexpr (C::X::WIDE) {   // everyone has left the step before: its stage takes the step STAGES later
+            if (threadIdx.x == 0 && it > 0) copy(it - 1 + C::STAGES);
+        }
         // the state before this block's rows
         F2 h[NP];
         if constexpr (CL) {
@@ -616,7 +679,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
                     push_pairs(&ex.H[p][q.rank][q.ch], H, &ex.bar[p], k);
                 }
             }
-            ok = ok && wait_peers(&ex.bar[p], (it >> 1) & 1);
+            ok = ok && wait_phase(&ex.bar[p], (it >> 1) & 1);
 #pragma unroll
             for (int j = 0; j < NP; ++j) h[j] = carry[j];
             fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, h, docs);
@@ -640,8 +703,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
             if (q.w == WARPS - 1 && q.seg == C::SEGS - 1) put_s(&carry_s[p][q.ch], h);
         }
         const int nr = q.on ? min(a.T - row0, RPT) : 0;   // rows to write
-        if (plain) fwd_store<C, true>(rr, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
-        else fwd_store<C, false>(rr, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
+        if (plain) fwd_store<C, true>(in, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
+        else fwd_store<C, false>(in, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
     }
     if constexpr (CL) {
         if (!ok) cluster_leave();
@@ -661,10 +724,18 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
     constexpr int GROUP = kSaveRows / C::WROWS;   // warps from one saved state to the next
     static_assert(ROWS % kSaveRows == 0 && kSaveRows % C::WROWS == 0, "steps start from saved states");
     const ScanArgs& a = g.s;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ uint64_t full[C::STAGES];
     __shared__ alignas(16) float aggA[2][WARPS][C::CH], aggH[2][WARPS][C::CH], aggG[2][WARPS][C::CH];
     __shared__ alignas(16) float carry_s[2][C::CH];
     __shared__ typename std::conditional<CL, Exchange<C>, int>::type ex;
     const Place<C> q(a);
+    if constexpr (C::X::WIDE) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < C::STAGES; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
+            ptx::fence_mbar_init();
+        }
+    }
     if constexpr (CL) open_exchange(ex);
     ptx::pdl_trigger();
     ptx::pdl_wait();
@@ -676,6 +747,23 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
     const char *fp = q.at(a.f), *vp = q.at(a.v), *rp = q.at(a.r), *yp = q.at(a.y);
     char *dfp = q.at(g.df), *dvp = q.at(g.dv), *drp = q.at(g.dr);
 
+    using In = Inputs<C, 4>;
+    const uint32_t ring = (ptx::smem_u32(smem) + 127u) & ~127u;
+    [[maybe_unused]] const char* lane_at = smem + (ring - ptx::smem_u32(smem)) + (q.w * C::WROWS + q.seg * RPT) * In::ROW_BYTES + q.c * 8;
+    auto step_of = [&](int it) { return static_cast<int64_t>(steps - 1) - (static_cast<int64_t>(it) * a.S + q.rank); };
+    auto has_rows = [&](int it) { return it < iters && step_of(it) >= 0 && step_of(it) * ROWS < len; };
+    // the first step with live rows: the stages' phases count from there
+    [[maybe_unused]] const int it0 = (max(steps - 1 - q.rank - max(len - 1, 0) / ROWS, 0) + a.S - 1) / a.S;
+    auto copy = [&](int it) {
+        if (has_rows(it))
+            copy_step<C, 4>(a.maps, ring + it % C::STAGES * (4 * In::TILE_BYTES), ptx::smem_u32(&full[it % C::STAGES]),
+                            q.d0 - q.ch, step_of(it), static_cast<int>(q.b));
+    };
+    if constexpr (C::X::WIDE) {
+        if (threadIdx.x == 0)
+            for (int i = 0; i < C::STAGES; ++i) copy(i);
+        __syncthreads();   // the barriers are set up before anyone waits
+    }
     [[maybe_unused]] bool ok = true;
     F2 lb[NP], carry[NP], dbias[NP];
     load_f32(a.f_bias == nullptr ? nullptr : a.f_bias + q.d, q.nch, lb, 0.0f);
@@ -684,28 +772,32 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
     for (int j = 0; j < NP; ++j) lb[j] = mul2(lb[j], both(-kLog2e)), dbias[j] = both(0.0f);
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
-        const int step = steps - 1 - (it * a.S + q.rank);   // below 0: nothing left for this block
-        const int64_t first = static_cast<int64_t>(step) * ROWS + q.w * C::WROWS + q.seg * RPT;
+        const int64_t step = step_of(it);   // below 0: nothing left for this block
+        const int64_t first = step * ROWS + q.w * C::WROWS + q.seg * RPT;
         const int row0 = step >= 0 && first < a.T ? static_cast<int>(first) : a.T;
         const int nl = min(max(len - row0, 0), RPT);
         if constexpr (CL) {
             if (threadIdx.x == 0)
                 ptx::mbar_arrive_expect_tx(ptx::smem_u32(&ex.bar[p]), static_cast<uint32_t>(a.S * C::CH * 2 * sizeof(float)));
         }
-        const bool full = __all_sync(0xffffffffu, nl == RPT);
-        typename X::Raw rf[RPT], rv[RPT], rr[RPT], rd[RPT];
-        load_rows<C>(rf, fp + row0 * a.f.st, a.f.st, nl, q.nch, full);
-        load_rows<C>(rv, vp + row0 * a.v.st, a.v.st, nl, q.nch, full);
-        load_rows<C>(rr, rp + row0 * a.r.st, a.r.st, nl, q.nch, full);
-        load_rows<C>(rd, yp + row0 * a.y.st, a.y.st, nl, q.nch, full);
+        const bool all_live = __all_sync(0xffffffffu, nl == RPT);
+        In in;
+        if constexpr (C::X::WIDE) in.at = lane_at + it % C::STAGES * (4 * In::TILE_BYTES);
+        in.load(0, fp + row0 * a.f.st, a.f.st, nl, q.nch, all_live);
+        in.load(1, vp + row0 * a.v.st, a.v.st, nl, q.nch, all_live);
+        in.load(2, rp + row0 * a.r.st, a.r.st, nl, q.nch, all_live);
+        in.load(3, yp + row0 * a.y.st, a.y.st, nl, q.nch, all_live);
         const uint32_t cut = start_bits<C>(a, q.b, step >= 0 ? static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))) : a.T,
                                            len, q.seg, q.lane);
-        const bool plain = full && (!docs || __all_sync(0xffffffffu, cut == 0));
+        const bool plain = all_live && (!docs || __all_sync(0xffffffffu, cut == 0));
         F2 h[NP];
         load_f32(row0 < a.T ? a.saved + (q.b * nsaved + row0 / kSaveRows) * a.D + q.d : nullptr, q.nch, h, 0.0f);
+        if constexpr (C::X::WIDE) {
+            if (has_rows(it)) ok = ok && wait_phase(&full[it % C::STAGES], ((it - it0) / C::STAGES) & 1);
+        }
         F2 s[RPT][NP], n[RPT][NP], o[RPT][NP], x[RPT][NP], A[NP], H[NP], G[NP];
-        if (plain) bwd_rows<C, true>(rf, rv, rr, rd, lb, nl, cut, s, n, o, x, A, H, G);
-        else bwd_rows<C, false>(rf, rv, rr, rd, lb, nl, cut, s, n, o, x, A, H, G);
+        if (plain) bwd_rows<C, true>(in, lb, nl, cut, s, n, o, x, A, H, G);
+        else bwd_rows<C, false>(in, lb, nl, cut, s, n, o, x, A, H, G);
         F2 PA[NP], PH[NP], QA[NP], QG[NP];
         warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, !plain);
         warp_prefix<C, true>(A, G, QA, QG, q.seg, q.c, !plain);
@@ -726,6 +818,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
             put_s(&aggG[p][q.w][q.ch], TG);
         }
         const bool cuts_here = sync_cuts(docs, cut);
+        if constexpr (C::X::WIDE) {   // everyone has left the step before: its stage takes the step STAGES later
+            if (threadIdx.x == 0 && it > 0) copy(it - 1 + C::STAGES);
+        }
         F2 e[NP];   // e after this segment's rows
         if constexpr (CL) {
             if (it == 0) cluster_wait();   // every peer has set up its barriers
@@ -738,7 +833,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
                     push_pairs(&ex.H[p][q.rank][q.ch], G, &ex.bar[p], k);
                 }
             }
-            ok = ok && wait_peers(&ex.bar[p], (it >> 1) & 1);
+            ok = ok && wait_phase(&ex.bar[p], (it >> 1) & 1);
 #pragma unroll
             for (int j = 0; j < NP; ++j) e[j] = carry[j];
             fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, e, docs);
@@ -759,8 +854,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
         }
         const int nr = q.on ? min(a.T - row0, RPT) : 0;   // rows to write
         char *dfr = dfp + row0 * g.df.st, *dvr = dvp + row0 * g.dv.st, *drr = drp + row0 * g.dr.st;
-        if (plain) bwd_store<C, true>(rv, s, n, o, x, nl, cut, nr, q.nch, h, e, dbias, dfr, g.df.st, dvr, g.dv.st, drr, g.dr.st);
-        else bwd_store<C, false>(rv, s, n, o, x, nl, cut, nr, q.nch, h, e, dbias, dfr, g.df.st, dvr, g.dv.st, drr, g.dr.st);
+        if (plain) bwd_store<C, true>(in, s, n, o, x, nl, cut, nr, q.nch, h, e, dbias, dfr, g.df.st, dvr, g.dv.st, drr, g.dr.st);
+        else bwd_store<C, false>(in, s, n, o, x, nl, cut, nr, q.nch, h, e, dbias, dfr, g.df.st, dvr, g.dv.st, drr, g.dr.st);
         if constexpr (!CL) {
             if (q.w == 0 && q.seg == 0) put_s(&carry_s[p][q.ch], e);
         }
@@ -866,13 +961,14 @@ namespace {
 size_t elem(int dtype) { return dtype == TERN_F32 ? 4 : 2; }
 
 // TERN_OK when x can be read or written as rows of elements, else the error; `wide` is cleared
-// when its address or strides keep it from 8-byte accesses.
-int check_act(const tern_act& x, int dtype, bool& wide) {
-    const int64_t es = static_cast<int64_t>(elem(dtype));
+// when its address or strides keep it from TMA copies.
+int check_act(const tern_act& x, const tern_scan* s, bool& wide) {
+    const int64_t es = static_cast<int64_t>(elem(s->dtype));
     if (x.p == nullptr || x.stride_b < 0 || x.stride_t < 0) return TERN_ERR_ARG;
     if (x.stride_b > INT64_MAX / 4 / es || x.stride_t > INT64_MAX / 4 / es) return TERN_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(x.p) % es != 0) return TERN_ERR_ALIGN;
-    if (reinterpret_cast<uintptr_t>(x.p) % 8 != 0 || x.stride_b * es % 8 != 0 || x.stride_t * es % 8 != 0) wide = false;
+    if (reinterpret_cast<uintptr_t>(x.p) % 16 != 0 || x.stride_b * es % 16 != 0 || x.stride_t * es % 16 != 0) wide = false;
+    if ((s->T > 1 && x.stride_t < s->D) || (s->B > 1 && x.stride_b == 0)) wide = false;   // overlapping rows
     return TERN_OK;
 }
 Strided strided(const tern_act& x, int dtype) {
@@ -884,11 +980,11 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 int check_scan(const tern_scan* s, bool& wide) {
     if (s == nullptr || (s->dtype != TERN_BF16 && s->dtype != TERN_F32)) return TERN_ERR_ARG;
     if (s->B < 0 || s->T < 0 || s->D < 0 || s->T > INT32_MAX - 256 || s->D > INT32_MAX - 256 || s->B > INT32_MAX - 256) return TERN_ERR_ARG;
-    wide = s->D * static_cast<int64_t>(elem(s->dtype)) % 8 == 0;
+    wide = s->D * static_cast<int64_t>(elem(s->dtype)) % 16 == 0;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (s->T > 0) {
         for (const tern_act* x : {&s->f, &s->v, &s->r})
-            if (int st = check_act(*x, s->dtype, wide)) return st;
+            if (int st = check_act(*x, s, wide)) return st;
     }
     if (!aligned4(s->f_bias) || !aligned4(s->lengths)) return TERN_ERR_ALIGN;
     return TERN_OK;
@@ -896,42 +992,87 @@ int check_scan(const tern_scan* s, bool& wide) {
 
 // Blocks per cluster: the largest power of two, at most kMaxCluster and less than twice the steps,
 // with which the blocks are all resident at once.
-int cluster_size(int64_t blocks, int64_t steps, int64_t slots) {
+template <class C>
+int cluster_size(int64_t blocks, int64_t steps, int num_sms) {
     int S = 1;
-    while (S < kMaxCluster && S < steps && 2 * S * blocks <= slots) S *= 2;
+    while (S < kMaxCluster && S < steps && 2 * S * blocks <= static_cast<int64_t>(C::MINB) * num_sms) S *= 2;
     return S;
 }
 
 int64_t steps_of(int64_t T, int64_t rows) { return (T + rows - 1) / rows; }
 
+// The tensor map of an input: [B][T][D] in boxes of ROWS rows by CH channels.
 template <class C>
+int input_map(CUtensorMap* m, const Strided& x, int64_t B, int64_t T, int64_t D) {
+    const CUtensorMapDataType type = sizeof(typename C::T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    // a stride that no second row or sequence uses may be anything that the encoding takes
+    const int64_t least = D * static_cast<int64_t>(sizeof(typename C::T));
+    return tensor_map_3d(m, x.p, type, D, T, B, T > 1 ? x.st : least, B > 1 ? x.sb : least, C::CH, C::ROWS);
+}
+
+template <class C, bool CL>
 int launch_fwd(const ScanArgs& a0, int64_t B, int num_sms, cudaStream_t s) {
     ScanArgs a = a0;
     a.tiles = (a.D + C::CH - 1) / C::CH;
     const int64_t blocks = B * a.tiles;
-    a.S = cluster_size(blocks, steps_of(a.T, C::ROWS), static_cast<int64_t>(C::MINB) * num_sms);
+    a.S = CL ? cluster_size<C>(blocks, steps_of(a.T, C::ROWS), num_sms) : 1;
     if (blocks * a.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * a.S);
-    if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, 0, a.S, s, a);
-    return launch_cluster(tern_scan_fwd_kernel<C, false>, grid, C::WARPS * 32, 0, 1, s, a);
+    if (C::X::WIDE && a.T > 0) {
+        const Strided* in[3] = {&a.f, &a.v, &a.r};
+        for (int i = 0; i < 3; ++i)
+            if (int st = input_map<C>(&a.maps[i], *in[i], B, a.T, a.D)) return st;
+    }
+    constexpr size_t smem = Inputs<C, 3>::SMEM;
+    if constexpr (CL) {
+        if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, smem, a.S, s, a);
+    }
+    return launch_cluster(tern_scan_fwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, s, a);
 }
 
-template <class C>
+template <class C, bool CL>
 int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStream_t s) {
     GradArgs g = g0;
     g.s.tiles = (g.s.D + C::CH - 1) / C::CH;
     const int64_t blocks = B * g.s.tiles;
-    g.s.S = cluster_size(blocks, steps_of(g.s.T, C::ROWS), static_cast<int64_t>(C::MINB) * num_sms);
+    g.s.S = CL ? cluster_size<C>(blocks, steps_of(g.s.T, C::ROWS), num_sms) : 1;
     if (blocks * g.s.S > INT32_MAX) return TERN_ERR_ARG;
     const unsigned grid = static_cast<unsigned>(blocks * g.s.S);
-    if (g.s.S > 1) {
-        if (int st = launch_cluster(tern_scan_bwd_kernel<C, true>, grid, C::WARPS * 32, 0, g.s.S, s, g)) return st;
-    } else if (int st = launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, 0, 1, s, g)) {
-        return st;
+    if (C::X::WIDE && g.s.T > 0) {
+        const Strided* in[4] = {&g.s.f, &g.s.v, &g.s.r, &g.s.y};
+        for (int i = 0; i < 4; ++i)
+            if (int st = input_map<C>(&g.s.maps[i], *in[i], B, g.s.T, g.s.D)) return st;
     }
+    constexpr size_t smem = Inputs<C, 4>::SMEM;
+    int st = TERN_OK;
+    if constexpr (CL) {
+        st = g.s.S > 1 ? launch_cluster(tern_scan_bwd_kernel<C, true>, grid, C::WARPS * 32, smem, g.s.S, s, g)
+                       : launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, s, g);
+    } else {
+        st = launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, s, g);
+    }
+    if (st != TERN_OK) return st;
     if (dbias == nullptr) return TERN_OK;
     return launch_pdl(tern_scan_dbias_kernel, dim3(static_cast<unsigned>((g.s.D + 31) / 32)), dim3(256), 0, s,
                       static_cast<const float*>(g.partial), B * g.s.S, g.s.D, dbias);
+}
+
+// The shape of the blocks, by how many there are of 64 bytes of channels by a whole sequence: enough
+// for more than two of four warps on each SM; else blocks of eight warps, in clusters where even
+// those leave SMs free; and tiles of half the channels where clusters of 16 still fill less than
+// half the GPU.  (Forward and gradient of 16 x 512 x 512: 13.6 + 22.8 us as clusters of four-warp
+// blocks, 12.2 + 19.8 us as eight-warp blocks; of 8 x 2048 x 2048: 59 + 125 us with four warps,
+// 67 + 134 us with eight; forward of 1 x 65536 x 512: 88 us in the narrow tiles, 122 us in wide ones.)
+template <class T, bool WIDE, int RPT, class F>
+int with_shape(int64_t B, int64_t D, int64_t T_, int num_sms, F run) {
+    using Four = Shape<T, WIDE, 8, RPT, 4, 4, 2>;
+    using Eight = Shape<T, WIDE, 8, RPT, 8, 2, 2>;
+    using Narrow = Shape<T, WIDE, 4, RPT, 4, 4, 2>;
+    const int64_t blocks = B * ((D + Four::CH - 1) / Four::CH);
+    if (blocks > 2 * num_sms) return run(Four{}, std::false_type{});
+    const int S = cluster_size<Eight>(blocks, steps_of(T_, Eight::ROWS), num_sms);
+    if (S == kMaxCluster && blocks * S * 2 <= 4 * num_sms) return run(Narrow{}, std::true_type{});
+    return run(Eight{}, std::true_type{});
 }
 
 ScanArgs scan_args(const tern_scan* s) {
@@ -968,7 +1109,7 @@ extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (s->T > 0) {
         if (y == nullptr) return TERN_ERR_ARG;
-        if (int st = check_act(*y, s->dtype, wide)) return st;
+        if (int st = check_act(*y, s, wide)) return st;
     }
     if (!aligned4(h0) || !aligned4(hT) || !aligned4(saved)) return TERN_ERR_ALIGN;
     if (saved != nullptr && saved_bytes < tern_scan_saved(s->B, s->T, s->D)) return TERN_ERR_WORKSPACE;
@@ -978,11 +1119,11 @@ extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act
     if (s->T > 0) a.y = strided(*y, s->dtype);
     a.saved = saved, a.h_in = h0, a.h_out = hT;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    auto run = [&](auto shape, auto cl) { return launch_fwd<decltype(shape), decltype(cl)::value>(a, s->B, num_sms, cs); };
     if (s->dtype == TERN_BF16)
-        return wide ? launch_fwd<Shape<__nv_bfloat16, true, 8, 8, 4, 4>>(a, s->B, num_sms, cs)
-                    : launch_fwd<Shape<__nv_bfloat16, false, 8, 8, 4, 4>>(a, s->B, num_sms, cs);
-    return wide ? launch_fwd<Shape<float, true, 8, 8, 4, 4>>(a, s->B, num_sms, cs)
-                : launch_fwd<Shape<float, false, 8, 8, 4, 4>>(a, s->B, num_sms, cs);
+        return wide ? with_shape<__nv_bfloat16, true, 8>(s->B, s->D, s->T, num_sms, run)
+                    : with_shape<__nv_bfloat16, false, 8>(s->B, s->D, s->T, num_sms, run);
+    return wide ? with_shape<float, true, 8>(s->B, s->D, s->T, num_sms, run) : with_shape<float, false, 8>(s->B, s->D, s->T, num_sms, run);
 }
 
 extern "C" size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D) {
@@ -1000,7 +1141,7 @@ extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_
         if (saved == nullptr) return TERN_ERR_ARG;
         for (const tern_act* x : {dy, df, dv, dr}) {
             if (x == nullptr) return TERN_ERR_ARG;
-            if (int st = check_act(*x, s->dtype, wide)) return st;
+            if (int st = check_act(*x, s, wide)) return st;
         }
     }
     if (!aligned4(saved) || !aligned4(dhT) || !aligned4(dbias) || !aligned4(dh0) || !aligned4(workspace)) return TERN_ERR_ALIGN;
@@ -1017,11 +1158,11 @@ extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_
     }
     g.partial = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    auto run = [&](auto shape, auto cl) { return launch_bwd<decltype(shape), decltype(cl)::value>(g, s->B, num_sms, dbias, cs); };
     if (s->dtype == TERN_BF16)
-        return wide ? launch_bwd<Shape<__nv_bfloat16, true, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs)
-                    : launch_bwd<Shape<__nv_bfloat16, false, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs);
-    return wide ? launch_bwd<Shape<float, true, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs)
-                : launch_bwd<Shape<float, false, 8, 4, 4, 4>>(g, s->B, num_sms, dbias, cs);
+        return wide ? with_shape<__nv_bfloat16, true, 4>(s->B, s->D, s->T, num_sms, run)
+                    : with_shape<__nv_bfloat16, false, 4>(s->B, s->D, s->T, num_sms, run);
+    return wide ? with_shape<float, true, 4>(s->B, s->D, s->T, num_sms, run) : with_shape<float, false, 4>(s->B, s->D, s->T, num_sms, run);
 }
 
 namespace {
@@ -1040,7 +1181,7 @@ extern "C" int tern_scan_step(const tern_scan* s, const float* h_in, float* h_ou
     if (s->T != 1 || s->lengths != nullptr || s->starts != nullptr) return TERN_ERR_ARG;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (h_in == nullptr || h_out == nullptr || y == nullptr) return TERN_ERR_ARG;
-    if (int st = check_act(*y, s->dtype, wide)) return st;
+    if (int st = check_act(*y, s, wide)) return st;
     if (!aligned4(h_in) || !aligned4(h_out)) return TERN_ERR_ALIGN;
     if (int st = check_device(nullptr)) return st;
     StepArgs a{};
