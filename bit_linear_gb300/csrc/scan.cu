@@ -595,7 +595,6 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
         }
     }
     if constexpr (CL) open_exchange(ex);
-    ptx::pdl_trigger();
     ptx::pdl_wait();
     const bool docs = a.starts != nullptr;
     const int len = rows_live(a, static_cast<int>(q.b));
@@ -628,6 +627,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
     [[maybe_unused]] bool ok = true;
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
+        // not at entry: blocks of the next kernel that wait in the free slots meanwhile would be its
+        // share of some SMs and not of others (a long document: 119 us back to back, 96 us alone)
+        if (it + 1 == iters) ptx::pdl_trigger();
         const int64_t first = step_of(it) * ROWS + q.w * C::WROWS + q.seg * RPT;
         const int row0 = first < a.T ? static_cast<int>(first) : a.T;
         const int nl = min(max(len - row0, 0), RPT);   // live rows of this segment
@@ -737,7 +739,6 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
         }
     }
     if constexpr (CL) open_exchange(ex);
-    ptx::pdl_trigger();
     ptx::pdl_wait();
     const bool docs = a.starts != nullptr;
     const int len = rows_live(a, static_cast<int>(q.b));
@@ -772,6 +773,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
     for (int j = 0; j < NP; ++j) lb[j] = mul2(lb[j], both(-kLog2e)), dbias[j] = both(0.0f);
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
+        if (it + 1 == iters) ptx::pdl_trigger();
         const int64_t step = step_of(it);   // below 0: nothing left for this block
         const int64_t first = step * ROWS + q.w * C::WROWS + q.seg * RPT;
         const int row0 = step >= 0 && first < a.T ? static_cast<int>(first) : a.T;
