@@ -31,7 +31,16 @@
 // the next one's main loop.  warp 0 copies, warp 1 issues the MMAs, warps 2-9 drain (two per TMEM
 // lane quarter).  The four operand tiles of a 64-deep k-block feed twelve MMAs: one and a half
 // times the work per byte of shared memory of a plain product.  256 x 256 tiles by CTA pairs where
-// they fill the GPU, else 128 x 128 or 128 x 64 by single CTAs.
+// they fill the GPU, else 128 x 128 or 128 x 64 by single CTAs, and clusters that share the
+// contraction of a few tiles.
+//
+// 4096 x 12288: 5.2 ms; a product of X runs at 1.82 PFLOP/s of executed passes (0.95 of the measured
+// cuBLAS burst rate, tensor pipe busy 0.85), the symmetric ones at 0.77 of that: 136 tiles on 76
+// pairs are two rounds, the second one of 60.  512 x 2048: 174 us, 10 us a product of which 5.6 are
+// a launch in the chain and most of the rest the copies of its operands (87 B/ns into an SM).  All
+// of it in one cooperative launch with barriers of the grid between the products was no faster
+// (176 us; 136 against 97 us at 32 x 64): the drain of the stores, the fences and the first copies
+// after a barrier take as long as a launch.
 #include <algorithm>
 #include <mutex>
 
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
 // Sum of squares of G, a partial sum per block in fp64 (fixed chunks and order).  Sixteen squares
 // at a time are added in fp32, whose rounding is then that of sixteen terms, unless their range
 // does not allow it: fp64 throughout would take as long as the arithmetic, not the reads
-// (227 us against 40 us for the 4096 x 12288 gradient).
+// (227 us against 44 us for the 4096 x 12288 gradient).
 constexpr int kSumBlocks = 304;
 __global__ void __launch_bounds__(256) tern_ortho_sumsq_kernel(const float* __restrict__ G, int64_t n, double* __restrict__ partial) {
     __shared__ double red[256];

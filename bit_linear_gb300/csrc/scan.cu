@@ -6,27 +6,32 @@
 // lengths[b] are padding (never read: a = 1, no input, y = 0, gradients 0).
 //
 // The map of one row, h -> a h + b, composes: rows i..j act as h -> A h + H with A = prod a and
-// H the state reached from 0.  A block takes a tile of channels and ROWS consecutive rows, all
-// held in registers: a lane has VEC neighbouring channels of RPT rows (a segment), LPR lanes side
-// by side make a row's whole 128-byte line, and a warp holds 32/LPR segments.
+// H the state reached from 0.  A block takes a tile of channels and ROWS consecutive rows: a lane
+// has four neighbouring channels (two in fp32) of RPT rows, a segment; LPR lanes side by side make
+// a row's 64 bytes (32 in narrow tiles), and a warp holds 32/LPR segments.
 //   1. each lane folds its RPT rows into (A, H); a warp's segments are joined by shuffles and
 //      its pair left in shared memory;
 //   2. after a barrier each lane folds what lies before it onto the block's incoming state;
-//   3. it runs its rows again from that state and writes y.
-// A block walks T in steps of ROWS.  Where sequences times channel tiles are too few blocks to
-// fill the GPU, a cluster of S blocks takes S consecutive steps at a time and exchanges the
-// blocks' totals through distributed shared memory, one cluster barrier per S steps.  Every
-// fold has a fixed order, so results do not depend on the schedule; nothing polls memory.
+//   3. it runs its rows again from that state, whose gates it kept in registers, and writes y.
+// A block walks T in steps of ROWS, its inputs copied one step ahead by TMA.  Where sequences times
+// channel tiles are too few blocks to fill the GPU, a cluster of S blocks takes S consecutive steps
+// at a time, and each block pushes its total into the others' shared memory (a cluster barrier
+// would wait for the block's stores each step: 414 against 165 us for a document of 65536).  Every
+// fold has a fixed order, so results do not depend on the schedule.
 //
 // The gradient runs the same way from the end of the sequence, with e_t = a_t dh_t as its state:
 //   dh_t = g_t + e_{t+1}, e_t = a_t dh_t, g_t = sigmoid(r_t) dy_t, e_T = dhT
 //   dv = (1 - a) dh, df = dh (h_{t-1} - v) a (1 - a), dr = dy h s (1 - s), dh0 = e_0
-// and recomputes h inside its 64 rows from the states the forward saved every 64 rows (1/8 B
-// per element beside the 22 B of a forward and a backward in bf16).
+// and recomputes h from the states the forward saved every 64 rows (1/8 B per element beside the
+// 22 B of a forward and a gradient in bf16).
 //
-// Bounded by HBM (each input read once, each output written once), with the instruction rate
-// close behind: 8 B per element at 45 B/ns per SM leave about 40 instructions per element.
-// Gates and states are fp32; outputs are rounded once.
+// HBM would allow 8 B per element in the forward and 14 B in the gradient (each input read once,
+// each output written once).  8 x 2048 x 2048 in bf16 with packed documents: forward 59 us, 0.67 of
+// the measured copy rate, gradient 125 us, 0.55.  What binds is the issue of instructions: 31 and 71
+// per element and lane, of which 17 and 32 are the arithmetic, at half of the issue slots (four
+// warps on a scheduler, each waiting on its own chain of exponential, reciprocal and fold).  More
+// warps with fewer rows each lost more to the folds than they hid (RPT 4: 77 us), fewer with more
+// rows hid less.  Gates and states are fp32; outputs are rounded once.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -37,7 +42,7 @@ namespace tern {
 namespace {
 
 constexpr int kSaveRows = 64;     // rows between saved states
-constexpr int kMaxCluster = 16;   // blocks of a cluster (8 portable, 16 by a function attribute)
+constexpr int kMaxCluster = 16;   // blocks of a cluster
 
 __device__ int g_scan_status;     // 1 once a wait for a peer's totals gave up
 
@@ -72,8 +77,8 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 __device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xffffffffu, a.v, from)}; }
 
 // --------------------------------------------------------------- element access
-// NP pairs of neighbouring elements of a row, eight bytes.  WIDE: inputs come by TMA and outputs are
-// stored eight bytes at a time; otherwise element by element (odd widths, strides or addresses),
+// NP pairs of neighbouring elements of a row, eight bytes.  WIDE: one access (and the sequences'
+// inputs come by TMA); otherwise element by element (odd widths, strides or addresses),
 // where a row's last lane may hold fewer: nch elements are there, loads repeat the last and stores
 // leave the others out.
 template <class T, bool WIDE_>
@@ -84,6 +89,7 @@ struct Io<__nv_bfloat16, WIDE_> {
     static constexpr int NP = 2;
     using Raw = uint2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
+        if constexpr (WIDE) return __ldg(reinterpret_cast<const uint2*>(p));
         const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
         const uint32_t x0 = __ldg(q), x1 = __ldg(q + min(1, nch - 1)), x2 = __ldg(q + min(2, nch - 1)), x3 = __ldg(q + min(3, nch - 1));
         return make_uint2(x0 | x1 << 16, x2 | x3 << 16);
@@ -117,6 +123,7 @@ struct Io<float, WIDE_> {
     static constexpr int NP = 1;
     using Raw = float2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
+        if constexpr (WIDE) return __ldg(reinterpret_cast<const float2*>(p));
         const float* q = reinterpret_cast<const float*>(p);
         return make_float2(__ldg(q), __ldg(q + min(1, nch - 1)));
     }
@@ -284,8 +291,9 @@ __device__ __forceinline__ void push_pairs(const float* mine, const F2 (&x)[NP],
     }
 }
 // Waits for a phase of the exchange or of a copy, at most about two seconds: a peer block is
-// resident, a copy on its way, and a healthy wait takes microseconds.  On expiry the status word is set; the thread waits no more
-// and runs its steps to the end, so that the block's barriers still match (its results are void).
+// resident, a copy on its way, and a healthy wait takes microseconds.  On expiry the status word is
+// set; the thread waits no more and runs its steps to the end, so that the block's barriers still
+// match (its results are void).
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
     const uint32_t b = ptx::smem_u32(bar);
     uint64_t last = 0, waited = 0;
