@@ -117,11 +117,31 @@ __device__ __forceinline__ void split16(float v, __half& hi, __half& lo) {
     lo = __float2half_rn(v - __half2float(hi));
 }
 
-// Eight columns c..c+7 (c % 8 == 0) of row `row`, from the accumulator's values.
-__device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&acc)[8], int row, int c) {
+// Lane i of each eight holds row i of an 8 x 8 block, x its columns; afterwards column i, x its rows.
+__device__ __forceinline__ void transpose8(uint32_t (&x)[8], int lane) {
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) {
+        const bool upper = (lane & d) != 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i & d) continue;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i | d], d);
+            if (upper) x[i] = other;
+            else x[i | d] = other;
+        }
+    }
+}
+
+// Eight columns c..c+7 (c % 8 == 0) of row `row`, from the accumulator's values; called by whole
+// warps, whose lanes hold 32 consecutive rows.  Of a symmetric product, the 8 x 8 blocks above the
+// diagonal are stored twice, as they are and transposed (in registers: stores of single elements
+// took 3.5 us to drain, most of a small product's time), those on it once.
+__device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&acc)[8], int row, int c, int lane) {
     const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
-    if (row >= a.rows || c >= a.ld || (sym && c + 7 < row)) return;
+    const int row8 = row & ~7;
+    const bool here = row < a.rows && c < a.ld && (!sym || c >= row8);
     if (a.kind == OUT_FINAL) {
+        if (!here) return;
         __nv_bfloat16* o = a.out + static_cast<int64_t>(row) * a.cols + c;
         if (a.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
             uint32_t u[4];
@@ -141,9 +161,11 @@ __device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&ac
     const int64_t base = static_cast<int64_t>(row) * a.ld + c;
     __align__(16) __half hi[8], lo[8];
     if (a.kind == OUT_POLY) {
-        __align__(16) __half ah[8], al[8];
-        *reinterpret_cast<uint4*>(ah) = *reinterpret_cast<const uint4*>(a.ch + base);
-        *reinterpret_cast<uint4*>(al) = *reinterpret_cast<const uint4*>(a.cl + base);
+        __align__(16) __half ah[8] = {}, al[8] = {};
+        if (here) {
+            *reinterpret_cast<uint4*>(ah) = *reinterpret_cast<const uint4*>(a.ch + base);
+            *reinterpret_cast<uint4*>(al) = *reinterpret_cast<const uint4*>(a.cl + base);
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float x = __half2float(ah[k]) + __half2float(al[k]);
@@ -153,21 +175,27 @@ __device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&ac
 #pragma unroll
         for (int k = 0; k < 8; ++k) split16(a.alpha * acc[k], hi[k], lo[k]);
     }
-    if (!sym || c >= row) {
+    if (here) {
         *reinterpret_cast<uint4*>(a.oh + base) = *reinterpret_cast<const uint4*>(hi);
         *reinterpret_cast<uint4*>(a.ol + base) = *reinterpret_cast<const uint4*>(lo);
-    } else {   // the diagonal lies in the group: one writer per element
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (c + k >= row) a.oh[base + k] = hi[k], a.ol[base + k] = lo[k];
     }
-    if (sym) {   // mirrored: a warp's 32 rows are 64 neighbouring bytes
+    if (sym) {
+        uint32_t x[8], h[4], l[4];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (c + k > row && c + k < a.rows) {
-                const int64_t at = static_cast<int64_t>(c + k) * a.ld + row;
-                a.oh[at] = hi[k], a.ol[at] = lo[k];
-            }
+            x[k] = static_cast<uint32_t>(__half_as_ushort(hi[k])) | static_cast<uint32_t>(__half_as_ushort(lo[k])) << 16;
+        transpose8(x, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = __byte_perm(x[2 * k], x[2 * k + 1], 0x5410);
+            l[k] = __byte_perm(x[2 * k], x[2 * k + 1], 0x7632);
+        }
+        const int mrow = c + (lane & 7);   // rows past the last are zeros, which the columns past it want
+        if (c > row8 && row8 < a.rows && mrow < a.rows) {
+            const int64_t at = static_cast<int64_t>(mrow) * a.ld + row8;
+            *reinterpret_cast<uint4*>(a.oh + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(a.ol + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
     }
 }
 
@@ -366,7 +394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
                         float v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[8 * g + k]);
-                        ortho_group(a, v, row0 + quad * 32 + lane, c0 + 8 * g);
+                        ortho_group(a, v, row0 + quad * 32 + lane, c0 + 8 * g, lane);
                     }
                 }
             }
@@ -401,7 +429,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] += x[i];
                 }
-                ortho_group(a, v, mt * C::TILE_M + r, nt * C::BN + col);
+                ortho_group(a, v, mt * C::TILE_M + r, nt * C::BN + col, lane);
             }
         }
     }
