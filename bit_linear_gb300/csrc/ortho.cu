@@ -136,10 +136,22 @@ __device__ __forceinline__ void transpose8(uint32_t (&x)[8], int lane) {
 // warps, whose lanes hold 32 consecutive rows.  Of a symmetric product, the 8 x 8 blocks above the
 // diagonal are stored twice, as they are and transposed (in registers: stores of single elements
 // took 3.5 us to drain, most of a small product's time), those on it once.
-__device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&acc)[8], int row, int c, int lane) {
+__device__ __forceinline__ bool group_here(const OrthoArgs& a, int row, int c) {
+    return row < a.rows && c < a.ld && ((a.kind != OUT_SYM && a.kind != OUT_POLY) || c >= (row & ~7));
+}
+// OUT_POLY: A's planes there.
+__device__ __forceinline__ void group_load(const OrthoArgs& a, int row, int c, uint4& h, uint4& l) {
+    h = l = make_uint4(0u, 0u, 0u, 0u);
+    if (a.kind == OUT_POLY && group_here(a, row, c)) {
+        h = *reinterpret_cast<const uint4*>(a.ch + static_cast<int64_t>(row) * a.ld + c);
+        l = *reinterpret_cast<const uint4*>(a.cl + static_cast<int64_t>(row) * a.ld + c);
+    }
+}
+__device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&acc)[8], const uint4& h0, const uint4& l0, int row, int c,
+                                            int lane) {
     const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
     const int row8 = row & ~7;
-    const bool here = row < a.rows && c < a.ld && (!sym || c >= row8);
+    const bool here = group_here(a, row, c);
     if (a.kind == OUT_FINAL) {
         if (!here) return;
         __nv_bfloat16* o = a.out + static_cast<int64_t>(row) * a.cols + c;
@@ -161,11 +173,9 @@ __device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&ac
     const int64_t base = static_cast<int64_t>(row) * a.ld + c;
     __align__(16) __half hi[8], lo[8];
     if (a.kind == OUT_POLY) {
-        __align__(16) __half ah[8] = {}, al[8] = {};
-        if (here) {
-            *reinterpret_cast<uint4*>(ah) = *reinterpret_cast<const uint4*>(a.ch + base);
-            *reinterpret_cast<uint4*>(al) = *reinterpret_cast<const uint4*>(a.cl + base);
-        }
+        __align__(16) __half ah[8], al[8];
+        *reinterpret_cast<uint4*>(ah) = h0;
+        *reinterpret_cast<uint4*>(al) = l0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float x = __half2float(ah[k]) + __half2float(al[k]);
@@ -202,7 +212,6 @@ __device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&ac
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_constant__ OrthoArgs a) {
     constexpr int CG = C::CG;
-    [[maybe_unused]] constexpr int PART_LD = C::BN + 4;   // SPLIT: floats between the rows of a partial tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -369,8 +378,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
             const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::BN;
             const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
             if constexpr (C::SPLIT) {
-                // the partial tile to shared memory, over the operand stages (all read by now)
-                float* p = reinterpret_cast<float*>(smem_raw + (base - raw)) + (quad * 32 + lane) * PART_LD;
+                // the partial tile to shared memory, over the operand stages (all read by now): four columns
+                // of all rows side by side, so that a warp's reads from a peer are of neighbouring bytes
+                // (of rows 272 bytes apart they took 3 us a tile)
+                uint4* p = reinterpret_cast<uint4*>(smem_raw + (base - raw)) + quad * 32 + lane;
 #pragma unroll 1
                 for (int j = j0; j < j0 + JPW; ++j) {
                     uint32_t r[32];
@@ -378,7 +389,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4*>(p + j * 32 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                        p[(j * 8 + k / 4) * kRows] = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
                 }
             } else if (row0 < a.rows) {
 #pragma unroll 1
@@ -394,7 +405,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
                         float v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[8 * g + k]);
-                        ortho_group(a, v, row0 + quad * 32 + lane, c0 + 8 * g, lane);
+                        uint4 ph, pl;
+                        group_load(a, row0 + quad * 32 + lane, c0 + 8 * g, ph, pl);
+                        ortho_group(a, v, ph, pl, row0 + quad * 32 + lane, c0 + 8 * g, lane);
                     }
                 }
             }
@@ -409,34 +422,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
 
     if constexpr (C::SPLIT) {
         // each CTA adds up its share of the tile's columns over the partial tiles, in order
+        const int share = C::BN / a.split, r = (warp & 3) * 32 + lane;
+        int mt = 0, nt = 0;
+        if (unit0 < a.units) unit_tile<C>(a, unit0, mt, nt);
+        const int row = mt * C::TILE_M + r;
+        const int g0 = (warp - 2) / 4;      // the first of this warp's groups of eight columns
+        uint4 ph, pl;                       // its planes of A are on their way during the exchange
+        if (warp >= 2 && unit0 < a.units) group_load(a, row, nt * C::BN + part * share + 8 * g0, ph, pl);
         __syncwarp();
         ptx::cluster_sync();
         if (warp >= 2 && unit0 < a.units) {
-            int mt, nt;
-            unit_tile<C>(a, unit0, mt, nt);
-            const int r = (warp & 3) * 32 + lane, share = C::BN / a.split;
-            for (int g = (warp - 2) / 4; g < share / 8; g += 2) {
+            for (int g = g0; g < share / 8; g += 2) {
                 const int col = part * share + 8 * g;
-                const uint32_t at = base + static_cast<uint32_t>(r * PART_LD + col) * 4u;
-                float v[8] = {};
-                for (int k = 0; k < a.split; ++k) {
-                    const uint32_t peer = ptx::mapa_shared(at, k);
-                    float x[8];
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(peer) : "memory");
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]) : "r"(peer + 16u) : "memory");
+                const uint32_t at = base + static_cast<uint32_t>(col / 4 * kRows + r) * 16u;
+                if (g != g0) group_load(a, row, nt * C::BN + col, ph, pl);
+                float x[8][8], v[8] = {};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] += x[i];
+                for (int k = 0; k < 8; ++k) {   // all in flight together
+                    if (k >= a.split) break;
+                    const uint32_t peer = ptx::mapa_shared(at, k);
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x[k][0]), "=f"(x[k][1]), "=f"(x[k][2]), "=f"(x[k][3]) : "r"(peer) : "memory");
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x[k][4]), "=f"(x[k][5]), "=f"(x[k][6]), "=f"(x[k][7]) : "r"(peer + kRows * 16u) : "memory");
                 }
-                ortho_group(a, v, mt * C::TILE_M + r, nt * C::BN + col, lane);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= a.split) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += x[k][i];
+                }
+                ortho_group(a, v, ph, pl, row, nt * C::BN + col, lane);
             }
         }
     }
     ptx::tc_fence_before();
     if constexpr (C::SPLIT) {
+        // The peers have read this CTA's partial tile (and used what they read).  Nothing is published
+        // here, so the barrier need not wait for the stores.
         __syncwarp();
-        ptx::cluster_sync();   // the peers have read this CTA's partial tile
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     } else if constexpr (CG == 2) {
         ptx::cluster_sync();
     } else {
