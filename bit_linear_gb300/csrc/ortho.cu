@@ -36,11 +36,9 @@
 //
 // 4096 x 12288: 5.2 ms; a product of X runs at 1.82 PFLOP/s of executed passes (0.95 of the measured
 // cuBLAS burst rate, tensor pipe busy 0.85), the symmetric ones at 0.77 of that: 136 tiles on 76
-// pairs are two rounds, the second one of 60.  512 x 2048: 174 us, 10 us a product of which 5.6 are
-// a launch in the chain and most of the rest the copies of its operands (87 B/ns into an SM).  All
-// of it in one cooperative launch with barriers of the grid between the products was no faster
-// (176 us; 136 against 97 us at 32 x 64): the drain of the stores, the fences and the first copies
-// after a barrier take as long as a launch.
+// pairs are two rounds, the second one of 60.  512 x 2048: 142 us, eight a product: the end of the
+// launch before it 2, the first copies 1.3, the k-blocks 0.45 each (operands at 87 B/ns into an SM),
+// the exchange and the stores 3.
 #include <algorithm>
 #include <mutex>
 
@@ -686,10 +684,11 @@ int ortho_product(OrthoArgs& a, const Operand& A, const Operand& B, int64_t dept
     };
     if (tiles(256, 256) * 8 >= 3 * num_sms) return ortho_gemm<OCfg<2, 256, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
     if (tiles(128, 128) * 4 >= 3 * num_sms) return ortho_gemm<OCfg<1, 128, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
-    // Few tiles: clusters of S CTAs share each one's contraction, at least two k-blocks a CTA.  Clusters
-    // of 8, 4 and 2 CTAs of this size fit 16, 36 and 76 times.
+    // Few tiles: clusters of S CTAs share each one's contraction, at least a k-block a CTA.  Clusters of
+    // 8, 4 and 2 CTAs of this size fit 16, 36 and 76 times.  (512 x 2048: 174 us without, 142 us; 256 x
+    // 1024: 111 us with at least two k-blocks a CTA, 105 us.)
     const int64_t n = tiles(128, 64) + (sym ? (a.rows + 127) / 128 : 0), kb = (depth + kBK - 1) / kBK;
-    const int S = n <= 16 && kb >= 16 ? 8 : n <= 36 && kb >= 8 ? 4 : n <= 76 && kb >= 4 ? 2 : 1;
+    const int S = n <= 16 && kb >= 8 ? 8 : n <= 36 && kb >= 4 ? 4 : n <= 76 && kb >= 2 ? 2 : 1;
     if (S > 1) return ortho_gemm<OCfg<1, 64, A_MN, B_MN, true>>(a, A, B, depth, num_sms, s, S);
     return ortho_gemm<OCfg<1, 64, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
 }
