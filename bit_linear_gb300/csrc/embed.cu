@@ -334,23 +334,28 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
             hist[k] = run;
         }
         ptx::cluster_sync();
-        // of each digit: the counts of the tiles before this one, and of all; then a scan over the digits
-        const int per = (digits + THREADS - 1) / THREADS;
+        // of each digit: the counts of the tiles before this one, and of all; then a scan over the digits.
+        // Two neighbouring digits a read: the exchange is bound by the number of requests.
+        const int per = (digits + 2 * THREADS - 1) / (2 * THREADS) * 2;
         int own = 0;
-        for (int j = 0; j < per; ++j) {
+        for (int j = 0; j < per; j += 2) {
             const int k = threadIdx.x * per + j;
             if (k >= digits) break;
             const uint32_t here = ptx::smem_u32(hist + k);
-            int before = 0, all = 0;
+            int b0 = 0, b1 = 0, t0 = 0, t1 = 0;
             for (int q = 0; q < P; ++q) {
-                int x;
-                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(ptx::mapa_shared(here, q)) : "memory");
-                if (q < rank) before += x;
-                all += x;
+                int x, y;
+                asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(ptx::mapa_shared(here, q)) : "memory");
+                if (q < rank) b0 += x, b1 += y;
+                t0 += x, t1 += y;
             }
-            base[k] = own + before;      // without the digits of lower threads, added below
-            own += all;
+            base[k] = own + b0;          // without the digits of lower threads, added below
+            base[k + 1] = own + t0 + b1;
+            own += t0 + t1;
         }
+        // the last pass: after this the peers' counts are read no more
+        const bool last = pass + 1 == g.passes;
+        if (last) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
         int sum = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -373,9 +378,10 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
             const int to = base[dg] + mine[dg] + rk[r];
             g.keys[pass & 1][to] = key[r];
             g.pos[pass & 1][to] = at[r];
-            if (pass + 1 == g.passes && g.s.present != nullptr && key[r] < g.s.V) g.s.present[key[r]] = 1;
+            if (last && g.s.present != nullptr && key[r] < g.s.V) g.s.present[key[r]] = 1;
         }
-        ptx::cluster_sync();   // the placed keys are visible to the cluster, and the peers have read hist
+        if (last) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // the peers have read hist
+        else ptx::cluster_sync();                                              // and the placed keys are visible to them
     }
 }
 
