@@ -158,6 +158,27 @@ def test_embed_graph_and_stream(cuda_lib):
     assert torch.equal(out, o1) and torch.equal(g, g1)
 
 
+def test_embed_tables_and_rows_past_32_bits(cuda_lib):
+    """A table of more than 2^31 elements, and output rows that far apart."""
+    bl = cuda_lib
+    V, D = 70000, 32768
+    t = torch.tensor([V - 1, 3, V - 1, 0, V], device="cuda")
+    dout = torch.randint(-8, 9, (5, D), device="cuda").bfloat16()
+    g = torch.full((V, D), 7.0, device="cuda")
+    ws = torch.empty(bl.tern_embed_bwd_workspace(5, V, D), dtype=torch.uint8, device="cuda")
+    bl.tern_embed_bwd(t, dout, g, ws)
+    assert torch.equal(g[V - 1], dout[0].float() + dout[2].float())
+    assert torch.equal(g[3], dout[1].float()) and torch.equal(g[0], dout[3].float())
+    assert torch.count_nonzero(g) == sum(torch.count_nonzero(g[k]) for k in (0, 3, V - 1))
+    n, ld = 2200, 1 << 20
+    out = torch.zeros(n * ld, dtype=torch.bfloat16, device="cuda").as_strided((n, 8), (ld, 1))
+    w = g[:, :8].contiguous()
+    tok = torch.full((n,), 1, device="cuda")
+    tok[-1] = V - 1
+    bl.tern_embed_fwd(tok, w, out)
+    assert torch.equal(out[-1].float(), w[V - 1].bfloat16().float()) and torch.count_nonzero(out[:-1]) == 0
+
+
 def test_embed_gradient_against_differences(cuda_lib):
     """The forward is linear in the table: <dout, embed(U)> = <dtable, U>, in fp64 sums."""
     bl = cuda_lib

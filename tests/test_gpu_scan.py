@@ -121,6 +121,29 @@ def test_scan_padding_and_documents(cuda_lib, T):
     Case(cuda_lib, 2, T, 32, torch.float32, 6, lengths=[-3, T + 9]).run().check()      # clamped to 0..T
 
 
+@pytest.mark.parametrize("B,T,D", [(330, 140, 32), (40, 700, 64), (2, 3000, 64), (5, 300, 129)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_scan_masks_in_every_block_shape(cuda_lib, B, T, D, dtype):
+    """Uneven lengths and packed documents with many blocks, eight-warp clusters and narrow tiles."""
+    rng = np.random.default_rng(T)
+    lengths = rng.integers(0, T + 1, B)
+    lengths[:2] = 0, T
+    Case(cuda_lib, B, T, D, dtype, 3, lengths=lengths.tolist(), starts=_starts(B, T, D, 0.01)).run().check()
+
+
+def test_scan_sequences_more_than_32_bits_apart(cuda_lib):
+    """Sequences 2^31 elements apart (the offsets pass 32 bits in elements and in bytes)."""
+    B, T, D = 2, 100, 64
+    far = 1 << 31
+    buf = torch.empty(far + 16 * T * D, dtype=torch.bfloat16, device="cuda")
+    c = Case(cuda_lib, B, T, D, torch.bfloat16, 11)
+    for i, name in enumerate(("f", "v", "r", "dy", "y", "df", "dv", "dr")):
+        x = buf.as_strided((B, T, D), (far, D, 1), i * T * D)
+        x.copy_(getattr(c, name))
+        setattr(c, name, x)
+    c.run().check()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), torch.finfo(torch.float32).min])
 def test_scan_masked_values_do_not_leak(cuda_lib, bad):
     """Whatever lies in padding, and whatever state an earlier document left, stays out."""
