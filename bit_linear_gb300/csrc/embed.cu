@@ -4,6 +4,7 @@
 //   dtable[k] = scale * sum over i with tok[i] = k of dout[i]   (ids outside the table: dropped)
 //
 // Forward: HBM-bound gather; a thread moves eight channels of a row (16-byte loads and stores).
+// With more rows than fit the GPU at once, blocks loop over them.
 //
 // Gradient: the positions are sorted by token (stable radix sort, hand-written here) and each
 // token's rows are then summed in the order of their positions, so no atomic adds in floating
@@ -14,10 +15,10 @@
 //            to 131072 positions one cluster does it all in one launch (8192 x 512 into 256 rows:
 //            the gradient 20 us against 27 us with three launches a pass)
 //   sum      a block takes 256 sorted positions (64 where those are too few blocks) and 256
-//            channels; each warp sums runs of equal tokens over its positions in registers; the block joins the runs that cross
-//            its warps.  A run inside the block is written once, straight to dtable.  The block's
-//            first run, if it began before the block, and its last, if it goes on, go to a
-//            partial buffer.
+//            channels; each warp sums runs of equal tokens over its positions in registers; the
+//            block joins the runs that cross its warps.  A run inside the block is written once,
+//            straight to dtable.  The block's first run, if it began before the block, and its
+//            last, if it goes on, go to a partial buffer.
 //   join     for each run that leaves its block: the block where it begins adds the partials of
 //            the blocks that it covers, in order.
 // Rows of dtable without a token are written as zeros by extra blocks of the sum launch, from a
@@ -25,9 +26,9 @@
 // beside the sort instead, on the SMs it leaves idle, was slower: 279 against 177 us at 32768
 // positions, 100003 x 2048.
 // Bounded by HBM for large tables and batches: the forward of 32768 tokens from 100003 x 4096 in
-// bf16 takes 69 us (0.77 of the measured copy rate for the rows' distinct bytes), the gradient of
+// bf16 takes 67 us (0.79 of the measured copy rate for the rows' distinct bytes), the gradient of
 // 32768 x 2048 into 100003 rows 167 us (0.84), of which the sums and zeros are 137.  A few thousand
-// tokens are bound by the three launches: 8192 x 512 into 256 rows takes 15 us where the bytes
+// tokens are bound by the three launches: 8192 x 512 into 256 rows takes 14 us where the bytes
 // would take 1.3.
 #include <cuda_bf16.h>
 
@@ -71,43 +72,53 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
 }
 
-// WIDE: eight channels per thread by 16-byte accesses; otherwise one.  A block covers `rows`
-// consecutive tokens, a power of two chosen so that its 256 threads span whole rows.
-template <class TOK, class TAB, bool WIDE>
+// WIDE: eight channels per thread by 16-byte accesses; otherwise one.  tx threads (a power of two)
+// share a row.  MANY: a block has several rows, and reads a row's token before the row in hand is
+// done (65536 x 1024: 50 us, 68 us with a block for every four rows; one row each is 0.4 us faster
+// where the grid is small enough for it).
+template <class TOK, class TAB, bool WIDE, bool MANY>
 __global__ void __launch_bounds__(256) tern_embed_fwd_kernel(const __grid_constant__ EmbedArgs a, int tx) {
     constexpr int VEC = WIDE ? 8 : 1;
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const int x = threadIdx.x & (tx - 1), ty = threadIdx.x / tx;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * (256 / tx) + ty;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / tx);
+    int64_t i = static_cast<int64_t>(blockIdx.x) * (256 / tx) + ty;
     if (i >= a.n) return;
-    const int row = token_row<TOK>(a.tokens, i, a.V);
-    const TAB* src = static_cast<const TAB*>(a.table) + static_cast<int64_t>(max(row, 0)) * a.D;
-    __nv_bfloat16* dst = a.out + i * a.ld_out;
+    int row = token_row<TOK>(a.tokens, i, a.V);
+    for (;;) {
+        int next = -1;
+        if (MANY && i + stride < a.n) next = token_row<TOK>(a.tokens, i + stride, a.V);
+        const TAB* src = static_cast<const TAB*>(a.table) + static_cast<int64_t>(max(row, 0)) * a.D;
+        __nv_bfloat16* dst = a.out + i * a.ld_out;
 #pragma unroll 4
-    for (int d = x * VEC; d < a.D; d += tx * VEC) {
-        if constexpr (WIDE) {
-            float v[8] = {};
-            if (row >= 0) {
-                if constexpr (sizeof(TAB) == 4) {
-                    const float4 p = __ldg(reinterpret_cast<const float4*>(src + d));
-                    const float4 q = __ldg(reinterpret_cast<const float4*>(src + d) + 1);
-                    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-                } else {
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(src + d)), v);
-                }
+        for (int d = x * VEC; d < a.D; d += tx * VEC) {
+            if constexpr (WIDE) {
+                float v[8] = {};
+                if (row >= 0) {
+                    if constexpr (sizeof(TAB) == 4) {
+                        const float4 p = __ldg(reinterpret_cast<const float4*>(src + d));
+                        const float4 q = __ldg(reinterpret_cast<const float4*>(src + d) + 1);
+                        v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+                    } else {
+                        unpack8(__ldg(reinterpret_cast<const uint4*>(src + d)), v);
+                    }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+                    for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+                }
+                *reinterpret_cast<uint4*>(dst + d) = pack8(v);
+            } else {
+                float v = 0.0f;
+                if (row >= 0) {
+                    if constexpr (sizeof(TAB) == 4) v = __ldg(src + d) * a.scale;
+                    else v = __bfloat162float(src[d]) * a.scale;
+                }
+                dst[d] = __float2bfloat16_rn(v);
             }
-            *reinterpret_cast<uint4*>(dst + d) = pack8(v);
-        } else {
-            float v = 0.0f;
-            if (row >= 0) {
-                if constexpr (sizeof(TAB) == 4) v = __ldg(src + d) * a.scale;
-                else v = __bfloat162float(src[d]) * a.scale;
-            }
-            dst[d] = __float2bfloat16_rn(v);
         }
+        i += stride;
+        if (!MANY || i >= a.n) return;
+        row = next;
     }
 }
 
@@ -628,15 +639,17 @@ bool bad_sizes(int64_t n, int64_t V, int64_t D) {
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 template <class TOK, class TAB>
-int launch_embed(const EmbedArgs& a, cudaStream_t s) {
+int launch_embed(const EmbedArgs& a, int num_sms, cudaStream_t s) {
     const bool wide = a.D % 8 == 0 && a.ld_out % 8 == 0 && aligned16(a.table) && aligned16(a.out);
     const int items = wide ? a.D / 8 : a.D;
     int tx = 8;                                   // threads per row
     while (tx < 256 && tx < items) tx *= 2;
     const int64_t blocks = (a.n + 256 / tx - 1) / (256 / tx);
-    if (blocks > INT32_MAX) return TERN_ERR_ARG;
-    return launch_pdl(wide ? tern_embed_fwd_kernel<TOK, TAB, true> : tern_embed_fwd_kernel<TOK, TAB, false>,
-                      dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, tx);
+    const bool many = blocks > 16ll * num_sms;
+    void (*const kernel)(EmbedArgs, int) =
+        many ? (wide ? tern_embed_fwd_kernel<TOK, TAB, true, true> : tern_embed_fwd_kernel<TOK, TAB, false, true>)
+             : (wide ? tern_embed_fwd_kernel<TOK, TAB, true, false> : tern_embed_fwd_kernel<TOK, TAB, false, false>);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(many ? 16ll * num_sms : blocks)), dim3(256), 0, s, a, tx);
 }
 
 }  // namespace
@@ -653,12 +666,13 @@ extern "C" int tern_embed_fwd(const void* tokens, int tokens_dtype, const void* 
     if (!tokens || !table || !out) return TERN_ERR_ARG;
     if (!aligned(tokens, tokens_dtype == TERN_I64 ? 8 : 4) || !aligned(table, table_dtype == TERN_F32 ? 4 : 2) || !aligned(out, 2))
         return TERN_ERR_ALIGN;
-    if (int st = check_device(nullptr)) return st;
+    int num_sms = 0;
+    if (int st = check_device(&num_sms)) return st;
     EmbedArgs a{tokens, table, static_cast<__nv_bfloat16*>(out), n, ld_out, static_cast<int>(V), static_cast<int>(D), scale};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (tokens_dtype == TERN_I64)
-        return table_dtype == TERN_F32 ? launch_embed<long long, float>(a, s) : launch_embed<long long, __nv_bfloat16>(a, s);
-    return table_dtype == TERN_F32 ? launch_embed<int, float>(a, s) : launch_embed<int, __nv_bfloat16>(a, s);
+        return table_dtype == TERN_F32 ? launch_embed<long long, float>(a, num_sms, s) : launch_embed<long long, __nv_bfloat16>(a, num_sms, s);
+    return table_dtype == TERN_F32 ? launch_embed<int, float>(a, num_sms, s) : launch_embed<int, __nv_bfloat16>(a, num_sms, s);
 }
 
 extern "C" size_t tern_embed_bwd_workspace(int64_t n, int64_t V, int64_t D) {
