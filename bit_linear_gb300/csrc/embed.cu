@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
             }
             hist[k] = run;
         }
+        __syncwarp();   // the cluster's barriers are for whole warps
         ptx::cluster_sync();
         // of each digit: the counts of the tiles before this one, and of all; then a scan over the digits.
         // Two neighbouring digits a read: the exchange is bound by the number of requests.
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
         }
         // the last pass: after this the peers' counts are read no more
         const bool last = pass + 1 == g.passes;
+        __syncwarp();
         if (last) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
         int sum = own;
 #pragma unroll
@@ -391,6 +393,7 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
             g.pos[pass & 1][to] = at[r];
             if (last && g.s.present != nullptr && key[r] < g.s.V) g.s.present[key[r]] = 1;
         }
+        __syncwarp();
         if (last) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // the peers have read hist
         else ptx::cluster_sync();                                              // and the placed keys are visible to them
     }

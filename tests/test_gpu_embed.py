@@ -34,6 +34,19 @@ def test_embed_fwd_is_exact(cuda_lib, n, V, D, table, tok):
     assert torch.equal(_bits(out), _bits(ref.to(torch.bfloat16)))
 
 
+@pytest.mark.parametrize("n,D", [(2432, 2048), (2433, 2048), (5001, 2056), (7000, 263), (200001, 16), (160000, 7)])
+@pytest.mark.parametrize("table", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_embed_fwd_of_more_rows_than_blocks(cuda_lib, n, D, table):
+    """Blocks that loop over rows, the last of them uneven: every row once, and none past the last."""
+    t = _tok(n, 900, n + D, torch.int32)
+    w = torch.randn(900, D, generator=torch.Generator().manual_seed(D)).to(table).cuda()
+    out = torch.full((n + 1, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    cuda_lib.tern_embed_fwd(t, w, out[:n], scale=0.3)
+    ok = ((t >= 0) & (t < 900))[:, None]
+    ref = torch.where(ok, w[t.long().clamp(0, 899)].float() * np.float32(0.3), torch.zeros((), device="cuda"))
+    assert torch.equal(_bits(out[:n]), _bits(ref.to(torch.bfloat16))) and torch.all(out[n] == 5.0)
+
+
 def test_embed_strided_rows_and_odd_addresses(cuda_lib):
     bl = cuda_lib
     for D in (64, 63):
