@@ -21,8 +21,10 @@
 //            last, if it goes on, go to a partial buffer.
 //   join     for each run that leaves its block: the block where it begins adds the partials of
 //            the blocks that it covers, in order.
-// Rows of dtable without a token are written as zeros by extra blocks of the sum launch, from a
-// byte per row that the sort's last pass sets (with accumulate they are left alone).  Writing them
+// Rows of dtable without a token are written as zeros by extra blocks of the sum launch, which look
+// them up in the sorted keys (with accumulate they are left alone).  Marking the rows with a token
+// in the sort's last pass instead cost it a fifth of its time in stores to the same few sectors
+// (131072 x 512 into 256 rows: the gradient 74 us, 64 us without).  Writing them
 // beside the sort instead, on the SMs it leaves idle, was slower: 279 against 177 us at 32768
 // positions, 100003 x 2048.
 // Bounded by HBM for large tables and batches: the forward of 32768 tokens from 100003 x 4096 in
@@ -131,9 +133,7 @@ struct SortArgs {
     int32_t* pos_out;
     int32_t* counts;           // [digits][tiles], then (scanned) each tile's offset within the digit
     int32_t* totals;           // [digits]
-    uint8_t* present;          // [V], or null
     int n, V, tiles, shift, bits, tokens64;
-    int last;
 };
 
 // The key of position i: its token, or V for an id outside the table (sorted to the end).
@@ -149,12 +149,6 @@ __global__ void __launch_bounds__(256) tern_embed_count_kernel(const __grid_cons
     ptx::pdl_wait();
     const int digits = 1 << a.bits;
     for (int k = threadIdx.x; k < digits; k += 256) hist[k] = 0;
-    if (a.present != nullptr && a.tokens != nullptr) {   // first pass: no row has a token yet
-        uint32_t* words = reinterpret_cast<uint32_t*>(a.present);   // the plan rounds its size up to 256 bytes
-        for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k * 4 < a.V; k += static_cast<int64_t>(gridDim.x) * 256)
-            words[k] = 0u;
-    }
-    if (blockIdx.x >= a.tiles) return;   // blocks beyond the tiles only clear
     __syncthreads();
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortTile;
 #pragma unroll
@@ -258,22 +252,6 @@ __global__ void __launch_bounds__(256) tern_embed_place_kernel(const __grid_cons
         const int at = base[dg] + cnt[w][dg] + rank[r];
         a.keys_out[at] = key[r];
         a.pos_out[at] = a.pos_in != nullptr ? a.pos_in[i] : i;
-        if (a.last && a.present != nullptr && key[r] < a.V) a.present[key[r]] = 1;
-    }
-}
-
-// Zeros for the rows [first, last) of dtable that have no token, one warp per row; `has` tells.
-template <bool WIDE, class F>
-__device__ __forceinline__ void fill_rows(float* dtable, int D, int64_t first, int64_t last, int warp, int warps, F has) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t v = first + warp; v < last; v += warps) {
-        if (has(v)) continue;
-        float* row = dtable + v * D;
-        if constexpr (WIDE) {
-            for (int c = lane * 4; c < D; c += 128) __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
-        } else {
-            for (int c = lane; c < D; c += 32) __stcs(row + c, 0.0f);
-        }
     }
 }
 
@@ -282,7 +260,7 @@ __device__ __forceinline__ void fill_rows(float* dtable, int D, int64_t first, i
 // follow one another in the launch (count, offsets and place take three launches a pass otherwise,
 // most of the time of a sort of some thousand tokens).
 struct ClusterSortArgs {
-    SortArgs s;                // tokens, V, n, bits, present
+    SortArgs s;                // tokens, V, n, bits
     int32_t *keys[2], *pos[2]; // pass i reads i-1 and writes i & 1
     int passes;
 };
@@ -299,11 +277,6 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, P = gridDim.x, rank = blockIdx.x;
-    if (g.s.present != nullptr) {
-        uint32_t* words = reinterpret_cast<uint32_t*>(g.s.present);      // the plan rounds its size up to 256 bytes
-        for (int64_t k = static_cast<int64_t>(rank) * THREADS + threadIdx.x; k * 4 < g.s.V; k += static_cast<int64_t>(P) * THREADS)
-            words[k] = 0u;
-    }
     const int64_t i0 = static_cast<int64_t>(rank) * TILE + w * (32 * R);
     for (int pass = 0; pass < g.passes; ++pass) {
         const int shift = pass * g.s.bits;
@@ -391,7 +364,6 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
             const int to = base[dg] + mine[dg] + rk[r];
             g.keys[pass & 1][to] = key[r];
             g.pos[pass & 1][to] = at[r];
-            if (last && g.s.present != nullptr && key[r] < g.s.V) g.s.present[key[r]] = 1;
         }
         __syncwarp();
         if (last) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // the peers have read hist
@@ -406,7 +378,6 @@ struct RunArgs {
     const __nv_bfloat16* dout;
     float* dtable;
     float* partial;            // [run tiles][2][D]: 0 the run that began before the tile, 1 the one that goes on
-    const uint8_t* present;    // null with accumulate
     int64_t ld_dout;
     int n, V, D, run, run_tiles, ch_tiles;   // run: sorted positions per block of the sum
     int accumulate;
@@ -443,6 +414,33 @@ __device__ __forceinline__ void write_row(const RunArgs& a, int key, int c0, int
     }
 }
 
+// Zeros for the rows that have no token: warp `warp` of `warps` takes every warps-th row, whose
+// lanes look 32 of them up in the sorted keys.
+template <bool WIDE>
+__device__ __forceinline__ void fill_rows(const RunArgs& a, int64_t warp, int64_t warps, int lane) {
+    for (int64_t v0 = warp; v0 < a.V; v0 += 32 * warps) {
+        const int64_t v = v0 + lane * warps;
+        bool absent = v < a.V;
+        if (absent) {
+            int lo = 0, hi = a.n;
+            while (lo < hi) {
+                const int mid = lo + (hi - lo) / 2;
+                if (a.keys[mid] < v) lo = mid + 1;
+                else hi = mid;
+            }
+            absent = lo == a.n || a.keys[lo] != v;
+        }
+        for (uint32_t m = __ballot_sync(0xffffffffu, absent); m != 0u; m &= m - 1u) {
+            float* row = a.dtable + (v0 + (__ffs(m) - 1) * warps) * a.D;
+            if constexpr (WIDE) {
+                for (int c = lane * 4; c < a.D; c += 128) __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
+            } else {
+                for (int c = lane; c < a.D; c += 32) __stcs(row + c, 0.0f);
+            }
+        }
+    }
+}
+
 // PW: positions per warp.
 template <bool WIDE, int PW>
 __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_constant__ RunArgs a) {
@@ -453,10 +451,8 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t unit = blockIdx.x;
     if (unit >= static_cast<int64_t>(a.run_tiles) * a.ch_tiles) {
-        // rows without a token
         const int64_t sums = static_cast<int64_t>(a.run_tiles) * a.ch_tiles;
-        fill_rows<WIDE>(a.dtable, a.D, 0, a.V, static_cast<int>(unit - sums) * 8 + w, static_cast<int>(gridDim.x - sums) * 8,
-                        [&](int64_t v) { return a.present[v] != 0; });
+        fill_rows<WIDE>(a, (unit - sums) * 8 + w, (gridDim.x - sums) * 8, lane);
         return;
     }
     const int tile = static_cast<int>(unit / a.ch_tiles), c0 = static_cast<int>(unit % a.ch_tiles) * kChTile;
@@ -599,7 +595,7 @@ int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {   // the sort's passes and the workspace's parts, in bytes
     int passes = 0, bits = 0, sort_tiles = 0, run = 0, run_tiles = 0;
-    int64_t keys[2], pos[2], counts, totals, present, partial, bytes = 0;
+    int64_t keys[2], pos[2], counts, totals, partial, bytes = 0;
 };
 
 Plan make_plan(int64_t n, int64_t V, int64_t D) {
@@ -621,7 +617,6 @@ Plan make_plan(int64_t n, int64_t V, int64_t D) {
     for (int i = 0; i < 2; ++i) p.keys[i] = take(4 * n), p.pos[i] = take(4 * n);
     p.counts = take(4 * (static_cast<int64_t>(1) << p.bits) * p.sort_tiles);
     p.totals = take(4 * (static_cast<int64_t>(1) << p.bits));
-    p.present = take(V);
     p.partial = take(8 * static_cast<int64_t>(p.run_tiles) * D);
     return p;
 }
@@ -702,7 +697,6 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
     q.n = static_cast<int>(n), q.V = static_cast<int>(V), q.tiles = p.sort_tiles, q.bits = p.bits;
     q.tokens64 = tokens_dtype == TERN_I64;
     q.counts = i32(p.counts), q.totals = i32(p.totals);
-    q.present = accumulate ? nullptr : ws + p.present;
     if (n == 0) {   // nothing to sort: every row is without a token
         TERN_CUDA_TRY(cudaMemsetAsync(dtable, 0, static_cast<size_t>(V) * D * sizeof(float), s));
         return TERN_OK;
@@ -726,18 +720,15 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
             q.keys_in = pass == 0 ? nullptr : i32(p.keys[(pass - 1) & 1]);
             q.pos_in = pass == 0 ? nullptr : i32(p.pos[(pass - 1) & 1]);
             q.keys_out = i32(p.keys[pass & 1]), q.pos_out = i32(p.pos[pass & 1]);
-            q.shift = pass * p.bits, q.last = pass == p.passes - 1;
-            // the first pass also clears `present`, four bytes a thread, by up to one block per SM
-            const int clear = pass == 0 && q.present != nullptr ? static_cast<int>(V / 4096 < num_sms ? V / 4096 : num_sms) : 0;
-            const int blocks = clear > p.sort_tiles ? clear : p.sort_tiles;
-            if (int st = launch_pdl(tern_embed_count_kernel, dim3(blocks), dim3(256), 0, s, q)) return st;
+            q.shift = pass * p.bits;
+            if (int st = launch_pdl(tern_embed_count_kernel, dim3(p.sort_tiles), dim3(256), 0, s, q)) return st;
             if (int st = launch_pdl(tern_embed_offsets_kernel, dim3((digits + 7) / 8), dim3(256), 0, s, q.counts, q.totals, digits, p.sort_tiles)) return st;
             if (int st = launch_pdl(tern_embed_place_kernel, dim3(p.sort_tiles), dim3(256), 0, s, q)) return st;
         }
     }
     RunArgs a{};
     a.keys = q.keys_out, a.pos = q.pos_out, a.dout = static_cast<const __nv_bfloat16*>(dout), a.dtable = dtable;
-    a.partial = reinterpret_cast<float*>(ws + p.partial), a.present = q.present, a.ld_dout = ld_dout;
+    a.partial = reinterpret_cast<float*>(ws + p.partial), a.ld_dout = ld_dout;
     a.n = q.n, a.V = q.V, a.D = static_cast<int>(D), a.run = p.run, a.run_tiles = p.run_tiles;
     a.ch_tiles = static_cast<int>((D + kChTile - 1) / kChTile);
     a.accumulate = accumulate ? 1 : 0, a.scale = scale;
