@@ -11,9 +11,10 @@
 // point and the same bits on every run.
 //   sort     digits of up to 11 bits, one pass for tables below 2048 rows and two below 4 million:
 //            digit counts per tile of positions, a scan of each digit's counts over the tiles,
-//            then each tile places its positions (rank within the tile from warp match masks).  Up
-//            to 131072 positions one cluster does it all in one launch (8192 x 512 into 256 rows:
-//            the gradient 20 us against 27 us with three launches a pass)
+//            then each tile of 1024 places its positions (rank within the tile from warp match
+//            masks; tiles of 2048 leave SMs without one: 131072 x 512 into 256 rows 59 us, 53 us).
+//            Up to 32768 positions one cluster does it all in one launch (32768 x 512 into 256
+//            rows: 21 us, 34 us with three launches a pass; 65536: 32 us both ways)
 //   sum      a block takes 256 sorted positions (64 where those are too few blocks) and 256
 //            channels; each warp sums runs of equal tokens over its positions in registers; the
 //            block joins the runs that cross its warps.  A run inside the block is written once,
@@ -24,9 +25,9 @@
 // Rows of dtable without a token are written as zeros by extra blocks of the sum launch, which look
 // them up in the sorted keys (with accumulate they are left alone).  Marking the rows with a token
 // in the sort's last pass instead cost it a fifth of its time in stores to the same few sectors
-// (131072 x 512 into 256 rows: the gradient 74 us, 64 us without).  Writing them
-// beside the sort instead, on the SMs it leaves idle, was slower: 279 against 177 us at 32768
-// positions, 100003 x 2048.
+// (131072 x 512 into 256 rows: the gradient 74 us, 64 us without).  Writing them beside the sort
+// instead, on the SMs it leaves idle, was slower: 279 against 177 us at 32768 positions, 100003 x
+// 2048.
 // Bounded by HBM for large tables and batches: the forward of 32768 tokens from 100003 x 4096 in
 // bf16 takes 67 us (0.79 of the measured copy rate for the rows' distinct bytes), the gradient of
 // 32768 x 2048 into 100003 rows 167 us (0.84), of which the sums and zeros are 137.  A few thousand
@@ -40,7 +41,7 @@ namespace tern {
 namespace {
 
 constexpr int kMaxBits = 11;         // digit bits of a sort pass
-constexpr int kSortTile = 2048;      // positions per block of the sort (256 threads x 8)
+constexpr int kSortTile = 1024;      // positions per block of the sort (256 threads x 4)
 constexpr int kChTile = 256;         // channels per block of the sum
 
 // ------------------------------------------------------------------------------ forward
@@ -216,9 +217,9 @@ __global__ void __launch_bounds__(256) tern_embed_place_kernel(const __grid_cons
             before += a.totals[k];
         }
     }
-    // ranks within the warp's 256 positions
+    // ranks within the warp's positions
     constexpr int R = kSortTile / 256;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + w * (kSortTile / 8);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + w * (32 * R);
     int key[R], rank[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) key[r] = i0 + r * 32 + lane < a.n ? sort_key(a, static_cast<int>(i0 + r * 32 + lane)) : -1;
@@ -621,7 +622,7 @@ Plan make_plan(int64_t n, int64_t V, int64_t D) {
     return p;
 }
 
-constexpr int64_t kClusterSort = 16 * 32 * 256;   // positions that one cluster sorts
+constexpr int64_t kClusterSort = 16 * 32 * 64;   // positions that one cluster sorts
 
 template <int WARPS, int R>
 int launch_sort(const ClusterSortArgs& c, int digits, cudaStream_t s) {
@@ -708,10 +709,7 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
         c.s = q, c.passes = p.passes;
         c.s.tokens = tokens;
         for (int i = 0; i < 2; ++i) c.keys[i] = i32(p.keys[i]), c.pos[i] = i32(p.pos[i]);
-        const int st = n <= 8192    ? launch_sort<8, 2>(c, digits, s)
-                       : n <= 32768 ? launch_sort<32, 2>(c, digits, s)
-                       : n <= 65536 ? launch_sort<32, 4>(c, digits, s)
-                                    : launch_sort<32, 8>(c, digits, s);
+        const int st = n <= 8192 ? launch_sort<8, 2>(c, digits, s) : launch_sort<32, 2>(c, digits, s);
         if (st != TERN_OK) return st;
         q.keys_out = c.keys[(p.passes - 1) & 1], q.pos_out = c.pos[(p.passes - 1) & 1];
     } else {
