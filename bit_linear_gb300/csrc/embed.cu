@@ -3,7 +3,8 @@
 //   out[i]    = scale * table[tok[i]]                       (ids outside the table: a row of zeros)
 //   dtable[k] = scale * sum over i with tok[i] = k of dout[i]   (ids outside the table: dropped)
 //
-// Forward: HBM-bound gather; a thread moves eight channels of a row (16-byte loads and stores).
+// Forward: HBM-bound gather; a thread moves eight channels of a row (16-byte loads and stores, shifted
+// into place where rows start at odd addresses).
 // With more rows than fit the GPU at once, blocks loop over them.
 //
 // Gradient: the positions are sorted by token (stable radix sort, hand-written here) and each
@@ -43,6 +44,10 @@ namespace {
 constexpr int kMaxBits = 11;         // digit bits of a sort pass
 constexpr int kSortTile = 1024;      // positions per block of the sort (256 threads x 4)
 constexpr int kChTile = 256;         // channels per block of the sum
+// Of rows that start anywhere, 31 lanes' worth: a lane's channels straddle its 16 bytes and the next
+// lane's (100000 rows of 513 into 50000: 94 us, by single elements 175).
+template <bool WIDE>
+__host__ __device__ constexpr int tile_channels() { return WIDE ? kChTile : kChTile - 8; }
 
 // ------------------------------------------------------------------------------ forward
 struct EmbedArgs {
@@ -75,13 +80,61 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
 }
 
-// WIDE: eight channels per thread by 16-byte accesses; otherwise one.  tx threads (a power of two)
-// share a row.  MANY: a block has several rows, and reads a row's token before the row in hand is
+// Eight bf16 from the sh-th on of two neighbouring 16-byte words.
+__device__ __forceinline__ uint4 realign8(const uint4& a, const uint4& b, int sh) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (sh & 4) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (sh & 2) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const int bits = (sh & 1) * 16;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+}
+
+// Eight elements from any address of the table that ends at `end`: the 16-byte words around them where
+// those are the table's own, else one by one.
+__device__ __forceinline__ void load8_any(const __nv_bfloat16* p, const void* table, const void* end, float (&x)[8]) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), lo = at & ~static_cast<uintptr_t>(15);
+    const int sh = static_cast<int>(at - lo) / 2;
+    if (lo >= reinterpret_cast<uintptr_t>(table) && lo + 32 <= reinterpret_cast<uintptr_t>(end)) {
+        const uint4* w = reinterpret_cast<const uint4*>(lo);
+        unpack8(realign8(__ldg(w), __ldg(w + 1), sh), x);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __bfloat162float(p[k]);
+    }
+}
+__device__ __forceinline__ void load8_any(const float* p, const void* table, const void* end, float (&x)[8]) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), lo = at & ~static_cast<uintptr_t>(15);
+    const int sh = static_cast<int>(at - lo) / 4;
+    if (lo >= reinterpret_cast<uintptr_t>(table) && lo + 48 <= reinterpret_cast<uintptr_t>(end)) {
+        const float4* w = reinterpret_cast<const float4*>(lo);
+        const float4 a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2);
+        float v[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+        if (sh & 2) {
+#pragma unroll
+            for (int i = 0; i < 9; ++i) v[i] = v[i + 2];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = sh & 1 ? v[k + 1] : v[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __ldg(p + k);
+    }
+}
+
+// Eight channels per thread by 16-byte accesses: WIDE, rows start on such boundaries; otherwise the
+// output's boundaries are taken and the table's words realigned to them (100000 rows of 513: 49 us, by
+// single elements 94).  tx threads (a power of two) share a row.  MANY: a block has several rows, and reads a row's token before the row in hand is
 // done (65536 x 1024: 50 us, 68 us with a block for every four rows; one row each is 0.4 us faster
 // where the grid is small enough for it).
 template <class TOK, class TAB, bool WIDE, bool MANY>
 __global__ void __launch_bounds__(256) tern_embed_fwd_kernel(const __grid_constant__ EmbedArgs a, int tx) {
-    constexpr int VEC = WIDE ? 8 : 1;
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const int x = threadIdx.x & (tx - 1), ty = threadIdx.x / tx;
@@ -94,31 +147,35 @@ __global__ void __launch_bounds__(256) tern_embed_fwd_kernel(const __grid_consta
         if (MANY && i + stride < a.n) next = token_row<TOK>(a.tokens, i + stride, a.V);
         const TAB* src = static_cast<const TAB*>(a.table) + static_cast<int64_t>(max(row, 0)) * a.D;
         __nv_bfloat16* dst = a.out + i * a.ld_out;
-#pragma unroll 4
-        for (int d = x * VEC; d < a.D; d += tx * VEC) {
-            if constexpr (WIDE) {
-                float v[8] = {};
-                if (row >= 0) {
-                    if constexpr (sizeof(TAB) == 4) {
-                        const float4 p = __ldg(reinterpret_cast<const float4*>(src + d));
-                        const float4 q = __ldg(reinterpret_cast<const float4*>(src + d) + 1);
-                        v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-                    } else {
-                        unpack8(__ldg(reinterpret_cast<const uint4*>(src + d)), v);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] *= a.scale;
-                }
-                *reinterpret_cast<uint4*>(dst + d) = pack8(v);
-            } else {
-                float v = 0.0f;
-                if (row >= 0) {
-                    if constexpr (sizeof(TAB) == 4) v = __ldg(src + d) * a.scale;
-                    else v = __bfloat162float(src[d]) * a.scale;
-                }
-                dst[d] = __float2bfloat16_rn(v);
-            }
+        // channels [head, tail) lie between the output's 16-byte boundaries, eight threads take those before
+        // and eight those after, one each
+        int head = 0, tail = a.D, edge = -1;
+        float at_edge = 0.0f;
+        if constexpr (!WIDE) {
+            head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(dst) % 16) % 16 / 2), a.D);
+            tail = head + (a.D - head) / 8 * 8;
+            if (x < 8 ? x < head : x < 16 && tail + x - 8 < a.D) edge = x < 8 ? x : tail + x - 8;
+            if (row >= 0 && edge >= 0) at_edge = static_cast<float>(src[edge]) * a.scale;
         }
+#pragma unroll 4
+        for (int d = head + x * 8; d < tail; d += tx * 8) {
+            float v[8] = {};
+            if (row >= 0) {
+                if constexpr (!WIDE) {
+                    load8_any(src + d, a.table, static_cast<const TAB*>(a.table) + static_cast<int64_t>(a.V) * a.D, v);
+                } else if constexpr (sizeof(TAB) == 4) {
+                    const float4 p = __ldg(reinterpret_cast<const float4*>(src + d));
+                    const float4 q = __ldg(reinterpret_cast<const float4*>(src + d) + 1);
+                    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+                } else {
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(src + d)), v);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+            }
+            *reinterpret_cast<uint4*>(dst + d) = pack8(v);
+        }
+        if (edge >= 0) dst[edge] = __float2bfloat16_rn(at_edge);
         i += stride;
         if (!MANY || i >= a.n) return;
         row = next;
@@ -376,7 +433,7 @@ __global__ void __launch_bounds__(WARPS * 32) tern_embed_sort_kernel(const __gri
 struct RunArgs {
     const int32_t* keys;       // sorted
     const int32_t* pos;
-    const __nv_bfloat16* dout;
+    const __nv_bfloat16 *dout, *dout_end;
     float* dtable;
     float* partial;            // [run tiles][2][D]: 0 the run that began before the tile, 1 the one that goes on
     int64_t ld_dout;
@@ -385,14 +442,9 @@ struct RunArgs {
     float scale;
 };
 
-// The eight channels of a lane in a 256-channel tile: consecutive (WIDE), or 32 apart.
+// Channels c0 + 8 lane onwards of a row's sum to dtable: WIDE by 16 bytes, else by way of `stage`.
 template <bool WIDE>
-__device__ __forceinline__ int channel(int c0, int lane, int k) {
-    return WIDE ? c0 + lane * 8 + k : c0 + k * 32 + lane;
-}
-
-template <bool WIDE>
-__device__ __forceinline__ void write_row(const RunArgs& a, int key, int c0, int lane, const float (&x)[8]) {
+__device__ __forceinline__ void write_row(const RunArgs& a, int key, int c0, int lane, const float (&x)[8], float* stage) {
     float* row = a.dtable + static_cast<int64_t>(key) * a.D;
     if constexpr (WIDE) {
         const int c = c0 + lane * 8;
@@ -407,10 +459,14 @@ __device__ __forceinline__ void write_row(const RunArgs& a, int key, int c0, int
         }
         p[0] = u, p[1] = v;
     } else {
+        __syncwarp();
+        *reinterpret_cast<float4*>(stage + 8 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(stage + 8 * lane + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int c = channel<false>(c0, lane, k);
-            if (c < a.D) row[c] = (a.accumulate ? row[c] : 0.0f) + x[k] * a.scale;
+            const int c = k * 32 + lane;
+            if (c < tile_channels<WIDE>() && c0 + c < a.D) row[c0 + c] = (a.accumulate ? row[c0 + c] : 0.0f) + stage[c] * a.scale;
         }
     }
 }
@@ -445,7 +501,8 @@ __device__ __forceinline__ void fill_rows(const RunArgs& a, int64_t warp, int64_
 // PW: positions per warp.
 template <bool WIDE, int PW>
 __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_constant__ RunArgs a) {
-    __shared__ float first_s[8][kChTile], last_s[8][kChTile];
+    constexpr int CH = tile_channels<WIDE>();
+    __shared__ alignas(16) float first_s[8][kChTile], last_s[8][kChTile];
     __shared__ int first_key[8], last_key[8];   // of a warp's positions; -1 without any
     ptx::pdl_trigger();
     ptx::pdl_wait();
@@ -456,7 +513,7 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
         fill_rows<WIDE>(a, (unit - sums) * 8 + w, (gridDim.x - sums) * 8, lane);
         return;
     }
-    const int tile = static_cast<int>(unit / a.ch_tiles), c0 = static_cast<int>(unit % a.ch_tiles) * kChTile;
+    const int tile = static_cast<int>(unit / a.ch_tiles), c0 = static_cast<int>(unit % a.ch_tiles) * CH;
     const int p0 = tile * (8 * PW) + w * PW;
     const int mine = lane < PW && p0 + lane < a.n ? a.keys[p0 + lane] : a.V;
     const int where = mine < a.V ? a.pos[p0 + lane] : 0;
@@ -468,22 +525,31 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
     constexpr int U = 8;    // rows in flight
     for (int i0 = 0; i0 < cnt; i0 += U) {
         uint4 raw[U];
+        uint32_t shifts = 0;     // elements between a row's 16-byte boundary and its channel c0
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int src = __shfl_sync(0xffffffffu, where, i0 + u);
             raw[u] = make_uint4(0u, 0u, 0u, 0u);
             if (i0 + u < cnt) {
-                const __nv_bfloat16* row = a.dout + static_cast<int64_t>(src) * a.ld_dout;
+                const __nv_bfloat16* row = a.dout + static_cast<int64_t>(src) * a.ld_dout + c0;
                 if constexpr (WIDE) {
-                    if (c0 + lane * 8 < a.D) raw[u] = __ldg(reinterpret_cast<const uint4*>(row + c0 + lane * 8));
+                    if (c0 + lane * 8 < a.D) raw[u] = __ldg(reinterpret_cast<const uint4*>(row + lane * 8));
                 } else {
-                    uint32_t h[8];
+                    const uintptr_t at = reinterpret_cast<uintptr_t>(row), lo = (at & ~static_cast<uintptr_t>(15)) + 16 * lane;
+                    const int sh = static_cast<int>(at & 15) / 2;
+                    shifts |= static_cast<uint32_t>(sh) << (4 * u);
+                    if (c0 + lane * 8 - sh >= a.D) continue;
+                    if (lo >= reinterpret_cast<uintptr_t>(a.dout) && lo + 16 <= reinterpret_cast<uintptr_t>(a.dout_end)) {
+                        raw[u] = __ldg(reinterpret_cast<const uint4*>(lo));
+                    } else {   // the tensor's first or last bytes
+                        uint32_t h[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int c = channel<false>(c0, lane, k);
-                        h[k] = c < a.D ? __ldg(reinterpret_cast<const unsigned short*>(row) + c) : 0u;
+                        for (int k = 0; k < 8; ++k) {
+                            const unsigned short* e = reinterpret_cast<const unsigned short*>(lo) + k;
+                            h[k] = e >= reinterpret_cast<const unsigned short*>(a.dout) && e < reinterpret_cast<const unsigned short*>(a.dout_end) ? *e : 0u;
+                        }
+                        raw[u] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
                     }
-                    raw[u] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
                 }
             }
         }
@@ -494,14 +560,20 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
             if (key != cur) {
                 if (first) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) first_s[w][channel<WIDE>(0, lane, k)] = acc[k];
+                    for (int k = 0; k < 8; ++k) first_s[w][lane * 8 + k] = acc[k];
                     first = false;
                 } else {
-                    write_row<WIDE>(a, cur, c0, lane, acc);
+                    write_row<WIDE>(a, cur, c0, lane, acc, last_s[w]);   // not in use before the end
                 }
                 cur = key;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+            }
+            if constexpr (!WIDE) {
+                uint4 next;
+                next.x = __shfl_down_sync(0xffffffffu, raw[u].x, 1), next.y = __shfl_down_sync(0xffffffffu, raw[u].y, 1);
+                next.z = __shfl_down_sync(0xffffffffu, raw[u].z, 1), next.w = __shfl_down_sync(0xffffffffu, raw[u].w, 1);
+                raw[u] = realign8(raw[u], next, shifts >> (4 * u) & 7);
             }
             float x[8];
             unpack8(raw[u], x);
@@ -510,13 +582,14 @@ __global__ void __launch_bounds__(256) tern_embed_sum_kernel(const __grid_consta
         }
     }
     // the warp's open run: its only one (first) or its last
+    if constexpr (!WIDE) __syncwarp();   // write_row's reads of last_s
 #pragma unroll
-    for (int k = 0; k < 8; ++k) (first ? first_s : last_s)[w][channel<WIDE>(0, lane, k)] = acc[k];
+    for (int k = 0; k < 8; ++k) (first ? first_s : last_s)[w][lane * 8 + k] = acc[k];
     if (lane == 0) last_key[w] = cnt == 0 ? -1 : (first ? -2 : cur);   // -2: a single run
     __syncthreads();
     // join the runs across the warps, a thread per channel
     const int c = c0 + threadIdx.x;
-    if (c >= a.D || first_key[0] < 0) return;
+    if (threadIdx.x >= CH || c >= a.D || first_key[0] < 0) return;
     const int begin = tile * (8 * PW), end = min(begin + 8 * PW, a.n);
     const bool from_before = begin > 0 && a.keys[begin - 1] == first_key[0];
     float* part = a.partial + static_cast<int64_t>(tile) * 2 * a.D + c;
@@ -640,8 +713,8 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 template <class TOK, class TAB>
 int launch_embed(const EmbedArgs& a, int num_sms, cudaStream_t s) {
     const bool wide = a.D % 8 == 0 && a.ld_out % 8 == 0 && aligned16(a.table) && aligned16(a.out);
-    const int items = wide ? a.D / 8 : a.D;
-    int tx = 8;                                   // threads per row
+    const int items = a.D / 8;
+    int tx = wide ? 8 : 16;                       // threads per row
     while (tx < 256 && tx < items) tx *= 2;
     const int64_t blocks = (a.n + 256 / tx - 1) / (256 / tx);
     const bool many = blocks > 16ll * num_sms;
@@ -728,7 +801,9 @@ extern "C" int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* 
     a.keys = q.keys_out, a.pos = q.pos_out, a.dout = static_cast<const __nv_bfloat16*>(dout), a.dtable = dtable;
     a.partial = reinterpret_cast<float*>(ws + p.partial), a.ld_dout = ld_dout;
     a.n = q.n, a.V = q.V, a.D = static_cast<int>(D), a.run = p.run, a.run_tiles = p.run_tiles;
-    a.ch_tiles = static_cast<int>((D + kChTile - 1) / kChTile);
+    a.dout_end = a.dout + (n - 1) * ld_dout + D;
+    const int ch = wide ? tile_channels<true>() : tile_channels<false>();
+    a.ch_tiles = static_cast<int>((D + ch - 1) / ch);
     a.accumulate = accumulate ? 1 : 0, a.scale = scale;
     const int64_t units = static_cast<int64_t>(a.run_tiles) * a.ch_tiles;
     const int64_t fill = accumulate ? 0 : (V + 7) / 8 < 8 * num_sms ? (V + 7) / 8 : 8 * num_sms;

@@ -47,6 +47,35 @@ def test_embed_fwd_of_more_rows_than_blocks(cuda_lib, n, D, table):
     assert torch.equal(_bits(out[:n]), _bits(ref.to(torch.bfloat16))) and torch.all(out[n] == 5.0)
 
 
+@pytest.mark.parametrize("D", [1, 5, 15, 16, 23, 247, 248, 249, 256, 263, 521])
+@pytest.mark.parametrize("table", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_embed_rows_at_every_address(cuda_lib, D, table):
+    """Tables, outputs and gradients that start at every element of a 16-byte word, with NaN on both
+    sides of each and between strided rows: bit for bit the aligned call's, and nothing else written."""
+    bl = cuda_lib
+    n, V = 130, 40
+    t = _tok(n, V, D, torch.int32)
+    w = torch.randn(V, D, generator=torch.Generator().manual_seed(D)).to(table).cuda()
+    ok = ((t >= 0) & (t < V))[:, None]
+    ref = torch.where(ok, w[t.long().clamp(0, V - 1)].float() * np.float32(0.7), torch.zeros((), device="cuda")).bfloat16()
+    ints = torch.randint(-9, 10, (n, D), device="cuda").bfloat16()
+    gref = torch.zeros(V, D, device="cuda").index_add_(0, t.long().clamp(0, V - 1), torch.where(ok, ints.float(), torch.zeros((), device="cuda")))
+    ws = torch.empty(bl.tern_embed_bwd_workspace(n, V, D), dtype=torch.uint8, device="cuda")
+    for off in range(8):
+        ld = D + (0, 3, 8)[off % 3]
+        nan = lambda k, dt: torch.full((k,), float("nan"), dtype=dt, device="cuda")  # noqa: E731
+        tbuf, obuf, dbuf, gbuf = nan(V * D + 9, table), nan(n * ld + 9, torch.bfloat16), nan(n * ld + 9, torch.bfloat16), nan(V * D + 9, torch.float32)
+        tab, g = (b[off:off + V * D].view(V, D) for b in (tbuf, gbuf))
+        out, dout = (b[off:off + n * ld].as_strided((n, D), (ld, 1), off) for b in (obuf, dbuf))
+        tab.copy_(w), dout.copy_(ints)
+        bl.tern_embed_fwd(t, tab, out, scale=0.7)
+        assert torch.equal(_bits(out), _bits(ref)) and int(obuf.isnan().sum()) == obuf.numel() - n * D
+        bl.tern_embed_bwd(t, dout, g, ws)
+        assert torch.equal(g, gref) and int(gbuf.isnan().sum()) == 9
+        bl.tern_embed_bwd(t, dout, g, ws, accumulate=True)
+        assert torch.equal(g, 2 * gref) and int(gbuf.isnan().sum()) == 9
+
+
 def test_embed_strided_rows_and_odd_addresses(cuda_lib):
     bl = cuda_lib
     for D in (64, 63):
