@@ -32,6 +32,7 @@
 // warps on a scheduler, each waiting on its own chain of exponential, reciprocal and fold).  More
 // warps with fewer rows each lost more to the folds than they hid (RPT 4: 77 us), fewer with more
 // rows hid less.  Gates and states are fp32; outputs are rounded once.
+#include <algorithm>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -77,22 +78,28 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 __device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xffffffffu, a.v, from)}; }
 
 // --------------------------------------------------------------- element access
-// NP pairs of neighbouring elements of a row, eight bytes.  WIDE: one access (and the sequences'
-// inputs come by TMA); otherwise element by element (odd widths, strides or addresses),
-// where a row's last lane may hold fewer: nch elements are there, loads repeat the last and stores
-// leave the others out.
-template <class T, bool WIDE_>
+// NP pairs of neighbouring elements of a row, eight bytes.  W is the alignment of every row, in
+// bytes.  16 (WIDE): one access, and the sequences' inputs come by TMA.  Otherwise (odd widths,
+// strides or addresses) words of W bytes, where a row's last lane may hold fewer elements: nch
+// are there, loads repeat a word that is and stores leave the others out.
+template <class T, int W>
 struct Io;
-template <bool WIDE_>
-struct Io<__nv_bfloat16, WIDE_> {
-    static constexpr bool WIDE = WIDE_;
+template <int W>
+struct Io<__nv_bfloat16, W> {
+    static constexpr bool WIDE = W == 16;
     static constexpr int NP = 2;
     using Raw = uint2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
-        if constexpr (WIDE) return __ldg(reinterpret_cast<const uint2*>(p));
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-        const uint32_t x0 = __ldg(q), x1 = __ldg(q + min(1, nch - 1)), x2 = __ldg(q + min(2, nch - 1)), x3 = __ldg(q + min(3, nch - 1));
-        return make_uint2(x0 | x1 << 16, x2 | x3 << 16);
+        if constexpr (W == 16) {
+            return __ldg(reinterpret_cast<const uint2*>(p));
+        } else if constexpr (W == 4) {   // nch is even
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+            return make_uint2(__ldg(q), __ldg(q + (nch > 2 ? 1 : 0)));
+        } else {
+            const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+            const uint32_t x0 = __ldg(q), x1 = __ldg(q + min(1, nch - 1)), x2 = __ldg(q + min(2, nch - 1)), x3 = __ldg(q + min(3, nch - 1));
+            return make_uint2(x0 | x1 << 16, x2 | x3 << 16);
+        }
     }
     static __device__ __forceinline__ void get(const Raw& r, F2 (&x)[2]) {
         x[0] = pair(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
@@ -106,8 +113,12 @@ struct Io<__nv_bfloat16, WIDE_> {
     }
     static __device__ __forceinline__ void store(char* p, const F2 (&x)[2], int nch) {
         const uint32_t a = round2(x[0]), b = round2(x[1]);
-        if constexpr (WIDE) {
+        if constexpr (W == 16) {
             *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+        } else if constexpr (W == 4) {
+            uint32_t* q = reinterpret_cast<uint32_t*>(p);
+            q[0] = a;
+            if (nch > 2) q[1] = b;
         } else {
             unsigned short* q = reinterpret_cast<unsigned short*>(p);
             q[0] = static_cast<unsigned short>(a);
@@ -117,9 +128,9 @@ struct Io<__nv_bfloat16, WIDE_> {
         }
     }
 };
-template <bool WIDE_>
-struct Io<float, WIDE_> {
-    static constexpr bool WIDE = WIDE_;
+template <int W>
+struct Io<float, W> {
+    static constexpr bool WIDE = W == 16;
     static constexpr int NP = 1;
     using Raw = float2;
     static __device__ __forceinline__ Raw load(const char* p, int nch) {
@@ -245,10 +256,10 @@ struct GradArgs {
 
 // How a block cuts its rows and channels: LPR lanes make a row of CH channels, a lane's segment
 // has RPT rows, a warp SEGS segments.
-template <class T_, bool WIDE_, int LPR_, int RPT_, int WARPS_, int MINB_, int STAGES_>
+template <class T_, int W, int LPR_, int RPT_, int WARPS_, int MINB_, int STAGES_>
 struct Shape {
     using T = T_;
-    using X = Io<T_, WIDE_>;
+    using X = Io<T_, W>;
     static constexpr int NP = X::NP, LPR = LPR_, RPT = RPT_;
     static constexpr int WARPS = WARPS_, MINB = MINB_, STAGES = STAGES_, SEGS = 32 / LPR, CH = LPR * NP * 2, WROWS = SEGS * RPT, ROWS = WARPS * WROWS;
 };
@@ -352,9 +363,9 @@ struct Inputs {
     // The rows of tensor t; those that are not live stay zero.
     __device__ __forceinline__ void load(int t, const char* p, int64_t st, int nl, int nch, bool full) {
         if constexpr (!WIDE) {
-            if (full) {
+            if (full && nch == 2 * C::NP) {   // all there: offsets known to the compiler
 #pragma unroll
-                for (int i = 0; i < C::RPT; ++i) raw[t][i] = C::X::load(p + i * st, nch);
+                for (int i = 0; i < C::RPT; ++i) raw[t][i] = C::X::load(p + i * st, 2 * C::NP);
             } else {
 #pragma unroll
                 for (int i = 0; i < C::RPT; ++i) {
@@ -936,9 +947,9 @@ struct StepArgs {
     int D;
 };
 
-template <class T, bool WIDE>
+template <class T, int W>
 __global__ void __launch_bounds__(128) tern_scan_step_kernel(const __grid_constant__ StepArgs a) {
-    using X = Io<T, WIDE>;
+    using X = Io<T, W>;
     constexpr int NP = X::NP;
     ptx::pdl_trigger();
     ptx::pdl_wait();
@@ -970,15 +981,17 @@ namespace {
 
 size_t elem(int dtype) { return dtype == TERN_F32 ? 4 : 2; }
 
-// TERN_OK when x can be read or written as rows of elements, else the error; `wide` is cleared
-// when its address or strides keep it from TMA copies.
-int check_act(const tern_act& x, const tern_scan* s, bool& wide) {
+// TERN_OK when x can be read or written as rows of elements, else the error; `align` becomes the
+// largest of 16, 4 and an element's bytes that its rows' addresses allow as well (16 for TMA copies).
+int check_act(const tern_act& x, const tern_scan* s, int& align) {
     const int64_t es = static_cast<int64_t>(elem(s->dtype));
     if (x.p == nullptr || x.stride_b < 0 || x.stride_t < 0) return TERN_ERR_ARG;
     if (x.stride_b > INT64_MAX / 4 / es || x.stride_t > INT64_MAX / 4 / es) return TERN_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(x.p) % es != 0) return TERN_ERR_ALIGN;
-    if (reinterpret_cast<uintptr_t>(x.p) % 16 != 0 || x.stride_b * es % 16 != 0 || x.stride_t * es % 16 != 0) wide = false;
-    if ((s->T > 1 && x.stride_t < s->D) || (s->B > 1 && x.stride_b == 0)) wide = false;   // overlapping rows
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(x.p) | static_cast<uintptr_t>(x.stride_b * es) | static_cast<uintptr_t>(x.stride_t * es);
+    if (bits % 16 != 0) align = std::min(align, 4);
+    if (bits % 4 != 0) align = 2;
+    if ((s->T > 1 && x.stride_t < s->D) || (s->B > 1 && x.stride_b == 0)) align = std::min(align, 4);   // overlapping rows
     return TERN_OK;
 }
 Strided strided(const tern_act& x, int dtype) {
@@ -987,14 +1000,15 @@ Strided strided(const tern_act& x, int dtype) {
 }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-int check_scan(const tern_scan* s, bool& wide) {
+int check_scan(const tern_scan* s, int& align) {
     if (s == nullptr || (s->dtype != TERN_BF16 && s->dtype != TERN_F32)) return TERN_ERR_ARG;
     if (s->B < 0 || s->T < 0 || s->D < 0 || s->T > INT32_MAX - 256 || s->D > INT32_MAX - 256 || s->B > INT32_MAX - 256) return TERN_ERR_ARG;
-    wide = s->D * static_cast<int64_t>(elem(s->dtype)) % 16 == 0;
+    const int64_t row = s->D * static_cast<int64_t>(elem(s->dtype));
+    align = row % 16 == 0 ? 16 : row % 4 == 0 ? 4 : 2;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (s->T > 0) {
         for (const tern_act* x : {&s->f, &s->v, &s->r})
-            if (int st = check_act(*x, s, wide)) return st;
+            if (int st = check_act(*x, s, align)) return st;
     }
     if (!aligned4(s->f_bias) || !aligned4(s->lengths)) return TERN_ERR_ALIGN;
     return TERN_OK;
@@ -1073,11 +1087,11 @@ int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStr
 // half the GPU.  (Forward and gradient of 16 x 512 x 512: 13.6 + 22.8 us as clusters of four-warp
 // blocks, 12.2 + 19.8 us as eight-warp blocks; of 8 x 2048 x 2048: 59 + 125 us with four warps,
 // 67 + 134 us with eight; forward of 1 x 65536 x 512: 88 us in the narrow tiles, 122 us in wide ones.)
-template <class T, bool WIDE, int RPT, class F>
+template <class T, int W, int RPT, class F>
 int with_shape(int64_t B, int64_t D, int64_t T_, int num_sms, F run) {
-    using Four = Shape<T, WIDE, 8, RPT, 4, 4, 2>;
-    using Eight = Shape<T, WIDE, 8, RPT, 8, 2, 2>;
-    using Narrow = Shape<T, WIDE, 4, RPT, 4, 4, 2>;
+    using Four = Shape<T, W, 8, RPT, 4, 4, 2>;
+    using Eight = Shape<T, W, 8, RPT, 8, 2, 2>;
+    using Narrow = Shape<T, W, 4, RPT, 4, 4, 2>;
     const int64_t blocks = B * ((D + Four::CH - 1) / Four::CH);
     if (blocks > 2 * num_sms) return run(Four{}, std::false_type{});
     const int S = cluster_size<Eight>(blocks, steps_of(T_, Eight::ROWS), num_sms);
@@ -1114,12 +1128,12 @@ extern "C" size_t tern_scan_saved(int64_t B, int64_t T, int64_t D) {
 
 extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act* y, float* hT, float* saved,
                              size_t saved_bytes, void* stream) {
-    bool wide;
-    if (int st = check_scan(s, wide)) return st;
+    int align;
+    if (int st = check_scan(s, align)) return st;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (s->T > 0) {
         if (y == nullptr) return TERN_ERR_ARG;
-        if (int st = check_act(*y, s, wide)) return st;
+        if (int st = check_act(*y, s, align)) return st;
     }
     if (!aligned4(h0) || !aligned4(hT) || !aligned4(saved)) return TERN_ERR_ALIGN;
     if (saved != nullptr && saved_bytes < tern_scan_saved(s->B, s->T, s->D)) return TERN_ERR_WORKSPACE;
@@ -1131,9 +1145,10 @@ extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     auto run = [&](auto shape, auto cl) { return launch_fwd<decltype(shape), decltype(cl)::value>(a, s->B, num_sms, cs); };
     if (s->dtype == TERN_BF16)
-        return wide ? with_shape<__nv_bfloat16, true, 8>(s->B, s->D, s->T, num_sms, run)
-                    : with_shape<__nv_bfloat16, false, 8>(s->B, s->D, s->T, num_sms, run);
-    return wide ? with_shape<float, true, 8>(s->B, s->D, s->T, num_sms, run) : with_shape<float, false, 8>(s->B, s->D, s->T, num_sms, run);
+        return align == 16  ? with_shape<__nv_bfloat16, 16, 8>(s->B, s->D, s->T, num_sms, run)
+               : align == 4 ? with_shape<__nv_bfloat16, 4, 8>(s->B, s->D, s->T, num_sms, run)
+                            : with_shape<__nv_bfloat16, 2, 8>(s->B, s->D, s->T, num_sms, run);
+    return align == 16 ? with_shape<float, 16, 8>(s->B, s->D, s->T, num_sms, run) : with_shape<float, 4, 8>(s->B, s->D, s->T, num_sms, run);
 }
 
 extern "C" size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D) {
@@ -1144,14 +1159,14 @@ extern "C" size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D) {
 extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_act* dy, const float* dhT,
                              const tern_act* df, const tern_act* dv, const tern_act* dr, float* dbias, float* dh0,
                              void* workspace, size_t ws_bytes, void* stream) {
-    bool wide;
-    if (int st = check_scan(s, wide)) return st;
+    int align;
+    if (int st = check_scan(s, align)) return st;
     if (s->B == 0 || s->D == 0) return s->D == 0 || dbias == nullptr ? TERN_OK : TERN_ERR_ARG;
     if (s->T > 0) {
         if (saved == nullptr) return TERN_ERR_ARG;
         for (const tern_act* x : {dy, df, dv, dr}) {
             if (x == nullptr) return TERN_ERR_ARG;
-            if (int st = check_act(*x, s, wide)) return st;
+            if (int st = check_act(*x, s, align)) return st;
         }
     }
     if (!aligned4(saved) || !aligned4(dhT) || !aligned4(dbias) || !aligned4(dh0) || !aligned4(workspace)) return TERN_ERR_ALIGN;
@@ -1170,28 +1185,29 @@ extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     auto run = [&](auto shape, auto cl) { return launch_bwd<decltype(shape), decltype(cl)::value>(g, s->B, num_sms, dbias, cs); };
     if (s->dtype == TERN_BF16)
-        return wide ? with_shape<__nv_bfloat16, true, 4>(s->B, s->D, s->T, num_sms, run)
-                    : with_shape<__nv_bfloat16, false, 4>(s->B, s->D, s->T, num_sms, run);
-    return wide ? with_shape<float, true, 4>(s->B, s->D, s->T, num_sms, run) : with_shape<float, false, 4>(s->B, s->D, s->T, num_sms, run);
+        return align == 16  ? with_shape<__nv_bfloat16, 16, 4>(s->B, s->D, s->T, num_sms, run)
+               : align == 4 ? with_shape<__nv_bfloat16, 4, 4>(s->B, s->D, s->T, num_sms, run)
+                            : with_shape<__nv_bfloat16, 2, 4>(s->B, s->D, s->T, num_sms, run);
+    return align == 16 ? with_shape<float, 16, 4>(s->B, s->D, s->T, num_sms, run) : with_shape<float, 4, 4>(s->B, s->D, s->T, num_sms, run);
 }
 
 namespace {
-template <class T, bool WIDE>
+template <class T, int W>
 int launch_step(const StepArgs& a, cudaStream_t s) {
-    constexpr int VEC = 2 * Io<T, WIDE>::NP;
+    constexpr int VEC = 2 * Io<T, W>::NP;
     const int64_t blocks = (a.rows * ((a.D + VEC - 1) / VEC) + 127) / 128;
     if (blocks > INT32_MAX) return TERN_ERR_ARG;
-    return launch_pdl(tern_scan_step_kernel<T, WIDE>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, s, a);
+    return launch_pdl(tern_scan_step_kernel<T, W>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, s, a);
 }
 }  // namespace
 
 extern "C" int tern_scan_step(const tern_scan* s, const float* h_in, float* h_out, const tern_act* y, void* stream) {
-    bool wide;
-    if (int st = check_scan(s, wide)) return st;
+    int align;
+    if (int st = check_scan(s, align)) return st;
     if (s->T != 1 || s->lengths != nullptr || s->starts != nullptr) return TERN_ERR_ARG;
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (h_in == nullptr || h_out == nullptr || y == nullptr) return TERN_ERR_ARG;
-    if (int st = check_act(*y, s, wide)) return st;
+    if (int st = check_act(*y, s, align)) return st;
     if (!aligned4(h_in) || !aligned4(h_out)) return TERN_ERR_ALIGN;
     if (int st = check_device(nullptr)) return st;
     StepArgs a{};
@@ -1202,6 +1218,6 @@ extern "C" int tern_scan_step(const tern_scan* s, const float* h_in, float* h_ou
     a.f_bias = s->f_bias, a.h_in = h_in, a.h_out = h_out;
     a.rows = s->B, a.D = static_cast<int>(s->D);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (s->dtype == TERN_BF16) return wide ? launch_step<__nv_bfloat16, true>(a, cs) : launch_step<__nv_bfloat16, false>(a, cs);
-    return wide ? launch_step<float, true>(a, cs) : launch_step<float, false>(a, cs);
+    if (s->dtype == TERN_BF16) return align == 16 ? launch_step<__nv_bfloat16, 16>(a, cs) : launch_step<__nv_bfloat16, 2>(a, cs);
+    return align == 16 ? launch_step<float, 16>(a, cs) : launch_step<float, 4>(a, cs);
 }
