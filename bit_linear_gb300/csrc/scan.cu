@@ -81,11 +81,14 @@ __device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xff
 // NP pairs of neighbouring elements of a row, eight bytes.  W is the alignment of every row, in
 // bytes.  16 (WIDE): one access, and the sequences' inputs come by TMA.  Otherwise (odd widths,
 // strides or addresses) words of W bytes, where a row's last lane may hold fewer elements: nch
-// are there, loads repeat a word that is and stores leave the others out.
+// are there, loads repeat a word that is and stores leave the others out.  (8 x 2048 x D in bf16, the
+// forward and the gradient: D = 1024 32 + 68 us; 1026 40 + 87, element by element 73 + 168; 1025 55 +
+// 129, with the words around a lane's elements where all of them are in the tensor.)
 template <class T, int W>
 struct Io;
-template <int W>
-struct Io<__nv_bfloat16, W> {
+template <int W_>
+struct Io<__nv_bfloat16, W_> {
+    static constexpr int W = W_;
     static constexpr bool WIDE = W == 16;
     static constexpr int NP = 2;
     using Raw = uint2;
@@ -100,6 +103,15 @@ struct Io<__nv_bfloat16, W> {
             const uint32_t x0 = __ldg(q), x1 = __ldg(q + min(1, nch - 1)), x2 = __ldg(q + min(2, nch - 1)), x3 = __ldg(q + min(3, nch - 1));
             return make_uint2(x0 | x1 << 16, x2 | x3 << 16);
         }
+    }
+    // W = 2, four elements with the words around them all in the tensor: two or three words, shifted.
+    static __device__ __forceinline__ Raw load_words(const char* p) {
+        const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 2u;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p - odd);
+        const uint32_t w0 = __ldg(q), w1 = __ldg(q + 1);
+        uint32_t w2 = 0u;
+        if (odd) w2 = __ldg(q + 2);
+        return make_uint2(__funnelshift_r(w0, w1, odd * 8), __funnelshift_r(w1, w2, odd * 8));
     }
     static __device__ __forceinline__ void get(const Raw& r, F2 (&x)[2]) {
         x[0] = pair(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
@@ -121,15 +133,24 @@ struct Io<__nv_bfloat16, W> {
             if (nch > 2) q[1] = b;
         } else {
             unsigned short* q = reinterpret_cast<unsigned short*>(p);
-            q[0] = static_cast<unsigned short>(a);
-            if (nch > 1) q[1] = static_cast<unsigned short>(a >> 16);
-            if (nch > 2) q[2] = static_cast<unsigned short>(b);
-            if (nch > 3) q[3] = static_cast<unsigned short>(b >> 16);
+            if (nch < 4) {
+                q[0] = static_cast<unsigned short>(a);
+                if (nch > 1) q[1] = static_cast<unsigned short>(a >> 16);
+                if (nch > 2) q[2] = static_cast<unsigned short>(b);
+            } else if (reinterpret_cast<uintptr_t>(p) & 2) {
+                q[0] = static_cast<unsigned short>(a);
+                *reinterpret_cast<uint32_t*>(q + 1) = __funnelshift_r(a, b, 16);
+                q[3] = static_cast<unsigned short>(b >> 16);
+            } else {
+                reinterpret_cast<uint32_t*>(p)[0] = a;
+                reinterpret_cast<uint32_t*>(p)[1] = b;
+            }
         }
     }
 };
-template <int W>
-struct Io<float, W> {
+template <int W_>
+struct Io<float, W_> {
+    static constexpr int W = W_;
     static constexpr bool WIDE = W == 16;
     static constexpr int NP = 1;
     using Raw = float2;
@@ -236,6 +257,7 @@ __device__ __forceinline__ void compose(F2 A2, F2 H2, F2& A, F2& H, bool docs) {
 struct Strided {
     char* p;
     int64_t sb, st;   // bytes between sequences and between rows
+    char* end;        // past the last row's last element
 };
 struct ScanArgs {
     Strided f, v, r, y;   // y: the forward's output, or the backward's dy
@@ -361,8 +383,16 @@ struct Inputs {
         else return raw[t][i];
     }
     // The rows of tensor t; those that are not live stay zero.
-    __device__ __forceinline__ void load(int t, const char* p, int64_t st, int nl, int nch, bool full) {
+    __device__ __forceinline__ void load(int t, const Strided& x, const char* p, int nl, int nch, bool full) {
         if constexpr (!WIDE) {
+            const int64_t st = x.st;
+            if constexpr (C::X::W == 2) {   // but for the tensor's first and last row the words around a lane's elements are its own
+                if (__all_sync(0xffffffffu, full && nch == 2 * C::NP && p - 2 >= x.p && p + (C::RPT - 1) * st + 10 <= x.end)) {
+#pragma unroll
+                    for (int i = 0; i < C::RPT; ++i) raw[t][i] = C::X::load_words(p + i * st);
+                    return;
+                }
+            }
             if (full && nch == 2 * C::NP) {   // all there: offsets known to the compiler
 #pragma unroll
                 for (int i = 0; i < C::RPT; ++i) raw[t][i] = C::X::load(p + i * st, 2 * C::NP);
@@ -662,9 +692,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
             in.at = lane_at + it % C::STAGES * (3 * In::TILE_BYTES);
             if (has_rows(it)) ok = ok && wait_phase(&full[it % C::STAGES], (it / C::STAGES) & 1);
         }
-        in.load(0, fp + row0 * a.f.st, a.f.st, nl, q.nch, all_live);
-        in.load(1, vp + row0 * a.v.st, a.v.st, nl, q.nch, all_live);
-        in.load(2, rp + row0 * a.r.st, a.r.st, nl, q.nch, all_live);
+        in.load(0, a.f, fp + row0 * a.f.st, nl, q.nch, all_live);
+        in.load(1, a.v, vp + row0 * a.v.st, nl, q.nch, all_live);
+        in.load(2, a.r, rp + row0 * a.r.st, nl, q.nch, all_live);
         const uint32_t cut = start_bits<C>(a, q.b, static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))), len, q.seg, q.lane);
         const bool plain = all_live && (!docs || __all_sync(0xffffffffu, cut == 0));
         // (A, H) of this lane's rows
@@ -804,10 +834,10 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
         const bool all_live = __all_sync(0xffffffffu, nl == RPT);
         In in;
         if constexpr (C::X::WIDE) in.at = lane_at + it % C::STAGES * (4 * In::TILE_BYTES);
-        in.load(0, fp + row0 * a.f.st, a.f.st, nl, q.nch, all_live);
-        in.load(1, vp + row0 * a.v.st, a.v.st, nl, q.nch, all_live);
-        in.load(2, rp + row0 * a.r.st, a.r.st, nl, q.nch, all_live);
-        in.load(3, yp + row0 * a.y.st, a.y.st, nl, q.nch, all_live);
+        in.load(0, a.f, fp + row0 * a.f.st, nl, q.nch, all_live);
+        in.load(1, a.v, vp + row0 * a.v.st, nl, q.nch, all_live);
+        in.load(2, a.r, rp + row0 * a.r.st, nl, q.nch, all_live);
+        in.load(3, a.y, yp + row0 * a.y.st, nl, q.nch, all_live);
         const uint32_t cut = start_bits<C>(a, q.b, step >= 0 ? static_cast<int>(min(first - q.seg * RPT, static_cast<int64_t>(a.T))) : a.T,
                                            len, q.seg, q.lane);
         const bool plain = all_live && (!docs || __all_sync(0xffffffffu, cut == 0));
@@ -994,9 +1024,10 @@ int check_act(const tern_act& x, const tern_scan* s, int& align) {
     if ((s->T > 1 && x.stride_t < s->D) || (s->B > 1 && x.stride_b == 0)) align = std::min(align, 4);   // overlapping rows
     return TERN_OK;
 }
-Strided strided(const tern_act& x, int dtype) {
-    const int64_t es = static_cast<int64_t>(elem(dtype));
-    return Strided{static_cast<char*>(x.p), x.stride_b * es, x.stride_t * es};
+Strided strided(const tern_act& x, const tern_scan* s) {
+    const int64_t es = static_cast<int64_t>(elem(s->dtype)), sb = x.stride_b * es, st = x.stride_t * es;
+    char* p = static_cast<char*>(x.p);
+    return Strided{p, sb, st, p + (s->B - 1) * sb + (s->T - 1) * st + s->D * es};
 }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -1101,7 +1132,7 @@ int with_shape(int64_t B, int64_t D, int64_t T_, int num_sms, F run) {
 
 ScanArgs scan_args(const tern_scan* s) {
     ScanArgs a{};
-    a.f = strided(s->f, s->dtype), a.v = strided(s->v, s->dtype), a.r = strided(s->r, s->dtype);
+    a.f = strided(s->f, s), a.v = strided(s->v, s), a.r = strided(s->r, s);
     a.f_bias = s->f_bias, a.lengths = s->lengths, a.starts = s->starts;
     a.T = static_cast<int>(s->T), a.D = static_cast<int>(s->D);
     return a;
@@ -1140,7 +1171,7 @@ extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act
     int num_sms = 0;
     if (int st = check_device(&num_sms)) return st;
     ScanArgs a = scan_args(s);
-    if (s->T > 0) a.y = strided(*y, s->dtype);
+    if (s->T > 0) a.y = strided(*y, s);
     a.saved = saved, a.h_in = h0, a.h_out = hT;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     auto run = [&](auto shape, auto cl) { return launch_fwd<decltype(shape), decltype(cl)::value>(a, s->B, num_sms, cs); };
@@ -1178,8 +1209,8 @@ extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_
     g.s = scan_args(s);
     g.s.saved = const_cast<float*>(saved), g.s.h_in = dhT, g.s.h_out = dh0;
     if (s->T > 0) {
-        g.s.y = strided(*dy, s->dtype);
-        g.df = strided(*df, s->dtype), g.dv = strided(*dv, s->dtype), g.dr = strided(*dr, s->dtype);
+        g.s.y = strided(*dy, s);
+        g.df = strided(*df, s), g.dv = strided(*dv, s), g.dr = strided(*dr, s);
     }
     g.partial = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -321,3 +321,38 @@ def test_scan_refusals(cuda_lib):
     assert e.value.status == bl.TERN_ERR_WORKSPACE
     with pytest.raises(ValueError):
         bl.tern_scan_step(c.f, c.v, c.r, c.h0, c.y)
+
+
+class Guarded(Case):
+    """Rows that start `off` elements past an aligned address and lie `pad` apart, NaN around them."""
+
+    @staticmethod
+    def place(x, layout):
+        off, pad = layout
+        B, T, D = x.shape
+        buf = torch.full((B * T * (D + pad) + 16,), float("nan"), dtype=x.dtype, device="cuda")
+        view = buf.as_strided((B, T, D), (T * (D + pad), D + pad, 1), off)
+        view.copy_(x)
+        return view
+
+    def outside(self):
+        """The elements around the outputs that a call wrote."""
+        n = 0
+        for t in (self.y, self.df, self.dv, self.dr):
+            whole = torch.empty(0, dtype=t.dtype, device="cuda").set_(t.untyped_storage())
+            n += int((~whole.isnan()).sum()) - t.numel()
+        return n
+
+
+@pytest.mark.parametrize("B,T,D", [(2, 130, 33), (3, 70, 34), (1, 600, 36), (320, 64, 35), (1, 2500, 71)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_scan_rows_at_every_address(cuda_lib, B, T, D, dtype):
+    """Whatever words the rows' addresses allow: right, the same bits, and nothing else read or written."""
+    first = None
+    for off, pad in ((0, 0), (1, 0), (2, 0), (3, 1), (5, 2), (0, 1), (4, 4)):
+        case = Guarded(cuda_lib, B, T, D, dtype, seed=D, layout=(off, pad)).run()
+        if first is None:
+            first = case.check().outputs()
+        for name, got in case.outputs().items():
+            assert torch.equal(got, first[name]), (name, off, pad)
+        assert case.outside() == 0, (off, pad)
