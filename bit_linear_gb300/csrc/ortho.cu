@@ -674,22 +674,35 @@ int ortho_gemm(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, 
     return TERN_OK;
 }
 
-// The largest tile of which there are enough for three quarters of the GPU, else the smallest.
+// The tile by the time that its rounds take.  A k-block takes 1.1 us in a 256 x 256 tile of a pair, 0.6
+// in a 128 x 128 tile and 0.45 in a 128 x 64 one, but 0.95 and 0.65 where every SM has one, which then
+// share what L2 delivers; the last tile's stores take 5, 3 and 1.5 us.  (2500 x 2500: the symmetric
+// products in 55 large tiles, one round, or 210 of 128 x 128, two: 1035 and 1248 us; 1500 x 4000: in 78
+// of 128 x 128 or 156 of 128 x 64: 570 and 761 us; 2049 x 2049: the products of X in 81 large tiles or
+// 289: 845 and 799 us; 2048 x 2048: in 64 or 256: 509 and 525 us; 512 x 2048: in 64 of 128 x 128 or 128
+// of 128 x 64: 159 and 143 us.)
 template <bool A_MN, bool B_MN>
 int ortho_product(OrthoArgs& a, const Operand& A, const Operand& B, int64_t depth, int num_sms, cudaStream_t s) {
     const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
     auto tiles = [&](int64_t tm, int64_t tn) {
-        const int64_t n = ((a.rows + tm - 1) / tm) * ((a.ld + tn - 1) / tn);
-        return sym ? n / 2 : n;
+        const int64_t m = (a.rows + tm - 1) / tm, n = (a.ld + tn - 1) / tn;
+        return m * n - (sym ? m * (m - 1) / 2 * (tm / tn) : 0);
     };
-    if (tiles(256, 256) * 8 >= 3 * num_sms) return ortho_gemm<OCfg<2, 256, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
-    if (tiles(128, 128) * 4 >= 3 * num_sms) return ortho_gemm<OCfg<1, 128, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
     // Few tiles: clusters of S CTAs share each one's contraction, at least a k-block a CTA.  Clusters of
     // 8, 4 and 2 CTAs of this size fit 16, 36 and 76 times.  (512 x 2048: 174 us without, 142 us; 256 x
     // 1024: 111 us with at least two k-blocks a CTA, 105 us.)
-    const int64_t n = tiles(128, 64) + (sym ? (a.rows + 127) / 128 : 0), kb = (depth + kBK - 1) / kBK;
+    const int64_t n = tiles(128, 64), kb = (depth + kBK - 1) / kBK;
     const int S = n <= 16 && kb >= 8 ? 8 : n <= 36 && kb >= 4 ? 4 : n <= 76 && kb >= 2 ? 2 : 1;
     if (S > 1) return ortho_gemm<OCfg<1, 64, A_MN, B_MN, true>>(a, A, B, depth, num_sms, s, S);
+    auto time = [&](int64_t n, int64_t at_once, int64_t full, int64_t least, int64_t stores) {   // in 10 ns
+        const int64_t rest = n % at_once;
+        return kb * (n / at_once * full + (rest != 0 ? std::max(least, full * rest / at_once) : 0)) + stores;
+    };
+    const int64_t large = time(tiles(256, 256), num_sms / 2, 110, 110, 500);
+    const int64_t middle = time(tiles(128, 128), num_sms, 95, 60, 300);
+    const int64_t small = time(n, num_sms, 65, 45, 150);
+    if (large <= middle && large <= small) return ortho_gemm<OCfg<2, 256, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
+    if (middle <= small) return ortho_gemm<OCfg<1, 128, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
     return ortho_gemm<OCfg<1, 64, A_MN, B_MN>>(a, A, B, depth, num_sms, s);
 }
 
