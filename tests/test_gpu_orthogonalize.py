@@ -75,6 +75,27 @@ def test_orthogonalize_steps(cuda_lib, steps):
     _check(_run(cuda_lib, G, steps=steps), _reference(G, steps=steps), steps=steps)
 
 
+@pytest.mark.parametrize("K,N", [(130, 8300), (8300, 130), (260, 4400), (1025, 2100), (900, 1300)])
+@pytest.mark.parametrize("steps", [1, 2, 5])
+def test_orthogonalize_long_sides(cuda_lib, K, N, steps):
+    """Both sides of the rule by which steps are taken two at a time, whole pairs and a last single one."""
+    G = _gradient(K, N, seed=K + steps)
+    _check(_run(cuda_lib, G, steps=steps), _reference(G, steps=steps), steps=steps)
+    assert cuda_lib.tern_device_status() == cuda_lib.TERN_OK
+
+
+@pytest.mark.parametrize("N", [4500, 700])
+def test_orthogonalize_keeps_weak_directions_of_long_sides(cuda_lib, N):
+    """As below, with steps two at a time and one at a time."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    U = torch.linalg.qr(torch.randn(256, 256, device="cuda", generator=g, dtype=torch.float64))[0]
+    V = torch.linalg.qr(torch.randn(N, 256, device="cuda", generator=g, dtype=torch.float64))[0]
+    G = ((U * torch.logspace(0, -3, 256, device="cuda", dtype=torch.float64)) @ V.T).float()
+    out, ref = _run(cuda_lib, G), _reference(G)
+    _check(out, ref)
+    assert (U[:, -64:].T @ (out.double() - ref)).norm() <= 2.0 ** -8 * ref.norm()
+
+
 def test_orthogonalize_keeps_weak_directions(cuda_lib):
     """Singular values from 1 down to 1e-3 of the largest: the weak ones keep their directions."""
     g = torch.Generator(device="cuda").manual_seed(4)
