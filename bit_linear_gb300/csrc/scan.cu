@@ -420,20 +420,46 @@ __device__ __forceinline__ void copy_step(const CUtensorMap* maps, uint32_t stag
             "l"(reinterpret_cast<uint64_t>(maps + t)), "r"(ch0), "r"(static_cast<int>(step * C::ROWS)), "r"(b), "r"(bar)
             : "memory");
 }
-// Within a warp: (PA, PH) = the map of the segments before this one (after it, for REV), from
-// each segment's (A, H).
-template <class C, bool REV>
-__device__ __forceinline__ void warp_prefix(const F2 (&A)[C::NP], const F2 (&H)[C::NP], F2 (&PA)[C::NP], F2 (&PH)[C::NP],
-                                            int seg, int c, bool docs) {
+// Within a warp, in log2(SEGS) exchanges: (PA, PH) = the map of the segments before this one, (A, H) that
+// of all of them; and for the gradient (QA, QG) = the map, run backwards, of the segments after it, (A, G)
+// that of all of them.  A, H and G come as the segment's own.
+template <class C, bool GRAD>
+__device__ __forceinline__ void warp_prefix(F2 (&A)[C::NP], F2 (&H)[C::NP], F2 (&G)[C::NP], F2 (&PA)[C::NP], F2 (&PH)[C::NP],
+                                            F2 (&QA)[C::NP], F2 (&QG)[C::NP], int seg, int lane, bool docs) {
 #pragma unroll
-    for (int j = 0; j < C::NP; ++j) PA[j] = both(1.0f), PH[j] = both(0.0f);
+    for (int j = 0; j < C::NP; ++j) {
+        PA[j] = both(1.0f), PH[j] = both(0.0f);
+        if constexpr (GRAD) QA[j] = both(1.0f), QG[j] = both(0.0f);
 #pragma unroll
-    for (int k = 0; k < C::SEGS - 1; ++k) {
-        const int from = REV ? C::SEGS - 1 - k : k;
-#pragma unroll
-        for (int j = 0; j < C::NP; ++j) {
-            const F2 Ak = shfl2(A[j], from * C::LPR + c), Hk = shfl2(H[j], from * C::LPR + c);
-            if (REV ? seg < from : seg > from) compose(Ak, Hk, PA[j], PH[j], docs);
+        for (int d = 1; d < C::SEGS; d <<= 1) {
+            const bool later = (seg & d) != 0;
+            const int from = lane ^ (d * C::LPR);
+            const F2 A2 = shfl2(A[j], from), H2 = shfl2(H[j], from);
+            if constexpr (GRAD) {
+                const F2 G2 = shfl2(G[j], from);
+                if (later) {
+                    F2 a = A[j], g = G[j];
+                    compose(A2, G2, a, g, docs);   // backwards this half runs first
+                    G[j] = g;
+                } else {
+                    F2 a = A2, g = G2;
+                    compose(QA[j], QG[j], a, g, docs);
+                    QA[j] = a, QG[j] = g;
+                    a = A2, g = G2;
+                    compose(A[j], G[j], a, g, docs);
+                    G[j] = g;
+                }
+            }
+            if (later) {
+                F2 a = A2, h = H2;
+                compose(PA[j], PH[j], a, h, docs);
+                PA[j] = a, PH[j] = h;
+                a = A2, h = H2;
+                compose(A[j], H[j], a, h, docs);
+                A[j] = a, H[j] = h;
+            } else {
+                compose(A2, H2, A[j], H[j], docs);
+            }
         }
     }
 }
@@ -702,16 +728,10 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
         if (plain) fwd_rows<C, true>(in, lb, nl, cut, ga, gb, A, H);
         else fwd_rows<C, false>(in, lb, nl, cut, ga, gb, A, H);
         F2 PA[NP], PH[NP];
-        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, !plain);
+        warp_prefix<C, false>(A, H, H, PA, PH, PA, PH, q.seg, q.lane, !plain);
         if (q.seg == C::SEGS - 1) {
-            F2 TA[NP], TH[NP];
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                TA[j] = PA[j], TH[j] = PH[j];
-                compose(A[j], H[j], TA[j], TH[j], !plain);
-            }
-            put_s(&aggA[p][q.w][q.ch], TA);
-            put_s(&aggH[p][q.w][q.ch], TH);
+            put_s(&aggA[p][q.w][q.ch], A);
+            put_s(&aggH[p][q.w][q.ch], H);
         }
         const bool cuts_here = sync_cuts(docs, cut);
         if constexpr (C::X::WIDE) {   // everyone has left the step before: its stage takes the step STAGES later
@@ -850,27 +870,15 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
         if (plain) bwd_rows<C, true>(in, lb, nl, cut, s, n, o, x, A, H, G);
         else bwd_rows<C, false>(in, lb, nl, cut, s, n, o, x, A, H, G);
         F2 PA[NP], PH[NP], QA[NP], QG[NP];
-        warp_prefix<C, false>(A, H, PA, PH, q.seg, q.c, !plain);
-        warp_prefix<C, true>(A, G, QA, QG, q.seg, q.c, !plain);
-        if (q.seg == C::SEGS - 1) {
-            F2 TA[NP], TH[NP];
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                TA[j] = PA[j], TH[j] = PH[j];
-                compose(A[j], H[j], TA[j], TH[j], !plain);
-            }
-            put_s(&aggA[p][q.w][q.ch], TA);
-            put_s(&aggH[p][q.w][q.ch], TH);
-        }
+        warp_prefix<C, true>(A, H, G, PA, PH, QA, QG, q.seg, q.lane, !plain);
         if (q.seg == 0) {
-            F2 TG[NP];
-#pragma unroll
-            for (int j = 0; j < NP; ++j) TG[j] = apply(A[j], G[j], QG[j], !plain);
-            put_s(&aggG[p][q.w][q.ch], TG);
+            put_s(&aggA[p][q.w][q.ch], A);
+            put_s(&aggH[p][q.w][q.ch], H);
+            put_s(&aggG[p][q.w][q.ch], G);
         }
         const bool cuts_here = sync_cuts(docs, cut);
         if constexpr (C::X::WIDE) {   // everyone has left the step before: its stage takes the step STAGES later
-            if (threadIdx.x == 0 && it > 0) copy(it - 1 + C::STAGES);
+            if (threadIdx.x == (WARPS - 1) * 32 && it > 0) copy(it - 1 + C::STAGES);   // warp 0 has the totals to send
         }
         F2 e[NP];   // e after this segment's rows
         if constexpr (CL) {
