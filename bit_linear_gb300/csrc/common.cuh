@@ -68,14 +68,15 @@ int launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cud
 }
 
 // The same in clusters of `cluster` blocks along x (above eight a size that not every part offers),
-// with `smem` bytes of dynamic shared memory.
+// with `smem` bytes of dynamic shared memory; `early` is launch_pdl's way, otherwise the launch waits
+// for the kernels before it to end.
 template <class... KArgs, class... Args>
-int launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t s,
-                   Args&&... args) {
+int launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster, bool early,
+                   cudaStream_t s, Args&&... args) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;

@@ -702,7 +702,7 @@ int launch_sort(const ClusterSortArgs& c, int digits, cudaStream_t s) {
     const int64_t tile = WARPS * 32 * R;
     unsigned P = 1;
     while (P * tile < c.s.n) P *= 2;
-    return launch_cluster(tern_embed_sort_kernel<WARPS, R>, P, WARPS * 32, digits * (8 + 2 * WARPS), P, s, c);
+    return launch_cluster(tern_embed_sort_kernel<WARPS, R>, P, WARPS * 32, digits * (8 + 2 * WARPS), P, true, s, c);
 }
 
 bool bad_sizes(int64_t n, int64_t V, int64_t D) {

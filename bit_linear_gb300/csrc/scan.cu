@@ -703,8 +703,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
         // not at entry: blocks of the next kernel that wait in the free slots meanwhile would be its
-        // share of some SMs and not of others (a long document: 119 us back to back, 96 us alone)
-        if (it + 1 == iters) ptx::pdl_trigger();
+        // share of some SMs and not of others
+        if (!CL && it + 1 == iters) ptx::pdl_trigger();
         const int64_t first = step_of(it) * ROWS + q.w * C::WROWS + q.seg * RPT;
         const int row0 = first < a.T ? static_cast<int>(first) : a.T;
         const int nl = min(max(len - row0, 0), RPT);   // live rows of this segment
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
     for (int j = 0; j < NP; ++j) lb[j] = mul2(lb[j], both(-kLog2e)), dbias[j] = both(0.0f);
     for (int it = 0; it < iters; ++it) {
         const int p = it & 1;
-        if (it + 1 == iters) ptx::pdl_trigger();
+        if (!CL && it + 1 == iters) ptx::pdl_trigger();
         const int64_t step = step_of(it);   // below 0: nothing left for this block
         const int64_t first = step * ROWS + q.w * C::WROWS + q.seg * RPT;
         const int row0 = step >= 0 && first < a.T ? static_cast<int>(first) : a.T;
@@ -956,7 +956,6 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
 __global__ void __launch_bounds__(256) tern_scan_dbias_kernel(const float* __restrict__ partial, int64_t parts, int D,
                                                               float* __restrict__ dbias) {
     __shared__ float red[8][32];
-    ptx::pdl_trigger();
     ptx::pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int d = blockIdx.x * 32 + lane;
@@ -1073,6 +1072,13 @@ int input_map(CUtensorMap* m, const Strided& x, int64_t B, int64_t T, int64_t D)
     return tensor_map_3d(m, x.p, type, D, T, B, T > 1 ? x.st : least, B > 1 ? x.sb : least, C::CH, C::ROWS);
 }
 
+// Clusters of more than two steps each are launched once the kernels before them have ended, and none let
+// the next kernel in before their own end: clusters that take the slots which happen to be free until then
+// leave the others an uneven share of the SMs for all of their run (the gradient of 1 x 65536 x 512 306 us
+// behind a small kernel that let it in early, 205 us so).  A short run would lose more by the later launch
+// (the gradient of 1 x 512 x 512: 8.0 us, 10.7 us).
+bool short_run(int64_t steps, int S) { return steps <= 2 * S; }
+
 template <class C, bool CL>
 int launch_fwd(const ScanArgs& a0, int64_t B, int num_sms, cudaStream_t s) {
     ScanArgs a = a0;
@@ -1088,9 +1094,9 @@ int launch_fwd(const ScanArgs& a0, int64_t B, int num_sms, cudaStream_t s) {
     }
     constexpr size_t smem = Inputs<C, 3>::SMEM;
     if constexpr (CL) {
-        if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, smem, a.S, s, a);
+        if (a.S > 1) return launch_cluster(tern_scan_fwd_kernel<C, true>, grid, C::WARPS * 32, smem, a.S, short_run(steps_of(a.T, C::ROWS), a.S), s, a);
     }
-    return launch_cluster(tern_scan_fwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, s, a);
+    return launch_cluster(tern_scan_fwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, true, s, a);
 }
 
 template <class C, bool CL>
@@ -1109,10 +1115,11 @@ int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStr
     constexpr size_t smem = Inputs<C, 4>::SMEM;
     int st = TERN_OK;
     if constexpr (CL) {
-        st = g.s.S > 1 ? launch_cluster(tern_scan_bwd_kernel<C, true>, grid, C::WARPS * 32, smem, g.s.S, s, g)
-                       : launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, s, g);
+        st = g.s.S > 1 ? launch_cluster(tern_scan_bwd_kernel<C, true>, grid, C::WARPS * 32, smem, g.s.S,
+                                        short_run(steps_of(g.s.T, C::ROWS), g.s.S), s, g)
+                       : launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, true, s, g);
     } else {
-        st = launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, s, g);
+        st = launch_cluster(tern_scan_bwd_kernel<C, false>, grid, C::WARPS * 32, smem, 1, true, s, g);
     }
     if (st != TERN_OK) return st;
     if (dbias == nullptr) return TERN_OK;
