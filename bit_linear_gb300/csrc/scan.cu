@@ -287,9 +287,10 @@ struct Shape {
 };
 
 // Totals of the S blocks of a cluster, pushed by each block into every block's shared memory
-// (st.async) and counted there on an mbarrier: two of each in turn.  A block sends those of
-// iteration i+1 only after all its warps have read those of i, and i+2 needs everyone's i+1, so a
-// buffer is read before it is written again.
+// (st.async) and counted there on an mbarrier: two of each in turn.  One warp sends, waits and folds
+// (all of them reading the same totals would take the shared memory's bandwidth) and hands the state
+// before the block's rows to the others.  It sends the totals of iteration i+1 only after it has read
+// those of i, and i+2 needs everyone's i+1, so a buffer is read before it is written again.
 template <class C>
 struct Exchange {
     alignas(16) float A[2][kMaxCluster][C::CH], H[2][kMaxCluster][C::CH];
@@ -481,6 +482,7 @@ __device__ __forceinline__ void put_s(float* p, const F2 (&x)[NP]) {
 // h := the maps at A, H (rows `stride` floats apart) k0, k0 + dk, ... up to but without k1, after h
 template <int NP>
 __device__ __forceinline__ void fold(const float* A, const float* H, int stride, int k0, int k1, int dk, F2 (&h)[NP], bool docs) {
+#pragma unroll 4
     for (int k = k0; k != k1; k += dk) {
         F2 Ak[NP], Hk[NP];
         get_s(A + k * stride, Ak);
@@ -493,6 +495,7 @@ __device__ __forceinline__ void fold(const float* A, const float* H, int stride,
 template <int NP>
 __device__ __forceinline__ void fold_map(const float* A, const float* H, int stride, int k0, int k1, int dk, F2 (&PA)[NP],
                                          F2 (&PH)[NP], bool docs) {
+#pragma unroll
     for (int k = k0; k != k1; k += dk) {
         F2 Ak[NP], Hk[NP];
         get_s(A + k * stride, Ak);
@@ -656,11 +659,12 @@ template <class C, bool CL>
 __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
     using X = typename C::X;
     constexpr int NP = C::NP, RPT = C::RPT, WARPS = C::WARPS, ROWS = C::ROWS;
+    constexpr int LEAD = WARPS - 1;   // the warp that exchanges totals with the cluster's other blocks
     static_assert(kSaveRows % RPT == 0, "saved states fall on segment boundaries");
     extern __shared__ __align__(128) char smem[];
     __shared__ uint64_t full[C::STAGES];
     __shared__ alignas(16) float aggA[2][WARPS][C::CH], aggH[2][WARPS][C::CH];
-    __shared__ alignas(16) float carry_s[2][C::CH];                // not CL: the state after a step
+    __shared__ alignas(16) float carry_s[2][C::CH];                // the state after a step (CL: before the block's)
     __shared__ typename std::conditional<CL, Exchange<C>, int>::type ex;
     const Place<C> q(a);
     if constexpr (C::X::WIDE) {
@@ -741,7 +745,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
         F2 h[NP];
         if constexpr (CL) {
             if (it == 0) cluster_wait();   // every peer has set up its barriers
-            if (q.w == WARPS - 1) {   // the block's total, to every block: a segment's lanes each serve S / SEGS of them
+            if (q.w == LEAD) {   // the block's total, to every block: a segment's lanes each serve S / SEGS of them
 #pragma unroll
                 for (int j = 0; j < NP; ++j) A[j] = both(1.0f), H[j] = both(0.0f);
                 fold_map(&aggA[p][0][q.ch], &aggH[p][0][q.ch], C::CH, 0, WARPS, 1, A, H, cuts_here);
@@ -749,14 +753,13 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
                     push_pairs(&ex.A[p][q.rank][q.ch], A, &ex.bar[p], k);
                     push_pairs(&ex.H[p][q.rank][q.ch], H, &ex.bar[p], k);
                 }
+                ok = ok && wait_phase(&ex.bar[p], (it >> 1) & 1);
+                fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, carry, docs);
+                if (q.seg == 0) put_s(&carry_s[p][q.ch], carry);
             }
-            ok = ok && wait_phase(&ex.bar[p], (it >> 1) & 1);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) h[j] = carry[j];
-            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, h, docs);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) carry[j] = h[j];
-            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, q.rank, a.S, 1, carry, docs);
+            __syncthreads();
+            if (q.w == LEAD) fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, q.rank, a.S, 1, carry, docs);
+            get_s(&carry_s[p][q.ch], h);
         } else {
 #pragma unroll
             for (int j = 0; j < NP; ++j) h[j] = carry[j];
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
         __syncthreads();
         if (iters > 0) get_s(&carry_s[(iters - 1) & 1][q.ch], carry);
     }
-    if (a.h_out != nullptr && q.on && q.rank == 0 && q.w == 0 && q.seg == 0)
+    if (a.h_out != nullptr && q.on && q.rank == 0 && q.w == (CL ? LEAD : 0) && q.seg == 0)
         store_f32(a.h_out + q.b * a.D + q.d, q.nch, carry);
 }
 
@@ -793,6 +796,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
     using X = typename C::X;
     constexpr int NP = C::NP, RPT = C::RPT, WARPS = C::WARPS, ROWS = C::ROWS;
     constexpr int GROUP = kSaveRows / C::WROWS;   // warps from one saved state to the next
+    constexpr int LEAD = 0;   // the warp that exchanges totals with the cluster's other blocks
     static_assert(ROWS % kSaveRows == 0 && kSaveRows % C::WROWS == 0, "steps start from saved states");
     const ScanArgs& a = g.s;
     extern __shared__ __align__(128) char smem[];
@@ -883,7 +887,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
         F2 e[NP];   // e after this segment's rows
         if constexpr (CL) {
             if (it == 0) cluster_wait();   // every peer has set up its barriers
-            if (q.w == 0) {
+            if (q.w == LEAD) {
 #pragma unroll
                 for (int j = 0; j < NP; ++j) A[j] = both(1.0f), G[j] = both(0.0f);
                 fold_map(&aggA[p][0][q.ch], &aggG[p][0][q.ch], C::CH, WARPS - 1, -1, -1, A, G, cuts_here);
@@ -891,14 +895,13 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
                     push_pairs(&ex.A[p][q.rank][q.ch], A, &ex.bar[p], k);
                     push_pairs(&ex.H[p][q.rank][q.ch], G, &ex.bar[p], k);
                 }
+                ok = ok && wait_phase(&ex.bar[p], (it >> 1) & 1);
+                fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, carry, docs);
+                if (q.seg == 0) put_s(&carry_s[p][q.ch], carry);
             }
-            ok = ok && wait_phase(&ex.bar[p], (it >> 1) & 1);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) e[j] = carry[j];
-            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, 0, q.rank, 1, e, docs);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) carry[j] = e[j];
-            fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, q.rank, a.S, 1, carry, docs);
+            __syncthreads();
+            if (q.w == LEAD) fold(&ex.A[p][0][q.ch], &ex.H[p][0][q.ch], C::CH, q.rank, a.S, 1, carry, docs);
+            get_s(&carry_s[p][q.ch], e);
         } else {
 #pragma unroll
             for (int j = 0; j < NP; ++j) e[j] = carry[j];
