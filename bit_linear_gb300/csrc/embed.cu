@@ -5,7 +5,6 @@
 //
 // Forward: HBM-bound gather; a thread moves eight channels of a row (16-byte loads and stores, shifted
 // into place where rows start at odd addresses).
-// With more rows than fit the GPU at once, blocks loop over them.
 //
 // Gradient: the positions are sorted by token (stable radix sort, hand-written here) and each
 // token's rows are then summed in the order of their positions, so no atomic adds in floating
@@ -130,9 +129,10 @@ __device__ __forceinline__ void load8_any(const float* p, const void* table, con
 
 // Eight channels per thread by 16-byte accesses: WIDE, rows start on such boundaries; otherwise the
 // output's boundaries are taken and the table's words realigned to them (100000 rows of 513: 49 us, by
-// single elements 94).  tx threads (a power of two) share a row.  MANY: a block has several rows, and reads a row's token before the row in hand is
-// done (65536 x 1024: 50 us, 68 us with a block for every four rows; one row each is 0.4 us faster
-// where the grid is small enough for it).
+// single elements 94).  tx threads (a power of two) share a row.  MANY: a block has several rows, and
+// reads a row's token before the row in hand is done.  It is for grids larger than the GPU holds, of rows
+// that are one chunk per thread (65536 x 1024: 40 us, 52 us with a block for every four rows; 32768 x 4096
+// in bf16, two chunks: 70 and 67 us; odd widths gain nothing; small grids lose 0.4 us).
 template <class TOK, class TAB, bool WIDE, bool MANY>
 __global__ void __launch_bounds__(256) tern_embed_fwd_kernel(const __grid_constant__ EmbedArgs a, int tx) {
     ptx::pdl_trigger();
@@ -717,10 +717,10 @@ int launch_embed(const EmbedArgs& a, int num_sms, cudaStream_t s) {
     int tx = wide ? 8 : 16;                       // threads per row
     while (tx < 256 && tx < items) tx *= 2;
     const int64_t blocks = (a.n + 256 / tx - 1) / (256 / tx);
-    const bool many = blocks > 16ll * num_sms;
-    void (*const kernel)(EmbedArgs, int) =
-        many ? (wide ? tern_embed_fwd_kernel<TOK, TAB, true, true> : tern_embed_fwd_kernel<TOK, TAB, false, true>)
-             : (wide ? tern_embed_fwd_kernel<TOK, TAB, true, false> : tern_embed_fwd_kernel<TOK, TAB, false, false>);
+    const bool many = wide && items <= 256 && blocks > 16ll * num_sms;
+    void (*const kernel)(EmbedArgs, int) = many   ? tern_embed_fwd_kernel<TOK, TAB, true, true>
+                                           : wide ? tern_embed_fwd_kernel<TOK, TAB, true, false>
+                                                  : tern_embed_fwd_kernel<TOK, TAB, false, false>;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(many ? 16ll * num_sms : blocks)), dim3(256), 0, s, a, tx);
 }
 
