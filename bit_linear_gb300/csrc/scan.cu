@@ -1055,12 +1055,18 @@ int check_scan(const tern_scan* s, int& align) {
     return TERN_OK;
 }
 
+// Clusters of 16 that are resident at once: a part of the GPU with an odd block over holds none more.
+template <class C>
+constexpr int fit16() { return C::WARPS == 8 ? 14 : 33; }
+
 // Blocks per cluster: the largest power of two, at most kMaxCluster and less than twice the steps,
 // with which the blocks are all resident at once.
 template <class C>
 int cluster_size(int64_t blocks, int64_t steps, int num_sms) {
     int S = 1;
-    while (S < kMaxCluster && S < steps && 2 * S * blocks <= static_cast<int64_t>(C::MINB) * num_sms) S *= 2;
+    while (S < kMaxCluster && S < steps && 2 * S * blocks <= static_cast<int64_t>(C::MINB) * num_sms &&
+           (2 * S < kMaxCluster || blocks <= fit16<C>()))
+        S *= 2;
     return S;
 }
 
@@ -1132,10 +1138,10 @@ int launch_bwd(const GradArgs& g0, int64_t B, int num_sms, float* dbias, cudaStr
 
 // The shape of the blocks, by how many there are of 64 bytes of channels by a whole sequence: enough
 // for more than two of four warps on each SM; else blocks of eight warps, in clusters where even
-// those leave SMs free; and tiles of half the channels where clusters of 16 still fill less than
-// half the GPU.  (Forward and gradient of 16 x 512 x 512: 13.6 + 22.8 us as clusters of four-warp
-// blocks, 12.2 + 19.8 us as eight-warp blocks; of 8 x 2048 x 2048: 59 + 125 us with four warps,
-// 67 + 134 us with eight; forward of 1 x 65536 x 512: 88 us in the narrow tiles, 122 us in wide ones.)
+// those leave SMs free; and tiles of half the channels where clusters of 16 such blocks are enough.
+// (Forward and gradient of 16 x 512 x 512: 15.5 + 24.8 us as clusters of four-warp blocks, 8.8 + 18.1 us
+// as eight-warp blocks; of 8 x 2048 x 2048: 53 + 118 us with four warps, 58 + 124 us with eight; of 1 x
+// 65536 x 512: 82 + 186 us in the narrow tiles, 134 + 295 us in wide ones.)
 template <class T, int W, int RPT, class F>
 int with_shape(int64_t B, int64_t D, int64_t T_, int num_sms, F run) {
     using Four = Shape<T, W, 8, RPT, 4, 4, 2>;
@@ -1143,8 +1149,7 @@ int with_shape(int64_t B, int64_t D, int64_t T_, int num_sms, F run) {
     using Narrow = Shape<T, W, 4, RPT, 4, 4, 2>;
     const int64_t blocks = B * ((D + Four::CH - 1) / Four::CH);
     if (blocks > 2 * num_sms) return run(Four{}, std::false_type{});
-    const int S = cluster_size<Eight>(blocks, steps_of(T_, Eight::ROWS), num_sms);
-    if (S == kMaxCluster && blocks * S * 2 <= 4 * num_sms) return run(Narrow{}, std::true_type{});
+    if (2 * blocks <= fit16<Narrow>() && steps_of(T_, Eight::ROWS) > kMaxCluster / 2) return run(Narrow{}, std::true_type{});
     return run(Eight{}, std::true_type{});
 }
 
