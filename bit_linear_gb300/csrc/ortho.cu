@@ -16,9 +16,10 @@
 // |X| <= 1.21 is stored times 2^14, |A| <= 1.46 and |M| <= 3.45 times 2^13 (bounds of the quintic
 // on [0, 1] and its image), so a lo plane's smallest spacing is 2^-38 of 1.
 //
-// Two steps at once, for m (n - m) of a million and more: with M0 = p(A), the next step's A is M0 A M0 =
-// (M0 M0) A, as all of these commute, and X = (M1 M0) X, so the pair needs one product of X in place
-// of two: 3 m^2 n / 2 + 5 m^3 / 2 multiply-adds against 3 m^2 n + m^3.  More than two would pass the
+// Two steps at once, for m (n - m) of a million and more, or n of 1.5 m and m of 1024: with M0 =
+// p(A), the next step's A is M0 A M0 = (M0 M0) A, as all of these commute, and X = (M1 M0) X, so
+// the pair needs one product of X in place of two: 3 m^2 n / 2 + 5 m^3 / 2 multiply-adds against
+// 3 m^2 n + m^3.  More than two would pass the
 // square of the amplification on to A's rounding.  The weak directions stay sound: where the
 // eigenvalue of A is lost in A's rounding M is still a, and they are X's own.
 //
@@ -727,8 +728,9 @@ OrthoPlan ortho_plan(int64_t K, int64_t N) {
     // From about a million on the products of X that a pair of steps saves, m m (n - m) each, are worth
     // more than its additional product of the smaller side: 512 x 4096 180 us, in pairs 168; 256 x 12000
     // 200 and 175; 900 x 4000 311 and 273; 4096 x 5000 3358 and 3143; but 512 x 2048 142 and 143, 1000 x
-    // 1500 231 and 235, 2048 x 2048 508 and 534.
-    p.pairs = p.m * (std::max(K, N) - p.m) >= 1 << 20;
+    // 1500 231 and 235, 2048 x 2048 508 and 534, 3000 x 3180 1584 and 1672.  From 1024 rows on they are equal at
+    // n = 1.5 m (1024 x 1536: 215), which the workspace's size turns on too.
+    p.pairs = p.m * (std::max(K, N) - p.m) >= 1 << 20 || (p.m >= 1024 && 2 * std::max(K, N) >= 3 * p.m);
     p.bytes = p.x + 4 * p.x_plane;
     for (int i = 0; i < (p.pairs ? 4 : 2); ++i) p.mat[i] = p.bytes, p.bytes += 2 * p.m_plane;
     return p;
