@@ -248,10 +248,19 @@ __device__ __forceinline__ F2 apply(F2 A, F2 H, F2 h, bool docs) {
     const F2 x = fma2(A, h, H);
     return docs ? where_cut(A, H, x) : x;
 }
-// (A, H) := the map (A2, H2) after (A, H)
+// (A, H) := the map (A2, H2) after (A, H).  A NaN in A2 takes the sign that A carries; the gradient, whose
+// maps run backwards to the documents before, keeps NaN out of A for that (without_nan).
 __device__ __forceinline__ void compose(F2 A2, F2 H2, F2& A, F2& H, bool docs) {
     H = apply(A2, H2, H, docs);
     A = docs ? where_cut(A2, A2, mul2(A, A2)) : mul2(A, A2);
+}
+
+// A >= 0 with 0 in the place of a NaN.  A row whose gate is NaN has NaN in H and in G too, so A need not
+// carry it; as a factor it would undo the mark of a document start on an earlier row.
+__device__ __forceinline__ F2 without_nan(F2 A) {
+    float x, y;
+    split(A, x, y);
+    return pair(fmaxf(x, 0.0f), fmaxf(y, 0.0f));
 }
 
 struct Strided {
@@ -569,10 +578,16 @@ __device__ __forceinline__ void bwd_rows(const Inputs<C, 4>& in, const F2 (&lb)[
             gate(r[j], so, x[i][j]);
             o[i][j] = mul2(so, dy[j]);
             if (!PLAIN && i >= nl) s[i][j] = both(1.0f), n[i][j] = both(0.0f), o[i][j] = both(0.0f);
-            const F2 m = !PLAIN && ((cut >> i) & 1u) ? both(-0.0f) : s[i][j], b = mul2(n[i][j], v[j]);
+            const F2 b = mul2(n[i][j], v[j]);
+            F2 m = s[i][j];
+            if constexpr (!PLAIN) m = (cut >> i) & 1u ? both(-0.0f) : without_nan(m);
             if (i == 0) A[j] = m, H[j] = b;
             else compose(m, b, A[j], H[j], !PLAIN);
         }
+    }
+    if constexpr (PLAIN) {
+#pragma unroll
+        for (int j = 0; j < C::NP; ++j) A[j] = without_nan(A[j]);
     }
 #pragma unroll
     for (int i = C::RPT - 1; i >= 0; --i)
