@@ -19,7 +19,10 @@
 // with fp32 arithmetic, one in three with one binary16 plane), and |out - fp64| / |fp64| is there 1.6580e-3
 // where rounding alone gives 1.6561e-3.  Scales of powers of two keep both planes normal numbers:
 // |X| <= 1.21 is stored times 2^14, |A| <= 1.46 and |M| <= 3.45 times 2^13 (bounds of the quintic
-// on [0, 1] and its image), so a lo plane's smallest spacing is 2^-38 of 1.
+// on [0, 1] and its image), so a lo plane's smallest spacing is 2^-38 of 1.  Where |G|_F is below eps, X
+// starts below 1/2 and would lose its low bits there: it is stored times 2^k more, with the k that takes
+// its norm to between 1/2 and 1, and A times 2^2k.  A step multiplies by up to 3.4445, so k falls with the
+// steps to 0, where X has reached the rest of the quintic; the products' factors undo it (Factors).
 //
 // Two steps at once, for m (n - m) of a million and more, or n of 1.5 m and m of 1024: with M0 =
 // p(A), the next step's A is M0 A M0 = (M0 M0) A, as all of these commute, and X = (M1 M0) X, so
@@ -46,6 +49,7 @@
 // launch before it 2, the first copies 1.3, the k-blocks 0.45 each (operands at 87 B/ns into an SM),
 // the exchange and the stores 3.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include <cuda_bf16.h>
@@ -75,6 +79,8 @@ struct OrthoArgs {
     __half *oh, *ol;              // D's planes
     const __half *ch, *cl;        // OUT_POLY: A's planes
     float alpha, pa, pb;          // OUT_POLY: pa I + pb A + alpha acc; else alpha acc
+    const int* k_first;           // k of the first X
+    int k_in, k_out;              // steps' worth of k gone by: of what is read, and of D
     __nv_bfloat16* out;           // OUT_FINAL: [rows][cols]
 };
 
@@ -116,6 +122,22 @@ __device__ __forceinline__ void unit_tile(const OrthoArgs& a, int unit, int& mt,
     }
 }
 
+// The accumulator's factor and A's with the powers of two by which operands and D are stored.  OUT_FINAL,
+// which stores X itself, has its power in two halves (pb and post), numbers of their own where it is none.
+struct Factors {
+    float alpha, pb, post;
+};
+__device__ __forceinline__ Factors factors(const OrthoArgs& a) {
+    const int k0 = *a.k_first, k = max(k0 - a.k_in, 0), to = max(k0 - a.k_out, 0);
+    Factors f{a.alpha, a.kind == OUT_FINAL ? 1.0f : a.pb, 1.0f};
+    if (k == 0) return f;
+    if (a.kind == OUT_POLY) f.alpha = ldexpf(a.alpha, -4 * k), f.pb = ldexpf(a.pb, -2 * k);   // A A and A, of 2^2k each
+    if (a.kind == OUT_SYM) f.alpha = ldexpf(a.alpha, 2 * (to - k));                           // A's next (else k_in = k_out)
+    if (a.kind == OUT_X) f.alpha = ldexpf(a.alpha, to - k);
+    if (a.kind == OUT_FINAL) f.post = ldexpf(1.0f, -(k / 2)), f.pb = ldexpf(1.0f, -(k - k / 2));
+    return f;
+}
+
 __device__ __forceinline__ void split16(float v, __half& hi, __half& lo) {
     hi = __float2half_rn(v);
     lo = __float2half_rn(v - __half2float(hi));
@@ -151,7 +173,7 @@ __device__ __forceinline__ void group_load(const OrthoArgs& a, int row, int c, u
         l = *reinterpret_cast<const uint4*>(a.cl + static_cast<int64_t>(row) * a.ld + c);
     }
 }
-__device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&acc)[8], const uint4& h0, const uint4& l0, int row, int c,
+__device__ __forceinline__ void ortho_group(const OrthoArgs& a, const Factors& f, const float (&acc)[8], const uint4& h0, const uint4& l0, int row, int c,
                                             int lane) {
     const bool sym = a.kind == OUT_SYM || a.kind == OUT_POLY;
     const int row8 = row & ~7;
@@ -163,14 +185,14 @@ __device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&ac
             uint32_t u[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 t = __floats2bfloat162_rn(a.alpha * acc[2 * k], a.alpha * acc[2 * k + 1]);
+                const __nv_bfloat162 t = __floats2bfloat162_rn(f.alpha * acc[2 * k] * f.pb * f.post, f.alpha * acc[2 * k + 1] * f.pb * f.post);
                 u[k] = *reinterpret_cast<const uint32_t*>(&t);
             }
             *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (c + k < a.cols) o[k] = __float2bfloat16_rn(a.alpha * acc[k]);
+                if (c + k < a.cols) o[k] = __float2bfloat16_rn(f.alpha * acc[k] * f.pb * f.post);
         }
         return;
     }
@@ -183,11 +205,11 @@ __device__ __forceinline__ void ortho_group(const OrthoArgs& a, const float (&ac
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float x = __half2float(ah[k]) + __half2float(al[k]);
-            split16(fmaf(a.alpha, acc[k], a.pb * x) + (c + k == row ? a.pa : 0.0f), hi[k], lo[k]);
+            split16(fmaf(f.alpha, acc[k], f.pb * x) + (c + k == row ? a.pa : 0.0f), hi[k], lo[k]);
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split16(a.alpha * acc[k], hi[k], lo[k]);
+        for (int k = 0; k < 8; ++k) split16(f.alpha * acc[k], hi[k], lo[k]);
     }
     if (here) {
         *reinterpret_cast<uint4*>(a.oh + base) = *reinterpret_cast<const uint4*>(hi);
@@ -266,6 +288,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
     ptx::pdl_trigger();
     ptx::pdl_wait();
 
+    Factors f{};
+    if (warp >= 2) f = factors(a);
     uint32_t issued = 0, issued_parity = 0;   // producer: stages with a copy issued, and its phase
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -411,7 +435,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
                         for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[8 * g + k]);
                         uint4 ph, pl;
                         group_load(a, row0 + quad * 32 + lane, c0 + 8 * g, ph, pl);
-                        ortho_group(a, v, ph, pl, row0 + quad * 32 + lane, c0 + 8 * g, lane);
+                        ortho_group(a, f, v, ph, pl, row0 + quad * 32 + lane, c0 + 8 * g, lane);
                     }
                 }
             }
@@ -456,7 +480,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_ortho_gemm(const __grid_co
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] += x[k][i];
                 }
-                ortho_group(a, v, ph, pl, row, nt * C::BN + col, lane);
+                ortho_group(a, f, v, ph, pl, row, nt * C::BN + col, lane);
             }
         }
     }
@@ -540,11 +564,11 @@ __global__ void __launch_bounds__(256) tern_ortho_sumsq_kernel(const float* __re
     if (threadIdx.x == 0) partial[blockIdx.x] = red[0];
 }
 
-// X's planes from G: rows of ld columns, zeros past the last.  Every block adds up the partial
-// sums for itself, in the same order.
+// X's planes from G: rows of ld columns, zeros past the last; and X's k.  Every block adds up the
+// partial sums for itself, in the same order.
 __global__ void __launch_bounds__(256) tern_ortho_load_kernel(const float* __restrict__ G, int64_t rows, int cols, int ld,
                                                               const double* __restrict__ partial, int parts, float eps,
-                                                              __half* __restrict__ hi, __half* __restrict__ lo) {
+                                                              __half* __restrict__ hi, __half* __restrict__ lo, int* k_first) {
     __shared__ double red[256];
     ptx::pdl_trigger();
     ptx::pdl_wait();
@@ -556,7 +580,16 @@ __global__ void __launch_bounds__(256) tern_ortho_load_kernel(const float* __res
         if (threadIdx.x < k) red[threadIdx.x] += red[threadIdx.x + k];
         __syncthreads();
     }
-    const float inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(red[0]) + static_cast<double>(eps)));
+    const double norm = sqrt(red[0]), size = norm + static_cast<double>(eps);
+    double scale = static_cast<double>(kScaleX) / size;
+    int k = 0, over = 0;
+    if (size >= 2.0 * norm && norm > 0.0) {
+        k = ilogb(size / norm);   // |X| 2^k: above 1/2, at most 1
+        scale = ldexp(scale, k);
+        over = max(ilogb(scale) - 120, 0);   // of norms below 2^-106 the factor would pass fp32's range
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *k_first = k;
+    const float inv = static_cast<float>(over == 0 ? scale : ldexp(scale, -over)), more = ldexpf(1.0f, over);
     const int per_row = ld / 8;
     const bool wide = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(G) & 15u) == 0;
     const int64_t total = rows * per_row;
@@ -578,7 +611,7 @@ __global__ void __launch_bounds__(256) tern_ortho_load_kernel(const float* __res
         }
         __align__(16) __half h[8], l[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split16(v[k] * inv, h[k], l[k]);
+        for (int k = 0; k < 8; ++k) split16(v[k] * inv * more, h[k], l[k]);
         *reinterpret_cast<uint4*>(hi + row * ld + c) = *reinterpret_cast<const uint4*>(h);
         *reinterpret_cast<uint4*>(lo + row * ld + c) = *reinterpret_cast<const uint4*>(l);
     }
@@ -716,7 +749,7 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 struct OrthoPlan {
     int64_t m, ldx, ldm;                     // smaller side; elements between rows of X and of A, M
-    int64_t sums, x, mat[4], bytes;            // parts of the workspace, in bytes (x: two X of two planes; A, M and two more for pairs of steps)
+    int64_t sums, k, x, mat[4], bytes;         // parts of the workspace, in bytes (x: two X of two planes; A, M and two more for pairs of steps)
     int64_t x_plane, m_plane;                // bytes of one plane
     bool pairs;                              // steps two at a time
 };
@@ -729,7 +762,8 @@ OrthoPlan ortho_plan(int64_t K, int64_t N) {
     p.x_plane = round_up(K * p.ldx * 2, 256);
     p.m_plane = round_up(p.m * p.ldm * 2, 256);
     p.sums = 0;
-    p.x = round_up(kSumBlocks * static_cast<int64_t>(sizeof(double)), 256);
+    p.k = kSumBlocks * static_cast<int64_t>(sizeof(double));
+    p.x = round_up(p.k + static_cast<int64_t>(sizeof(int)), 256);
     // From about a million on the products of X that a pair of steps saves, m m (n - m) each, are worth
     // more than its additional product of the smaller side: 512 x 4096 180 us, in pairs 168; 256 x 12000
     // 200 and 175; 900 x 4000 311 and 273; 4096 x 5000 3358 and 3143; but 512 x 2048 142 and 143, 1000 x
@@ -775,6 +809,7 @@ extern "C" int tern_orthogonalize(const float* G, int64_t K, int64_t N, int step
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     double* sums = reinterpret_cast<double*>(ws + p.sums);
+    int* k_first = reinterpret_cast<int*>(ws + p.k);
     auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
     __half* x[2][2];
     for (int q = 0; q < 2; ++q)
@@ -784,23 +819,31 @@ extern "C" int tern_orthogonalize(const float* G, int64_t K, int64_t N, int step
     const int64_t chunks = K * (p.ldx / 8);
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, 8 * num_sms));
     if (int st = launch_pdl(tern_ortho_load_kernel, dim3(blocks), dim3(256), 0, s, G, K, static_cast<int>(N),
-                            static_cast<int>(p.ldx), static_cast<const double*>(sums), parts, eps, x[0][0], x[0][1]))
+                            static_cast<int>(p.ldx), static_cast<const double*>(sums), parts, eps, x[0][0], x[0][1], k_first))
         return st;
+    // that many steps' worth of k: X grows by up to 3.4445 in each
+    auto grown = [](int t) { return static_cast<int>(std::ceil(t * std::log2(static_cast<double>(kA)))); };
     const bool tall = K > N;
     Operand mat[4];   // symmetric, by commuting factors: A, M, and for pairs of steps M0 M0 then M1, and the second A
     for (int i = 0; i < (p.pairs ? 4 : 2); ++i) mat[i] = Operand{half(p.mat[i]), half(p.mat[i] + p.m_plane), p.ldm, p.m};
     auto to = [](OrthoArgs& a, const Operand& d) { a.oh = const_cast<__half*>(d.hi), a.ol = const_cast<__half*>(d.lo); };
-    // D = alpha L R, of which half the tiles are computed
-    auto product = [&](const Operand& L, const Operand& R, const Operand& D, float alpha) {
+    // Of a product that reads the t-th step's X or A, and whose D is the next-th's.
+    auto steps_args = [&](int t, int next) {
         OrthoArgs a{};
+        a.k_first = k_first, a.k_in = grown(t), a.k_out = grown(next);
+        return a;
+    };
+    // D = alpha L R, of which half the tiles are computed
+    auto product = [&](const Operand& L, const Operand& R, const Operand& D, float alpha, int t, int next) {
+        OrthoArgs a = steps_args(t, next);
         a.rows = static_cast<int>(p.m), a.cols = a.rows, a.ld = static_cast<int>(p.ldm);
         a.kind = OUT_SYM, a.alpha = alpha;
         to(a, D);
         return ortho_product<false, false>(a, L, R, p.ldm, num_sms, s);
     };
     // D = a I + b A + c A A
-    auto poly = [&](const Operand& A, const Operand& D) {
-        OrthoArgs a{};
+    auto poly = [&](const Operand& A, const Operand& D, int t) {
+        OrthoArgs a = steps_args(t, t);
         a.rows = static_cast<int>(p.m), a.cols = a.rows, a.ld = static_cast<int>(p.ldm);
         a.kind = OUT_POLY, a.ch = A.hi, a.cl = A.lo;
         a.alpha = kScaleM * kC / (kScaleA * kScaleA), a.pa = kScaleM * kA, a.pb = kScaleM * kB / kScaleA;
@@ -810,25 +853,26 @@ extern "C" int tern_orthogonalize(const float* G, int64_t K, int64_t N, int step
     int cur = 0;
     for (int t = 0; t < steps; cur ^= 1) {
         const Operand X{x[cur][0], x[cur][1], p.ldx, K};
-        OrthoArgs a{};
+        const int t0 = t;
+        OrthoArgs a = steps_args(t0, t0);
         a.rows = static_cast<int>(p.m), a.cols = a.rows, a.ld = static_cast<int>(p.ldm);
         a.kind = OUT_SYM, a.alpha = kScaleA / (kScaleX * kScaleX);
         to(a, mat[0]);
         if (int st = tall ? ortho_product<true, true>(a, X, X, K, num_sms, s) : ortho_product<false, false>(a, X, X, p.ldx, num_sms, s))
             return st;
-        if (int st = poly(mat[0], mat[1])) return st;
+        if (int st = poly(mat[0], mat[1], t0)) return st;
         Operand Q = mat[1];
         float q_scale = kScaleM;
         t += 1;
         if (p.pairs && t < steps) {
-            if (int st = product(mat[1], mat[1], mat[2], kScaleQ / (kScaleM * kScaleM))) return st;   // M0 M0
-            if (int st = product(mat[2], mat[0], mat[3], 1.0f / kScaleQ)) return st;                  // the second A
-            if (int st = poly(mat[3], mat[2])) return st;                                             // M1
-            if (int st = product(mat[2], mat[1], mat[0], kScaleQ / (kScaleM * kScaleM))) return st;   // M1 M0
+            if (int st = product(mat[1], mat[1], mat[2], kScaleQ / (kScaleM * kScaleM), t0, t0)) return st;   // M0 M0
+            if (int st = product(mat[2], mat[0], mat[3], 1.0f / kScaleQ, t0, t0 + 1)) return st;              // the second A
+            if (int st = poly(mat[3], mat[2], t0 + 1)) return st;                                             // M1
+            if (int st = product(mat[2], mat[1], mat[0], kScaleQ / (kScaleM * kScaleM), t0, t0)) return st;   // M1 M0
             Q = mat[0], q_scale = kScaleQ;
             t += 1;
         }
-        a = OrthoArgs{};
+        a = steps_args(t0, t);
         a.rows = static_cast<int>(K), a.cols = static_cast<int>(N), a.ld = static_cast<int>(p.ldx);
         a.kind = t == steps ? OUT_FINAL : OUT_X;
         a.oh = x[cur ^ 1][0], a.ol = x[cur ^ 1][1], a.out = reinterpret_cast<__nv_bfloat16*>(out);
