@@ -34,6 +34,7 @@
 // rows hid less.  Gates and states are fp32; outputs are rounded once.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include <cuda_bf16.h>
 
@@ -1049,6 +1050,22 @@ int check_act(const tern_act& x, const tern_scan* s, int& align) {
     if ((s->T > 1 && x.stride_t < s->D) || (s->B > 1 && x.stride_b == 0)) align = std::min(align, 4);   // overlapping rows
     return TERN_OK;
 }
+// Whether two rows of x share an element: blocks would write them in any order.
+bool rows_overlap(const tern_act& x, const tern_scan* s) {
+    int64_t n0 = s->B, s0 = x.stride_b, n1 = s->T, s1 = x.stride_t;
+    if (n0 == 1) n0 = n1, s0 = s1, n1 = 1;   // the stride of a size of one is not used
+    if (n1 > 1 && s0 > s1) std::swap(n0, n1), std::swap(s0, s1);
+    if (n0 > 1 && s0 < s->D) return true;
+    if (n0 <= 1 || n1 <= 1) return false;
+    const __int128 d = s->D, inner = static_cast<__int128>(n0 - 1) * s0;
+    if (s1 >= inner + d) return false;       // one sequence (or row of all sequences) after the other
+    // interleaved: some j s1 within a row of some i s0
+    for (int64_t j = 1; j < n1 && static_cast<__int128>(j) * s1 < inner + d; ++j) {
+        const __int128 at = static_cast<__int128>(j) * s1, i = at / s0;
+        if ((i < n0 && at - i * s0 < d) || (i + 1 < n0 && (i + 1) * s0 - at < d)) return true;
+    }
+    return false;
+}
 Strided strided(const tern_act& x, const tern_scan* s) {
     const int64_t es = static_cast<int64_t>(elem(s->dtype)), sb = x.stride_b * es, st = x.stride_t * es;
     char* p = static_cast<char*>(x.p);
@@ -1203,6 +1220,7 @@ extern "C" int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act
     if (s->T > 0) {
         if (y == nullptr) return TERN_ERR_ARG;
         if (int st = check_act(*y, s, align)) return st;
+        if (rows_overlap(*y, s)) return TERN_ERR_ARG;
     }
     if (!aligned4(h0) || !aligned4(hT) || !aligned4(saved)) return TERN_ERR_ALIGN;
     if (saved != nullptr && saved_bytes < tern_scan_saved(s->B, s->T, s->D)) return TERN_ERR_WORKSPACE;
@@ -1236,6 +1254,7 @@ extern "C" int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_
         for (const tern_act* x : {dy, df, dv, dr}) {
             if (x == nullptr) return TERN_ERR_ARG;
             if (int st = check_act(*x, s, align)) return st;
+            if (x != dy && rows_overlap(*x, s)) return TERN_ERR_ARG;
         }
     }
     if (!aligned4(saved) || !aligned4(dhT) || !aligned4(dbias) || !aligned4(dh0) || !aligned4(workspace)) return TERN_ERR_ALIGN;
@@ -1277,6 +1296,7 @@ extern "C" int tern_scan_step(const tern_scan* s, const float* h_in, float* h_ou
     if (s->B == 0 || s->D == 0) return TERN_OK;
     if (h_in == nullptr || h_out == nullptr || y == nullptr) return TERN_ERR_ARG;
     if (int st = check_act(*y, s, align)) return st;
+    if (rows_overlap(*y, s)) return TERN_ERR_ARG;
     if (!aligned4(h_in) || !aligned4(h_out)) return TERN_ERR_ALIGN;
     if (int st = check_device(nullptr)) return st;
     StepArgs a{};

@@ -408,7 +408,8 @@ int tern_embed_bwd(const void* tokens, int tokens_dtype, const void* dout, int64
                    void* stream);
 
 /* Activations [B][T][D] with D contiguous: element (b,t,d) at p[b*stride_b + t*stride_t + d],
- * strides in elements, >= 0.  Outputs must not overlap themselves or an input. */
+ * strides in elements, >= 0.  Outputs must not overlap an input or themselves (rows of one output
+ * that overlap are refused: TERN_ERR_ARG). */
 typedef struct tern_act {
     void* p;
     int64_t stride_b, stride_t;
