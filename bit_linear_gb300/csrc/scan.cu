@@ -3,7 +3,8 @@
 //   a_t = sigmoid(f_t + bias), h_t = a_t h_{t-1} + (1 - a_t) v_t, y_t = sigmoid(r_t) h_t
 //
 // per sequence b and channel d; h_{t-1} is read as 0 at a document start, and rows at or past
-// lengths[b] are padding (never read: a = 1, no input, y = 0, gradients 0).
+// lengths[b] are padding (a = 1, no input, y = 0, gradients 0; their values are never used, though
+// copies by TMA bring those of a sequence's last live step along).
 //
 // The map of one row, h -> a h + b, composes: rows i..j act as h -> A h + H with A = prod a and
 // H the state reached from 0.  A block takes a tile of channels and ROWS consecutive rows: a lane

@@ -422,8 +422,9 @@ typedef struct tern_act {
  *   y_t = sigmoid(r_t) h_t
  * f, v, r, y: `dtype` (TERN_BF16 or TERN_F32); gates and states are fp32, y is rounded once.
  *   f_bias   [D] fp32, or NULL (0)
- *   lengths  [B], or NULL (T): rows t >= lengths[b] are padding; they are not read, the state
- *            passes them unchanged, and y there is 0.  Values are clamped to 0..T.
+ *   lengths  [B], or NULL (T): rows t >= lengths[b] are padding: whatever they hold has no effect,
+ *            the state passes them unchanged, and y there is 0.  They must be readable memory all
+ *            the same (whole tiles of rows are copied).  Values are clamped to 0..T.
  *   starts   [B][T] bytes, or NULL: where nonzero (and not padding) a document starts: h_{t-1}
  *            is taken as 0, whatever it was.
  * B, T, D >= 0, B, T and D below 2^31 - 256.
@@ -447,7 +448,7 @@ int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act* y, float*
                   size_t saved_bytes, void* stream);
 /*
  * Gradient, from the same inputs and the forward's saved states.  dy and the outputs df, dv, dr
- * have s->dtype (0 is written in padding; dy is not read there); dhT [B][D] fp32 is the gradient
+ * have s->dtype (0 is written in padding, where dy has no effect, as above); dhT [B][D] fp32 is the gradient
  * of hT, or NULL (0); dh0 [B][D] fp32 and dbias [D] fp32 (the sum of df over sequences and rows,
  * before df is rounded) are written unless NULL.  dbias wants tern_scan_bwd_workspace() bytes
  * and B >= 1.  Sums run in a fixed order.
