@@ -362,6 +362,15 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
         }
     }
 }
+// The last of a thread whose wait gave up (none of the block's barriers follows: the others do not come
+// here).  Copies that are still on their way get time to land before the block leaves its shared memory.
+template <bool CL>
+__device__ __forceinline__ void leave_late() {
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t i = 0; i < (1u << 24) && ptx::globaltimer() - t0 < 100000ull; ++i) {
+    }
+    if constexpr (CL) cluster_leave();
+}
 
 __device__ __forceinline__ int rows_live(const ScanArgs& a, int b) {
     return a.lengths != nullptr ? min(max(a.lengths[b], 0), a.T) : a.T;
@@ -797,14 +806,13 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_fwd_kernel(c
         if (plain) fwd_store<C, true>(in, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
         else fwd_store<C, false>(in, gb, yp + row0 * a.y.st, a.y.st, nl, nr, q.nch);
     }
-    if constexpr (CL) {
-        if (!ok) cluster_leave();
-    } else {
+    if constexpr (!CL) {
         __syncthreads();
         if (iters > 0) get_s(&carry_s[(iters - 1) & 1][q.ch], carry);
     }
     if (a.h_out != nullptr && q.on && q.rank == 0 && q.w == (CL ? LEAD : 0) && q.seg == 0)
         store_f32(a.h_out + q.b * a.D + q.d, q.nch, carry);
+    if (!ok) leave_late<CL>();
 }
 
 // ------------------------------------------------------------------------------ backward
@@ -939,9 +947,6 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
             if (q.w == 0 && q.seg == 0) put_s(&carry_s[p][q.ch], e);
         }
     }
-    if constexpr (CL) {
-        if (!ok) cluster_leave();
-    }
     __syncthreads();
     if constexpr (!CL) {
         if (iters > 0) get_s(&carry_s[(iters - 1) & 1][q.ch], carry);
@@ -970,6 +975,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::MINB) tern_scan_bwd_kernel(c
             store_f32(g.partial + (q.b * a.S + q.rank) * a.D + q.d, q.nch, sum);
         }
     }
+    if (!ok) leave_late<CL>();
 }
 
 // dbias[d] = sum of the blocks' partial sums: 8 warps take every eighth partial, then in order.
