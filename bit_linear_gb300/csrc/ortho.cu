@@ -24,7 +24,7 @@
 // its norm to between 1/2 and 1, and A times 2^2k.  A step multiplies by up to 3.4445, so k falls with the
 // steps to 0, where X has reached the rest of the quintic; the products' factors undo it (Factors).
 //
-// Two steps at once, for m (n - m) of a million and more, or n of 1.5 m and m of 1024: with M0 =
+// Two steps at once, for m (n - m) of a million and more (and at 1024 rows from n = 1536 on): with M0 =
 // p(A), the next step's A is M0 A M0 = (M0 M0) A, as all of these commute, and X = (M1 M0) X, so
 // the pair needs one product of X in place of two: 3 m^2 n / 2 + 5 m^3 / 2 multiply-adds against
 // 3 m^2 n + m^3.  More than two would pass the
@@ -765,11 +765,15 @@ OrthoPlan ortho_plan(int64_t K, int64_t N) {
     p.k = kSumBlocks * static_cast<int64_t>(sizeof(double));
     p.x = round_up(p.k + static_cast<int64_t>(sizeof(int)), 256);
     // From about a million on the products of X that a pair of steps saves, m m (n - m) each, are worth
-    // more than its additional product of the smaller side: 512 x 4096 180 us, in pairs 168; 256 x 12000
-    // 200 and 175; 900 x 4000 311 and 273; 4096 x 5000 3358 and 3143; but 512 x 2048 142 and 143, 1000 x
-    // 1500 231 and 235, 2048 x 2048 508 and 534, 3000 x 3180 1584 and 1672.  From 1024 rows on they are equal at
-    // n = 1.5 m (1024 x 1536: 215), which the workspace's size turns on too.
-    p.pairs = p.m * (std::max(K, N) - p.m) >= 1 << 20 || (p.m >= 1024 && 2 * std::max(K, N) >= 3 * p.m);
+    // more than its additional products of the smaller side: 512 x 4096 180 us, in pairs 168; 900 x 4000 311
+    // and 273; 4096 x 5000 3358 and 3143.  Just below, either may be the faster (512 x 2400 153 and 151, 600 x
+    // 2200 181 and 176, 896 x 1900 235 both, 1100 x 1900 313 and 326, 1152 x 2040 310 and 323), and far below
+    // single steps are (600 x 1500 166 and 171, 1000 x 1530 234 and 239, 1280 x 1920 315 and 333, 2048 x 2048
+    // 508 and 534, 3000 x 3180 1584 and 1672).  At 1024 rows, the most whose symmetric products share their
+    // contractions over clusters of two, pairs are as good from n = 1.5 m on: 1024 x 1536 216 both, 1024 x 1800
+    // 227 and 224, 2040 x 1024 225 and 221 (1100 x 1650, without the clusters, 310 and 325).
+    const int64_t n = std::max(K, N);
+    p.pairs = p.m * (n - p.m) >= 1 << 20 || (p.m == 1024 && n >= 1536);
     p.bytes = p.x + 4 * p.x_plane;
     for (int i = 0; i < (p.pairs ? 4 : 2); ++i) p.mat[i] = p.bytes, p.bytes += 2 * p.m_plane;
     return p;
