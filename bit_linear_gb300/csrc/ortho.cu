@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(256) tern_ortho_load_kernel(const float* __res
     const double norm = sqrt(red[0]), size = norm + static_cast<double>(eps);
     double scale = static_cast<double>(kScaleX) / size;
     int k = 0, over = 0;
-    if (size >= 2.0 * norm && norm > 0.0) {
+    if (norm > 0.0 && norm <= static_cast<double>(eps) && isfinite(size)) {
         k = ilogb(size / norm);   // |X| 2^k: above 1/2, at most 1
         scale = ldexp(scale, k);
         over = max(ilogb(scale) - 120, 0);   // of norms below 2^-106 the factor would pass fp32's range
