@@ -44,8 +44,8 @@
 // contraction of a few tiles.
 //
 // 4096 x 12288: 5.2 ms; a product of X runs at 1.82 PFLOP/s of executed passes (0.95 of the measured
-// cuBLAS burst rate, tensor pipe busy 0.85), the symmetric ones at 0.77 of that: 136 tiles on 76
-// pairs are two rounds, the second one of 60.  512 x 2048: 142 us, eight a product: the end of the
+// cuBLAS burst rate, tensor pipe busy 0.84), the symmetric ones at 0.77 of that: 136 tiles on 76
+// pairs are two rounds, the second one of 60.  512 x 2048: 143 us, eight a product: the end of the
 // launch before it 2, the first copies 1.3, the k-blocks 0.45 each (operands at 87 B/ns into an SM),
 // the exchange and the stores 3.
 #include <algorithm>

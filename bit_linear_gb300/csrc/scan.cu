@@ -28,11 +28,14 @@
 //
 // HBM would allow 8 B per element in the forward and 14 B in the gradient (each input read once,
 // each output written once).  8 x 2048 x 2048 in bf16 with packed documents: forward 59 us, 0.67 of
-// the measured copy rate, gradient 125 us, 0.55.  What binds is the issue of instructions: 31 and 71
-// per element and lane, of which 17 and 32 are the arithmetic, at half of the issue slots (four
-// warps on a scheduler, each waiting on its own chain of exponential, reciprocal and fold).  More
-// warps with fewer rows each lost more to the folds than they hid (RPT 4: 77 us), fewer with more
-// rows hid less.  Gates and states are fp32; outputs are rounded once.
+// the measured copy rate, gradient 127 us, 0.55; without documents 53 and 120 us; in fp32 86 us, 0.92, and
+// 173 us, 0.80.  What binds in bf16 is latency, no unit: 31 and 72 instructions per element and lane, of
+// which 17 and 32 are the arithmetic, take 48% and 54% of the issue slots, and DRAM is busy 51% and 43% of
+// the time.  Of four warps on a scheduler, each on its own chain of exponential, reciprocal and fold, 1.6
+// and 1.4 wait for a result of fixed latency when one issues, 1.3 and 1.4 for a global load (the start
+// bytes and the gradient's saved states, loaded in the step that uses them), 0.8 and 0.4 for shared memory
+// or a special function.  More warps with fewer rows each lost more to the folds than they hid (RPT 4: 77
+// us), fewer with more rows hid less.  Gates and states are fp32; outputs are rounded once.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -84,8 +87,9 @@ __device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xff
 // bytes.  16 (WIDE): one access, and the sequences' inputs come by TMA.  Otherwise (odd widths,
 // strides or addresses) words of W bytes, where a row's last lane may hold fewer elements: nch
 // are there, loads repeat a word that is and stores leave the others out.  (8 x 2048 x D in bf16, the
-// forward and the gradient: D = 1024 32 + 68 us; 1026 40 + 87, element by element 73 + 168; 1025 55 +
-// 129, with the words around a lane's elements where all of them are in the tensor.)
+// forward and the gradient: D = 1024 31 + 65 us; 1026 39 + 84, element by element 73 + 168; 1025 55 +
+// 129, with the words around a lane's elements where all of them are in the tensor.  In fp32 1024 44 + 91,
+// 1025 55 + 141.)
 template <class T, int W>
 struct Io;
 template <int W_>
@@ -191,8 +195,10 @@ __device__ __forceinline__ void store_f32(float* p, int nch, const F2 (&x)[NP]) 
     }
 }
 
-// s = sigmoid(x + bias) and n = 1 - s = sigmoid(-x - bias), both good to a few units in the last
-// place: n is not formed as 1 - s, which loses it where s is near 1.  `lb` is -bias * log2(e).
+// s = sigmoid(x + bias) and n = 1 - s = sigmoid(-x - bias), to about 4 + |x + bias| units of 2^-24 relative
+// for the smaller of the two (the exponent is rounded once: 6 units up to 4, 17 up to 16, 65 at the cap, with
+// an exact exponential), a few for the larger; the approximate exponential and reciprocal add two or three.
+// n is not formed as 1 - s, which loses it where s is near 1.  `lb` is -bias * log2(e).
 // e = exp(-(x + bias)) is capped at 2^125 so that s and e*s stay normal numbers: for arguments
 // below -86 (-inf included) s is 2^-125 and n is 1.  A NaN stays one.  The approximate
 // exponential and reciprocal are taken without their subnormal paths, which the cap rules out

@@ -448,10 +448,10 @@ int tern_scan_fwd(const tern_scan* s, const float* h0, const tern_act* y, float*
                   size_t saved_bytes, void* stream);
 /*
  * Gradient, from the same inputs and the forward's saved states.  dy and the outputs df, dv, dr
- * have s->dtype (0 is written in padding, where dy has no effect, as above); dhT [B][D] fp32 is the gradient
- * of hT, or NULL (0); dh0 [B][D] fp32 and dbias [D] fp32 (the sum of df over sequences and rows,
- * before df is rounded) are written unless NULL.  dbias wants tern_scan_bwd_workspace() bytes
- * and B >= 1.  Sums run in a fixed order.
+ * have s->dtype (0 is written in padding, where dy has no effect, as above); dhT [B][D] fp32 is
+ * the gradient of hT, or NULL (0); dh0 [B][D] fp32 and dbias [D] fp32 (the sum of df over
+ * sequences and rows, before df is rounded) are written unless NULL.  dbias wants
+ * tern_scan_bwd_workspace() bytes and B >= 1.  Sums run in a fixed order.
  */
 size_t tern_scan_bwd_workspace(int64_t B, int64_t T, int64_t D);
 int tern_scan_bwd(const tern_scan* s, const float* saved, const tern_act* dy, const float* dhT,
