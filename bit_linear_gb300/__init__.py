@@ -16,9 +16,12 @@ current stream.  The functions carry the C names:
     tern_scan_step(f, v, r, h, y, h_out=None, f_bias=None)
     tern_orthogonalize(G, out, workspace, steps=5, eps=1e-7, gain=1.0)
 
+    tern_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None)
+    tern_norm_bwd(x, dy, mean, rstd, dx, workspace=None, weight=None, dweight=None, dbias=None)
+
 Materialize, MaterializeGrouped, GroupedForward, GroupedBackward, MultiAdamW, EmbedForward,
-EmbedBackward, ScanForward, ScanBackward, ScanStep and Orthogonalize are the same calls with
-their arguments checked and marshalled once, for loops that repeat them on the
+EmbedBackward, ScanForward, ScanBackward, ScanStep, Orthogonalize, NormForward and NormBackward
+are the same calls with their arguments checked and marshalled once, for loops that repeat them on the
 same buffers.
 
 Importing this package loads ``lib/libtern.so``; if it is missing the import
@@ -59,7 +62,8 @@ ABI_SYMBOLS = ("tern_tiles_bytes", "tern_materialize", "tern_materialize_grouped
                "tern_grad_sumsq", "adamw_step_multi", "tern_sr4_workspace", "tern_sr4_step", "tern_sr4_panel",
                "tern_embed_fwd", "tern_embed_bwd_workspace", "tern_embed_bwd", "tern_scan_saved", "tern_scan_fwd",
                "tern_scan_bwd_workspace", "tern_scan_bwd", "tern_scan_step",
-               "tern_orthogonalize_workspace", "tern_orthogonalize", "tern_strerror",
+               "tern_orthogonalize_workspace", "tern_orthogonalize",
+               "tern_norm_fwd", "tern_norm_bwd_workspace", "tern_norm_bwd", "tern_strerror",
                "tern_device_status", "tern_device_diagnostics", "tern_selftest_wait_timeout")
 
 
@@ -137,6 +141,9 @@ def _load():
         "tern_scan_step": ([ctypes.POINTER(_Scan), vp, vp, ctypes.POINTER(_Act), vp], ci),
         "tern_orthogonalize_workspace": ([i64, i64], sz),
         "tern_orthogonalize": ([vp, i64, i64, ci, cf, cf, vp, vp, sz, vp], ci),
+        "tern_norm_fwd": ([vp, ci, i64, vp, vp, i64, i64, cf, vp, ci, i64, vp, vp, vp], ci),
+        "tern_norm_bwd_workspace": ([i64, i64], sz),
+        "tern_norm_bwd": ([vp, ci, i64, vp, vp, vp, vp, ci, i64, i64, i64, vp, i64, vp, vp, vp, sz, vp], ci),
         "tern_strerror": ([ci], ctypes.c_char_p),
         "tern_device_status": ([vp, ci], ci),
         "tern_device_diagnostics": ([ctypes.POINTER(i64), ci], ci),
@@ -722,6 +729,64 @@ class Orthogonalize:
 def tern_orthogonalize(G, out, workspace, steps=5, eps=1e-7, gain=1.0, stream=None):
     """out (bf16) = gain * G with its singular values moved to about 1 by Newton-Schulz products."""
     Orthogonalize(G, out, workspace, steps, eps, gain)(stream)
+
+
+def _same_device(*tensors):
+    """The tensors of a call live on the current device, whose stream it is enqueued on."""
+    on = {t.device for t in tensors if t is not None}
+    if on - {torch.device("cuda", torch.cuda.current_device())}:
+        raise ValueError(f"tensors on {', '.join(sorted(str(d) for d in on))}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+class NormForward:
+    """tern_norm_fwd with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None):
+        tx, ty = _kind(x, _FLOATS, "x"), _kind(y, _FLOATS, "y")
+        n, D = x.shape
+        (xp, ldx), (yp, ldy) = _rows(x, x.dtype, (n, D), "x"), _rows(y, y.dtype, (n, D), "y")
+        self._args = (xp, tx, ldx, _ptr(weight, torch.float32, (D,), "weight"), _ptr(bias, torch.float32, (D,), "bias"), n, D,
+                      float(eps), yp, ty, ldy, _ptr(mean, torch.float32, (n,), "mean"), _ptr(rstd, torch.float32, (n,), "rstd"))
+        self._refs = (x, y, weight, bias, mean, rstd)
+        _same_device(*self._refs)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_norm_fwd(*self._args, _stream(stream)), "tern_norm_fwd")
+
+
+def tern_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of x [n, D]: y = (x - mean) * rstd * weight + bias (bf16 or fp32 each)."""
+    NormForward(x, y, weight, bias, eps, mean, rstd)(stream)
+
+
+def tern_norm_bwd_workspace(n, D) -> int:
+    return int(lib.tern_norm_bwd_workspace(int(n), int(D)))
+
+
+class NormBackward:
+    """tern_norm_bwd with its arguments (and workspace) marshalled once; see GroupedForward."""
+
+    def __init__(self, x, dy, mean, rstd, dx, workspace=None, weight=None, dweight=None, dbias=None):
+        tx, ty = _kind(x, _FLOATS, "x"), _kind(dy, _FLOATS, "dy")
+        n, D = x.shape
+        (xp, ldx), (dyp, lddy) = _rows(x, x.dtype, (n, D), "x"), _rows(dy, dy.dtype, (n, D), "dy")
+        dxp, lddx = _rows(dx, x.dtype, (n, D), "dx")
+        vec = lambda t, k, name: _ptr(t, torch.float32, (k,), name)  # noqa: E731
+        self._args = (xp, tx, ldx, vec(weight, D, "weight"), vec(mean, n, "mean"), vec(rstd, n, "rstd"), dyp, ty, lddy, n, D, dxp,
+                      lddx, vec(dweight, D, "dweight"), vec(dbias, D, "dbias"), *_scratch(workspace, "workspace"))
+        self._refs = (x, dy, mean, rstd, dx, workspace, weight, dweight, dbias)
+        _same_device(*self._refs)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_norm_bwd(*self._args, _stream(stream)), "tern_norm_bwd")
+
+
+def tern_norm_bwd(x, dy, mean, rstd, dx, workspace=None, weight=None, dweight=None, dbias=None, stream=None):
+    """dx (x's type) and, where given, dweight and dbias (fp32 [D]) of tern_norm_fwd, from its mean and rstd."""
+    NormBackward(x, dy, mean, rstd, dx, workspace, weight, dweight, dbias)(stream)
 
 
 def tern_device_status(stream=None, clear=True) -> int:

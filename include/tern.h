@@ -478,6 +478,40 @@ size_t tern_orthogonalize_workspace(int64_t K, int64_t N);
 int tern_orthogonalize(const float* G, int64_t K, int64_t N, int steps, float eps, float gain, uint16_t* out,
                        void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------
+ * Between and behind the projections: the layer norm before them, the gated feed-forward
+ * layer, the log probabilities of tokens, and the loss of a student against a teacher's top
+ * logits.  The same rules hold; any size, zero included, and any alignment of whole elements
+ * unless a line below says otherwise.  Matrices have contiguous rows `ld` elements apart,
+ * ld >= the row's length.
+ * ------------------------------------------------------------------------------------
+ */
+
+/*
+ * Layer norm of n rows of D channels:
+ *   mean = sum x / D, rstd = 1 / sqrt(sum (x - mean)^2 / D + eps)
+ *   y    = (x - mean) * rstd * weight + bias
+ * x: x_dtype, y: y_dtype (TERN_BF16 or TERN_F32 each); weight, bias [D] fp32 or NULL (1, 0); mean,
+ * rstd [n] fp32, written unless NULL (the gradient reads them).  Sums are fp32, y is rounded once.
+ * eps > 0 (1e-5 is usual); n < 2^31 - 2048, D at most 2^22.
+ */
+int tern_norm_fwd(const void* x, int x_dtype, int64_t ld_x, const float* weight, const float* bias, int64_t n,
+                  int64_t D, float eps, void* y, int y_dtype, int64_t ld_y, float* mean, float* rstd, void* stream);
+/*
+ * Gradient, from the same x and weight and the forward's mean and rstd; dy has y's type, dx x's:
+ *   g  = dy * weight, xhat = (x - mean) * rstd
+ *   dx = rstd * (g - sum g / D - xhat * sum (g xhat) / D)
+ *   dweight = sum over rows of dy * xhat, dbias = sum over rows of dy    (fp32 [D]; NULL to skip)
+ * dx is rounded once.  Sums run in a fixed order.  A padding row adds nothing to dweight and dbias where
+ * its dy is 0 and its x finite.
+ *   workspace: >= tern_norm_bwd_workspace() bytes, 16-byte aligned, for dweight or dbias (else NULL).
+ */
+size_t tern_norm_bwd_workspace(int64_t n, int64_t D);
+int tern_norm_bwd(const void* x, int x_dtype, int64_t ld_x, const float* weight, const float* mean, const float* rstd,
+                  const void* dy, int y_dtype, int64_t ld_dy, int64_t n, int64_t D, void* dx, int64_t ld_dx,
+                  float* dweight, float* dbias, void* workspace, size_t ws_bytes, void* stream);
+
 /* Text of a status code (static storage). */
 const char* tern_strerror(int status);
 
