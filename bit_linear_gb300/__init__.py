@@ -18,10 +18,12 @@ current stream.  The functions carry the C names:
 
     tern_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None)
     tern_norm_bwd(x, dy, mean, rstd, dx, workspace=None, weight=None, dweight=None, dbias=None)
+    tern_glu_fwd(X, tiles, scale, H, saved=None, act="silu")
+    tern_glu_bwd(dH, dY, saved=None, X=None, tiles=None, scale=None, act="silu")
 
 Materialize, MaterializeGrouped, GroupedForward, GroupedBackward, MultiAdamW, EmbedForward,
-EmbedBackward, ScanForward, ScanBackward, ScanStep, Orthogonalize, NormForward and NormBackward
-are the same calls with their arguments checked and marshalled once, for loops that repeat them on the
+EmbedBackward, ScanForward, ScanBackward, ScanStep, Orthogonalize, NormForward, NormBackward,
+GluForward and GluBackward are the same calls with their arguments checked and marshalled once, for loops that repeat them on the
 same buffers.
 
 Importing this package loads ``lib/libtern.so``; if it is missing the import
@@ -53,6 +55,7 @@ TERN_ADAM_MAX_TENSORS = 64
 TERN_BWD_ACCUMULATE = 1
 TERN_BWD_DX_SPLIT8 = 2
 TERN_BF16, TERN_F32, TERN_I32, TERN_I64 = 0, 1, 2, 3
+TERN_ACT_SILU, TERN_ACT_GELU, TERN_ACT_RELU2, TERN_ACT_SIGMOID = 0, 1, 2, 3
 
 # the C ABI's exported symbols (tests check the library exports every one)
 ABI_SYMBOLS = ("tern_tiles_bytes", "tern_materialize", "tern_materialize_grouped", "tern_linear_fwd", "tern_linear_bwd_workspace_min",
@@ -63,7 +66,8 @@ ABI_SYMBOLS = ("tern_tiles_bytes", "tern_materialize", "tern_materialize_grouped
                "tern_embed_fwd", "tern_embed_bwd_workspace", "tern_embed_bwd", "tern_scan_saved", "tern_scan_fwd",
                "tern_scan_bwd_workspace", "tern_scan_bwd", "tern_scan_step",
                "tern_orthogonalize_workspace", "tern_orthogonalize",
-               "tern_norm_fwd", "tern_norm_bwd_workspace", "tern_norm_bwd", "tern_strerror",
+               "tern_norm_fwd", "tern_norm_bwd_workspace", "tern_norm_bwd",
+               "tern_glu_fwd", "tern_glu_bwd", "tern_strerror",
                "tern_device_status", "tern_device_diagnostics", "tern_selftest_wait_timeout")
 
 
@@ -144,6 +148,8 @@ def _load():
         "tern_norm_fwd": ([vp, ci, i64, vp, vp, i64, i64, cf, vp, ci, i64, vp, vp, vp], ci),
         "tern_norm_bwd_workspace": ([i64, i64], sz),
         "tern_norm_bwd": ([vp, ci, i64, vp, vp, vp, vp, ci, i64, i64, i64, vp, i64, vp, vp, vp, sz, vp], ci),
+        "tern_glu_fwd": ([vp, tp, vp, ci, vp, vp, i64, i64, i64, vp], ci),
+        "tern_glu_bwd": ([vp, vp, vp, tp, vp, ci, vp, i64, i64, i64, vp], ci),
         "tern_strerror": ([ci], ctypes.c_char_p),
         "tern_device_status": ([vp, ci], ci),
         "tern_device_diagnostics": ([ctypes.POINTER(i64), ci], ci),
@@ -787,6 +793,67 @@ class NormBackward:
 def tern_norm_bwd(x, dy, mean, rstd, dx, workspace=None, weight=None, dweight=None, dbias=None, stream=None):
     """dx (x's type) and, where given, dweight and dbias (fp32 [D]) of tern_norm_fwd, from its mean and rstd."""
     NormBackward(x, dy, mean, rstd, dx, workspace, weight, dweight, dbias)(stream)
+
+
+_ACTS = {"silu": TERN_ACT_SILU, "gelu": TERN_ACT_GELU, "relu2": TERN_ACT_RELU2, "sigmoid": TERN_ACT_SIGMOID}
+
+
+def _glu_weight(X, tiles, scale, act):
+    """(X, tiles, scale, act, M, K, N) as the C calls take them, for a weight of 2 N columns."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}")
+    M, K = X.shape
+    if tiles.K != K or tiles.N % 2:
+        raise ValueError(f"tiles of {K} rows and an even number of columns are wanted, got {tiles.K} x {tiles.N}")
+    ct = tiles._c()
+    return _ptr(X, torch.bfloat16, (M, K), "X"), ct, _ptr(scale, torch.float32, (tiles.N,), "scale"), _ACTS[act], M, K, tiles.N // 2
+
+
+class GluForward:
+    """tern_glu_fwd with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, X, tiles: Tiles, scale, H, saved=None, act="silu"):
+        x, self._ct, sc, code, M, K, N = _glu_weight(X, tiles, scale, act)
+        self._args = (x, ctypes.byref(self._ct), sc, code, _ptr(H, torch.bfloat16, (M, N), "H"),
+                      _ptr(saved, torch.bfloat16, (M, 2 * N), "saved"), M, K, N)
+        self._refs = (X, tiles, scale, H, saved)
+        _same_device(X, tiles.packed, tiles.t_bf16, scale, H, saved)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_glu_fwd(*self._args, _stream(stream)), "tern_glu_fwd")
+
+
+def tern_glu_fwd(X, tiles: Tiles, scale, H, saved=None, act="silu", stream=None):
+    """H [M, N] bf16 = act(g) * u, g | u = scale * (X T) of a ternary weight of 2 N columns; `saved`
+    [M, 2 N] bf16 keeps the factors of the gradient."""
+    GluForward(X, tiles, scale, H, saved, act)(stream)
+
+
+class GluBackward:
+    """tern_glu_bwd with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, dH, dY, saved=None, X=None, tiles=None, scale=None, act="silu"):
+        M, N = dH.shape
+        x, w, sc, code, K = None, None, None, _ACTS.get(act, -1), 0
+        if saved is None:
+            if X is None or tiles is None or scale is None:
+                raise ValueError("either saved or X, tiles and scale are wanted")
+            x, self._ct, sc, code, Mx, K, Nw = _glu_weight(X, tiles, scale, act)
+            if (Mx, Nw) != (M, N):
+                raise ValueError(f"dH must have shape {(Mx, Nw)}, got {(M, N)}")
+            w = ctypes.byref(self._ct)
+        self._args = (_ptr(dH, torch.bfloat16, (M, N), "dH"), _ptr(saved, torch.bfloat16, (M, 2 * N), "saved"), x, w, sc, code,
+                      _ptr(dY, torch.bfloat16, (M, 2 * N), "dY"), M, K, N)
+        self._refs = (dH, dY, saved, X, tiles, scale)
+        _same_device(dH, dY, saved, X, None if tiles is None else tiles.t_bf16, scale)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_glu_bwd(*self._args, _stream(stream)), "tern_glu_bwd")
+
+
+def tern_glu_bwd(dH, dY, saved=None, X=None, tiles=None, scale=None, act="silu", stream=None):
+    """dY [M, 2 N] bf16 = dH u act'(g) | dH act(g): from `saved`, or from X, tiles and scale again."""
+    GluBackward(dH, dY, saved, X, tiles, scale, act)(stream)
 
 
 def tern_device_status(stream=None, clear=True) -> int:

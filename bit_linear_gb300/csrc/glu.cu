@@ -1,0 +1,716 @@
+// Gated feed-forward layer on ternary weights: both projections, the activation and the product.
+//
+//   g | u = scale (X T), T = ternary weight [K][2N], the gate's columns first
+//   H     = act(g) u
+//   dY    = dH u act'(g) | dH act(g)      the dY [M][2N] that tern_linear_bwd takes for the same weight
+//
+// Many rows: one persistent tcgen05 GEMM whose tile holds the gate's and the value's columns of the same
+// HN outputs side by side (accumulator columns 0..HN-1 and HN..2HN-1), so that the epilogue has both
+// and g, u never reach memory.  A pair of CTAs (256 rows) splits the B operand the same way: the
+// leader copies the gate's columns, its peer the value's.  Operands as in the ternary forward: X
+// (K-major) and the bf16 plane T (MN-major), by TMA with the 128-byte swizzle; products with -1, 0
+// and 1 are exact and sums fp32.  The epilogue rounds H once.  For training it also stores the
+// factors u act'(g) | act(g) as bf16, which leaves the gradient a product: that costs a second
+// rounding (2^-8 at most each) and four bytes an element, where g and u in fp32 would cost eight and
+// recomputing them the whole GEMM again.  The gradient without stored factors is that: the same
+// GEMM, with dH read and dY written in the epilogue, rounded once.
+//
+// A few rows (single tokens): the 2-bit codes are read, an eighth of T's bytes.  See glu_codes below.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include <cuda_bf16.h>
+
+#include "mma.cuh"
+#include "rows.cuh"
+
+namespace tern {
+
+__device__ int g_glu_status;
+
+namespace {
+
+constexpr int kBM = 128;   // rows of X per CTA
+
+__device__ __forceinline__ float pow2(float x) {   // 2^x, from the special function unit
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// act(g) and, with D, act'(g).  The special functions' errors (2^-22 relative each) are far below the
+// outputs' rounding to bf16.
+template <int ACT, bool D>
+__device__ __forceinline__ void activate(float g, float& a, float& d) {
+    if constexpr (ACT == TERN_ACT_RELU2) {
+        const float r = g < 0.f ? 0.f : g;   // NaN passes
+        a = r * r;
+        d = 2.f * r;
+    } else if constexpr (ACT == TERN_ACT_GELU) {
+        // g Phi(g): the upper tail's approximation by Hastings (Abramowitz and Stegun 7.1.26, 1.5e-7
+        // absolute in erf), whose exponential the density shares
+        const float z = fabsf(g) * 0.70710678f;
+        const float t = reciprocal(fmaf(0.3275911f, z, 1.f));
+        const float e = pow2(g * g * -0.72134752f);   // exp(-g^2 / 2)
+        float p = fmaf(1.061405429f, t, -1.453152027f);
+        p = fmaf(p, t, 1.421413741f);
+        p = fmaf(p, t, -0.284496736f);
+        p = fmaf(p, t, 0.254829592f);
+        const float tail = 0.5f * p * t * e;
+        const float cdf = g < 0.f ? tail : 1.f - tail;
+        a = g * cdf;
+        if (D) d = fmaf(g * 0.39894228f, e, cdf);
+    } else {
+        // sigmoid from exp(-|g|), which cannot overflow; its complement without a difference
+        const float e = pow2(fabsf(g) * -1.44269504f);
+        const float r = reciprocal(1.f + e);
+        const float s = g < 0.f ? e * r : r, c = g < 0.f ? r : e * r;
+        if constexpr (ACT == TERN_ACT_SIGMOID) {
+            a = s;
+            if (D) d = s * c;
+        } else {
+            a = g * s;
+            if (D) d = fmaf(a, c, s);
+        }
+    }
+}
+
+struct GluArgs {
+    CUtensorMap mX, mT;
+    const float* scale;     // [2N]
+    const uint16_t* dH;     // [M][N]: the gradient is computed; else H
+    uint16_t* H;            // [M][N]
+    uint16_t* pair;         // [M][2N]: the factors (with H; may be null), or dY (with dH)
+    int M, N, K, act;
+    int tiles_m, tiles_n, num_kb;
+};
+
+// CG CTAs share a tile of 128 CG rows by HN outputs: 2 HN accumulator columns.
+template <int CG_, int HN_, int STAGES_>
+struct GluCfg {
+    static constexpr int CG = CG_, HN = HN_, STAGES = STAGES_, BK = 64, BN = 2 * HN;
+    static constexpr int TILE_M = kBM * CG;
+    static constexpr int B_COLS = BN / CG;
+    static constexpr int A_BYTES = kBM * BK * 2, B_BYTES = B_COLS * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int RASTER = 16 / CG;      // as in the ternary forward
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+    static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "TMEM allocation must be a power of two");
+    static_assert(SMEM_BYTES <= 232448 && B_COLS % 64 == 0, "stage");
+};
+
+__device__ __forceinline__ bool glu_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, bool watch) {
+    return wait_limited(bar, parity, abort_flag, watch, kWaitLimitNs, [] { atomicExch(&g_glu_status, 1); });
+}
+
+// 32 rows (a lane each) of 32 bf16, four 16-byte units a lane: within four lanes the 4 x 4 units are
+// transposed by shuffles, so that a store writes whole 64-byte rows, eight at a time.
+__device__ __forceinline__ void store_rows(uint16_t* base, int64_t ld, int rows, int cols, const uint32_t (&w)[16], int lane) {
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+#pragma unroll
+    for (int d = 2; d >= 1; d >>= 1) {
+        const bool upper = (lane & d) != 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+            const uint4 send = upper ? u[i] : u[i | d];
+            uint4 recv;
+            recv.x = __shfl_xor_sync(0xffffffffu, send.x, d);
+            recv.y = __shfl_xor_sync(0xffffffffu, send.y, d);
+            recv.z = __shfl_xor_sync(0xffffffffu, send.z, d);
+            recv.w = __shfl_xor_sync(0xffffffffu, send.w, d);
+            if (upper) u[i] = recv;
+            else u[i | d] = recv;
+        }
+    }
+    const int q = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (lane & ~3) + i;
+        if (r < rows && 8 * q < cols) *reinterpret_cast<uint4*>(base + static_cast<int64_t>(r) * ld + 8 * q) = u[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// 32 outputs of a lane's row, columns c0..c0+31, from the accumulators at TMEM columns tg (the gate's)
+// and tu (the value's): H, or H and the factors, or dY.  Sixteen columns at a time, which the
+// registers hold beside the results.
+template <int ACT, bool BACK, bool TWO>
+__device__ __forceinline__ void glu_chunk(const GluArgs& a, uint32_t tg, uint32_t tu, int wrow, int c0, int lane) {
+    const int cols = min(32, a.N - c0);   // a multiple of 16
+    const int rows = a.M - wrow;          // > 0
+    uint32_t h[16], p[16], q[16];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t rg[16], ru[16];
+        ptx::tmem_ld_32x32b_x16(tg + 16 * half, rg);
+        ptx::tmem_ld_32x32b_x16(tu + 16 * half, ru);
+        const int c = min(c0 + 16 * half, a.N - 16);   // past the last column: anything readable, not stored
+        Raw<__nv_bfloat16, 16> dh;
+        if (BACK) dh = load_raw<__nv_bfloat16, 16>(reinterpret_cast<const __nv_bfloat16*>(a.dH) + (wrow + min(lane, rows - 1)) * static_cast<int64_t>(a.N) + c);
+        const float4* pg = reinterpret_cast<const float4*>(a.scale + c);
+        const float4* pu = reinterpret_cast<const float4*>(a.scale + a.N + c);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {   // four columns
+            const float4 sg = __ldg(pg + b), su = __ldg(pu + b);
+            const float g[4] = {__uint_as_float(rg[4 * b]) * sg.x, __uint_as_float(rg[4 * b + 1]) * sg.y, __uint_as_float(rg[4 * b + 2]) * sg.z,
+                                __uint_as_float(rg[4 * b + 3]) * sg.w};
+            const float u[4] = {__uint_as_float(ru[4 * b]) * su.x, __uint_as_float(ru[4 * b + 1]) * su.y, __uint_as_float(ru[4 * b + 2]) * su.z,
+                                __uint_as_float(ru[4 * b + 3]) * su.w};
+            const int o = 8 * half + 2 * b;
+            float f[4], d[4];
+            if constexpr (TWO) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) activate<ACT, true>(g[i], f[i], d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] *= u[i];
+                if constexpr (BACK) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = raw_at<__nv_bfloat16, 16>(dh, 4 * b + i);
+                        d[i] *= x;
+                        f[i] *= x;
+                    }
+                }
+                p[o] = pack_bf16(d[0], d[1]), p[o + 1] = pack_bf16(d[2], d[3]);
+                q[o] = pack_bf16(f[0], f[1]), q[o + 1] = pack_bf16(f[2], f[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) activate<ACT, false>(g[i], f[i], d[i]);
+            }
+            if constexpr (!BACK) h[o] = pack_bf16(f[0] * u[0], f[1] * u[1]), h[o + 1] = pack_bf16(f[2] * u[2], f[3] * u[3]);
+        }
+    }
+    if constexpr (!BACK) store_rows(a.H + static_cast<int64_t>(wrow) * a.N + c0, a.N, rows, cols, h, lane);
+    if constexpr (TWO) {
+        uint16_t* to = a.pair + static_cast<int64_t>(wrow) * 2 * a.N + c0;
+        store_rows(to, 2 * static_cast<int64_t>(a.N), rows, cols, p, lane);
+        store_rows(to + a.N, 2 * static_cast<int64_t>(a.N), rows, cols, q, lane);
+    }
+}
+
+template <bool BACK, bool TWO>
+__device__ __forceinline__ void glu_act(const GluArgs& a, uint32_t tg, uint32_t tu, int wrow, int c0, int lane) {
+    switch (a.act) {
+    case TERN_ACT_SILU: glu_chunk<TERN_ACT_SILU, BACK, TWO>(a, tg, tu, wrow, c0, lane); break;
+    case TERN_ACT_GELU: glu_chunk<TERN_ACT_GELU, BACK, TWO>(a, tg, tu, wrow, c0, lane); break;
+    case TERN_ACT_RELU2: glu_chunk<TERN_ACT_RELU2, BACK, TWO>(a, tg, tu, wrow, c0, lane); break;
+    default: glu_chunk<TERN_ACT_SIGMOID, BACK, TWO>(a, tg, tu, wrow, c0, lane); break;
+    }
+}
+
+// Roles as in the ternary forward: warp 0 copies, warp 1 allocates TMEM and (in the leader) issues the
+// MMAs, warps 2-9 are the epilogue, two for each 32 rows.  Two accumulators, so that a tile's
+// epilogue runs beside the next tile's products.
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) tern_glu_gemm(const __grid_constant__ GluArgs a) {
+    constexpr int CG = C::CG;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + C::STAGES * C::STAGE_BYTES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t FULL0 = ptx::smem_u32(bars), EMPTY0 = FULL0 + 8u * C::STAGES;
+    const uint32_t TFULL0 = FULL0 + 16u * C::STAGES, TEMPTY0 = TFULL0 + 16u, DRAIN = TFULL0 + 32u;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;   // 0 = leader of the pair
+    const int unit = static_cast<int>(blockIdx.x) / CG, units = static_cast<int>(gridDim.x) / CG;
+    const int total = a.tiles_m * a.tiles_n;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            ptx::mbar_init(FULL0 + 8u * s, 1);
+            ptx::mbar_init(EMPTY0 + 8u * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(TFULL0 + 8u * b, 1);
+            ptx::mbar_init(TEMPTY0 + 8u * b, C::EPI_WARPS * CG);
+        }
+        ptx::mbar_init(DRAIN, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) {
+            ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::pdl_trigger();   // TMEM is allocated everywhere: small kernels may follow
+    ptx::pdl_wait();
+
+    uint32_t issued = 0, issued_parity = 0;
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------------ copies
+        ptx::tma_prefetch_desc(&a.mX);
+        ptx::tma_prefetch_desc(&a.mT);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = unit; ok && tile < total; tile += units) {
+            int mt, nt;
+            tile_coords<C::RASTER>(tile, a.tiles_m, a.tiles_n, mt, nt);
+            const int arow = mt * C::TILE_M + static_cast<int>(rank) * kBM;
+            for (int kb = 0; kb < a.num_kb; ++kb) {
+                if (!glu_wait(EMPTY0 + 8u * stage, phase ^ 1u, abort_flag, true)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = FULL0 + 8u * stage;
+                const uint32_t full_at = CG == 2 ? ptx::mapa_shared(full, 0) : full;   // a pair counts on the leader's
+                const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
+                if (rank == 0) ptx::mbar_arrive_expect_tx(full, CG * C::STAGE_BYTES);
+                auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y) {
+                    if constexpr (CG == 2) ptx::tma_load_2d_pair(dst, m, x, y, full_at);
+                    else ptx::tma_load_2d(dst, m, x, y, full_at);
+                };
+                load(sA, &a.mX, kb * C::BK, arow);
+#pragma unroll
+                for (int j = 0; j < C::B_COLS / 64; ++j) {
+                    // column of the accumulator, the gate's below HN; N is a multiple of 16, so that x is
+                    // aligned.  A last tile's columns past N are the value's first (or zeros): not stored.
+                    const int c = static_cast<int>(rank) * C::B_COLS + j * 64;
+                    const int x = c < C::HN ? nt * C::HN + c : a.N + nt * C::HN + c - C::HN;
+                    load(sB + j * 64 * C::BK * 2, &a.mT, x, kb * C::BK);
+                }
+                issued |= 1u << stage;
+                issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // every stage's release has arrived before the CTA may exit
+        if (ok)
+            for (int s = 0; s < C::STAGES; ++s)
+                if (issued & (1u << s)) glu_wait(EMPTY0 + 8u * s, (issued_parity >> s) & 1u, abort_flag, true);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t IDESC = make_idesc(C::TILE_M, C::BN, false, true);
+        int stage = 0, local = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = unit; ok && tile < total; tile += units, ++local) {
+            const int acc = local & 1;
+            if (!glu_wait(TEMPTY0 + 8u * acc, ((local >> 1) & 1) ^ 1u, abort_flag, true)) break;
+            ptx::tc_fence_after();
+            const uint32_t d_tmem = tmem_base + acc * C::BN;
+            for (int kb = 0; kb < a.num_kb; ++kb) {
+                if (!glu_wait(FULL0 + 8u * stage, phase, abort_flag, true)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < C::BK / 16; ++kk) {
+                    const uint64_t da = op_desc<false, C::BK>(sA, kk), db = op_desc<true, C::BK>(sB, kk);
+                    const uint32_t more = kb != 0 || kk != 0;
+                    if constexpr (CG == 2) ptx::mma_bf16_pair(d_tmem, da, db, IDESC, more);
+                    else ptx::mma_bf16(d_tmem, da, db, IDESC, more);
+                }
+                if constexpr (CG == 2) ptx::mma_commit_pair_mc(EMPTY0 + 8u * stage, 0x3);
+                else ptx::mma_commit(EMPTY0 + 8u * stage);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if constexpr (CG == 2) ptx::mma_commit_pair_mc(TFULL0 + 8u * acc, 0x3);
+            else ptx::mma_commit(TFULL0 + 8u * acc);
+        }
+        if constexpr (CG == 2) ptx::mma_commit_pair(DRAIN); else ptx::mma_commit(DRAIN);
+        glu_wait(DRAIN, 0, abort_flag, false);
+        if (ok && !*abort_flag) {   // the epilogues' last releases have arrived
+            for (int acc = 0; acc < 2; ++acc) {
+                if (local <= acc) continue;
+                const int last = (local - 1) - (((local - 1) - acc) & 1);
+                glu_wait(TEMPTY0 + 8u * acc, static_cast<uint32_t>(last >> 1) & 1u, abort_flag, true);
+            }
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue
+        const int quad = warp & 3;   // a warp may touch TMEM lanes 32 (warp % 4) .. + 31
+        const uint32_t tempty_leader = CG == 2 ? ptx::mapa_shared(TEMPTY0, 0) : TEMPTY0;
+        constexpr int JPW = C::HN / 64;
+        const int j0 = ((warp - 2) / 4) * JPW;
+        int local = 0;
+        for (int tile = unit; tile < total; tile += units, ++local) {
+            const int acc = local & 1;
+            const bool full = glu_wait(TFULL0 + 8u * acc, (local >> 1) & 1, abort_flag, true);
+            if (!__all_sync(0xffffffffu, full)) break;   // one decision a warp: the loads are the warp's
+            ptx::tc_fence_after();
+            int mt, nt;
+            tile_coords<C::RASTER>(tile, a.tiles_m, a.tiles_n, mt, nt);
+            const int wrow = mt * C::TILE_M + static_cast<int>(rank) * kBM + quad * 32;
+            if (wrow < a.M) {
+                const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::BN;
+#pragma unroll 1
+                for (int j = j0; j < j0 + JPW; ++j) {
+                    const int c0 = nt * C::HN + j * 32;
+                    if (c0 >= a.N) break;
+                    const uint32_t tg = trow + j * 32, tu = tg + C::HN;
+                    if (a.dH) glu_act<true, true>(a, tg, tu, wrow, c0, lane);
+                    else if (a.pair) glu_act<false, true>(a, tg, tu, wrow, c0, lane);
+                    else glu_act<false, false>(a, tg, tu, wrow, c0, lane);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) ptx::mbar_arrive_cluster(tempty_leader + 8u * acc);
+                else ptx::mbar_arrive(TEMPTY0 + 8u * acc);
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if constexpr (CG == 2) ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        // after an abort, copies still in flight must land before the shared memory is released
+        if constexpr (CG == 1) {
+            for (int s = 0; s < C::STAGES; ++s)
+                if (issued & (1u << s)) glu_wait(FULL0 + 8u * s, (issued_parity >> s) & 1u, abort_flag, false);
+        } else {
+            const uint64_t t0 = ptx::globaltimer();   // a pair's copies count on the leader's barriers: give them time
+            while (ptx::globaltimer() - t0 < 100000ull) {
+            }
+        }
+    }
+}
+
+using GluPair = GluCfg<2, 128, 7>;
+using GluOne = GluCfg<1, 128, 4>;
+
+// ------------------------------------------------------------------------------ a few rows
+//
+// glu_codes: up to 16 rows from the 2-bit codes.  A code's two bits as the upper two bits of a bf16 are
+// twice its value (00: 0, 01: 0x4000 = 2, 11: 0xC000 = -2), so an operand register of two weights
+// takes a shift and a mask.  The products run on mma.sync (m16n8k16), with the weights as the 16-row
+// operand and the tokens as the 8 columns: with so few rows the time is that of reading and
+// expanding codes, a tcgen05 tile of 128 rows would be mostly padding and would want the operand
+// written to shared memory.  Element order within an MMA is free as long as both operands agree:
+// lane (g, t) = (lane / 4, lane % 4) reads the words of 16 columns 16 g.. at the four weight rows
+// 4 t.. of a block of 16 rows, and MMA j takes its columns 16 g + j and 16 g + j + 8.
+//
+// A block has 128 outputs (128 columns of the gate, 128 of the value); its warps and, where there are
+// few blocks, the blocks of a cluster share the weight's rows.  Sums are added in a fixed order: a
+// warp's blocks of rows, the warps of a block, the blocks of a cluster.
+constexpr int kCodeOut = 128, kCodeWarps = 8;
+constexpr int kCodeCols = 2 * kCodeOut, kCodePad = kCodeCols + 4;   // the pad keeps a warp's stores free of conflicts
+constexpr int kCodeRows = 16;                                       // most rows of X
+
+struct CodeArgs {
+    const uint16_t* X;
+    const uint32_t* packed;
+    const float* scale;
+    uint16_t* H;
+    int M, N, K, act;
+};
+
+__device__ __forceinline__ void mma_tokens(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes of eight columns at two rows: the lower (upper) halves of two words side by side.
+__device__ __forceinline__ uint32_t halves(uint32_t w0, uint32_t w1, bool upper) { return __byte_perm(w0, w1, upper ? 0x7632 : 0x5410); }
+
+template <int MT>   // tokens in eights
+__global__ void __launch_bounds__(kCodeWarps * 32) glu_codes(const __grid_constant__ CodeArgs a) {
+    extern __shared__ float part[];   // [warps][8 MT][kCodePad]
+    ptx::pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint32_t rank, size;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(size));
+    const int n0 = static_cast<int>(blockIdx.x / size) * kCodeOut;
+    const int words = a.N / 8;                       // of a weight row: 2N / 16
+    const bool live = n0 + 16 * g < a.N;             // N % 16 == 0
+    const uint32_t* wg = a.packed + (live ? n0 / 16 + g : 0);
+    const int up = a.N / 16;                         // words from the gate's columns to the value's
+    float acc[2][8][MT][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[s][j][m][i] = 0.f;
+    ptx::pdl_wait();
+    const int blocks = a.K / 16, step = static_cast<int>(size) * kCodeWarps;
+#pragma unroll 2
+    for (int b = static_cast<int>(rank) * kCodeWarps + warp; b < blocks; b += step) {
+        const int64_t k = 16 * b + 4 * t;
+        uint32_t w[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) w[s][i] = live ? __ldg(wg + (k + i) * words + s * up) : 0u;
+        uint2 x[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            x[m] = 8 * m + g < a.M ? __ldg(reinterpret_cast<const uint2*>(a.X + (8 * m + g) * static_cast<int64_t>(a.K) + k)) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t l0 = halves(w[s][0], w[s][1], false), h0 = halves(w[s][0], w[s][1], true);
+            const uint32_t l1 = halves(w[s][2], w[s][3], false), h1 = halves(w[s][2], w[s][3], true);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                constexpr uint32_t TOP = 0xC000C000u;
+                const int sh = 14 - 2 * j;
+                const uint32_t a0 = (l0 << sh) & TOP, a1 = (h0 << sh) & TOP, a2 = (l1 << sh) & TOP, a3 = (h1 << sh) & TOP;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma_tokens(acc[s][j][m], a0, a1, a2, a3, x[m].x, x[m].y);
+            }
+        }
+    }
+    // column 16 g + c of a half lies at 8 c + g: lanes of a store in different banks
+    float* mine = part + warp * (8 * MT) * kCodePad;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mine[(8 * m + 2 * t + (i & 1)) * kCodePad + s * kCodeOut + 8 * (j + 8 * (i >> 1)) + g] = acc[s][j][m][i];
+    __syncthreads();
+    // the warps' sums, in place of the first warp's
+    for (int e = threadIdx.x; e < 8 * MT * kCodeCols; e += kCodeWarps * 32) {
+        const int at = (e / kCodeCols) * kCodePad + e % kCodeCols;
+        float v = part[at];
+#pragma unroll
+        for (int w = 1; w < kCodeWarps; ++w) v += part[w * (8 * MT) * kCodePad + at];
+        part[at] = v;
+    }
+    if (size > 1) ptx::cluster_sync(); else __syncthreads();
+    const int per = kCodeOut / static_cast<int>(size);
+    for (int e = threadIdx.x; e < per * a.M; e += kCodeWarps * 32) {
+        const int m = e / per, c = e % per + static_cast<int>(rank) * per;
+        const int at = m * kCodePad + 8 * (c & 15) + (c >> 4);
+        float vg = 0.f, vu = 0.f;
+        if (size > 1) {
+            for (uint32_t r = 0; r < size; ++r) {
+                float pg, pu;
+                const uint32_t from = ptx::mapa_shared(ptx::smem_u32(part + at), r);
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pg) : "r"(from) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pu) : "r"(from + kCodeOut * 4u) : "memory");
+                vg += pg;
+                vu += pu;
+            }
+        } else {
+            vg = part[at], vu = part[at + kCodeOut];
+        }
+        const int n = n0 + c;
+        if (n < a.N) {
+            // half of the sums: the operand was twice the weight
+            vg *= 0.5f * __ldg(a.scale + n);
+            vu *= 0.5f * __ldg(a.scale + a.N + n);
+            float f, d;
+            switch (a.act) {
+            case TERN_ACT_SILU: activate<TERN_ACT_SILU, false>(vg, f, d); break;
+            case TERN_ACT_GELU: activate<TERN_ACT_GELU, false>(vg, f, d); break;
+            case TERN_ACT_RELU2: activate<TERN_ACT_RELU2, false>(vg, f, d); break;
+            default: activate<TERN_ACT_SIGMOID, false>(vg, f, d); break;
+            }
+            a.H[m * static_cast<int64_t>(a.N) + n] = __bfloat16_as_ushort(__float2bfloat16_rn(f * vu));
+        }
+    }
+    if (size > 1) ptx::cluster_sync();   // the peers have read this block's sums
+}
+
+// ------------------------------------------------------------------------------ gradient from factors
+// dY = dH f_g | dH f_u, eight elements of a row a thread; dY may lie in place of the factors.
+__global__ void __launch_bounds__(256) glu_factors(const uint16_t* __restrict__ dH, const uint16_t* saved, uint16_t* dY, int64_t rows, int N) {
+    using B = __nv_bfloat16;
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+    const int units = N / 8;
+    const int64_t total = rows * units, step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total; e += step) {
+        const int64_t row = e / units;
+        const int c = static_cast<int>(e - row * units) * 8;
+        const auto d = load_raw<B, 8>(reinterpret_cast<const B*>(dH) + row * N + c);
+        const int64_t at = row * 2 * N + c;
+        const uint4* ps = reinterpret_cast<const uint4*>(saved + at);
+        const uint4 fg = *ps, fu = *reinterpret_cast<const uint4*>(saved + at + N);
+        Raw<B, 8> rg, ru;
+        rg.w[0] = fg.x, rg.w[1] = fg.y, rg.w[2] = fg.z, rg.w[3] = fg.w;
+        ru.w[0] = fu.x, ru.w[1] = fu.y, ru.w[2] = fu.z, ru.w[3] = fu.w;
+        float vg[8], vu[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = raw_at<B, 8>(d, i);
+            vg[i] = x * raw_at<B, 8>(rg, i);
+            vu[i] = x * raw_at<B, 8>(ru, i);
+        }
+        store_as<B, 8>(reinterpret_cast<B*>(dY) + at, vg);
+        store_as<B, 8>(reinterpret_cast<B*>(dY) + at + N, vu);
+    }
+}
+
+// ------------------------------------------------------------------------------ host side
+template <class C>
+int glu_units(int num_sms, int* units) {
+    static std::once_flag once[64];
+    static cudaError_t status[64];
+    static int pairs[64];
+    int dev = 0;
+    TERN_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return TERN_ERR_DEVICE;
+    std::call_once(once[dev], [&] {
+        status[dev] = cudaFuncSetAttribute(tern_glu_gemm<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        if (status[dev] != cudaSuccess || C::CG == 1) return;
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2 * (num_sms / 2));
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM_BYTES;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        status[dev] = cudaOccupancyMaxActiveClusters(&n, tern_glu_gemm<C>, &cfg);
+        pairs[dev] = n > 0 ? n : 1;
+    });
+    TERN_CUDA_TRY(status[dev]);
+    *units = C::CG == 2 ? pairs[dev] : num_sms;
+    return TERN_OK;
+}
+
+// Launched as the other GEMMs: after every earlier kernel of the stream has completed.
+template <class C>
+int glu_gemm(GluArgs& a, const uint16_t* X, const uint16_t* T, int num_sms, cudaStream_t s) {
+    a.tiles_m = (a.M + C::TILE_M - 1) / C::TILE_M;
+    a.tiles_n = (a.N + C::HN - 1) / C::HN;
+    a.num_kb = (a.K + C::BK - 1) / C::BK;
+    if (int st = tensor_map_2d(&a.mX, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.K, a.M, C::BK, kBM, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
+    if (int st = tensor_map_2d(&a.mT, T, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2 * static_cast<int64_t>(a.N), a.K, 64, C::BK, CU_TENSOR_MAP_SWIZZLE_128B))
+        return st;
+    int units = 0;
+    if (int st = glu_units<C>(num_sms, &units)) return st;
+    const int grid = C::CG * static_cast<int>(std::min<int64_t>(static_cast<int64_t>(a.tiles_m) * a.tiles_n, units));
+    return launch_cluster(tern_glu_gemm<C>, grid, C::THREADS, C::SMEM_BYTES, C::CG, false, s, a);
+}
+
+int glu_many(GluArgs& a, const uint16_t* X, const uint16_t* T, int num_sms, cudaStream_t s) {
+    return a.M > kBM ? glu_gemm<GluPair>(a, X, T, num_sms, s) : glu_gemm<GluOne>(a, X, T, num_sms, s);
+}
+
+int glu_few(const CodeArgs& a, int num_sms, cudaStream_t s) {
+    const int tiles = (a.N + kCodeOut - 1) / kCodeOut, blocks = a.K / 16;
+    // clusters until the SMs have a block each, as long as every warp keeps a block of rows
+    int c = 1;
+    while (c < 8 && tiles * c < num_sms && blocks > c * kCodeWarps) c *= 2;
+    const int MT = a.M <= 8 ? 1 : 2;
+    const size_t smem = static_cast<size_t>(kCodeWarps) * 8 * MT * kCodePad * sizeof(float);
+    if (MT == 1) return launch_cluster(glu_codes<1>, tiles * c, kCodeWarps * 32, smem, c, true, s, a);
+    return launch_cluster(glu_codes<2>, tiles * c, kCodeWarps * 32, smem, c, true, s, a);
+}
+
+bool glu_dims(int64_t M, int64_t K, int64_t N) {
+    // 2N columns within 31 bits; rows of dY and of the weight within the tensor maps' limits
+    return M >= 0 && K >= 16 && N >= 16 && M < (1ll << 31) - 1024 && K < (1ll << 31) - 1024 && N < (1ll << 30) - 1024 && M * K < (1ll << 40) &&
+           K * N < (1ll << 39) && M * N < (1ll << 39) &&
+           ((M + 127) / 128) * ((N + 63) / 64) < (1ll << 31) - 1024;
+}
+
+}  // namespace
+
+int glu_status_read(int clear) {
+    int v = 0;
+    TERN_CUDA_TRY(cudaMemcpyFromSymbol(&v, g_glu_status, sizeof(int)));
+    if (clear) {
+        const int zero = 0;
+        TERN_CUDA_TRY(cudaMemcpyToSymbol(g_glu_status, &zero, sizeof(int)));
+    }
+    return v ? TERN_ERR_TIMEOUT : TERN_OK;
+}
+
+}  // namespace tern
+
+using namespace tern;
+
+extern "C" int tern_glu_fwd(const uint16_t* X, const tern_tiles* W, const float* scale, int act, uint16_t* H, uint16_t* saved, int64_t M,
+                            int64_t K, int64_t N, void* stream) {
+    if (!glu_dims(M, K, N) || act < TERN_ACT_SILU || act > TERN_ACT_SIGMOID) return TERN_ERR_ARG;
+    if (K % 16 || N % 16) return TERN_ERR_ALIGN;
+    if (M == 0) return TERN_OK;
+    if (!X || !W || !scale || !H) return TERN_ERR_ARG;
+    const bool codes = M <= kCodeRows && !saved && W->packed;
+    if (!codes && !W->t_bf16) return TERN_ERR_ARG;
+    const void* weight = codes ? static_cast<const void*>(W->packed) : static_cast<const void*>(W->t_bf16);
+    if (!aligned16(X) || !aligned16(weight) || !aligned16(scale) || !aligned16(H) || !aligned16(saved)) return TERN_ERR_ALIGN;
+    int num_sms = 0;
+    if (int st = check_device(&num_sms)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (codes) {
+        const CodeArgs c{X, W->packed, scale, H, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), act};
+        return glu_few(c, num_sms, s);
+    }
+    GluArgs a{};
+    a.scale = scale, a.H = H, a.pair = saved;
+    a.M = static_cast<int>(M), a.N = static_cast<int>(N), a.K = static_cast<int>(K), a.act = act;
+    return glu_many(a, X, W->t_bf16, num_sms, s);
+}
+
+extern "C" int tern_glu_bwd(const uint16_t* dH, const uint16_t* saved, const uint16_t* X, const tern_tiles* W, const float* scale, int act,
+                            uint16_t* dY, int64_t M, int64_t K, int64_t N, void* stream) {
+    if (!glu_dims(M, saved ? 16 : K, N) || act < TERN_ACT_SILU || act > TERN_ACT_SIGMOID) return TERN_ERR_ARG;
+    if (N % 16 || (!saved && K % 16)) return TERN_ERR_ALIGN;
+    if (M == 0) return TERN_OK;
+    if (!dH || !dY || (!saved && (!X || !W || !W->t_bf16 || !scale))) return TERN_ERR_ARG;
+    if (!aligned16(dH) || !aligned16(dY) || !aligned16(saved)) return TERN_ERR_ALIGN;
+    if (!saved && (!aligned16(X) || !aligned16(W->t_bf16) || !aligned16(scale))) return TERN_ERR_ALIGN;
+    int num_sms = 0;
+    if (int st = check_device(&num_sms)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (saved) {
+        const int64_t units = M * (N / 8);
+        const int grid = static_cast<int>(std::min<int64_t>((units + 255) / 256, static_cast<int64_t>(num_sms) * 8));
+        return launch_pdl(glu_factors, dim3(grid), dim3(256), 0, s, dH, saved, dY, M, static_cast<int>(N));
+    }
+    GluArgs a{};
+    a.scale = scale, a.dH = dH, a.pair = dY;
+    a.M = static_cast<int>(M), a.N = static_cast<int>(N), a.K = static_cast<int>(K), a.act = act;
+    return glu_many(a, X, W->t_bf16, num_sms, s);
+}

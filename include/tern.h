@@ -512,6 +512,36 @@ int tern_norm_bwd(const void* x, int x_dtype, int64_t ld_x, const float* weight,
                   const void* dy, int y_dtype, int64_t ld_dy, int64_t n, int64_t D, void* dx, int64_t ld_dx,
                   float* dweight, float* dbias, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * Gated feed-forward layer: one ternary weight [K][2N] holds the gate's N columns and then the value's,
+ *   g | u = scale * (X T)         as tern_linear_fwd's Y of the K x 2N weight
+ *   H     = act(g) * u            bf16 [M][N]
+ * in one kernel.  act: TERN_ACT_SILU g sigmoid(g), TERN_ACT_GELU g Phi(g) (to 1e-7 in Phi),
+ * TERN_ACT_RELU2 max(g, 0)^2, TERN_ACT_SIGMOID sigmoid(g).
+ *   X [M][K] bf16, scale [2N] fp32, W the tiles of the K x 2N weight.  Up to 16 rows without `saved`
+ *   read W->packed where it is given (single tokens: an eighth of the bytes); every other call, and
+ *   those without W->packed, reads W->t_bf16 (NULL: TERN_ERR_ARG).
+ *   saved [M][2N] bf16, or NULL: the factors  u act'(g) | act(g)  that tern_glu_bwd multiplies.
+ * K, N multiples of 16, at least 16 (tern_materialize wants no more); M >= 0; dense matrices, every
+ * pointer 16-byte aligned.  H is rounded once from fp32.
+ */
+#define TERN_ACT_SILU 0
+#define TERN_ACT_GELU 1
+#define TERN_ACT_RELU2 2
+#define TERN_ACT_SIGMOID 3
+int tern_glu_fwd(const uint16_t* X, const tern_tiles* W, const float* scale, int act, uint16_t* H, uint16_t* saved,
+                 int64_t M, int64_t K, int64_t N, void* stream);
+/*
+ * Its gradient up to the projection: from dH bf16 [M][N]
+ *   dY [M][2N] bf16 = dH u act'(g) | dH act(g)
+ * which is the dY that tern_linear_bwd (or _grouped) of the K x 2N weight takes for dX, gq and sgrad.
+ * With `saved` (from tern_glu_fwd, which dY may replace in place) it is one product an element, of
+ * factors rounded to bf16; X, W, scale, act and K are not read then.  With saved NULL g and u are
+ * computed again from X, W->t_bf16 and scale, and dY is rounded once.
+ */
+int tern_glu_bwd(const uint16_t* dH, const uint16_t* saved, const uint16_t* X, const tern_tiles* W, const float* scale,
+                 int act, uint16_t* dY, int64_t M, int64_t K, int64_t N, void* stream);
+
 /* Text of a status code (static storage). */
 const char* tern_strerror(int status);
 
