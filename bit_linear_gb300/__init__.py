@@ -20,10 +20,13 @@ current stream.  The functions carry the C names:
     tern_norm_bwd(x, dy, mean, rstd, dx, workspace=None, weight=None, dweight=None, dbias=None)
     tern_glu_fwd(X, tiles, scale, H, saved=None, act="silu")
     tern_glu_bwd(dH, dY, saved=None, X=None, tiles=None, scale=None, act="silu")
+    tern_score(logits, tokens=None, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None)
+    tern_distill(logits, ids, top, loss, lse=None, dlogits=None, weight=None, temperature=1.0)
+    tern_distill_bwd(logits, ids, top, lse, dlogits, weight=None, temperature=1.0)
 
 Materialize, MaterializeGrouped, GroupedForward, GroupedBackward, MultiAdamW, EmbedForward,
 EmbedBackward, ScanForward, ScanBackward, ScanStep, Orthogonalize, NormForward, NormBackward,
-GluForward and GluBackward are the same calls with their arguments checked and marshalled once, for loops that repeat them on the
+GluForward, GluBackward, Score, Distill and DistillBackward are the same calls with their arguments checked and marshalled once, for loops that repeat them on the
 same buffers.
 
 Importing this package loads ``lib/libtern.so``; if it is missing the import
@@ -55,6 +58,7 @@ TERN_ADAM_MAX_TENSORS = 64
 TERN_BWD_ACCUMULATE = 1
 TERN_BWD_DX_SPLIT8 = 2
 TERN_BF16, TERN_F32, TERN_I32, TERN_I64 = 0, 1, 2, 3
+TERN_SCORE_MAX_TOP, TERN_DISTILL_MAX_TOP = 64, 256
 TERN_ACT_SILU, TERN_ACT_GELU, TERN_ACT_RELU2, TERN_ACT_SIGMOID = 0, 1, 2, 3
 
 # the C ABI's exported symbols (tests check the library exports every one)
@@ -67,7 +71,7 @@ ABI_SYMBOLS = ("tern_tiles_bytes", "tern_materialize", "tern_materialize_grouped
                "tern_scan_bwd_workspace", "tern_scan_bwd", "tern_scan_step",
                "tern_orthogonalize_workspace", "tern_orthogonalize",
                "tern_norm_fwd", "tern_norm_bwd_workspace", "tern_norm_bwd",
-               "tern_glu_fwd", "tern_glu_bwd", "tern_strerror",
+               "tern_glu_fwd", "tern_glu_bwd", "tern_score", "tern_distill", "tern_distill_bwd", "tern_strerror",
                "tern_device_status", "tern_device_diagnostics", "tern_selftest_wait_timeout")
 
 
@@ -104,6 +108,12 @@ class _Scan(ctypes.Structure):
     _fields_ = [("f", _Act), ("v", _Act), ("r", _Act), ("f_bias", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
                 ("starts", ctypes.c_void_p), ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
                 ("dtype", ctypes.c_int)]
+
+
+class _Distillation(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("n", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("ids_dtype", ctypes.c_int), ("ids", ctypes.c_void_p), ("top", ctypes.c_void_p),
+                ("k", ctypes.c_int), ("temperature", ctypes.c_float), ("weight", ctypes.c_void_p)]
 
 
 def _load():
@@ -150,6 +160,9 @@ def _load():
         "tern_norm_bwd": ([vp, ci, i64, vp, vp, vp, vp, ci, i64, i64, i64, vp, i64, vp, vp, vp, sz, vp], ci),
         "tern_glu_fwd": ([vp, tp, vp, ci, vp, vp, i64, i64, i64, vp], ci),
         "tern_glu_bwd": ([vp, vp, vp, tp, vp, ci, vp, i64, i64, i64, vp], ci),
+        "tern_score": ([vp, ci, i64, i64, i64, vp, ci, vp, vp, vp, ci, vp, vp, vp], ci),
+        "tern_distill": ([ctypes.POINTER(_Distillation), vp, vp, vp, i64, vp], ci),
+        "tern_distill_bwd": ([ctypes.POINTER(_Distillation), vp, vp, i64, vp], ci),
         "tern_strerror": ([ci], ctypes.c_char_p),
         "tern_device_status": ([vp, ci], ci),
         "tern_device_diagnostics": ([ctypes.POINTER(i64), ci], ci),
@@ -854,6 +867,88 @@ class GluBackward:
 def tern_glu_bwd(dH, dY, saved=None, X=None, tiles=None, scale=None, act="silu", stream=None):
     """dY [M, 2 N] bf16 = dH u act'(g) | dH act(g): from `saved`, or from X, tiles and scale again."""
     GluBackward(dH, dY, saved, X, tiles, scale, act)(stream)
+
+
+_IDS = (torch.int32, torch.int64)
+
+
+class Score:
+    """tern_score with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, logits, tokens=None, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None):
+        kind = _kind(logits, _FLOATS, "logits")
+        n, V = logits.shape
+        xp, ld = _rows(logits, logits.dtype, (n, V), "logits")
+        if logp is not None and tokens is None:
+            raise ValueError("logp wants tokens")
+        if (top_ids is None) != (top_logp is None):
+            raise ValueError("top_ids and top_logp are given together")
+        k = 0 if top_ids is None else top_ids.shape[1]
+        tk = TERN_I64 if tokens is None else _kind(tokens, _IDS, "tokens")
+        row = lambda t, name: _ptr(t, torch.float32, (n,), name)  # noqa: E731
+        self._args = (xp, kind, ld, n, V, None if tokens is None else _ptr(tokens, tokens.dtype, (n,), "tokens"), tk, row(logp, "logp"),
+                      row(entropy, "entropy"), row(lse, "lse"), k, _ptr(top_ids, torch.int32, (n, k), "top_ids"),
+                      _ptr(top_logp, torch.float32, (n, k), "top_logp"))
+        self._refs = (logits, tokens, logp, entropy, lse, top_ids, top_logp)
+        _same_device(*self._refs)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_score(*self._args, _stream(stream)), "tern_score")
+
+
+def tern_score(logits, tokens=None, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None, stream=None):
+    """Of the rows of logits [n, V]: the log probability of a token each, the entropy, log sum exp, and the
+    k most likely entries (top_ids int32 and top_logp [n, k], largest first, the lower id first where equal)."""
+    Score(logits, tokens, logp, entropy, lse, top_ids, top_logp)(stream)
+
+
+def _distillation(logits, ids, top, weight, temperature):
+    kind = _kind(logits, _FLOATS, "logits")
+    n, V = logits.shape
+    xp, ld = _rows(logits, logits.dtype, (n, V), "logits")
+    k = ids.shape[1]
+    return _Distillation(xp, ld, n, V, kind, _kind(ids, _IDS, "ids"), _ptr(ids, ids.dtype, (n, k), "ids"), _ptr(top, torch.float32, (n, k), "top"),
+                         k, float(temperature), _ptr(weight, torch.float32, (n,), "weight"))
+
+
+class Distill:
+    """tern_distill with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, logits, ids, top, loss, lse=None, dlogits=None, weight=None, temperature=1.0):
+        self._t = _distillation(logits, ids, top, weight, temperature)
+        n = logits.shape[0]
+        dp, ldd = (None, 0) if dlogits is None else _rows(dlogits, logits.dtype, logits.shape, "dlogits")
+        self._args = (ctypes.byref(self._t), _ptr(loss, torch.float32, (n,), "loss"), _ptr(lse, torch.float32, (n,), "lse"), dp, ldd)
+        self._refs = (logits, ids, top, loss, lse, dlogits, weight)
+        _same_device(*self._refs)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_distill(*self._args, _stream(stream)), "tern_distill")
+
+
+def tern_distill(logits, ids, top, loss, lse=None, dlogits=None, weight=None, temperature=1.0, stream=None):
+    """loss [n] of student logits [n, V] against a teacher's entries (ids and top logits [n, k]), and where
+    given lse and dlogits (the gradient of the sum of the losses, in place of the logits if it is they)."""
+    Distill(logits, ids, top, loss, lse, dlogits, weight, temperature)(stream)
+
+
+class DistillBackward:
+    """tern_distill_bwd with its arguments marshalled once; see GroupedForward."""
+
+    def __init__(self, logits, ids, top, lse, dlogits, weight=None, temperature=1.0):
+        self._t = _distillation(logits, ids, top, weight, temperature)
+        dp, ldd = _rows(dlogits, logits.dtype, logits.shape, "dlogits")
+        self._args = (ctypes.byref(self._t), _ptr(lse, torch.float32, (logits.shape[0],), "lse"), dp, ldd)
+        self._refs = (logits, ids, top, lse, dlogits, weight)
+        _same_device(*self._refs)
+
+    def __call__(self, stream=None):
+        _check(lib.tern_distill_bwd(*self._args, _stream(stream)), "tern_distill_bwd")
+
+
+def tern_distill_bwd(logits, ids, top, lse, dlogits, weight=None, temperature=1.0, stream=None):
+    """dlogits of tern_distill from its lse."""
+    DistillBackward(logits, ids, top, lse, dlogits, weight, temperature)(stream)
 
 
 def tern_device_status(stream=None, clear=True) -> int:

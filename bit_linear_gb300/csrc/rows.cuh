@@ -28,16 +28,16 @@ __device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
     if constexpr (B >= 16) {
 #pragma unroll
         for (int i = 0; i < B / 16; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            const uint4 u = reinterpret_cast<const uint4*>(p)[i];
             r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
         }
     } else if constexpr (B == 8) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
         r.w[0] = u.x, r.w[1] = u.y;
     } else if constexpr (B == 4) {
-        r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        r.w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
-        r.w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+        r.w[0] = *reinterpret_cast<const unsigned short*>(p);
     }
     return r;
 }

@@ -542,6 +542,53 @@ int tern_glu_fwd(const uint16_t* X, const tern_tiles* W, const float* scale, int
 int tern_glu_bwd(const uint16_t* dH, const uint16_t* saved, const uint16_t* X, const tern_tiles* W, const float* scale,
                  int act, uint16_t* dY, int64_t M, int64_t K, int64_t N, void* stream);
 
+/*
+ * Scores of n rows of V logits (`dtype`: TERN_BF16 or TERN_F32), in one reading:
+ *   lse     [n] fp32 = log sum exp(x)
+ *   logp    [n] fp32 = x[token] - lse of the row's token (TERN_I32 or TERN_I64); 0 for an id outside 0..V-1
+ *   entropy [n] fp32 of softmax(x)
+ *   top_ids [n][k] int32, top_logp [n][k] fp32: the k largest logits and their x - lse, largest first, the
+ *           lower id first where equal
+ * logp, entropy and lse may be NULL (so may tokens without logp); 0 <= k <= TERN_SCORE_MAX_TOP and V, and
+ * with k = 0 the last two are not used.  Masked entries are -inf: they have probability 0 and rank
+ * last, by id.  A row of nothing else has lse and every log probability -inf and entropy 0.  A row with
+ * NaN or +inf gives NaN (its largest entries are still found; NaN ranks above +inf).
+ * n < 2^27, V < 2^31 - 65536.
+ */
+#define TERN_SCORE_MAX_TOP 64
+int tern_score(const void* logits, int dtype, int64_t ld, int64_t n, int64_t V, const void* tokens, int tokens_dtype,
+               float* logp, float* entropy, float* lse, int k, int32_t* top_ids, float* top_logp, void* stream);
+
+/*
+ * Distillation: the loss of n rows of student logits x [V] against a teacher's k entries a row (its top
+ * logits, or log probabilities as tern_score gives them),
+ *   p = softmax(top / T) over the row's entries, q = softmax(x / T)
+ *   loss    = w T^2 sum p (log p - log q[id])
+ *   dlogits = w T (q - p)                              the gradient of the sum of the losses
+ * Entries whose id is outside 0..V-1, and those of -inf, are left out; an id given twice counts with
+ * both probabilities.  A row without entries, or of weight 0, has loss, lse and gradient 0 whatever
+ * its logits hold.  With k = 1 this is cross entropy of the id (top may be NULL then).
+ */
+#define TERN_DISTILL_MAX_TOP 256
+typedef struct tern_distillation {
+    const void* logits;   /* [n] rows of V, `dtype` (TERN_BF16 or TERN_F32), ld apart */
+    int64_t ld, n, V;
+    int dtype, ids_dtype; /* ids: TERN_I32 or TERN_I64 */
+    const void* ids;      /* [n][k] */
+    const float* top;     /* [n][k] */
+    int k;                /* 1 .. TERN_DISTILL_MAX_TOP */
+    float temperature;    /* T, 1e-6 .. 1e6 */
+    const float* weight;  /* [n] w, or NULL (1) */
+} tern_distillation;
+/*
+ * loss [n] fp32, and unless NULL lse [n] fp32 = log sum exp(x / T) and dlogits (the logits' type, rounded
+ * once; it may be the logits themselves, with the same ld): with dlogits the row is read and its
+ * gradient written in the same call.
+ */
+int tern_distill(const tern_distillation* t, float* loss, float* lse, void* dlogits, int64_t ld_dlogits, void* stream);
+/* The gradient alone, from tern_distill's lse. */
+int tern_distill_bwd(const tern_distillation* t, const float* lse, void* dlogits, int64_t ld_dlogits, void* stream);
+
 /* Text of a status code (static storage). */
 const char* tern_strerror(int status);
 
