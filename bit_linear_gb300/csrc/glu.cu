@@ -100,7 +100,7 @@ struct GluCfg {
     static constexpr int A_BYTES = kBM * BK * 2, B_BYTES = B_COLS * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int RASTER = 16 / CG;      // as in the ternary forward
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int EPI_WARPS = 16, THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "TMEM allocation must be a power of two");
     static_assert(SMEM_BYTES <= 232448 && B_COLS % 64 == 0, "stage");
@@ -110,34 +110,22 @@ __device__ __forceinline__ bool glu_wait(uint32_t bar, uint32_t parity, volatile
     return wait_limited(bar, parity, abort_flag, watch, kWaitLimitNs, [] { atomicExch(&g_glu_status, 1); });
 }
 
-// 32 rows (a lane each) of 32 bf16, four 16-byte units a lane: within four lanes the 4 x 4 units are
-// transposed by shuffles, so that a store writes whole 64-byte rows, eight at a time.
-__device__ __forceinline__ void store_rows(uint16_t* base, int64_t ld, int rows, int cols, const uint32_t (&w)[16], int lane) {
-    uint4 u[4];
+// 32 rows (a lane each) of 16 bf16, two 16-byte units a lane: neighbouring lanes swap one, so that a store
+// writes whole 32-byte sectors, of sixteen rows at a time.
+__device__ __forceinline__ void store_rows(uint16_t* base, int64_t ld, int rows, const uint32_t (&w)[8], int lane) {
+    const bool odd = lane & 1;
+    uint32_t give[4], keep[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int i = 0; i < 4; ++i) give[i] = odd ? w[i] : w[4 + i], keep[i] = odd ? w[4 + i] : w[i];
 #pragma unroll
-    for (int d = 2; d >= 1; d >>= 1) {
-        const bool upper = (lane & d) != 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & d) continue;
-            const uint4 send = upper ? u[i] : u[i | d];
-            uint4 recv;
-            recv.x = __shfl_xor_sync(0xffffffffu, send.x, d);
-            recv.y = __shfl_xor_sync(0xffffffffu, send.y, d);
-            recv.z = __shfl_xor_sync(0xffffffffu, send.z, d);
-            recv.w = __shfl_xor_sync(0xffffffffu, send.w, d);
-            if (upper) u[i] = recv;
-            else u[i | d] = recv;
-        }
-    }
-    const int q = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (lane & ~3) + i;
-        if (r < rows && 8 * q < cols) *reinterpret_cast<uint4*>(base + static_cast<int64_t>(r) * ld + 8 * q) = u[i];
-    }
+    for (int i = 0; i < 4; ++i) give[i] = __shfl_xor_sync(0xffffffffu, give[i], 1);
+    // an even lane has its own first unit and its neighbour's, an odd lane the second units
+    const int r = lane & ~1;
+    uint16_t* to = base + r * ld + 8 * (lane & 1);
+    const uint4 lower = odd ? make_uint4(give[0], give[1], give[2], give[3]) : make_uint4(keep[0], keep[1], keep[2], keep[3]);
+    const uint4 upper = odd ? make_uint4(keep[0], keep[1], keep[2], keep[3]) : make_uint4(give[0], give[1], give[2], give[3]);
+    if (r < rows) *reinterpret_cast<uint4*>(to) = lower;
+    if (r + 1 < rows) *reinterpret_cast<uint4*>(to + ld) = upper;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -145,61 +133,54 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// 32 outputs of a lane's row, columns c0..c0+31, from the accumulators at TMEM columns tg (the gate's)
-// and tu (the value's): H, or H and the factors, or dY.  Sixteen columns at a time, which the
-// registers hold beside the results.
+// 16 outputs of a lane's row, columns c0..c0+15, from the accumulators at TMEM columns tg (the gate's)
+// and tu (the value's): H, or H and the factors, or dY.
 template <int ACT, bool BACK, bool TWO>
 __device__ __forceinline__ void glu_chunk(const GluArgs& a, uint32_t tg, uint32_t tu, int wrow, int c0, int lane) {
-    const int cols = min(32, a.N - c0);   // a multiple of 16
-    const int rows = a.M - wrow;          // > 0
-    uint32_t h[16], p[16], q[16];
+    const int rows = a.M - wrow;   // > 0
+    uint32_t h[8], p[8], q[8];
+    uint32_t rg[16], ru[16];
+    ptx::tmem_ld_32x32b_x16(tg, rg);
+    ptx::tmem_ld_32x32b_x16(tu, ru);
+    Raw<__nv_bfloat16, 16> dh;
+    if (BACK) dh = load_raw<__nv_bfloat16, 16>(reinterpret_cast<const __nv_bfloat16*>(a.dH) + (wrow + min(lane, rows - 1)) * static_cast<int64_t>(a.N) + c0);
+    const float4* pg = reinterpret_cast<const float4*>(a.scale + c0);
+    const float4* pu = reinterpret_cast<const float4*>(a.scale + a.N + c0);
+    ptx::tmem_wait_ld();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        uint32_t rg[16], ru[16];
-        ptx::tmem_ld_32x32b_x16(tg + 16 * half, rg);
-        ptx::tmem_ld_32x32b_x16(tu + 16 * half, ru);
-        const int c = min(c0 + 16 * half, a.N - 16);   // past the last column: anything readable, not stored
-        Raw<__nv_bfloat16, 16> dh;
-        if (BACK) dh = load_raw<__nv_bfloat16, 16>(reinterpret_cast<const __nv_bfloat16*>(a.dH) + (wrow + min(lane, rows - 1)) * static_cast<int64_t>(a.N) + c);
-        const float4* pg = reinterpret_cast<const float4*>(a.scale + c);
-        const float4* pu = reinterpret_cast<const float4*>(a.scale + a.N + c);
-        ptx::tmem_wait_ld();
+    for (int b = 0; b < 4; ++b) {   // four columns
+        const float4 sg = __ldg(pg + b), su = __ldg(pu + b);
+        const float g[4] = {__uint_as_float(rg[4 * b]) * sg.x, __uint_as_float(rg[4 * b + 1]) * sg.y, __uint_as_float(rg[4 * b + 2]) * sg.z,
+                            __uint_as_float(rg[4 * b + 3]) * sg.w};
+        const float u[4] = {__uint_as_float(ru[4 * b]) * su.x, __uint_as_float(ru[4 * b + 1]) * su.y, __uint_as_float(ru[4 * b + 2]) * su.z,
+                            __uint_as_float(ru[4 * b + 3]) * su.w};
+        float f[4], d[4];
+        if constexpr (TWO) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {   // four columns
-            const float4 sg = __ldg(pg + b), su = __ldg(pu + b);
-            const float g[4] = {__uint_as_float(rg[4 * b]) * sg.x, __uint_as_float(rg[4 * b + 1]) * sg.y, __uint_as_float(rg[4 * b + 2]) * sg.z,
-                                __uint_as_float(rg[4 * b + 3]) * sg.w};
-            const float u[4] = {__uint_as_float(ru[4 * b]) * su.x, __uint_as_float(ru[4 * b + 1]) * su.y, __uint_as_float(ru[4 * b + 2]) * su.z,
-                                __uint_as_float(ru[4 * b + 3]) * su.w};
-            const int o = 8 * half + 2 * b;
-            float f[4], d[4];
-            if constexpr (TWO) {
+            for (int i = 0; i < 4; ++i) activate<ACT, true>(g[i], f[i], d[i]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) activate<ACT, true>(g[i], f[i], d[i]);
+            for (int i = 0; i < 4; ++i) d[i] *= u[i];
+            if constexpr (BACK) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] *= u[i];
-                if constexpr (BACK) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = raw_at<__nv_bfloat16, 16>(dh, 4 * b + i);
-                        d[i] *= x;
-                        f[i] *= x;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float x = raw_at<__nv_bfloat16, 16>(dh, 4 * b + i);
+                    d[i] *= x;
+                    f[i] *= x;
                 }
-                p[o] = pack_bf16(d[0], d[1]), p[o + 1] = pack_bf16(d[2], d[3]);
-                q[o] = pack_bf16(f[0], f[1]), q[o + 1] = pack_bf16(f[2], f[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) activate<ACT, false>(g[i], f[i], d[i]);
             }
-            if constexpr (!BACK) h[o] = pack_bf16(f[0] * u[0], f[1] * u[1]), h[o + 1] = pack_bf16(f[2] * u[2], f[3] * u[3]);
+            p[2 * b] = pack_bf16(d[0], d[1]), p[2 * b + 1] = pack_bf16(d[2], d[3]);
+            q[2 * b] = pack_bf16(f[0], f[1]), q[2 * b + 1] = pack_bf16(f[2], f[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) activate<ACT, false>(g[i], f[i], d[i]);
         }
+        if constexpr (!BACK) h[2 * b] = pack_bf16(f[0] * u[0], f[1] * u[1]), h[2 * b + 1] = pack_bf16(f[2] * u[2], f[3] * u[3]);
     }
-    if constexpr (!BACK) store_rows(a.H + static_cast<int64_t>(wrow) * a.N + c0, a.N, rows, cols, h, lane);
+    if constexpr (!BACK) store_rows(a.H + static_cast<int64_t>(wrow) * a.N + c0, a.N, rows, h, lane);
     if constexpr (TWO) {
         uint16_t* to = a.pair + static_cast<int64_t>(wrow) * 2 * a.N + c0;
-        store_rows(to, 2 * static_cast<int64_t>(a.N), rows, cols, p, lane);
-        store_rows(to + a.N, 2 * static_cast<int64_t>(a.N), rows, cols, q, lane);
+        store_rows(to, 2 * static_cast<int64_t>(a.N), rows, p, lane);
+        store_rows(to + a.N, 2 * static_cast<int64_t>(a.N), rows, q, lane);
     }
 }
 
@@ -214,7 +195,8 @@ __device__ __forceinline__ void glu_act(const GluArgs& a, uint32_t tg, uint32_t 
 }
 
 // Roles as in the ternary forward: warp 0 copies, warp 1 allocates TMEM and (in the leader) issues the
-// MMAs, warps 2-9 are the epilogue, two for each 32 rows.  Two accumulators, so that a tile's
+// MMAs, warps 2-17 are the epilogue, four for each 32 rows (with two, the epilogue's latencies showed
+// where K is small: 8192 x 512 x 1360 with gelu 31 us, its gradient 40).  Two accumulators, so that a tile's
 // epilogue runs beside the next tile's products.
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) tern_glu_gemm(const __grid_constant__ GluArgs a) {
@@ -358,8 +340,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_glu_gemm(const __grid_cons
         // ------------------------------------------------------------ epilogue
         const int quad = warp & 3;   // a warp may touch TMEM lanes 32 (warp % 4) .. + 31
         const uint32_t tempty_leader = CG == 2 ? ptx::mapa_shared(TEMPTY0, 0) : TEMPTY0;
-        constexpr int JPW = C::HN / 64;
-        const int j0 = ((warp - 2) / 4) * JPW;
+        constexpr int CHUNKS = C::HN / 16 / (C::EPI_WARPS / 4);   // of 16 columns, a warp's
+        const int j0 = ((warp - 2) / 4) * CHUNKS;
         int local = 0;
         for (int tile = unit; tile < total; tile += units, ++local) {
             const int acc = local & 1;
@@ -372,10 +354,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_glu_gemm(const __grid_cons
             if (wrow < a.M) {
                 const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::BN;
 #pragma unroll 1
-                for (int j = j0; j < j0 + JPW; ++j) {
-                    const int c0 = nt * C::HN + j * 32;
-                    if (c0 >= a.N) break;
-                    const uint32_t tg = trow + j * 32, tu = tg + C::HN;
+                for (int j = j0; j < j0 + CHUNKS; ++j) {
+                    const int c0 = nt * C::HN + j * 16;
+                    if (c0 >= a.N) break;   // N % 16 == 0
+                    const uint32_t tg = trow + j * 16, tu = tg + C::HN;
                     if (a.dH) glu_act<true, true>(a, tg, tu, wrow, c0, lane);
                     else if (a.pair) glu_act<false, true>(a, tg, tu, wrow, c0, lane);
                     else glu_act<false, false>(a, tg, tu, wrow, c0, lane);
@@ -412,6 +394,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_glu_gemm(const __grid_cons
 
 using GluPair = GluCfg<2, 128, 7>;
 using GluOne = GluCfg<1, 128, 4>;
+using GluPairNarrow = GluCfg<2, 64, 9>;   // for outputs of few tiles
+using GluOneNarrow = GluCfg<1, 64, 6>;
 
 // ------------------------------------------------------------------------------ a few rows
 //
@@ -424,12 +408,12 @@ using GluOne = GluCfg<1, 128, 4>;
 // lane (g, t) = (lane / 4, lane % 4) reads the words of 16 columns 16 g.. at the four weight rows
 // 4 t.. of a block of 16 rows, and MMA j takes its columns 16 g + j and 16 g + j + 8.
 //
-// A block has 128 outputs (128 columns of the gate, 128 of the value); its warps and, where there are
-// few blocks, the blocks of a cluster share the weight's rows.  Sums are added in a fixed order: a
-// warp's blocks of rows, the warps of a block, the blocks of a cluster.
-constexpr int kCodeOut = 128, kCodeWarps = 8;
-constexpr int kCodeCols = 2 * kCodeOut, kCodePad = kCodeCols + 4;   // the pad keeps a warp's stores free of conflicts
-constexpr int kCodeRows = 16;                                       // most rows of X
+// A block has 128 outputs: half of its eight warps take the gate's 128 columns, half the value's, and share
+// the weight's rows; where there are fewer blocks than SMs, the blocks of a cluster share them too.
+// Sums are added in a fixed order: a warp's blocks of rows, the warps of a block, the blocks of a cluster.
+constexpr int kCodeOut = 128, kCodeWarps = 4;       // warps for each of the two
+constexpr int kCodePad = kCodeOut + 4;              // the pad keeps a warp's stores free of conflicts
+constexpr int kCodeRows = 16;                       // most rows of X
 
 struct CodeArgs {
     const uint16_t* X;
@@ -449,110 +433,118 @@ __device__ __forceinline__ void mma_tokens(float (&c)[4], uint32_t a0, uint32_t 
 // Codes of eight columns at two rows: the lower (upper) halves of two words side by side.
 __device__ __forceinline__ uint32_t halves(uint32_t w0, uint32_t w1, bool upper) { return __byte_perm(w0, w1, upper ? 0x7632 : 0x5410); }
 
-template <int MT>   // tokens in eights
-__global__ void __launch_bounds__(kCodeWarps * 32) glu_codes(const __grid_constant__ CodeArgs a) {
-    extern __shared__ float part[];   // [warps][8 MT][kCodePad]
-    ptx::pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+template <int MT, int AHEAD>   // tokens in eights; blocks of 16 weight rows that a warp asks for at once
+__global__ void __launch_bounds__(kCodeWarps * 64, 2) glu_codes(const __grid_constant__ CodeArgs a) {
+    // [2][warps][8 MT][kCodePad] sums of the warps; then what the cluster's blocks push: [blocks][columns of one][2 M]
+    extern __shared__ float part[];
+    constexpr int SUMS = 8 * MT * kCodePad;
+    float* pushed = part + 2 * kCodeWarps * SUMS;
+    const int warp = (threadIdx.x >> 5) & (kCodeWarps - 1), side = threadIdx.x / (32 * kCodeWarps);   // 0: the gate
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint32_t rank, size;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(size));
+    if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    ptx::pdl_trigger();
     const int n0 = static_cast<int>(blockIdx.x / size) * kCodeOut;
     const int words = a.N / 8;                       // of a weight row: 2N / 16
     const bool live = n0 + 16 * g < a.N;             // N % 16 == 0
-    const uint32_t* wg = a.packed + (live ? n0 / 16 + g : 0);
-    const int up = a.N / 16;                         // words from the gate's columns to the value's
-    float acc[2][8][MT][4];
+    float acc[8][MT][4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[s][j][m][i] = 0.f;
-    ptx::pdl_wait();
-    const int blocks = a.K / 16, step = static_cast<int>(size) * kCodeWarps;
-#pragma unroll 2
-    for (int b = static_cast<int>(rank) * kCodeWarps + warp; b < blocks; b += step) {
-        const int64_t k = 16 * b + 4 * t;
-        uint32_t w[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) w[s][i] = live ? __ldg(wg + (k + i) * words + s * up) : 0u;
-        uint2 x[MT];
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-            x[m] = 8 * m + g < a.M ? __ldg(reinterpret_cast<const uint2*>(a.X + (8 * m + g) * static_cast<int64_t>(a.K) + k)) : make_uint2(0u, 0u);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const uint32_t l0 = halves(w[s][0], w[s][1], false), h0 = halves(w[s][0], w[s][1], true);
-            const uint32_t l1 = halves(w[s][2], w[s][3], false), h1 = halves(w[s][2], w[s][3], true);
+            for (int i = 0; i < 4; ++i) acc[j][m][i] = 0.f;
+    const int step = static_cast<int>(size) * kCodeWarps, b0 = static_cast<int>(rank) * kCodeWarps + warp;
+    const uint32_t* wp = a.packed + side * (a.N / 16) + (live ? n0 / 16 + g : 0) + (16 * static_cast<int64_t>(b0) + 4 * t) * words;
+    const int64_t wstep = 16 * static_cast<int64_t>(step) * words;
+    const uint16_t* xp = a.X + 16 * b0 + 4 * t + (g < a.M ? g : 0) * static_cast<int64_t>(a.K);
+    const int64_t up = 8 * static_cast<int64_t>(a.K);
+    const bool in0 = g < a.M, in1 = MT > 1 && 8 + g < a.M;
+    ptx::pdl_wait();
+    for (int left = (a.K / 16 - b0 + step - 1) / step; left > 0; left -= AHEAD) {   // this warp's blocks
+        uint32_t w[AHEAD][4];
+        uint2 x[AHEAD][MT];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                constexpr uint32_t TOP = 0xC000C000u;
-                const int sh = 14 - 2 * j;
-                const uint32_t a0 = (l0 << sh) & TOP, a1 = (h0 << sh) & TOP, a2 = (l1 << sh) & TOP, a3 = (h1 << sh) & TOP;
+        for (int q = 0; q < AHEAD; ++q) {
+            const bool in = q < left;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma_tokens(acc[s][j][m], a0, a1, a2, a3, x[m].x, x[m].y);
+            for (int i = 0; i < 4; ++i) w[q][i] = in && live ? __ldg(wp + i * words) : 0u;
+            x[q][0] = in && in0 ? __ldg(reinterpret_cast<const uint2*>(xp)) : make_uint2(0u, 0u);
+            if constexpr (MT > 1) x[q][MT - 1] = in && in1 ? __ldg(reinterpret_cast<const uint2*>(xp + up)) : make_uint2(0u, 0u);
+            wp += wstep;
+            xp += 16 * step;
+        }
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+            if (q < left) {
+                const uint32_t l0 = halves(w[q][0], w[q][1], false), h0 = halves(w[q][0], w[q][1], true);
+                const uint32_t l1 = halves(w[q][2], w[q][3], false), h1 = halves(w[q][2], w[q][3], true);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    constexpr uint32_t TOP = 0xC000C000u;
+                    const int sh = 14 - 2 * j;
+                    const uint32_t a0 = (l0 << sh) & TOP, a1 = (h0 << sh) & TOP, a2 = (l1 << sh) & TOP, a3 = (h1 << sh) & TOP;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) mma_tokens(acc[j][m], a0, a1, a2, a3, x[q][m].x, x[q][m].y);
+                }
             }
         }
     }
-    // column 16 g + c of a half lies at 8 c + g: lanes of a store in different banks
-    float* mine = part + warp * (8 * MT) * kCodePad;
+    // column 16 g + c lies at 8 c + g: lanes of a store in different banks
+    float* mine = part + (side * kCodeWarps + warp) * SUMS;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int i = 0; i < 2; ++i) {
+            const int token = 8 * m + 2 * t + i;
+            if (token < a.M) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mine[(8 * m + 2 * t + (i & 1)) * kCodePad + s * kCodeOut + 8 * (j + 8 * (i >> 1)) + g] = acc[s][j][m][i];
+                for (int j = 0; j < 8; ++j) {
+                    mine[token * kCodePad + 8 * j + g] = acc[j][m][i];
+                    mine[token * kCodePad + 8 * (j + 8) + g] = acc[j][m][i + 2];
+                }
+            }
+        }
     __syncthreads();
-    // the warps' sums, in place of the first warp's
-    for (int e = threadIdx.x; e < 8 * MT * kCodeCols; e += kCodeWarps * 32) {
-        const int at = (e / kCodeCols) * kCodePad + e % kCodeCols;
-        float v = part[at];
+    const int per = (kCodeOut + static_cast<int>(size) - 1) / static_cast<int>(size);   // columns that a block finishes
+    if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every block has started
+    // the warps' sums, to the block that finishes the column
+    for (int e = threadIdx.x; e < 2 * a.M * kCodeOut; e += 64 * kCodeWarps) {
+        const int at0 = e % kCodeOut, c = (at0 >> 3) + 16 * (at0 & 7), m = e / kCodeOut, of = m >= a.M, token = m - of * a.M;
+        const float* from = part + of * kCodeWarps * SUMS + token * kCodePad + at0;
+        float v = from[0];
 #pragma unroll
-        for (int w = 1; w < kCodeWarps; ++w) v += part[w * (8 * MT) * kCodePad + at];
-        part[at] = v;
+        for (int w = 1; w < kCodeWarps; ++w) v += from[w * SUMS];
+        const int to = c / per;
+        const uint32_t at = ptx::smem_u32(pushed + (static_cast<int>(rank) * 2 * a.M + m) * per + c - to * per);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ptx::mapa_shared(at, to)), "f"(v) : "memory");
     }
+    __syncwarp();
     if (size > 1) ptx::cluster_sync(); else __syncthreads();
-    const int per = kCodeOut / static_cast<int>(size);
-    for (int e = threadIdx.x; e < per * a.M; e += kCodeWarps * 32) {
-        const int m = e / per, c = e % per + static_cast<int>(rank) * per;
-        const int at = m * kCodePad + 8 * (c & 15) + (c >> 4);
+    for (int e = threadIdx.x; e < per * a.M; e += 64 * kCodeWarps) {
+        const int m = e / per, q = e - m * per, c = q + static_cast<int>(rank) * per, n = n0 + c;
+        if (c >= kCodeOut || n >= a.N) continue;
+        // half of the sums: the operand was twice the weight
+        const float sg = 0.5f * __ldg(a.scale + n), su = 0.5f * __ldg(a.scale + a.N + n);
         float vg = 0.f, vu = 0.f;
-        if (size > 1) {
-            for (uint32_t r = 0; r < size; ++r) {
-                float pg, pu;
-                const uint32_t from = ptx::mapa_shared(ptx::smem_u32(part + at), r);
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pg) : "r"(from) : "memory");
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pu) : "r"(from + kCodeOut * 4u) : "memory");
-                vg += pg;
-                vu += pu;
-            }
-        } else {
-            vg = part[at], vu = part[at + kCodeOut];
+#pragma unroll 4
+        for (int r = 0; r < static_cast<int>(size); ++r) {
+            vg += pushed[(r * 2 * a.M + m) * per + q];
+            vu += pushed[(r * 2 * a.M + a.M + m) * per + q];
         }
-        const int n = n0 + c;
-        if (n < a.N) {
-            // half of the sums: the operand was twice the weight
-            vg *= 0.5f * __ldg(a.scale + n);
-            vu *= 0.5f * __ldg(a.scale + a.N + n);
-            float f, d;
-            switch (a.act) {
-            case TERN_ACT_SILU: activate<TERN_ACT_SILU, false>(vg, f, d); break;
-            case TERN_ACT_GELU: activate<TERN_ACT_GELU, false>(vg, f, d); break;
-            case TERN_ACT_RELU2: activate<TERN_ACT_RELU2, false>(vg, f, d); break;
-            default: activate<TERN_ACT_SIGMOID, false>(vg, f, d); break;
-            }
-            a.H[m * static_cast<int64_t>(a.N) + n] = __bfloat16_as_ushort(__float2bfloat16_rn(f * vu));
+        vg *= sg;
+        vu *= su;
+        float f, d;
+        switch (a.act) {
+        case TERN_ACT_SILU: activate<TERN_ACT_SILU, false>(vg, f, d); break;
+        case TERN_ACT_GELU: activate<TERN_ACT_GELU, false>(vg, f, d); break;
+        case TERN_ACT_RELU2: activate<TERN_ACT_RELU2, false>(vg, f, d); break;
+        default: activate<TERN_ACT_SIGMOID, false>(vg, f, d); break;
         }
+        a.H[m * static_cast<int64_t>(a.N) + n] = __bfloat16_as_ushort(__float2bfloat16_rn(f * vu));
     }
-    if (size > 1) ptx::cluster_sync();   // the peers have read this block's sums
 }
 
 // ------------------------------------------------------------------------------ gradient from factors
@@ -632,19 +624,71 @@ int glu_gemm(GluArgs& a, const uint16_t* X, const uint16_t* T, int num_sms, cuda
     return launch_cluster(tern_glu_gemm<C>, grid, C::THREADS, C::SMEM_BYTES, C::CG, false, s, a);
 }
 
+template <class C>
+int64_t glu_rounds(const GluArgs& a, int num_sms) {
+    const int64_t tiles = static_cast<int64_t>((a.M + C::TILE_M - 1) / C::TILE_M) * ((a.N + C::HN - 1) / C::HN), units = num_sms / C::CG;
+    return (tiles + units - 1) / units;
+}
+template <class Wide, class Narrow>
+int glu_width(GluArgs& a, const uint16_t* X, const uint16_t* T, int num_sms, cudaStream_t s) {
+    // a narrow tile takes a little more than half of a wide one's time
+    if (glu_rounds<Narrow>(a, num_sms) * 5 < glu_rounds<Wide>(a, num_sms) * 9) return glu_gemm<Narrow>(a, X, T, num_sms, s);
+    return glu_gemm<Wide>(a, X, T, num_sms, s);
+}
 int glu_many(GluArgs& a, const uint16_t* X, const uint16_t* T, int num_sms, cudaStream_t s) {
-    return a.M > kBM ? glu_gemm<GluPair>(a, X, T, num_sms, s) : glu_gemm<GluOne>(a, X, T, num_sms, s);
+    return a.M > kBM ? glu_width<GluPair, GluPairNarrow>(a, X, T, num_sms, s) : glu_width<GluOne, GluOneNarrow>(a, X, T, num_sms, s);
 }
 
-int glu_few(const CodeArgs& a, int num_sms, cudaStream_t s) {
+constexpr int kCodeMost = 8;   // blocks of a cluster
+
+template <int MT>
+size_t code_smem(int M, int c) {
+    const int per = (kCodeOut + c - 1) / c;
+    return (static_cast<size_t>(2 * kCodeWarps) * 8 * MT * kCodePad + static_cast<size_t>(c) * 2 * M * per) * sizeof(float);
+}
+
+// Clusters of c blocks that are resident at once (with the shared memory of the most rows).
+template <int MT, int AHEAD>
+int code_room(int c, int* clusters) {
+    static std::once_flag once[64];
+    static cudaError_t status[64];
+    static int room[64][kCodeMost + 1];
+    int dev = 0;
+    TERN_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return TERN_ERR_DEVICE;
+    std::call_once(once[dev], [&] {
+        const size_t most = code_smem<MT>(8 * MT, 1) + 8 * MT * 64;   // the columns of uneven shares
+        status[dev] = cudaFuncSetAttribute(glu_codes<MT, AHEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+        for (int k = 1; k <= kCodeMost && status[dev] == cudaSuccess; ++k) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = k;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(64 * k);
+            cfg.blockDim = dim3(kCodeWarps * 64);
+            cfg.dynamicSmemBytes = code_smem<MT>(8 * MT, k);
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            status[dev] = cudaOccupancyMaxActiveClusters(&room[dev][k], glu_codes<MT, AHEAD>, &cfg);
+        }
+    });
+    TERN_CUDA_TRY(status[dev]);
+    *clusters = room[dev][c];
+    return TERN_OK;
+}
+
+// Clusters as large as leave every block resident at once and every warp a block of rows.
+template <int MT, int AHEAD>
+int glu_few(const CodeArgs& a, cudaStream_t s) {
     const int tiles = (a.N + kCodeOut - 1) / kCodeOut, blocks = a.K / 16;
-    // clusters until the SMs have a block each, as long as every warp keeps a block of rows
-    int c = 1;
-    while (c < 8 && tiles * c < num_sms && blocks > c * kCodeWarps) c *= 2;
-    const int MT = a.M <= 8 ? 1 : 2;
-    const size_t smem = static_cast<size_t>(kCodeWarps) * 8 * MT * kCodePad * sizeof(float);
-    if (MT == 1) return launch_cluster(glu_codes<1>, tiles * c, kCodeWarps * 32, smem, c, true, s, a);
-    return launch_cluster(glu_codes<2>, tiles * c, kCodeWarps * 32, smem, c, true, s, a);
+    int c = 1, room = 0;
+    for (int k = 2; k <= kCodeMost && blocks > (k - 1) * kCodeWarps; ++k) {
+        if (int st = code_room<MT, AHEAD>(k, &room)) return st;
+        if (tiles <= room) c = k;
+    }
+    return launch_cluster(glu_codes<MT, AHEAD>, tiles * c, kCodeWarps * 64, code_smem<MT>(a.M, c), c, true, s, a);
 }
 
 bool glu_dims(int64_t M, int64_t K, int64_t N) {
@@ -685,7 +729,7 @@ extern "C" int tern_glu_fwd(const uint16_t* X, const tern_tiles* W, const float*
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (codes) {
         const CodeArgs c{X, W->packed, scale, H, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), act};
-        return glu_few(c, num_sms, s);
+        return M <= 8 ? glu_few<1, 4>(c, s) : glu_few<2, 3>(c, s);
     }
     GluArgs a{};
     a.scale = scale, a.H = H, a.pair = saved;

@@ -7,20 +7,20 @@
 //
 // Memory bounds both: the score reads each logit once, the distillation reads it once and writes its
 // gradient once.  One pass keeps a running maximum and sums relative to it; threads, blocks and the
-// blocks of a cluster (which share a row where rows are few) are joined at the end.  Rows of up to
-// 1024 entries belong to a warp each, which holds them in registers.
+// blocks of a cluster (which share a row where rows are few) are joined at the end.  Rows of up to 256
+// entries belong to a warp each, which holds them in registers.
 //
 // Rows start at any element: whole 16-byte words of a row are its body, the few entries before and
 // after them its head and tail.
 #include <algorithm>
 #include <cmath>
 
+#include "pairs.cuh"
 #include "rows.cuh"
 
 namespace tern {
 namespace {
 
-constexpr int kWarpRow = 1024;    // widest row of a warp
 constexpr int kMaxTop = TERN_SCORE_MAX_TOP;
 constexpr int kMaxTeacher = TERN_DISTILL_MAX_TOP;
 constexpr float kLog2e = 1.44269504f;
@@ -37,15 +37,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
     return y;
 }
 
-// A running softmax: maximum, sum of 2^(c (x - m)) and, for the entropy, the same with the factor (x - m).
+// A softmax's maximum, sum of 2^(c (x - m)) and, for the entropy, the same with the factor (x - m);
 // c = log2(e) / T.  The difference is taken first: it is exact near the maximum, where it counts.
 template <bool ENT>
 struct Stats {
-    float m = kNegInf, s = 0.f, q = 0.f, c;
-    __device__ __forceinline__ explicit Stats(float c_) : c(c_) {}
+    float m = kNegInf, s = 0.f, q = 0.f;
 
-    // Moves to the maximum mn >= m (finite, or inf: then s becomes NaN as it should).
-    __device__ __forceinline__ void rebase(float mn) {
+    // Relative to mn >= m (finite, or inf: then s becomes NaN, as it should).
+    __device__ __forceinline__ void rebase(float mn, float c) {
         if (m != kNegInf) {   // of nothing but -inf s and q are 0, or s is NaN
             const float d = m - mn, f = pow2(d * c);
             if (ENT) q = (q + s * d) * f;
@@ -53,57 +52,79 @@ struct Stats {
         }
         m = mn;
     }
-
-    template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N], float top) {
-        const float mn = fmaxf(m, top);   // drops NaN; the sums below bring it back
-        if (mn == kNegInf) {              // nothing but -inf (and NaN) so far
-            float t = 0.f;
+    // The sums of a warp's 32 in every lane, in a fixed order.
+    __device__ __forceinline__ void join_warp(float c) {
+        float mn = m;
 #pragma unroll
-            for (int i = 0; i < N; ++i) t += x[i];
-            if (t != t) s = t;
-            return;
-        }
-        if (mn > m) rebase(mn);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            // -inf (a masked entry) would give 0 times infinity
-            const float z = ENT ? max_nan(x[i] - mn, -1e4f) : x[i] - mn;
-            const float e = pow2(z * c);
-            s += e;
-            if (ENT) q = fmaf(e, z, q);
-        }
-    }
-
-    __device__ __forceinline__ void join(float om, float os, float oq) {
-        const float mn = fmaxf(m, om);
-        if (mn == kNegInf) {
-            s += os;
-            return;
-        }
-        Stats o(c);
-        o.m = om, o.s = os, o.q = oq;
-        rebase(mn);
-        o.rebase(mn);
-        s += o.s;
-        q += o.q;
-    }
-
-    __device__ __forceinline__ void join_warp() {
+        for (int d = 16; d >= 1; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+        rebase(mn, c);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, d), os = __shfl_xor_sync(0xffffffffu, s, d);
-            const float oq = ENT ? __shfl_xor_sync(0xffffffffu, q, d) : 0.f;
-            // the lower lane's first in both, so that all lanes hold the same bits
-            if ((threadIdx.x & d) == 0) {
-                join(om, os, oq);
-            } else {
-                Stats o(c);
-                o.m = om, o.s = os, o.q = oq;
-                o.join(m, s, q);
-                *this = o;
-            }
+            s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (ENT) q += __shfl_xor_sync(0xffffffffu, q, d);
         }
+    }
+};
+
+// A thread's running softmax over batches of pairs.
+template <bool ENT>
+struct Run {
+    float m = kNegInf;
+    F2 s = both(0.f), q = both(0.f);
+
+    // `top`: the largest of the batch (NaN dropped); `masked`: there may be -inf among it, which would
+    // give 0 times infinity in the entropy's sum.
+    template <int N2>
+    __device__ __forceinline__ void add(const F2 (&x)[N2], float top, bool masked, float c) {
+        if (top > m) {
+            if (m != kNegInf) {
+                const float d = m - top, f = pow2(d * c);
+                if (ENT) q = mul2(fma2(s, both(d), q), both(f));
+                s = mul2(s, both(f));
+            }
+            m = top;
+        }
+        if (m == kNegInf) {   // nothing but -inf, and NaN
+            F2 t = x[0];
+#pragma unroll
+            for (int i = 1; i < N2; ++i) t = add2(t, x[i]);
+            float lo, hi;
+            split(t, lo, hi);
+            if (lo + hi != lo + hi) s = both(lo + hi);
+            return;
+        }
+        const F2 shift = both(-m), scale = both(c);
+        if (ENT && masked) {
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+                float z0, z1;
+                split(add2(x[i], shift), z0, z1);
+                sum(pair(max_nan(z0, -1e4f), max_nan(z1, -1e4f)), scale);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N2; ++i) sum(add2(x[i], shift), scale);
+        }
+    }
+    __device__ __forceinline__ void sum(F2 z, F2 scale) {
+        float t0, t1;
+        split(mul2(z, scale), t0, t1);
+        const F2 e = pair(pow2(t0), pow2(t1));
+        s = add2(s, e);
+        if (ENT) q = fma2(e, z, q);
+    }
+    __device__ __forceinline__ void add1(float x, float c) {
+        const F2 one[1] = {pair(x, kNegInf)};
+        add(one, x, true, c);
+    }
+    __device__ __forceinline__ Stats<ENT> get() const {
+        Stats<ENT> r;
+        float a, b;
+        split(s, a, b);
+        r.m = m, r.s = a + b;
+        split(q, a, b);
+        r.q = a + b;
+        return r;
     }
 };
 
@@ -127,11 +148,36 @@ struct Row {
 };
 
 template <class T, int V>
-__device__ __forceinline__ float raw_max(const Raw<T, V>& r) {   // drops NaN
-    float m = raw_at<T, V>(r, 0);
+__device__ __forceinline__ void raw_pairs(const Raw<T, V>& r, F2* x) {
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = fmaxf(m, raw_at<T, V>(r, i));
-    return m;
+    for (int i = 0; i < V / 2; ++i) x[i] = pair(raw_at<T, V>(r, 2 * i), raw_at<T, V>(r, 2 * i + 1));
+}
+
+// The largest and the smallest of U words' entries (NaN dropped).
+template <class T, int V, int U>
+__device__ __forceinline__ float raw_max(const Raw<T, V> (&r)[U]) {
+    if constexpr (kElem<T> == 2) {
+        uint32_t m = r[0].w[0];
+#pragma unroll
+        for (int i = 1; i < U * V / 2; ++i) asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(r[i / (V / 2)].w[i % (V / 2)]));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    } else {
+        float m = raw_at<T, V>(r[0], 0);
+#pragma unroll
+        for (int i = 1; i < U * V; ++i) m = fmaxf(m, raw_at<T, V>(r[i / V], i % V));
+        return m;
+    }
+}
+template <class T, int V, int U>
+__device__ __forceinline__ bool raw_masked(const Raw<T, V> (&r)[U]) {   // whether there may be -inf
+    if constexpr (kElem<T> == 2) {
+        uint32_t m = r[0].w[0];
+#pragma unroll
+        for (int i = 1; i < U * V / 2; ++i) asm("min.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(r[i / (V / 2)].w[i % (V / 2)]));
+        return fminf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)) == kNegInf;
+    } else {
+        return true;   // looking costs what the bound that it would save does
+    }
 }
 
 // The words that block `rank` of `size` takes of a row's body: [first, last).
@@ -142,71 +188,105 @@ __device__ __forceinline__ void slice(int nb, int rank, int size, int& first, in
 }
 
 // One pass of a block of T threads over its words of a row (and, in block 0, the edges): thread t
-// takes the words first + t, first + t + T, ...
+// takes the words first + t, first + t + T, ...  With `tops`, each thread leaves the largest entry of
+// each segment, `seg` of its words in turn (one, or a multiple of kBatch; NaN dropped), at
+// tops[segment T + t].
+constexpr int kBatch = 4;      // words a thread asks for at once
+constexpr int kSegments = 8;
+__device__ __forceinline__ int segment_words(int words, int T) {
+    const int each = (words + T - 1) / T;
+    return each <= kSegments ? 1 : ((each + kSegments - 1) / kSegments + kBatch - 1) / kBatch * kBatch;
+}
+
 template <class TX, int T, bool ENT>
-__device__ __forceinline__ void read_row(const Row<TX>& r, int first, int last, bool edges, Stats<ENT>& st) {
-    constexpr int VE = Row<TX>::VE, U = 4;
+__device__ __forceinline__ Stats<ENT> read_row(const Row<TX>& r, int first, int last, bool edges, float c, float* tops = nullptr, int seg = 0) {
+    constexpr int VE = Row<TX>::VE, U = kBatch;
+    Run<ENT> run;
     int i = first + static_cast<int>(threadIdx.x);
+    float most = kNegInf;   // of the segment
+    int left = seg;
+    float* to = tops + threadIdx.x;
     for (; i + (U - 1) * T < last; i += U * T) {
         Raw<TX, VE> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) raw[u] = load_raw<TX, VE>(r.word(i + u * T));
-        float top = kNegInf;
+        F2 x[U * VE / 2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) top = fmaxf(top, raw_max<TX, VE>(raw[u]));
-        float x[U * VE];
+        for (int u = 0; u < U; ++u) raw_pairs<TX, VE>(raw[u], x + u * (VE / 2));
+        const float top = raw_max(raw);
+        run.add(x, top, ENT && raw_masked(raw), c);
+        if (ENT && tops && seg == 1) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) x[u * VE + e] = raw_at<TX, VE>(raw[u], e);
-        st.add(x, top);
+            for (int u = 0; u < U; ++u) {
+                const Raw<TX, VE> one[1] = {raw[u]};
+                *to = raw_max(one);
+                to += T;
+            }
+        } else if (ENT && tops) {
+            most = fmaxf(most, top);
+            if ((left -= U) == 0) *to = most, to += T, most = kNegInf, left = seg;
+        }
     }
     for (; i < last; i += T) {
-        const auto raw = load_raw<TX, VE>(r.word(i));
-        float x[VE];
-#pragma unroll
-        for (int e = 0; e < VE; ++e) x[e] = raw_at<TX, VE>(raw, e);
-        st.add(x, raw_max<TX, VE>(raw));
+        const Raw<TX, VE> raw[1] = {load_raw<TX, VE>(r.word(i))};
+        F2 x[VE / 2];
+        raw_pairs<TX, VE>(raw[0], x);
+        const float top = raw_max(raw);
+        run.add(x, top, true, c);
+        if (ENT && tops) {
+            most = fmaxf(most, top);
+            if (--left == 0) *to = most, to += T, most = kNegInf, left = seg;
+        }
     }
-    if (edges && static_cast<int>(threadIdx.x) < r.edges()) {
-        const float x[1] = {r.at(r.edge(threadIdx.x))};
-        st.add(x, x[0]);
-    }
+    if (ENT && tops && left < seg) *to = most;
+    if (edges && static_cast<int>(threadIdx.x) < r.edges()) run.add1(r.at(r.edge(threadIdx.x)), c);
+    return run.get();
 }
 
-// Joins the threads of a block (through s: 3 T / 32 floats), and the blocks of a cluster; every
-// thread holds the result.  Uses barriers of both.
+// Joins the threads of a block through s (3 T / 32 floats); every thread holds the result.
 template <int T, bool ENT>
-__device__ __forceinline__ void join_block(Stats<ENT>& st, float* s, uint32_t rank, uint32_t size) {
+__device__ __forceinline__ void join_block(Stats<ENT>& st, float* s, float c) {
     constexpr int W = T / 32;
-    st.join_warp();
-    if ((threadIdx.x & 31) == 0) {
+    const int lane = threadIdx.x & 31;
+    st.join_warp(c);
+    if (lane == 0) {
         float* at = s + 3 * (threadIdx.x >> 5);
         at[0] = st.m, at[1] = st.s, at[2] = st.q;
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        const bool in = lane < W;
-        st.m = in ? s[3 * lane] : kNegInf, st.s = in ? s[3 * lane + 1] : 0.f, st.q = in ? s[3 * lane + 2] : 0.f;
-        st.join_warp();
-        __syncwarp();
-        if (lane == 0) s[0] = st.m, s[1] = st.s, s[2] = st.q;
+    const bool in = lane < W;
+    st.m = in ? s[3 * lane] : kNegInf, st.s = in ? s[3 * lane + 1] : 0.f, st.q = in ? s[3 * lane + 2] : 0.f;
+    st.join_warp(c);
+}
+
+constexpr int kMaxBlocks = 16;   // of a cluster
+
+// The blocks of a cluster push what the others need into their shared memory, so that no block waits at
+// its end for the others to read its own: arrive at the start; wait (every block has started), push,
+// arrive and wait.  For whole warps.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// This block's sums to slot `rank` of every block's `all` (4 floats each), by warp 0.
+template <bool ENT>
+__device__ __forceinline__ void push_stats(const Stats<ENT>& st, float4* all, uint32_t rank, uint32_t size) {
+    if (threadIdx.x < size) {
+        const uint32_t to = ptx::mapa_shared(ptx::smem_u32(all + rank), threadIdx.x);
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(st.m), "f"(st.s), "f"(st.q), "f"(0.f) : "memory");
     }
-    if (size > 1) ptx::cluster_sync(); else __syncthreads();
-    if (size == 1) {
-        st.m = s[0], st.s = s[1], st.q = s[2];
-    } else {
-        st = Stats<ENT>(st.c);
-        for (uint32_t r = 0; r < size; ++r) {
-            const uint32_t from = ptx::mapa_shared(ptx::smem_u32(s), r);
-            float m, v, q;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m) : "r"(from) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + 4u) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(from + 8u) : "memory");
-            st.join(m, v, q);
-        }
-    }
+}
+template <bool ENT>
+__device__ __forceinline__ void join_cluster(Stats<ENT>& st, const float4* all, uint32_t size, float c) {
+    const uint32_t lane = threadIdx.x & 31;
+    const float4 v = lane < size ? all[lane] : make_float4(kNegInf, 0.f, 0.f, 0.f);
+    st.m = v.x, st.s = v.y, st.q = v.z;
+    st.join_warp(c);
 }
 
 __device__ __forceinline__ void cluster_place(uint32_t& rank, uint32_t& size) {
@@ -218,12 +298,14 @@ __device__ __forceinline__ void cluster_place(uint32_t& rank, uint32_t& size) {
 //
 // The k largest entries, the lower index first where equal: a thread's running maximum is at hand after
 // the pass, and the k-th largest of the threads' maxima is a bound that at least k entries reach.  Few
-// others do (with T threads of E entries each about k + k^2 / 2T), so only the words of threads whose
+// others do (about k + k^2 / 2T of T threads' entries in no order), so only the words of threads whose
 // maximum reaches it are read again, from L2.  Entries are ordered by 64-bit keys, the value above
 // the complement of the index, all different; each candidate's rank is the number of larger keys.
-// Where more entries reach the bound than there is room for (masked rows, constant ones) the exact
-// k-th value is found by bisection, and entries equal to it are taken in the order of the row.
-constexpr int kCand = 1024;
+// Where more entries reach the bound than there is room for (masked rows, constant ones, large entries
+// in few threads' words) the exact k-th value is found, by bisection if it must be, and entries equal
+// to it are taken in the order of the row.
+template <int T>
+constexpr int kCand = T == 32 ? 256 : 1024;
 
 __device__ __forceinline__ uint32_t order_key(float x) {   // larger for larger x; NaN above all, -0 as 0; never 0
     if (x != x) return 0xFFFFFFFFu;
@@ -251,41 +333,63 @@ struct ScoreArgs {
 
 template <int T>
 struct TopSpace {
-    unsigned long long cand[kCand];
+    unsigned long long cand[kCand<T>];
     unsigned long long best[kMaxTop];
-    uint16_t list[T];
+    unsigned long long lists[T == 32 ? 1 : kMaxBlocks * kMaxTop];   // the cluster's
+    float tops[kSegments * T];                                      // read_row's
+    uint16_t list[kSegments * T];
     int rank[kMaxTop];
     int count, listed;
     int warps[T / 32];
 };
 
 // Every entry of the slice with a key of at least lo, as candidates; sp.count of them (kCand are kept).
+// Only segments whose largest entry reaches lo are read again; all of them where there is NaN (`every`).
 template <class TX, int T>
-__device__ __forceinline__ void collect(const Row<TX>& r, int first, int last, bool edges, uint32_t mine, uint32_t lo, TopSpace<T>& sp) {
-    constexpr int VE = Row<TX>::VE;
+__device__ __forceinline__ void collect(const Row<TX>& r, int first, int last, bool edges, bool every, uint32_t lo, TopSpace<T>& sp) {
+    constexpr int VE = Row<TX>::VE, U = kBatch;
+    const int t = threadIdx.x, seg = segment_words(last - first, T);
     __syncthreads();
-    if (threadIdx.x == 0) sp.count = sp.listed = 0;
+    if (t == 0) sp.count = sp.listed = 0;
     __syncthreads();
-    if (mine >= lo) sp.list[atomicAdd(&sp.listed, 1)] = static_cast<uint16_t>(threadIdx.x);
+    const float bound = key_value(lo);   // NaN for 0 and above +inf: reached by all
+    for (int g = 0; first + t + g * seg * T < last; ++g)
+        if (every || !(sp.tops[g * T + t] < bound)) sp.list[atomicAdd(&sp.listed, 1)] = static_cast<uint16_t>(g * T + t);
     auto offer = [&](float x, int e) {
         const uint32_t key = order_key(x);
         if (key >= lo) {
             const int at = atomicAdd(&sp.count, 1);
-            if (at < kCand) sp.cand[at] = entry_key(key, e);
+            if (at < kCand<T>) sp.cand[at] = entry_key(key, e);
         }
     };
     __syncthreads();
-    const int listed = sp.listed, rounds = (last - first + T - 1) / T;
-    for (int w = threadIdx.x; w < listed * rounds; w += T) {
-        const int i = first + sp.list[w % listed] + (w / listed) * T;
-        if (i < last) {
-            const auto raw = load_raw<TX, VE>(r.word(i));
+    const int listed = sp.listed;
+    for (int w0 = t; w0 < listed * seg; w0 += U * T) {
+        Raw<TX, VE> raw[U];
+        int at[U];
 #pragma unroll
-            for (int e = 0; e < VE; ++e) offer(raw_at<TX, VE>(raw, e), r.head + i * VE + e);
+        for (int u = 0; u < U; ++u) {
+            const int w = w0 + u * T;
+            at[u] = last;
+            if (w < listed * seg) {
+                const int q = w / listed, item = sp.list[w - q * listed];
+                at[u] = first + item % T + (item / T * seg + q) * T;
+            }
+            if (at[u] < last) raw[u] = load_raw<TX, VE>(r.word(at[u]));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (at[u] < last) {
+                const Raw<TX, VE> one[1] = {raw[u]};
+                if (every || !(raw_max(one) < bound)) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) offer(raw_at<TX, VE>(raw[u], e), r.head + at[u] * VE + e);
+                }
+            }
         }
     }
-    if (edges && static_cast<int>(threadIdx.x) < r.edges()) {
-        const int e = r.edge(threadIdx.x);
+    if (edges && t < r.edges()) {
+        const int e = r.edge(t);
         offer(r.at(e), e);
     }
     __syncthreads();
@@ -313,28 +417,63 @@ __device__ __forceinline__ int count_from(const Row<TX>& r, int first, int last,
 }
 
 // The k largest entries of the slice into sp.best, largest first, zeros where there are fewer.
-// `mine`: the largest key among the thread's entries, 0 without any.
+// `mine`: the largest key among the thread's entries, 0 without any; `every`: there is NaN.
 template <class TX, int T>
-__device__ __forceinline__ void block_top(const Row<TX>& r, int first, int last, bool edges, uint32_t mine, int k, TopSpace<T>& sp) {
+__device__ __forceinline__ void block_top(const Row<TX>& r, int first, int last, bool edges, bool every, uint32_t mine, int k, TopSpace<T>& sp) {
     constexpr int VE = Row<TX>::VE;
     uint32_t lo = 0;   // the upper 16 bits of the bound: all that bf16 has
+    if constexpr (T == 32) {   // of the segments' maxima
+        const int seg = segment_words(last - first, T);
+        uint32_t top[kSegments];
+#pragma unroll
+        for (int g = 0; g < kSegments; ++g)
+            top[g] = !every && first + static_cast<int>(threadIdx.x) + g * seg * T < last ? order_key(sp.tops[g * T + threadIdx.x]) : 0u;
+        if (every) top[0] = mine;
 #pragma unroll 1
-    for (int b = 31; b >= 16; --b)
-        if (__syncthreads_count(mine >= (lo | (1u << b))) >= k) lo |= 1u << b;
-    collect<TX, T>(r, first, last, edges, mine, lo, sp);
-    int n = sp.count;
-    if (n > kCand) {
-        // the k-th largest value exactly.  A bf16's lower bits are known (ones where negative, and of
-        // NaN), and nothing but -inf has its upper bits.
-        if (kElem<TX> == 2 || lo == 0x007F0000u) {
-            if (lo < 0x80000000u || lo == 0xFFFF0000u) lo |= 0xFFFFu;
-        } else {
-#pragma unroll 1
-            for (int b = 15; b >= 0; --b)
-                if (count_from<TX, T>(r, first, last, edges, lo | (1u << b), sp) >= k) lo |= 1u << b;
+        for (int b = 31; b >= 16; --b) {
+            int reach = 0;
+#pragma unroll
+            for (int g = 0; g < kSegments; ++g) reach += __popc(__ballot_sync(0xffffffffu, top[g] >= (lo | (1u << b))));
+            if (reach >= k) {
+                lo |= 1u << b;
+                if (reach <= k + k / 4 + 2) break;   // near enough
+            }
         }
-        collect<TX, T>(r, first, last, edges, mine, lo + 1, sp);   // fewer than k; of NaN alone (no lo + 1) none below
-        n = lo == 0xFFFFFFFFu ? 0 : sp.count;
+    } else {
+#pragma unroll 1
+        for (int b = 31; b >= 16; --b) {
+            const int reach = __syncthreads_count(mine >= (lo | (1u << b)));
+            if (reach >= k) {
+                lo |= 1u << b;
+                if (reach <= k + k / 4 + 2) break;
+            }
+        }
+    }
+    collect<TX, T>(r, first, last, edges, every, lo, sp);
+    int n = sp.count;
+    if (n > kCand<T>) {
+        // Too many.  They may all be one value: every bf16 with the bound's upper bits (the lower are
+        // ones where negative, and of NaN), and -inf, which alone has its own.
+        bool one = kElem<TX> == 2 || lo >> 16 == 0x007Fu;
+        if (one) {
+            if (lo < 0x80000000u || lo >> 16 == 0xFFFFu) lo |= 0xFFFFu;
+            collect<TX, T>(r, first, last, edges, every, lo + 1, sp);
+            n = lo == 0xFFFFFFFFu ? 0 : sp.count;   // nothing is above NaN
+            one = n < k;
+        }
+        if (n > kCand<T>) {   // the k-th largest value by bisection; at least k entries reach lo
+            uint32_t v = 0;
+#pragma unroll 1
+            for (int b = 31; b >= 0; --b) {
+                const uint32_t c = v | (1u << b);
+                if (c <= lo || count_from<TX, T>(r, first, last, edges, c, sp) >= k) v = c;
+            }
+            lo = v;
+            collect<TX, T>(r, first, last, edges, every, lo + 1, sp);
+            n = lo == 0xFFFFFFFFu ? 0 : sp.count;
+            one = true;
+        }
+        if (one) {
         // the first of those equal to it: the head, the body in order, the tail
         int want = k - n, found = 0;
         auto place = [&](bool hit, int before, int e) {
@@ -381,14 +520,22 @@ __device__ __forceinline__ void block_top(const Row<TX>& r, int first, int last,
             }
         n += min(found, want);
         __syncthreads();
+        }
     }
     for (int c = threadIdx.x; c < k; c += T)
         if (c >= n) sp.best[c] = 0ull;
-    for (int c = threadIdx.x; c < n; c += T) {
+    // several threads a candidate where there are enough
+    int parts = 1;
+    while (parts < 8 && n * parts * 2 <= T) parts *= 2;
+    for (int c = threadIdx.x / parts; c < n; c += T / parts) {
         const unsigned long long key = sp.cand[c];
         int rank = 0;
-        for (int o = 0; o < n; ++o) rank += sp.cand[o] > key;
-        if (rank < k) sp.best[rank] = key;
+#pragma unroll 4
+        for (int o = threadIdx.x % parts; o < n; o += parts) rank += sp.cand[o] > key;
+        // a candidate's threads are neighbours in a warp, all of them here (parts > 1: one round of all candidates)
+        const uint32_t who = ((1u << parts) - 1) << ((threadIdx.x & 31) / parts * parts);
+        for (int d = parts / 2; d >= 1; d >>= 1) rank += __shfl_xor_sync(who, rank, d);
+        if (rank < k && threadIdx.x % parts == 0) sp.best[rank] = key;
     }
     __syncthreads();
 }
@@ -408,38 +555,43 @@ __device__ __forceinline__ void write_top(const ScoreArgs& a, int64_t row, int c
     a.top_logp[row * a.k + c] = l.logp(key_value(static_cast<uint32_t>(key >> 32)));
 }
 
-template <class TX>
-__device__ __forceinline__ void write_row(const ScoreArgs& a, int64_t row, const Row<TX>& r, const Stats<true>& st, const RowLog& l) {
+__device__ __forceinline__ int row_token(const ScoreArgs& a, int64_t row) {   // -1: none, or outside the row
+    if (!a.logp) return -1;
+    const int64_t tok = a.wide_ids ? __ldg(static_cast<const long long*>(a.tokens) + row) : __ldg(static_cast<const int32_t*>(a.tokens) + row);
+    return tok >= 0 && tok < a.V ? static_cast<int>(tok) : -1;
+}
+__device__ __forceinline__ void write_row(const ScoreArgs& a, int64_t row, int tok, float x, const Stats<true>& st, const RowLog& l) {
     if (a.lse) a.lse[row] = l.lse();
     if (a.entropy) a.entropy[row] = l.dead ? 0.f : fmaxf(l.log_s - st.q / st.s, 0.f) + (st.s != st.s ? st.s : 0.f);
-    if (a.logp) {
-        const int64_t tok = a.wide_ids ? __ldg(static_cast<const long long*>(a.tokens) + row) : __ldg(static_cast<const int32_t*>(a.tokens) + row);
-        a.logp[row] = tok >= 0 && tok < a.V ? l.logp(r.at(static_cast<int>(tok))) : 0.f;
-    }
+    if (a.logp) a.logp[row] = tok >= 0 ? l.logp(x) : 0.f;
 }
 
 // A row a cluster (of one block, or of several where rows are few).
 template <class TX, int T>
-__global__ void __launch_bounds__(T) score_rows(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) score_rows(const __grid_constant__ ScoreArgs a) {
     __shared__ float s[3 * (T / 32)];
+    __shared__ float4 all[kMaxBlocks];
     __shared__ TopSpace<T> sp;
-    uint32_t rank, size;
-    cluster_place(rank, size);
+    uint32_t rank = 0, size = 1;
+    if constexpr (T > 32) cluster_place(rank, size);
+    if (size > 1) cluster_arrive();
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const int64_t row = blockIdx.x / size;
+    const bool edges = rank == 0, writes = edges && threadIdx.x == 0;
+    const int tok = writes ? row_token(a, row) : -1;
     const Row<TX> r(a.logits, row, a.ld, a.V);
     int first, last;
     slice(r.nb, rank, size, first, last);
-    const bool edges = rank == 0;
-    Stats<true> st(kLog2e);
-    read_row<TX, T, true>(r, first, last, edges, st);
-    uint32_t mine = 0;
-    if (a.k) {
+    const int k = a.k;
+    Stats<true> st = read_row<TX, T, true>(r, first, last, edges, kLog2e, k ? sp.tops : nullptr, k ? segment_words(last - first, T) : 0);
+    const float xtok = tok >= 0 ? r.at(tok) : 0.f;   // under way while the sums are joined
+    if (k) {
         const bool any = first + static_cast<int>(threadIdx.x) < last || (edges && static_cast<int>(threadIdx.x) < r.edges());
-        mine = any ? order_key(st.m) : 0u;
+        uint32_t mine = any ? order_key(st.m) : 0u;
         // infinities and NaN: the maximum that the sums are relative to may not be the largest entry's key
-        if (__syncthreads_or(st.s != st.s)) {
+        const bool every = __syncthreads_or(st.s != st.s);
+        if (every) {
             mine = 0;
             for (int i = first + static_cast<int>(threadIdx.x); i < last; i += T) {
                 const auto raw = load_raw<TX, Row<TX>::VE>(r.word(i));
@@ -448,35 +600,37 @@ __global__ void __launch_bounds__(T) score_rows(const __grid_constant__ ScoreArg
             }
             if (edges && static_cast<int>(threadIdx.x) < r.edges()) mine = max(mine, order_key(r.at(r.edge(threadIdx.x))));
         }
+        block_top<TX, T>(r, first, last, edges, every, mine, k, sp);
     }
-    join_block<T, true>(st, s, rank, size);
-    const RowLog l(st);
-    if (rank == 0 && threadIdx.x == 0) write_row(a, row, r, st, l);
-    if (a.k == 0) {
-        if (size > 1) ptx::cluster_sync();   // the peers have read this block's sums
-        return;
-    }
-    block_top<TX, T>(r, first, last, edges, mine, a.k, sp);
+    join_block<T, true>(st, s, kLog2e);
     if (size == 1) {
-        for (int c = threadIdx.x; c < a.k; c += T) write_top(a, row, c, sp.best[c], l);
+        const RowLog l(st);
+        if (writes) write_row(a, row, tok, xtok, st, l);
+        for (int c = threadIdx.x; c < k; c += T) write_top(a, row, c, sp.best[c], l);
         return;
     }
-    // each block ranks its own entries among all blocks' sorted lists, copied here first
-    ptx::cluster_sync();
-    const int k = a.k, lists = static_cast<int>(size);
+    cluster_wait();   // every block has started
+    push_stats(st, all, rank, size);
+    const int lists = static_cast<int>(size);
     for (int w = threadIdx.x; w < k * lists; w += T) {
-        const uint32_t from = ptx::mapa_shared(ptx::smem_u32(&sp.best[w % k]), static_cast<uint32_t>(w / k));
-        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(sp.cand[w]) : "r"(from) : "memory");
+        const int c = w % k;
+        const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sp.lists[rank * k + c]), static_cast<uint32_t>(w / k));
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(sp.best[c]) : "memory");
     }
     for (int c = threadIdx.x; c < k; c += T) sp.rank[c] = 0;
-    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    join_cluster(st, all, size, kLog2e);
+    const RowLog l(st);
+    if (writes) write_row(a, row, tok, xtok, st, l);
+    // each block ranks its own entries among all blocks' sorted lists
     for (int w = threadIdx.x; w < k * lists; w += T) {
         const int c = w % k, o = w / k;
         const unsigned long long key = sp.best[c];
-        int lo = 0, hi = k;   // entries of list o above the key: a sorted list's first ones
+        int lo = 0, hi = k;   // entries of list o above the key: its first ones
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
-            if (sp.cand[o * k + mid] > key) lo = mid + 1;
+            if (sp.lists[o * k + mid] > key) lo = mid + 1;
             else hi = mid;
         }
         if (lo) atomicAdd(&sp.rank[c], lo);
@@ -484,51 +638,160 @@ __global__ void __launch_bounds__(T) score_rows(const __grid_constant__ ScoreArg
     __syncthreads();
     for (int c = threadIdx.x; c < k; c += T)
         if (sp.best[c] && sp.rank[c] < k) write_top(a, row, sp.rank[c], sp.best[c], l);
-    ptx::cluster_sync();   // the peers have read this block's list
 }
 
-// A row of up to 32 EPL entries in a warp's registers: lane l holds entries j 32 + l.
-template <class TX, int EPL>
-__global__ void __launch_bounds__(128) score_warps(const __grid_constant__ ScoreArgs a) {
-    ptx::pdl_trigger();
+// ---- rows of up to 256 entries, a warp each: EPL entries a lane.  VEC: as whole 16-byte words (row
+// starts and width allow it), else lane by lane.
+template <class TX, int EPL, bool VEC>
+struct WarpRow {
+    static constexpr int VE = VEC ? Row<TX>::VE : 1;
+    TX* p;
+    int V, lane;
+    // entry of the lane's j-th register
+    __device__ __forceinline__ int index(int j) const { return (j / VE) * 32 * VE + lane * VE + j % VE; }
+    __device__ __forceinline__ void load(float (&x)[EPL]) const {
+#pragma unroll
+        for (int j = 0; j < EPL; j += VE) {
+            const bool in = index(j) < V;
+            Raw<TX, VE> raw;
+            if (in) raw = load_raw<TX, VE>(p + index(j));
+#pragma unroll
+            for (int e = 0; e < VE; ++e) x[j + e] = in ? raw_at<TX, VE>(raw, e) : kNegInf;
+        }
+    }
+    __device__ __forceinline__ void store(const float (&x)[EPL]) const {
+#pragma unroll
+        for (int j = 0; j < EPL; j += VE) {
+            if (index(j) < V) {
+                float v[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) v[e] = x[j + e];
+                store_as<TX, VE>(p + index(j), v);
+            }
+        }
+    }
+};
+
+template <int EPL, bool ENT>
+__device__ __forceinline__ Stats<ENT> warp_stats(const float (&x)[EPL], float c) {
+    float top = x[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) top = fmaxf(top, x[j]);
+    F2 xx[EPL / 2];
+#pragma unroll
+    for (int j = 0; j < EPL / 2; ++j) xx[j] = pair(x[2 * j], x[2 * j + 1]);
+    Run<ENT> run;
+    run.add(xx, top, true, c);
+    Stats<ENT> st = run.get();
+    st.join_warp(c);
+    return st;
+}
+
+// The k largest of a warp's entries into best, largest first: candidates from a bound as in block_top
+// (the k-th largest of the maxima of groups of registers), their ranks by comparison.
+template <int EPL, class R>
+__device__ __forceinline__ void warp_top(const uint32_t (&key)[EPL], const R& row, int k, unsigned long long* cand, unsigned long long* best) {
+    constexpr int G = EPL < 4 ? EPL : 4;   // groups a lane
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    uint32_t lo = 0;
+    if (k <= 8) {   // the lanes' maxima, largest first
+        uint32_t top = key[0];
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) top = max(top, key[j]);
+        for (int c = 0; c < k; ++c) {
+            lo = __reduce_max_sync(0xffffffffu, top);
+            if (top == lo) top = 0;   // several at once where equal: the bound is lower, and still one
+        }
+    } else {
+        uint32_t top[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            top[g] = key[g];
+#pragma unroll
+            for (int j = g + G; j < EPL; j += G) top[g] = max(top[g], key[j]);
+        }
+#pragma unroll 1
+        for (int b = 31; b >= 16; --b) {
+            const uint32_t c = lo | (1u << b);
+            int reach = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) reach += __popc(__ballot_sync(0xffffffffu, top[g] >= c));
+            if (reach >= k) {
+                lo = c;
+                if (reach <= k + k / 4 + 2) break;
+            }
+        }
+    }
+    auto reach_of = [&](uint32_t c) {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) n += key[j] >= c;
+        return static_cast<int>(__reduce_add_sync(0xffffffffu, n));
+    };
+    lo = max(lo, 1u);   // 0: no entry
+    int n = 0, most = -1;   // most: index of the last entry equal to lo that is wanted, -1 for all above lo and at it
+    if (reach_of(lo) > k + 64) {
+        // many equal ones, or a poor bound: the k-th value by bisection, and the index up to which entries equal to it count
+        uint32_t v = 0;
+#pragma unroll 1
+        for (int b = 31; b >= 0; --b) {
+            const uint32_t c = v | (1u << b);
+            if (c <= lo || reach_of(c) >= k) v = c;
+        }
+        lo = v;
+        const int want = k - (lo == 0xFFFFFFFFu ? 0 : reach_of(lo + 1));
+        int from = 0, to = row.V - 1;   // the smallest index with `want` equal entries up to it
+        while (from < to) {
+            const int mid = (from + to) / 2;
+            int c = 0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) c += key[j] == lo && row.index(j) <= mid;
+            if (static_cast<int>(__reduce_add_sync(0xffffffffu, c)) >= want) to = mid;
+            else from = mid + 1;
+        }
+        most = from;
+    }
+    const uint32_t below = (1u << lane) - 1;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        const bool hit = key[j] > lo || (key[j] == lo && (most < 0 || row.index(j) <= most));
+        const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+        if (hit) cand[n + __popc(hits & below)] = entry_key(key[j], row.index(j));
+        n += __popc(hits);
+    }
+    __syncwarp();
+    for (int c = lane; c < n; c += 32) {
+        const unsigned long long mine = cand[c];
+        int rank = 0;
+        for (int o = 0; o < n; ++o) rank += cand[o] > mine;
+        if (rank < k) best[rank] = mine;
+    }
+    __syncwarp();
+}
+
+template <class TX, int EPL, bool VEC>
+__global__ void __launch_bounds__(128) score_warps(const __grid_constant__ ScoreArgs a) {
+    __shared__ unsigned long long cand4[4][kMaxTop + 64], best4[4][kMaxTop];
+    ptx::pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + warp;
     ptx::pdl_wait();
     if (row >= a.n) return;
     const Row<TX> r(a.logits, row, a.ld, a.V);
+    const WarpRow<TX, EPL, VEC> wr{const_cast<TX*>(r.p), a.V, lane};
+    const int tok = lane == 0 ? row_token(a, row) : -1;
     float x[EPL];
-    float top = kNegInf;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        x[j] = j * 32 + lane < a.V ? r.at(j * 32 + lane) : kNegInf;
-        top = fmaxf(top, x[j]);
-    }
-    Stats<true> st(kLog2e);
-    st.add(x, top);
-    st.join_warp();
+    wr.load(x);
+    const float xtok = tok >= 0 ? r.at(tok) : 0.f;
+    const Stats<true> st = warp_stats<EPL, true>(x, kLog2e);
     const RowLog l(st);
-    if (lane == 0) write_row(a, row, r, st, l);
+    if (lane == 0) write_row(a, row, tok, xtok, st, l);
     if (a.k == 0) return;
-    // the largest k times, the lowest index first: each lane's best entry below the last one taken
     uint32_t key[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) key[j] = j * 32 + lane < a.V ? order_key(x[j]) : 0u;
-    for (int c = 0; c < a.k; ++c) {
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int j = EPL - 1; j >= 0; --j)
-            if (key[j] >= best) best = key[j], at = j;
-        const uint32_t all = __reduce_max_sync(0xffffffffu, best);
-        const int e = at * 32 + lane;
-        const int index = static_cast<int>(__reduce_min_sync(0xffffffffu, best == all ? static_cast<uint32_t>(e) : 0xFFFFFFFFu));
-        if (index == e) {
-            write_top(a, row, c, entry_key(all, index), l);
-#pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                if (j == at) key[j] = 0u;
-        }
-    }
+    for (int j = 0; j < EPL; ++j) key[j] = wr.index(j) < a.V ? order_key(x[j]) : 0u;
+    warp_top<EPL>(key, wr, a.k, cand4[warp], best4[warp]);
+    for (int c = lane; c < a.k; c += 32) write_top(a, row, c, best4[warp][c], l);
 }
 
 // ------------------------------------------------------------------------------ distillation
@@ -613,95 +876,102 @@ __device__ __forceinline__ void teacher_gradient(const DistillArgs& a, const int
     store_as<TX, 1>(d + ids[c], v);
 }
 
-// A row a cluster.  The gradient reads the row again (from L2).  VEC: the gradient's rows start at the
-// same place of a 16-byte word as the logits' do.
+// A row a cluster of blocks.  The gradient reads the row again, from L2 as far as it holds the rows in work.  VEC: the gradient's rows start at the same place of a 16-byte word as the
+// logits' do.
 template <class TX, int T, bool VEC>
-__global__ void __launch_bounds__(T) distill_rows(const __grid_constant__ DistillArgs a) {
-    constexpr int VE = Row<TX>::VE;
+__global__ void __launch_bounds__(T, T == 256 ? 6 : T == 128 ? 12 : 32) distill_rows(const __grid_constant__ DistillArgs a) {
+    constexpr int VE = Row<TX>::VE, U = kBatch;
     __shared__ float s[3 * (T / 32)];
+    __shared__ float4 all[kMaxBlocks];
     __shared__ int ids[kMaxTeacher];
     __shared__ float p[kMaxTeacher], xs[kMaxTeacher];
     __shared__ int alive;
-    uint32_t rank, size;
-    cluster_place(rank, size);
+    uint32_t rank = 0, size = 1;
+    if constexpr (T > 32) cluster_place(rank, size);
+    if (size > 1) cluster_arrive();
     ptx::pdl_trigger();
     ptx::pdl_wait();
     const int64_t row = blockIdx.x / size;
-    const float w = a.weight ? __ldg(a.weight + row) : 1.f;
-    if (threadIdx.x < 32) {
-        const bool any = teacher(a, row, ids, p, w);
-        if (threadIdx.x == 0) alive = any;
-    }
-    __syncthreads();
     const Row<TX> r(a.logits, row, a.ld, a.V);
     int first, last;
     slice(r.nb, rank, size, first, last);
-    const bool live = alive, edges = rank == 0;   // live: the same in every block of the cluster
+    const bool edges = rank == 0;
+    const float w = a.weight ? __ldg(a.weight + row) : 1.f;
     auto own = [&](int e) { return e < r.head || e >= r.tail0 ? edges : e >= r.head + first * VE && e < r.head + last * VE; };
+    if (T == 32 || threadIdx.x >= T - 32) {   // the last warp, while the others read
+        const bool any = teacher(a, row, ids, p, w);
+        if (threadIdx.x == T - 1) alive = any;
+        // all of them for the loss; for the gradient this block's own
+        at_teacher(a, r, ids, xs, threadIdx.x & 31, 32, [&](int e) { return (edges && !a.lse_in) || own(e); });
+    }
     Gradient g{a.inv_t * kLog2e, 0.f, 0.f, 0.f};
-    if (live && a.lse_in) {
-        at_teacher(a, r, ids, xs, threadIdx.x, T, own);
+    bool live;
+    if (a.lse_in) {
         g.base = __ldg(a.lse_in + row) * kLog2e;
         g.coef = w * a.T;
         __syncthreads();
-    } else if (live) {
-        if (edges || a.dlogits) at_teacher(a, r, ids, xs, threadIdx.x, T, [](int) { return true; });
-        Stats<false> st(g.c);
-        read_row<TX, T, false>(r, first, last, edges, st);
-        join_block<T, false>(st, s, rank, size);
+        live = alive;
+        if (size > 1) cluster_wait();   // the arrival at the start
+    } else {
+        Stats<false> st = read_row<TX, T, false>(r, first, last, edges, g.c);
+        join_block<T, false>(st, s, g.c);
+        live = alive;
+        if (size > 1) {
+            cluster_wait();   // every block has started
+            push_stats(st, all, rank, size);
+            cluster_arrive();
+            cluster_wait();
+            join_cluster(st, all, size, g.c);
+        }
         const float log_s = logf(st.s);
         if (edges && threadIdx.x < 32) {
             const float loss = row_loss(a, ids, p, xs, w, st.m, log_s);
             if (threadIdx.x == 0) {
-                a.loss[row] = loss;
-                if (a.lse_out) a.lse_out[row] = fmaf(st.m, a.inv_t, log_s);
+                a.loss[row] = live ? loss : 0.f;
+                if (a.lse_out) a.lse_out[row] = live ? fmaf(st.m, a.inv_t, log_s) : 0.f;
             }
         }
         g.shift = st.m;
         g.coef = w * a.T / st.s;
-    } else if (edges && threadIdx.x == 0 && !a.lse_in) {
-        a.loss[row] = 0.f;
-        if (a.lse_out) a.lse_out[row] = 0.f;
     }
-    if (a.dlogits) {
-        TX* d = static_cast<TX*>(a.dlogits) + row * a.ld_d;
-#pragma unroll 4
-        for (int i = first + static_cast<int>(threadIdx.x); i < last; i += T) {
-            float v[VE];
-            if (live) {
-                const auto raw = load_raw<TX, VE>(r.word(i));
+    if (!a.dlogits) return;
+    TX* d = static_cast<TX*>(a.dlogits) + row * a.ld_d;
+    auto word = [&](const Raw<TX, VE>& x, int i) {
+        float v[VE];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) v[e] = g(raw_at<TX, VE>(raw, e));
-            } else {
+        for (int e = 0; e < VE; ++e) v[e] = live ? g(raw_at<TX, VE>(x, e)) : 0.f;
+        TX* to = d + r.head + static_cast<int64_t>(i) * VE;
+        if constexpr (VEC) {
+            store_as<TX, VE>(to, v);
+        } else {
 #pragma unroll
-                for (int e = 0; e < VE; ++e) v[e] = 0.f;
-            }
-            TX* to = d + r.head + static_cast<int64_t>(i) * VE;
-            if constexpr (VEC) {
-                store_as<TX, VE>(to, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    const float one[1] = {v[e]};
-                    store_as<TX, 1>(to + e, one);
-                }
+            for (int e = 0; e < VE; ++e) {
+                const float one[1] = {v[e]};
+                store_as<TX, 1>(to + e, one);
             }
         }
-        if (edges && static_cast<int>(threadIdx.x) < r.edges()) {
-            const int e = r.edge(threadIdx.x);
-            const float v[1] = {live ? g(r.at(e)) : 0.f};
-            store_as<TX, 1>(d + e, v);
-        }
-        __syncthreads();
-        if (live)
-            for (int c = threadIdx.x; c < a.k; c += T)
-                if (ids[c] >= 0 && own(ids[c])) teacher_gradient(a, ids, p, c, xs[c], g, w * a.T, d);
+    };
+    int i = first + static_cast<int>(threadIdx.x);
+    for (; i + (U - 1) * T < last; i += U * T) {
+        Raw<TX, VE> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = load_raw<TX, VE>(r.word(i + u * T));
+#pragma unroll
+        for (int u = 0; u < U; ++u) word(raw[u], i + u * T);
     }
-    if (size > 1) ptx::cluster_sync();   // the peers have read this block's sums
+    for (; i < last; i += T) word(load_raw<TX, VE>(r.word(i)), i);
+    if (edges && static_cast<int>(threadIdx.x) < r.edges()) {
+        const int e = r.edge(threadIdx.x);
+        const float v[1] = {live ? g(r.at(e)) : 0.f};
+        store_as<TX, 1>(d + e, v);
+    }
+    __syncthreads();
+    if (live)
+        for (int c = threadIdx.x; c < a.k; c += T)
+            if (ids[c] >= 0 && own(ids[c])) teacher_gradient(a, ids, p, c, xs[c], g, w * a.T, d);
 }
 
-// A row of up to 32 EPL entries in a warp's registers.
-template <class TX, int EPL>
+template <class TX, int EPL, bool VEC>
 __global__ void __launch_bounds__(128) distill_warps(const __grid_constant__ DistillArgs a) {
     __shared__ int ids4[4][kMaxTeacher];
     __shared__ float p4[4][kMaxTeacher], xs4[4][kMaxTeacher];
@@ -712,27 +982,20 @@ __global__ void __launch_bounds__(128) distill_warps(const __grid_constant__ Dis
     float *p = p4[warp], *xs = xs4[warp];
     ptx::pdl_wait();
     if (row >= a.n) return;
+    const Row<TX> r(a.logits, row, a.ld, a.V);
+    const WarpRow<TX, EPL, VEC> wr{const_cast<TX*>(r.p), a.V, lane};
+    float x[EPL];
+    wr.load(x);   // under way while the teacher's entries are read
     const float w = a.weight ? __ldg(a.weight + row) : 1.f;
     const bool live = teacher(a, row, ids, p, w);
-    const Row<TX> r(a.logits, row, a.ld, a.V);
-    float x[EPL];
     Gradient g{a.inv_t * kLog2e, 0.f, 0.f, 0.f};
     if (live) {
-        float top = kNegInf;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            x[j] = j * 32 + lane < a.V ? r.at(j * 32 + lane) : kNegInf;
-            top = fmaxf(top, x[j]);
-        }
         at_teacher(a, r, ids, xs, lane, 32, [](int) { return true; });
-        __syncwarp();
         if (a.lse_in) {
             g.base = __ldg(a.lse_in + row) * kLog2e;
             g.coef = w * a.T;
         } else {
-            Stats<false> st(g.c);
-            st.add(x, top);
-            st.join_warp();
+            const Stats<false> st = warp_stats<EPL, false>(x, g.c);
             const float log_s = logf(st.s), loss = row_loss(a, ids, p, xs, w, st.m, log_s);
             if (lane == 0) {
                 a.loss[row] = loss;
@@ -746,14 +1009,12 @@ __global__ void __launch_bounds__(128) distill_warps(const __grid_constant__ Dis
         if (a.lse_out) a.lse_out[row] = 0.f;
     }
     if (!a.dlogits) return;
-    TX* d = static_cast<TX*>(a.dlogits) + row * a.ld_d;
+    __syncwarp();   // the entries' logits are read before the row is written, maybe in their place
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        if (j * 32 + lane < a.V) {
-            const float v[1] = {live ? g(x[j]) : 0.f};
-            store_as<TX, 1>(d + j * 32 + lane, v);
-        }
-    }
+    for (int j = 0; j < EPL; ++j) x[j] = live ? g(x[j]) : 0.f;
+    TX* d = static_cast<TX*>(a.dlogits) + row * a.ld_d;
+    const WarpRow<TX, EPL, VEC> wd{d, a.V, lane};
+    wd.store(x);
     __syncwarp();
     if (live)
         for (int c = lane; c < a.k; c += 32)
@@ -767,39 +1028,58 @@ int elem(int t) { return t == TERN_BF16 ? 2 : 4; }
 bool ld_ok(int64_t ld, int64_t V) { return ld >= V && ld < (1ll << 40); }
 bool aligned_to(const void* p, int b) { return reinterpret_cast<uintptr_t>(p) % b == 0; }
 
-// Blocks that share a row: none while the rows fill the GPU twice, and each thread keeps a word.
+// Threads of a block: 256 for rows above 16 KB, below that a warp where rows are many (no barriers, and
+// many rows at once), else 128.
+int row_block(int64_t n, int64_t V, int es, int num_sms) { return V * es > 16384 ? 256 : n >= 16 * num_sms ? 32 : 128; }
+
+// Blocks that share a row: twice as many until the rows fill the GPU twice, as long as each thread keeps a word.
 int row_blocks(int64_t n, int64_t V, int es, int T, int num_sms) {
     int c = 1;
-    while (c < 16 && n * c < 2 * num_sms && V * es / (2 * c) >= 16 * T) c *= 2;
+    while (T > 32 && c < kMaxBlocks && n * c < 2 * num_sms && V * es / (2 * c) >= 16 * T) c *= 2;
     return c;
 }
-bool narrow(int64_t V, int es) { return V * es <= 16384; }   // a block of 128 threads, else 512
+
+// Whether a warp's rows can be taken in 16-byte words.
+bool warp_words(const void* p, int64_t ld, int64_t n, int64_t V, int es) { return rows_allow(p, ld, n, V, 16 / es, es); }
+
+constexpr int kWarpRow = 256;   // widest row that a warp holds in registers
 
 template <class TX>
 int run_score(const ScoreArgs& a, int num_sms, cudaStream_t s) {
-    if (a.V <= 256) return launch_pdl(score_warps<TX, 8>, dim3((a.n + 3) / 4), dim3(128), 0, s, a);
-    if (a.V <= kWarpRow) return launch_pdl(score_warps<TX, 32>, dim3((a.n + 3) / 4), dim3(128), 0, s, a);
-    const bool few = narrow(a.V, kElem<TX>);
-    const int c = row_blocks(a.n, a.V, kElem<TX>, few ? 128 : 512, num_sms);
-    if (few) return launch_cluster(score_rows<TX, 128>, a.n * c, 128, 0, c, true, s, a);
-    return launch_cluster(score_rows<TX, 512>, a.n * c, 512, 0, c, true, s, a);
+    constexpr int es = kElem<TX>;
+    if (a.V <= kWarpRow) {
+        const dim3 grid((a.n + 3) / 4), block(128);
+        if (warp_words(a.logits, a.ld, a.n, a.V, es)) return launch_pdl(score_warps<TX, kWarpRow / 32, true>, grid, block, 0, s, a);
+        return launch_pdl(score_warps<TX, kWarpRow / 32, false>, grid, block, 0, s, a);
+    }
+    const int T = row_block(a.n, a.V, es, num_sms), c = row_blocks(a.n, a.V, es, T, num_sms);
+    if (T == 32) return launch_cluster(score_rows<TX, 32>, a.n, T, 0, 1, true, s, a);
+    if (T == 128) return launch_cluster(score_rows<TX, 128>, a.n * c, T, 0, c, true, s, a);
+    return launch_cluster(score_rows<TX, 256>, a.n * c, T, 0, c, true, s, a);
 }
 
-template <class TX, int T>
+template <class TX, bool VEC>
 int run_distill_rows(const DistillArgs& a, int num_sms, cudaStream_t s) {
     constexpr int es = kElem<TX>;
+    const int T = row_block(a.n, a.V, es, num_sms);
     const int c = row_blocks(a.n, a.V, es, T, num_sms);
-    const bool vec = (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.dlogits)) % 16 == 0 &&
-                     (a.n <= 1 || (a.ld - a.ld_d) * es % 16 == 0);
-    if (vec) return launch_cluster(distill_rows<TX, T, true>, a.n * c, T, 0, c, true, s, a);
-    return launch_cluster(distill_rows<TX, T, false>, a.n * c, T, 0, c, true, s, a);
+    if (T == 32) return launch_cluster(distill_rows<TX, 32, VEC>, a.n, T, 0, 1, true, s, a);
+    if (T == 128) return launch_cluster(distill_rows<TX, 128, VEC>, a.n * c, T, 0, c, true, s, a);
+    return launch_cluster(distill_rows<TX, 256, VEC>, a.n * c, T, 0, c, true, s, a);
 }
 
 template <class TX>
 int run_distill(const DistillArgs& a, int num_sms, cudaStream_t s) {
-    if (a.V <= 256) return launch_pdl(distill_warps<TX, 8>, dim3((a.n + 3) / 4), dim3(128), 0, s, a);
-    if (a.V <= kWarpRow) return launch_pdl(distill_warps<TX, 32>, dim3((a.n + 3) / 4), dim3(128), 0, s, a);
-    return narrow(a.V, kElem<TX>) ? run_distill_rows<TX, 128>(a, num_sms, s) : run_distill_rows<TX, 512>(a, num_sms, s);
+    constexpr int es = kElem<TX>;
+    if (a.V <= kWarpRow) {
+        const dim3 grid((a.n + 3) / 4), block(128);
+        if (warp_words(a.logits, a.ld, a.n, a.V, es) && (!a.dlogits || warp_words(a.dlogits, a.ld_d, a.n, a.V, es)))
+            return launch_pdl(distill_warps<TX, kWarpRow / 32, true>, grid, block, 0, s, a);
+        return launch_pdl(distill_warps<TX, kWarpRow / 32, false>, grid, block, 0, s, a);
+    }
+    const bool vec = (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.dlogits)) % 16 == 0 &&
+                     (a.n <= 1 || (a.ld - a.ld_d) * es % 16 == 0);
+    return vec ? run_distill_rows<TX, true>(a, num_sms, s) : run_distill_rows<TX, false>(a, num_sms, s);
 }
 
 int distill(const tern_distillation* t, const float* lse_in, float* loss, float* lse, void* dlogits, int64_t ld_d, void* stream) {

@@ -43,6 +43,7 @@
 #include <cuda_bf16.h>
 
 #include "mma.cuh"
+#include "pairs.cuh"
 
 namespace tern {
 namespace {
@@ -52,34 +53,6 @@ constexpr int kMaxCluster = 16;   // blocks of a cluster
 
 __device__ int g_scan_status;     // 1 once a wait for a peer's totals gave up
 
-// --------------------------------------------------------------- pairs of fp32
-// Two neighbouring channels in one 64-bit register pair: sm_103a multiplies and adds both in one
-// instruction, which the instruction count of these kernels needs.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 pair(float x, float y) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
-__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
 __device__ __forceinline__ F2 shfl2(F2 a, int from) { return F2{__shfl_sync(0xffffffffu, a.v, from)}; }
 
 // --------------------------------------------------------------- element access

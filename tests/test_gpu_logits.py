@@ -115,6 +115,25 @@ def test_score_masks_and_ties(cuda_lib, V, dtype):
             _check_score(cuda_lib, x[r:r + 1], _tokens(1, V) + 3, kk)
 
 
+@pytest.mark.parametrize("V", [900, 8000, 70000])
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_score_large_entries_in_few_places(cuda_lib, V, dtype):
+    """Thousands of large entries, all in the words of fewer threads than k (of blocks of 128 or 256, or the
+    lanes of a warp), largest last, and with many equal ones at the k-th place."""
+    randn, rand = _gen(V + 1)
+    i = torch.arange(V, device="cuda")
+    words = i // (8 if dtype == torch.bfloat16 else 4)
+    rows = []
+    for T, few in ((256, 8), (128, 24), (512, 20), (32, 5)):
+        big = words % T < few
+        rows += [torch.where(big, 5 + 3 * i / V, randn(V)), torch.where(big, 5 + 3 * rand(V), randn(V)), torch.where(big, 7.0, randn(V)),
+                 torch.where(big, 5 + torch.round(2 * rand(V)), randn(V)), torch.where(big, -1.0, -math.inf), torch.where(big, randn(V), -math.inf)]
+    x = torch.stack(rows).to(dtype)
+    for k in (1, 9, 40, 64):
+        _check_score(cuda_lib, x, _tokens(len(rows), V), k)
+        _check_score(cuda_lib, x[6:7], _tokens(1, V) + 3, k)
+
+
 @pytest.mark.parametrize("V", [40, 900, 3000, 40000])
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_score_rows_without_a_distribution(cuda_lib, V, dtype):
