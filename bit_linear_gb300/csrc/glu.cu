@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 
 #include "mma.cuh"
+#include "pairs.cuh"
 #include "rows.cuh"
 
 namespace tern {
@@ -44,39 +45,54 @@ __device__ __forceinline__ float reciprocal(float x) {
     return y;
 }
 
-// act(g) and, with D, act'(g).  The special functions' errors (2^-22 relative each) are far below the
-// outputs' rounding to bf16.
+__device__ __forceinline__ F2 each(F2 x, float (*f)(float)) {
+    float a, b;
+    split(x, a, b);
+    return pair(f(a), f(b));
+}
+__device__ __forceinline__ float magnitude(float x) { return fabsf(x); }
+__device__ __forceinline__ float positive(float x) { return x < 0.f ? 0.f : x; }   // NaN passes
+__device__ __forceinline__ float bounded(float x) {                               // by 126; NaN passes
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(126.f));
+    return y;
+}
+
+// act(g) and, with D, act'(g), of two neighbours.  The special functions' errors (2^-22 relative each) are
+// far below the outputs' rounding to bf16.
 template <int ACT, bool D>
-__device__ __forceinline__ void activate(float g, float& a, float& d) {
+__device__ __forceinline__ void activate(F2 g, F2& a, F2& d) {
     if constexpr (ACT == TERN_ACT_RELU2) {
-        const float r = g < 0.f ? 0.f : g;   // NaN passes
-        a = r * r;
-        d = 2.f * r;
+        const F2 r = each(g, positive);
+        a = mul2(r, r);
+        if (D) d = add2(r, r);
     } else if constexpr (ACT == TERN_ACT_GELU) {
         // g Phi(g): the upper tail's approximation by Hastings (Abramowitz and Stegun 7.1.26, 1.5e-7
         // absolute in erf), whose exponential the density shares
-        const float z = fabsf(g) * 0.70710678f;
-        const float t = reciprocal(fmaf(0.3275911f, z, 1.f));
-        const float e = pow2(g * g * -0.72134752f);   // exp(-g^2 / 2)
-        float p = fmaf(1.061405429f, t, -1.453152027f);
-        p = fmaf(p, t, 1.421413741f);
-        p = fmaf(p, t, -0.284496736f);
-        p = fmaf(p, t, 0.254829592f);
-        const float tail = 0.5f * p * t * e;
-        const float cdf = g < 0.f ? tail : 1.f - tail;
-        a = g * cdf;
-        if (D) d = fmaf(g * 0.39894228f, e, cdf);
+        const F2 z = each(g, magnitude);
+        const F2 t = each(fma2(z, both(0.3275911f * 0.70710678f), both(1.f)), reciprocal);
+        const F2 e = each(mul2(mul2(g, g), both(-0.72134752f)), pow2);   // exp(-g^2 / 2)
+        F2 p = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+        p = fma2(p, t, both(0.5f * 1.421413741f));
+        p = fma2(p, t, both(0.5f * -0.284496736f));
+        p = fma2(p, t, both(0.5f * 0.254829592f));
+        const F2 half = fma2(mul2(p, t), mul2(e, both(-1.f)), both(0.5f));   // Phi(|g|) - 1/2
+        float h0, h1, g0, g1;
+        split(half, h0, h1);
+        split(g, g0, g1);
+        const F2 cdf = add2(pair(copysignf(h0, g0), copysignf(h1, g1)), both(0.5f));
+        a = mul2(g, cdf);
+        if (D) d = fma2(mul2(g, both(0.39894228f)), e, cdf);
     } else {
-        // sigmoid from exp(-|g|), which cannot overflow; its complement without a difference
-        const float e = pow2(fabsf(g) * -1.44269504f);
-        const float r = reciprocal(1.f + e);
-        const float s = g < 0.f ? e * r : r, c = g < 0.f ? r : e * r;
+        // s = 1 / (1 + e) and its complement e / (1 + e); e = exp(-g) kept finite
+        const F2 e = each(each(mul2(g, both(-1.44269504f)), bounded), pow2);
+        const F2 s = each(add2(e, both(1.f)), reciprocal), c = mul2(e, s);
         if constexpr (ACT == TERN_ACT_SIGMOID) {
             a = s;
-            if (D) d = s * c;
+            if (D) d = mul2(s, c);
         } else {
-            a = g * s;
-            if (D) d = fmaf(a, c, s);
+            a = mul2(g, s);
+            if (D) d = fma2(a, c, s);
         }
     }
 }
@@ -89,6 +105,7 @@ struct GluArgs {
     uint16_t* pair;         // [M][2N]: the factors (with H; may be null), or dY (with dH)
     int M, N, K, act;
     int tiles_m, tiles_n, num_kb;
+    bool whole;             // H and pair are 32-byte aligned
 };
 
 // CG CTAs share a tile of 128 CG rows by HN outputs: 2 HN accumulator columns.
@@ -110,25 +127,21 @@ __device__ __forceinline__ bool glu_wait(uint32_t bar, uint32_t parity, volatile
     return wait_limited(bar, parity, abort_flag, watch, kWaitLimitNs, [] { atomicExch(&g_glu_status, 1); });
 }
 
-// 32 rows (a lane each) of 16 bf16, two 16-byte units a lane: neighbouring lanes swap one, so that a store
-// writes whole 32-byte sectors, of sixteen rows at a time.
-__device__ __forceinline__ void store_rows(uint16_t* base, int64_t ld, int rows, const uint32_t (&w)[8], int lane) {
-    const bool odd = lane & 1;
-    uint32_t give[4], keep[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) give[i] = odd ? w[i] : w[4 + i], keep[i] = odd ? w[4 + i] : w[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) give[i] = __shfl_xor_sync(0xffffffffu, give[i], 1);
-    // an even lane has its own first unit and its neighbour's, an odd lane the second units
-    const int r = lane & ~1;
-    uint16_t* to = base + r * ld + 8 * (lane & 1);
-    const uint4 lower = odd ? make_uint4(give[0], give[1], give[2], give[3]) : make_uint4(keep[0], keep[1], keep[2], keep[3]);
-    const uint4 upper = odd ? make_uint4(keep[0], keep[1], keep[2], keep[3]) : make_uint4(give[0], give[1], give[2], give[3]);
-    if (r < rows) *reinterpret_cast<uint4*>(to) = lower;
-    if (r + 1 < rows) *reinterpret_cast<uint4*>(to + ld) = upper;
+// A lane's 16 bf16 of a row, 32 bytes: one access where rows are aligned to that (`whole`).
+__device__ __forceinline__ void store_row(uint16_t* to, const uint32_t (&w)[8], bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                     "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+__device__ __forceinline__ uint32_t pack_bf16(F2 x) {
+    float a, b;
+    split(x, a, b);
     const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&t);
 }
@@ -137,50 +150,46 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // and tu (the value's): H, or H and the factors, or dY.
 template <int ACT, bool BACK, bool TWO>
 __device__ __forceinline__ void glu_chunk(const GluArgs& a, uint32_t tg, uint32_t tu, int wrow, int c0, int lane) {
-    const int rows = a.M - wrow;   // > 0
+    const int64_t row = wrow + lane;
+    const bool in = row < a.M;
     uint32_t h[8], p[8], q[8];
     uint32_t rg[16], ru[16];
     ptx::tmem_ld_32x32b_x16(tg, rg);
     ptx::tmem_ld_32x32b_x16(tu, ru);
     Raw<__nv_bfloat16, 16> dh;
-    if (BACK) dh = load_raw<__nv_bfloat16, 16>(reinterpret_cast<const __nv_bfloat16*>(a.dH) + (wrow + min(lane, rows - 1)) * static_cast<int64_t>(a.N) + c0);
+    if (BACK) dh = load_raw<__nv_bfloat16, 16>(reinterpret_cast<const __nv_bfloat16*>(a.dH) + (in ? row : wrow) * a.N + c0);
     const float4* pg = reinterpret_cast<const float4*>(a.scale + c0);
     const float4* pu = reinterpret_cast<const float4*>(a.scale + a.N + c0);
     ptx::tmem_wait_ld();
 #pragma unroll
     for (int b = 0; b < 4; ++b) {   // four columns
         const float4 sg = __ldg(pg + b), su = __ldg(pu + b);
-        const float g[4] = {__uint_as_float(rg[4 * b]) * sg.x, __uint_as_float(rg[4 * b + 1]) * sg.y, __uint_as_float(rg[4 * b + 2]) * sg.z,
-                            __uint_as_float(rg[4 * b + 3]) * sg.w};
-        const float u[4] = {__uint_as_float(ru[4 * b]) * su.x, __uint_as_float(ru[4 * b + 1]) * su.y, __uint_as_float(ru[4 * b + 2]) * su.z,
-                            __uint_as_float(ru[4 * b + 3]) * su.w};
-        float f[4], d[4];
-        if constexpr (TWO) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) activate<ACT, true>(g[i], f[i], d[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] *= u[i];
-            if constexpr (BACK) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = raw_at<__nv_bfloat16, 16>(dh, 4 * b + i);
-                    d[i] *= x;
-                    f[i] *= x;
+        for (int i = 0; i < 2; ++i) {
+            const int o = 2 * b + i;   // two of them
+            const F2 g = mul2(pair(__uint_as_float(rg[2 * o]), __uint_as_float(rg[2 * o + 1])), i ? pair(sg.z, sg.w) : pair(sg.x, sg.y));
+            const F2 u = mul2(pair(__uint_as_float(ru[2 * o]), __uint_as_float(ru[2 * o + 1])), i ? pair(su.z, su.w) : pair(su.x, su.y));
+            F2 f, d;
+            activate<ACT, TWO>(g, f, d);
+            if constexpr (!BACK) h[o] = pack_bf16(mul2(f, u));
+            if constexpr (TWO) {
+                d = mul2(d, u);
+                if constexpr (BACK) {
+                    const F2 x = pair(raw_at<__nv_bfloat16, 16>(dh, 2 * o), raw_at<__nv_bfloat16, 16>(dh, 2 * o + 1));
+                    d = mul2(d, x);
+                    f = mul2(f, x);
                 }
+                p[o] = pack_bf16(d);
+                q[o] = pack_bf16(f);
             }
-            p[2 * b] = pack_bf16(d[0], d[1]), p[2 * b + 1] = pack_bf16(d[2], d[3]);
-            q[2 * b] = pack_bf16(f[0], f[1]), q[2 * b + 1] = pack_bf16(f[2], f[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) activate<ACT, false>(g[i], f[i], d[i]);
         }
-        if constexpr (!BACK) h[2 * b] = pack_bf16(f[0] * u[0], f[1] * u[1]), h[2 * b + 1] = pack_bf16(f[2] * u[2], f[3] * u[3]);
     }
-    if constexpr (!BACK) store_rows(a.H + static_cast<int64_t>(wrow) * a.N + c0, a.N, rows, h, lane);
+    if (!in) return;
+    if constexpr (!BACK) store_row(a.H + row * a.N + c0, h, a.whole);
     if constexpr (TWO) {
-        uint16_t* to = a.pair + static_cast<int64_t>(wrow) * 2 * a.N + c0;
-        store_rows(to, 2 * static_cast<int64_t>(a.N), rows, p, lane);
-        store_rows(to + a.N, 2 * static_cast<int64_t>(a.N), rows, q, lane);
+        uint16_t* to = a.pair + row * 2 * a.N + c0;
+        store_row(to, p, a.whole);
+        store_row(to + a.N, q, a.whole);
     }
 }
 
@@ -536,14 +545,17 @@ __global__ void __launch_bounds__(kCodeWarps * 64, 2) glu_codes(const __grid_con
         }
         vg *= sg;
         vu *= su;
-        float f, d;
+        F2 f, d;
+        const F2 g2 = both(vg);
         switch (a.act) {
-        case TERN_ACT_SILU: activate<TERN_ACT_SILU, false>(vg, f, d); break;
-        case TERN_ACT_GELU: activate<TERN_ACT_GELU, false>(vg, f, d); break;
-        case TERN_ACT_RELU2: activate<TERN_ACT_RELU2, false>(vg, f, d); break;
-        default: activate<TERN_ACT_SIGMOID, false>(vg, f, d); break;
+        case TERN_ACT_SILU: activate<TERN_ACT_SILU, false>(g2, f, d); break;
+        case TERN_ACT_GELU: activate<TERN_ACT_GELU, false>(g2, f, d); break;
+        case TERN_ACT_RELU2: activate<TERN_ACT_RELU2, false>(g2, f, d); break;
+        default: activate<TERN_ACT_SIGMOID, false>(g2, f, d); break;
         }
-        a.H[m * static_cast<int64_t>(a.N) + n] = __bfloat16_as_ushort(__float2bfloat16_rn(f * vu));
+        float act, same;
+        split(f, act, same);
+        a.H[m * static_cast<int64_t>(a.N) + n] = __bfloat16_as_ushort(__float2bfloat16_rn(act * vu));
     }
 }
 
@@ -636,6 +648,7 @@ int glu_width(GluArgs& a, const uint16_t* X, const uint16_t* T, int num_sms, cud
     return glu_gemm<Wide>(a, X, T, num_sms, s);
 }
 int glu_many(GluArgs& a, const uint16_t* X, const uint16_t* T, int num_sms, cudaStream_t s) {
+    a.whole = ((reinterpret_cast<uintptr_t>(a.H) | reinterpret_cast<uintptr_t>(a.pair)) & 31) == 0;   // N % 16 == 0: every row then
     return a.M > kBM ? glu_width<GluPair, GluPairNarrow>(a, X, T, num_sms, s) : glu_width<GluOne, GluOneNarrow>(a, X, T, num_sms, s);
 }
 

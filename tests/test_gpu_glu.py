@@ -123,6 +123,24 @@ def test_few_rows_from_either_weight(cuda_lib, M, K, N):
         assert torch.equal(out, again) and torch.all(guard == 99.0)
 
 
+def test_outputs_at_16_bytes(cuda_lib):
+    """Outputs that start between 32-byte words: the same bits."""
+    bl = cuda_lib
+    M, K, N = 150, 64, 80
+    X, q, scale, dH = _inputs(M, K, N, 3)
+    tiles = _tiles(bl, q, scale)
+    outs = []
+    for off in (0, 8):
+        place = lambda k: torch.full((M * k + 16,), 9.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+        bufs = [place(N), place(2 * N), place(2 * N)]
+        H, pair, dY = (b[off:off + M * k].view(M, k) for b, k in zip(bufs, (N, 2 * N, 2 * N)))
+        bl.tern_glu_fwd(X, tiles, scale, H, saved=pair)
+        bl.tern_glu_bwd(dH, dY, X=X, tiles=tiles, scale=scale)
+        assert all(torch.all(b[:off] == 9.0) and torch.all(b[off + M * k:] == 9.0) for b, k in zip(bufs, (N, 2 * N, 2 * N)))
+        outs.append([t.clone() for t in (H, pair, dY)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 def test_extreme_gates(cuda_lib):
     """Gates far out on both sides: no overflow, no NaN; a NaN row stays in its row."""
     bl = cuda_lib
