@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_glu_gemm(const __grid_cons
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue
         const int quad = warp & 3;   // a warp may touch TMEM lanes 32 (warp % 4) .. + 31
-        const uint32_t tempty_leader = CG == 2 ? ptx::mapa_shared(TEMPTY0, 0) : TEMPTY0;
+        const uint32_t tempty_leader = CG == 2 ? ptx::mapa_shared(TEMPTY0, 0) : TEMPTY0;   // shared::cta addresses are its own block's shared::cluster ones
         constexpr int CHUNKS = C::HN / 16 / (C::EPI_WARPS / 4);   // of 16 columns, a warp's
         const int j0 = ((warp - 2) / 4) * CHUNKS;
         int local = 0;
@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tern_glu_gemm(const __grid_cons
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (CG == 2) ptx::mbar_arrive_cluster(tempty_leader + 8u * acc);
-                else ptx::mbar_arrive(TEMPTY0 + 8u * acc);
+                // Relaxed: what it tells is that the accumulator has been read.  A release would wait for the
+                // tile's stores to memory (8192 x 512 x 1360: 37.5 us for the gradient).
+                asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(tempty_leader + 8u * acc) : "memory");
             }
         }
     }
