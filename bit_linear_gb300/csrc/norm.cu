@@ -21,12 +21,13 @@
 #include <algorithm>
 #include <cmath>
 
+#include "pairs.cuh"
 #include "rows.cuh"
 
 namespace tern {
 namespace {
 
-constexpr int kPartMax = 608;   // blocks of the gradient: four for each of 152 SMs
+constexpr int kPartMax = 1216;   // blocks of the gradient: eight for each of 152 SMs
 
 struct NormArgs {
     const void* x;
@@ -43,16 +44,17 @@ struct NormArgs {
 };
 
 // EPT elements of a row in registers: thread t holds V neighbouring elements at (j T + t) V.
-// T threads a row, R rows a block side by side (R > 1 with T = 32 only).
+// T threads a row, R rows a block side by side (R > 1 with T <= 32 only).
 template <class TX, class TY, int T, int R, int EPT, int V>
 __global__ void __launch_bounds__(T * R, 1) norm_fwd(const __grid_constant__ NormArgs a) {
     constexpr int NV = EPT / V;
-    __shared__ float sums[2][2 * (T / 32)];
+    __shared__ float sums[2][2 * ((T + 31) / 32)];
     ptx::pdl_trigger();
     const int t = threadIdx.x % T;
-    const int row = static_cast<int>(blockIdx.x) * R + static_cast<int>(threadIdx.x) / T;
+    const int64_t mine = static_cast<int64_t>(blockIdx.x) * R + static_cast<int>(threadIdx.x) / T;
     ptx::pdl_wait();
-    if (row >= a.n) return;   // whole warps, and with T > 32 whole blocks
+    const bool in = mine < a.n;   // a last block's other rows do the last one again, unwritten
+    const int64_t row = in ? mine : a.n - 1;
     const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
     Raw<TX, V> raw[NV];
 #pragma unroll
@@ -88,6 +90,7 @@ __global__ void __launch_bounds__(T * R, 1) norm_fwd(const __grid_constant__ Nor
     const float delta = q[0] * a.inv_d;
     const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-delta, delta, q[1] * a.inv_d), 0.f) + a.eps);
     // fmaxf drops a NaN: the row's own comes back through x - mean
+    if (!in) return;
     if (t == 0) {
         if (a.mean) a.mean[row] = mean + delta;
         if (a.rstd) a.rstd[row] = q[1] == q[1] ? rstd : q[1];
@@ -316,48 +319,349 @@ __global__ void __launch_bounds__(256) norm_cols_wide(const __grid_constant__ No
     if (dbias) dbias[c] = b;
 }
 
-// Sums of the blocks' columns: a block takes 32 columns, warp w adds the parts w, w + 16, ... and the
-// warps' sums are added in order.  grid.y = 2: the weight's, the bias's.
-__global__ void __launch_bounds__(512) norm_cols(const float* __restrict__ part, int parts, int D, float* dweight, float* dbias) {
-    __shared__ float s[16][33];
+// Sums of the blocks' columns: a block takes 32 columns, warp w adds the parts w, w + 32, ... (all asked
+// for at once) and the warps' sums are added in order.  grid.y = 2: the weight's, the bias's.
+__global__ void __launch_bounds__(1024) norm_cols(const float* __restrict__ part, int parts, int D, float* dweight, float* dbias) {
+    constexpr int EACH = (kPartMax + 31) / 32;
+    __shared__ float s[32][33];
     ptx::pdl_trigger();
     ptx::pdl_wait();
     float* out = blockIdx.y == 0 ? dweight : dbias;
     if (!out) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = static_cast<int>(blockIdx.x) * 32 + lane;
-    float v = 0.f;
-    if (c < D) {
-        const float* p = part + static_cast<int64_t>(blockIdx.y) * parts * D + c;
-#pragma unroll 8
-        for (int k = warp; k < parts; k += 16) v += __ldcg(p + static_cast<int64_t>(k) * D);
-    }
-    s[warp][lane] = v;
-    __syncthreads();
-    if (warp == 0 && c < D) {
-        float t = 0.f;
+    const float* p = part + (static_cast<int64_t>(blockIdx.y) * parts + warp) * D + c;
+    float v[EACH], t = 0.f;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) t += s[w][lane];
-        out[c] = t;
+    for (int k = 0; k < EACH; ++k) v[k] = c < D && warp + 32 * k < parts ? __ldcg(p + static_cast<int64_t>(32 * k) * D) : 0.f;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) t += v[k];
+    s[warp][lane] = t;
+    __syncthreads();
+    t = s[lane][warp];   // column `warp`, the warps' sums side by side
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+    const int mine = static_cast<int>(blockIdx.x) * 32 + warp;
+    if (lane == 0 && mine < D) out[mine] = t;
+}
+
+// ---- rows in 16-byte words (the usual case): the same sums, with rows on their way while others are
+// worked on.  A block takes two rows at a time, whose sums share their exchanges and barriers, and copies
+// the two after next into shared memory as it leaves their places; a thread reads only the words that
+// it copied itself.  Arithmetic on pairs of neighbours (an element takes 8 instructions in the forward
+// and 11 in the gradient; twice as many without).
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait_all_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// A thread takes 16 elements of a row, in two runs of eight.  Blocks that an SM holds:
+constexpr int pair_blocks(int T, bool bwd) { return T == 64 ? 8 : T <= 128 ? (bwd ? 4 : 6) : T == 256 ? (bwd ? 2 : 3) : 1; }
+constexpr int kPairWidest = 8192;          // channels of a row that 512 threads take
+constexpr size_t kPairSpace = 216 << 10;   // shared memory for it
+
+// A thread's copies of eight elements: one word of bf16, two of fp32, THREADS words apart.
+template <class T, int THREADS>
+struct Eight {
+    static constexpr int WORDS = kElem<T> == 2 ? 1 : 2;
+    static __device__ __forceinline__ void ask(uint4* to, const T* from) {
+#pragma unroll
+        for (int h = 0; h < WORDS; ++h) copy16(ptx::smem_u32(to + h * THREADS), from + h * (16 / kElem<T>));
+    }
+    static __device__ __forceinline__ void get(const uint4* from, F2 (&x)[4]) {
+#pragma unroll
+        for (int h = 0; h < WORDS; ++h) {
+            const uint4 u = from[h * THREADS];
+            if constexpr (WORDS == 1) {
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            } else {
+                x[2 * h] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
+                x[2 * h + 1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
+            }
+        }
+    }
+    static __device__ __forceinline__ void put(T* to, const F2 (&x)[4]) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split(x[i], v[2 * i], v[2 * i + 1]);
+        store_as<T, 8>(to, v);
+    }
+};
+
+__device__ __forceinline__ float sum_of(F2 x) {
+    float a, b;
+    split(x, a, b);
+    return a + b;
+}
+// Eight parameters of the columns from c, or a value where there are none.
+__device__ __forceinline__ void params(const float* p, int c, int D, float other, F2 (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = both(other);
+    if (p && c < D) {
+        const auto raw = load_raw<float, 8>(p + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = pair(raw_at<float, 8>(raw, 2 * i), raw_at<float, 8>(raw, 2 * i + 1));
+    }
+}
+
+template <class TX, class TY, int T, int R>
+__global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(const __grid_constant__ NormArgs a) {
+    using X = Eight<TX, T * R>;
+    extern __shared__ uint4 ring[];   // [2 turns][2 rows][2 runs][X::WORDS][T R]
+    __shared__ float sums[2][4 * ((T + 31) / 32)];
+    ptx::pdl_trigger();
+    const int t = threadIdx.x % T;
+    const int64_t step = 2 * static_cast<int64_t>(gridDim.x) * R;
+    int64_t row = 2 * (static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / T);
+    const int ahead = T < 32 ? 2 * (threadIdx.x % 32 / T) : 0;   // of the warp's first row: a warp stays together
+    auto place = [&](int turn, int which, int j) { return ring + ((turn * 2 + which) * 2 + j) * X::WORDS * T * R + threadIdx.x; };
+    auto ask = [&](int64_t of, int turn) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = (j * T + t) * 8;
+                if (of + which < a.n && c < a.D) X::ask(place(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c);
+            }
+        copies_close();
+    };
+    ptx::pdl_wait();
+    ask(row, 0);
+    ask(row + step, 1);
+    F2 w[2][4], b[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        params(a.weight, (j * T + t) * 8, a.D, 1.f, w[j]);
+        params(a.bias, (j * T + t) * 8, a.D, 0.f, b[j]);
+    }
+    for (int turn = 0; row - ahead < a.n; row += step, turn ^= 1) {
+        copies_wait_all_but_one();
+        F2 x[4];
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            F2 u = both(0.f);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if ((j * T + t) * 8 < a.D) {
+                    X::get(place(turn, which, j), x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u = add2(u, x[i]);
+                }
+            }
+            s[which] = sum_of(u);
+        }
+        row_sums<T, 2>(s, sums[0]);
+        const float mean[2] = {s[0] * a.inv_d, s[1] * a.inv_d};
+        float q[4];
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            F2 u = both(0.f), v = both(0.f);
+            const F2 shift = both(-mean[which]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if ((j * T + t) * 8 < a.D) {
+                    X::get(place(turn, which, j), x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 d = add2(x[i], shift);
+                        u = add2(u, d);
+                        v = fma2(d, d, v);
+                    }
+                }
+            }
+            q[2 * which] = sum_of(u), q[2 * which + 1] = sum_of(v);
+        }
+        row_sums<T, 4>(q, sums[1]);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            if (row + which >= a.n) break;
+            const float delta = q[2 * which] * a.inv_d, sq = q[2 * which + 1];
+            const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-delta, delta, sq * a.inv_d), 0.f) + a.eps);
+            if (t == 0) {
+                if (a.mean) a.mean[row + which] = mean[which] + delta;
+                if (a.rstd) a.rstd[row + which] = sq == sq ? rstd : sq;   // fmaxf drops a NaN
+            }
+            TY* y = static_cast<TY*>(a.y) + (row + which) * a.ld_y;
+            const F2 shift = both(-mean[which]), rest = both(-delta), scale = both(rstd);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = (j * T + t) * 8;
+                if (c < a.D) {
+                    X::get(place(turn, which, j), x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = fma2(mul2(add2(add2(x[i], shift), rest), scale), w[j][i], b[j][i]);
+                    Eight<TY, T * R>::put(y + c, x);
+                }
+            }
+        }
+        ask(row + 2 * step, turn);
+    }
+}
+
+template <class TX, class TY, int T, int R>
+__global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(const __grid_constant__ NormArgs a) {
+    using X = Eight<TX, T * R>;
+    using Y = Eight<TY, T * R>;
+    constexpr int ROW = 2 * (X::WORDS + Y::WORDS) * T * R;   // words of a row of x and one of dy
+    extern __shared__ uint4 ring[];                          // [2 turns][2 rows] of them
+    __shared__ float sums[2][6 * ((T + 31) / 32)];
+    ptx::pdl_trigger();
+    const int t = threadIdx.x % T, r = static_cast<int>(threadIdx.x) / T;
+    const int64_t step = 2 * static_cast<int64_t>(gridDim.x) * R;
+    int64_t row = 2 * (static_cast<int64_t>(blockIdx.x) * R + r);
+    const int ahead = T < 32 ? 2 * (threadIdx.x % 32 / T) : 0;   // of the warp's first row: a warp stays together
+    auto place_x = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + j * X::WORDS * T * R + threadIdx.x; };
+    auto place_d = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + (2 * X::WORDS + j * Y::WORDS) * T * R + threadIdx.x; };
+    float mean[2], rstd[2], mean_next[2] = {0.f, 0.f}, rstd_next[2] = {0.f, 0.f};
+    auto ask = [&](int64_t of, int turn) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = (j * T + t) * 8;
+                if (of + which < a.n && c < a.D) {
+                    X::ask(place_x(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c);
+                    Y::ask(place_d(turn, which, j), static_cast<const TY*>(a.dy) + (of + which) * a.ld_dy + c);
+                }
+            }
+        copies_close();
+    };
+    auto stats = [&](int64_t of, float (&m)[2], float (&s)[2]) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const bool in = of + which < a.n;
+            m[which] = in ? __ldg(a.mean + of + which) : 0.f;
+            s[which] = in ? __ldg(a.rstd + of + which) : 0.f;
+        }
+    };
+    ptx::pdl_wait();
+    ask(row, 0);
+    ask(row + step, 1);
+    stats(row, mean, rstd);
+    F2 w[2][4], dw[2][4], db[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        params(a.weight, (j * T + t) * 8, a.D, 1.f, w[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = both(0.f);
+    }
+    for (int turn = 0; row - ahead < a.n; row += step, turn ^= 1) {
+        stats(row + step, mean_next, rstd_next);
+        copies_wait_all_but_one();
+        F2 x[4], d[4];
+        float s[6];   // a row's sums of g, g (x - mean), x - mean
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            F2 u0 = both(0.f), u1 = u0, u2 = u0;
+            const F2 shift = both(-mean[which]);
+            if (row + which < a.n) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if ((j * T + t) * 8 < a.D) {
+                        X::get(place_x(turn, which, j), x);
+                        Y::get(place_d(turn, which, j), d);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const F2 e = add2(x[i], shift), g = mul2(d[i], w[j][i]);
+                            u0 = add2(u0, g);
+                            u1 = fma2(g, e, u1);
+                            u2 = add2(u2, e);
+                        }
+                    }
+                }
+            }
+            s[3 * which] = sum_of(u0), s[3 * which + 1] = sum_of(u1), s[3 * which + 2] = sum_of(u2);
+        }
+        row_sums<T, 6>(s, sums[turn]);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            if (row + which >= a.n) break;
+            const float delta = s[3 * which + 2] * a.inv_d;
+            const F2 along = both(-rstd[which] * fmaf(-delta, s[3 * which], s[3 * which + 1]) * a.inv_d);   // minus the sum of g xhat / D
+            const F2 base = both(-rstd[which] * s[3 * which] * a.inv_d);
+            const F2 shift = both(-mean[which]), rest = both(-delta), scale = both(rstd[which]);
+            TX* dx = static_cast<TX*>(a.y) + (row + which) * a.ld_y;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = (j * T + t) * 8;
+                if (c < a.D) {
+                    X::get(place_x(turn, which, j), x);
+                    Y::get(place_d(turn, which, j), d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 xhat = mul2(add2(add2(x[i], shift), rest), scale);
+                        dw[j][i] = fma2(d[i], xhat, dw[j][i]);
+                        db[j][i] = add2(db[j][i], d[i]);
+                        x[i] = fma2(mul2(xhat, scale), along, fma2(mul2(d[i], w[j][i]), scale, base));
+                    }
+                    X::put(dx + c, x);
+                }
+            }
+        }
+        ask(row + 2 * step, turn);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) mean[which] = mean_next[which], rstd[which] = rstd_next[which];
+    }
+    if (!a.part) return;
+    float v[16], u[16];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            split(dw[j][i], v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+            split(db[j][i], u[8 * j + 2 * i], u[8 * j + 2 * i + 1]);
+        }
+    if constexpr (R > 1) {   // the block's rows side by side, added in order in the ring's place
+        float* cols = reinterpret_cast<float*>(ring);   // [2][16][T]
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        for (int k = 0; k < R; ++k) {
+            if (r == k) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int at = e * T + t;
+                    if (k > 0) v[e] += cols[at], u[e] += cols[16 * T + at];
+                    cols[at] = v[e], cols[16 * T + at] = u[e];
+                }
+            }
+            __syncthreads();
+        }
+        if (r != R - 1) return;
+    }
+    float* pw = a.part + static_cast<int64_t>(blockIdx.x) * a.D;
+    float* pb = pw + static_cast<int64_t>(gridDim.x) * a.D;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int c = (j * T + t) * 8;
+        if (c < a.D) {
+            float v8[8], u8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v8[i] = v[8 * j + i], u8[i] = u[8 * j + i];
+            store_as<float, 8>(pw + c, v8);
+            store_as<float, 8>(pb + c, u8);
+        }
     }
 }
 
 constexpr int kFwdEpt = 16, kBwdEpt = 16;
 constexpr int kWidest = 16384;   // channels that a block of 1024 threads holds
 
-// Threads a row takes at 16 elements each: a warp, or a block of 128 to 1024.
-int row_threads(int64_t D) {
-    int t = 32;
-    while (static_cast<int64_t>(t) * 16 < D) t = t == 32 ? 128 : 2 * t;
+// Threads a row takes at 16 elements each: part of a warp (where its elements come eight at a time), a
+// warp, or a block of 64 to 1024.
+int row_threads(int64_t D, int V) {
+    int t = V == 8 ? 8 : 32;
+    while (static_cast<int64_t>(t) * 16 < D) t *= 2;
     return t;
 }
-
-constexpr int kWarpRows = 4;   // rows a block side by side, of a warp each
+constexpr int rows_beside(int T) { return T <= 32 ? 128 / T : 1; }   // rows of a block
 
 int bwd_parts(int64_t n, int64_t D) {
     if (D > kWidest) return 0;
-    const int R = row_threads(D) == 32 ? kWarpRows : 1;
-    return static_cast<int>(std::min<int64_t>(kPartMax, (n + R - 1) / R));
+    return static_cast<int>(std::min<int64_t>(kPartMax, n));   // as few rows a block as there may be
 }
 
 template <bool BWD, class TX, class TY, int T, int R, int V>
@@ -369,16 +673,59 @@ int launch_rows(const NormArgs& a, int grid, cudaStream_t s) {
 }
 
 template <bool BWD, class TX, class TY, int V>
-int pick_rows(const NormArgs& a, cudaStream_t s) {
-    const int T = row_threads(a.D);
-    const int R = T == 32 ? kWarpRows : 1;
-    const int grid = BWD ? bwd_parts(a.n, a.D) : (a.n + R - 1) / R;
+int pick_rows(const NormArgs& a, int* parts, cudaStream_t s) {
+    const int T = row_threads(a.D, BWD ? 1 : V), R = rows_beside(T);
+    int grid = static_cast<int>((static_cast<int64_t>(a.n) + R - 1) / R);
+    if (BWD) grid = std::min(grid, kPartMax / 2);
+    *parts = grid;
     switch (T) {
-    case 32: return launch_rows<BWD, TX, TY, 32, kWarpRows, V>(a, grid, s);
+    case 8:
+        if constexpr (!BWD && V == 8) return launch_rows<BWD, TX, TY, 8, rows_beside(8), V>(a, grid, s);
+    case 16:
+        if constexpr (!BWD && V == 8) return launch_rows<BWD, TX, TY, 16, rows_beside(16), V>(a, grid, s);
+    case 32: return launch_rows<BWD, TX, TY, 32, rows_beside(32), V>(a, grid, s);
+    case 64: return launch_rows<BWD, TX, TY, 64, 1, V>(a, grid, s);
     case 128: return launch_rows<BWD, TX, TY, 128, 1, V>(a, grid, s);
     case 256: return launch_rows<BWD, TX, TY, 256, 1, V>(a, grid, s);
     case 512: return launch_rows<BWD, TX, TY, 512, 1, V>(a, grid, s);
     default: return launch_rows<BWD, TX, TY, 1024, 1, V>(a, grid, s);
+    }
+}
+
+template <bool BWD, class TX, class TY, int T, int R>
+int launch_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
+    constexpr size_t smem = 8u * T * R * 16 * (Eight<TX, 1>::WORDS + (BWD ? Eight<TY, 1>::WORDS : 0));
+    if constexpr (smem > kPairSpace) {
+        return pick_rows<BWD, TX, TY, 8>(a, parts, s);
+    } else {
+    const int64_t pairs = (static_cast<int64_t>(a.n) + 2 * R - 1) / (2 * R);
+    const int blocks = std::min(pair_blocks(T, BWD), static_cast<int>(kPairSpace / smem));
+    const int grid = static_cast<int>(std::min({pairs, static_cast<int64_t>(num_sms) * blocks, static_cast<int64_t>(kPartMax)}));
+    *parts = grid;
+    auto kernel = [] {
+        if constexpr (BWD) return norm_bwd_pairs<TX, TY, T, R>;
+        else return norm_fwd_pairs<TX, TY, T, R>;
+    }();
+    if (smem > 40 * 1024) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    return launch_pdl(kernel, dim3(grid), dim3(T * R), smem, s, a);
+    }
+}
+
+template <bool BWD, class TX, class TY>
+int pick_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
+    if constexpr (BWD) {
+        switch (row_threads(a.D, 8)) {
+        case 8: return launch_pairs<BWD, TX, TY, 8, rows_beside(8)>(a, num_sms, parts, s);
+        case 16: return launch_pairs<BWD, TX, TY, 16, rows_beside(16)>(a, num_sms, parts, s);
+        case 32: return launch_pairs<BWD, TX, TY, 32, rows_beside(32)>(a, num_sms, parts, s);
+        case 64: return launch_pairs<BWD, TX, TY, 64, 1>(a, num_sms, parts, s);
+        case 128: return launch_pairs<BWD, TX, TY, 128, 1>(a, num_sms, parts, s);
+        default: break;
+        }
+    }
+    switch (row_threads(a.D, 8)) {
+    case 256: return launch_pairs<BWD, TX, TY, 256, 1>(a, num_sms, parts, s);
+    default: return launch_pairs<BWD, TX, TY, 512, 1>(a, num_sms, parts, s);
     }
 }
 
@@ -390,7 +737,7 @@ bool all_allow(const NormArgs& a, bool bwd, int V, int ex, int ey) {
 }
 
 template <bool BWD, class TX, class TY>
-int run_norm(const NormArgs& a, float* dweight, float* dbias, cudaStream_t s) {
+int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaStream_t s) {
     if (a.D > kWidest) {
         if constexpr (BWD) {
             if (a.n > 0)
@@ -401,26 +748,31 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, cudaStream_t s) {
             return launch_pdl(norm_fwd_wide<TX, TY>, dim3(a.n), dim3(1024), 0, s, a);
         }
     }
+    int parts = 0;
     if (a.n > 0) {
         constexpr int ex = kElem<TX>, ey = kElem<TY>;
         int st;
-        if (all_allow(a, BWD, 8, ex, ey)) st = pick_rows<BWD, TX, TY, 8>(a, s);
-        else if (all_allow(a, BWD, 2, ex, ey)) st = pick_rows<BWD, TX, TY, 2>(a, s);
-        else st = pick_rows<BWD, TX, TY, 1>(a, s);
+        // Pairs of rows: the gradient from a pair for each SM on (32768 x 4096 bf16 137 us, row by row 311;
+        // 64 x 4096 6.8, 5.7), the forward of wide bf16 rows (32768 x 4096 99 us, 135; 16384 x 1024 28, 22;
+        // in fp32 227, 187).
+        const bool pairs = a.D <= kPairWidest && (BWD ? a.n > 2 * num_sms * rows_beside(row_threads(a.D, 8)) : ex == 2 && a.D > 2048 && a.n > 2 * num_sms);
+        if (all_allow(a, BWD, 8, ex, ey)) {
+            st = pairs ? pick_pairs<BWD, TX, TY>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 8>(a, &parts, s);
+        } else if (all_allow(a, BWD, 2, ex, ey)) st = pick_rows<BWD, TX, TY, 2>(a, &parts, s);
+        else st = pick_rows<BWD, TX, TY, 1>(a, &parts, s);
         if (st) return st;
     }
     if (BWD && (dweight || dbias))   // of no rows: zeros
-        return launch_pdl(norm_cols, dim3((a.D + 31) / 32, 2), dim3(512), 0, s, static_cast<const float*>(a.part), bwd_parts(a.n, a.D), a.D,
-                          dweight, dbias);
+        return launch_pdl(norm_cols, dim3((a.D + 31) / 32, 2), dim3(1024), 0, s, static_cast<const float*>(a.part), parts, a.D, dweight, dbias);
     return TERN_OK;
 }
 
 template <bool BWD>
-int run_types(const NormArgs& a, int tx, int ty, float* dweight, float* dbias, cudaStream_t s) {
+int run_types(const NormArgs& a, int tx, int ty, float* dweight, float* dbias, int num_sms, cudaStream_t s) {
     using B = __nv_bfloat16;
     if (tx == TERN_BF16)
-        return ty == TERN_BF16 ? run_norm<BWD, B, B>(a, dweight, dbias, s) : run_norm<BWD, B, float>(a, dweight, dbias, s);
-    return ty == TERN_BF16 ? run_norm<BWD, float, B>(a, dweight, dbias, s) : run_norm<BWD, float, float>(a, dweight, dbias, s);
+        return ty == TERN_BF16 ? run_norm<BWD, B, B>(a, dweight, dbias, num_sms, s) : run_norm<BWD, B, float>(a, dweight, dbias, num_sms, s);
+    return ty == TERN_BF16 ? run_norm<BWD, float, B>(a, dweight, dbias, num_sms, s) : run_norm<BWD, float, float>(a, dweight, dbias, num_sms, s);
 }
 
 bool sizes_ok(int64_t n, int64_t D) { return n >= 0 && D >= 0 && n < (1ll << 31) - 2048 && D <= (1ll << 22); }
@@ -443,12 +795,13 @@ extern "C" int tern_norm_fwd(const void* x, int x_dtype, int64_t ld_x, const flo
     if (!aligned_to(x, elem(x_dtype)) || !aligned_to(y, elem(y_dtype)) || !aligned_to(weight, 4) || !aligned_to(bias, 4) ||
         !aligned_to(mean, 4) || !aligned_to(rstd, 4))
         return TERN_ERR_ALIGN;
-    if (int st = check_device(nullptr)) return st;
+    int num_sms = 0;
+    if (int st = check_device(&num_sms)) return st;
     NormArgs a{};
     a.x = x, a.y = y, a.weight = weight, a.bias = bias, a.mean = mean, a.rstd = rstd;
     a.ld_x = ld_x, a.ld_y = ld_y, a.n = static_cast<int>(n), a.D = static_cast<int>(D), a.eps = eps;
     a.inv_d = static_cast<float>(1.0 / static_cast<double>(D));
-    return run_types<false>(a, x_dtype, y_dtype, nullptr, nullptr, static_cast<cudaStream_t>(stream));
+    return run_types<false>(a, x_dtype, y_dtype, nullptr, nullptr, num_sms, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t tern_norm_bwd_workspace(int64_t n, int64_t D) {
@@ -470,11 +823,12 @@ extern "C" int tern_norm_bwd(const void* x, int x_dtype, int64_t ld_x, const flo
     if (!aligned_to(x, elem(x_dtype)) || !aligned_to(dx, elem(x_dtype)) || !aligned_to(dy, elem(y_dtype)) || !aligned_to(weight, 4) ||
         !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4) || (sums && !aligned16(workspace)))
         return TERN_ERR_ALIGN;
-    if (int st = check_device(nullptr)) return st;
+    int num_sms = 0;
+    if (int st = check_device(&num_sms)) return st;
     NormArgs a{};
     a.x = x, a.dy = dy, a.y = dx, a.weight = weight, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
     a.part = sums ? static_cast<float*>(workspace) : nullptr;
     a.ld_x = ld_x, a.ld_dy = ld_dy, a.ld_y = ld_dx, a.n = static_cast<int>(n), a.D = static_cast<int>(D);
     a.inv_d = static_cast<float>(1.0 / static_cast<double>(D));
-    return run_types<true>(a, x_dtype, y_dtype, dweight, dbias, static_cast<cudaStream_t>(stream));
+    return run_types<true>(a, x_dtype, y_dtype, dweight, dbias, num_sms, static_cast<cudaStream_t>(stream));
 }

@@ -89,15 +89,15 @@ __device__ __forceinline__ void store_as(T* p, const float (&v)[V]) {
     store_raw<T, V>(p, r);
 }
 
-// Sums of N values over the threads that share a row: a warp (T == 32), or the whole block of T
-// threads through `s` (N * T / 32 floats; the caller keeps it from being reused too early by
+// Sums of N values over the threads that share a row: T neighbours of a warp (T <= 32, all of the warp
+// calling), or the whole block of T threads through `s` (N * T / 32 floats; the caller keeps it from being reused too early by
 // alternating two of them).  Every thread gets the sums; the order is fixed.
 template <int T, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* s) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+        for (int d = T < 32 ? T / 2 : 16; d >= 1; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
     if constexpr (T > 32) {
         constexpr int W = T / 32;
         if ((threadIdx.x & 31) == 0) {

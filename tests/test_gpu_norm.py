@@ -52,6 +52,25 @@ def _inputs(n, D, tx, ty, seed, shift=0.0):
     return (r(n, D) * (0.2 + 3 * torch.rand(n, 1, device="cuda", generator=g)) + shift).to(tx), 1 + 0.3 * r(D), 0.5 * r(D), (0.1 * r(n, D)).to(ty)
 
 
+# Enough rows for the kernels that take pairs of them, odd counts and uneven ends among them; sums over up to
+# 14 rows a block in turn, 16 side by side, then 19 and 32: under 128 too
+@pytest.mark.parametrize("n,D", [(9999, 8), (6001, 64), (5001, 128), (5003, 136), (2600, 256), (2501, 264), (1303, 512), (700, 520), (2611, 600), (2600, 1024), (611, 1032), (402, 2048), (705, 2056),
+                                 (403, 4096), (350, 4104), (309, 8192), (320, 8200)])
+@pytest.mark.parametrize("tx,ty", TYPES, ids=IDS)
+def test_many_rows(cuda_lib, n, D, tx, ty):
+    x, w, b, dy = _inputs(n, D, tx, ty, n + D)
+    got, refs = _run(cuda_lib, x, w, b, dy), _ref(x, w, b, 1e-5, dy)
+    for g, ref, name in zip(got, refs, NAMES):
+        _near(g, ref, name)
+    assert all(torch.equal(p, q) for p, q in zip(got, _run(cuda_lib, x, w, b, dy)))
+    # strided, with NaN between the rows; nothing else written
+    wide = torch.full((n, D + 8), float("nan"), dtype=tx, device="cuda")
+    wide[:, :D] = x
+    dx = torch.full((n, D + 8), 5.0, dtype=tx, device="cuda")
+    again = _run(cuda_lib, wide[:, :D], w, b, dy, dx=dx[:, :D])
+    assert all(torch.equal(p, q) for p, q in zip(got, again)) and torch.all(dx[:, D:] == 5.0)
+
+
 def _run(bl, x, w, b, dy, eps=1e-5, y=None, dx=None):
     n, D = x.shape
     f32 = lambda *s: torch.full(s, float("nan"), device="cuda")  # noqa: E731
