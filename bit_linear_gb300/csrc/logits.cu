@@ -66,16 +66,20 @@ struct Stats {
     }
 };
 
+template <class T, int V>
+__device__ __forceinline__ void raw_pairs(const Raw<T, V>& r, F2* x) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) x[i] = pair(raw_at<T, V>(r, 2 * i), raw_at<T, V>(r, 2 * i + 1));
+}
+
 // A thread's running softmax over batches of pairs.
 template <bool ENT>
 struct Run {
     float m = kNegInf;
     F2 s = both(0.f), q = both(0.f);
 
-    // `top`: the largest of the batch (NaN dropped); `masked`: there may be -inf among it, which would
-    // give 0 times infinity in the entropy's sum.
-    template <int N2>
-    __device__ __forceinline__ void add(const F2 (&x)[N2], float top, bool masked, float c) {
+    // To the largest of a batch (NaN dropped); false while there is nothing but -inf (and NaN).
+    __device__ __forceinline__ bool raise(float top, float c) {
         if (top > m) {
             if (m != kNegInf) {
                 const float d = m - top, f = pow2(d * c);
@@ -84,27 +88,57 @@ struct Run {
             }
             m = top;
         }
-        if (m == kNegInf) {   // nothing but -inf, and NaN
+        return m != kNegInf;
+    }
+    // `masked`: there may be -inf among the batch, which would give 0 times infinity in the entropy's sum.
+    template <int N2>
+    __device__ __forceinline__ void add(const F2 (&x)[N2], float top, bool masked, float c) {
+        if (raise(top, c)) {
+            const F2 shift = both(-m), scale = both(c);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) one(add2(x[i], shift), masked, scale);
+        } else {
             F2 t = x[0];
 #pragma unroll
             for (int i = 1; i < N2; ++i) t = add2(t, x[i]);
-            float lo, hi;
-            split(t, lo, hi);
-            if (lo + hi != lo + hi) s = both(lo + hi);
-            return;
+            nan_of(t);
         }
-        const F2 shift = both(-m), scale = both(c);
-        if (ENT && masked) {
+    }
+    // The same of U words as they are in memory.
+    template <class T, int V, int U>
+    __device__ __forceinline__ void add_words(const Raw<T, V> (&raw)[U], float top, bool masked, float c) {
+        F2 x[V / 2];
+        if (raise(top, c)) {
+            const F2 shift = both(-m), scale = both(c);
 #pragma unroll
-            for (int i = 0; i < N2; ++i) {
-                float z0, z1;
-                split(add2(x[i], shift), z0, z1);
-                sum(pair(max_nan(z0, -1e4f), max_nan(z1, -1e4f)), scale);
+            for (int u = 0; u < U; ++u) {
+                raw_pairs<T, V>(raw[u], x);
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) one(add2(x[i], shift), masked, scale);
             }
         } else {
+            F2 t = both(0.f);
 #pragma unroll
-            for (int i = 0; i < N2; ++i) sum(add2(x[i], shift), scale);
+            for (int u = 0; u < U; ++u) {
+                raw_pairs<T, V>(raw[u], x);
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) t = add2(t, x[i]);
+            }
+            nan_of(t);
         }
+    }
+    __device__ __forceinline__ void nan_of(F2 t) {
+        float lo, hi;
+        split(t, lo, hi);
+        if (lo + hi != lo + hi) s = both(lo + hi);
+    }
+    __device__ __forceinline__ void one(F2 z, bool masked, F2 scale) {
+        if (ENT && masked) {
+            float z0, z1;
+            split(z, z0, z1);
+            z = pair(max_nan(z0, -1e4f), max_nan(z1, -1e4f));
+        }
+        sum(z, scale);
     }
     __device__ __forceinline__ void sum(F2 z, F2 scale) {
         float t0, t1;
@@ -147,12 +181,6 @@ struct Row {
     __device__ __forceinline__ float at(int e) const { return raw_at<T, 1>(load_raw<T, 1>(p + e), 0); }
 };
 
-template <class T, int V>
-__device__ __forceinline__ void raw_pairs(const Raw<T, V>& r, F2* x) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) x[i] = pair(raw_at<T, V>(r, 2 * i), raw_at<T, V>(r, 2 * i + 1));
-}
-
 // The largest and the smallest of U words' entries (NaN dropped).
 template <class T, int V, int U>
 __device__ __forceinline__ float raw_max(const Raw<T, V> (&r)[U]) {
@@ -189,13 +217,15 @@ __device__ __forceinline__ void slice(int nb, int rank, int size, int& first, in
 
 // One pass of a block of T threads over its words of a row (and, in block 0, the edges): thread t
 // takes the words first + t, first + t + T, ...  With `tops`, each thread leaves the largest entry of
-// each segment, `seg` of its words in turn (one, or a multiple of kBatch; NaN dropped), at
+// each segment, `seg` of its words in turn (one, or a power of two from kBatch on; NaN dropped), at
 // tops[segment T + t].
 constexpr int kBatch = 4;      // words a thread asks for at once
 constexpr int kSegments = 8;
 __device__ __forceinline__ int segment_words(int words, int T) {
     const int each = (words + T - 1) / T;
-    return each <= kSegments ? 1 : ((each + kSegments - 1) / kSegments + kBatch - 1) / kBatch * kBatch;
+    int seg = 1;
+    while (seg * kSegments < each) seg = seg < kBatch ? kBatch : 2 * seg;
+    return seg;
 }
 
 template <class TX, int T, bool ENT>
@@ -206,15 +236,19 @@ __device__ __forceinline__ Stats<ENT> read_row(const Row<TX>& r, int first, int 
     float most = kNegInf;   // of the segment
     int left = seg;
     float* to = tops + threadIdx.x;
+    Raw<TX, VE> raw[U], next[U];   // the next batch is on its way while one is summed
+    const auto ask = [&](Raw<TX, VE>(&to)[U], int at) {
+        if (at + (U - 1) * T < last) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) to[u] = load_raw<TX, VE>(r.word(at + u * T));
+        }
+    };
+    ask(raw, i);
     for (; i + (U - 1) * T < last; i += U * T) {
-        Raw<TX, VE> raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = load_raw<TX, VE>(r.word(i + u * T));
-        F2 x[U * VE / 2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) raw_pairs<TX, VE>(raw[u], x + u * (VE / 2));
+        ask(next, i + U * T);
         const float top = raw_max(raw);
-        run.add(x, top, ENT && raw_masked(raw), c);
+        if (ENT && !raw_masked(raw)) run.add_words(raw, top, false, c);
+        else run.add_words(raw, top, true, c);
         if (ENT && tops && seg == 1) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -226,13 +260,13 @@ __device__ __forceinline__ Stats<ENT> read_row(const Row<TX>& r, int first, int 
             most = fmaxf(most, top);
             if ((left -= U) == 0) *to = most, to += T, most = kNegInf, left = seg;
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = next[u];
     }
     for (; i < last; i += T) {
         const Raw<TX, VE> raw[1] = {load_raw<TX, VE>(r.word(i))};
-        F2 x[VE / 2];
-        raw_pairs<TX, VE>(raw[0], x);
         const float top = raw_max(raw);
-        run.add(x, top, true, c);
+        run.add_words(raw, top, true, c);
         if (ENT && tops) {
             most = fmaxf(most, top);
             if (--left == 0) *to = most, to += T, most = kNegInf, left = seg;
@@ -305,7 +339,7 @@ __device__ __forceinline__ void cluster_place(uint32_t& rank, uint32_t& size) {
 // in few threads' words) the exact k-th value is found, by bisection if it must be, and entries equal
 // to it are taken in the order of the row.
 template <int T>
-constexpr int kCand = T == 32 ? 256 : 1024;
+constexpr int kCand = T == 32 ? 512 : 1024;
 
 __device__ __forceinline__ uint32_t order_key(float x) {   // larger for larger x; NaN above all, -0 as 0; never 0
     if (x != x) return 0xFFFFFFFFu;
@@ -348,7 +382,7 @@ struct TopSpace {
 template <class TX, int T>
 __device__ __forceinline__ void collect(const Row<TX>& r, int first, int last, bool edges, bool every, uint32_t lo, TopSpace<T>& sp) {
     constexpr int VE = Row<TX>::VE, U = kBatch;
-    const int t = threadIdx.x, seg = segment_words(last - first, T);
+    const int t = threadIdx.x, seg = 1 << (31 - __clz(segment_words(last - first, T)));   // a power of two, said so
     __syncthreads();
     if (t == 0) sp.count = sp.listed = 0;
     __syncthreads();
@@ -356,6 +390,7 @@ __device__ __forceinline__ void collect(const Row<TX>& r, int first, int last, b
     for (int g = 0; first + t + g * seg * T < last; ++g)
         if (every || !(sp.tops[g * T + t] < bound)) sp.list[atomicAdd(&sp.listed, 1)] = static_cast<uint16_t>(g * T + t);
     auto offer = [&](float x, int e) {
+        if (!every && x < bound) return;
         const uint32_t key = order_key(x);
         if (key >= lo) {
             const int at = atomicAdd(&sp.count, 1);
@@ -372,8 +407,8 @@ __device__ __forceinline__ void collect(const Row<TX>& r, int first, int last, b
             const int w = w0 + u * T;
             at[u] = last;
             if (w < listed * seg) {
-                const int q = w / listed, item = sp.list[w - q * listed];
-                at[u] = first + item % T + (item / T * seg + q) * T;
+                const int item = sp.list[w / seg];
+                at[u] = first + item % T + (item / T * seg + w % seg) * T;
             }
             if (at[u] < last) raw[u] = load_raw<TX, VE>(r.word(at[u]));
         }
@@ -417,34 +452,48 @@ __device__ __forceinline__ int count_from(const Row<TX>& r, int first, int last,
 }
 
 // The k largest entries of the slice into sp.best, largest first, zeros where there are fewer.
-// `mine`: the largest key among the thread's entries, 0 without any; `every`: there is NaN.
+// `mine`: the largest key among the thread's entries, 0 without any; `most_key`: one that none is above;
+// `every`: there is NaN.
 template <class TX, int T>
-__device__ __forceinline__ void block_top(const Row<TX>& r, int first, int last, bool edges, bool every, uint32_t mine, int k, TopSpace<T>& sp) {
+__device__ __forceinline__ void block_top(const Row<TX>& r, int first, int last, bool edges, bool every, uint32_t mine, uint32_t most_key, int k, TopSpace<T>& sp) {
     constexpr int VE = Row<TX>::VE;
     uint32_t lo = 0;   // the upper 16 bits of the bound: all that bf16 has
     if constexpr (T == 32) {   // of the segments' maxima
-        const int seg = segment_words(last - first, T);
-        uint32_t top[kSegments];
+        const int seg = segment_words(last - first, T), segs = every ? 1 : (last - first + seg * T - 1) / (seg * T);
+        uint32_t top[kSegments], most = mine;
 #pragma unroll
         for (int g = 0; g < kSegments; ++g)
             top[g] = !every && first + static_cast<int>(threadIdx.x) + g * seg * T < last ? order_key(sp.tops[g * T + threadIdx.x]) : 0u;
         if (every) top[0] = mine;
+        if (k <= 8) {   // the lanes' largest in turn; several at once where equal: the bound is lower, and still one
+            for (int c = 0; c < k; ++c) {
+                lo = __reduce_max_sync(0xffffffffu, most);
+                if (most == lo) most = 0;
+            }
+        } else {
+            most = __reduce_max_sync(0xffffffffu, most);
 #pragma unroll 1
-        for (int b = 31; b >= 16; --b) {
-            int reach = 0;
+            for (int b = 31; b >= 16; --b) {
+                const uint32_t c = lo | (1u << b);
+                if (c > most) continue;
+                int reach = 0;
 #pragma unroll
-            for (int g = 0; g < kSegments; ++g) reach += __popc(__ballot_sync(0xffffffffu, top[g] >= (lo | (1u << b))));
-            if (reach >= k) {
-                lo |= 1u << b;
-                if (reach <= k + k / 4 + 2) break;   // near enough
+                for (int g = 0; g < kSegments; ++g)
+                    if (g < segs) reach += __popc(__ballot_sync(0xffffffffu, top[g] >= c));
+                if (reach >= k) {
+                    lo = c;
+                    if (reach <= k + k / 4 + 2) break;   // near enough
+                }
             }
         }
     } else {
 #pragma unroll 1
         for (int b = 31; b >= 16; --b) {
-            const int reach = __syncthreads_count(mine >= (lo | (1u << b)));
+            const uint32_t c = lo | (1u << b);
+            if (c > most_key) continue;
+            const int reach = __syncthreads_count(mine >= c);
             if (reach >= k) {
-                lo |= 1u << b;
+                lo = c;
                 if (reach <= k + k / 4 + 2) break;
             }
         }
@@ -520,6 +569,35 @@ __device__ __forceinline__ void block_top(const Row<TX>& r, int first, int last,
             }
         n += min(found, want);
         __syncthreads();
+        }
+    }
+    if constexpr (T == 32) {
+        // Rows of few segments have a poor bound: the candidates are thinned out before they are compared
+        // with one another (32768 x 700 with 64 alternatives: 301 us without)
+        if (n > k + 32) {
+            uint32_t v = 0;
+#pragma unroll 1
+            for (int b = 31; b >= 8; --b) {
+                const uint32_t at = v | (1u << b);
+                int reach = 0;
+                for (int c = threadIdx.x; c < n; c += 32) reach += static_cast<uint32_t>(sp.cand[c] >> 32) >= at;
+                reach = __reduce_add_sync(0xffffffffu, reach);
+                if (reach >= k) {
+                    v = at;
+                    if (reach <= k + 8) break;
+                }
+            }
+            int kept = 0;
+            for (int c0 = 0; c0 < n; c0 += 32) {
+                const int c = c0 + static_cast<int>(threadIdx.x);
+                const unsigned long long key = c < n ? sp.cand[c] : 0ull;
+                const bool keep = c < n && static_cast<uint32_t>(key >> 32) >= v;
+                const uint32_t all = __ballot_sync(0xffffffffu, keep);   // every lane has read its candidate
+                if (keep) sp.cand[kept + __popc(all & ((1u << threadIdx.x) - 1))] = key;
+                kept += __popc(all);
+                __syncwarp();
+            }
+            n = kept;
         }
     }
     for (int c = threadIdx.x; c < k; c += T)
@@ -600,9 +678,11 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) score_row
             }
             if (edges && static_cast<int>(threadIdx.x) < r.edges()) mine = max(mine, order_key(r.at(r.edge(threadIdx.x))));
         }
-        block_top<TX, T>(r, first, last, edges, every, mine, k, sp);
+        join_block<T, true>(st, s, kLog2e);
+        block_top<TX, T>(r, first, last, edges, every, mine, every ? 0xFFFFFFFFu : order_key(st.m), k, sp);
+    } else {
+        join_block<T, true>(st, s, kLog2e);
     }
-    join_block<T, true>(st, s, kLog2e);
     if (size == 1) {
         const RowLog l(st);
         if (writes) write_row(a, row, tok, xtok, st, l);
@@ -825,6 +905,7 @@ __device__ __forceinline__ bool teacher(const DistillArgs& a, int64_t row, int* 
         any |= in;
         if (in) m = fmaxf(m, t);   // drops NaN, which the sum brings back
     }
+    if (lane < 3 && a.k + lane < (a.k + 3) / 4 * 4) ids[a.k + lane] = -1;
     any = __any_sync(0xffffffffu, any) && w != 0.f;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -860,62 +941,124 @@ __device__ __forceinline__ float row_loss(const DistillArgs& a, const int* ids, 
 struct Gradient {
     float c, shift, base, coef;
     __device__ __forceinline__ float operator()(float x) const { return coef * pow2(fmaf(x - shift, c, -base)); }
+    __device__ __forceinline__ void operator()(F2 x, float& a, float& b) const {
+        float t0, t1;
+        split(fma2(add2(x, both(-shift)), both(c), both(-base)), t0, t1);
+        split(mul2(pair(pow2(t0), pow2(t1)), both(coef)), a, b);
+    }
 };
 
-// Where the teacher has probability: w T (q - p), by the first entry of each id.
+// Where the teacher has probability: w T (q - p), by the first entry of each id.  ids is 16-byte aligned
+// and goes on to a multiple of four with -1.
 template <class TX>
 __device__ __forceinline__ void teacher_gradient(const DistillArgs& a, const int* ids, const float* p, int c, float x, const Gradient& g, float wt, TX* d) {
+    const int id = ids[c];
     float sum = p[c];
-    for (int o = 0; o < a.k; ++o) {
-        if (ids[o] == ids[c] && o != c) {
-            if (o < c) return;
-            sum += p[o];
+    for (int o = 0; o < a.k; o += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(ids + o);
+        if (v.x == id || v.y == id || v.z == id || v.w == id) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (ids[o + i] == id && o + i != c) {
+                    if (o + i < c) return;
+                    sum += p[o + i];
+                }
+            }
         }
     }
     const float v[1] = {g(x) - wt * sum};
-    store_as<TX, 1>(d + ids[c], v);
+    store_as<TX, 1>(d + id, v);
 }
 
-// A row a cluster of blocks.  The gradient reads the row again, from L2 as far as it holds the rows in work.  VEC: the gradient's rows start at the same place of a 16-byte word as the
-// logits' do.
+// A row a cluster of blocks.  The gradient reads the row again, from L2 as far as it holds the rows in
+// work.  The teacher's entries belong to the threads, E each; they are asked for before the row and their
+// logits after it, so that only the block's exchange waits for them.  VEC: the gradient's rows start at
+// the same place of a 16-byte word as the logits' do.
 template <class TX, int T, bool VEC>
-__global__ void __launch_bounds__(T, T == 256 ? 6 : T == 128 ? 12 : 32) distill_rows(const __grid_constant__ DistillArgs a) {
-    constexpr int VE = Row<TX>::VE, U = kBatch;
-    __shared__ float s[3 * (T / 32)];
+__global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) distill_rows(const __grid_constant__ DistillArgs a) {
+    constexpr int VE = Row<TX>::VE, U = kBatch, W = T / 32, E = (kMaxTeacher + T - 1) / T;
+    __shared__ float s[3 * W], parts[W];
+    __shared__ float2 teach[W];   // the warps' largest entry and sum relative to it
     __shared__ float4 all[kMaxBlocks];
-    __shared__ int ids[kMaxTeacher];
-    __shared__ float p[kMaxTeacher], xs[kMaxTeacher];
-    __shared__ int alive;
+    __shared__ __align__(16) int ids[kMaxTeacher];
+    __shared__ float p[kMaxTeacher];
     uint32_t rank = 0, size = 1;
     if constexpr (T > 32) cluster_place(rank, size);
     if (size > 1) cluster_arrive();
     ptx::pdl_trigger();
     ptx::pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x / size;
     const Row<TX> r(a.logits, row, a.ld, a.V);
     int first, last;
     slice(r.nb, rank, size, first, last);
     const bool edges = rank == 0;
     const float w = a.weight ? __ldg(a.weight + row) : 1.f;
-    auto own = [&](int e) { return e < r.head || e >= r.tail0 ? edges : e >= r.head + first * VE && e < r.head + last * VE; };
-    if (T == 32 || threadIdx.x >= T - 32) {   // the last warp, while the others read
-        const bool any = teacher(a, row, ids, p, w);
-        if (threadIdx.x == T - 1) alive = any;
-        // all of them for the loss; for the gradient this block's own
-        at_teacher(a, r, ids, xs, threadIdx.x & 31, 32, [&](int e) { return (edges && !a.lse_in) || own(e); });
+    int id[E];
+    float t[E], x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = e * T + threadIdx.x;
+        id[e] = -1, t[e] = kNegInf, x[e] = 0.f;
+        if (c < a.k) {
+            const int64_t at = row * a.k + c;
+            const int64_t of = a.wide_ids ? __ldg(static_cast<const long long*>(a.ids) + at) : __ldg(static_cast<const int32_t*>(a.ids) + at);
+            t[e] = a.top ? __ldg(a.top + at) * a.inv_t : 0.f;
+            if (of >= 0 && of < a.V && t[e] != kNegInf) id[e] = static_cast<int>(of);
+        }
     }
+    auto own = [&](int e) { return e < r.head || e >= r.tail0 ? edges : e >= r.head + first * VE && e < r.head + last * VE; };
     Gradient g{a.inv_t * kLog2e, 0.f, 0.f, 0.f};
-    bool live;
+    Stats<false> st;
+    if (!a.lse_in) st = read_row<TX, T, false>(r, first, last, edges, g.c);
+    // The entries' logits, before any of the gradient is written, which may lie in their place: all of them
+    // for the loss, this block's own for the gradient (of which alone it can be sure in a gradient alone)
+    float tm = kNegInf, ts = 0.f;
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e * T < a.k) {
+            if (id[e] >= 0) {
+                if (!a.lse_in || own(id[e])) x[e] = r.at(id[e]);
+                tm = fmaxf(tm, t[e]);   // drops NaN, which the sum brings back
+                any = true;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, d));
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (e * T < a.k && id[e] >= 0) ts += pow2((t[e] - tm) * kLog2e);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) ts += __shfl_xor_sync(0xffffffffu, ts, d);
+    if (!a.lse_in) st.join_warp(g.c);
+    if (lane == 0) {
+        s[3 * warp] = st.m, s[3 * warp + 1] = st.s, s[3 * warp + 2] = 0.f;
+        teach[warp] = make_float2(tm, ts);
+    }
+    const bool live = __syncthreads_or(any) && w != 0.f;   // the same in every block of the cluster
+    {
+        const float2 mine = lane < W ? teach[lane] : make_float2(kNegInf, 0.f);
+        float m = mine.x;
+#pragma unroll
+        for (int d = W / 2; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        tm = __shfl_sync(0xffffffffu, m, 0);
+        ts = mine.x == kNegInf ? mine.y : mine.y * pow2((mine.x - tm) * kLog2e);   // without an entry 0, or NaN
+#pragma unroll
+        for (int d = W / 2; d >= 1; d >>= 1) ts += __shfl_xor_sync(0xffffffffu, ts, d);
+        ts = __shfl_sync(0xffffffffu, ts, 0);
+    }
     if (a.lse_in) {
         g.base = __ldg(a.lse_in + row) * kLog2e;
         g.coef = w * a.T;
-        __syncthreads();
-        live = alive;
         if (size > 1) cluster_wait();   // the arrival at the start
     } else {
-        Stats<false> st = read_row<TX, T, false>(r, first, last, edges, g.c);
-        join_block<T, false>(st, s, g.c);
-        live = alive;
+        if constexpr (W > 1) {
+            const bool in = lane < W;
+            st.m = in ? s[3 * lane] : kNegInf, st.s = in ? s[3 * lane + 1] : 0.f;
+            st.join_warp(g.c);
+        }
         if (size > 1) {
             cluster_wait();   // every block has started
             push_stats(st, all, rank, size);
@@ -923,57 +1066,93 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : T == 128 ? 12 : 32) distill_
             cluster_wait();
             join_cluster(st, all, size, g.c);
         }
-        const float log_s = logf(st.s);
-        if (edges && threadIdx.x < 32) {
-            const float loss = row_loss(a, ids, p, xs, w, st.m, log_s);
-            if (threadIdx.x == 0) {
-                a.loss[row] = live ? loss : 0.f;
-                if (a.lse_out) a.lse_out[row] = live ? fmaf(st.m, a.inv_t, log_s) : 0.f;
-            }
-        }
         g.shift = st.m;
         g.coef = w * a.T / st.s;
     }
-    if (!a.dlogits) return;
     TX* d = static_cast<TX*>(a.dlogits) + row * a.ld_d;
-    auto word = [&](const Raw<TX, VE>& x, int i) {
-        float v[VE];
+    if (a.dlogits) {
+        auto word = [&](const Raw<TX, VE>& x, int i) {
+            float v[VE];
+            if (live) {
+                F2 xx[VE / 2];
+                raw_pairs<TX, VE>(x, xx);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[e] = live ? g(raw_at<TX, VE>(x, e)) : 0.f;
-        TX* to = d + r.head + static_cast<int64_t>(i) * VE;
-        if constexpr (VEC) {
-            store_as<TX, VE>(to, v);
-        } else {
+                for (int e = 0; e < VE / 2; ++e) g(xx[e], v[2 * e], v[2 * e + 1]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float one[1] = {v[e]};
-                store_as<TX, 1>(to + e, one);
+                for (int e = 0; e < VE; ++e) v[e] = 0.f;
             }
+            TX* to = d + r.head + static_cast<int64_t>(i) * VE;
+            if constexpr (VEC) {
+                store_as<TX, VE>(to, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float one[1] = {v[e]};
+                    store_as<TX, 1>(to + e, one);
+                }
+            }
+        };
+        int i = first + static_cast<int>(threadIdx.x);
+        Raw<TX, VE> raw[U], next[U];
+        const auto ask = [&](Raw<TX, VE>(&to)[U], int at) {
+            if (at + (U - 1) * T < last) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) to[u] = load_raw<TX, VE>(r.word(at + u * T));
+            }
+        };
+        ask(raw, i);
+        for (; i + (U - 1) * T < last; i += U * T) {
+            ask(next, i + U * T);
+#pragma unroll
+            for (int u = 0; u < U; ++u) word(raw[u], i + u * T);
+#pragma unroll
+            for (int u = 0; u < U; ++u) raw[u] = next[u];
         }
-    };
-    int i = first + static_cast<int>(threadIdx.x);
-    for (; i + (U - 1) * T < last; i += U * T) {
-        Raw<TX, VE> raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = load_raw<TX, VE>(r.word(i + u * T));
-#pragma unroll
-        for (int u = 0; u < U; ++u) word(raw[u], i + u * T);
+        for (; i < last; i += T) word(load_raw<TX, VE>(r.word(i)), i);
+        if (edges && static_cast<int>(threadIdx.x) < r.edges()) {
+            const int e = r.edge(threadIdx.x);
+            const float v[1] = {live ? g(r.at(e)) : 0.f};
+            store_as<TX, 1>(d + e, v);
+        }
     }
-    for (; i < last; i += T) word(load_raw<TX, VE>(r.word(i)), i);
-    if (edges && static_cast<int>(threadIdx.x) < r.edges()) {
-        const int e = r.edge(threadIdx.x);
-        const float v[1] = {live ? g(r.at(e)) : 0.f};
-        store_as<TX, 1>(d + e, v);
+    // the teacher's share: its probabilities, the loss, and the gradient at its entries
+    const float log_s = logf(st.s);
+    float loss = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = e * T + threadIdx.x;
+        if (e * T < a.k && c < (a.k + 3) / 4 * 4) {
+            const float q = id[e] >= 0 ? pow2((t[e] - tm) * kLog2e) / ts : 0.f;
+            ids[c] = id[e], p[c] = q, t[e] = q;
+            if (id[e] >= 0 && q != 0.f) loss += q * (logf(q) - ((x[e] - st.m) * a.inv_t - log_s));
+        }
     }
-    __syncthreads();
-    if (live)
-        for (int c = threadIdx.x; c < a.k; c += T)
-            if (ids[c] >= 0 && own(ids[c])) teacher_gradient(a, ids, p, c, xs[c], g, w * a.T, d);
+    if (edges && !a.lse_in) {
+#pragma unroll
+        for (int d2 = 16; d2 >= 1; d2 >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, d2);
+        if (lane == 0) parts[warp] = loss;
+    }
+    __syncthreads();   // and the row is written
+    if (edges && !a.lse_in && threadIdx.x == 0) {
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < W; ++v) sum += parts[v];
+        a.loss[row] = live ? w * (a.T * a.T) * sum : 0.f;
+        if (a.lse_out) a.lse_out[row] = live ? fmaf(st.m, a.inv_t, log_s) : 0.f;
+    }
+    if (a.dlogits && live) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = e * T + threadIdx.x;
+            if (e * T < a.k && id[e] >= 0 && own(id[e])) teacher_gradient(a, ids, p, c, x[e], g, w * a.T, d);
+        }
+    }
 }
 
 template <class TX, int EPL, bool VEC>
 __global__ void __launch_bounds__(128) distill_warps(const __grid_constant__ DistillArgs a) {
-    __shared__ int ids4[4][kMaxTeacher];
+    __shared__ __align__(16) int ids4[4][kMaxTeacher];
     __shared__ float p4[4][kMaxTeacher], xs4[4][kMaxTeacher];
     ptx::pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1011,7 +1190,10 @@ __global__ void __launch_bounds__(128) distill_warps(const __grid_constant__ Dis
     if (!a.dlogits) return;
     __syncwarp();   // the entries' logits are read before the row is written, maybe in their place
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) x[j] = live ? g(x[j]) : 0.f;
+    for (int j = 0; j < EPL; j += 2) g(pair(x[j], x[j + 1]), x[j], x[j + 1]);
+    if (!live)
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) x[j] = 0.f;
     TX* d = static_cast<TX*>(a.dlogits) + row * a.ld_d;
     const WarpRow<TX, EPL, VEC> wd{d, a.V, lane};
     wd.store(x);
@@ -1028,9 +1210,15 @@ int elem(int t) { return t == TERN_BF16 ? 2 : 4; }
 bool ld_ok(int64_t ld, int64_t V) { return ld >= V && ld < (1ll << 40); }
 bool aligned_to(const void* p, int b) { return reinterpret_cast<uintptr_t>(p) % b == 0; }
 
-// Threads of a block: 256 for rows above 16 KB, below that a warp where rows are many (no barriers, and
-// many rows at once), else 128.
-int row_block(int64_t n, int64_t V, int es, int num_sms) { return V * es > 16384 ? 256 : n >= 16 * num_sms ? 32 : 128; }
+// Threads of a block.  Where rows are many, a warp up to 16 KB (no barriers, many rows at once) and 128 up to
+// 56 KB; distillation of bf16 rows with 32, 128 and 256 threads: 32768 x 700 58, 134, 238 us; 4096 x 8000 36,
+// 40, 52; 4096 x 12000 54, 48, 59; 4096 x 20000 86, 69, 77; 4096 x 40000 168, 159, 126.  Scores cross at the
+// same sizes.
+int row_block(int64_t n, int64_t V, int es, int num_sms) {
+    const int64_t bytes = V * es;
+    if (bytes <= 16384) return n >= 16 * num_sms ? 32 : 128;
+    return bytes <= 57344 && n >= 8 * num_sms ? 128 : 256;
+}
 
 // Blocks that share a row: twice as many until the rows fill the GPU twice, as long as each thread keeps a word.
 int row_blocks(int64_t n, int64_t V, int es, int T, int num_sms) {
@@ -1062,7 +1250,11 @@ template <class TX, bool VEC>
 int run_distill_rows(const DistillArgs& a, int num_sms, cudaStream_t s) {
     constexpr int es = kElem<TX>;
     const int T = row_block(a.n, a.V, es, num_sms);
-    const int c = row_blocks(a.n, a.V, es, T, num_sms);
+    int c = row_blocks(a.n, a.V, es, T, num_sms);
+    // Rows that L2 would not keep until the gradient reads them again, with four blocks of 256 threads an SM each
+    // on its own: two blocks a row (4096 x 100003 bf16: 368 to 331 us; four cost more than they save, 397; the
+    // loss alone 132, 163 and 220).
+    if (T == 256 && c == 1 && a.dlogits && !a.lse_in && 4 * num_sms * static_cast<int64_t>(a.V) * es > (80 << 20)) c = 2;
     if (T == 32) return launch_cluster(distill_rows<TX, 32, VEC>, a.n, T, 0, 1, true, s, a);
     if (T == 128) return launch_cluster(distill_rows<TX, 128, VEC>, a.n * c, T, 0, c, true, s, a);
     return launch_cluster(distill_rows<TX, 256, VEC>, a.n * c, T, 0, c, true, s, a);
