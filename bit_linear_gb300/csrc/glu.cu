@@ -409,7 +409,7 @@ using GluOneNarrow = GluCfg<1, 64, 6>;
 
 // ------------------------------------------------------------------------------ a few rows
 //
-// glu_codes: up to 16 rows from the 2-bit codes.  A code's two bits as the upper two bits of a bf16 are
+// glu_codes: 16 rows a block from the 2-bit codes.  A code's two bits as the upper two bits of a bf16 are
 // twice its value (00: 0, 01: 0x4000 = 2, 11: 0xC000 = -2), so an operand register of two weights
 // takes a shift and a mask.  The products run on mma.sync (m16n8k16), with the weights as the 16-row
 // operand and the tokens as the 8 columns: with so few rows the time is that of reading and
@@ -423,14 +423,14 @@ using GluOneNarrow = GluCfg<1, 64, 6>;
 // Sums are added in a fixed order: a warp's blocks of rows, the warps of a block, the blocks of a cluster.
 constexpr int kCodeOut = 128, kCodeWarps = 4;       // warps for each of the two
 constexpr int kCodePad = kCodeOut + 4;              // the pad keeps a warp's stores free of conflicts
-constexpr int kCodeRows = 16;                       // most rows of X
+constexpr int kCodeRows = 16;                       // rows of X that a block takes
 
 struct CodeArgs {
     const uint16_t* X;
     const uint32_t* packed;
     const float* scale;
     uint16_t* H;
-    int M, N, K, act;
+    int M, N, K, act, tiles;
 };
 
 __device__ __forceinline__ void mma_tokens(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -444,7 +444,7 @@ __device__ __forceinline__ void mma_tokens(float (&c)[4], uint32_t a0, uint32_t 
 __device__ __forceinline__ uint32_t halves(uint32_t w0, uint32_t w1, bool upper) { return __byte_perm(w0, w1, upper ? 0x7632 : 0x5410); }
 
 template <int MT, int AHEAD>   // tokens in eights; blocks of 16 weight rows that a warp asks for at once
-__global__ void __launch_bounds__(kCodeWarps * 64, 2) glu_codes(const __grid_constant__ CodeArgs a) {
+__global__ void __launch_bounds__(kCodeWarps * 64, 2) glu_codes(const __grid_constant__ CodeArgs args) {
     // [2][warps][8 MT][kCodePad] sums of the warps; then what the cluster's blocks push: [blocks][columns of one][2 M]
     extern __shared__ float part[];
     constexpr int SUMS = 8 * MT * kCodePad;
@@ -456,7 +456,12 @@ __global__ void __launch_bounds__(kCodeWarps * 64, 2) glu_codes(const __grid_con
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(size));
     if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     ptx::pdl_trigger();
-    const int n0 = static_cast<int>(blockIdx.x / size) * kCodeOut;
+    const int unit = static_cast<int>(blockIdx.x / size), group = unit / args.tiles;
+    CodeArgs a = args;   // of the block's rows
+    a.X += group * kCodeRows * static_cast<int64_t>(a.K);
+    a.H += group * kCodeRows * static_cast<int64_t>(a.N);
+    a.M = min(kCodeRows, a.M - group * kCodeRows);
+    const int n0 = (unit - group * a.tiles) * kCodeOut;
     const int words = a.N / 8;                       // of a weight row: 2N / 16
     const bool live = n0 + 16 * g < a.N;             // N % 16 == 0
     float acc[8][MT][4];
@@ -695,14 +700,28 @@ int code_room(int c, int* clusters) {
 
 // Clusters as large as leave every block resident at once and every warp a block of rows.
 template <int MT, int AHEAD>
-int glu_few(const CodeArgs& a, cudaStream_t s) {
-    const int tiles = (a.N + kCodeOut - 1) / kCodeOut, blocks = a.K / 16;
+int glu_few(CodeArgs a, cudaStream_t s) {
+    a.tiles = (a.N + kCodeOut - 1) / kCodeOut;
+    const int blocks = a.K / 16;
+    const int64_t units = static_cast<int64_t>(a.tiles) * ((a.M + kCodeRows - 1) / kCodeRows);
     int c = 1, room = 0;
     for (int k = 2; k <= kCodeMost && blocks > (k - 1) * kCodeWarps; ++k) {
         if (int st = code_room<MT, AHEAD>(k, &room)) return st;
-        if (tiles <= room) c = k;
+        if (units <= room) c = k;
     }
-    return launch_cluster(glu_codes<MT, AHEAD>, tiles * c, kCodeWarps * 64, code_smem<MT>(a.M, c), c, true, s, a);
+    return launch_cluster(glu_codes<MT, AHEAD>, static_cast<unsigned>(units * c), kCodeWarps * 64, code_smem<MT>(std::min(a.M, kCodeRows), c), c, true, s, a);
+}
+
+// Whether M rows (17 .. 128) go through the codes, from what both take in us: sixteen rows at a time
+// (4096 x 12288 weights: 8.6 each beside a launch) against the GEMM's longer set-up with its rounds of
+// tiles, 0.27 for each 64 of K, or the bytes of the bf16 plane.  40 x 3872 x 192: 6.5 us by the codes, 22.5
+// in the GEMM; 64 x 4096 x 6144: 25 us in the GEMM, 38 by the codes.
+bool few_by_codes(const GluArgs& a, int num_sms) {
+    const double groups = (a.M + kCodeRows - 1) / kCodeRows;
+    const int64_t wide = glu_rounds<GluOne>(a, num_sms), narrow = glu_rounds<GluOneNarrow>(a, num_sms);
+    const double rounds = std::min(static_cast<double>(wide), 0.55 * static_cast<double>(narrow));
+    const double weights = 2.0 * a.K * a.N;
+    return groups * weights * 0.17e-6 < 2.5 + std::max(0.27 * a.K / 64 * rounds, weights * 2 / 6.5e6);
 }
 
 bool glu_dims(int64_t M, int64_t K, int64_t N) {
@@ -734,20 +753,20 @@ extern "C" int tern_glu_fwd(const uint16_t* X, const tern_tiles* W, const float*
     if (K % 16 || N % 16) return TERN_ERR_ALIGN;
     if (M == 0) return TERN_OK;
     if (!X || !W || !scale || !H) return TERN_ERR_ARG;
-    const bool codes = M <= kCodeRows && !saved && W->packed;
-    if (!codes && !W->t_bf16) return TERN_ERR_ARG;
-    const void* weight = codes ? static_cast<const void*>(W->packed) : static_cast<const void*>(W->t_bf16);
-    if (!aligned16(X) || !aligned16(weight) || !aligned16(scale) || !aligned16(H) || !aligned16(saved)) return TERN_ERR_ALIGN;
+    const bool can = M <= kBM && !saved && W->packed;   // the codes serve few rows
+    if (!can && !W->t_bf16) return TERN_ERR_ARG;
+    if (!aligned16(X) || !aligned16(scale) || !aligned16(H) || !aligned16(saved) || (can && !aligned16(W->packed)) || !aligned16(W->t_bf16))
+        return TERN_ERR_ALIGN;
     int num_sms = 0;
     if (int st = check_device(&num_sms)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (codes) {
-        const CodeArgs c{X, W->packed, scale, H, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), act};
-        return M <= 8 ? glu_few<1, 4>(c, s) : glu_few<2, 3>(c, s);
-    }
     GluArgs a{};
     a.scale = scale, a.H = H, a.pair = saved;
     a.M = static_cast<int>(M), a.N = static_cast<int>(N), a.K = static_cast<int>(K), a.act = act;
+    if (can && (M <= kCodeRows || !W->t_bf16 || few_by_codes(a, num_sms))) {
+        const CodeArgs c{X, W->packed, scale, H, a.M, a.N, a.K, act, 0};
+        return M <= 8 ? glu_few<1, 4>(c, s) : glu_few<2, 3>(c, s);
+    }
     return glu_many(a, X, W->t_bf16, num_sms, s);
 }
 

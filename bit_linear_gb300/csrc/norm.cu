@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(1024) norm_cols(const float* __restrict__ part
     if (lane == 0 && mine < D) out[mine] = t;
 }
 
-// ---- rows in 16-byte words (the usual case): the same sums, with rows on their way while others are
+// ---- rows of pairs of elements (even widths; V = 8: of whole 16-byte words): the same sums, with rows on their way while others are
 // worked on.  A block takes two rows at a time, whose sums share their exchanges and barriers, and copies
 // the two after next into shared memory as it leaves their places; a thread reads only the words that
 // it copied itself.  Arithmetic on pairs of neighbours (an element takes 8 instructions in the forward
@@ -361,13 +361,29 @@ constexpr int pair_blocks(int T, bool bwd) { return T == 64 ? 8 : T <= 128 ? (bw
 constexpr int kPairWidest = 8192;          // channels of a row that 512 threads take
 constexpr size_t kPairSpace = 216 << 10;   // shared memory for it
 
-// A thread's copies of eight elements: one word of bf16, two of fp32, THREADS words apart.
-template <class T, int THREADS>
+template <int B>
+__device__ __forceinline__ void copy_small(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(B) : "memory");
+}
+
+// A thread's copies of eight elements: one word of bf16, two of fp32, THREADS words apart.  They are
+// copied in words of V elements (two of bf16 in four bytes, for instance), `pairs` of them there are.
+template <class T, int THREADS, int V>
 struct Eight {
     static constexpr int WORDS = kElem<T> == 2 ? 1 : 2;
-    static __device__ __forceinline__ void ask(uint4* to, const T* from) {
+    static __device__ __forceinline__ void ask(uint4* to, const T* from, int pairs) {
 #pragma unroll
-        for (int h = 0; h < WORDS; ++h) copy16(ptx::smem_u32(to + h * THREADS), from + h * (16 / kElem<T>));
+        for (int h = 0; h < WORDS; ++h) {
+            constexpr int EACH = 8 / WORDS;   // elements of a word
+            const uint32_t at = ptx::smem_u32(to + h * THREADS);
+            if constexpr (V == 8) {
+                copy16(at, from + h * EACH);
+            } else {
+#pragma unroll
+                for (int i = 0; i < EACH / 2; ++i)
+                    if (h * (EACH / 2) + i < pairs) copy_small<2 * kElem<T>>(at + i * 2 * kElem<T>, from + h * EACH + 2 * i);
+            }
+        }
     }
     static __device__ __forceinline__ void get(const uint4* from, F2 (&x)[4]) {
 #pragma unroll
@@ -383,11 +399,19 @@ struct Eight {
             }
         }
     }
-    static __device__ __forceinline__ void put(T* to, const F2 (&x)[4]) {
+    static __device__ __forceinline__ void put(T* to, const F2 (&x)[4], int pairs) {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split(x[i], v[2 * i], v[2 * i + 1]);
-        store_as<T, 8>(to, v);
+        if constexpr (V == 8) {
+            store_as<T, 8>(to, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float two[2] = {v[2 * i], v[2 * i + 1]};
+                if (i < pairs) store_as<T, 2>(to + 2 * i, two);
+            }
+        }
     }
 };
 
@@ -396,20 +420,28 @@ __device__ __forceinline__ float sum_of(F2 x) {
     split(x, a, b);
     return a + b;
 }
-// Eight parameters of the columns from c, or a value where there are none.
-__device__ __forceinline__ void params(const float* p, int c, int D, float other, F2 (&x)[4]) {
+// Eight parameters of the columns from c, of which `pairs` pairs there are, or a value in place of them.
+template <int V>
+__device__ __forceinline__ void params(const float* p, int c, int pairs, float other, F2 (&x)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = both(other);
-    if (p && c < D) {
-        const auto raw = load_raw<float, 8>(p + c);
+    if (!p) return;
+    if constexpr (V == 8) {
+        if (pairs > 0) {
+            const auto raw = load_raw<float, 8>(p + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = pair(raw_at<float, 8>(raw, 2 * i), raw_at<float, 8>(raw, 2 * i + 1));
+            for (int i = 0; i < 4; ++i) x[i] = pair(raw_at<float, 8>(raw, 2 * i), raw_at<float, 8>(raw, 2 * i + 1));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < pairs) x[i] = pair(__ldg(p + c + 2 * i), __ldg(p + c + 2 * i + 1));
     }
 }
 
 template <class TX, class TY, int T, int R>
 __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(const __grid_constant__ NormArgs a) {
-    using X = Eight<TX, T * R>;
+    using X = Eight<TX, T * R, 8>;
     extern __shared__ uint4 ring[];   // [2 turns][2 rows][2 runs][X::WORDS][T R]
     __shared__ float sums[2][4 * ((T + 31) / 32)];
     ptx::pdl_trigger();
@@ -424,7 +456,7 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = (j * T + t) * 8;
-                if (of + which < a.n && c < a.D) X::ask(place(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c);
+                if (of + which < a.n && c < a.D) X::ask(place(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c, 4);
             }
         copies_close();
     };
@@ -434,8 +466,9 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
     F2 w[2][4], b[2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        params(a.weight, (j * T + t) * 8, a.D, 1.f, w[j]);
-        params(a.bias, (j * T + t) * 8, a.D, 0.f, b[j]);
+        const int c = (j * T + t) * 8;
+        params<8>(a.weight, c, c < a.D ? 4 : 0, 1.f, w[j]);
+        params<8>(a.bias, c, c < a.D ? 4 : 0, 0.f, b[j]);
     }
     for (int turn = 0; row - ahead < a.n; row += step, turn ^= 1) {
         copies_wait_all_but_one();
@@ -494,7 +527,7 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
                     X::get(place(turn, which, j), x);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[i] = fma2(mul2(add2(add2(x[i], shift), rest), scale), w[j][i], b[j][i]);
-                    Eight<TY, T * R>::put(y + c, x);
+                    Eight<TY, T * R, 8>::put(y + c, x, 4);
                 }
             }
         }
@@ -502,10 +535,10 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
     }
 }
 
-template <class TX, class TY, int T, int R>
+template <class TX, class TY, int T, int R, int V>
 __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(const __grid_constant__ NormArgs a) {
-    using X = Eight<TX, T * R>;
-    using Y = Eight<TY, T * R>;
+    using X = Eight<TX, T * R, V>;
+    using Y = Eight<TY, T * R, V>;
     constexpr int ROW = 2 * (X::WORDS + Y::WORDS) * T * R;   // words of a row of x and one of dy
     extern __shared__ uint4 ring[];                          // [2 turns][2 rows] of them
     __shared__ float sums[2][6 * ((T + 31) / 32)];
@@ -516,6 +549,10 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
     const int ahead = T < 32 ? 2 * (threadIdx.x % 32 / T) : 0;   // of the warp's first row: a warp stays together
     auto place_x = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + j * X::WORDS * T * R + threadIdx.x; };
     auto place_d = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + (2 * X::WORDS + j * Y::WORDS) * T * R + threadIdx.x; };
+    int pairs[2];   // of each run, that lie in the row
+#pragma unroll
+    for (int j = 0; j < 2; ++j) pairs[j] = min(4, max(0, (a.D - (j * T + t) * 8) / 2));
+    const auto in_row = [&](int j, int i) { return V == 8 ? pairs[j] > 0 : i < pairs[j]; };
     float mean[2], rstd[2], mean_next[2] = {0.f, 0.f}, rstd_next[2] = {0.f, 0.f};
     auto ask = [&](int64_t of, int turn) {
 #pragma unroll
@@ -523,9 +560,9 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = (j * T + t) * 8;
-                if (of + which < a.n && c < a.D) {
-                    X::ask(place_x(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c);
-                    Y::ask(place_d(turn, which, j), static_cast<const TY*>(a.dy) + (of + which) * a.ld_dy + c);
+                if (of + which < a.n && pairs[j] > 0) {
+                    X::ask(place_x(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c, pairs[j]);
+                    Y::ask(place_d(turn, which, j), static_cast<const TY*>(a.dy) + (of + which) * a.ld_dy + c, pairs[j]);
                 }
             }
         copies_close();
@@ -545,7 +582,7 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
     F2 w[2][4], dw[2][4], db[2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        params(a.weight, (j * T + t) * 8, a.D, 1.f, w[j]);
+        params<V>(a.weight, (j * T + t) * 8, pairs[j], 1.f, w[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = both(0.f);
     }
@@ -561,11 +598,12 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
             if (row + which < a.n) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if ((j * T + t) * 8 < a.D) {
+                    if (pairs[j] > 0) {
                         X::get(place_x(turn, which, j), x);
                         Y::get(place_d(turn, which, j), d);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
+                            if (!in_row(j, i)) continue;
                             const F2 e = add2(x[i], shift), g = mul2(d[i], w[j][i]);
                             u0 = add2(u0, g);
                             u1 = fma2(g, e, u1);
@@ -588,17 +626,18 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = (j * T + t) * 8;
-                if (c < a.D) {
+                if (pairs[j] > 0) {
                     X::get(place_x(turn, which, j), x);
                     Y::get(place_d(turn, which, j), d);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        if (!in_row(j, i)) continue;
                         const F2 xhat = mul2(add2(add2(x[i], shift), rest), scale);
                         dw[j][i] = fma2(d[i], xhat, dw[j][i]);
                         db[j][i] = add2(db[j][i], d[i]);
                         x[i] = fma2(mul2(xhat, scale), along, fma2(mul2(d[i], w[j][i]), scale, base));
                     }
-                    X::put(dx + c, x);
+                    X::put(dx + c, x, pairs[j]);
                 }
             }
         }
@@ -641,8 +680,14 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
             float v8[8], u8[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v8[i] = v[8 * j + i], u8[i] = u[8 * j + i];
-            store_as<float, 8>(pw + c, v8);
-            store_as<float, 8>(pb + c, u8);
+            if constexpr (V == 8) {
+                store_as<float, 8>(pw + c, v8);
+                store_as<float, 8>(pb + c, u8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < a.D) pw[c + i] = v8[i], pb[c + i] = u8[i];
+            }
         }
     }
 }
@@ -692,18 +737,18 @@ int pick_rows(const NormArgs& a, int* parts, cudaStream_t s) {
     }
 }
 
-template <bool BWD, class TX, class TY, int T, int R>
+template <bool BWD, class TX, class TY, int T, int R, int V>
 int launch_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
-    constexpr size_t smem = 8u * T * R * 16 * (Eight<TX, 1>::WORDS + (BWD ? Eight<TY, 1>::WORDS : 0));
+    constexpr size_t smem = 8u * T * R * 16 * (Eight<TX, 1, V>::WORDS + (BWD ? Eight<TY, 1, V>::WORDS : 0));
     if constexpr (smem > kPairSpace) {
-        return pick_rows<BWD, TX, TY, 8>(a, parts, s);
+        return pick_rows<BWD, TX, TY, V>(a, parts, s);
     } else {
     const int64_t pairs = (static_cast<int64_t>(a.n) + 2 * R - 1) / (2 * R);
     const int blocks = std::min(pair_blocks(T, BWD), static_cast<int>(kPairSpace / smem));
     const int grid = static_cast<int>(std::min({pairs, static_cast<int64_t>(num_sms) * blocks, static_cast<int64_t>(kPartMax)}));
     *parts = grid;
     auto kernel = [] {
-        if constexpr (BWD) return norm_bwd_pairs<TX, TY, T, R>;
+        if constexpr (BWD) return norm_bwd_pairs<TX, TY, T, R, V>;
         else return norm_fwd_pairs<TX, TY, T, R>;
     }();
     if (smem > 40 * 1024) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
@@ -711,21 +756,21 @@ int launch_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     }
 }
 
-template <bool BWD, class TX, class TY>
+template <bool BWD, class TX, class TY, int V>
 int pick_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     if constexpr (BWD) {
         switch (row_threads(a.D, 8)) {
-        case 8: return launch_pairs<BWD, TX, TY, 8, rows_beside(8)>(a, num_sms, parts, s);
-        case 16: return launch_pairs<BWD, TX, TY, 16, rows_beside(16)>(a, num_sms, parts, s);
-        case 32: return launch_pairs<BWD, TX, TY, 32, rows_beside(32)>(a, num_sms, parts, s);
-        case 64: return launch_pairs<BWD, TX, TY, 64, 1>(a, num_sms, parts, s);
-        case 128: return launch_pairs<BWD, TX, TY, 128, 1>(a, num_sms, parts, s);
+        case 8: return launch_pairs<BWD, TX, TY, 8, rows_beside(8), V>(a, num_sms, parts, s);
+        case 16: return launch_pairs<BWD, TX, TY, 16, rows_beside(16), V>(a, num_sms, parts, s);
+        case 32: return launch_pairs<BWD, TX, TY, 32, rows_beside(32), V>(a, num_sms, parts, s);
+        case 64: return launch_pairs<BWD, TX, TY, 64, 1, V>(a, num_sms, parts, s);
+        case 128: return launch_pairs<BWD, TX, TY, 128, 1, V>(a, num_sms, parts, s);
         default: break;
         }
     }
     switch (row_threads(a.D, 8)) {
-    case 256: return launch_pairs<BWD, TX, TY, 256, 1>(a, num_sms, parts, s);
-    default: return launch_pairs<BWD, TX, TY, 512, 1>(a, num_sms, parts, s);
+    case 256: return launch_pairs<BWD, TX, TY, 256, 1, V>(a, num_sms, parts, s);
+    default: return launch_pairs<BWD, TX, TY, 512, 1, V>(a, num_sms, parts, s);
     }
 }
 
@@ -757,9 +802,13 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaS
         // in fp32 227, 187).
         const bool pairs = a.D <= kPairWidest && (BWD ? a.n > 2 * num_sms * rows_beside(row_threads(a.D, 8)) : ex == 2 && a.D > 2048 && a.n > 2 * num_sms);
         if (all_allow(a, BWD, 8, ex, ey)) {
-            st = pairs ? pick_pairs<BWD, TX, TY>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 8>(a, &parts, s);
-        } else if (all_allow(a, BWD, 2, ex, ey)) st = pick_rows<BWD, TX, TY, 2>(a, &parts, s);
-        else st = pick_rows<BWD, TX, TY, 1>(a, &parts, s);
+            st = pairs ? pick_pairs<BWD, TX, TY, 8>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 8>(a, &parts, s);
+        } else if (all_allow(a, BWD, 2, ex, ey)) {
+            if constexpr (BWD) st = pairs ? pick_pairs<BWD, TX, TY, 2>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, &parts, s);
+            else st = pick_rows<BWD, TX, TY, 2>(a, &parts, s);
+        } else {
+            st = pick_rows<BWD, TX, TY, 1>(a, &parts, s);
+        }
         if (st) return st;
     }
     if (BWD && (dweight || dbias))   // of no rows: zeros

@@ -518,9 +518,10 @@ int tern_norm_bwd(const void* x, int x_dtype, int64_t ld_x, const float* weight,
  *   H     = act(g) * u            bf16 [M][N]
  * in one kernel.  act: TERN_ACT_SILU g sigmoid(g), TERN_ACT_GELU g Phi(g) (to 1e-7 in Phi),
  * TERN_ACT_RELU2 max(g, 0)^2, TERN_ACT_SIGMOID sigmoid(g).
- *   X [M][K] bf16, scale [2N] fp32, W the tiles of the K x 2N weight.  Up to 16 rows without `saved`
- *   read W->packed where it is given (single tokens: an eighth of the bytes); every other call, and
- *   those without W->packed, reads W->t_bf16 (NULL: TERN_ERR_ARG).
+ *   X [M][K] bf16, scale [2N] fp32, W the tiles of the K x 2N weight.  With up to 128 rows and no `saved`,
+ *   either W->packed (single tokens: an eighth of the bytes) or W->t_bf16 may be NULL; given both, the
+ *   sizes decide which is read (up to 16 rows W->packed).  Every other call reads W->t_bf16 (NULL:
+ *   TERN_ERR_ARG).  The two sum in different orders.
  *   saved [M][2N] bf16, or NULL: the factors  u act'(g) | act(g)  that tern_glu_bwd multiplies.
  * K, N multiples of 16, at least 16 (tern_materialize wants no more); M >= 0; dense matrices, every
  * pointer 16-byte aligned.  H is rounded once from fp32.

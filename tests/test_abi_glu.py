@@ -23,7 +23,7 @@ def test_forward_checks(lib):
     f = lib.lib.tern_glu_fwd
     both = _tiles(lib)
 
-    def call(X=P(0x10000), W=both, scale=P(0x20000), act=0, H=P(0x30000), saved=None, M=40, K=32, N=48):
+    def call(X=P(0x10000), W=both, scale=P(0x20000), act=0, H=P(0x30000), saved=None, M=140, K=32, N=48):
         return f(X, W, scale, act, H, saved, M, K, N, None)
 
     assert call(M=0) == lib.TERN_OK

@@ -107,7 +107,8 @@ def test_forward_and_both_gradients(cuda_lib, M, K, N, act):
     assert bl.tern_device_status() == bl.TERN_OK
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 16, 16), (1, 8192, 48), (2, 528, 2064), (8, 512, 1360), (11, 4096, 1024), (16, 160, 4112)])
+@pytest.mark.parametrize("M,K,N", [(1, 16, 16), (1, 8192, 48), (2, 528, 2064), (8, 512, 1360), (11, 4096, 1024), (16, 160, 4112), (17, 4096, 208), (33, 512, 144),
+                                   (64, 1024, 400), (100, 48, 1360), (128, 2048, 16), (127, 80, 2064)])
 def test_few_rows_from_either_weight(cuda_lib, M, K, N):
     """The codes alone, the bf16 plane alone, and both: each within the same bound, each the same every time."""
     bl = cuda_lib
@@ -222,7 +223,7 @@ def test_refusals(cuda_lib):
         bl.tern_glu_fwd(X.float(), tiles, scale, H)
     with pytest.raises(ValueError):
         bl.tern_glu_bwd(dH, pair, X=X)
-    with pytest.raises(bl.TernError):
-        bl.tern_glu_fwd(X, _tiles(bl, q, scale, t=False), scale, H)          # 20 rows read the bf16 plane
-    with pytest.raises(bl.TernError):
-        bl.tern_glu_fwd(X[:4], _tiles(bl, q, scale, t=False), scale, H[:4], saved=pair[:4])   # so do factors
+    with pytest.raises(bl.TernError):                          # from 129 rows on the bf16 plane is read
+        bl.tern_glu_fwd(X.repeat(7, 1), _tiles(bl, q, scale, t=False), scale, H.repeat(7, 1))
+    with pytest.raises(bl.TernError):                          # and for the factors
+        bl.tern_glu_fwd(X[:4], _tiles(bl, q, scale, t=False), scale, H[:4], saved=pair[:4])

@@ -54,7 +54,7 @@ def _inputs(n, D, tx, ty, seed, shift=0.0):
 
 # Enough rows for the kernels that take pairs of them, odd counts and uneven ends among them; sums over up to
 # 14 rows a block in turn, 16 side by side, then 19 and 32: under 128 too
-@pytest.mark.parametrize("n,D", [(9999, 8), (6001, 64), (5001, 128), (5003, 136), (2600, 256), (2501, 264), (1303, 512), (700, 520), (2611, 600), (2600, 1024), (611, 1032), (402, 2048), (705, 2056),
+@pytest.mark.parametrize("n,D", [(9999, 8), (9999, 2), (6001, 62), (6001, 64), (5001, 130), (2601, 254), (1300, 510), (2605, 602), (703, 1030), (702, 2058), (401, 4102), (5001, 128), (5003, 136), (2600, 256), (2501, 264), (1303, 512), (700, 520), (2611, 600), (2600, 1024), (611, 1032), (402, 2048), (705, 2056),
                                  (403, 4096), (350, 4104), (309, 8192), (320, 8200)])
 @pytest.mark.parametrize("tx,ty", TYPES, ids=IDS)
 def test_many_rows(cuda_lib, n, D, tx, ty):
