@@ -46,7 +46,7 @@ struct Stats {
     // Relative to mn >= m (finite, or inf: then s becomes NaN, as it should).
     __device__ __forceinline__ void rebase(float mn, float c) {
         if (m != kNegInf) {   // of nothing but -inf s and q are 0, or s is NaN
-            const float d = m - mn, f = pow2(d * c);
+            const float d = ENT ? fmaxf(m - mn, -1e4f) : m - mn, f = pow2(d * c);   // s d finite, whatever the maximum was
             if (ENT) q = (q + s * d) * f;
             s *= f;
         }
@@ -82,7 +82,7 @@ struct Run {
     __device__ __forceinline__ bool raise(float top, float c) {
         if (top > m) {
             if (m != kNegInf) {
-                const float d = m - top, f = pow2(d * c);
+                const float d = ENT ? fmaxf(m - top, -1e4f) : m - top, f = pow2(d * c);
                 if (ENT) q = mul2(fma2(s, both(d), q), both(f));
                 s = mul2(s, both(f));
             }
@@ -90,7 +90,7 @@ struct Run {
         }
         return m != kNegInf;
     }
-    // `masked`: there may be -inf among the batch, which would give 0 times infinity in the entropy's sum.
+    // `masked`: a difference may be -inf, which would give 0 times infinity in the entropy's sum.
     template <int N2>
     __device__ __forceinline__ void add(const F2 (&x)[N2], float top, bool masked, float c) {
         if (raise(top, c)) {
@@ -196,13 +196,14 @@ __device__ __forceinline__ float raw_max(const Raw<T, V> (&r)[U]) {
         return m;
     }
 }
+// Whether a difference to the maximum may be -inf: masked entries, or values near the type's ends.
 template <class T, int V, int U>
-__device__ __forceinline__ bool raw_masked(const Raw<T, V> (&r)[U]) {   // whether there may be -inf
+__device__ __forceinline__ bool raw_masked(const Raw<T, V> (&r)[U], float top) {
     if constexpr (kElem<T> == 2) {
         uint32_t m = r[0].w[0];
 #pragma unroll
         for (int i = 1; i < U * V / 2; ++i) asm("min.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(r[i / (V / 2)].w[i % (V / 2)]));
-        return fminf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)) == kNegInf;
+        return fminf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)) < -1e30f || top > 1e30f;
     } else {
         return true;   // looking costs what the bound that it would save does
     }
@@ -247,7 +248,7 @@ __device__ __forceinline__ Stats<ENT> read_row(const Row<TX>& r, int first, int 
     for (; i + (U - 1) * T < last; i += U * T) {
         ask(next, i + U * T);
         const float top = raw_max(raw);
-        if (ENT && !raw_masked(raw)) run.add_words(raw, top, false, c);
+        if (ENT && !raw_masked(raw, top)) run.add_words(raw, top, false, c);
         else run.add_words(raw, top, true, c);
         if (ENT && tops && seg == 1) {
 #pragma unroll
@@ -377,6 +378,20 @@ struct TopSpace {
     int warps[T / 32];
 };
 
+// Places for n of each lane in a list whose length is *count: one atomic a warp.
+__device__ __forceinline__ int append(int* count, int n) {
+    const int lane = threadIdx.x & 31;
+    int incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+    }
+    int base = 0;
+    if (lane == 31 && incl) base = atomicAdd(count, incl);
+    return __shfl_sync(0xffffffffu, base, 31) + incl - n;
+}
+
 // Every entry of the slice with a key of at least lo, as candidates; sp.count of them (kCand are kept).
 // Only segments whose largest entry reaches lo are read again; all of them where there is NaN (`every`).
 template <class TX, int T>
@@ -386,46 +401,60 @@ __device__ __forceinline__ void collect(const Row<TX>& r, int first, int last, b
     __syncthreads();
     if (t == 0) sp.count = sp.listed = 0;
     __syncthreads();
-    const float bound = key_value(lo);   // NaN for 0 and above +inf: reached by all
+    // For finite bounds the floats compare as the keys do; it is NaN, reached by all, for a lo below -inf's key
+    const float bound = key_value(lo);
+    uint32_t mask = 0;
     for (int g = 0; first + t + g * seg * T < last; ++g)
-        if (every || !(sp.tops[g * T + t] < bound)) sp.list[atomicAdd(&sp.listed, 1)] = static_cast<uint16_t>(g * T + t);
-    auto offer = [&](float x, int e) {
-        if (!every && x < bound) return;
-        const uint32_t key = order_key(x);
-        if (key >= lo) {
-            const int at = atomicAdd(&sp.count, 1);
-            if (at < kCand<T>) sp.cand[at] = entry_key(key, e);
-        }
-    };
+        if (every || !(sp.tops[g * T + t] < bound)) mask |= 1u << g;
+    __syncwarp();
+    for (int at = append(&sp.listed, __popc(mask)); mask; mask &= mask - 1) sp.list[at++] = static_cast<uint16_t>((__ffs(mask) - 1) * T + t);
     __syncthreads();
-    const int listed = sp.listed;
-    for (int w0 = t; w0 < listed * seg; w0 += U * T) {
+    const int units = sp.listed * seg;
+    for (int w0 = 0; w0 < units; w0 += U * T) {
         Raw<TX, VE> raw[U];
         int at[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int w = w0 + u * T;
+            const int w = w0 + u * T + t;
             at[u] = last;
-            if (w < listed * seg) {
+            if (w < units) {
                 const int item = sp.list[w / seg];
                 at[u] = first + item % T + (item / T * seg + w % seg) * T;
             }
             if (at[u] < last) raw[u] = load_raw<TX, VE>(r.word(at[u]));
         }
+        mask = 0;   // of the words' entries, VE bits each
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (at[u] < last) {
                 const Raw<TX, VE> one[1] = {raw[u]};
                 if (every || !(raw_max(one) < bound)) {
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) offer(raw_at<TX, VE>(raw[u], e), r.head + at[u] * VE + e);
+                    for (int e = 0; e < VE; ++e) {
+                        const float x = raw_at<TX, VE>(raw[u], e);
+                        mask |= static_cast<uint32_t>(every ? order_key(x) >= lo : !(x < bound)) << (u * VE + e);
+                    }
                 }
             }
+        }
+        __syncwarp();
+        for (int to = append(&sp.count, __popc(mask)); mask; mask &= mask - 1, ++to) {
+            const int bit = __ffs(mask) - 1, u = bit / VE;
+            int i = at[0];
+#pragma unroll
+            for (int v = 1; v < U; ++v)
+                if (u == v) i = at[v];
+            const int e = r.head + i * VE + bit % VE;
+            if (to < kCand<T>) sp.cand[to] = entry_key(order_key(r.at(e)), e);
         }
     }
     if (edges && t < r.edges()) {
         const int e = r.edge(t);
-        offer(r.at(e), e);
+        const uint32_t key = order_key(r.at(e));
+        if (key >= lo) {
+            const int to = atomicAdd(&sp.count, 1);
+            if (to < kCand<T>) sp.cand[to] = entry_key(key, e);
+        }
     }
     __syncthreads();
 }
@@ -937,13 +966,13 @@ __device__ __forceinline__ float row_loss(const DistillArgs& a, const int* ids, 
     return w * (a.T * a.T) * t;
 }
 
-// coef 2^(c (x - shift) - base) = w T q
+// coef 2^(c (x - shift)) = w T q, from the maximum or (the gradient alone) from T lse
 struct Gradient {
-    float c, shift, base, coef;
-    __device__ __forceinline__ float operator()(float x) const { return coef * pow2(fmaf(x - shift, c, -base)); }
+    float c, shift, coef;
+    __device__ __forceinline__ float operator()(float x) const { return coef * pow2((x - shift) * c); }
     __device__ __forceinline__ void operator()(F2 x, float& a, float& b) const {
         float t0, t1;
-        split(fma2(add2(x, both(-shift)), both(c), both(-base)), t0, t1);
+        split(mul2(add2(x, both(-shift)), both(c)), t0, t1);
         split(mul2(pair(pow2(t0), pow2(t1)), both(coef)), a, b);
     }
 };
@@ -1008,7 +1037,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) distill_r
         }
     }
     auto own = [&](int e) { return e < r.head || e >= r.tail0 ? edges : e >= r.head + first * VE && e < r.head + last * VE; };
-    Gradient g{a.inv_t * kLog2e, 0.f, 0.f, 0.f};
+    Gradient g{a.inv_t * kLog2e, 0.f, 0.f};
     Stats<false> st;
     if (!a.lse_in) st = read_row<TX, T, false>(r, first, last, edges, g.c);
     // The entries' logits, before any of the gradient is written, which may lie in their place: all of them
@@ -1050,7 +1079,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) distill_r
         ts = __shfl_sync(0xffffffffu, ts, 0);
     }
     if (a.lse_in) {
-        g.base = __ldg(a.lse_in + row) * kLog2e;
+        g.shift = __ldg(a.lse_in + row) * a.T;
         g.coef = w * a.T;
         if (size > 1) cluster_wait();   // the arrival at the start
     } else {
@@ -1167,11 +1196,11 @@ __global__ void __launch_bounds__(128) distill_warps(const __grid_constant__ Dis
     wr.load(x);   // under way while the teacher's entries are read
     const float w = a.weight ? __ldg(a.weight + row) : 1.f;
     const bool live = teacher(a, row, ids, p, w);
-    Gradient g{a.inv_t * kLog2e, 0.f, 0.f, 0.f};
+    Gradient g{a.inv_t * kLog2e, 0.f, 0.f};
     if (live) {
         at_teacher(a, r, ids, xs, lane, 32, [](int) { return true; });
         if (a.lse_in) {
-            g.base = __ldg(a.lse_in + row) * kLog2e;
+            g.shift = __ldg(a.lse_in + row) * a.T;
             g.coef = w * a.T;
         } else {
             const Stats<false> st = warp_stats<EPL, false>(x, g.c);
@@ -1213,11 +1242,11 @@ bool aligned_to(const void* p, int b) { return reinterpret_cast<uintptr_t>(p) % 
 // Threads of a block.  Where rows are many, a warp up to 16 KB (no barriers, many rows at once) and 128 up to
 // 56 KB; distillation of bf16 rows with 32, 128 and 256 threads: 32768 x 700 58, 134, 238 us; 4096 x 8000 36,
 // 40, 52; 4096 x 12000 54, 48, 59; 4096 x 20000 86, 69, 77; 4096 x 40000 168, 159, 126.  Scores cross at the
-// same sizes.
-int row_block(int64_t n, int64_t V, int es, int num_sms) {
+// same sizes, but with few alternatives to find 128 do up to 128 KB (8192 x 60000 with 10: 183, 216 us).
+int row_block(int64_t n, int64_t V, int es, int num_sms, int64_t most = 57344) {
     const int64_t bytes = V * es;
     if (bytes <= 16384) return n >= 16 * num_sms ? 32 : 128;
-    return bytes <= 57344 && n >= 8 * num_sms ? 128 : 256;
+    return bytes <= most && n >= 8 * num_sms ? 128 : 256;
 }
 
 // Blocks that share a row: twice as many until the rows fill the GPU twice, as long as each thread keeps a word.
@@ -1240,7 +1269,7 @@ int run_score(const ScoreArgs& a, int num_sms, cudaStream_t s) {
         if (warp_words(a.logits, a.ld, a.n, a.V, es)) return launch_pdl(score_warps<TX, kWarpRow / 32, true>, grid, block, 0, s, a);
         return launch_pdl(score_warps<TX, kWarpRow / 32, false>, grid, block, 0, s, a);
     }
-    const int T = row_block(a.n, a.V, es, num_sms), c = row_blocks(a.n, a.V, es, T, num_sms);
+    const int T = row_block(a.n, a.V, es, num_sms, a.k > 0 && a.k <= 32 ? 131072 : 57344), c = row_blocks(a.n, a.V, es, T, num_sms);
     if (T == 32) return launch_cluster(score_rows<TX, 32>, a.n, T, 0, 1, true, s, a);
     if (T == 128) return launch_cluster(score_rows<TX, 128>, a.n * c, T, 0, c, true, s, a);
     return launch_cluster(score_rows<TX, 256>, a.n * c, T, 0, c, true, s, a);

@@ -587,7 +587,7 @@ typedef struct tern_distillation {
  * gradient written in the same call.
  */
 int tern_distill(const tern_distillation* t, float* loss, float* lse, void* dlogits, int64_t ld_dlogits, void* stream);
-/* The gradient alone, from tern_distill's lse. */
+/* The gradient alone, from tern_distill's lse (whose rounding, 2^-24 of its size, is then in the exponent). */
 int tern_distill_bwd(const tern_distillation* t, const float* lse, void* dlogits, int64_t ld_dlogits, void* stream);
 
 /* Text of a status code (static storage). */

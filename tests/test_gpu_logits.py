@@ -34,7 +34,8 @@ def _stats(x, T=1.0):
 
 
 def _close(got, ref, tol, name):
-    same = (got.double() == ref) | (got.isnan() & ref.isnan())
+    # equal, or equal once rounded: a value past the type's range (log probabilities down to -6.8e38) is infinite
+    same = (got.double() == ref) | (got == ref.to(got.dtype)) | (got.isnan() & ref.isnan())
     err = torch.where(same, torch.zeros_like(ref), (got.double() - ref).abs())
     bound = torch.where(same, torch.zeros_like(ref), tol + HALF[got.dtype] * (ref.abs() + tol))
     assert not (err.isnan() & ~same).any() and torch.all(err <= bound), (name, float((err - bound).max()))
@@ -113,6 +114,22 @@ def test_score_masks_and_ties(cuda_lib, V, dtype):
         _check_score(cuda_lib, x[:1], _tokens(1, V) + 3, kk)     # a row that blocks share
         for r in (3, 4, 5, 6, 7, 13):
             _check_score(cuda_lib, x[r:r + 1], _tokens(1, V) + 3, kk)
+
+
+@pytest.mark.parametrize("V", [200, 3000, 40000])
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_masks_of_the_lowest_value(cuda_lib, V, dtype):
+    """Entries masked by the type's lowest value in place of -inf, rows of nothing else, and values near both ends."""
+    randn, rand = _gen(V)
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x = torch.stack([randn(V).masked_fill(rand(V) < 0.5, low), torch.full((V,), low, device="cuda"),
+                     torch.where(rand(V) < 0.5, low, high), torch.where(torch.arange(V, device="cuda") == 7, 1.0, low)]).to(dtype)
+    _check_score(cuda_lib, x, torch.full((4,), 7, device="cuda"), 20)
+    for r in range(4):
+        _check_score(cuda_lib, x[r:r + 1], torch.full((1,), 7, device="cuda"), 20)
+    # the teacher's entries where the student has probability
+    ids = x.float().argmax(1, keepdim=True).int().repeat(1, 2)
+    _check_distill(cuda_lib, x[[0, 1, 3]], ids[[0, 1, 3]], torch.zeros(3, 2, device="cuda"), torch.ones(3, device="cuda"), 1.0)
 
 
 @pytest.mark.parametrize("V", [900, 8000, 70000])
