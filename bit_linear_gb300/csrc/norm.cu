@@ -319,30 +319,39 @@ __global__ void __launch_bounds__(256) norm_cols_wide(const __grid_constant__ No
     if (dbias) dbias[c] = b;
 }
 
-// Sums of the blocks' columns: a block takes 32 columns, warp w adds the parts w, w + 32, ... (all asked
-// for at once) and the warps' sums are added in order.  grid.y = 2: the weight's, the bias's.
+// Sums of the blocks' columns: a block takes C columns, a warp's lanes 32 / C parts of each, further
+// parts in turn (ten asked for at once); lanes and warps are added in a fixed order.  grid.y = 2: the weight's,
+// the bias's.  Eight columns a block where that makes too few blocks otherwise.
+template <int C>
 __global__ void __launch_bounds__(1024) norm_cols(const float* __restrict__ part, int parts, int D, float* dweight, float* dbias) {
-    constexpr int EACH = (kPartMax + 31) / 32;
-    __shared__ float s[32][33];
+    constexpr int BESIDE = 32 / C, STEP = 32 * BESIDE, EACH = 10;
+    __shared__ float s[32][C + 1];
     ptx::pdl_trigger();
     ptx::pdl_wait();
     float* out = blockIdx.y == 0 ? dweight : dbias;
     if (!out) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = static_cast<int>(blockIdx.x) * 32 + lane;
-    const float* p = part + (static_cast<int64_t>(blockIdx.y) * parts + warp) * D + c;
-    float v[EACH], t = 0.f;
+    const int c = static_cast<int>(blockIdx.x) * C + lane % C, first = warp * BESIDE + lane / C;
+    const float* p = part + (static_cast<int64_t>(blockIdx.y) * parts + first) * D + c;
+    float t = 0.f;
+    for (int k0 = 0; k0 * STEP < parts; k0 += EACH) {
+        float v[EACH];
 #pragma unroll
-    for (int k = 0; k < EACH; ++k) v[k] = c < D && warp + 32 * k < parts ? __ldcg(p + static_cast<int64_t>(32 * k) * D) : 0.f;
+        for (int k = 0; k < EACH; ++k) v[k] = c < D && first + (k0 + k) * STEP < parts ? __ldcg(p + static_cast<int64_t>((k0 + k) * STEP) * D) : 0.f;
 #pragma unroll
-    for (int k = 0; k < EACH; ++k) t += v[k];
-    s[warp][lane] = t;
+        for (int k = 0; k < EACH; ++k) t += v[k];
+    }
+#pragma unroll
+    for (int d = 16; d >= C; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+    if (lane < C) s[warp][lane] = t;
     __syncthreads();
-    t = s[lane][warp];   // column `warp`, the warps' sums side by side
+    if (warp < C) {
+        t = s[lane][warp];   // column `warp`, the warps' sums side by side
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-    const int mine = static_cast<int>(blockIdx.x) * 32 + warp;
-    if (lane == 0 && mine < D) out[mine] = t;
+        for (int d = 16; d >= 1; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+        const int mine = static_cast<int>(blockIdx.x) * C + warp;
+        if (lane == 0 && mine < D) out[mine] = t;
+    }
 }
 
 // ---- rows of pairs of elements (even widths; V = 8: of whole 16-byte words): the same sums, with rows on their way while others are
@@ -743,32 +752,27 @@ int launch_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     if constexpr (smem > kPairSpace) {
         return pick_rows<BWD, TX, TY, V>(a, parts, s);
     } else {
-    const int64_t pairs = (static_cast<int64_t>(a.n) + 2 * R - 1) / (2 * R);
-    const int blocks = std::min(pair_blocks(T, BWD), static_cast<int>(kPairSpace / smem));
-    const int grid = static_cast<int>(std::min({pairs, static_cast<int64_t>(num_sms) * blocks, static_cast<int64_t>(kPartMax)}));
-    *parts = grid;
-    auto kernel = [] {
-        if constexpr (BWD) return norm_bwd_pairs<TX, TY, T, R, V>;
-        else return norm_fwd_pairs<TX, TY, T, R>;
-    }();
-    if (smem > 40 * 1024) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    return launch_pdl(kernel, dim3(grid), dim3(T * R), smem, s, a);
+        const int64_t pairs = (static_cast<int64_t>(a.n) + 2 * R - 1) / (2 * R);
+        const int blocks = std::min(pair_blocks(T, BWD), static_cast<int>(kPairSpace / smem));
+        const int grid = static_cast<int>(std::min({pairs, static_cast<int64_t>(num_sms) * blocks, static_cast<int64_t>(kPartMax)}));
+        *parts = grid;
+        auto kernel = [] {
+            if constexpr (BWD) return norm_bwd_pairs<TX, TY, T, R, V>;
+            else return norm_fwd_pairs<TX, TY, T, R>;
+        }();
+        if (smem > 40 * 1024) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+        return launch_pdl(kernel, dim3(grid), dim3(T * R), smem, s, a);
     }
 }
 
 template <bool BWD, class TX, class TY, int V>
 int pick_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
-    if constexpr (BWD) {
-        switch (row_threads(a.D, 8)) {
-        case 8: return launch_pairs<BWD, TX, TY, 8, rows_beside(8), V>(a, num_sms, parts, s);
-        case 16: return launch_pairs<BWD, TX, TY, 16, rows_beside(16), V>(a, num_sms, parts, s);
-        case 32: return launch_pairs<BWD, TX, TY, 32, rows_beside(32), V>(a, num_sms, parts, s);
-        case 64: return launch_pairs<BWD, TX, TY, 64, 1, V>(a, num_sms, parts, s);
-        case 128: return launch_pairs<BWD, TX, TY, 128, 1, V>(a, num_sms, parts, s);
-        default: break;
-        }
-    }
     switch (row_threads(a.D, 8)) {
+    case 8: return launch_pairs<BWD, TX, TY, 8, rows_beside(8), V>(a, num_sms, parts, s);
+    case 16: return launch_pairs<BWD, TX, TY, 16, rows_beside(16), V>(a, num_sms, parts, s);
+    case 32: return launch_pairs<BWD, TX, TY, 32, rows_beside(32), V>(a, num_sms, parts, s);
+    case 64: return launch_pairs<BWD, TX, TY, 64, 1, V>(a, num_sms, parts, s);
+    case 128: return launch_pairs<BWD, TX, TY, 128, 1, V>(a, num_sms, parts, s);
     case 256: return launch_pairs<BWD, TX, TY, 256, 1, V>(a, num_sms, parts, s);
     default: return launch_pairs<BWD, TX, TY, 512, 1, V>(a, num_sms, parts, s);
     }
@@ -797,12 +801,14 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaS
     if (a.n > 0) {
         constexpr int ex = kElem<TX>, ey = kElem<TY>;
         int st;
-        // Pairs of rows: the gradient from a pair for each SM on (32768 x 4096 bf16 137 us, row by row 311;
-        // 64 x 4096 6.8, 5.7), the forward of wide bf16 rows (32768 x 4096 99 us, 135; 16384 x 1024 28, 22;
-        // in fp32 227, 187).
-        const bool pairs = a.D <= kPairWidest && (BWD ? a.n > 2 * num_sms * rows_beside(row_threads(a.D, 8)) : ex == 2 && a.D > 2048 && a.n > 2 * num_sms);
+        // Pairs of rows, from a pair for each SM on: the gradient (32768 x 4096 bf16 137 us, row by row 311; 64 x 4096
+        // 6.8, 5.7) and the forward from bf16 to bf16 (32768 x 4096 99 us, 135; 65536 x 1024 56, 69; from fp32
+        // row by row is faster: 32768 x 4096 187 us, 227).
+        constexpr bool PAIRS = BWD || (ex == 2 && ey == 2);
+        const bool pairs = a.D <= kPairWidest && a.n > 2 * num_sms * rows_beside(row_threads(a.D, 8));
         if (all_allow(a, BWD, 8, ex, ey)) {
-            st = pairs ? pick_pairs<BWD, TX, TY, 8>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 8>(a, &parts, s);
+            if constexpr (PAIRS) st = pairs ? pick_pairs<BWD, TX, TY, 8>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 8>(a, &parts, s);
+            else st = pick_rows<BWD, TX, TY, 8>(a, &parts, s);
         } else if (all_allow(a, BWD, 2, ex, ey)) {
             if constexpr (BWD) st = pairs ? pick_pairs<BWD, TX, TY, 2>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, &parts, s);
             else st = pick_rows<BWD, TX, TY, 2>(a, &parts, s);
@@ -811,8 +817,11 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaS
         }
         if (st) return st;
     }
-    if (BWD && (dweight || dbias))   // of no rows: zeros
-        return launch_pdl(norm_cols, dim3((a.D + 31) / 32, 2), dim3(1024), 0, s, static_cast<const float*>(a.part), parts, a.D, dweight, dbias);
+    if (BWD && (dweight || dbias)) {   // of no rows: zeros
+        const float* part = a.part;
+        if (a.D <= 2048) return launch_pdl(norm_cols<8>, dim3((a.D + 7) / 8, 2), dim3(1024), 0, s, part, parts, a.D, dweight, dbias);
+        return launch_pdl(norm_cols<32>, dim3((a.D + 31) / 32, 2), dim3(1024), 0, s, part, parts, a.D, dweight, dbias);
+    }
     return TERN_OK;
 }
 
