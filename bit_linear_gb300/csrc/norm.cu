@@ -16,6 +16,9 @@
 // the pass that needs x - mean anyway and taken out of xhat: in the forward, and again in the
 // gradient, where sum g xhat = rstd (sum g d - delta sum g) with d = x - mean.
 //
+// The mean that is kept has delta in it only where delta is more than its own rounding (2^-20 of the
+// deviation): around zero the first sum is the better one, of bf16 often exact.
+//
 // The gradient's blocks stay for many rows and keep the sums of their columns in registers; each
 // block stores its sums once, and a second launch adds the blocks' in a fixed order.
 #include <algorithm>
@@ -42,6 +45,10 @@ struct NormArgs {
     int n, D;
     float eps, inv_d;
 };
+
+__device__ __forceinline__ float kept_mean(float mean, float delta, float rstd) {
+    return fabsf(delta) * rstd > 9.5367432e-7f ? mean + delta : mean;
+}
 
 // EPT elements of a row in registers: thread t holds V neighbouring elements at (j T + t) V.
 // T threads a row, R rows a block side by side (R > 1 with T <= 32 only).
@@ -92,7 +99,7 @@ __global__ void __launch_bounds__(T * R, 1) norm_fwd(const __grid_constant__ Nor
     // fmaxf drops a NaN: the row's own comes back through x - mean
     if (!in) return;
     if (t == 0) {
-        if (a.mean) a.mean[row] = mean + delta;
+        if (a.mean) a.mean[row] = kept_mean(mean, delta, rstd);
         if (a.rstd) a.rstd[row] = q[1] == q[1] ? rstd : q[1];
     }
     TY* y = static_cast<TY*>(a.y) + row * a.ld_y;
@@ -138,7 +145,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide(const __grid_constant__ No
     const float delta = q[0] * a.inv_d;
     const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-delta, delta, q[1] * a.inv_d), 0.f) + a.eps);
     if (threadIdx.x == 0) {
-        if (a.mean) a.mean[row] = mean + delta;
+        if (a.mean) a.mean[row] = kept_mean(mean, delta, rstd);
         if (a.rstd) a.rstd[row] = q[1] == q[1] ? rstd : q[1];
     }
     for (int c = threadIdx.x; c < a.D; c += 1024) {
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
             const float delta = q[2 * which] * a.inv_d, sq = q[2 * which + 1];
             const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-delta, delta, sq * a.inv_d), 0.f) + a.eps);
             if (t == 0) {
-                if (a.mean) a.mean[row + which] = mean[which] + delta;
+                if (a.mean) a.mean[row + which] = kept_mean(mean[which], delta, rstd);
                 if (a.rstd) a.rstd[row + which] = sq == sq ? rstd : sq;   // fmaxf drops a NaN
             }
             TY* y = static_cast<TY*>(a.y) + (row + which) * a.ld_y;

@@ -3,7 +3,7 @@
 Bounds, with u = 2^-24 (half a step of fp32) and h the half step of the output's type: a sum over a row
 adds at most 16 terms in a thread (D / 1024 in the widest rows), 5 in a warp and 32 over warps, so it is off by less than 64 u
 times the sum of magnitudes; xhat by the roundings of x - mean and rstd (whose variance has such a sum)
-and by delta's sum.  Sums over rows add at most ceil(n / 608) rows a block, 4 side by side, and 38 + 16
+and by delta's sum; the mean by its rounding and delta's sum, or by a delta of at most 16 u deviations.  Sums over rows add at most ceil(n / 608) rows a block, 4 side by side, and 38 + 16
 blocks: under 128 for the sizes here."""
 import pytest
 import torch
@@ -26,7 +26,7 @@ def _ref(x, w, b, eps, dy=None):
     md = d.abs().mean(1, keepdim=True)
     off = U * (80 * xhat.abs() + 64 * md * rstd)
     y = xhat * w + b
-    out = [(y, w.abs() * off + 2 * U * (y.abs() + (w * xhat).abs())), (mean[:, 0], (U * (mean.abs() + 64 * md))[:, 0]), (rstd[:, 0], 40 * U * rstd[:, 0])]
+    out = [(y, w.abs() * off + 2 * U * (y.abs() + (w * xhat).abs())), (mean[:, 0], (U * (mean.abs() + 64 * md + 16 / rstd))[:, 0]), (rstd[:, 0], 40 * U * rstd[:, 0])]
     if dy is None:
         return out
     dy = dy.double()
