@@ -16,6 +16,12 @@
 // GEMM, with dH read and dY written in the epilogue, rounded once.
 //
 // A few rows (single tokens): the 2-bit codes are read, an eighth of T's bytes.  See glu_codes below.
+//
+// 32768 x 4096 x 6144 (3.3 TFLOP): 1.64 ms, 2010 TFLOP/s, above cuBLAS's measured burst; with the factors stored
+// 1.75 ms, and the product with dH 0.30 ms (0.92 of the copy rate).  8192 x 512 x 1360: 24 us, with factors 29, the
+// gradient recomputed 35, where the products alone would take 12: eight of it before and after the tiles (no
+// launch overlaps another), then 4.6 rounds of tiles in five whose epilogue (stores of 32 bytes a lane, rows 2 N
+// apart) takes longer than their 512-deep products.  Copying dH ahead of the products changed nothing.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -417,6 +423,9 @@ using GluOneNarrow = GluCfg<1, 64, 6>;
 // written to shared memory.  Element order within an MMA is free as long as both operands agree:
 // lane (g, t) = (lane / 4, lane % 4) reads the words of 16 columns 16 g.. at the four weight rows
 // 4 t.. of a block of 16 rows, and MMA j takes its columns 16 g + j and 16 g + j + 8.
+//
+// What bounds them is mma.sync itself, at 25 cycles an SM quarter for 256 weights: 1 x 4096 x 6144 7.6 us, 8 rows 8.8,
+// 16 rows (two MMAs for each operand) 12.2, of which a launch is 3.6 and the codes' bytes would be 1.9.
 //
 // A block has 128 outputs: half of its eight warps take the gate's 128 columns, half the value's, and share
 // the weight's rows; where there are fewer blocks than SMs, the blocks of a cluster share them too.

@@ -21,6 +21,13 @@
 //
 // The gradient's blocks stay for many rows and keep the sums of their columns in registers; each
 // block stores its sums once, and a second launch adds the blocks' in a fixed order.
+//
+// 32768 x 4096 in bf16: forward 99 us, 0.80 of the measured copy rate, gradient 137 us, 0.87; 65536 x 1024 56 and
+// 67 us (0.71, 0.88).  Row by row, each block waiting for its one row: 135 and 311, 69 and 132 us.  The
+// forward uses two thirds of the issue slots: three passes over a row's words, its floor with them in
+// registers is no lower (the barriers then stand alone).  8192 x 512 from fp32: 5.3 and 17 us, of which two
+// launches in turn, the blocks' 2.5 MB of sums and two rounds of rows; floors 3.7 and 6.2.  Odd widths in bf16
+// go element by element: 32768 x 4095 203 and 266 us.
 #include <algorithm>
 #include <cmath>
 
