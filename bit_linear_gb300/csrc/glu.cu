@@ -58,9 +58,9 @@ __device__ __forceinline__ F2 each(F2 x, float (*f)(float)) {
 }
 __device__ __forceinline__ float magnitude(float x) { return fabsf(x); }
 __device__ __forceinline__ float positive(float x) { return x < 0.f ? 0.f : x; }   // NaN passes
-__device__ __forceinline__ float bounded(float x) {                               // by 126; NaN passes
+__device__ __forceinline__ float bounded(float x) {                               // by 127; NaN passes
     float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(126.f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(127.f));
     return y;
 }
 
@@ -82,15 +82,17 @@ __device__ __forceinline__ void activate(F2 g, F2& a, F2& d) {
         p = fma2(p, t, both(0.5f * 1.421413741f));
         p = fma2(p, t, both(0.5f * -0.284496736f));
         p = fma2(p, t, both(0.5f * 0.254829592f));
-        const F2 half = fma2(mul2(p, t), mul2(e, both(-1.f)), both(0.5f));   // Phi(|g|) - 1/2
-        float h0, h1, g0, g1;
-        split(half, h0, h1);
+        const F2 tail = mul2(mul2(p, t), e), rest = fma2(tail, both(-1.f), both(1.f));   // Phi(-|g|), Phi(|g|)
+        float t0, t1, r0, r1, g0, g1;
+        split(tail, t0, t1);
+        split(rest, r0, r1);
         split(g, g0, g1);
-        const F2 cdf = add2(pair(copysignf(h0, g0), copysignf(h1, g1)), both(0.5f));
+        const F2 cdf = pair(g0 < 0.f ? t0 : r0, g1 < 0.f ? t1 : r1);
         a = mul2(g, cdf);
         if (D) d = fma2(mul2(g, both(0.39894228f)), e, cdf);
     } else {
-        // s = 1 / (1 + e) and its complement e / (1 + e); e = exp(-g) kept finite
+        // s = 1 / (1 + e) and its complement e / (1 + e); e = exp(-g) kept finite.  At its bound s is 0 (the
+        // reciprocal, 2^-127, is flushed), so that no gate, however far, leaves a product with it.
         const F2 e = each(each(mul2(g, both(-1.44269504f)), bounded), pow2);
         const F2 s = each(add2(e, both(1.f)), reciprocal), c = mul2(e, s);
         if constexpr (ACT == TERN_ACT_SIGMOID) {

@@ -22,12 +22,13 @@
 // The gradient's blocks stay for many rows and keep the sums of their columns in registers; each
 // block stores its sums once, and a second launch adds the blocks' in a fixed order.
 //
-// 32768 x 4096 in bf16: forward 99 us, 0.80 of the measured copy rate, gradient 137 us, 0.87; 65536 x 1024 56 and
-// 67 us (0.71, 0.88).  Row by row, each block waiting for its one row: 135 and 311, 69 and 132 us.  The
-// forward uses two thirds of the issue slots: three passes over a row's words, its floor with them in
-// registers is no lower (the barriers then stand alone).  8192 x 512 from fp32: 5.3 and 17 us, of which two
-// launches in turn, the blocks' 2.5 MB of sums and two rounds of rows; floors 3.7 and 6.2.  Odd widths in bf16
-// go element by element: 32768 x 4095 203 and 266 us.
+// 32768 x 4096 in bf16: forward 99 us, 0.80 of the measured copy rate, gradient 137 us, 0.87; 65536 x 1024 49 and
+// 65 us (0.80, 0.91); from fp32 to bf16 124 and 237 us (0.96, 0.83), in fp32 alone 245 (0.97) for the gradient.
+// Row by row, each block waiting for its one row: 124 and 308 in bf16, 124 and 367 from fp32.  The forward in
+// bf16 uses two thirds of the issue slots: three passes over a row's words; with them in registers the
+// barriers stand alone.  8192 x 512 from fp32: 5.0 and 13.3 us, of which two launches in turn and two rounds of
+// rows; floors 3.7 and 6.2.  Odd widths in bf16 go element by element: 32768 x 4095 203 and 266 us (aligned
+// words with a first and last run of which a part is others' took as long or longer).
 #include <algorithm>
 #include <cmath>
 
@@ -379,58 +380,63 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait_all_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-// A thread takes 16 elements of a row, in two runs of eight.  Blocks that an SM holds:
-constexpr int pair_blocks(int T, bool bwd) { return T == 64 ? 8 : T <= 128 ? (bwd ? 4 : 6) : T == 256 ? (bwd ? 2 : 3) : 1; }
+// A thread takes 16 elements of a row, in runs of a 16-byte word: eight of bf16; four where there is fp32
+// (neighbouring threads' words are neighbours then; with runs of eight, each of two words, a 32-byte piece came
+// over in halves: 32768 x 4096 from fp32 to bf16, gradient 297 us for 237, forward, row by row, 187 for 124).
+// The forward's blocks that an SM holds:
+constexpr int pair_blocks(int T) { return T == 64 ? 8 : T <= 128 ? 6 : T == 256 ? 3 : 1; }
 constexpr int kPairWidest = 8192;          // channels of a row that 512 threads take
 constexpr size_t kPairSpace = 216 << 10;   // shared memory for it
+template <class TX, class TY>
+constexpr int kRun = kElem<TX> + kElem<TY> == 4 ? 8 : 4;
 
 template <int B>
 __device__ __forceinline__ void copy_small(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(B) : "memory");
 }
 
-// A thread's copies of eight elements: one word of bf16, two of fp32, THREADS words apart.  They are
-// copied in words of V elements (two of bf16 in four bytes, for instance), `pairs` of them there are.
-template <class T, int THREADS, int V>
-struct Eight {
-    static constexpr int WORDS = kElem<T> == 2 ? 1 : 2;
-    static __device__ __forceinline__ void ask(uint4* to, const T* from, int pairs) {
-#pragma unroll
-        for (int h = 0; h < WORDS; ++h) {
-            constexpr int EACH = 8 / WORDS;   // elements of a word
-            const uint32_t at = ptx::smem_u32(to + h * THREADS);
-            if constexpr (V == 8) {
-                copy16(at, from + h * EACH);
-            } else {
-#pragma unroll
-                for (int i = 0; i < EACH / 2; ++i)
-                    if (h * (EACH / 2) + i < pairs) copy_small<2 * kElem<T>>(at + i * 2 * kElem<T>, from + h * EACH + 2 * i);
-            }
-        }
-    }
-    static __device__ __forceinline__ void get(const uint4* from, F2 (&x)[4]) {
-#pragma unroll
-        for (int h = 0; h < WORDS; ++h) {
-            const uint4 u = from[h * THREADS];
-            if constexpr (WORDS == 1) {
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-            } else {
-                x[2 * h] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
-                x[2 * h + 1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
-            }
-        }
-    }
-    static __device__ __forceinline__ void put(T* to, const F2 (&x)[4], int pairs) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split(x[i], v[2 * i], v[2 * i + 1]);
-        if constexpr (V == 8) {
-            store_as<T, 8>(to, v);
+// A thread's run of RUN elements, one word in shared memory.  WHOLE: copied and stored as such; else two
+// elements at a time, `pairs` of which there are.
+template <class T, int RUN, bool WHOLE>
+struct Run {
+    static constexpr int BYTES = RUN * kElem<T>, PAIRS = RUN / 2;
+    static_assert(BYTES == 8 || BYTES == 16, "a word");
+    static __device__ __forceinline__ void ask(const uint8_t* to, const T* from, int pairs) {
+        const uint32_t at = ptx::smem_u32(to);
+        if constexpr (WHOLE && BYTES == 16) {
+            copy16(at, from);
+        } else if constexpr (WHOLE) {
+            copy_small<8>(at, from);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < PAIRS; ++i)
+                if (i < pairs) copy_small<2 * kElem<T>>(at + i * 2 * kElem<T>, from + 2 * i);
+        }
+    }
+    static __device__ __forceinline__ void get(const uint8_t* from, F2 (&x)[PAIRS]) {
+        uint32_t w[BYTES / 4];
+        if constexpr (BYTES == 16) {
+            const uint4 u = *reinterpret_cast<const uint4*>(from);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(from);
+            w[0] = u.x, w[1] = u.y;
+        }
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            if constexpr (kElem<T> == 2) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            else x[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        }
+    }
+    static __device__ __forceinline__ void put(T* to, const F2 (&x)[PAIRS], int pairs) {
+        float v[RUN];
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) split(x[i], v[2 * i], v[2 * i + 1]);
+        if constexpr (WHOLE) {
+            store_as<T, RUN>(to, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
                 const float two[2] = {v[2 * i], v[2 * i + 1]};
                 if (i < pairs) store_as<T, 2>(to + 2 * i, two);
             }
@@ -443,69 +449,70 @@ __device__ __forceinline__ float sum_of(F2 x) {
     split(x, a, b);
     return a + b;
 }
-// Eight parameters of the columns from c, of which `pairs` pairs there are, or a value in place of them.
-template <int V>
-__device__ __forceinline__ void params(const float* p, int c, int pairs, float other, F2 (&x)[4]) {
+// A run's parameters, columns from c of which `pairs` pairs there are, or a value in place of them.
+template <int RUN, bool WHOLE>
+__device__ __forceinline__ void params(const float* p, int c, int pairs, float other, F2 (&x)[RUN / 2]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = both(other);
+    for (int i = 0; i < RUN / 2; ++i) x[i] = both(other);
     if (!p) return;
-    if constexpr (V == 8) {
+    if constexpr (WHOLE) {
         if (pairs > 0) {
-            const auto raw = load_raw<float, 8>(p + c);
+            const auto raw = load_raw<float, RUN>(p + c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = pair(raw_at<float, 8>(raw, 2 * i), raw_at<float, 8>(raw, 2 * i + 1));
+            for (int i = 0; i < RUN / 2; ++i) x[i] = pair(raw_at<float, RUN>(raw, 2 * i), raw_at<float, RUN>(raw, 2 * i + 1));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RUN / 2; ++i)
             if (i < pairs) x[i] = pair(__ldg(p + c + 2 * i), __ldg(p + c + 2 * i + 1));
     }
 }
 
 template <class TX, class TY, int T, int R>
-__global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(const __grid_constant__ NormArgs a) {
-    using X = Eight<TX, T * R, 8>;
-    extern __shared__ uint4 ring[];   // [2 turns][2 rows][2 runs][X::WORDS][T R]
+__global__ void __launch_bounds__(T * R, pair_blocks(T)) norm_fwd_pairs(const __grid_constant__ NormArgs a) {
+    constexpr int RUN = kRun<TX, TY>, RUNS = 16 / RUN, PAIRS = RUN / 2;
+    using X = Run<TX, RUN, true>;
+    extern __shared__ __align__(16) uint8_t ring[];   // [2 turns][2 rows][RUNS][T R] words
     __shared__ float sums[2][4 * ((T + 31) / 32)];
     ptx::pdl_trigger();
     const int t = threadIdx.x % T;
     const int64_t step = 2 * static_cast<int64_t>(gridDim.x) * R;
     int64_t row = 2 * (static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / T);
     const int ahead = T < 32 ? 2 * (threadIdx.x % 32 / T) : 0;   // of the warp's first row: a warp stays together
-    auto place = [&](int turn, int which, int j) { return ring + ((turn * 2 + which) * 2 + j) * X::WORDS * T * R + threadIdx.x; };
+    auto place = [&](int turn, int which, int j) { return ring + (((turn * 2 + which) * RUNS + j) * T * R + threadIdx.x) * X::BYTES; };
     auto ask = [&](int64_t of, int turn) {
 #pragma unroll
         for (int which = 0; which < 2; ++which)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = (j * T + t) * 8;
-                if (of + which < a.n && c < a.D) X::ask(place(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c, 4);
+            for (int j = 0; j < RUNS; ++j) {
+                const int c = (j * T + t) * RUN;
+                if (of + which < a.n && c < a.D) X::ask(place(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c, PAIRS);
             }
         copies_close();
     };
     ptx::pdl_wait();
     ask(row, 0);
     ask(row + step, 1);
-    F2 w[2][4], b[2][4];
+    F2 w[RUNS][PAIRS], b[RUNS][PAIRS];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int c = (j * T + t) * 8;
-        params<8>(a.weight, c, c < a.D ? 4 : 0, 1.f, w[j]);
-        params<8>(a.bias, c, c < a.D ? 4 : 0, 0.f, b[j]);
+    for (int j = 0; j < RUNS; ++j) {
+        const int c = (j * T + t) * RUN;
+        params<RUN, true>(a.weight, c, c < a.D ? PAIRS : 0, 1.f, w[j]);
+        params<RUN, true>(a.bias, c, c < a.D ? PAIRS : 0, 0.f, b[j]);
     }
     for (int turn = 0; row - ahead < a.n; row += step, turn ^= 1) {
         copies_wait_all_but_one();
-        F2 x[4];
+        F2 x[PAIRS];
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             F2 u = both(0.f);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if ((j * T + t) * 8 < a.D) {
+            for (int j = 0; j < RUNS; ++j) {
+                if ((j * T + t) * RUN < a.D) {
                     X::get(place(turn, which, j), x);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u = add2(u, x[i]);
+                    for (int i = 0; i < PAIRS; ++i) u = add2(u, x[i]);
                 }
             }
             s[which] = sum_of(u);
@@ -518,11 +525,11 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
             F2 u = both(0.f), v = both(0.f);
             const F2 shift = both(-mean[which]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if ((j * T + t) * 8 < a.D) {
+            for (int j = 0; j < RUNS; ++j) {
+                if ((j * T + t) * RUN < a.D) {
                     X::get(place(turn, which, j), x);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < PAIRS; ++i) {
                         const F2 d = add2(x[i], shift);
                         u = add2(u, d);
                         v = fma2(d, d, v);
@@ -544,13 +551,13 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
             TY* y = static_cast<TY*>(a.y) + (row + which) * a.ld_y;
             const F2 shift = both(-mean[which]), rest = both(-delta), scale = both(rstd);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = (j * T + t) * 8;
+            for (int j = 0; j < RUNS; ++j) {
+                const int c = (j * T + t) * RUN;
                 if (c < a.D) {
                     X::get(place(turn, which, j), x);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = fma2(mul2(add2(add2(x[i], shift), rest), scale), w[j][i], b[j][i]);
-                    Eight<TY, T * R, 8>::put(y + c, x, 4);
+                    for (int i = 0; i < PAIRS; ++i) x[i] = fma2(mul2(add2(add2(x[i], shift), rest), scale), w[j][i], b[j][i]);
+                    Run<TY, RUN, true>::put(y + c, x, PAIRS);
                 }
             }
         }
@@ -558,31 +565,62 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, false)) norm_fwd_pairs(c
     }
 }
 
-template <class TX, class TY, int T, int R, int V>
-__global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(const __grid_constant__ NormArgs a) {
-    using X = Eight<TX, T * R, V>;
-    using Y = Eight<TY, T * R, V>;
-    constexpr int ROW = 2 * (X::WORDS + Y::WORDS) * T * R;   // words of a row of x and one of dy
-    extern __shared__ uint4 ring[];                          // [2 turns][2 rows] of them
-    __shared__ float sums[2][6 * ((T + 31) / 32)];
-    ptx::pdl_trigger();
+// As row_sums, for T neighbours of a block of T R threads; r: which of the R.
+template <int T, int R, int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float* s, int r) {
+    if constexpr (T <= 32 || R == 1) {
+        row_sums<T, N>(v, s);
+    } else {
+        constexpr int W = T / 32;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+        s += r * N * W;
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i * W + threadIdx.x % T / 32] = v[i];
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + r), "n"(T) : "memory");
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float t = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) t += s[i * W + w];
+            v[i] = t;
+        }
+    }
+}
+
+// The gradient: one block an SM, of R rows' threads that go their own ways (barriers of T threads), so that
+// there are as few sums of columns to store as SMs (2048 x 2048 bf16 11.6 us, with four blocks an SM 12.4; 4096 x
+// 512 7.3, 8.3).
+template <class TX, class TY, int T, int R, bool WHOLE>
+__global__ void __launch_bounds__(T * R, 1) norm_bwd_pairs(const __grid_constant__ NormArgs a) {
+    constexpr int RUN = kRun<TX, TY>, RUNS = 16 / RUN, PAIRS = RUN / 2;
+    using X = Run<TX, RUN, WHOLE>;
+    using Y = Run<TY, RUN, WHOLE>;
+    constexpr int ROW = RUNS * (X::BYTES + Y::BYTES) * T * R;   // of a row of x and one of dy, each as [RUNS][T R] words
+    extern __shared__ __align__(16) uint8_t ring[];             // [2 turns][2 rows] of them
+    __shared__ float sums[2][6 * R * ((T + 31) / 32)];
+    constexpr int SUB = T < 32 ? 32 / T : 1;                 // rows of a warp
     const int t = threadIdx.x % T, r = static_cast<int>(threadIdx.x) / T;
     const int64_t step = 2 * static_cast<int64_t>(gridDim.x) * R;
-    int64_t row = 2 * (static_cast<int64_t>(blockIdx.x) * R + r);
-    const int ahead = T < 32 ? 2 * (threadIdx.x % 32 / T) : 0;   // of the warp's first row: a warp stays together
-    auto place_x = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + j * X::WORDS * T * R + threadIdx.x; };
-    auto place_d = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + (2 * X::WORDS + j * Y::WORDS) * T * R + threadIdx.x; };
-    int pairs[2];   // of each run, that lie in the row
+    const int ahead = 2 * (r % SUB);   // of the warp's first row: a warp stays together
+    int64_t row = 2 * SUB * (static_cast<int64_t>(r / SUB) * gridDim.x + blockIdx.x) + ahead;
+    auto place_x = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + (j * T * R + threadIdx.x) * X::BYTES; };
+    auto place_d = [&](int turn, int which, int j) { return ring + (turn * 2 + which) * ROW + (RUNS * X::BYTES + j * Y::BYTES) * T * R + threadIdx.x * Y::BYTES; };
+    int pairs[RUNS];   // of each run, that lie in the row
 #pragma unroll
-    for (int j = 0; j < 2; ++j) pairs[j] = min(4, max(0, (a.D - (j * T + t) * 8) / 2));
-    const auto in_row = [&](int j, int i) { return V == 8 ? pairs[j] > 0 : i < pairs[j]; };
+    for (int j = 0; j < RUNS; ++j) pairs[j] = min(PAIRS, max(0, (a.D - (j * T + t) * RUN) / 2));
+    const auto in_row = [&](int j, int i) { return WHOLE ? pairs[j] > 0 : i < pairs[j]; };
     float mean[2], rstd[2], mean_next[2] = {0.f, 0.f}, rstd_next[2] = {0.f, 0.f};
     auto ask = [&](int64_t of, int turn) {
 #pragma unroll
         for (int which = 0; which < 2; ++which)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = (j * T + t) * 8;
+            for (int j = 0; j < RUNS; ++j) {
+                const int c = (j * T + t) * RUN;
                 if (of + which < a.n && pairs[j] > 0) {
                     X::ask(place_x(turn, which, j), static_cast<const TX*>(a.x) + (of + which) * a.ld_x + c, pairs[j]);
                     Y::ask(place_d(turn, which, j), static_cast<const TY*>(a.dy) + (of + which) * a.ld_dy + c, pairs[j]);
@@ -602,17 +640,17 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
     ask(row, 0);
     ask(row + step, 1);
     stats(row, mean, rstd);
-    F2 w[2][4], dw[2][4], db[2][4];
+    F2 w[RUNS][PAIRS], dw[RUNS][PAIRS], db[RUNS][PAIRS];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        params<V>(a.weight, (j * T + t) * 8, pairs[j], 1.f, w[j]);
+    for (int j = 0; j < RUNS; ++j) {
+        params<RUN, WHOLE>(a.weight, (j * T + t) * RUN, pairs[j], 1.f, w[j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = both(0.f);
+        for (int i = 0; i < PAIRS; ++i) dw[j][i] = db[j][i] = both(0.f);
     }
     for (int turn = 0; row - ahead < a.n; row += step, turn ^= 1) {
         stats(row + step, mean_next, rstd_next);
         copies_wait_all_but_one();
-        F2 x[4], d[4];
+        F2 x[PAIRS], d[PAIRS];
         float s[6];   // a row's sums of g, g (x - mean), x - mean
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
@@ -620,12 +658,12 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
             const F2 shift = both(-mean[which]);
             if (row + which < a.n) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < RUNS; ++j) {
                     if (pairs[j] > 0) {
                         X::get(place_x(turn, which, j), x);
                         Y::get(place_d(turn, which, j), d);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < PAIRS; ++i) {
                             if (!in_row(j, i)) continue;
                             const F2 e = add2(x[i], shift), g = mul2(d[i], w[j][i]);
                             u0 = add2(u0, g);
@@ -637,7 +675,7 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
             }
             s[3 * which] = sum_of(u0), s[3 * which + 1] = sum_of(u1), s[3 * which + 2] = sum_of(u2);
         }
-        row_sums<T, 6>(s, sums[turn]);
+        group_sums<T, R, 6>(s, sums[turn], r);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             if (row + which >= a.n) break;
@@ -647,13 +685,13 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
             const F2 shift = both(-mean[which]), rest = both(-delta), scale = both(rstd[which]);
             TX* dx = static_cast<TX*>(a.y) + (row + which) * a.ld_y;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = (j * T + t) * 8;
+            for (int j = 0; j < RUNS; ++j) {
+                const int c = (j * T + t) * RUN;
                 if (pairs[j] > 0) {
                     X::get(place_x(turn, which, j), x);
                     Y::get(place_d(turn, which, j), d);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < PAIRS; ++i) {
                         if (!in_row(j, i)) continue;
                         const F2 xhat = mul2(add2(add2(x[i], shift), rest), scale);
                         dw[j][i] = fma2(d[i], xhat, dw[j][i]);
@@ -668,49 +706,49 @@ __global__ void __launch_bounds__(T * R, pair_blocks(T, true)) norm_bwd_pairs(co
 #pragma unroll
         for (int which = 0; which < 2; ++which) mean[which] = mean_next[which], rstd[which] = rstd_next[which];
     }
+    ptx::pdl_trigger();   // not before: blocks that wait would take registers from rows (1048576 x 64 88, 76 us)
     if (!a.part) return;
-    float v[16], u[16];
+    float v[2][16];   // the weight's and the bias's
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < RUNS; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            split(dw[j][i], v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-            split(db[j][i], u[8 * j + 2 * i], u[8 * j + 2 * i + 1]);
+        for (int i = 0; i < PAIRS; ++i) {
+            split(dw[j][i], v[0][RUN * j + 2 * i], v[0][RUN * j + 2 * i + 1]);
+            split(db[j][i], v[1][RUN * j + 2 * i], v[1][RUN * j + 2 * i + 1]);
         }
-    if constexpr (R > 1) {   // the block's rows side by side, added in order in the ring's place
-        float* cols = reinterpret_cast<float*>(ring);   // [2][16][T]
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncthreads();
-        for (int k = 0; k < R; ++k) {
-            if (r == k) {
+    // Rows side by side, added in a fixed order: a warp's by lanes, the block's through the ring's place
+    if constexpr (T < 32) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int at = e * T + t;
-                    if (k > 0) v[e] += cols[at], u[e] += cols[16 * T + at];
-                    cols[at] = v[e], cols[16 * T + at] = u[e];
-                }
-            }
-            __syncthreads();
-        }
-        if (r != R - 1) return;
+        for (int which = 0; which < 2; ++which)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+#pragma unroll
+                for (int d = T; d < 32; d *= 2) v[which][e] += __shfl_xor_sync(0xffffffffu, v[which][e], d);
     }
-    float* pw = a.part + static_cast<int64_t>(blockIdx.x) * a.D;
-    float* pb = pw + static_cast<int64_t>(gridDim.x) * a.D;
+    constexpr int GROUPS = R / SUB;
+    float* cols = reinterpret_cast<float*>(ring);   // [GROUPS][2][16][T]
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    if (r % SUB == 0) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int c = (j * T + t) * 8;
-        if (c < a.D) {
-            float v8[8], u8[8];
+        for (int e = 0; e < 32; ++e) cols[((r / SUB) * 32 + e) * T + t] = v[e / 16][e % 16];
+    }
+    __syncthreads();
+    for (int unit = threadIdx.x; unit < 8 * T; unit += T * R) {   // four columns of one of the two sums
+        const int four = unit / T, of = unit % T;                // four = (which, run, part of it)
+        const int c = ((four & 3) * 4 / RUN * T + of) * RUN + (four & 3) * 4 % RUN;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v8[i] = v[8 * j + i], u8[i] = u[8 * j + i];
-            if constexpr (V == 8) {
-                store_as<float, 8>(pw + c, v8);
-                store_as<float, 8>(pb + c, u8);
-            } else {
+        for (int k = 0; k < GROUPS; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i < a.D) pw[c + i] = v8[i], pb[c + i] = u8[i];
-            }
+            for (int i = 0; i < 4; ++i) x[i] += cols[(k * 32 + four * 4 + i) * T + of];
+        float* to = a.part + (static_cast<int64_t>(four >> 2) * gridDim.x + blockIdx.x) * a.D + c;
+        if constexpr (WHOLE) {
+            if (c < a.D) store_as<float, 4>(to, x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + i < a.D) to[i] = x[i];
         }
     }
 }
@@ -721,7 +759,7 @@ constexpr int kWidest = 16384;   // channels that a block of 1024 threads holds
 // Threads a row takes at 16 elements each: part of a warp (where its elements come eight at a time), a
 // warp, or a block of 64 to 1024.
 int row_threads(int64_t D, int V) {
-    int t = V == 8 ? 8 : 32;
+    int t = V >= 4 ? 8 : 32;
     while (static_cast<int64_t>(t) * 16 < D) t *= 2;
     return t;
 }
@@ -748,9 +786,9 @@ int pick_rows(const NormArgs& a, int* parts, cudaStream_t s) {
     *parts = grid;
     switch (T) {
     case 8:
-        if constexpr (!BWD && V == 8) return launch_rows<BWD, TX, TY, 8, rows_beside(8), V>(a, grid, s);
+        if constexpr (!BWD && V >= 4) return launch_rows<BWD, TX, TY, 8, rows_beside(8), V>(a, grid, s);
     case 16:
-        if constexpr (!BWD && V == 8) return launch_rows<BWD, TX, TY, 16, rows_beside(16), V>(a, grid, s);
+        if constexpr (!BWD && V >= 4) return launch_rows<BWD, TX, TY, 16, rows_beside(16), V>(a, grid, s);
     case 32: return launch_rows<BWD, TX, TY, 32, rows_beside(32), V>(a, grid, s);
     case 64: return launch_rows<BWD, TX, TY, 64, 1, V>(a, grid, s);
     case 128: return launch_rows<BWD, TX, TY, 128, 1, V>(a, grid, s);
@@ -760,35 +798,48 @@ int pick_rows(const NormArgs& a, int* parts, cudaStream_t s) {
     }
 }
 
-template <bool BWD, class TX, class TY, int T, int R, int V>
+// Rows side by side in the gradient's blocks: whole warps, up to 512 threads and the shared memory.
+template <class TX, class TY, int T>
+constexpr int bwd_beside() {
+    const int each = 4 * 16 * (kElem<TX> + kElem<TY>);   // bytes of a thread
+    const int threads = std::min(512, static_cast<int>(kPairSpace) / each) / std::max(T, 32) * std::max(T, 32);
+    return threads / T;
+}
+
+template <bool BWD, class TX, class TY, int T, bool WHOLE>
 int launch_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
-    constexpr size_t smem = 8u * T * R * 16 * (Eight<TX, 1, V>::WORDS + (BWD ? Eight<TY, 1, V>::WORDS : 0));
-    if constexpr (smem > kPairSpace) {
-        return pick_rows<BWD, TX, TY, V>(a, parts, s);
+    if constexpr (BWD) {
+        constexpr int R = bwd_beside<TX, TY, T>(), SUB = T < 32 ? 32 / T : 1;
+        if constexpr (R == 0) {
+            return pick_rows<BWD, TX, TY, WHOLE ? kRun<TX, TY> : 2>(a, parts, s);
+        } else {
+            constexpr int smem = 4 * 16 * T * R * (kElem<TX> + kElem<TY>);
+            static_assert(smem >= R / SUB * 32 * T * 4, "the columns' sums");
+            *parts = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(a.n) + 2 * SUB - 1) / (2 * SUB), num_sms));
+            TERN_CUDA_TRY(cudaFuncSetAttribute(norm_bwd_pairs<TX, TY, T, R, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+            return launch_pdl(norm_bwd_pairs<TX, TY, T, R, WHOLE>, dim3(*parts), dim3(T * R), smem, s, a);
+        }
     } else {
+        constexpr int R = rows_beside(T);
+        constexpr size_t smem = 4u * 16 * T * R * kElem<TX>;
         const int64_t pairs = (static_cast<int64_t>(a.n) + 2 * R - 1) / (2 * R);
-        const int blocks = std::min(pair_blocks(T, BWD), static_cast<int>(kPairSpace / smem));
-        const int grid = static_cast<int>(std::min({pairs, static_cast<int64_t>(num_sms) * blocks, static_cast<int64_t>(kPartMax)}));
-        *parts = grid;
-        auto kernel = [] {
-            if constexpr (BWD) return norm_bwd_pairs<TX, TY, T, R, V>;
-            else return norm_fwd_pairs<TX, TY, T, R>;
-        }();
-        if (smem > 40 * 1024) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-        return launch_pdl(kernel, dim3(grid), dim3(T * R), smem, s, a);
+        const int blocks = std::min(pair_blocks(T), static_cast<int>(kPairSpace / smem));
+        const int grid = static_cast<int>(std::min(pairs, static_cast<int64_t>(num_sms) * blocks));
+        if (smem > 40 * 1024) TERN_CUDA_TRY(cudaFuncSetAttribute(norm_fwd_pairs<TX, TY, T, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+        return launch_pdl(norm_fwd_pairs<TX, TY, T, R>, dim3(grid), dim3(T * R), smem, s, a);
     }
 }
 
-template <bool BWD, class TX, class TY, int V>
+template <bool BWD, class TX, class TY, bool WHOLE>
 int pick_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     switch (row_threads(a.D, 8)) {
-    case 8: return launch_pairs<BWD, TX, TY, 8, rows_beside(8), V>(a, num_sms, parts, s);
-    case 16: return launch_pairs<BWD, TX, TY, 16, rows_beside(16), V>(a, num_sms, parts, s);
-    case 32: return launch_pairs<BWD, TX, TY, 32, rows_beside(32), V>(a, num_sms, parts, s);
-    case 64: return launch_pairs<BWD, TX, TY, 64, 1, V>(a, num_sms, parts, s);
-    case 128: return launch_pairs<BWD, TX, TY, 128, 1, V>(a, num_sms, parts, s);
-    case 256: return launch_pairs<BWD, TX, TY, 256, 1, V>(a, num_sms, parts, s);
-    default: return launch_pairs<BWD, TX, TY, 512, 1, V>(a, num_sms, parts, s);
+    case 8: return launch_pairs<BWD, TX, TY, 8, WHOLE>(a, num_sms, parts, s);
+    case 16: return launch_pairs<BWD, TX, TY, 16, WHOLE>(a, num_sms, parts, s);
+    case 32: return launch_pairs<BWD, TX, TY, 32, WHOLE>(a, num_sms, parts, s);
+    case 64: return launch_pairs<BWD, TX, TY, 64, WHOLE>(a, num_sms, parts, s);
+    case 128: return launch_pairs<BWD, TX, TY, 128, WHOLE>(a, num_sms, parts, s);
+    case 256: return launch_pairs<BWD, TX, TY, 256, WHOLE>(a, num_sms, parts, s);
+    default: return launch_pairs<BWD, TX, TY, 512, WHOLE>(a, num_sms, parts, s);
     }
 }
 
@@ -815,16 +866,17 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaS
     if (a.n > 0) {
         constexpr int ex = kElem<TX>, ey = kElem<TY>;
         int st;
-        // Pairs of rows, from a pair for each SM on: the gradient (32768 x 4096 bf16 137 us, row by row 311; 64 x 4096
-        // 6.8, 5.7) and the forward from bf16 to bf16 (32768 x 4096 99 us, 135; 65536 x 1024 56, 69; from fp32
-        // row by row is faster: 32768 x 4096 187 us, 227).
-        constexpr bool PAIRS = BWD || (ex == 2 && ey == 2);
-        const bool pairs = a.D <= kPairWidest && a.n > 2 * num_sms * rows_beside(row_threads(a.D, 8));
-        if (all_allow(a, BWD, 8, ex, ey)) {
-            if constexpr (PAIRS) st = pairs ? pick_pairs<BWD, TX, TY, 8>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 8>(a, &parts, s);
-            else st = pick_rows<BWD, TX, TY, 8>(a, &parts, s);
+        // Pairs of rows where there are some for each SM: the gradient (32768 x 4096 bf16 137 us, row by row 308; 64 x
+        // 4096 7.2, 5.7; 304 x 4096 7.8, 8.6; 600 x 1024 6.3, 7.6) and the forward from bf16 to bf16 (32768 x 4096 99 us, 124;
+        // 65536 x 1024 49, 69) or of rows that a block of 512 threads takes (32768 x 8192 from fp32 251, 305).  Else
+        // the forward with fp32 is near the copy rate row by row (32768 x 4096 to bf16 124 us, 136 by pairs).
+        constexpr int V = kRun<TX, TY>;
+        const int T = row_threads(a.D, 8);
+        const bool pairs = a.D <= kPairWidest && (BWD || V == 8 || T == 512) && a.n > num_sms * (BWD && T >= 256 ? 1 : 2 * rows_beside(T));
+        if (all_allow(a, BWD, V, ex, ey)) {
+            st = pairs ? pick_pairs<BWD, TX, TY, true>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, V>(a, &parts, s);
         } else if (all_allow(a, BWD, 2, ex, ey)) {
-            if constexpr (BWD) st = pairs ? pick_pairs<BWD, TX, TY, 2>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, &parts, s);
+            if constexpr (BWD) st = pairs ? pick_pairs<BWD, TX, TY, false>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, &parts, s);
             else st = pick_rows<BWD, TX, TY, 2>(a, &parts, s);
         } else {
             st = pick_rows<BWD, TX, TY, 1>(a, &parts, s);

@@ -172,6 +172,36 @@ def test_extreme_gates(cuda_lib):
                 _near(got[rest, N:], fu[0][rest], fu[1][rest], 1, act)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid"])
+def test_gates_of_any_size(cuda_lib, act):
+    """Gates of +-1e5 to +-1e38, exact in fp32: act is 0 or g (sigmoid: 0 or 1), act' 0 or 1 (sigmoid: 0).
+    One rounding, and 2^-20 for the reciprocal and its product."""
+    bl, N = cuda_lib, 64
+    for M in (4, 40):
+        X = torch.zeros(M, 16, device="cuda", dtype=torch.bfloat16)
+        X[0::2, 0], X[1::2, 0], X[:, 1] = 1.0, -1.0, 1.0
+        q = torch.zeros(16, 2 * N, dtype=torch.int8, device="cuda")
+        q[0, :N] = 7
+        q[1, N:] = 7
+        scale = torch.cat([torch.logspace(5, 38, N, device="cuda"), torch.ones(N, device="cuda")])
+        tiles = _tiles(bl, q, scale)
+        H, pair = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(M, 2 * N, dtype=torch.bfloat16, device="cuda")
+        bl.tern_glu_fwd(X, tiles, scale, H, act=act)
+        outs = [(H, None)]
+        H2 = torch.empty_like(H)
+        bl.tern_glu_fwd(X, tiles, scale, H2, saved=pair, act=act)
+        outs.append((H2, pair))
+        value = torch.ones(N, device="cuda").double() if act == "sigmoid" else scale[:N].double()
+        slope = 0.0 if act == "sigmoid" else 1.0
+        for h, f in outs:
+            assert torch.all(h[1::2].double().abs() <= 1e-37)
+            assert torch.all((h[0::2].double() - value).abs() <= value * (H8 + 2.0 ** -20) * (1 + H8))
+            if f is not None:
+                assert torch.all(f[1::2].double().abs() <= 1e-37)
+                assert torch.all((f[0::2, :N].double() - slope).abs() <= H8 + 2.0 ** -20)
+                assert torch.equal(f[0::2, N:], h[0::2])
+
+
 def test_same_bits_streams_and_graphs(cuda_lib):
     bl = cuda_lib
     for M in (1, 16, 200):
