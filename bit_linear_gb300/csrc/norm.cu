@@ -22,8 +22,8 @@
 // The gradient's blocks stay for many rows and keep the sums of their columns in registers; each
 // block stores its sums once, and a second launch adds the blocks' in a fixed order.
 //
-// 32768 x 4096 in bf16: forward 99 us, 0.80 of the measured copy rate, gradient 137 us, 0.87; 65536 x 1024 49 and
-// 65 us (0.80, 0.91); from fp32 to bf16 124 and 237 us (0.96, 0.83), in fp32 alone 245 (0.97) for the gradient.
+// 32768 x 4096 in bf16: forward 99 us, 0.80 of the measured copy rate, gradient 137 us, 0.87; 65536 x 1024 46 and
+// 65 us (0.86, 0.91); from fp32 to bf16 124 and 237 us (0.96, 0.83), in fp32 alone 245 (0.97) for the gradient.
 // Row by row, each block waiting for its one row: 124 and 308 in bf16, 124 and 367 from fp32.  The forward in
 // bf16 uses two thirds of the issue slots: three passes over a row's words; with them in registers the
 // barriers stand alone.  8192 x 512 from fp32: 5.0 and 13.3 us, of which two launches in turn and two rounds of
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(1024) norm_cols(const float* __restrict__ part
     }
 }
 
-// ---- rows of pairs of elements (even widths; V = 8: of whole 16-byte words): the same sums, with rows on their way while others are
+// ---- rows of pairs of elements (even widths): the same sums, with rows on their way while others are
 // worked on.  A block takes two rows at a time, whose sums share their exchanges and barriers, and copies
 // the two after next into shared memory as it leaves their places; a thread reads only the words that
 // it copied itself.  Arithmetic on pairs of neighbours (an element takes 8 instructions in the forward
@@ -384,7 +384,7 @@ __device__ __forceinline__ void copies_wait_all_but_one() { asm volatile("cp.asy
 // (neighbouring threads' words are neighbours then; with runs of eight, each of two words, a 32-byte piece came
 // over in halves: 32768 x 4096 from fp32 to bf16, gradient 297 us for 237, forward, row by row, 187 for 124).
 // The forward's blocks that an SM holds:
-constexpr int pair_blocks(int T) { return T == 64 ? 8 : T <= 128 ? 6 : T == 256 ? 3 : 1; }
+constexpr int pair_blocks(int T) { return T == 64 ? 10 : T <= 128 ? 6 : T == 256 ? 3 : 1; }   // 65536 x 1024 with 8, 9, 10: 56, 50, 46 us
 constexpr int kPairWidest = 8192;          // channels of a row that 512 threads take
 constexpr size_t kPairSpace = 216 << 10;   // shared memory for it
 template <class TX, class TY>
@@ -868,7 +868,7 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaS
         int st;
         // Pairs of rows where there are some for each SM: the gradient (32768 x 4096 bf16 137 us, row by row 308; 64 x
         // 4096 7.2, 5.7; 304 x 4096 7.8, 8.6; 600 x 1024 6.3, 7.6) and the forward from bf16 to bf16 (32768 x 4096 99 us, 124;
-        // 65536 x 1024 49, 69) or of rows that a block of 512 threads takes (32768 x 8192 from fp32 251, 305).  Else
+        // 65536 x 1024 46, 69) or of rows that a block of 512 threads takes (32768 x 8192 from fp32 251, 305).  Else
         // the forward with fp32 is near the copy rate row by row (32768 x 4096 to bf16 124 us, 136 by pairs).
         constexpr int V = kRun<TX, TY>;
         const int T = row_threads(a.D, 8);
