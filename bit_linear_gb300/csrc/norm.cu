@@ -27,8 +27,8 @@
 // Row by row, each block waiting for its one row: 124 and 308 in bf16, 124 and 367 from fp32.  The forward in
 // bf16 uses two thirds of the issue slots: three passes over a row's words; with them in registers the
 // barriers stand alone.  8192 x 512 from fp32: 5.0 and 13.3 us, of which two launches in turn and two rounds of
-// rows; floors 3.7 and 6.2.  Odd widths in bf16 go element by element: 32768 x 4095 203 and 266 us (aligned
-// words with a first and last run of which a part is others' took as long or longer).
+// rows; floors 3.7 and 6.2.  Odd widths go element by element: 32768 x 4095 in bf16 136 and 266 us (runs of
+// aligned words, of which a row's first and last are in part others', took as long or longer).
 #include <algorithm>
 #include <cmath>
 
@@ -127,6 +127,82 @@ __global__ void __launch_bounds__(T * R, 1) norm_fwd(const __grid_constant__ Nor
             }
             store_as<TY, V>(y + c, v);
         }
+    }
+}
+
+// The same for many rows off 16-byte words: blocks stay, with weight and bias in registers (element by
+// element they take as many loads as the rows) and the next row under way.
+constexpr int loop_blocks(int threads) { return threads >= 512 ? 1 : 640 / threads; }   // of an SM
+
+template <class TX, class TY, int T, int R, int EPT, int V>
+__global__ void __launch_bounds__(T * R, loop_blocks(T * R)) norm_fwd_loop(const __grid_constant__ NormArgs a) {
+    constexpr int NV = EPT / V;
+    __shared__ float sums[2][2 * ((T + 31) / 32)];
+    ptx::pdl_trigger();
+    const int t = threadIdx.x % T;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * R + static_cast<int>(threadIdx.x) / T;
+    Raw<TX, V> raw[NV], next[NV];
+    auto fetch = [&](int64_t of, Raw<TX, V>(&to)[NV]) {
+        const TX* x = static_cast<const TX*>(a.x) + of * a.ld_x;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * T + t) * V;
+            if (c < a.D) to[j] = load_raw<TX, V>(x + c);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < Raw<TX, V>::WORDS; ++i) raw[j].w[i] = next[j].w[i] = 0u;   // behind the row: always
+    ptx::pdl_wait();
+    if (row < a.n) fetch(row, raw);
+    float w[EPT], b[EPT];
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+        const int c = (e / V * T + t) * V + e % V;
+        w[e] = a.weight && c < a.D ? __ldg(a.weight + c) : 1.f;
+        b[e] = a.bias && c < a.D ? __ldg(a.bias + c) : 0.f;
+    }
+    for (; row < a.n; row += step) {
+        if (row + step < a.n) fetch(row + step, next);
+        float s[1] = {0.f};
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) s[0] += raw_at<TX, V>(raw[e / V], e % V);
+        row_sums<T, 1>(s, sums[0]);
+        const float mean = s[0] * a.inv_d;
+        float q[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if ((j * T + t) * V < a.D) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = raw_at<TX, V>(raw[j], i) - mean;
+                    q[0] += d;
+                    q[1] = fmaf(d, d, q[1]);
+                }
+            }
+        }
+        row_sums<T, 2>(q, sums[1]);
+        const float delta = q[0] * a.inv_d;
+        const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-delta, delta, q[1] * a.inv_d), 0.f) + a.eps);
+        if (t == 0) {
+            if (a.mean) a.mean[row] = kept_mean(mean, delta, rstd);
+            if (a.rstd) a.rstd[row] = q[1] == q[1] ? rstd : q[1];   // fmaxf drops a NaN
+        }
+        TY* y = static_cast<TY*>(a.y) + row * a.ld_y;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * T + t) * V;
+            if (c < a.D) {
+                float v[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = fmaf((raw_at<TX, V>(raw[j], i) - mean - delta) * rstd, w[j * V + i], b[j * V + i]);
+                store_as<TY, V>(y + c, v);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) raw[j] = next[j];
     }
 }
 
@@ -753,7 +829,6 @@ __global__ void __launch_bounds__(T * R, 1) norm_bwd_pairs(const __grid_constant
     }
 }
 
-constexpr int kFwdEpt = 16, kBwdEpt = 16;
 constexpr int kWidest = 16384;   // channels that a block of 1024 threads holds
 
 // Threads a row takes at 16 elements each: part of a warp (where its elements come eight at a time), a
@@ -770,31 +845,43 @@ int bwd_parts(int64_t n, int64_t D) {
     return static_cast<int>(std::min<int64_t>(kPartMax, n));   // as few rows a block as there may be
 }
 
-template <bool BWD, class TX, class TY, int T, int R, int V>
-int launch_rows(const NormArgs& a, int grid, cudaStream_t s) {
-    if constexpr (BWD)
-        return launch_pdl(norm_bwd<TX, TY, T, R, kBwdEpt, V>, dim3(grid), dim3(T * R), R > 1 ? 2 * kBwdEpt * 32 * sizeof(float) : 0, s, a);
-    else
-        return launch_pdl(norm_fwd<TX, TY, T, R, kFwdEpt, V>, dim3(grid), dim3(T * R), 0, s, a);
+template <bool BWD, class TX, class TY, int T, int R, int V, int EPT = 16>
+int launch_rows(const NormArgs& a, int grid, int num_sms, cudaStream_t s) {
+    if constexpr (T == 32 && V <= 2 && EPT == 16) {   // narrow rows: fewer elements a thread (1048576 x 63 361, 265 us)
+        if (a.D <= 64) return launch_rows<BWD, TX, TY, T, R, V, 2>(a, grid, num_sms, s);
+        if (a.D <= 128) return launch_rows<BWD, TX, TY, T, R, V, 4>(a, grid, num_sms, s);
+        if (a.D <= 256) return launch_rows<BWD, TX, TY, T, R, V, 8>(a, grid, num_sms, s);
+    }
+    if constexpr (BWD) {
+        return launch_pdl(norm_bwd<TX, TY, T, R, EPT, V>, dim3(grid), dim3(T * R), R > 1 ? 2 * EPT * 32 * sizeof(float) : 0, s, a);
+    } else {
+        // More than 256 channels off 16-byte words: blocks that stay (32768 x 4095 bf16 136 us, a block a row 204;
+        // 500 x 4095 4.4, 5.4; 4096 x 511 4.2, 5.9; narrower 500000 x 127 167, 129; of whole words 32768 x 4096
+        // from fp32 135, 124).
+        if constexpr (V <= 2 && EPT == 16 && T <= 512)
+            return launch_pdl(norm_fwd_loop<TX, TY, T, R, EPT, V>, dim3(std::min(grid, num_sms * loop_blocks(T * R))), dim3(T * R), 0, s, a);
+        else
+            return launch_pdl(norm_fwd<TX, TY, T, R, EPT, V>, dim3(grid), dim3(T * R), 0, s, a);
+    }
 }
 
 template <bool BWD, class TX, class TY, int V>
-int pick_rows(const NormArgs& a, int* parts, cudaStream_t s) {
+int pick_rows(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     const int T = row_threads(a.D, BWD ? 1 : V), R = rows_beside(T);
     int grid = static_cast<int>((static_cast<int64_t>(a.n) + R - 1) / R);
     if (BWD) grid = std::min(grid, kPartMax / 2);
     *parts = grid;
     switch (T) {
     case 8:
-        if constexpr (!BWD && V >= 4) return launch_rows<BWD, TX, TY, 8, rows_beside(8), V>(a, grid, s);
+        if constexpr (!BWD && V >= 4) return launch_rows<BWD, TX, TY, 8, rows_beside(8), V>(a, grid, num_sms, s);
     case 16:
-        if constexpr (!BWD && V >= 4) return launch_rows<BWD, TX, TY, 16, rows_beside(16), V>(a, grid, s);
-    case 32: return launch_rows<BWD, TX, TY, 32, rows_beside(32), V>(a, grid, s);
-    case 64: return launch_rows<BWD, TX, TY, 64, 1, V>(a, grid, s);
-    case 128: return launch_rows<BWD, TX, TY, 128, 1, V>(a, grid, s);
-    case 256: return launch_rows<BWD, TX, TY, 256, 1, V>(a, grid, s);
-    case 512: return launch_rows<BWD, TX, TY, 512, 1, V>(a, grid, s);
-    default: return launch_rows<BWD, TX, TY, 1024, 1, V>(a, grid, s);
+        if constexpr (!BWD && V >= 4) return launch_rows<BWD, TX, TY, 16, rows_beside(16), V>(a, grid, num_sms, s);
+    case 32: return launch_rows<BWD, TX, TY, 32, rows_beside(32), V>(a, grid, num_sms, s);
+    case 64: return launch_rows<BWD, TX, TY, 64, 1, V>(a, grid, num_sms, s);
+    case 128: return launch_rows<BWD, TX, TY, 128, 1, V>(a, grid, num_sms, s);
+    case 256: return launch_rows<BWD, TX, TY, 256, 1, V>(a, grid, num_sms, s);
+    case 512: return launch_rows<BWD, TX, TY, 512, 1, V>(a, grid, num_sms, s);
+    default: return launch_rows<BWD, TX, TY, 1024, 1, V>(a, grid, num_sms, s);
     }
 }
 
@@ -811,7 +898,7 @@ int launch_pairs(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     if constexpr (BWD) {
         constexpr int R = bwd_beside<TX, TY, T>(), SUB = T < 32 ? 32 / T : 1;
         if constexpr (R == 0) {
-            return pick_rows<BWD, TX, TY, WHOLE ? kRun<TX, TY> : 2>(a, parts, s);
+            return pick_rows<BWD, TX, TY, WHOLE ? kRun<TX, TY> : 2>(a, num_sms, parts, s);
         } else {
             constexpr int smem = 4 * 16 * T * R * (kElem<TX> + kElem<TY>);
             static_assert(smem >= R / SUB * 32 * T * 4, "the columns' sums");
@@ -874,12 +961,12 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaS
         const int T = row_threads(a.D, 8);
         const bool pairs = a.D <= kPairWidest && (BWD || V == 8 || T == 512) && a.n > num_sms * (BWD && T >= 256 ? 1 : 2 * rows_beside(T));
         if (all_allow(a, BWD, V, ex, ey)) {
-            st = pairs ? pick_pairs<BWD, TX, TY, true>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, V>(a, &parts, s);
+            st = pairs ? pick_pairs<BWD, TX, TY, true>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, V>(a, num_sms, &parts, s);
         } else if (all_allow(a, BWD, 2, ex, ey)) {
-            if constexpr (BWD) st = pairs ? pick_pairs<BWD, TX, TY, false>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, &parts, s);
-            else st = pick_rows<BWD, TX, TY, 2>(a, &parts, s);
+            if constexpr (BWD) st = pairs ? pick_pairs<BWD, TX, TY, false>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, num_sms, &parts, s);
+            else st = pick_rows<BWD, TX, TY, 2>(a, num_sms, &parts, s);
         } else {
-            st = pick_rows<BWD, TX, TY, 1>(a, &parts, s);
+            st = pick_rows<BWD, TX, TY, 1>(a, num_sms, &parts, s);
         }
         if (st) return st;
     }

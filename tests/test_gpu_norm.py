@@ -86,6 +86,17 @@ def _run(bl, x, w, b, dy, eps=1e-5, y=None, dx=None):
 NAMES = ("y", "mean", "rstd", "dx", "dweight", "dbias")
 
 
+@pytest.mark.parametrize("n,D", [(7001, 63), (6501, 127), (3501, 255), (6301, 301), (3201, 515), (1601, 2047), (640, 4097), (333, 8191), (1601, 2046), (333, 8190)])
+@pytest.mark.parametrize("tx,ty", TYPES, ids=IDS)
+def test_many_rows_off_words(cuda_lib, n, D, tx, ty):
+    """More rows than the forward's blocks that stay, of widths that no 16-byte words hold."""
+    x, w, b, dy = _inputs(n, D, tx, ty, n + D)
+    got, refs = _run(cuda_lib, x, w, b, dy), _ref(x, w, b, 1e-5, dy)
+    for g, ref, name in zip(got, refs, NAMES):
+        _near(g, ref, name)
+    assert all(torch.equal(p, q) for p, q in zip(got, _run(cuda_lib, x, w, b, dy)))
+
+
 @pytest.mark.parametrize("n,D", [(1, 1), (1, 512), (3, 2), (5, 31), (7, 32), (2500, 64), (9, 511), (33, 512), (10, 513), (4, 1000), (700, 2048),
                                  (6, 2049), (5, 4096), (3, 4100), (2, 8191), (3, 8200), (2, 16384), (2, 16385), (3, 20002)])
 @pytest.mark.parametrize("tx,ty", TYPES, ids=IDS)
