@@ -23,10 +23,10 @@
 // block stores its sums once, and a second launch adds the blocks' in a fixed order.
 //
 // 32768 x 4096 in bf16: forward 99 us, 0.80 of the measured copy rate, gradient 137 us, 0.87; 65536 x 1024 46 and
-// 65 us (0.86, 0.91); from fp32 to bf16 124 and 237 us (0.96, 0.83), in fp32 alone 245 (0.97) for the gradient.
+// 65 us (0.86, 0.91); from fp32 to bf16 117 and 237 us (1.01, 0.83), in fp32 alone 245 (0.97) for the gradient.
 // Row by row, each block waiting for its one row: 124 and 308 in bf16, 124 and 367 from fp32.  The forward in
 // bf16 uses two thirds of the issue slots: three passes over a row's words; with them in registers the
-// barriers stand alone.  8192 x 512 from fp32: 5.0 and 13.3 us, of which two launches in turn and two rounds of
+// barriers stand alone.  8192 x 512 from fp32: 4.6 and 13.3 us, of which two launches in turn and two rounds of
 // rows; floors 3.7 and 6.2.  Odd widths go element by element: 32768 x 4095 in bf16 136 and 266 us (runs of
 // aligned words, of which a row's first and last are in part others', took as long or longer).
 #include <algorithm>
@@ -38,7 +38,7 @@
 namespace tern {
 namespace {
 
-constexpr int kPartMax = 1216;   // blocks of the gradient: eight for each of 152 SMs
+constexpr int kPartMax = 608;   // blocks of the gradient: four for each of 152 SMs
 
 struct NormArgs {
     const void* x;
@@ -61,7 +61,7 @@ __device__ __forceinline__ float kept_mean(float mean, float delta, float rstd) 
 // EPT elements of a row in registers: thread t holds V neighbouring elements at (j T + t) V.
 // T threads a row, R rows a block side by side (R > 1 with T <= 32 only).
 template <class TX, class TY, int T, int R, int EPT, int V>
-__global__ void __launch_bounds__(T * R, 1) norm_fwd(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(T * R, EPT > 16 ? 1024 / (T * R) : 1) norm_fwd(const __grid_constant__ NormArgs a) {
     constexpr int NV = EPT / V;
     __shared__ float sums[2][2 * ((T + 31) / 32)];
     ptx::pdl_trigger();
@@ -458,7 +458,7 @@ __device__ __forceinline__ void copies_wait_all_but_one() { asm volatile("cp.asy
 
 // A thread takes 16 elements of a row, in runs of a 16-byte word: eight of bf16; four where there is fp32
 // (neighbouring threads' words are neighbours then; with runs of eight, each of two words, a 32-byte piece came
-// over in halves: 32768 x 4096 from fp32 to bf16, gradient 297 us for 237, forward, row by row, 187 for 124).
+// over in halves: 32768 x 4096 from fp32 to bf16, gradient 297 us for 237, forward, row by row, 187 for 124 and, with 32 elements a thread, 117).
 // The forward's blocks that an SM holds:
 constexpr int pair_blocks(int T) { return T == 64 ? 10 : T <= 128 ? 6 : T == 256 ? 3 : 1; }   // 65536 x 1024 with 8, 9, 10: 56, 50, 46 us
 constexpr int kPairWidest = 8192;          // channels of a row that 512 threads take
@@ -869,7 +869,7 @@ template <bool BWD, class TX, class TY, int V>
 int pick_rows(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     const int T = row_threads(a.D, BWD ? 1 : V), R = rows_beside(T);
     int grid = static_cast<int>((static_cast<int64_t>(a.n) + R - 1) / R);
-    if (BWD) grid = std::min(grid, kPartMax / 2);
+    if (BWD) grid = std::min(grid, kPartMax);
     *parts = grid;
     switch (T) {
     case 8:
@@ -881,7 +881,24 @@ int pick_rows(const NormArgs& a, int num_sms, int* parts, cudaStream_t s) {
     case 128: return launch_rows<BWD, TX, TY, 128, 1, V>(a, grid, num_sms, s);
     case 256: return launch_rows<BWD, TX, TY, 256, 1, V>(a, grid, num_sms, s);
     case 512: return launch_rows<BWD, TX, TY, 512, 1, V>(a, grid, num_sms, s);
-    default: return launch_rows<BWD, TX, TY, 1024, 1, V>(a, grid, num_sms, s);
+    default:
+        if constexpr (BWD) return launch_rows<BWD, TX, TY, 1024, 1, V>(a, grid, num_sms, s);
+        else return launch_rows<BWD, TX, TY, 512, 1, V, 32>(a, grid, num_sms, s);   // two rows an SM
+    }
+}
+
+// The forward with 32 elements a thread, half of T threads a row.
+template <class TX, class TY>
+int pick_tall(const NormArgs& a, int T, int num_sms, cudaStream_t s) {
+    constexpr int V = kRun<TX, TY>;
+    const auto blocks = [&](int R) { return static_cast<int>((static_cast<int64_t>(a.n) + R - 1) / R); };
+    switch (T) {
+    case 16: return launch_rows<false, TX, TY, 8, 16, V, 32>(a, blocks(16), num_sms, s);
+    case 32: return launch_rows<false, TX, TY, 16, 8, V, 32>(a, blocks(8), num_sms, s);
+    case 64: return launch_rows<false, TX, TY, 32, 4, V, 32>(a, blocks(4), num_sms, s);
+    case 128: return launch_rows<false, TX, TY, 64, 1, V, 32>(a, a.n, num_sms, s);
+    case 256: return launch_rows<false, TX, TY, 128, 1, V, 32>(a, a.n, num_sms, s);
+    default: return launch_rows<false, TX, TY, 256, 1, V, 32>(a, a.n, num_sms, s);
     }
 }
 
@@ -954,16 +971,28 @@ int run_norm(const NormArgs& a, float* dweight, float* dbias, int num_sms, cudaS
         constexpr int ex = kElem<TX>, ey = kElem<TY>;
         int st;
         // Pairs of rows where there are some for each SM: the gradient (32768 x 4096 bf16 137 us, row by row 308; 64 x
-        // 4096 7.2, 5.7; 304 x 4096 7.8, 8.6; 600 x 1024 6.3, 7.6) and the forward from bf16 to bf16 (32768 x 4096 99 us, 124;
-        // 65536 x 1024 46, 69) or of rows that a block of 512 threads takes (32768 x 8192 from fp32 251, 305).  Else
-        // the forward with fp32 is near the copy rate row by row (32768 x 4096 to bf16 124 us, 136 by pairs).
+        // 4096 7.2, 5.7; 304 x 4096 7.8, 8.6; 600 x 1024 6.3, 7.6) and the forward of bf16 (32768 x 4096 99 us, 124;
+        // 65536 x 1024 46, 69).  Else, and of bf16 rows that leave many of those threads idle or take 512, the forward
+        // gives a thread 32 elements as soon as rows are more than fit at once with 16, from pairs or 16 to 32:
+        // from fp32 32768 x 4096 124, 117 us, 65536 x 1024 71, 61, 65536 x 600 69, 39, 8192 x 512 5.1, 4.6, 65536 x 512 31,
+        // 32, 600 x 4096 3.6, 4.9; bf16 32768 x 8192 227, 222, 32768 x 6000 210, 180, 262144 x 160 48, 37, 32768 x
+        // 4096 99, 105.
         constexpr int V = kRun<TX, TY>;
         const int T = row_threads(a.D, 8);
-        const bool pairs = a.D <= kPairWidest && (BWD || V == 8 || T == 512) && a.n > num_sms * (BWD && T >= 256 ? 1 : 2 * rows_beside(T));
+        const bool many = a.D <= kPairWidest && a.n > num_sms * (BWD && T >= 256 ? 1 : 2 * rows_beside(T));
+        const bool tall = a.D <= kPairWidest && static_cast<int64_t>(a.n) * T > 1536 * num_sms &&
+                          (V == 4 ? T >= 32 : T == 512 || (T >= 16 && a.D * 6 < 16 * 5 * T));
         if (all_allow(a, BWD, V, ex, ey)) {
-            st = pairs ? pick_pairs<BWD, TX, TY, true>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, V>(a, num_sms, &parts, s);
+            if constexpr (BWD) {
+                st = many ? pick_pairs<BWD, TX, TY, true>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, V>(a, num_sms, &parts, s);
+            } else if (tall) {
+                st = pick_tall<TX, TY>(a, T, num_sms, s);
+            } else {
+                if constexpr (V == 8) st = many ? pick_pairs<BWD, TX, TY, true>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, V>(a, num_sms, &parts, s);
+                else st = pick_rows<BWD, TX, TY, V>(a, num_sms, &parts, s);
+            }
         } else if (all_allow(a, BWD, 2, ex, ey)) {
-            if constexpr (BWD) st = pairs ? pick_pairs<BWD, TX, TY, false>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, num_sms, &parts, s);
+            if constexpr (BWD) st = many ? pick_pairs<BWD, TX, TY, false>(a, num_sms, &parts, s) : pick_rows<BWD, TX, TY, 2>(a, num_sms, &parts, s);
             else st = pick_rows<BWD, TX, TY, 2>(a, num_sms, &parts, s);
         } else {
             st = pick_rows<BWD, TX, TY, 1>(a, num_sms, &parts, s);

@@ -18,7 +18,7 @@ def lib():
 def test_sizes(lib):
     f = lib.tern_norm_bwd_workspace
     assert f(1, 512) == 2 * 512 * 4 and f(9, 513) == 2 * 9 * 513 * 4      # the sums of at most a block a row
-    assert f(1 << 20, 4096) == 2 * 1216 * 4096 * 4                        # at most 1216 blocks
+    assert f(1 << 20, 4096) == 2 * 608 * 4096 * 4                         # at most 608 blocks
     assert f(77, 16385) == 77 * 4
     assert f(0, 512) == 0 and f(-1, 5) == 0 and f(5, (1 << 22) + 1) == 0
 

@@ -97,6 +97,17 @@ def test_many_rows_off_words(cuda_lib, n, D, tx, ty):
     assert all(torch.equal(p, q) for p, q in zip(got, _run(cuda_lib, x, w, b, dy)))
 
 
+@pytest.mark.parametrize("n,D", [(15001, 136), (7501, 264), (7401, 508), (3703, 520), (1901, 1032), (1001, 2056), (501, 4104), (501, 8192)])
+@pytest.mark.parametrize("tx,ty", TYPES, ids=IDS)
+def test_more_rows_than_fit(cuda_lib, n, D, tx, ty):
+    """More rows than are resident with 16 elements a thread: the forward gives each 32."""
+    x, w, b, dy = _inputs(n, D, tx, ty, n + D)
+    got, refs = _run(cuda_lib, x, w, b, dy), _ref(x, w, b, 1e-5, dy)
+    for g, ref, name in zip(got, refs, NAMES):
+        _near(g, ref, name)
+    assert all(torch.equal(p, q) for p, q in zip(got, _run(cuda_lib, x, w, b, dy)))
+
+
 @pytest.mark.parametrize("n,D", [(1, 1), (1, 512), (3, 2), (5, 31), (7, 32), (2500, 64), (9, 511), (33, 512), (10, 513), (4, 1000), (700, 2048),
                                  (6, 2049), (5, 4096), (3, 4100), (2, 8191), (3, 8200), (2, 16384), (2, 16385), (3, 20002)])
 @pytest.mark.parametrize("tx,ty", TYPES, ids=IDS)
