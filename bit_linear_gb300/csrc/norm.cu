@@ -8,8 +8,8 @@
 //
 // What bounds it is memory: a row is read once into registers, and everything that needs the whole
 // row (two passes of sums in the forward, three sums at once in the gradient) works there.  A row
-// belongs to a warp or to a block, whichever holds it at EPT elements a thread; rows wider than a
-// block of 1024 threads holds are read again for each pass (from L2 as a rule).
+// belongs to part of a warp, a warp or a block, whichever holds it at 16 or 32 elements a thread; rows of more
+// than 16384 channels are read again for each pass (from L2 as a rule).
 //
 // The mean of a row far from zero rounds by up to half a unit of its own size, which may be large
 // beside the row's spread.  So what the rounded mean leaves, delta = sum (x - mean) / D, is summed in
