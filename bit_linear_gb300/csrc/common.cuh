@@ -42,8 +42,17 @@ int split8_dy(const uint16_t* dY, const float* scale, int64_t M, int64_t N, void
 }  // namespace tern
 
 #ifdef __CUDACC__
+#include <mutex>
 #include <utility>
 namespace tern {
+// A kernel's limit of dynamic shared memory is state of the process.  Where it depends on a call's sizes, it
+// is set and the kernel launched under this lock: another thread's call of other sizes could lower it
+// in between, and the launch would fail.
+inline std::mutex& smem_limit_lock() {
+    static std::mutex lock;
+    return lock;
+}
+
 // Every kernel of the library is launched with programmatic stream serialization
 // (programmatic dependent launch): the next kernel on the stream may launch while
 // this one finishes, and each kernel waits for its predecessor (ptx::pdl_wait)
@@ -88,8 +97,11 @@ int launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (smem > 40 * 1024)   // beside static shared memory, more than a launch gets unasked
+    std::unique_lock<std::mutex> hold(smem_limit_lock(), std::defer_lock);
+    if (smem > 40 * 1024) {   // beside static shared memory, more than a launch gets unasked
+        hold.lock();
         TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    }
     if (cluster > 8) TERN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     TERN_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
     return TERN_OK;
