@@ -783,7 +783,7 @@ extern "C" int tern_glu_fwd(const uint16_t* X, const tern_tiles* W, const float*
 
 extern "C" int tern_glu_bwd(const uint16_t* dH, const uint16_t* saved, const uint16_t* X, const tern_tiles* W, const float* scale, int act,
                             uint16_t* dY, int64_t M, int64_t K, int64_t N, void* stream) {
-    if (!glu_dims(M, saved ? 16 : K, N) || act < TERN_ACT_SILU || act > TERN_ACT_SIGMOID) return TERN_ERR_ARG;
+    if (!glu_dims(M, saved ? 16 : K, N) || (!saved && (act < TERN_ACT_SILU || act > TERN_ACT_SIGMOID))) return TERN_ERR_ARG;
     if (N % 16 || (!saved && K % 16)) return TERN_ERR_ALIGN;
     if (M == 0) return TERN_OK;
     if (!dH || !dY || (!saved && (!X || !W || !W->t_bf16 || !scale))) return TERN_ERR_ARG;
