@@ -928,7 +928,8 @@ struct DistillArgs {
 };
 
 // The teacher's entries of a row: ids (-1 where left out) and probabilities, by a warp into shared
-// memory; false for a row without any, or of weight 0.
+// memory; false for a row without any, or of weight 0.  An entry counts by its difference to the largest,
+// taken before the division by T: divided first, large entries would be infinite.
 __device__ __forceinline__ bool teacher(const DistillArgs& a, int64_t row, int* ids, float* p, float w) {
     const int lane = threadIdx.x & 31;
     float m = kNegInf;
@@ -936,7 +937,7 @@ __device__ __forceinline__ bool teacher(const DistillArgs& a, int64_t row, int* 
     for (int c = lane; c < a.k; c += 32) {
         const int64_t at = row * a.k + c;
         const int64_t id = a.wide_ids ? __ldg(static_cast<const long long*>(a.ids) + at) : __ldg(static_cast<const int32_t*>(a.ids) + at);
-        const float t = a.top ? __ldg(a.top + at) * a.inv_t : 0.f;
+        const float t = a.top ? __ldg(a.top + at) : 0.f;
         const bool in = id >= 0 && id < a.V && t != kNegInf;
         ids[c] = in ? static_cast<int>(id) : -1;
         p[c] = t;
@@ -949,7 +950,7 @@ __device__ __forceinline__ bool teacher(const DistillArgs& a, int64_t row, int* 
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     float s = 0.f;
     for (int c = lane; c < a.k; c += 32)
-        if (ids[c] >= 0) s += p[c] = pow2((p[c] - m) * kLog2e);
+        if (ids[c] >= 0) s += p[c] = pow2((p[c] - m) * (a.inv_t * kLog2e));
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     for (int c = lane; c < a.k; c += 32) p[c] = ids[c] >= 0 ? p[c] / s : 0.f;
@@ -1041,7 +1042,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) distill_r
         if (c < a.k) {
             const int64_t at = row * a.k + c;
             const int64_t of = a.wide_ids ? __ldg(static_cast<const long long*>(a.ids) + at) : __ldg(static_cast<const int32_t*>(a.ids) + at);
-            t[e] = a.top ? __ldg(a.top + at) * a.inv_t : 0.f;
+            t[e] = a.top ? __ldg(a.top + at) : 0.f;
             if (of >= 0 && of < a.V && t[e] != kNegInf) id[e] = static_cast<int>(of);
         }
     }
@@ -1067,7 +1068,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) distill_r
     for (int d = 16; d >= 1; d >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, d));
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        if (e * T < a.k && id[e] >= 0) ts += pow2((t[e] - tm) * kLog2e);
+        if (e * T < a.k && id[e] >= 0) ts += pow2((t[e] - tm) * g.c);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) ts += __shfl_xor_sync(0xffffffffu, ts, d);
     if (!a.lse_in) st.join_warp(g.c);
@@ -1082,7 +1083,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) distill_r
 #pragma unroll
         for (int d = W / 2; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         tm = __shfl_sync(0xffffffffu, m, 0);
-        ts = mine.x == kNegInf ? mine.y : mine.y * pow2((mine.x - tm) * kLog2e);   // without an entry 0, or NaN
+        ts = mine.x == kNegInf ? mine.y : mine.y * pow2((mine.x - tm) * g.c);   // without an entry 0, or NaN
 #pragma unroll
         for (int d = W / 2; d >= 1; d >>= 1) ts += __shfl_xor_sync(0xffffffffu, ts, d);
         ts = __shfl_sync(0xffffffffu, ts, 0);
@@ -1161,7 +1162,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : T == 128 ? 8 : 32) distill_r
     for (int e = 0; e < E; ++e) {
         const int c = e * T + threadIdx.x;
         if (e * T < a.k && c < (a.k + 3) / 4 * 4) {
-            const float q = id[e] >= 0 ? pow2((t[e] - tm) * kLog2e) / ts : 0.f;
+            const float q = id[e] >= 0 ? pow2((t[e] - tm) * g.c) / ts : 0.f;
             ids[c] = id[e], p[c] = q, t[e] = q;
             if (id[e] >= 0 && q != 0.f) loss += q * (logf(q) - ((x[e] - st.m) * a.inv_t - log_s));
         }
