@@ -65,7 +65,9 @@ __device__ __forceinline__ float bounded(float x) {                             
 }
 
 // act(g) and, with D, act'(g), of two neighbours.  The special functions' errors (2^-22 relative each) are
-// far below the outputs' rounding to bf16.
+// far below the outputs' rounding to bf16.  So is GELU's approximation but for its lower tail, where it is
+// relative to Phi 1.6e-3 at g = -5, 3.6e-3 at -6 (the rounding's 2^-8 from there on) and 1e-2 at -8, of
+// values below 1e-8; 1 + erf in fp32 has nothing left there.
 template <int ACT, bool D>
 __device__ __forceinline__ void activate(F2 g, F2& a, F2& d) {
     if constexpr (ACT == TERN_ACT_RELU2) {
@@ -426,8 +428,10 @@ using GluOneNarrow = GluCfg<1, 64, 6>;
 // lane (g, t) = (lane / 4, lane % 4) reads the words of 16 columns 16 g.. at the four weight rows
 // 4 t.. of a block of 16 rows, and MMA j takes its columns 16 g + j and 16 g + j + 8.
 //
-// What bounds them is mma.sync itself, at 25 cycles an SM quarter for 256 weights: 1 x 4096 x 6144 7.6 us, 8 rows 8.8,
-// 16 rows (two MMAs for each operand) 12.2, of which a launch is 3.6 and the codes' bytes would be 1.9.
+// 1 x 4096 x 6144 7.6 us, 8 rows 8.8, 16 rows (two MMAs for each operand) 12.2, of which a launch is 3.6 and the
+// codes' bytes would be 1.9.  No unit is at its limit: at 16 rows the tensor pipe is busy for 23% of the time,
+// the issue slots for 35%, and per issue 2.1 warps wait for a result of fixed latency, 2.1 for a global load and
+// 0.8 for a pipe.  So latency bounds it, at two blocks an SM; and 240 blocks for 304 places leave 64 SMs with one.
 //
 // A block has 128 outputs: half of its eight warps take the gate's 128 columns, half the value's, and share
 // the weight's rows; where there are fewer blocks than SMs, the blocks of a cluster share them too.

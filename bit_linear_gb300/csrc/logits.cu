@@ -19,8 +19,11 @@
 // scalar form eight: 169 us without alternatives).  Loss and gradient 330 us, 0.74: the row is read twice, and
 // L2 keeps it from the first to the second only with two blocks a row, whose exchange the next rows cover in
 // part.  Rows held in shared memory by persistent clusters of eight blocks read memory once but took 1464 us
-// (a teacher's entries by one warp, loops of unknown length).  One row of 100003: 4.5 us, with 20 alternatives 9.1,
-// most of it the first run through code that is not in the instruction cache.
+// (a teacher's entries by one warp, loops of unknown length).  One row of 100003: 4.5 us, with 20 alternatives 9.1: a
+// chain of reading, bound, list, words again, ranks and the cluster's exchange with nothing beside it (which of
+// these it waits for was not measured).  32768 x 700, distillation 57 us, floor 14: rows of fewer words than a whole
+// batch of a warp are loaded a word at a time, an SM holds 32 such warps, and the forms with 32 threads spill
+// 40 to 128 bytes (a teacher of up to 256 entries in registers).
 #include <algorithm>
 #include <cmath>
 

@@ -20,7 +20,8 @@
 // deviation): around zero the first sum is the better one, of bf16 often exact.
 //
 // The gradient's blocks stay for many rows and keep the sums of their columns in registers; each
-// block stores its sums once, and a second launch adds the blocks' in a fixed order.
+// block stores its sums once, and a second launch adds the blocks' in a fixed order.  Rows of more than 16384
+// channels have a kernel of their own for the columns' sums, by parts of the rows.
 //
 // 32768 x 4096 in bf16: forward 99 us, 0.80 of the measured copy rate, gradient 137 us, 0.87; 65536 x 1024 46 and
 // 65 us (0.86, 0.91); from fp32 to bf16 117 and 237 us (1.01, 0.83), in fp32 alone 245 (0.97) for the gradient.
@@ -28,7 +29,11 @@
 // bf16 uses two thirds of the issue slots: three passes over a row's words; with them in registers the
 // barriers stand alone.  8192 x 512 from fp32: 4.6 and 13.3 us, of which two launches in turn and two rounds of
 // rows; floors 3.7 and 6.2.  Odd widths go element by element: 32768 x 4095 in bf16 136 and 266 us (runs of
-// aligned words, of which a row's first and last are in part others', took as long or longer).
+// aligned words, of which a row's first and last are in part others', took as long or longer).  More than 8192
+// channels: the gradient with 1024 threads has 64 registers a thread and spills 268 to 576 bytes (16384 x 12288 from
+// fp32 873 us, floor 297; 8192 x 16384 in bf16 376, 119); more than 16384, rows read three times in the
+// forward and x and dy three times in the gradient: 8192 x 16385 in bf16 228 and 556 us (floors 79, 119), 8192 x 20000
+// 298 and 670 (97, 145).
 #include <algorithm>
 #include <cmath>
 

@@ -494,7 +494,8 @@ int tern_orthogonalize(const float* G, int64_t K, int64_t N, int steps, float ep
  *   y    = (x - mean) * rstd * weight + bias
  * x: x_dtype, y: y_dtype (TERN_BF16 or TERN_F32 each); weight, bias [D] fp32 or NULL (1, 0); mean,
  * rstd [n] fp32, written unless NULL (the gradient reads them).  Sums are fp32, y is rounded once.
- * eps > 0 (1e-5 is usual); n < 2^31 - 2048, D at most 2^22.
+ * eps > 0 (1e-5 is usual); n < 2^31 - 2048, D at most 2^22.  A row with NaN or an infinity gives NaN.  Rows
+ * whose sum, or sum of squared deviations, passes fp32's range are outside (entries up to 1e15 never do).
  */
 int tern_norm_fwd(const void* x, int x_dtype, int64_t ld_x, const float* weight, const float* bias, int64_t n,
                   int64_t D, float eps, void* y, int y_dtype, int64_t ld_y, float* mean, float* rstd, void* stream);
@@ -504,7 +505,7 @@ int tern_norm_fwd(const void* x, int x_dtype, int64_t ld_x, const float* weight,
  *   dx = rstd * (g - sum g / D - xhat * sum (g xhat) / D)
  *   dweight = sum over rows of dy * xhat, dbias = sum over rows of dy    (fp32 [D]; NULL to skip)
  * dx is rounded once.  Sums run in a fixed order.  A padding row adds nothing to dweight and dbias where
- * its dy is 0 and its x finite.
+ * its dy is 0 and its x, mean and rstd are finite.
  *   workspace: >= tern_norm_bwd_workspace() bytes, 16-byte aligned, for dweight or dbias (else NULL).
  */
 size_t tern_norm_bwd_workspace(int64_t n, int64_t D);
@@ -554,7 +555,7 @@ int tern_glu_bwd(const uint16_t* dH, const uint16_t* saved, const uint16_t* X, c
  * with k = 0 the last two are not used.  Masked entries are -inf: they have probability 0 and rank
  * last, by id.  A row of nothing else has lse and every log probability -inf and entropy 0.  A row with
  * NaN or +inf gives NaN (its largest entries are still found; NaN ranks above +inf).
- * n < 2^27, V < 2^31 - 65536.
+ * n < 2^27, 1 <= V < 2^31 - 65536 (n = 0 included).
  */
 #define TERN_SCORE_MAX_TOP 64
 int tern_score(const void* logits, int dtype, int64_t ld, int64_t n, int64_t V, const void* tokens, int tokens_dtype,
@@ -569,6 +570,7 @@ int tern_score(const void* logits, int dtype, int64_t ld, int64_t n, int64_t V, 
  * Entries whose id is outside 0..V-1, and those of -inf, are left out; an id given twice counts with
  * both probabilities.  A row without entries, or of weight 0, has loss, lse and gradient 0 whatever
  * its logits hold.  With k = 1 this is cross entropy of the id (top may be NULL then).
+ * n < 2^27, 1 <= V < 2^31 - 65536 (n = 0 included).
  */
 #define TERN_DISTILL_MAX_TOP 256
 typedef struct tern_distillation {
